@@ -58,7 +58,9 @@ typedef enum {
   MUON_ERR_TIMEOUT = 6        /* a bounded device wait ran out (from muon_handle_check) */
 } muon_status_t;
 
-typedef enum { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype_t;
+/* MUON_F16: the training operators only (layer norm, attention, 8-bit
+ * activations). */
+typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2 } muon_dtype_t;
 
 /* Newton-Schulz method: "standard" iterates on X; "gram" iterates on the
  * small square R = XX^T and applies the accumulated polynomial to X0 once
@@ -265,6 +267,133 @@ muon_status_t muon_noalloc_check(void* stream);
  * 0: MUON_ERR_INVALID_ARG. */
 muon_status_t muon_noalloc_set_timeout_ns(uint64_t timeout_ns);
 
+/* ------------------------------------------------------------------------
+ * Training operators: what a transformer block's forward and backward pass
+ * needs around the optimizer step.  Their gradients are what muon_step and
+ * adamw_step take.  (No counterpart on the source pages.)
+ *
+ * Conventions, beyond those at the top of this file:
+ *   - The last dimension is contiguous; the others have strides in elements.
+ *   - Nothing is kept in the handle between calls: calls from one
+ *     host thread may run on several streams at once.
+ *   - `workspace` is caller-owned device memory, 256-byte aligned, of at
+ *     least the bytes that the matching *_workspace call reports (host only,
+ *     from shapes alone; 0 bytes: NULL is fine).  It is scratch: free for
+ *     other use once the call's work on `stream` is done.
+ *   - Sums, statistics and softmax are held in fp32; each output is rounded
+ *     once to its type.  Results do not change from call to call.
+ *   - An operand of an unsupported size, stride or alignment gives
+ *     MUON_ERR_INVALID_ARG before anything is enqueued.
+ */
+
+/* Layer norm over the last dimension of `rows` rows of `cols` elements:
+ *   mean = E[x], rstd = (E[(x - mean)^2] + eps)^(-1/2)
+ *   y = (x - mean) rstd w + b
+ *   x, y          dtype, row strides ldx, ldy >= cols (y may be x)
+ *   weight, bias  wdtype (MUON_F32 or dtype), [cols]; NULL: ones, zeros
+ *   mean, rstd    fp32 [rows], written (the backward pass reads them)
+ * 1 <= cols <= 16384.  rows == 0 is a valid no-op. */
+muon_status_t muon_layer_norm_forward(muon_handle_t h, const void* x, int64_t ldx, const void* weight,
+                                      const void* bias, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows,
+                                      int64_t cols, int32_t dtype, int32_t wdtype, float eps, void* stream);
+
+/* Its backward pass: with xh = (x - mean) rstd and g = dy w,
+ *   dx = rstd (g - E[g] - xh E[g xh]),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   dy, x, dx        dtype, row strides lddy, ldx, lddx (dx may be dy or x)
+ *   dweight, dbias   fp32 [cols], overwritten (zeros when rows == 0) */
+muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                       const float* mean, const float* rstd, const void* weight, void* dx,
+                                       int64_t lddx, float* dweight, float* dbias, int64_t rows, int64_t cols,
+                                       int32_t dtype, int32_t wdtype, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+muon_status_t muon_layer_norm_workspace(muon_handle_t h, int64_t rows, int64_t cols, uint64_t* bytes);
+
+/* Attention.  Query i of a sequence with sq queries and sk keys stands at
+ * place i + sk - sq.  causal: it sees the keys at places up to its own; with
+ * window > 0 only the last `window` of those.  Otherwise it sees every key.
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),
+ *   o_i = sum_j exp(s_ij - lse_i) v_j
+ * A query that sees no key has o = 0, lse = -inf and no part in any
+ * gradient.  Head h of q uses head h / (heads / kv_heads) of k and v.
+ *
+ * Batched: tensors are [batch][token][head][dim] with the given strides.
+ * Packed (cu_seqlens_q != NULL): the sequences lie one after another on one
+ * token axis; sq and sk are the axes' lengths, sequence b holds the tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device int32 [batch + 1], rising
+ * from 0 to sq / sk; read on the device: values outside the axis or running
+ * backwards are cut to a valid range, tokens of no sequence get o = 0, lse =
+ * -inf and zero gradients), the batch strides are unused.
+ *
+ *   dim      a multiple of 8, 8 .. 128
+ *   dtype    MUON_BF16 or MUON_F16, every tensor but lse
+ *   strides  {batch, token, head}, multiples of 8; pointers 16-byte aligned
+ *   lse      fp32 [batch][heads][sq] ([heads][sq] when packed), contiguous
+ * Rows of a sequence are cut at its length: what lies past it, NaN and
+ * infinity included, has no part in the result. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;                /* forward: written; backward: read */
+  float* lse;             /* forward: written; backward: read */
+  const void* dout;       /* backward only, as the pointers below: gradient of o */
+  void* dq;
+  void* dk;
+  void* dv;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3], dout_stride[3], dq_stride[3], dk_stride[3],
+      dv_stride[3];
+  int32_t batch, sq, sk, heads, kv_heads, dim;
+  int32_t causal, window, dtype;
+  float scale;
+} muon_attention_t;
+
+muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a, void* stream);
+
+/* The backward pass, which recomputes the probabilities p_ij = exp(s_ij -
+ * lse_i): with delta_i = dout_i . o_i,
+ *   dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - delta_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
+ * dk and dv summed over the query heads that share them. */
+muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+muon_status_t muon_attention_workspace(muon_handle_t h, const muon_attention_t* a, uint64_t* bytes);
+
+/* Activations kept in 8 bits for the backward pass.  Each row is cut into
+ * blocks of 128 columns; a block with largest magnitude a is stored as e4m3
+ * codes of x 2^-e, rounded to nearest even, e the smallest integer >= -111
+ * with a 2^-e <= 448.  The scale byte is e + 127.  A block with a NaN or an
+ * infinity gets the byte 255 and codes 0, which stand for NaN.
+ *   x       dtype, [rows][cols], row stride ldx
+ *   codes   [rows], row stride ldc bytes: a multiple of 128, >= cols; the
+ *           codes past the last column up to the block's end are set to 0;
+ *           16-byte aligned
+ *   scales  [ceil(cols / 128)], lds bytes apart: a multiple of 16, >= rows;
+ *           one byte a row; 16-byte aligned */
+muon_status_t muon_act8_store(muon_handle_t h, const void* x, int64_t ldx, uint8_t* codes, int64_t ldc,
+                              uint8_t* scales, int64_t lds, int64_t rows, int64_t cols, int32_t dtype, void* stream);
+/* out[r][c] = code 2^e, rounded to dtype (exact in fp32, and in bf16 below
+ * its largest value) */
+muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                int64_t lds, void* out, int64_t ldo, int64_t rows, int64_t cols, int32_t dtype,
+                                void* stream);
+
+/* The weight's gradient of a linear layer y = x w^T whose input x was stored
+ * in 8 bits, straight from the codes:
+ *   dw[o][n] = sum over rows t of dy[t][o] x[t][n]  (+ add[o][n])
+ *   dy       bf16 [rows][out], row stride lddy
+ *   add, dw  odtype (MUON_F32 or MUON_BF16) [out][cols], row strides ldadd,
+ *            lddw; add may be NULL, or dw itself
+ * rows == 0 gives zeros (or add). */
+muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t lddy, const uint8_t* codes, int64_t ldc,
+                                    const uint8_t* scales, int64_t lds, const void* add, int64_t ldadd, void* dw,
+                                    int64_t lddw, int64_t rows, int64_t cols, int64_t out, int32_t odtype,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, int64_t rows, int64_t cols, int64_t out, int64_t lddy,
+                                              uint64_t* bytes);
+
 /* Kernel classes reported by muon_handle_profile(). */
 enum {
   MUON_K_PREPARE = 0, /* momentum / Nesterov / norm partials / working copy */
@@ -275,7 +404,11 @@ enum {
   MUON_K_FINAL = 5,   /* last update fused with the parameter write         */
   MUON_K_APPLY = 6,   /* parameter write when no NS iteration runs          */
   MUON_K_ADAMW = 7,   /* AdamW fallback                                     */
-  MUON_K_COUNT = 8
+  MUON_K_LAYER_NORM = 8,
+  MUON_K_ATTENTION = 9,
+  MUON_K_ACT8 = 10,   /* store and restore                                  */
+  MUON_K_WGRAD = 11,  /* weight gradient from 8-bit activations             */
+  MUON_K_COUNT = 12
 };
 
 /* Enable (1) or disable (0) per-launch CUDA-event timing on the launching

@@ -16,7 +16,7 @@ import torch
 
 from ._build import LIB_PATH
 
-MUON_F32, MUON_BF16 = 0, 1
+MUON_F32, MUON_BF16, MUON_F16 = 0, 1, 2
 MUON_NS_STANDARD, MUON_NS_GRAM, MUON_NS_AUTO = 0, 1, 2
 MUON_SCALE_RMS, MUON_SCALE_MUP = 0, 1
 QUINTIC = (3.4445, -4.7750, 2.0315)
@@ -29,8 +29,12 @@ EXPORTS = ("muon_handle_create", "muon_handle_destroy", "muon_handle_set_workspa
            "adamw_step", "muon_selftest_timeout", "muon_status_string", "muon_last_error", "muon_version",
            "muon_handle_set_profiling", "muon_handle_profile", "muon_handle_launch_count",
            "muon_orthogonalize_noalloc", "muon_handle_profile_records", "muon_step_ex", "muon_workspace_size",
-           "muon_noalloc_check", "muon_noalloc_set_timeout_ns")
-KERNEL_CLASSES = ("prepare", "norm", "syrk", "poly", "update", "final", "apply", "adamw")
+           "muon_noalloc_check", "muon_noalloc_set_timeout_ns",
+           "muon_layer_norm_forward", "muon_layer_norm_backward", "muon_layer_norm_workspace",
+           "muon_attention_forward", "muon_attention_backward", "muon_attention_workspace",
+           "muon_act8_store", "muon_act8_restore", "muon_act8_weight_grad", "muon_act8_weight_grad_workspace")
+KERNEL_CLASSES = ("prepare", "norm", "syrk", "poly", "update", "final", "apply", "adamw", "layer_norm", "attention",
+                  "act8", "wgrad")
 
 
 class MuonError(RuntimeError):
@@ -53,6 +57,15 @@ class MuonStepOptionsC(ctypes.Structure):
                 ("coeffs", ctypes.POINTER(ctypes.c_float)), ("ns_dtype", ctypes.c_int32),
                 ("scale_mode", ctypes.c_int32), ("update_rms", ctypes.c_float), ("extra_scale", ctypes.c_float),
                 ("coeffs_per_step", ctypes.c_int32)]
+
+
+class MuonAttentionC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv", "cu_seqlens_q",
+                                                "cu_seqlens_k")]
+                + [(n + "_stride", ctypes.c_int64 * 3) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
+                + [(n, ctypes.c_int32) for n in ("batch", "sq", "sk", "heads", "kv_heads", "dim", "causal", "window",
+                                                 "dtype")]
+                + [("scale", ctypes.c_float)])
 
 
 _lib = None
@@ -96,6 +109,18 @@ def load_library(path: str | None = None):
             "muon_handle_profile_records": (i32, [vp, ctypes.POINTER(i32), ctypes.POINTER(i32), fptr, i32,
                                                   ctypes.POINTER(i32)]),
             "muon_step_ex": (i32, [vp, ctypes.POINTER(MuonParamC), i32, ctypes.POINTER(MuonStepOptionsC), vp]),
+            "muon_layer_norm_forward": (i32, [vp, vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, i32, i32, f32, vp]),
+            "muon_layer_norm_backward": (i32, [vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, i32, i32,
+                                               vp, ctypes.c_size_t, vp]),
+            "muon_layer_norm_workspace": (i32, [vp, i64, i64, ctypes.POINTER(u64)]),
+            "muon_attention_forward": (i32, [vp, ctypes.POINTER(MuonAttentionC), vp]),
+            "muon_attention_backward": (i32, [vp, ctypes.POINTER(MuonAttentionC), vp, ctypes.c_size_t, vp]),
+            "muon_attention_workspace": (i32, [vp, ctypes.POINTER(MuonAttentionC), ctypes.POINTER(u64)]),
+            "muon_act8_store": (i32, [vp, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
+            "muon_act8_restore": (i32, [vp, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
+            "muon_act8_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp,
+                                            ctypes.c_size_t, vp]),
+            "muon_act8_weight_grad_workspace": (i32, [vp, i64, i64, i64, i64, ctypes.POINTER(u64)]),
             "muon_workspace_size": (i32, [vp, ctypes.POINTER(MuonParamC), i32, i32, i32, i32, ctypes.POINTER(u64)]),
         }
         for name, (res, args) in sig.items():

@@ -268,4 +268,73 @@ cudaError_t launch_apply(const ApplyParams& p, int batch, cudaStream_t s);
 cudaError_t launch_adamw(const AdamParams& p, int n_chunks, cudaStream_t s);
 cudaError_t launch_wait_selftest(unsigned long long timeout_ns, unsigned* err, cudaStream_t s);
 
+// ---------------------------------------------------------- layer norm
+struct NormParams {
+  const void* x;           // [rows], row stride ldx elements
+  const void* dy;          // backward: row stride lddy
+  void* y;                 // forward: y; backward: dx; row stride ldy
+  const void* weight;      // [cols] of wdtype, or nullptr (ones)
+  const void* bias;        // [cols] of wdtype, or nullptr (zeros)
+  float* mean;             // [rows], written by the forward pass, read by the backward pass
+  float* rstd;
+  float* part;             // backward: [parts][2][cols] partial sums of dw and db
+  long long rows, ldx, ldy, lddy;
+  int cols, dtype, wdtype;
+  int wvec;                // set by the launcher: weight and bias are 16-byte aligned
+  float eps;
+};
+constexpr int kNormMaxCols = 16384;
+int norm_threads(int cols);                             // threads that share a row
+int norm_parts(long long rows, int cols, int sms);      // CTAs of a pass = partial rows of dw and db
+cudaError_t launch_norm_fwd(const NormParams& p, int parts, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormParams& p, int parts, cudaStream_t s);
+cudaError_t launch_norm_join(const NormParams& p, int parts, float* dw, float* db, cudaStream_t s);
+
+// ------------------------------------------- activations kept in 8 bits
+struct Act8Params {
+  const void* x;           // store: input; restore: unused.  [rows], row stride ldx elements
+  void* out;               // restore: output, row stride ldx
+  uint8_t* codes;          // e4m3 codes, row stride ldc bytes
+  uint8_t* scales;         // [blocks of 128 columns], lds bytes apart, one byte a row
+  long long rows, ldx, ldc, lds;
+  int cols, dtype;
+};
+cudaError_t launch_act8_store(const Act8Params& p, cudaStream_t s);
+cudaError_t launch_act8_restore(const Act8Params& p, cudaStream_t s);
+
+struct WgradParams {
+  const __nv_bfloat16* dy; // [rows], row stride ldy elements
+  const uint8_t* codes;    // as above
+  const uint8_t* scales;
+  const void* add;         // [out][cols] of odtype, row stride ldw, or nullptr
+  void* dw;                // [out][cols] of odtype, row stride ldw
+  long long rows, ldy, ldc, lds, ldadd, ldw;
+  int cols, out, odtype;
+};
+cudaError_t launch_act8_wgrad(const WgradParams& p, cudaStream_t s);
+
+// ------------------------------------------------------------ attention
+struct AttnParams {
+  const void *q, *k, *v;   // element (b, s, h, d) at b * s?b + s * s?s + h * s?h + d
+  const void* o;           // backward: the forward pass's output
+  const void* dout;        // backward: its gradient
+  float* lse;              // written by the forward pass, read by the backward pass: (b, h, s) at
+                           // b * lse_b + h * lse_h + s
+  void *out;               // forward: o
+  void *dq, *dk, *dv;      // backward
+  float* delta;            // backward: rowsum(dO * O), laid out as lse
+  long long qb, qs, qh, kb, ks, kh, vb, vs, vh, ob, os, oh, dob, dos, doh;   // strides in elements
+  long long dqb, dqs, dqh, dkb, dks, dkh, dvb, dvs, dvh;
+  long long lse_b, lse_h;
+  const int* cu_q;         // packed: [batch + 1] offsets into the token axis, or nullptr
+  const int* cu_k;
+  int batch, sq, sk;       // packed: sq and sk are the token axes' lengths
+  int heads, kv_heads, dim;
+  int causal, window;      // window > 0: a query sees at most the last `window` keys up to its own place
+  int dtype;
+  float scale;
+};
+cudaError_t launch_attn_fwd(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_bwd(const AttnParams& p, cudaStream_t s);
+
 }  // namespace muon

@@ -1,0 +1,215 @@
+// Activations kept in 8 bits between the forward and the backward pass.
+//
+// Each token's row is cut into blocks of 128 columns.  A block with largest
+// magnitude a is stored as e4m3 codes of x 2^-e, rounded to nearest even,
+// with the smallest e (at least -111) for which a 2^-e <= 448, the largest
+// e4m3 value.  The scale 2^e is a power of two: scaling is exact, the codes
+// are the only rounding, and code times scale is exact in bf16 (4
+// significant bits; e >= -111 keeps the smallest code's value 2^(e-9) a
+// normal bf16 number).  e + 127 is kept in one byte.  A block with a NaN or
+// an infinity gets the byte 255 and codes 0, which restore to NaN: a wrong
+// activation stays visible in every gradient that it reaches.
+//
+// Both directions are bound by HBM.  A group of 16 lanes handles a block, 8
+// columns a lane, so a 16-bit input is one 16-byte load a lane; a warp
+// handles its 16 rows of one block column two at a time, and 16 lanes write
+// the rows' scale bytes at once (scales lie block column by block column,
+// one byte a row, as the weight-gradient kernel reads them).
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "op_common.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int ABLK = 128;       // columns of a block
+constexpr int AROWS = 16;       // rows of a warp's work item
+constexpr int AWARPS = 8;
+
+// The scale byte of a block with largest magnitude a (finite, >= 0).
+__device__ __forceinline__ int scale_byte(float a) {
+  // a = m 2^k, 1 <= m < 2 (a below the normal range: k <= -127, clamped)
+  const int bits = __float_as_int(a);
+  const int k = (bits >> 23) - 127;
+  const int e = (bits & 0x7FFFFF) <= 0x600000 ? k - 8 : k - 7;   // 448 = 1.75 * 2^8
+  return max(e + 127, 16);
+}
+
+// Eight consecutive values of a row from column c, as loaded: zeros past the
+// last column and past the last row.
+template <typename T, bool VEC>
+struct Eight {
+  static constexpr int NV = VEC ? 8 * static_cast<int>(sizeof(T)) / 16 : 1;
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
+  Raw raw[VEC ? NV : 8];
+
+  __device__ __forceinline__ void load(const T* row, int c, int cols, bool in) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        raw[i] = in && c < cols ? ld_stream16(row + c + i * (16 / sizeof(T))) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = in && c + i < cols ? row[c + i] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) unpack16<T>(raw[i], f + i * (16 / sizeof(T)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(raw[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t e4m3x4(const float* f) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// The four values of a word of codes, each times `unit`.
+__device__ __forceinline__ void e4m3x4_values(uint32_t w, float unit, float* f) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * k)), __NV_E4M3));
+    const float2 v = __half22float2(h);
+    f[2 * k] = v.x * unit;
+    f[2 * k + 1] = v.y * unit;
+  }
+}
+
+// A warp takes AROWS rows of one block column, two rows at a time, with the
+// loads of AHEAD row pairs in flight.  Rows of codes are padded to whole
+// blocks, so a lane always writes its eight bytes; columns past the last get
+// code 0.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(AWARPS * 32) act8_store_kernel(const Act8Params p, int blocks) {
+  constexpr int AHEAD = VEC && sizeof(T) == 2 ? 8 : 4;
+  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  const long long groups = (p.rows + AROWS - 1) / AROWS;
+  const long long item = static_cast<long long>(blockIdx.x) * AWARPS + (threadIdx.x >> 5);
+  if (item >= groups * blocks) return;
+  const int blk = static_cast<int>(item % blocks);
+  const long long r0 = item / blocks * AROWS;
+  const int c = blk * ABLK + l * 8;
+  int mine = 0;                       // scale byte of row r0 + l
+#pragma unroll
+  for (int i0 = 0; i0 < AROWS; i0 += 2 * AHEAD) {
+    Eight<T, VEC> in[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const long long r = r0 + i0 + 2 * j + half;
+      in[j].load(static_cast<const T*>(p.x) + r * p.ldx, c, p.cols, r < p.rows);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + 2 * j;
+      const long long r = r0 + i + half;
+      float f[8];
+      in[j].get(f);
+      // magnitudes compare as their bit patterns, NaN above infinity
+      int top = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, __float_as_int(f[k]) & 0x7FFFFFFF);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool fine = top < 0x7F800000;
+      const int e = fine ? scale_byte(__int_as_float(top)) : 255;
+      const float unit = __int_as_float((254 - e) << 23);       // 2^-(e - 127)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = fine ? f[k] * unit : 0.f;
+      if (r < p.rows)
+        *reinterpret_cast<uint2*>(p.codes + r * p.ldc + c) = make_uint2(e4m3x4(f), e4m3x4(f + 4));
+      const int e0 = __shfl_sync(0xffffffffu, e, 0), e1 = __shfl_sync(0xffffffffu, e, 16);
+      if (l == i) mine = e0;
+      if (l == i + 1) mine = e1;
+    }
+  }
+  if (lane < AROWS && r0 + lane < p.rows) p.scales[blk * p.lds + r0 + lane] = static_cast<uint8_t>(mine);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(AWARPS * 32) act8_restore_kernel(const Act8Params p, int blocks) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  const long long groups = (p.rows + AROWS - 1) / AROWS;
+  const long long item = static_cast<long long>(blockIdx.x) * AWARPS + (threadIdx.x >> 5);
+  if (item >= groups * blocks) return;
+  const int blk = static_cast<int>(item % blocks);
+  const long long r0 = item / blocks * AROWS;
+  const int c = blk * ABLK + l * 8;
+  if (c >= p.cols) return;
+  uint2 w[AROWS / 2];
+  int e[AROWS / 2];
+#pragma unroll
+  for (int j = 0; j < AROWS / 2; ++j) {
+    const long long r = r0 + 2 * j + half;
+    const bool in = r < p.rows;
+    w[j] = in ? *reinterpret_cast<const uint2*>(p.codes + r * p.ldc + c) : make_uint2(0u, 0u);
+    e[j] = in ? p.scales[blk * p.lds + r] : 0;
+  }
+#pragma unroll
+  for (int j = 0; j < AROWS / 2; ++j) {
+    const long long r = r0 + 2 * j + half;
+    if (r >= p.rows) break;
+    float f[8];
+    const float unit = __int_as_float(e[j] << 23);              // 255: infinity, times code 0: NaN
+    e4m3x4_values(w[j].x, unit, f);
+    e4m3x4_values(w[j].y, unit, f + 4);
+    T* row = static_cast<T*>(p.out) + r * p.ldx;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 16 / static_cast<int>(sizeof(T)))
+        *reinterpret_cast<uint4*>(row + c + i) = pack16<T>(f + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < p.cols) row[c + i] = from_f32<T>(f[i]);
+    }
+  }
+}
+
+// 16-byte loads (stores) need rows of whole 8-column groups on 16-byte
+// boundaries; anything else goes element by element.
+template <typename T>
+cudaError_t launch_type(const Act8Params& p, bool store, cudaStream_t s) {
+  const int blocks = (p.cols + ABLK - 1) / ABLK;
+  const long long items = (p.rows + AROWS - 1) / AROWS * blocks;
+  const long long ctas = (items + AWARPS - 1) / AWARPS;
+  if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(ctas));
+  const void* base = store ? p.x : p.out;
+  const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0 &&
+                   p.ldx * static_cast<long long>(sizeof(T)) % 16 == 0;
+  if (store) {
+    if (vec)
+      act8_store_kernel<T, true><<<grid, AWARPS * 32, 0, s>>>(p, blocks);
+    else
+      act8_store_kernel<T, false><<<grid, AWARPS * 32, 0, s>>>(p, blocks);
+  } else {
+    if (vec)
+      act8_restore_kernel<T, true><<<grid, AWARPS * 32, 0, s>>>(p, blocks);
+    else
+      act8_restore_kernel<T, false><<<grid, AWARPS * 32, 0, s>>>(p, blocks);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_any(const Act8Params& p, bool store, cudaStream_t s) {
+  switch (p.dtype) {
+    case DT_F32: return launch_type<float>(p, store, s);
+    case DT_BF16: return launch_type<__nv_bfloat16>(p, store, s);
+    default: return launch_type<__half>(p, store, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_act8_store(const Act8Params& p, cudaStream_t s) { return launch_any(p, true, s); }
+cudaError_t launch_act8_restore(const Act8Params& p, cudaStream_t s) { return launch_any(p, false, s); }
+
+}  // namespace muon

@@ -1,0 +1,354 @@
+// C ABI of the training operators (see include/muon.h): checks of the
+// arguments, workspace layout and launches.  No exception leaves an entry.
+#include <cmath>
+#include <string>
+
+#include "common.cuh"
+#include "handle.h"
+#include "internal.h"
+#include "muon.h"
+
+using namespace muon;
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;     // token and row counts fit an int with room to spare
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
+bool op_dtype(int32_t t) { return t == MUON_F32 || t == MUON_BF16 || t == MUON_F16; }
+
+template <typename F>
+muon_status_t guarded(F&& f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return MUON_ERR_WORKSPACE;       // host memory ran out
+  }
+}
+
+#define MUON_CHECK(cond, msg) \
+  do {                        \
+    if (!(cond)) return fail(h, MUON_ERR_INVALID_ARG, msg); \
+  } while (0)
+
+muon_status_t check_norm(muon_handle_t h, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype) {
+  MUON_CHECK(rows >= 0 && rows <= kMaxTokens, "rows must be in [0, 2^30]");
+  MUON_CHECK(cols >= 1 && cols <= kNormMaxCols, "cols must be in [1, 16384]");
+  MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
+  MUON_CHECK(wdtype == MUON_F32 || wdtype == dtype, "wdtype must be MUON_F32 or dtype");
+  return MUON_OK;
+}
+
+muon_status_t check_act8(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                         int64_t rows, int64_t cols) {
+  MUON_CHECK(rows >= 0 && rows <= kMaxTokens && cols >= 0 && cols <= kMaxTokens, "negative or oversized shape");
+  if (rows == 0 || cols == 0) return MUON_OK;
+  MUON_CHECK(codes != nullptr && scales != nullptr, "codes or scales is NULL");
+  MUON_CHECK(ldc % 128 == 0 && ldc >= cols && aligned(codes, 16),
+             "codes need a row stride that is a multiple of 128 and a 16-byte aligned start");
+  MUON_CHECK(lds % 16 == 0 && lds >= rows && aligned(scales, 16),
+             "scales need a block stride that is a multiple of 16 and a 16-byte aligned start");
+  return MUON_OK;
+}
+
+uint64_t attn_workspace(const muon_attention_t& a) {
+  const uint64_t b = a.cu_seqlens_q != nullptr ? 1 : static_cast<uint64_t>(a.batch);
+  return round256(b * static_cast<uint64_t>(a.heads) * static_cast<uint64_t>(a.sq) * 4);
+}
+
+muon_status_t check_attention(muon_handle_t h, const muon_attention_t* a) {
+  MUON_CHECK(a != nullptr, "a is NULL");
+  MUON_CHECK(a->batch >= 0 && a->sq >= 0 && a->sk >= 0 && a->sq <= kMaxTokens && a->sk <= kMaxTokens,
+             "negative or oversized shape");
+  MUON_CHECK(a->batch <= 65535, "batch must be at most 65535");
+  MUON_CHECK(a->heads >= 1 && a->heads <= 65535 && a->kv_heads >= 1 && a->heads % a->kv_heads == 0,
+             "heads must be in [1, 65535] and a multiple of kv_heads");
+  MUON_CHECK(a->dim >= 8 && a->dim <= 128 && a->dim % 8 == 0, "dim must be a multiple of 8 in [8, 128]");
+  MUON_CHECK(a->dtype == MUON_BF16 || a->dtype == MUON_F16, "dtype must be MUON_BF16 or MUON_F16");
+  MUON_CHECK(a->window >= 0 && (a->window == 0 || a->causal), "a window needs causal = 1 and a length >= 0");
+  MUON_CHECK(std::isfinite(a->scale), "non-finite scale");
+  MUON_CHECK((a->cu_seqlens_q == nullptr) == (a->cu_seqlens_k == nullptr),
+             "cu_seqlens_q and cu_seqlens_k go together");
+  return MUON_OK;
+}
+
+bool bad_operand(const void* p, const int64_t* st, bool packed) {
+  return p == nullptr || !aligned(p, 16) || st[1] % 8 || st[2] % 8 || (!packed && st[0] % 8) || st[1] < 0 ||
+         st[2] < 0 || (!packed && st[0] < 0);
+}
+
+AttnParams attn_params(const muon_attention_t& a) {
+  AttnParams p{};
+  const bool packed = a.cu_seqlens_q != nullptr;
+  auto set = [packed](const int64_t* st, long long* b, long long* s, long long* hh) {
+    *b = packed ? 0 : st[0];
+    *s = st[1];
+    *hh = st[2];
+  };
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.lse = a.lse;
+  set(a.q_stride, &p.qb, &p.qs, &p.qh);
+  set(a.k_stride, &p.kb, &p.ks, &p.kh);
+  set(a.v_stride, &p.vb, &p.vs, &p.vh);
+  set(a.o_stride, &p.ob, &p.os, &p.oh);
+  set(a.dout_stride, &p.dob, &p.dos, &p.doh);
+  set(a.dq_stride, &p.dqb, &p.dqs, &p.dqh);
+  set(a.dk_stride, &p.dkb, &p.dks, &p.dkh);
+  set(a.dv_stride, &p.dvb, &p.dvs, &p.dvh);
+  p.lse_h = a.sq;
+  p.lse_b = static_cast<long long>(a.heads) * a.sq;
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_k = a.cu_seqlens_k;
+  p.batch = a.batch;
+  p.sq = a.sq;
+  p.sk = a.sk;
+  p.heads = a.heads;
+  p.kv_heads = a.kv_heads;
+  p.dim = a.dim;
+  p.causal = a.causal ? 1 : 0;
+  p.window = a.window;
+  p.dtype = a.dtype;
+  p.scale = a.scale;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status_t muon_layer_norm_forward(muon_handle_t h, const void* x, int64_t ldx, const void* weight,
+                                      const void* bias, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows,
+                                      int64_t cols, int32_t dtype, int32_t wdtype, float eps, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_norm(h, rows, cols, dtype, wdtype);
+    if (st != MUON_OK) return st;
+    MUON_CHECK(std::isfinite(eps) && eps >= 0.f, "eps must be finite and not negative");
+    if (rows == 0) return MUON_OK;
+    MUON_CHECK(x != nullptr && y != nullptr && mean != nullptr && rstd != nullptr, "NULL tensor pointer");
+    MUON_CHECK((ldx >= cols && ldy >= cols) || rows == 1, "row strides must be at least cols");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    NormParams p{};
+    p.x = x;
+    p.y = y;
+    p.weight = weight;
+    p.bias = bias;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.rows = rows;
+    p.ldx = ldx;
+    p.ldy = ldy;
+    p.cols = static_cast<int>(cols);
+    p.dtype = dtype;
+    p.wdtype = wdtype;
+    p.eps = eps;
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_fwd(p, norm_parts(rows, p.cols, h->num_sms), stream),
+                "layer norm launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_layer_norm_workspace(muon_handle_t h, int64_t rows, int64_t cols, uint64_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_norm(h, rows, cols, MUON_F32, MUON_F32);
+    if (st != MUON_OK) return st;
+    *bytes = round256(static_cast<uint64_t>(norm_parts(rows, static_cast<int>(cols), h->num_sms)) * 2 * cols * 4);
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                       const float* mean, const float* rstd, const void* weight, void* dx,
+                                       int64_t lddx, float* dweight, float* dbias, int64_t rows, int64_t cols,
+                                       int32_t dtype, int32_t wdtype, void* workspace, size_t workspace_bytes,
+                                       void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    uint64_t need = 0;
+    muon_status_t st = check_norm(h, rows, cols, dtype, wdtype);
+    if (st == MUON_OK) st = muon_layer_norm_workspace(h, rows, cols, &need);
+    if (st != MUON_OK) return st;
+    MUON_CHECK(dweight != nullptr && dbias != nullptr, "dweight or dbias is NULL");
+    NormParams p{};
+    p.cols = static_cast<int>(cols);
+    const int parts = norm_parts(rows, p.cols, h->num_sms);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    if (rows > 0) {
+      MUON_CHECK(dy != nullptr && x != nullptr && dx != nullptr && mean != nullptr && rstd != nullptr,
+                 "NULL tensor pointer");
+      MUON_CHECK((ldx >= cols && lddx >= cols && lddy >= cols) || rows == 1, "row strides must be at least cols");
+      MUON_CHECK(workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256),
+                 "the workspace is too small or not 256-byte aligned");
+    }
+    DeviceGuard guard(h->device);
+    p.x = x;
+    p.dy = dy;
+    p.y = dx;
+    p.weight = weight;
+    p.mean = const_cast<float*>(mean);
+    p.rstd = const_cast<float*>(rstd);
+    p.part = static_cast<float*>(workspace);
+    p.rows = rows;
+    p.ldx = ldx;
+    p.ldy = lddx;
+    p.lddy = lddy;
+    p.dtype = dtype;
+    p.wdtype = wdtype;
+    h->prof_tag = -1;
+    if (rows > 0) MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_bwd(p, parts, stream), "layer norm backward launch");
+    MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_join(p, parts, dweight, dbias, stream), "layer norm join launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_attention(h, a);
+    if (st != MUON_OK) return st;
+    const bool packed = a->cu_seqlens_q != nullptr;
+    if (a->sq == 0 || (a->batch == 0 && !packed)) return MUON_OK;
+    MUON_CHECK(!bad_operand(a->q, a->q_stride, packed) && !bad_operand(a->o, a->o_stride, packed) &&
+                   (a->sk == 0 ||
+                    (!bad_operand(a->k, a->k_stride, packed) && !bad_operand(a->v, a->v_stride, packed))),
+               "operands need 16-byte aligned pointers and strides that are multiples of 8 elements");
+    MUON_CHECK(a->lse != nullptr, "lse is NULL");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    AttnParams p = attn_params(*a);
+    p.out = a->o;
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_fwd(p, stream), "attention launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_attention_workspace(muon_handle_t h, const muon_attention_t* a, uint64_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_attention(h, a);
+    if (st != MUON_OK) return st;
+    *bytes = attn_workspace(*a);
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a, void* workspace,
+                                      size_t workspace_bytes, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_attention(h, a);
+    if (st != MUON_OK) return st;
+    const bool packed = a->cu_seqlens_q != nullptr;
+    if ((a->sq == 0 && a->sk == 0) || (a->batch == 0 && !packed)) return MUON_OK;
+    auto bad = [&](const void* q, const int64_t* s) { return bad_operand(q, s, packed); };
+    MUON_CHECK((a->sq == 0 || !(bad(a->q, a->q_stride) || bad(a->o, a->o_stride) || bad(a->dout, a->dout_stride) ||
+                                bad(a->dq, a->dq_stride))) &&
+                   (a->sk == 0 || !(bad(a->k, a->k_stride) || bad(a->v, a->v_stride) || bad(a->dk, a->dk_stride) ||
+                                    bad(a->dv, a->dv_stride))),
+               "operands need 16-byte aligned pointers and strides that are multiples of 8 elements");
+    if (a->sq > 0) {
+      MUON_CHECK(a->lse != nullptr, "lse is NULL");
+      MUON_CHECK(workspace != nullptr && workspace_bytes >= attn_workspace(*a) && aligned(workspace, 256),
+                 "the workspace is too small or not 256-byte aligned");
+    }
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    AttnParams p = attn_params(*a);
+    p.o = a->o;
+    p.dout = a->dout;
+    p.dq = a->dq;
+    p.dk = a->dk;
+    p.dv = a->dv;
+    p.delta = static_cast<float*>(workspace);
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, stream), "attention backward launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_store(muon_handle_t h, const void* x, int64_t ldx, uint8_t* codes, int64_t ldc,
+                              uint8_t* scales, int64_t lds, int64_t rows, int64_t cols, int32_t dtype,
+                              void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
+    const muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
+    if (st != MUON_OK) return st;
+    if (rows == 0 || cols == 0) return MUON_OK;
+    MUON_CHECK(x != nullptr && (ldx >= cols || rows == 1), "x is NULL or its row stride is below cols");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    const Act8Params p{x, nullptr, codes, scales, rows, ldx, ldc, lds, static_cast<int>(cols), dtype};
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_ACT8, launch_act8_store(p, stream), "act8 store launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                int64_t lds, void* out, int64_t ldo, int64_t rows, int64_t cols, int32_t dtype,
+                                void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
+    const muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
+    if (st != MUON_OK) return st;
+    if (rows == 0 || cols == 0) return MUON_OK;
+    MUON_CHECK(out != nullptr && (ldo >= cols || rows == 1), "out is NULL or its row stride is below cols");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    const Act8Params p{nullptr, out,  const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), rows, ldo, ldc,
+                       lds,     static_cast<int>(cols), dtype};
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_ACT8, launch_act8_restore(p, stream), "act8 restore launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, int64_t rows, int64_t cols, int64_t out, int64_t lddy,
+                                              uint64_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    MUON_CHECK(rows >= 0 && rows <= kMaxTokens && cols >= 0 && cols <= kMaxTokens && out >= 0 && out <= kMaxTokens,
+               "negative or oversized shape");
+    (void)lddy;
+    *bytes = 0;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t lddy, const uint8_t* codes, int64_t ldc,
+                                    const uint8_t* scales, int64_t lds, const void* add, int64_t ldadd, void* dw,
+                                    int64_t lddw, int64_t rows, int64_t cols, int64_t out, int32_t odtype,
+                                    void* workspace, size_t workspace_bytes, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    uint64_t need = 0;
+    muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
+    if (st == MUON_OK) st = muon_act8_weight_grad_workspace(h, rows, cols, out, lddy, &need);
+    if (st != MUON_OK) return st;
+    MUON_CHECK(odtype == MUON_F32 || odtype == MUON_BF16, "odtype must be MUON_F32 or MUON_BF16");
+    if (cols == 0 || out == 0) return MUON_OK;
+    MUON_CHECK(dw != nullptr && (lddw >= cols || out == 1), "dw is NULL or its row stride is below cols");
+    MUON_CHECK(add == nullptr || ldadd >= cols || out == 1, "add's row stride is below cols");
+    MUON_CHECK(rows == 0 || (dy != nullptr && (lddy >= out || rows == 1)), "dy is NULL or its row stride is below out");
+    MUON_CHECK(need == 0 || (workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256)),
+               "the workspace is too small or not 256-byte aligned");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    const WgradParams p{static_cast<const __nv_bfloat16*>(dy), codes, scales, add, dw, rows, lddy, ldc, lds, ldadd,
+                        lddw, static_cast<int>(cols), static_cast<int>(out), odtype};
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, stream), "weight gradient launch");
+    return MUON_OK;
+  });
+}
+
+}  // extern "C"

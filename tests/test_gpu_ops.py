@@ -1,0 +1,476 @@
+"""The training operators on the GPU against their plain 64-bit forms.
+
+Tolerances, element by element.  u is the unit roundoff of the storage type:
+2^-8 for bf16 (8 significant bits), 2^-11 for fp16, 2^-24 for fp32.
+  * One rounding to the output type: u |ref|.
+  * Attention forms p (and ds) in fp32 and rounds it once to the operand type
+    before the second product, so a sum of products is off by at most
+    u sum |p||v|.  fp32 arithmetic before that (a dot product of up to 128
+    products, an exponential of an argument below 2^8, the difference dP -
+    delta) stays below 2^-15 of the terms' magnitudes.
+  * Layer norm: fp32 sums of up to 16384 terms held in partial sums of at
+    most a few dozen: 2^-19 of the terms' magnitudes; sums over rows 2^-18.
+  * The weight gradient multiplies exact bf16 factors and sums in fp32, 16
+    products at a time: (rows / 16 + 16) 2^-23 of the terms' magnitudes.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from _margins import record
+from oracle import ops_oracle as oo
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def muon():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import newton_schulz_orthogonalized_muon_gb300 as pkg
+    torch.cuda.set_device(0)
+    return pkg
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rand(seed, *shape, dtype=FP, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def close(name, got, ref, tol):
+    """|got - ref| <= tol element by element; where ref is not finite, got is the same."""
+    got, ref = host(got) if isinstance(got, torch.Tensor) else got, np.asarray(ref)
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    fine = np.isfinite(ref)
+    assert np.array_equal(got[~fine], ref[~fine], equal_nan=True), name
+    tol = np.broadcast_to(np.maximum(tol, 1e-30), ref.shape)
+    ratio = float(np.max(np.abs(got[fine] - ref[fine]) / tol[fine], initial=0.0))
+    record(name, ratio, 1.0)
+    assert ratio <= 1.0, (name, ratio)
+
+
+# ---------------------------------------------------------------- layer norm
+NORM = [  # rows, cols, pad, dtype, wdtype
+    (1, 1, 0, FP, FP), (3, 7, 0, BF, FP), (5, 256, 0, BF, BF), (9, 257, 0, HF, FP), (4, 768, 0, BF, FP),
+    (33, 1023, 6, FP, FP), (2, 1024, 0, HF, HF), (7, 2048, 8, BF, FP), (3, 4096, 0, BF, BF), (611, 4096, 0, BF, FP),
+    (2, 5000, 0, FP, FP), (3, 8192, 0, BF, FP), (3, 9001, 3, BF, FP), (5, 16384, 0, BF, FP), (2, 16384, 0, FP, FP),
+    (1301, 33, 0, BF, FP), (700, 1000, 0, HF, FP), (0, 64, 0, BF, FP)]
+
+
+@pytest.mark.parametrize("rows,cols,pad,dtype,wdtype", NORM)
+def test_layer_norm(muon, rows, cols, pad, dtype, wdtype):
+    x = (rand(1, rows, cols + pad) * 3 + 5).to(dtype)[:, :cols]
+    dy = rand(2, rows, cols + pad, dtype=dtype)[:, :cols]
+    w, b = (1 + rand(3, cols) * 0.3).to(wdtype), rand(4, cols, dtype=wdtype)
+    y, mean, rstd = muon.layer_norm(x, w, b, eps=1e-5)
+    dx, dw, db = muon.layer_norm_backward(dy, x, mean, rstd, w)
+    assert y.dtype == dx.dtype == dtype and dw.dtype == db.dtype == FP
+    xd, dyd, wd, bd = host(x), host(dy), host(w), host(b)
+    yr, mr, rr = oo.layer_norm(xd, wd, bd, 1e-5) if rows else (np.zeros((0, cols)), np.zeros(0), np.zeros(0))
+    tag = f"layer norm {rows}x{cols} {dtype}"
+    e = 2.0 ** -19
+    xmag = np.abs(xd).mean(1) if rows else np.zeros(0)
+    close(tag + " mean", mean, mr, e * xmag)
+    # the mean's error shifts every x - mean; relative to the spread it enters rstd squared
+    off = e * xmag * rr
+    close(tag + " rstd", rstd, rr, rr * (e + off * off + e * np.abs(xd).max(1, initial=0) * rr))
+    xh = np.abs(xd - mr[:, None]) * rr[:, None]
+    inner = off[:, None] + (e + (e * np.abs(xd).max(1, initial=0) * rr)[:, None]) * xh
+    close(tag + " y", y, yr, U[dtype] * np.abs(yr) + inner * np.abs(wd) + e * (xh * np.abs(wd) + np.abs(bd)))
+    # the backward pass takes the mean and rstd that it is given
+    md, rd = host(mean), host(rstd)
+    dxr, dwr, dbr = oo.layer_norm_backward(dyd, xd, md, rd, wd) if rows else (np.zeros((0, cols)), np.zeros(cols),
+                                                                              np.zeros(cols))
+    g = np.abs(dyd * wd)
+    xh = (np.abs(xd) + np.abs(md)[:, None]) * rd[:, None]
+    xt = np.abs(xd - md[:, None]) * rd[:, None]
+    mag = rd[:, None] * (g + (g.mean(1, keepdims=True) if rows else 0)
+                         + xh * ((g * xt).mean(1, keepdims=True) if rows else 0)
+                         + xt * ((g * xh).mean(1, keepdims=True) if rows else 0))
+    close(tag + " dx", dx, dxr, U[dtype] * np.abs(dxr) + e * mag)
+    close(tag + " dw", dw, dwr, 2.0 ** -18 * (np.abs(dyd) * xh).sum(0))
+    close(tag + " db", db, dbr, 2.0 ** -18 * np.abs(dyd).sum(0))
+
+
+def test_layer_norm_without_weights_and_in_more_dimensions(muon):
+    x = rand(5, 3, 4, 96, dtype=BF)
+    y, mean, rstd = muon.layer_norm(x)
+    assert y.shape == x.shape and mean.shape == rstd.shape == (3, 4)
+    yr, _, _ = oo.layer_norm(host(x).reshape(12, 96), np.ones(96), np.zeros(96), 1e-5)
+    close("layer norm plain", y.reshape(12, 96), yr, U[BF] * np.abs(yr) + 2.0 ** -17)
+    dx, dw, db = muon.layer_norm_backward(x, x, mean, rstd)
+    assert dx.shape == x.shape
+    t = x.transpose(0, 1)                       # rows without one stride: copied
+    assert torch.equal(muon.layer_norm(t)[0], y.transpose(0, 1))
+    assert torch.equal(muon.layer_norm_backward(t, t, mean.t().contiguous(), rstd.t().contiguous())[0],
+                       dx.transpose(0, 1))
+
+
+def test_layer_norm_far_mean_does_not_cancel(muon):
+    x = rand(6, 8, 1000) + 4096.0
+    y, mean, rstd = muon.layer_norm(x)
+    yr, _, rr = oo.layer_norm(host(x), 1.0, 0.0, 1e-5)
+    # x - mean is exact to the mean's own rounding (half an ulp of 4096)
+    close("far mean y", y, yr, 2.0 ** -12 + 2.0 ** -10 * np.abs(yr))
+    close("far mean rstd", rstd, rr, 2.0 ** -18 * rr)
+
+
+def test_layer_norm_gradient_against_differences(muon):
+    x, w, b, g = rand(7, 4, 24), 1 + rand(8, 24) * 0.2, rand(9, 24), rand(10, 4, 24)
+    _, mean, rstd = muon.layer_norm(x, w, b)
+    dx, dw, db = muon.layer_norm_backward(g, x, mean, rstd, w)
+    gd, h = host(g), 1e-6
+
+    def loss(xx, ww, bb):
+        return (oo.layer_norm(xx, ww, bb, 1e-5)[0] * gd).sum()
+    args = [host(x), host(w), host(b)]
+    for i, got in enumerate((dx, dw, db)):
+        num = np.zeros(args[i].size)
+        for j in range(args[i].size):
+            up, dn = [a.copy() for a in args], [a.copy() for a in args]
+            up[i].flat[j] += h
+            dn[i].flat[j] -= h
+            num[j] = (loss(*up) - loss(*dn)) / (2 * h)
+        close(f"layer norm difference {i}", got, num.reshape(args[i].shape), np.full(args[i].shape, 2e-5))
+
+
+def test_layer_norm_nan_stays_in_its_row(muon):
+    x = rand(11, 5, 512, dtype=BF)
+    want = muon.layer_norm(x)[0]
+    x[2, 7] = float("nan")
+    got = muon.layer_norm(x)[0]
+    assert got[2].isnan().all() and torch.equal(got[[0, 1, 3, 4]], want[[0, 1, 3, 4]])
+
+
+# ----------------------------------------------------------------- attention
+ATTN = [  # batch, sq, sk, heads, kv_heads, dim, causal, window, dtype
+    (1, 1, 1, 1, 1, 8, True, 0, BF), (2, 61, 61, 3, 3, 64, True, 0, BF), (1, 128, 128, 2, 1, 128, True, 0, BF),
+    (1, 129, 129, 4, 1, 128, True, 0, HF), (1, 127, 257, 2, 2, 64, False, 0, BF), (2, 300, 300, 4, 2, 128, True, 0, HF),
+    (1, 1, 517, 4, 2, 128, True, 0, BF), (1, 517, 1, 2, 2, 64, False, 0, BF), (1, 200, 70, 2, 1, 64, True, 0, BF),
+    (1, 70, 333, 2, 1, 40, True, 0, HF), (2, 260, 260, 2, 2, 72, True, 1, BF), (1, 400, 400, 2, 1, 128, True, 130, BF),
+    (1, 513, 600, 1, 1, 96, True, 37, BF), (1, 300, 200, 1, 1, 64, True, 20, HF), (1, 640, 640, 2, 2, 64, True, 0, BF),
+    (3, 65, 63, 2, 2, 24, False, 0, HF), (1, 256, 0, 2, 2, 64, False, 0, BF), (1, 1030, 1030, 1, 1, 128, False, 0, BF),
+    (1, 5, 900, 8, 1, 120, True, 0, BF)]
+
+
+def attn_tol(u, ref, mag, wide=None):
+    return u * np.abs(ref) + (1.02 * u) * mag + 2.0 ** -15 * (mag if wide is None else wide)
+
+
+def check_attention(tag, dtype, scale, causal, window, spans, q, k, v, do, o, lse, grads):
+    """spans: (batch index or None, q0, q1, k0, k1) of each sequence."""
+    qd, kd, vd, dod, od, ld = (host(t) for t in (q, k, v, do, o, lse))
+    dq, dk, dv = (host(t) for t in grads)
+    u = U[dtype]
+    for n, (b, q0, q1, k0, k1) in enumerate(spans):
+        at = (lambda t, i0, i1: t[i0:i1]) if b is None else (lambda t, i0, i1: t[b, i0:i1])
+        ls = ld[:, q0:q1] if b is None else ld[b]
+        qs, ks, vs, gs, os_ = at(qd, q0, q1), at(kd, k0, k1), at(vd, k0, k1), at(dod, q0, q1), at(od, q0, q1)
+        ref, lr, mag = oo.attention(qs, ks, vs, causal, window, scale)
+        close(f"{tag} o {n}", os_, ref, attn_tol(u, ref, mag))
+        smag = np.abs(np.where(np.isfinite(lr), lr, 0)) + 1
+        close(f"{tag} lse {n}", ls, lr, 2.0 ** -17 * smag)
+        refs, mags, wides = oo.attention_backward(gs, qs, ks, vs, os_, causal, window, scale)
+        for name, got, r, m, wd in zip(("dq", "dk", "dv"), (at(dq, q0, q1), at(dk, k0, k1), at(dv, k0, k1)), refs,
+                                       mags, wides):
+            close(f"{tag} {name} {n}", got, r, attn_tol(u, r, m, wd))
+
+
+@pytest.mark.parametrize("batch,sq,sk,heads,kv,dim,causal,window,dtype", ATTN)
+def test_attention(muon, batch, sq, sk, heads, kv, dim, causal, window, dtype):
+    q, k, v = rand(20, batch, sq, heads, dim, dtype=dtype), rand(21, batch, sk, kv, dim, dtype=dtype), \
+        rand(22, batch, sk, kv, dim, dtype=dtype)
+    do = rand(23, batch, sq, heads, dim, dtype=dtype)
+    kw = dict(causal=causal, window=window)
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    assert muon.default_handle().check() == 0
+    spans = [(b, 0, sq, 0, sk) for b in range(batch)]
+    check_attention(f"attention {sq}x{sk} h{heads}/{kv} d{dim} {dtype}", dtype, dim ** -0.5, causal, window, spans, q,
+                    k, v, do, o, lse, grads)
+    # the same call again: the same bits
+    assert torch.equal(o, muon.attention(q, k, v, **kw)[0])
+    for a, b in zip(grads, muon.attention_backward(do, q, k, v, o, lse, **kw)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cuts_q,cuts_k", [
+    ([0, 0, 1, 130, 130, 386, 391, 647], None), ([0, 300], None), ([0, 5, 135, 140], [0, 200, 210, 210]),
+    ([0, 64, 64, 128], [0, 0, 30, 300])])
+def test_packed_attention(muon, causal, cuts_q, cuts_k):
+    cuts_k = cuts_q if cuts_k is None else cuts_k
+    h, kv, d, dtype = 4, 2, 64, BF
+    fused = rand(30, max(cuts_q[-1], cuts_k[-1]), h + 2 * kv, d, dtype=dtype)
+    q, k, v = fused[:cuts_q[-1], :h], fused[:cuts_k[-1], h:h + kv], fused[:cuts_k[-1], h + kv:]
+    do = rand(31, cuts_q[-1], h, d, dtype=dtype)
+    kw = dict(causal=causal, cu_seqlens_q=torch.tensor(cuts_q, dtype=torch.int32).cuda(),
+              cu_seqlens_k=torch.tensor(cuts_k, dtype=torch.int32).cuda())
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    spans = [(None, *s) for s in zip(cuts_q, cuts_q[1:], cuts_k, cuts_k[1:])]
+    check_attention(f"packed {cuts_q} {causal}", dtype, d ** -0.5, causal, 0, spans, q, k, v, do, o, lse, grads)
+
+
+def test_packed_tokens_of_no_sequence_and_bad_offsets(muon):
+    q = rand(32, 400, 2, 64, dtype=BF)
+    for cuts in ([10, 200, 390], [0, 200, 100, 5000], [-7, 150, 150]):
+        cu = torch.tensor(cuts, dtype=torch.int32).cuda()
+        kw = dict(causal=True, cu_seqlens_q=cu, cu_seqlens_k=cu)
+        o, lse = muon.attention(q, q, q, **kw)
+        grads = muon.attention_backward(q, q, q, q, o, lse, **kw)
+        cut = lambda c: min(max(c, 0), 400)  # noqa: E731
+        spans = [(cut(a), max(cut(b), cut(a))) for a, b in zip(cuts, cuts[1:])]
+        inside = torch.zeros(400, dtype=torch.bool)
+        for a, b in spans:
+            inside[a:b] = True
+        if cuts[0] == 10:
+            assert (o[~inside] == 0).all() and (lse[:, ~inside.cuda()] == -math.inf).all()
+            assert all((g[~inside] == 0).all() for g in grads)
+        assert all(torch.isfinite(g).all() for g in grads) and torch.isfinite(o).all()
+    assert muon.default_handle().check() == 0
+
+
+def test_attention_keys_past_the_end_have_no_part(muon):
+    """NaN and infinity next to a sequence (rows past its end, other documents, other heads)."""
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        big = [rand(40 + i, 2, 300, 4, 64, dtype=BF) for i in range(4)]
+        q, k, v, do = (t[:, 20:181, 1:3] for t in big)
+        want = [t.clone() for t in (q, k, v, do)]
+        o0, l0 = muon.attention(*want[:3], causal=True)
+        g0 = muon.attention_backward(want[3], *want[:3], o0, l0, causal=True)
+        for t in big:
+            keep = t[:, 20:181, 1:3].clone()
+            t.fill_(bad)
+            t[:, 20:181, 1:3] = keep
+        o1, l1 = muon.attention(q, k, v, causal=True)
+        g1 = muon.attention_backward(do, q, k, v, o1, l1, causal=True)
+        assert torch.equal(o0, o1) and torch.equal(l0, l1) and all(torch.equal(a, b) for a, b in zip(g0, g1))
+        # a document of such values beside a fine one
+        cu = torch.tensor([0, 100, 161, 300], dtype=torch.int32).cuda()
+        x = rand(44, 300, 2, 64, dtype=BF)
+        kw = dict(causal=False, cu_seqlens_q=cu, cu_seqlens_k=cu)
+        o0, l0 = muon.attention(x, x, x, **kw)
+        g0 = muon.attention_backward(x, x, x, x, o0, l0, **kw)
+        y = x.clone()
+        y[100:161] = bad
+        o1, l1 = muon.attention(y, y, y, **kw)
+        g1 = muon.attention_backward(y, y, y, y, o1, l1, **kw)
+        for a, b in ((o0, o1), *zip(g0, g1)):
+            assert torch.equal(a[:100], b[:100]) and torch.equal(a[161:], b[161:])
+
+
+@pytest.mark.parametrize("gain", [1e-4, 8.0, 40.0])
+def test_attention_range_of_scores(muon, gain):
+    """Scores near zero (a flat softmax) and far beyond exp's range."""
+    q, k, v, do = (rand(50 + i, 1, 333, 2, 64, dtype=BF) for i in range(4))
+    q = (q.float() * gain).to(BF)
+    o, lse = muon.attention(q, k, v)
+    ref, lr, mag = oo.attention(host(q)[0], host(k)[0], host(v)[0], False, 0, 0.125)
+    # an fp32 score of magnitude s is off by up to 2^-22 s, and p by as much, relatively
+    smax = np.abs(lr).max() + 1
+    extra = 2.0 ** -21 * smax
+    close(f"scores x{gain} o", o[0], ref, attn_tol(U[BF], ref, mag) + extra * mag)
+    close(f"scores x{gain} lse", lse[0], lr, 2.0 ** -17 + 2.0 ** -21 * np.abs(lr))
+    grads = muon.attention_backward(do, q, k, v, o, lse)
+    refs, mags, wides = oo.attention_backward(*(host(t)[0] for t in (do, q, k, v, o)), False, 0, 0.125)
+    for name, g, r, m, w in zip(("dq", "dk", "dv"), grads, refs, mags, wides):
+        close(f"scores x{gain} {name}", g[0], r, attn_tol(U[BF], r, m, w) + extra * w)
+
+
+def test_attention_gradient_against_differences(muon):
+    """Directional differences of the 64-bit forward form."""
+    q, k, v, do = (rand(60 + i, 1, 40, 2, 32, dtype=HF) for i in range(4))
+    o, lse = muon.attention(q, k, v, causal=True, scale=0.2)
+    grads = muon.attention_backward(do, q, k, v, o, lse, causal=True, scale=0.2)
+    args, g, h = [host(t)[0] for t in (q, k, v)], host(do)[0], 1e-5
+    rng = np.random.default_rng(1)
+    for i in range(3):
+        for _ in range(4):
+            d = rng.standard_normal(args[i].shape)
+            up, dn = [a.copy() for a in args], [a.copy() for a in args]
+            up[i] += h * d
+            dn[i] -= h * d
+            num = ((oo.attention(*up, True, 0, 0.2)[0] - oo.attention(*dn, True, 0, 0.2)[0]) * g).sum() / (2 * h)
+            got = (host(grads[i])[0] * d).sum()
+            # o is rounded before delta, each gradient once at the end: u of the sum's magnitude, with room for
+            # the roundings inside
+            tol = 4 * U[HF] * (np.abs(host(grads[i])[0]) * np.abs(d)).sum() + 1e-6
+            record(f"attention difference {i}", abs(got - num) / tol, 1.0)
+            assert abs(got - num) <= tol
+
+
+def test_attention_strided_and_expanded_operands(muon):
+    qkv = rand(70, 2, 190, 3, 4, 64, dtype=BF)
+    q, k, v = qkv.unbind(2)
+    want = [t.contiguous() for t in (q, k, v)]
+    assert torch.equal(muon.attention(q, k, v, causal=True)[0], muon.attention(*want, causal=True)[0])
+    bhsd = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in want]     # heads outside tokens
+    o, lse = muon.attention(*bhsd, causal=True)
+    assert torch.equal(o, muon.attention(*want, causal=True)[0])
+    one = torch.ones(1, 1, 1, 1, dtype=BF, device="cuda").expand(2, 190, 4, 64)   # the gradient of a sum
+    a = muon.attention_backward(one, *want, o, lse, causal=True)
+    b = muon.attention_backward(one.contiguous(), q, k, v, o, lse, causal=True)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# --------------------------------------------------- activations in 8 bits
+@pytest.mark.parametrize("rows,cols,pad,dtype", [
+    (1, 1, 0, BF), (5, 127, 0, BF), (17, 128, 0, HF), (33, 129, 0, FP), (16, 768, 0, BF), (40, 1000, 24, BF),
+    (21, 1001, 2, HF), (50, 513, 0, FP), (100, 256, 0, FP)])
+def test_act8_codes_are_exact(muon, rows, cols, pad, dtype):
+    x = (rand(80, rows, cols + pad) * torch.exp(2 * rand(81, cols + pad))).to(dtype)
+    if rows > 12:
+        x[2] = 0
+        x[3] *= 0.0
+        x[4] = x[4] * 1e-5 if dtype == HF else x[4] * 1e-37      # below the smallest scale in part
+        x[5] = 448.0
+        x[6] = 449.0
+        x[7, :] = torch.tensor([2.0 ** -9, 3 * 2.0 ** -10, 17.0, 19.0, 448.0, -464.0, 27.0, 25.0]).to(dtype).cuda()[
+            torch.arange(cols + pad) % 8]                         # midpoints between codes
+        x[8, 0] = float("nan")
+        x[9, cols - 1] = float("inf")
+        if dtype != HF:
+            x[10] *= 1e37
+    x = x[:, :cols]
+    codes, scales = muon.act8_store(x)
+    cr, sr = oo.act8_encode(host(x))
+    assert codes.dtype == torch.float8_e4m3fn and codes.shape == x.shape
+    assert np.array_equal(scales.cpu().numpy(), sr)
+    assert np.array_equal(codes.view(torch.uint8).cpu().numpy() & np.where(cr & 0x7F, 0xFF, 0x7F), cr & np.where(
+        cr & 0x7F, 0xFF, 0x7F))                                   # the sign of a zero aside
+    want = oo.act8_decode(cr, sr)
+    for out in (FP, BF, HF):
+        got = muon.act8_restore(codes, scales, dtype=out)
+        with np.errstate(over="ignore", invalid="ignore"):
+            ref = host(torch.tensor(want).to(FP).to(out))
+        assert np.array_equal(host(got), ref, equal_nan=True), out
+
+
+def test_act8_error_is_a_sixteenth(muon):
+    x = rand(82, 64, 512, dtype=BF)
+    codes, scales = muon.act8_store(x)
+    back = host(muon.act8_restore(codes, scales))
+    top = np.abs(host(x)).reshape(64, 4, 128).max(2).repeat(128, 1)
+    # half an e4m3 step: 2^-4 of the value, or of 2^-6 of the scaled grid's smallest normal number
+    assert (np.abs(back - host(x)) <= np.maximum(2.0 ** -4 * np.abs(host(x)), top * 2.0 ** -17)).all()
+
+
+WGRAD = [  # rows, cols, out, odtype, add
+    (1, 16, 16, FP, False), (64, 128, 128, FP, False), (65, 130, 139, FP, True), (200, 256, 256, BF, False),
+    (333, 300, 511, BF, True), (1001, 512, 264, FP, True), (5000, 384, 200, FP, False), (2049, 1, 1, FP, False),
+    (0, 40, 24, FP, False), (0, 40, 24, FP, True), (130, 1409, 40, FP, False)]
+
+
+@pytest.mark.parametrize("rows,cols,out,odtype,add", WGRAD)
+def test_act8_weight_grad(muon, rows, cols, out, odtype, add):
+    x, dy = rand(83, rows, cols, dtype=BF) + 0.2, rand(84, rows, out, dtype=BF)
+    codes, scales = muon.act8_store(x)
+    base = rand(85, out, cols, dtype=odtype) if add else None
+    got = muon.act8_weight_grad(dy, codes, scales, add=base, dtype=odtype)
+    ref, mag = oo.act8_weight_grad(host(dy), host(muon.act8_restore(codes, scales, dtype=FP)))
+    ref = ref + (host(base) if add else 0)
+    mag = mag + (np.abs(host(base)) if add else 0)
+    tol = U[odtype] * np.abs(ref) + (rows / 16 + 16) * 2.0 ** -23 * mag
+    close(f"weight grad {rows}x{cols}x{out} {odtype}", got, ref, tol)
+    assert torch.equal(got, muon.act8_weight_grad(dy, codes, scales, add=base, dtype=odtype))
+    if add:                                      # in place
+        assert muon.act8_weight_grad(dy, codes, scales, add=base, out=base) is base
+        assert torch.equal(base, got)
+    # other layouts of the same values
+    wide = torch.zeros(rows, out + 3, dtype=BF, device="cuda")
+    wide[:, :out] = dy
+    dst = torch.full((out, cols + 5), 7.0, dtype=odtype, device="cuda")
+    if not add:
+        muon.act8_weight_grad(wide[:, :out], codes.clone(), scales.contiguous(), out=dst[:, :cols])
+        assert torch.equal(dst[:, :cols], got) and (dst[:, cols:] == 7.0).all()
+
+
+def test_act8_weight_grad_carries_nan(muon):
+    x, dy = rand(86, 40, 256, dtype=BF), rand(87, 40, 24, dtype=BF)
+    x[7, 130] = float("inf")
+    dw = muon.act8_weight_grad(dy, *muon.act8_store(x))
+    assert torch.isfinite(dw[:, :128]).all() and dw[:, 128:].isnan().all()
+
+
+# ------------------------------------------------- streams, refusals, errors
+def test_operators_on_a_side_stream_and_in_a_graph(muon):
+    x, dy = rand(90, 64, 512, dtype=BF), rand(91, 64, 64, dtype=BF)
+    q = rand(92, 1, 200, 2, 64, dtype=BF)
+
+    def work(stream=None):
+        y, mean, rstd = muon.layer_norm(x, stream=stream)
+        dx, dw, db = muon.layer_norm_backward(x, x, mean, rstd, stream=stream)
+        c, s = muon.act8_store(x, stream=stream)
+        w = muon.act8_weight_grad(dy, c, s, stream=stream)
+        o, lse = muon.attention(q, q, q, causal=True, stream=stream)
+        return [y, dx, dw, db, muon.act8_restore(c, s, stream=stream), w, o, lse,
+                *muon.attention_backward(q, q, q, q, o, lse, causal=True, stream=stream)]
+
+    want = work()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = work(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for t in held:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+def test_operators_count_their_launches(muon):
+    h = muon.default_handle()
+    n0 = h.launch_count()
+    muon.layer_norm(rand(93, 4, 64, dtype=BF))
+    assert h.launch_count() > n0
+
+
+def test_refusals(muon):
+    x, v = rand(94, 4, 64, dtype=BF), rand(95, 64)
+    q, k = rand(96, 1, 8, 4, 64, dtype=BF), rand(97, 1, 8, 2, 64, dtype=BF)
+    o, lse = muon.attention(q, k, k)
+    cu = torch.tensor([0, 8], dtype=torch.int32).cuda()
+    codes, scales = muon.act8_store(x)
+    mean = torch.zeros(4, device="cuda")
+    calls = [
+        lambda: muon.layer_norm(x.double()), lambda: muon.layer_norm(x, v[:32]), lambda: muon.layer_norm(x, v.half()),
+        lambda: muon.layer_norm(rand(98, 2, 16385)), lambda: muon.layer_norm(x, eps=float("nan")),
+        lambda: muon.layer_norm(x, v, v.to(BF)), lambda: muon.layer_norm(torch.zeros(3, 0, device="cuda")),
+        lambda: muon.layer_norm_backward(x.float(), x, mean, mean), lambda: muon.layer_norm_backward(x, x, mean[:3], mean),
+        lambda: muon.attention(q.float(), k.float(), k.float()), lambda: muon.attention(q, k, k.half()),
+        lambda: muon.attention(q, k[:, :, :, :32], k[:, :, :, :32]), lambda: muon.attention(q, k, k, window=4),
+        lambda: muon.attention(q, k, k, causal=True, window=-1), lambda: muon.attention(q[:, :, :3], k, k),
+        lambda: muon.attention(q[0], k[0], k[0]), lambda: muon.attention(q, k, k, cu_seqlens_q=cu),
+        lambda: muon.attention(q[0], k[0], k[0], cu_seqlens_q=cu, cu_seqlens_k=cu.long()),
+        lambda: muon.attention(rand(99, 1, 4, 2, 12, dtype=BF), *[rand(99, 1, 4, 2, 12, dtype=BF)] * 2),
+        lambda: muon.attention(*[rand(99, 1, 4, 2, 136, dtype=BF)] * 3),
+        lambda: muon.attention(*[rand(99, 1, 4, 2, 20, dtype=BF)[..., 2:18]] * 3),
+        lambda: muon.attention(q, k, k, scale=float("inf")), lambda: muon.attention_backward(o, q, k, k, o, lse.double()),
+        lambda: muon.attention_backward(o[:, :4], q, k, k, o, lse), lambda: muon.act8_store(x[0]),
+        lambda: muon.act8_store(x.int()), lambda: muon.act8_restore(codes, scales[:, :2]),
+        lambda: muon.act8_restore(codes, scales, dtype=torch.int32),
+        lambda: muon.act8_weight_grad(x.half(), codes, scales), lambda: muon.act8_weight_grad(x[:2], codes, scales),
+        lambda: muon.act8_weight_grad(x, codes, scales, dtype=HF),
+        lambda: muon.act8_weight_grad(x, codes, scales, add=torch.zeros(64, 63, device="cuda")),
+        lambda: muon.act8_weight_grad(x, codes, scales, out=torch.zeros(64, 64, device="cuda").t()),
+    ]
+    n0 = muon.default_handle().launch_count()
+    for i, call in enumerate(calls):
+        with pytest.raises((ValueError, muon.MuonError)):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+    assert muon.default_handle().launch_count() == n0
