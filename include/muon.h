@@ -321,13 +321,15 @@ muon_status_t muon_layer_norm_workspace(muon_handle_t h, int64_t rows, int64_t c
  * Packed (cu_seqlens_q != NULL): the sequences lie one after another on one
  * token axis; sq and sk are the axes' lengths, sequence b holds the tokens
  * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device int32 [batch + 1], rising
- * from 0 to sq / sk; read on the device: values outside the axis or running
- * backwards are cut to a valid range, tokens of no sequence get o = 0, lse =
- * -inf and zero gradients), the batch strides are unused.
+ * from 0 to sq / sk; read on the device: an offset outside the axis, or below
+ * the largest before it, is raised or cut to that; tokens of no sequence get
+ * o = 0, lse = -inf and zero gradients), the batch strides are unused.
  *
  *   dim      a multiple of 8, 8 .. 128
+ *   scale    finite, above 0
  *   dtype    MUON_BF16 or MUON_F16, every tensor but lse
- *   strides  {batch, token, head}, multiples of 8; pointers 16-byte aligned
+ *   strides  {batch, token, head}, positive multiples of 8 (that of a
+ *            dimension of one element is not used); pointers 16-byte aligned
  *   lse      fp32 [batch][heads][sq] ([heads][sq] when packed), contiguous
  * Rows of a sequence are cut at its length: what lies past it, NaN and
  * infinity included, has no part in the result. */

@@ -322,7 +322,8 @@ struct AttnParams {
                            // b * lse_b + h * lse_h + s
   void *out;               // forward: o
   void *dq, *dk, *dv;      // backward
-  float* delta;            // backward: rowsum(dO * O), laid out as lse
+  float* stat_lse;         // backward, scratch: lse log2(e) and rowsum(dO * O), 128 values a query tile:
+  float* stat_delta;       // tile t of (b, h) at ((b * heads + h) * qtiles + t) * 128
   long long qb, qs, qh, kb, ks, kh, vb, vs, vh, ob, os, oh, dob, dos, doh;   // strides in elements
   long long dqb, dqs, dqh, dkb, dks, dkh, dvb, dvs, dvh;
   long long lse_b, lse_h;
@@ -333,8 +334,15 @@ struct AttnParams {
   int causal, window;      // window > 0: a query sees at most the last `window` keys up to its own place
   int dtype;
   float scale;
+  int qtiles;              // query tiles of 128 rows of a (batch, head): a bound when packed
+  unsigned* err;           // the handle's error word
+  unsigned long long timeout_ns;
 };
-cudaError_t launch_attn_fwd(const AttnParams& p, cudaStream_t s);
-cudaError_t launch_attn_bwd(const AttnParams& p, cudaStream_t s);
+int attn_qtiles(int sq, int batch, bool packed);
+// m: 4-D tensor maps {dim, head, token, batch} with boxes of 64 columns and
+// 128 tokens, 128-byte swizzle: q, k, v (and do).
+cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s);
+// part 0: statistics; 1: dk and dv; 2: dq
+cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s);
 
 }  // namespace muon

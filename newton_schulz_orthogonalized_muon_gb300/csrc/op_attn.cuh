@@ -1,34 +1,392 @@
-// What the attention kernels share: where a sequence lies on a packed token
-// axis, and which keys a query sees.
+// What the attention kernels share: how a work item finds its sequence, the
+// operand tiles in shared memory, and the tensor-core and TMEM access.
+//
+// A tile is 128 rows (tokens of one head) by DP = 64 or 128 columns of 16-bit
+// elements, in boxes of 128 rows x 64 columns (128-byte rows, 128-byte
+// swizzle, 16 KB), as TMA writes them from a 4-D map {dim, head, token,
+// batch}.  Columns past `dim` and, in the batched form, rows past the
+// sequence are filled with zeros.  One such tile serves both as a K-major
+// operand (the product runs over dim) and as an MN-major one (over tokens).
 #pragma once
 
+#include "common.cuh"
 #include "internal.h"
+#include "op_common.cuh"
 
 namespace muon {
+namespace attn {
 
-struct Span {
-  int start, len;
-};
+constexpr int TILE = 128;                    // rows of a tile
+constexpr int BOX_BYTES = 128 * 128;         // 128 rows x 64 16-bit columns
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr unsigned long long DRAIN_NS = 1000000000ull;
 
-// Sequence i of a packed axis of `total` tokens.  Offsets come from device
-// memory and are not trusted: what lies outside the axis, or runs backwards,
-// is cut to a valid (possibly empty) range.
-__device__ __forceinline__ Span span_of(const int* cu, int i, int total) {
-  const int a = min(max(cu[i], 0), total);
-  const int b = min(max(cu[i + 1], a), total);
-  return Span{a, b - a};
+template <int DP>
+__host__ __device__ constexpr int tile_bytes() {
+  return DP / 64 * BOX_BYTES;
 }
 
-struct Keys {
-  int first, end;
+// ------------------------------------------------------------- work items
+// One tile of rows of one sequence, and the sequence on both token axes.
+struct Work {
+  int q0, nq;        // first query token and queries
+  int k0, nk;        // first key token and keys
+  int tile;          // the item's tile within the sequence
+  int qtile;         // the sequence's first query tile in the padded numbering
+  int b, h;          // batch index (0 when packed), head of the item's axis
+  int ok;            // 0: the grid's bound is above the real number of tiles
 };
 
-// The keys [first, end) that query i of a sequence with nq queries and nk
-// keys sees; empty when end <= first.
-__device__ __forceinline__ Keys keys_of(const AttnParams& p, int i, int nq, int nk) {
-  if (!p.causal) return Keys{0, nk};
-  const int place = i + nk - nq;
-  return Keys{p.window > 0 ? max(place - p.window + 1, 0) : 0, min(place + 1, nk)};
+// Packed sequences: finds the sequence that tile `tile` (of `rows` rows) of
+// the query (by_q) or key axis belongs to.  Every sequence has
+// ceil(length / rows) tiles; the
+// tokens before the first offset and after the last form sequences of their
+// own that see nothing.  Offsets are device data and not trusted: they are
+// clamped to the axis and to the largest before them.  All 32 lanes call it.
+__device__ __forceinline__ Work find_packed(const AttnParams& p, bool by_q, int rows, int tile) {
+  const int lane = threadIdx.x & 31;
+  const int n = p.batch;
+  int pq = 0, pk = 0, tiles = 0, qtiles = 0;
+  Work w{};
+  for (int d0 = 0; d0 <= n + 1; d0 += 32) {
+    const int d = d0 + lane;                     // segment d ends at offset d (the last: at the axis' end)
+    int eq = d <= n ? min(max(p.cu_q[d], 0), p.sq) : p.sq;
+    int ek = d <= n ? min(max(p.cu_k[d], 0), p.sk) : p.sk;
+    eq = max(eq, pq);
+    ek = max(ek, pk);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, eq, o), c = __shfl_up_sync(0xffffffffu, ek, o);
+      if (lane >= o) {
+        eq = max(eq, a);
+        ek = max(ek, c);
+      }
+    }
+    int bq = __shfl_up_sync(0xffffffffu, eq, 1), bk = __shfl_up_sync(0xffffffffu, ek, 1);
+    if (lane == 0) {
+      bq = pq;
+      bk = pk;
+    }
+    int nq = eq - bq, nk = ek - bk;
+    const int tq = (nq + TILE - 1) / TILE;
+    const int t = ((by_q ? nq : nk) + rows - 1) / rows;
+    int st = t, sq = tq;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, st, o), c = __shfl_up_sync(0xffffffffu, sq, o);
+      if (lane >= o) {
+        st += a;
+        sq += c;
+      }
+    }
+    const int first = tiles + st - t;
+    const unsigned hit = __ballot_sync(0xffffffffu, tile >= first && tile < first + t);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      if (d < 1 || d > n) {                      // not a sequence: nothing on the other axis
+        if (by_q)
+          nk = 0;
+        else
+          nq = 0;
+      }
+      w.q0 = __shfl_sync(0xffffffffu, bq, src);
+      w.nq = __shfl_sync(0xffffffffu, nq, src);
+      w.k0 = __shfl_sync(0xffffffffu, bk, src);
+      w.nk = __shfl_sync(0xffffffffu, nk, src);
+      w.tile = tile - __shfl_sync(0xffffffffu, first, src);
+      w.qtile = __shfl_sync(0xffffffffu, qtiles + sq - tq, src);
+      w.ok = 1;
+      return w;
+    }
+    tiles += __shfl_sync(0xffffffffu, st, 31);
+    qtiles += __shfl_sync(0xffffffffu, sq, 31);
+    pq = __shfl_sync(0xffffffffu, eq, 31);
+    pk = __shfl_sync(0xffffffffu, ek, 31);
+  }
+  return w;
 }
 
+// Work item `item` of a grid of tiles of `rows` rows x (heads x batch), heads fastest.  The
+// longest items of a causal grid come first: the key tiles in their order,
+// the query tiles (`tiles` of them at most) from the last.
+__device__ __forceinline__ Work find_work(const AttnParams& p, bool by_q, int rows, int heads, int tiles, long long item) {
+  const long long hb = static_cast<long long>(heads) * (p.cu_q != nullptr ? 1 : p.batch);
+  int tile = static_cast<int>(item / hb);
+  const int r = static_cast<int>(item % hb);
+  if (by_q) tile = tiles - 1 - tile;
+  Work w;
+  if (p.cu_q != nullptr) {
+    w = find_packed(p, by_q, rows, tile);
+    w.b = 0;
+  } else {
+    w = Work{0, p.sq, 0, p.sk, tile, 0, r / heads, 0, 1};
+  }
+  w.h = r % heads;
+  return w;
+}
+
+// Tiles of an axis: exact in the batched form, a bound when packed (every
+// sequence, and what lies outside them, can end in a part of a tile).
+inline long long tile_bound(int len, int rows, int batch, bool packed) {
+  return packed ? len / rows + static_cast<long long>(batch) + 2 : (len + rows - 1) / rows;
+}
+
+struct Range {
+  int first, count;
+};
+
+// Key tiles that the queries [i0, i1] of a sequence see (count 0: none).
+__device__ __forceinline__ Range key_tiles(const AttnParams& p, const Work& w, int i0, int i1) {
+  int beg = 0, end = w.nk;
+  if (p.causal) {
+    const int off = w.nk - w.nq;
+    end = min(end, i1 + off + 1);
+    if (p.window > 0) beg = max(0, i0 + off - p.window + 1);
+  }
+  if (end <= beg) return Range{0, 0};
+  return Range{beg / TILE, (end + TILE - 1) / TILE - beg / TILE};
+}
+
+// Query tiles that see any of the keys [j0, j1].
+__device__ __forceinline__ Range query_tiles(const AttnParams& p, const Work& w, int j0, int j1) {
+  int beg = 0, end = w.nq;
+  if (p.causal) {
+    const int off = w.nk - w.nq;
+    beg = max(0, j0 - off);
+    if (p.window > 0) end = static_cast<int>(min(static_cast<long long>(end), static_cast<long long>(j1) - off + p.window));
+  }
+  if (end <= beg) return Range{0, 0};
+  return Range{beg / TILE, (end + TILE - 1) / TILE - beg / TILE};
+}
+
+// ------------------------------------------------------------------- waits
+// Every lane polls; the warp leaves together.  Gives up (and says so in the
+// error word) after the time limit, or when another warp gave up.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const AttnParams& p) {
+  const uint32_t a = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    if ((it & 31u) == 0u) {
+      const bool late = globaltimer_ns() - t0 > p.timeout_ns;
+      if (__any_sync(0xffffffffu, late || *abort != 0)) {
+        if ((threadIdx.x & 31) == 0) {
+          if (late) atomicOr(p.err, ERRBIT_TIMEOUT);
+          *abort = 1;
+        }
+        return false;
+      }
+    }
+  }
+}
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, const AttnParams& p) {
+  if (mbar_wait_bounded(bar, parity, abort, p.timeout_ns)) return true;
+  if (*abort == 0) atomicOr(p.err, ERRBIT_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+
+// The swizzled tiles need shared memory that starts on a 1 KB boundary, which
+// a kernel without static shared memory gets.
+__device__ __forceinline__ bool swizzle_aligned(uint32_t base, const AttnParams& p) {
+  if ((base & 1023u) == 0u) return true;
+  if (threadIdx.x == 0) atomicOr(p.err, ERRBIT_TIMEOUT);
+  return false;
+}
+
+// -------------------------------------------------------------------- TMA
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int u) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
+      : "memory");
+}
+// Untiled copy: both addresses and the size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Loads a tile whose rows start at token `row`, by one lane, signalled on
+// `bar` (which the caller has armed with the tile's bytes).
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int h, int row, int b) {
+#pragma unroll
+  for (int x = 0; x < DP / 64; ++x) tma_load_4d(dst + x * BOX_BYTES, map, bar, 64 * x, h, row, b);
+}
+
+// The same by a whole warp for a packed sequence that ends inside the tile:
+// the next sequence's rows are loaded with it and then overwritten with
+// zeros, so that a NaN or an infinity there has no part in a product with a
+// zero probability.  `edge` is the warp's own barrier; on return the tile is
+// complete for the async proxy.
+template <int DP>
+__device__ __forceinline__ bool load_edge_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* edge, uint32_t& phase,
+                                               int h, int row, int valid, volatile int* abort, const AttnParams& p) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(edge, tile_bytes<DP>());
+    load_tile<DP>(smem_u32(dst), map, edge, h, row, 0);
+  }
+  __syncwarp();
+  if (!wait_warp(edge, phase & 1u, abort, p)) return false;
+  ++phase;
+#pragma unroll
+  for (int x = 0; x < DP / 64; ++x)
+    for (int i = valid * 8 + lane; i < TILE * 8; i += 32)
+      *reinterpret_cast<uint4*>(dst + x * BOX_BYTES + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+  return true;
+}
+
+// ---------------------------------------------------------------- tcgen05
+// kind::f16 with 16-bit operands of T and fp32 accumulation, M = 128.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc(int n, int b_mn_major) {
+  const uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(b_mn_major) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(TILE >> 4) << 24);
+}
+// A from TMEM
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc));
+}
+
+// D[128 x 128] = A B^T over dim: both tiles K-major.
+template <typename T, int DP>
+__device__ __forceinline__ void mma_over_dim(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = idesc<T>(TILE, 0);
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * BOX_BYTES + (kk & 3) * 32;
+    umma_bf16(d, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id, kk != 0 ? 1u : 0u);
+  }
+}
+// D[128 x DP] (+)= A B over 128 tokens: A 16-bit in TMEM, 64 tokens in 32
+// columns from `a0` and the other 64 from `a1`; B a tile read MN-major.
+template <typename T, int DP>
+__device__ __forceinline__ void mma_over_tokens(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
+  constexpr uint32_t id = idesc<T>(DP, 1);
+#pragma unroll
+  for (int kk = 0; kk < TILE / 16; ++kk)
+    umma_ts(d, kk < 4 ? a0 + kk * 8 : a1 + (kk - 4) * 8, sdesc_sw128(b + kk * 2048, BOX_BYTES, 1024), id,
+            (acc || kk != 0) ? 1u : 0u);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------- pairs of fp32 values
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2_make(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_split(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 32 consecutive fp32 TMEM columns of this warp's rows, times `mul`, rounded
+// to T, into columns c0 .. c0 + 31 of row `dst` (nullptr: nowhere).
+template <typename T>
+__device__ __forceinline__ void store_cols32(uint32_t taddr, T* dst, int c0, int dim, float mul) {
+  float v[32];
+  tmem_ld32(taddr, v);
+  tmem_ld_wait();
+  if (dst == nullptr) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (c0 + 8 * q < dim) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * q + e] *= mul;
+      *reinterpret_cast<uint4*>(dst + c0 + 8 * q) = pack16<T>(v + 8 * q);
+    }
+  }
+}
+
+// one arrival of a warp whose lanes' TMEM accesses are complete
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// After a wait ran out: no copy may still be in flight when the CTA's shared
+// memory goes away.  `n` tiles were issued into a ring of R.
+template <int R>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int n) {
+  for (int s = 0; s < R && s < n; ++s) {
+    const int uses = (n - 1 - s) / R;
+    mbar_wait_bounded(&full[s], static_cast<uint32_t>(uses & 1), nullptr, DRAIN_NS);
+  }
+}
+
+// 64 values of a row, rounded to T, into 32 TMEM columns.
+template <typename T>
+__device__ __forceinline__ void store_half(uint32_t taddr, const float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) r[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+  tmem_st32(taddr, r);
+  tmem_st_wait();
+}
+
+}  // namespace attn
 }  // namespace muon

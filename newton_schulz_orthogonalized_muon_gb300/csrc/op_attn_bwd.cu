@@ -1,0 +1,578 @@
+// The backward pass of attention, recomputing the probabilities.
+//
+//   p_ij = exp(scale q_i . k_j - lse_i),  delta_i = do_i . o_i
+//   dv_j = sum_i p_ij do_i,   ds_ij = p_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
+//
+// Three kernels.  attn_prep_kernel writes lse_i log2(e) and delta_i, tile by
+// tile (HBM-bound: it reads o and do).  attn_dkv_kernel owns a tile of 128
+// keys, walks the query tiles that see them (of every query head that shares
+// the key head) and keeps dk and dv in TMEM; attn_dq_kernel owns a tile of
+// 128 queries, walks its key tiles and keeps dq in TMEM.  No value is added
+// by atomics, so results do not change from call to call; the price is that
+// scores and dP are formed twice, seven products a tile pair instead of five.
+//
+// Both are bound by the tensor cores and the exponentials: per tile pair of
+// 128 x 128 with dim 128 the products take 1024 (768) cycles of the tensor
+// pipe at its full rate.  One CTA an SM, warp-specialised: warp 0 loads tiles
+// by TMA, one thread of warp 1 issues every tcgen05.mma, warps 4 - 11 turn
+// scores into p and ds.  p and ds never leave the SM: each warp writes its 16
+// bit values over the fp32 scores (or dP) that it read, and the next product
+// takes them from TMEM as its A operand.  Scores are transposed in the dkv
+// kernel (rows are keys), so that p and ds are that operand as they stand.
+#include "common.cuh"
+#include "internal.h"
+#include "op_attn.cuh"
+
+namespace muon {
+namespace {
+
+using namespace attn;
+
+constexpr int CTRL_WARPS = 4;
+constexpr int CALC_WARPS = 8;                     // two warps a TMEM lane quadrant, 64 columns each
+constexpr int THREADS = 32 * (CTRL_WARPS + CALC_WARPS);
+
+// ------------------------------------------------------------ statistics
+// lse log2(e) and delta of one tile of queries, 128 values each, padded: rows
+// past the sequence and rows that see no key get +inf, so that their p is 0.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int tiles) {
+  __shared__ Work sw;
+  if (threadIdx.x < 32) {
+    const Work w = find_work(p, true, TILE, p.heads, tiles, blockIdx.x);
+    if (threadIdx.x == 0) sw = w;
+  }
+  __syncthreads();
+  const Work w = sw;
+  if (!w.ok) return;
+  const int l = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE;
+#pragma unroll
+  for (int k = 0; k < TILE; k += 16) {
+    const int i = w.tile * TILE + k + r;
+    float s = 0.f;
+    if (i < w.nq && 8 * l < p.dim) {
+      const long long t = w.q0 + i;
+      float a[8], b[8];
+      unpack16<T>(ld_stream16(static_cast<const T*>(p.o) + w.b * p.ob + t * p.os + w.h * p.oh + 8 * l), a);
+      unpack16<T>(ld_stream16(static_cast<const T*>(p.dout) + w.b * p.dob + t * p.dos + w.h * p.doh + 8 * l), b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (l == 0) {
+      float e = INFINITY;
+      if (i < w.nq) {
+        const float lse = p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + i];
+        if (lse != -INFINITY) e = lse * LOG2E;
+      }
+      p.stat_lse[at + k + r] = e;
+      p.stat_delta[at + k + r] = i < w.nq ? s : 0.f;
+    }
+  }
+}
+
+// --------------------------------------------------------- shared memory
+// Two tiles stay (K and V, or Q and dO); the rings hold the tiles that are
+// walked: three of the operand that two products a step read, two of the other.
+template <int DP>
+struct Smem {
+  static constexpr int T = tile_bytes<DP>();
+  static constexpr int RA = 3;
+  static constexpr int RB = DP == 128 ? 2 : 3;
+  static constexpr int STAT = 2 * TILE * 4;       // lse and delta of one query tile
+  static constexpr int A_OFF = 2 * T;
+  static constexpr int B_OFF = A_OFF + RA * T;
+  static constexpr int STAT_OFF = B_OFF + RB * T;
+  static constexpr int BAR_OFF = STAT_OFF + RB * STAT;
+  static constexpr int BYTES = BAR_OFF + 256;
+  static_assert(BYTES <= 232448, "shared memory");
+};
+
+struct Bars {
+  uint64_t own[2];          // the two tiles that stay
+  uint64_t a_full[3], a_empty[3];
+  uint64_t b_full[3], b_empty[3];
+  uint64_t s_full, s_free;  // scores: written, and read into registers
+  uint64_t p_full;
+  uint64_t dp_full[2], ds_full[2];
+  uint64_t done, edge;
+  uint32_t tmem;
+  int abort;
+  Work work;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+__device__ __forceinline__ void init_bars(Bars* s) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&s->own[i], 1);
+    mbar_init(&s->dp_full[i], 1);
+    mbar_init(&s->ds_full[i], CALC_WARPS);
+  }
+  for (int i = 0; i < 3; ++i) {
+    mbar_init(&s->a_full[i], 1);
+    mbar_init(&s->a_empty[i], 1);
+    mbar_init(&s->b_full[i], 1);
+    mbar_init(&s->b_empty[i], 1);
+  }
+  mbar_init(&s->s_full, 1);
+  mbar_init(&s->s_free, CALC_WARPS);
+  mbar_init(&s->p_full, CALC_WARPS);
+  mbar_init(&s->done, 1);
+  mbar_init(&s->edge, 1);
+  s->abort = 0;
+  fence_mbar_init();
+}
+
+// 64 scores of a row to probabilities: v <- 2^(v c - e[col]), e the columns'
+// values in shared memory; columns outside [lo, hi) get 0.
+template <bool MASK>
+__device__ __forceinline__ void probs_by_col(float* v, float c, const float* e, int lo, int hi) {
+  const F2 cc = f2_make(c, c);
+#pragma unroll
+  for (int k = 0; k < 64; k += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(e + k);
+    const float2 a = f2_split(f2_fma(f2_make(v[k], v[k + 1]), cc, f2_make(-l4.x, -l4.y)));
+    const float2 b = f2_split(f2_fma(f2_make(v[k + 2], v[k + 3]), cc, f2_make(-l4.z, -l4.w)));
+    v[k] = exp2_fast(a.x);
+    v[k + 1] = exp2_fast(a.y);
+    v[k + 2] = exp2_fast(b.x);
+    v[k + 3] = exp2_fast(b.y);
+    if (MASK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + i < lo || k + i >= hi) v[k + i] = 0.f;
+    }
+  }
+}
+
+// ------------------------------------------------------------- dk and dv
+template <typename T, int DP>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                    const AttnParams p, int tiles, int qtiles) {
+  using S = Smem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sb = smem_u32(smem);
+  if (!swizzle_aligned(sb, p)) return;
+  if (warp == 0) {
+    const Work w = find_work(p, false, TILE, p.kv_heads, tiles, blockIdx.x);
+    if (lane == 0) {
+      bar->work = w;
+      init_bars(bar);
+    }
+  }
+  if (warp == 1) tmem_alloc(&bar->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Work w = bar->work;
+  volatile int* abort = &bar->abort;
+  const uint32_t tmem = bar->tmem;
+  constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 256 + DP;
+  const int group = p.heads / p.kv_heads;
+  const int j0 = w.tile * TILE;
+  Range r{0, 0};
+  if (w.ok) r = query_tiles(p, w, j0, min(j0 + TILE, w.nk) - 1);
+  const int n = r.count * group;                   // steps: the group's heads one after another
+
+  if (warp == 0 && n > 0) {
+    // ---------------------------------------------------------- loads
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bar->own[0], S::T);
+      load_tile<DP>(sb, &mk, &bar->own[0], w.h, w.k0 + j0, w.b);
+      mbar_arrive_expect_tx(&bar->own[1], S::T);
+      load_tile<DP>(sb + S::T, &mv, &bar->own[1], w.h, w.k0 + j0, w.b);
+    }
+    uint32_t edges = 0;
+    int ia = 0, ib = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      const int hq = w.h * group + i / r.count, tq = r.first + i % r.count;
+      const int row = w.q0 + tq * TILE, valid = w.nq - tq * TILE;
+      const bool edge = p.cu_q != nullptr && valid < TILE;
+      const int sa = i % S::RA, sbuf = i % S::RB;
+      if (i >= S::RA && !wait_warp(&bar->a_empty[sa], (i / S::RA - 1) & 1, abort, p)) break;
+      if (edge) {
+        ok = load_edge_tile<DP>(smem + S::A_OFF + sa * S::T, &mq, &bar->edge, edges, hq, row, valid, abort, p);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&bar->a_full[sa]);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&bar->a_full[sa], S::T);
+        load_tile<DP>(sb + S::A_OFF + sa * S::T, &mq, &bar->a_full[sa], hq, row, w.b);
+      }
+      ++ia;
+      if (i >= S::RB && !wait_warp(&bar->b_empty[sbuf], (i / S::RB - 1) & 1, abort, p)) break;
+      if (edge) {
+        ok = load_edge_tile<DP>(smem + S::B_OFF + sbuf * S::T, &mdo, &bar->edge, edges, hq, row, valid, abort, p);
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        const long long at =
+            ((static_cast<long long>(w.b) * p.heads + hq) * qtiles + w.qtile + tq) * TILE;
+        const uint32_t st = sb + S::STAT_OFF + sbuf * S::STAT;
+        mbar_arrive_expect_tx(&bar->b_full[sbuf], S::STAT + (edge ? 0 : S::T));
+        bulk_load(st, p.stat_lse + at, TILE * 4, &bar->b_full[sbuf]);
+        bulk_load(st + TILE * 4, p.stat_delta + at, TILE * 4, &bar->b_full[sbuf]);
+        if (!edge) load_tile<DP>(sb + S::B_OFF + sbuf * S::T, &mdo, &bar->b_full[sbuf], hq, row, w.b);
+      }
+      ++ib;
+    }
+    if (*abort != 0 && lane == 0) {
+      mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
+      mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
+      drain_ring<S::RA>(bar->a_full, ia);
+      drain_ring<S::RB>(bar->b_full, ib);
+    }
+    __syncwarp();
+  } else if (warp == 1 && n > 0) {
+    // -------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t k_s = sb, v_s = sb + S::T;
+      auto scores = [&](int i) {
+        if (!wait_one(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
+        tc_fence_after();
+        mma_over_dim<T, DP>(tmem + S_COL, k_s, sb + S::A_OFF + (i % S::RA) * S::T);
+        umma_commit(&bar->s_full);
+        return true;
+      };
+      auto dprobs = [&](int i) {
+        if (!wait_one(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
+        tc_fence_after();
+        mma_over_dim<T, DP>(tmem + DP_COL, v_s, sb + S::B_OFF + (i % S::RB) * S::T);
+        umma_commit(&bar->dp_full[0]);
+        return true;
+      };
+      bool ok = wait_one(&bar->own[0], 0, abort, p) && scores(0) && wait_one(&bar->own[1], 0, abort, p) && dprobs(0);
+      for (int i = 0; ok && i < n; ++i) {
+        ok = wait_one(&bar->p_full, i & 1, abort, p);
+        if (!ok) break;
+        tc_fence_after();
+        mma_over_tokens<T, DP>(tmem + DV_COL, tmem + S_COL, tmem + S_COL + 64, sb + S::B_OFF + (i % S::RB) * S::T,
+                               i != 0);
+        umma_commit(&bar->b_empty[i % S::RB]);     // dP(i), issued earlier, has read this dO tile too
+        // the next scores overwrite the probabilities: the tensor pipe runs in order
+        if (i + 1 < n) ok = scores(i + 1);
+        ok = ok && wait_one(&bar->ds_full[0], i & 1, abort, p);
+        if (!ok) break;
+        tc_fence_after();
+        mma_over_tokens<T, DP>(tmem + DK_COL, tmem + DP_COL, tmem + DP_COL + 64, sb + S::A_OFF + (i % S::RA) * S::T,
+                               i != 0);
+        umma_commit(&bar->a_empty[i % S::RA]);
+        if (i + 1 < n) ok = dprobs(i + 1);
+      }
+      umma_commit(&bar->done);
+      if (!ok) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
+    }
+    __syncwarp();
+  } else if (warp >= CTRL_WARPS && w.ok) {
+    // --------------------------------------- probabilities, then outputs
+    const int quad = warp & 3, half = (warp - CTRL_WARPS) >> 2, c0 = 64 * half;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int j = j0 + quad * 32 + lane;           // this thread's key
+    const float c = p.scale * LOG2E;
+    const int off = w.nk - w.nq;
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      const int q0 = (r.first + i % r.count) * TILE;
+      const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + (i % S::RB) * S::STAT) + c0;
+      // queries q0 .. q0 + 127 against keys j0 .. j0 + 127: does everyone see everything?
+      const bool mask = p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window));
+      float v[64];
+      ok = wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p) && wait_warp(&bar->s_full, i & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tmem + lanes + S_COL + c0, v);
+      tmem_ld32(tmem + lanes + S_COL + c0 + 32, v + 32);
+      tmem_ld_wait();
+      if (mask) {
+        const int lo = j - off - q0 - c0;          // first query (column) that sees key j
+        probs_by_col<true>(v, c, st, lo, p.window > 0 ? lo + p.window : 64);
+      } else {
+        probs_by_col<false>(v, c, st, 0, 64);
+      }
+      store_half<T>(tmem + lanes + S_COL + c0, v);
+      warp_arrive(&bar->p_full);
+      ok = wait_warp(&bar->dp_full[0], i & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k0 = 0; k0 < 64; k0 += 32) {
+        float d[32];
+        tmem_ld32(tmem + lanes + DP_COL + c0 + k0, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 dl = *reinterpret_cast<const float4*>(st + TILE + k0 + k);
+          const F2 a = f2_mul(f2_make(v[k0 + k], v[k0 + k + 1]), f2_add(f2_make(d[k], d[k + 1]), f2_make(-dl.x, -dl.y)));
+          const F2 b = f2_mul(f2_make(v[k0 + k + 2], v[k0 + k + 3]),
+                              f2_add(f2_make(d[k + 2], d[k + 3]), f2_make(-dl.z, -dl.w)));
+          const float2 x = f2_split(a), y = f2_split(b);
+          v[k0 + k] = x.x;
+          v[k0 + k + 1] = x.y;
+          v[k0 + k + 2] = y.x;
+          v[k0 + k + 3] = y.y;
+        }
+      }
+      store_half<T>(tmem + lanes + DP_COL + c0, v);
+      warp_arrive(&bar->ds_full[0]);
+    }
+    if (ok && n > 0) {
+      ok = wait_warp(&bar->done, 0, abort, p);
+      tc_fence_after();
+    }
+    if (ok) {
+      // dv by the first four warps, dk by the others
+      const long long t = w.k0 + j;
+      T* row = half == 0 ? static_cast<T*>(p.dv) + w.b * p.dvb + t * p.dvs + w.h * p.dvh
+                         : static_cast<T*>(p.dk) + w.b * p.dkb + t * p.dks + w.h * p.dkh;
+      if (j >= w.nk) row = nullptr;
+      if (n > 0) {
+#pragma unroll
+        for (int k = 0; k < DP; k += 32)
+          store_cols32<T>(tmem + lanes + (half == 0 ? DV_COL : DK_COL) + k, row, k, p.dim, half == 0 ? 1.f : p.scale);
+      } else if (row != nullptr) {
+        for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// -------------------------------------------------------------------- dq
+template <typename T, int DP>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                   const AttnParams p, int tiles) {
+  using S = Smem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sb = smem_u32(smem);
+  if (!swizzle_aligned(sb, p)) return;
+  if (warp == 0) {
+    const Work w = find_work(p, true, TILE, p.heads, tiles, blockIdx.x);
+    if (lane == 0) {
+      bar->work = w;
+      init_bars(bar);
+    }
+  }
+  if (warp == 1) tmem_alloc(&bar->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Work w = bar->work;
+  volatile int* abort = &bar->abort;
+  const uint32_t tmem = bar->tmem;
+  // dP is kept twice, so that the next tile's products need not wait for this tile's ds
+  constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 384;
+  const int hk = w.h / (p.heads / p.kv_heads);
+  const int i0 = w.tile * TILE;
+  Range r{0, 0};
+  if (w.ok) r = key_tiles(p, w, i0, min(i0 + TILE, w.nq) - 1);
+  const int n = r.count;
+
+  if (warp == 0 && n > 0) {
+    // ---------------------------------------------------------- loads
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bar->own[0], S::T);
+      load_tile<DP>(sb, &mq, &bar->own[0], w.h, w.q0 + i0, w.b);
+      mbar_arrive_expect_tx(&bar->own[1], S::T);
+      load_tile<DP>(sb + S::T, &mdo, &bar->own[1], w.h, w.q0 + i0, w.b);
+    }
+    uint32_t edges = 0;
+    int ia = 0, ib = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      const int j = (r.first + i) * TILE, row = w.k0 + j, valid = w.nk - j;
+      const bool edge = p.cu_q != nullptr && valid < TILE;
+      const int sa = i % S::RA, sbuf = i % S::RB;
+      if (i >= S::RA && !wait_warp(&bar->a_empty[sa], (i / S::RA - 1) & 1, abort, p)) break;
+      if (edge) {
+        ok = load_edge_tile<DP>(smem + S::A_OFF + sa * S::T, &mk, &bar->edge, edges, hk, row, valid, abort, p);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&bar->a_full[sa]);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&bar->a_full[sa], S::T);
+        load_tile<DP>(sb + S::A_OFF + sa * S::T, &mk, &bar->a_full[sa], hk, row, w.b);
+      }
+      ++ia;
+      if (i >= S::RB && !wait_warp(&bar->b_empty[sbuf], (i / S::RB - 1) & 1, abort, p)) break;
+      if (edge) {
+        ok = load_edge_tile<DP>(smem + S::B_OFF + sbuf * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&bar->b_full[sbuf]);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&bar->b_full[sbuf], S::T);
+        load_tile<DP>(sb + S::B_OFF + sbuf * S::T, &mv, &bar->b_full[sbuf], hk, row, w.b);
+      }
+      ++ib;
+    }
+    if (*abort != 0 && lane == 0) {
+      mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
+      mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
+      drain_ring<S::RA>(bar->a_full, ia);
+      drain_ring<S::RB>(bar->b_full, ib);
+    }
+    __syncwarp();
+  } else if (warp == 1 && n > 0) {
+    // -------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t q_s = sb, do_s = sb + S::T;
+      auto scores = [&](int i) {
+        if (!wait_one(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
+        tc_fence_after();
+        mma_over_dim<T, DP>(tmem + S_COL, q_s, sb + S::A_OFF + (i % S::RA) * S::T);
+        umma_commit(&bar->s_full);
+        return true;
+      };
+      auto dprobs = [&](int i) {
+        if (!wait_one(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
+        tc_fence_after();
+        mma_over_dim<T, DP>(tmem + DP_COL + (i & 1) * 128, do_s, sb + S::B_OFF + (i % S::RB) * S::T);
+        umma_commit(&bar->dp_full[i & 1]);
+        umma_commit(&bar->b_empty[i % S::RB]);
+        return true;
+      };
+      bool ok = wait_one(&bar->own[0], 0, abort, p) && scores(0) && wait_one(&bar->own[1], 0, abort, p) && dprobs(0);
+      for (int i = 0; ok && i < n; ++i) {
+        // the next tile's scores and dP (over ds(i - 1), which dq(i - 1) has read: the tensor pipe runs in order)
+        if (i + 1 < n) ok = wait_one(&bar->s_free, i & 1, abort, p) && scores(i + 1) && dprobs(i + 1);
+        ok = ok && wait_one(&bar->ds_full[i & 1], (i >> 1) & 1, abort, p);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ds = tmem + DP_COL + (i & 1) * 128;
+        mma_over_tokens<T, DP>(tmem + DQ_COL, ds, ds + 64, sb + S::A_OFF + (i % S::RA) * S::T, i != 0);
+        umma_commit(&bar->a_empty[i % S::RA]);
+      }
+      umma_commit(&bar->done);
+      if (!ok) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
+    }
+    __syncwarp();
+  } else if (warp >= CTRL_WARPS && w.ok) {
+    // --------------------------------------- probabilities, then outputs
+    const int quad = warp & 3, half = (warp - CTRL_WARPS) >> 2, c0 = 64 * half;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int q = i0 + quad * 32 + lane;           // this thread's query
+    const float c = p.scale * LOG2E;
+    const int off = w.nk - w.nq;
+    const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE + quad * 32 + lane;
+    const float lse = n > 0 ? p.stat_lse[at] : 0.f, delta = n > 0 ? p.stat_delta[at] : 0.f;
+    const F2 cc = f2_make(c, c), ll = f2_make(-lse, -lse), dd = f2_make(-delta, -delta);
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      const int j0 = (r.first + i) * TILE;
+      const bool mask = j0 + TILE > w.nk ||
+                        (p.causal && (j0 + TILE - 1 > i0 + off || (p.window > 0 && i0 + TILE - 1 + off - j0 >= p.window)));
+      float v[64];
+      ok = wait_warp(&bar->s_full, i & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tmem + lanes + S_COL + c0, v);
+      tmem_ld32(tmem + lanes + S_COL + c0 + 32, v + 32);
+      tmem_ld_wait();
+      warp_arrive(&bar->s_free);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        const float2 a = f2_split(f2_fma(f2_make(v[k], v[k + 1]), cc, ll));
+        v[k] = exp2_fast(a.x);
+        v[k + 1] = exp2_fast(a.y);
+      }
+      if (mask) {
+        // keys (columns) [lo, hi) are seen by query q
+        int lo = 0, hi = w.nk - j0 - c0;
+        if (p.causal) {
+          hi = min(hi, q + off + 1 - j0 - c0);
+          if (p.window > 0) lo = q + off - p.window + 1 - j0 - c0;
+        }
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (k < lo || k >= hi) v[k] = 0.f;
+      }
+      ok = wait_warp(&bar->dp_full[i & 1], (i >> 1) & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t dp = tmem + lanes + DP_COL + (i & 1) * 128 + c0;
+#pragma unroll
+      for (int k0 = 0; k0 < 64; k0 += 32) {
+        float d[32];
+        tmem_ld32(dp + k0, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float2 x = f2_split(f2_mul(f2_make(v[k0 + k], v[k0 + k + 1]), f2_add(f2_make(d[k], d[k + 1]), dd)));
+          v[k0 + k] = x.x;
+          v[k0 + k + 1] = x.y;
+        }
+      }
+      store_half<T>(dp, v);
+      warp_arrive(&bar->ds_full[i & 1]);
+    }
+    if (ok && n > 0) {
+      ok = wait_warp(&bar->done, 0, abort, p);
+      tc_fence_after();
+    }
+    if (ok) {
+      T* row = q < w.nq ? static_cast<T*>(p.dq) + w.b * p.dqb + static_cast<long long>(w.q0 + q) * p.dqs + w.h * p.dqh
+                        : nullptr;
+      if (n > 0) {
+#pragma unroll
+        for (int k = 0; k < DP / 2; k += 32)
+          store_cols32<T>(tmem + lanes + DQ_COL + half * (DP / 2) + k, row, half * (DP / 2) + k, p.dim, p.scale);
+      } else if (row != nullptr && half == 0) {
+        for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+long long seqs(const AttnParams& p) { return p.cu_q != nullptr ? 1 : p.batch; }
+
+template <typename T, int DP>
+cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s) {
+  const long long qt = p.qtiles, kt = tile_bound(p.sk, TILE, p.batch, p.cu_q != nullptr);
+  const long long nq = qt * p.heads * seqs(p), nk = kt * p.kv_heads * seqs(p);
+  if (nq > 0x7FFFFFFFll || nk > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  if (part == 0) {
+    attn_prep_kernel<T><<<static_cast<unsigned>(nq), 256, 0, s>>>(p, static_cast<int>(qt));
+    return cudaGetLastError();
+  }
+  auto dkv = attn_dkv_kernel<T, DP>;
+  auto dq = attn_dq_kernel<T, DP>;
+  const void* f = part == 1 ? reinterpret_cast<const void*>(dkv) : reinterpret_cast<const void*>(dq);
+  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP>::BYTES);
+  if (e != cudaSuccess) return e;
+  if (part == 1)
+    dkv<<<static_cast<unsigned>(nk), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(kt),
+                                                                    static_cast<int>(qt));
+  else
+    dq<<<static_cast<unsigned>(nq), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(qt));
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_part(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s) {
+  return p.dim <= 64 ? launch_dims<T, 64>(p, m, part, s) : launch_dims<T, 128>(p, m, part, s);
+}
+
+}  // namespace
+
+// part 0: statistics; 1: dk and dv; 2: dq.  m: maps of q, k, v, do.
+cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s) {
+  return p.dtype == DT_BF16 ? launch_part<__nv_bfloat16>(p, m, part, s) : launch_part<__half>(p, m, part, s);
+}
+
+}  // namespace muon

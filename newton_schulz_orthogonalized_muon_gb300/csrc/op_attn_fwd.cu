@@ -1,0 +1,327 @@
+// Attention, forward: o_i = sum_j p_ij v_j, p_ij = exp(scale q_i . k_j -
+// lse_i), in one pass over the keys with a running maximum and sum.
+//
+// A CTA owns two tiles of 128 queries of one head and walks the key tiles
+// that they see.  Warp 0 loads by TMA, one thread of warp 1 issues every
+// tcgen05.mma, and each tile has a warpgroup of its own (warps 4 - 7, 8 - 11)
+// with one thread a query: while one tile's scores go through the
+// exponential, the tensor pipe works for the other.  The scores (fp32) and o
+// stay in TMEM; the probabilities are rounded to the operands' 16-bit type
+// and written over the scores, from where the second product takes them as
+// its A operand.  The row sum is taken from the probabilities before they
+// are rounded.
+//
+// The maximum that a row's exponents are taken against is raised only when a
+// new score passes it by more than 2^8 (in exp2 units): o and the sum are
+// then scaled down in TMEM.  Below that the probabilities stay under 256,
+// exact in the same relative precision, and o is left alone.
+//
+// Bound by the tensor cores and the exponentials alike: a 128 x 128 tile
+// pair with dim 128 takes 512 cycles of products and 16 K exponentials.
+#include "common.cuh"
+#include "internal.h"
+#include "op_attn.cuh"
+
+namespace muon {
+namespace {
+
+using namespace attn;
+
+constexpr int CTRL_WARPS = 4;
+constexpr int THREADS = 32 * (CTRL_WARPS + 8);
+constexpr int ROWS = 2 * TILE;
+constexpr float RAISE = 8.f;
+
+template <int DP>
+struct Smem {
+  static constexpr int T = tile_bytes<DP>();
+  static constexpr int RK = 3;
+  static constexpr int RV = DP == 128 ? 2 : 3;
+  static constexpr int K_OFF = 2 * T;
+  static constexpr int V_OFF = K_OFF + RK * T;
+  static constexpr int BAR_OFF = V_OFF + RV * T;
+  static constexpr int BYTES = BAR_OFF + 256;
+  static_assert(BYTES <= 232448, "shared memory");
+};
+
+struct Bars {
+  uint64_t q_full[2];
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t drain, edge;
+  uint32_t tmem;
+  int abort;
+  Work work;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const AttnParams p, int tiles) {
+  using S = Smem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sb = smem_u32(smem);
+  if (!swizzle_aligned(sb, p)) return;
+  if (warp == 0) {
+    const Work w = find_work(p, true, ROWS, p.heads, tiles, blockIdx.x);
+    if (lane == 0) {
+      bar->work = w;
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar->q_full[i], 1);
+        mbar_init(&bar->s_full[i], 1);
+        mbar_init(&bar->p_full[i], 4);
+        mbar_init(&bar->o_done[i], 1);
+      }
+      for (int i = 0; i < 3; ++i) {
+        mbar_init(&bar->k_full[i], 1);
+        mbar_init(&bar->k_empty[i], 1);
+        mbar_init(&bar->v_full[i], 1);
+        mbar_init(&bar->v_empty[i], 1);
+      }
+      mbar_init(&bar->drain, 1);
+      mbar_init(&bar->edge, 1);
+      bar->abort = 0;
+      fence_mbar_init();
+    }
+  }
+  if (warp == 1) tmem_alloc(&bar->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Work w = bar->work;
+  volatile int* abort = &bar->abort;
+  const uint32_t tmem = bar->tmem;
+  const int hk = w.h / (p.heads / p.kv_heads);
+  const int i0 = w.tile * ROWS;
+  // key tiles of each query tile, and of both
+  Range r[2] = {{0, 0}, {0, 0}};
+  if (w.ok) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (i0 + t * TILE < w.nq) r[t] = key_tiles(p, w, i0 + t * TILE, min(i0 + (t + 1) * TILE, w.nq) - 1);
+  }
+  int beg = 0, end = 0;
+  if (r[0].count > 0 || r[1].count > 0) {
+    beg = r[0].count == 0 ? r[1].first : r[1].count == 0 ? r[0].first : min(r[0].first, r[1].first);
+    end = max(r[0].first + r[0].count, r[1].first + r[1].count);
+  }
+  const int n = end - beg;
+  auto sees = [&](int t, int tile) { return tile >= r[t].first && tile < r[t].first + r[t].count; };
+
+  if (warp == 0 && n > 0) {
+    // ---------------------------------------------------------- loads
+    if (lane == 0) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (r[t].count > 0) {
+          mbar_arrive_expect_tx(&bar->q_full[t], S::T);
+          load_tile<DP>(sb + t * S::T, &mq, &bar->q_full[t], w.h, w.q0 + i0 + t * TILE, w.b);
+        }
+      }
+    }
+    uint32_t edges = 0;
+    int ik = 0, iv = 0;
+    for (int i = 0; i < n; ++i) {
+      const int j = (beg + i) * TILE, row = w.k0 + j, valid = w.nk - j;
+      const int sk = i % S::RK, sv = i % S::RV;
+      if (i >= S::RK && !wait_warp(&bar->k_empty[sk], (i / S::RK - 1) & 1, abort, p)) break;
+      if (lane == 0) {
+        // rows past the sequence give scores that are masked, whatever they hold
+        mbar_arrive_expect_tx(&bar->k_full[sk], S::T);
+        load_tile<DP>(sb + S::K_OFF + sk * S::T, &mk, &bar->k_full[sk], hk, row, w.b);
+      }
+      ++ik;
+      if (i >= S::RV && !wait_warp(&bar->v_empty[sv], (i / S::RV - 1) & 1, abort, p)) break;
+      if (p.cu_q != nullptr && valid < TILE) {
+        if (!load_edge_tile<DP>(smem + S::V_OFF + sv * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p)) break;
+        if (lane == 0) mbar_arrive(&bar->v_full[sv]);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&bar->v_full[sv], S::T);
+        load_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, &bar->v_full[sv], hk, row, w.b);
+      }
+      ++iv;
+    }
+    if (*abort != 0 && lane == 0) {
+      for (int t = 0; t < 2; ++t)
+        if (r[t].count > 0) mbar_wait_bounded(&bar->q_full[t], 0, nullptr, DRAIN_NS);
+      drain_ring<S::RK>(bar->k_full, ik);
+      drain_ring<S::RV>(bar->v_full, iv);
+    }
+    __syncwarp();
+  } else if (warp == 1 && n > 0) {
+    // -------------------------------------------------------- products
+    if (lane == 0) {
+      int steps[2] = {0, 0};                       // key tiles done, of each query tile
+      auto scores = [&](int t, int i) {
+        if (!wait_one(&bar->k_full[i % S::RK], (i / S::RK) & 1, abort, p)) return false;
+        if (steps[t] == 0 && !wait_one(&bar->q_full[t], 0, abort, p)) return false;
+        tc_fence_after();
+        mma_over_dim<T, DP>(tmem + t * TILE, sb + t * S::T, sb + S::K_OFF + (i % S::RK) * S::T);
+        umma_commit(&bar->s_full[t]);
+        return true;
+      };
+      bool ok = true;
+      for (int t = 0; t < 2; ++t)
+        if (ok && sees(t, beg)) ok = scores(t, 0);
+      if (ok) umma_commit(&bar->k_empty[0]);
+      for (int i = 0; ok && i < n; ++i) {
+        for (int t = 0; ok && t < 2; ++t) {
+          if (sees(t, beg + i)) {
+            ok = wait_one(&bar->p_full[t], steps[t] & 1, abort, p) &&
+                 wait_one(&bar->v_full[i % S::RV], (i / S::RV) & 1, abort, p);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t pr = tmem + t * TILE;
+            mma_over_tokens<T, DP>(tmem + 256 + t * TILE, pr, pr + 32, sb + S::V_OFF + (i % S::RV) * S::T,
+                                   steps[t] != 0);
+            umma_commit(&bar->o_done[t]);
+            ++steps[t];
+          }
+          // over the probabilities just used: the tensor pipe runs in order
+          if (i + 1 < n && sees(t, beg + i + 1)) ok = scores(t, i + 1);
+        }
+        if (!ok) break;
+        umma_commit(&bar->v_empty[i % S::RV]);
+        if (i + 1 < n) umma_commit(&bar->k_empty[(i + 1) % S::RK]);
+      }
+      if (!ok) {
+        umma_commit(&bar->drain);
+        mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= CTRL_WARPS && w.ok) {
+    // ------------------------------------------------ softmax, output
+    const int t = (warp - CTRL_WARPS) >> 2, quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * TILE, o_at = tmem + lanes + 256 + t * TILE;
+    const int q0 = i0 + t * TILE, q = q0 + quad * 32 + lane;
+    const int off = w.nk - w.nq;
+    const float c = p.scale * LOG2E;
+    float top = -INFINITY;                         // the scores' reference, before scaling
+    F2 sum2 = f2_make(0.f, 0.f);
+    bool ok = true;
+    const int cnt = r[t].count;
+    for (int i = 0; i < cnt; ++i) {
+      const int j0 = (r[t].first + i) * TILE;
+      float v[TILE];
+      ok = wait_warp(&bar->s_full[t], i & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < TILE; k += 32) tmem_ld32(s_at + k, v + k);
+      tmem_ld_wait();
+      if (j0 + TILE > w.nk ||
+          (p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window)))) {
+        int lo = 0, hi = w.nk - j0;
+        if (p.causal) {
+          hi = min(hi, q + off + 1 - j0);
+          if (p.window > 0) lo = q + off - p.window + 1 - j0;
+        }
+#pragma unroll
+        for (int k = 0; k < TILE; ++k)
+          if (k < lo || k >= hi) v[k] = -INFINITY;
+      }
+      float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int k = 4; k < TILE; k += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = k + 4 + e < TILE ? fmaxf(fmaxf(m[e], v[k + e]), v[k + 4 + e]) : fmaxf(m[e], v[k + e]);
+      }
+      const float mt = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+      if (i == 0) {
+        top = mt;
+      } else {
+        const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
+        if (__any_sync(0xffffffffu, up)) {
+          ok = wait_warp(&bar->o_done[t], (i - 1) & 1, abort, p);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = !up ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - mt) * c);
+          if (up) top = mt;
+          sum2 = f2_mul(sum2, f2_make(f, f));
+#pragma unroll 1
+          for (int k = 0; k < DP; k += 32) {
+            float o[32];
+            tmem_ld32(o_at + k, o);
+            tmem_ld_wait();
+            uint32_t* u = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(o_at + k, u);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float ref = top == -INFINITY ? 0.f : -top * c;
+      const F2 cc = f2_make(c, c), rr = f2_make(ref, ref);
+#pragma unroll
+      for (int k = 0; k < TILE; k += 64) {
+#pragma unroll
+        for (int e = k; e < k + 64; e += 2) {
+          const float2 a = f2_split(f2_fma(f2_make(v[e], v[e + 1]), cc, rr));
+          v[e] = exp2_fast(a.x);
+          v[e + 1] = exp2_fast(a.y);
+          sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
+        }
+        store_half<T>(s_at + k / 2, v + k);
+      }
+      warp_arrive(&bar->p_full[t]);
+    }
+    if (ok && cnt > 0) {
+      ok = wait_warp(&bar->o_done[t], (cnt - 1) & 1, abort, p);
+      tc_fence_after();
+    }
+    if (ok) {
+      const float2 s2 = f2_split(sum2);
+      const float sum = s2.x + s2.y;
+      T* row = q < w.nq ? static_cast<T*>(p.out) + w.b * p.ob + static_cast<long long>(w.q0 + q) * p.os + w.h * p.oh
+                        : nullptr;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (cnt > 0) {
+#pragma unroll 1
+        for (int k = 0; k < DP; k += 32) store_cols32<T>(o_at + k, row, k, p.dim, inv);
+      } else if (row != nullptr) {
+        for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (row != nullptr)
+        p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + q] =
+            sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int DP>
+cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
+  const bool packed = p.cu_q != nullptr;
+  const long long tiles = tile_bound(p.sq, ROWS, p.batch, packed);
+  const long long items = tiles * p.heads * (packed ? 1 : p.batch);
+  if (items > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  auto kern = attn_fwd_kernel<T, DP>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP>::BYTES);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(items), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], p, static_cast<int>(tiles));
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
+  return p.dim <= 64 ? launch_dims<T, 64>(p, m, s) : launch_dims<T, 128>(p, m, s);
+}
+
+}  // namespace
+
+int attn_qtiles(int sq, int batch, bool packed) { return static_cast<int>(tile_bound(sq, TILE, batch, packed)); }
+
+cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
+  return p.dtype == DT_BF16 ? launch_type<__nv_bfloat16>(p, m, s) : launch_type<__half>(p, m, s);
+}
+
+}  // namespace muon

@@ -27,6 +27,9 @@ muon_status_t guarded(F&& f) noexcept {
   }
 }
 
+const char* const kBadOperand =
+    "operands need 16-byte aligned pointers and positive strides that are multiples of 8 elements";
+
 #define MUON_CHECK(cond, msg) \
   do {                        \
     if (!(cond)) return fail(h, MUON_ERR_INVALID_ARG, msg); \
@@ -53,8 +56,9 @@ muon_status_t check_act8(muon_handle_t h, const uint8_t* codes, int64_t ldc, con
 }
 
 uint64_t attn_workspace(const muon_attention_t& a) {
-  const uint64_t b = a.cu_seqlens_q != nullptr ? 1 : static_cast<uint64_t>(a.batch);
-  return round256(b * static_cast<uint64_t>(a.heads) * static_cast<uint64_t>(a.sq) * 4);
+  const bool packed = a.cu_seqlens_q != nullptr;
+  const uint64_t b = packed ? 1 : static_cast<uint64_t>(a.batch);
+  return 2 * 512 * b * static_cast<uint64_t>(a.heads) * static_cast<uint64_t>(attn_qtiles(a.sq, a.batch, packed));
 }
 
 muon_status_t check_attention(muon_handle_t h, const muon_attention_t* a) {
@@ -67,19 +71,41 @@ muon_status_t check_attention(muon_handle_t h, const muon_attention_t* a) {
   MUON_CHECK(a->dim >= 8 && a->dim <= 128 && a->dim % 8 == 0, "dim must be a multiple of 8 in [8, 128]");
   MUON_CHECK(a->dtype == MUON_BF16 || a->dtype == MUON_F16, "dtype must be MUON_BF16 or MUON_F16");
   MUON_CHECK(a->window >= 0 && (a->window == 0 || a->causal), "a window needs causal = 1 and a length >= 0");
-  MUON_CHECK(std::isfinite(a->scale), "non-finite scale");
+  MUON_CHECK(std::isfinite(a->scale) && a->scale > 0.f, "scale must be finite and above 0");
   MUON_CHECK((a->cu_seqlens_q == nullptr) == (a->cu_seqlens_k == nullptr),
              "cu_seqlens_q and cu_seqlens_k go together");
   return MUON_OK;
 }
 
-bool bad_operand(const void* p, const int64_t* st, bool packed) {
-  return p == nullptr || !aligned(p, 16) || st[1] % 8 || st[2] % 8 || (!packed && st[0] % 8) || st[1] < 0 ||
-         st[2] < 0 || (!packed && st[0] < 0);
+// The stride of a dimension of one element is never used.
+bool bad_operand(const void* p, const int64_t* st, const int64_t* size) {
+  bool bad = p == nullptr || !aligned(p, 16);
+  for (int i = 0; i < 3; ++i) bad = bad || (size[i] > 1 && (st[i] % 8 || st[i] < 8 || st[i] > (int64_t(1) << 38)));
+  return bad;
 }
 
-AttnParams attn_params(const muon_attention_t& a) {
+// Map of an operand [batch][token][head][dim] with boxes of one head, 128
+// tokens and 64 columns (a whole 128-byte swizzle row).
+bool attn_map(muon_handle_t h, CUtensorMap* map, const void* base, const int64_t* st, const int64_t* size, int dim,
+              int dtype) {
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(size[2]),
+                        static_cast<cuuint64_t>(size[1]), static_cast<cuuint64_t>(size[0])};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i)
+    strides[i] = size[2 - i] > 1 ? static_cast<cuuint64_t>(st[2 - i]) * 2 : static_cast<cuuint64_t>(dim) * 2;
+  cuuint32_t box[4] = {64, 1, 128, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return h->encode(map, dtype == MUON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+AttnParams attn_params(muon_handle_t h, const muon_attention_t& a) {
   AttnParams p{};
+  p.err = h->err;
+  p.timeout_ns = h->timeout_ns;
+  p.qtiles = attn_qtiles(a.sq, a.batch, a.cu_seqlens_q != nullptr);
   const bool packed = a.cu_seqlens_q != nullptr;
   auto set = [packed](const int64_t* st, long long* b, long long* s, long long* hh) {
     *b = packed ? 0 : st[0];
@@ -109,7 +135,7 @@ AttnParams attn_params(const muon_attention_t& a) {
   p.kv_heads = a.kv_heads;
   p.dim = a.dim;
   p.causal = a.causal ? 1 : 0;
-  p.window = a.window;
+  p.window = a.window < kMaxTokens ? a.window : static_cast<int>(kMaxTokens);   // nothing is further away
   p.dtype = a.dtype;
   p.scale = a.scale;
   return p;
@@ -214,17 +240,24 @@ muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a,
     if (st != MUON_OK) return st;
     const bool packed = a->cu_seqlens_q != nullptr;
     if (a->sq == 0 || (a->batch == 0 && !packed)) return MUON_OK;
-    MUON_CHECK(!bad_operand(a->q, a->q_stride, packed) && !bad_operand(a->o, a->o_stride, packed) &&
-                   (a->sk == 0 ||
-                    (!bad_operand(a->k, a->k_stride, packed) && !bad_operand(a->v, a->v_stride, packed))),
-               "operands need 16-byte aligned pointers and strides that are multiples of 8 elements");
+    const int64_t nb = packed ? 1 : a->batch;
+    const int64_t qn[3] = {nb, a->sq, a->heads}, kn[3] = {nb, a->sk, a->kv_heads};
+    MUON_CHECK(!bad_operand(a->q, a->q_stride, qn) && !bad_operand(a->o, a->o_stride, qn) &&
+                   (a->sk == 0 || (!bad_operand(a->k, a->k_stride, kn) && !bad_operand(a->v, a->v_stride, kn))),
+               kBadOperand);
     MUON_CHECK(a->lse != nullptr, "lse is NULL");
     DeviceGuard guard(h->device);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
-    AttnParams p = attn_params(*a);
+    AttnParams p = attn_params(h, *a);
     p.out = a->o;
+    CUtensorMap m[3] = {};
+    bool ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype);
+    if (a->sk > 0)
+      ok = ok && attn_map(h, &m[1], a->k, a->k_stride, kn, a->dim, a->dtype) &&
+           attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype);
+    if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
-    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_fwd(p, stream), "attention launch");
+    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_fwd(p, m, stream), "attention launch");
     return MUON_OK;
   });
 }
@@ -247,12 +280,15 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
     if (st != MUON_OK) return st;
     const bool packed = a->cu_seqlens_q != nullptr;
     if ((a->sq == 0 && a->sk == 0) || (a->batch == 0 && !packed)) return MUON_OK;
-    auto bad = [&](const void* q, const int64_t* s) { return bad_operand(q, s, packed); };
-    MUON_CHECK((a->sq == 0 || !(bad(a->q, a->q_stride) || bad(a->o, a->o_stride) || bad(a->dout, a->dout_stride) ||
-                                bad(a->dq, a->dq_stride))) &&
-                   (a->sk == 0 || !(bad(a->k, a->k_stride) || bad(a->v, a->v_stride) || bad(a->dk, a->dk_stride) ||
-                                    bad(a->dv, a->dv_stride))),
-               "operands need 16-byte aligned pointers and strides that are multiples of 8 elements");
+    const int64_t nb = packed ? 1 : a->batch;
+    const int64_t qn[3] = {nb, a->sq, a->heads}, kn[3] = {nb, a->sk, a->kv_heads};
+    MUON_CHECK((a->sq == 0 ||
+                !(bad_operand(a->q, a->q_stride, qn) || bad_operand(a->o, a->o_stride, qn) ||
+                  bad_operand(a->dout, a->dout_stride, qn) || bad_operand(a->dq, a->dq_stride, qn))) &&
+                   (a->sk == 0 ||
+                    !(bad_operand(a->k, a->k_stride, kn) || bad_operand(a->v, a->v_stride, kn) ||
+                      bad_operand(a->dk, a->dk_stride, kn) || bad_operand(a->dv, a->dv_stride, kn))),
+               kBadOperand);
     if (a->sq > 0) {
       MUON_CHECK(a->lse != nullptr, "lse is NULL");
       MUON_CHECK(workspace != nullptr && workspace_bytes >= attn_workspace(*a) && aligned(workspace, 256),
@@ -260,15 +296,27 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
     }
     DeviceGuard guard(h->device);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
-    AttnParams p = attn_params(*a);
+    AttnParams p = attn_params(h, *a);
     p.o = a->o;
     p.dout = a->dout;
     p.dq = a->dq;
     p.dk = a->dk;
     p.dv = a->dv;
-    p.delta = static_cast<float*>(workspace);
+    p.stat_lse = static_cast<float*>(workspace);
+    p.stat_delta = p.stat_lse + attn_workspace(*a) / 8;
+    CUtensorMap m[4] = {};
+    bool ok = true;
+    if (a->sq > 0)
+      ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype) &&
+           attn_map(h, &m[3], a->dout, a->dout_stride, qn, a->dim, a->dtype);
+    if (a->sk > 0)
+      ok = ok && attn_map(h, &m[1], a->k, a->k_stride, kn, a->dim, a->dtype) &&
+           attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype);
+    if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
-    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, stream), "attention backward launch");
+    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 0, stream), "attention statistics launch");
+    if (a->sk > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 1, stream), "attention dk, dv launch");
+    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 2, stream), "attention dq launch");
     return MUON_OK;
   });
 }
