@@ -385,7 +385,8 @@ muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t l
 /* The weight's gradient of a linear layer y = x w^T whose input x was stored
  * in 8 bits, straight from the codes:
  *   dw[o][n] = sum over rows t of dy[t][o] x[t][n]  (+ add[o][n])
- *   dy       bf16 [rows][out], row stride lddy
+ *   dy       bf16 [rows][out], row stride lddy (a multiple of 8 on a 16-byte
+ *            aligned start is read in place, anything else copied first)
  *   add, dw  odtype (MUON_F32 or MUON_BF16) [out][cols], row strides ldadd,
  *            lddw; add may be NULL, or dw itself
  * rows == 0 gives zeros (or add). */
@@ -393,8 +394,9 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
                                     const uint8_t* scales, int64_t lds, const void* add, int64_t ldadd, void* dw,
                                     int64_t lddw, int64_t rows, int64_t cols, int64_t out, int32_t odtype,
                                     void* workspace, size_t workspace_bytes, void* stream);
-muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, int64_t rows, int64_t cols, int64_t out, int64_t lddy,
-                                              uint64_t* bytes);
+/* dy: only its alignment is looked at. */
+muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, const void* dy, int64_t lddy, int64_t rows,
+                                              int64_t cols, int64_t out, uint64_t* bytes);
 
 /* Kernel classes reported by muon_handle_profile(). */
 enum {

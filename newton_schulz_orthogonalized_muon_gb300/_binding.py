@@ -120,7 +120,7 @@ def load_library(path: str | None = None):
             "muon_act8_restore": (i32, [vp, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp,
                                             ctypes.c_size_t, vp]),
-            "muon_act8_weight_grad_workspace": (i32, [vp, i64, i64, i64, i64, ctypes.POINTER(u64)]),
+            "muon_act8_weight_grad_workspace": (i32, [vp, vp, i64, i64, i64, i64, ctypes.POINTER(u64)]),
             "muon_workspace_size": (i32, [vp, ctypes.POINTER(MuonParamC), i32, i32, i32, i32, ctypes.POINTER(u64)]),
         }
         for name, (res, args) in sig.items():

@@ -308,10 +308,21 @@ struct WgradParams {
   const uint8_t* scales;
   const void* add;         // [out][cols] of odtype, row stride ldw, or nullptr
   void* dw;                // [out][cols] of odtype, row stride ldw
+  float* part;             // [splits][out][cols] partial results when splits > 1
   long long rows, ldy, ldc, lds, ldadd, ldw;
   int cols, out, odtype;
+  int splits;              // parts that the rows are cut into
+  unsigned* err;           // the handle's error word
+  unsigned long long timeout_ns;
+  int tiles_o, tiles_n, vec, vec_add;   // set by the launcher
 };
-cudaError_t launch_act8_wgrad(const WgradParams& p, cudaStream_t s);
+int wgrad_splits(long long rows, int cols, int out, int pairs);
+// maps, 3-D with 128-byte swizzle: {out, rows, 1} of dy in boxes of 64 columns and 64 rows, {columns, rows, 1} of
+// the codes in boxes of 128 columns and 64 rows
+cudaError_t launch_act8_wgrad(const WgradParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s);
+cudaError_t launch_act8_wgrad_join(const WgradParams& p, int sms, cudaStream_t s);
+cudaError_t launch_pad_rows(const __nv_bfloat16* src, long long lds, __nv_bfloat16* dst, long long ldd, long long rows,
+                            int cols, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------ attention
 struct AttnParams {

@@ -180,14 +180,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
     }
   }
 }
-// The same for one thread.
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, const AttnParams& p) {
-  if (mbar_wait_bounded(bar, parity, abort, p.timeout_ns)) return true;
-  if (*abort == 0) atomicOr(p.err, ERRBIT_TIMEOUT);
-  *abort = 1;
-  return false;
-}
-
 // The swizzled tiles need shared memory that starts on a 1 KB boundary, which
 // a kernel without static shared memory gets.
 __device__ __forceinline__ bool swizzle_aligned(uint32_t base, const AttnParams& p) {
@@ -205,13 +197,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
       : "memory");
 }
-// Untiled copy: both addresses and the size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // Loads a tile whose rows start at token `row`, by one lane, signalled on
 // `bar` (which the caller has armed with the tile's bytes).
 template <int DP>
@@ -253,36 +238,66 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, int b_mn_major) {
   return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(b_mn_major) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(TILE >> 4) << 24);
 }
+// The products are issued by one warp whose lanes stay together: every value
+// is warp-uniform and the instruction itself picks one lane.  Issued from a
+// branch that one lane takes, with descriptors rebuilt each time, a product
+// of 64 cycles took about 100 to issue.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p, q;\n"
+      " elect.sync _|q, 0xffffffff;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
 // A from TMEM
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n"
-      " .reg .pred p;\n"
+      " .reg .pred p, q;\n"
+      " elect.sync _|q, 0xffffffff;\n"
       " setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
       "}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc));
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
 }
+// arrives on `bar` when every product issued so far by this warp is done
+__device__ __forceinline__ void commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n"
+      " .reg .pred q;\n"
+      " elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// Descriptors of a tile: K-major (over dim) and MN-major (over tokens).  A
+// step along either adds its byte offset / 16.
+__device__ __forceinline__ uint64_t desc_dim(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_tokens(uint32_t tile) { return sdesc_sw128(tile, BOX_BYTES, 1024); }
 
 // D[128 x 128] = A B^T over dim: both tiles K-major.
 template <typename T, int DP>
-__device__ __forceinline__ void mma_over_dim(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_over_dim(uint32_t d, uint64_t a, uint64_t b) {
   constexpr uint32_t id = idesc<T>(TILE, 0);
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * BOX_BYTES + (kk & 3) * 32;
-    umma_bf16(d, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id, kk != 0 ? 1u : 0u);
+    const uint32_t off = ((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4;
+    umma_ss(d, a + off, b + off, id, kk != 0 ? 1u : 0u);
   }
 }
 // D[128 x DP] (+)= A B over 128 tokens: A 16-bit in TMEM, 64 tokens in 32
 // columns from `a0` and the other 64 from `a1`; B a tile read MN-major.
 template <typename T, int DP>
-__device__ __forceinline__ void mma_over_tokens(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_over_tokens(uint32_t d, uint32_t a0, uint32_t a1, uint64_t b, uint32_t acc) {
   constexpr uint32_t id = idesc<T>(DP, 1);
 #pragma unroll
   for (int kk = 0; kk < TILE / 16; ++kk)
-    umma_ts(d, kk < 4 ? a0 + kk * 8 : a1 + (kk - 4) * 8, sdesc_sw128(b + kk * 2048, BOX_BYTES, 1024), id,
-            (acc || kk != 0) ? 1u : 0u);
+    umma_ts(d, kk < 4 ? a0 + kk * 8 : a1 + (kk - 4) * 8, b + kk * (2048 >> 4), id, kk != 0 ? 1u : acc);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {

@@ -15,7 +15,7 @@
 // Both are bound by the tensor cores and the exponentials: per tile pair of
 // 128 x 128 with dim 128 the products take 1024 (768) cycles of the tensor
 // pipe at its full rate.  One CTA an SM, warp-specialised: warp 0 loads tiles
-// by TMA, one thread of warp 1 issues every tcgen05.mma, warps 4 - 11 turn
+// by TMA, warp 1 issues every tcgen05.mma, warps 4 - 11 turn
 // scores into p and ds.  p and ds never leave the SM: each warp writes its 16
 // bit values over the fp32 scores (or dP) that it read, and the next product
 // takes them from TMEM as its A operand.  Scores are transposed in the dkv
@@ -232,43 +232,41 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1 && n > 0) {
     // -------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t k_s = sb, v_s = sb + S::T;
-      auto scores = [&](int i) {
-        if (!wait_one(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
-        tc_fence_after();
-        mma_over_dim<T, DP>(tmem + S_COL, k_s, sb + S::A_OFF + (i % S::RA) * S::T);
-        umma_commit(&bar->s_full);
-        return true;
-      };
-      auto dprobs = [&](int i) {
-        if (!wait_one(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
-        tc_fence_after();
-        mma_over_dim<T, DP>(tmem + DP_COL, v_s, sb + S::B_OFF + (i % S::RB) * S::T);
-        umma_commit(&bar->dp_full[0]);
-        return true;
-      };
-      bool ok = wait_one(&bar->own[0], 0, abort, p) && scores(0) && wait_one(&bar->own[1], 0, abort, p) && dprobs(0);
-      for (int i = 0; ok && i < n; ++i) {
-        ok = wait_one(&bar->p_full, i & 1, abort, p);
-        if (!ok) break;
-        tc_fence_after();
-        mma_over_tokens<T, DP>(tmem + DV_COL, tmem + S_COL, tmem + S_COL + 64, sb + S::B_OFF + (i % S::RB) * S::T,
-                               i != 0);
-        umma_commit(&bar->b_empty[i % S::RB]);     // dP(i), issued earlier, has read this dO tile too
-        // the next scores overwrite the probabilities: the tensor pipe runs in order
-        if (i + 1 < n) ok = scores(i + 1);
-        ok = ok && wait_one(&bar->ds_full[0], i & 1, abort, p);
-        if (!ok) break;
-        tc_fence_after();
-        mma_over_tokens<T, DP>(tmem + DK_COL, tmem + DP_COL, tmem + DP_COL + 64, sb + S::A_OFF + (i % S::RA) * S::T,
-                               i != 0);
-        umma_commit(&bar->a_empty[i % S::RA]);
-        if (i + 1 < n) ok = dprobs(i + 1);
-      }
-      umma_commit(&bar->done);
-      if (!ok) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
+    const uint64_t k_d = desc_dim(sb), v_d = desc_dim(sb + S::T);
+    auto scores = [&](int i) {
+      if (!wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
+      tc_fence_after();
+      mma_over_dim<T, DP>(tmem + S_COL, k_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
+      commit_warp(&bar->s_full);
+      return true;
+    };
+    auto dprobs = [&](int i) {
+      if (!wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
+      tc_fence_after();
+      mma_over_dim<T, DP>(tmem + DP_COL, v_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
+      commit_warp(&bar->dp_full[0]);
+      return true;
+    };
+    bool ok = wait_warp(&bar->own[0], 0, abort, p) && scores(0) && wait_warp(&bar->own[1], 0, abort, p) && dprobs(0);
+    for (int i = 0; ok && i < n; ++i) {
+      ok = wait_warp(&bar->p_full, i & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+      mma_over_tokens<T, DP>(tmem + DV_COL, tmem + S_COL, tmem + S_COL + 64,
+                             desc_tokens(sb + S::B_OFF + (i % S::RB) * S::T), i != 0 ? 1u : 0u);
+      commit_warp(&bar->b_empty[i % S::RB]);     // dP(i), issued earlier, has read this dO tile too
+      // the next scores overwrite the probabilities: the tensor pipe runs in order
+      if (i + 1 < n) ok = scores(i + 1);
+      ok = ok && wait_warp(&bar->ds_full[0], i & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+      mma_over_tokens<T, DP>(tmem + DK_COL, tmem + DP_COL, tmem + DP_COL + 64,
+                             desc_tokens(sb + S::A_OFF + (i % S::RA) * S::T), i != 0 ? 1u : 0u);
+      commit_warp(&bar->a_empty[i % S::RA]);
+      if (i + 1 < n) ok = dprobs(i + 1);
     }
+    commit_warp(&bar->done);
+    if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
     __syncwarp();
   } else if (warp >= CTRL_WARPS && w.ok) {
     // --------------------------------------- probabilities, then outputs
@@ -426,37 +424,36 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1 && n > 0) {
     // -------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t q_s = sb, do_s = sb + S::T;
-      auto scores = [&](int i) {
-        if (!wait_one(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
-        tc_fence_after();
-        mma_over_dim<T, DP>(tmem + S_COL, q_s, sb + S::A_OFF + (i % S::RA) * S::T);
-        umma_commit(&bar->s_full);
-        return true;
-      };
-      auto dprobs = [&](int i) {
-        if (!wait_one(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
-        tc_fence_after();
-        mma_over_dim<T, DP>(tmem + DP_COL + (i & 1) * 128, do_s, sb + S::B_OFF + (i % S::RB) * S::T);
-        umma_commit(&bar->dp_full[i & 1]);
-        umma_commit(&bar->b_empty[i % S::RB]);
-        return true;
-      };
-      bool ok = wait_one(&bar->own[0], 0, abort, p) && scores(0) && wait_one(&bar->own[1], 0, abort, p) && dprobs(0);
-      for (int i = 0; ok && i < n; ++i) {
-        // the next tile's scores and dP (over ds(i - 1), which dq(i - 1) has read: the tensor pipe runs in order)
-        if (i + 1 < n) ok = wait_one(&bar->s_free, i & 1, abort, p) && scores(i + 1) && dprobs(i + 1);
-        ok = ok && wait_one(&bar->ds_full[i & 1], (i >> 1) & 1, abort, p);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t ds = tmem + DP_COL + (i & 1) * 128;
-        mma_over_tokens<T, DP>(tmem + DQ_COL, ds, ds + 64, sb + S::A_OFF + (i % S::RA) * S::T, i != 0);
-        umma_commit(&bar->a_empty[i % S::RA]);
-      }
-      umma_commit(&bar->done);
-      if (!ok) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
+    const uint64_t q_d = desc_dim(sb), do_d = desc_dim(sb + S::T);
+    auto scores = [&](int i) {
+      if (!wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
+      tc_fence_after();
+      mma_over_dim<T, DP>(tmem + S_COL, q_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
+      commit_warp(&bar->s_full);
+      return true;
+    };
+    auto dprobs = [&](int i) {
+      if (!wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
+      tc_fence_after();
+      mma_over_dim<T, DP>(tmem + DP_COL + (i & 1) * 128, do_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
+      commit_warp(&bar->dp_full[i & 1]);
+      commit_warp(&bar->b_empty[i % S::RB]);
+      return true;
+    };
+    bool ok = wait_warp(&bar->own[0], 0, abort, p) && scores(0) && wait_warp(&bar->own[1], 0, abort, p) && dprobs(0);
+    for (int i = 0; ok && i < n; ++i) {
+      // the next tile's scores and dP (over ds(i - 1), which dq(i - 1) has read: the tensor pipe runs in order)
+      if (i + 1 < n) ok = wait_warp(&bar->s_free, i & 1, abort, p) && scores(i + 1) && dprobs(i + 1);
+      ok = ok && wait_warp(&bar->ds_full[i & 1], (i >> 1) & 1, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t ds = tmem + DP_COL + (i & 1) * 128;
+      mma_over_tokens<T, DP>(tmem + DQ_COL, ds, ds + 64, desc_tokens(sb + S::A_OFF + (i % S::RA) * S::T),
+                             i != 0 ? 1u : 0u);
+      commit_warp(&bar->a_empty[i % S::RA]);
     }
+    commit_warp(&bar->done);
+    if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
     __syncwarp();
   } else if (warp >= CTRL_WARPS && w.ok) {
     // --------------------------------------- probabilities, then outputs

@@ -2,8 +2,7 @@
 // lse_i), in one pass over the keys with a running maximum and sum.
 //
 // A CTA owns two tiles of 128 queries of one head and walks the key tiles
-// that they see.  Warp 0 loads by TMA, one thread of warp 1 issues every
-// tcgen05.mma, and each tile has a warpgroup of its own (warps 4 - 7, 8 - 11)
+// that they see.  Warp 0 loads by TMA, warp 1 issues every tcgen05.mma, and each tile has a warpgroup of its own (warps 4 - 7, 8 - 11)
 // with one thread a query: while one tile's scores go through the
 // exponential, the tensor pipe works for the other.  The scores (fp32) and o
 // stay in TMEM; the probabilities are rounded to the operands' 16-bit type
@@ -111,185 +110,191 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int n = end - beg;
   auto sees = [&](int t, int tile) { return tile >= r[t].first && tile < r[t].first + r[t].count; };
 
-  if (warp == 0 && n > 0) {
-    // ---------------------------------------------------------- loads
-    if (lane == 0) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (r[t].count > 0) {
-          mbar_arrive_expect_tx(&bar->q_full[t], S::T);
-          load_tile<DP>(sb + t * S::T, &mq, &bar->q_full[t], w.h, w.q0 + i0 + t * TILE, w.b);
+  // a softmax thread holds a row of 128 scores: registers move from the
+  // control warps (4 x 32 x 88 + 8 x 32 x 200 of the 384 x 168 at launch)
+  if (warp < CTRL_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0 && n > 0) {
+      // ---------------------------------------------------------- loads
+      if (lane == 0) {
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (r[t].count > 0) {
+            mbar_arrive_expect_tx(&bar->q_full[t], S::T);
+            load_tile<DP>(sb + t * S::T, &mq, &bar->q_full[t], w.h, w.q0 + i0 + t * TILE, w.b);
+          }
         }
       }
-    }
-    uint32_t edges = 0;
-    int ik = 0, iv = 0;
-    for (int i = 0; i < n; ++i) {
-      const int j = (beg + i) * TILE, row = w.k0 + j, valid = w.nk - j;
-      const int sk = i % S::RK, sv = i % S::RV;
-      if (i >= S::RK && !wait_warp(&bar->k_empty[sk], (i / S::RK - 1) & 1, abort, p)) break;
-      if (lane == 0) {
-        // rows past the sequence give scores that are masked, whatever they hold
-        mbar_arrive_expect_tx(&bar->k_full[sk], S::T);
-        load_tile<DP>(sb + S::K_OFF + sk * S::T, &mk, &bar->k_full[sk], hk, row, w.b);
+      uint32_t edges = 0;
+      int ik = 0, iv = 0;
+      for (int i = 0; i < n; ++i) {
+        const int j = (beg + i) * TILE, row = w.k0 + j, valid = w.nk - j;
+        const int sk = i % S::RK, sv = i % S::RV;
+        if (i >= S::RK && !wait_warp(&bar->k_empty[sk], (i / S::RK - 1) & 1, abort, p)) break;
+        if (lane == 0) {
+          // rows past the sequence give scores that are masked, whatever they hold
+          mbar_arrive_expect_tx(&bar->k_full[sk], S::T);
+          load_tile<DP>(sb + S::K_OFF + sk * S::T, &mk, &bar->k_full[sk], hk, row, w.b);
+        }
+        ++ik;
+        if (i >= S::RV && !wait_warp(&bar->v_empty[sv], (i / S::RV - 1) & 1, abort, p)) break;
+        if (p.cu_q != nullptr && valid < TILE) {
+          if (!load_edge_tile<DP>(smem + S::V_OFF + sv * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p)) break;
+          if (lane == 0) mbar_arrive(&bar->v_full[sv]);
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(&bar->v_full[sv], S::T);
+          load_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, &bar->v_full[sv], hk, row, w.b);
+        }
+        ++iv;
       }
-      ++ik;
-      if (i >= S::RV && !wait_warp(&bar->v_empty[sv], (i / S::RV - 1) & 1, abort, p)) break;
-      if (p.cu_q != nullptr && valid < TILE) {
-        if (!load_edge_tile<DP>(smem + S::V_OFF + sv * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p)) break;
-        if (lane == 0) mbar_arrive(&bar->v_full[sv]);
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(&bar->v_full[sv], S::T);
-        load_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, &bar->v_full[sv], hk, row, w.b);
+      if (*abort != 0 && lane == 0) {
+        for (int t = 0; t < 2; ++t)
+          if (r[t].count > 0) mbar_wait_bounded(&bar->q_full[t], 0, nullptr, DRAIN_NS);
+        drain_ring<S::RK>(bar->k_full, ik);
+        drain_ring<S::RV>(bar->v_full, iv);
       }
-      ++iv;
-    }
-    if (*abort != 0 && lane == 0) {
-      for (int t = 0; t < 2; ++t)
-        if (r[t].count > 0) mbar_wait_bounded(&bar->q_full[t], 0, nullptr, DRAIN_NS);
-      drain_ring<S::RK>(bar->k_full, ik);
-      drain_ring<S::RV>(bar->v_full, iv);
-    }
-    __syncwarp();
-  } else if (warp == 1 && n > 0) {
-    // -------------------------------------------------------- products
-    if (lane == 0) {
+      __syncwarp();
+    } else if (warp == 1 && n > 0) {
+      // -------------------------------------------------------- products
       int steps[2] = {0, 0};                       // key tiles done, of each query tile
       auto scores = [&](int t, int i) {
-        if (!wait_one(&bar->k_full[i % S::RK], (i / S::RK) & 1, abort, p)) return false;
-        if (steps[t] == 0 && !wait_one(&bar->q_full[t], 0, abort, p)) return false;
+        if (!wait_warp(&bar->k_full[i % S::RK], (i / S::RK) & 1, abort, p)) return false;
+        if (steps[t] == 0 && !wait_warp(&bar->q_full[t], 0, abort, p)) return false;
         tc_fence_after();
-        mma_over_dim<T, DP>(tmem + t * TILE, sb + t * S::T, sb + S::K_OFF + (i % S::RK) * S::T);
-        umma_commit(&bar->s_full[t]);
+        mma_over_dim<T, DP>(tmem + t * TILE, desc_dim(sb + t * S::T), desc_dim(sb + S::K_OFF + (i % S::RK) * S::T));
+        commit_warp(&bar->s_full[t]);
         return true;
       };
       bool ok = true;
       for (int t = 0; t < 2; ++t)
         if (ok && sees(t, beg)) ok = scores(t, 0);
-      if (ok) umma_commit(&bar->k_empty[0]);
+      if (ok) commit_warp(&bar->k_empty[0]);
       for (int i = 0; ok && i < n; ++i) {
         for (int t = 0; ok && t < 2; ++t) {
           if (sees(t, beg + i)) {
-            ok = wait_one(&bar->p_full[t], steps[t] & 1, abort, p) &&
-                 wait_one(&bar->v_full[i % S::RV], (i / S::RV) & 1, abort, p);
+            ok = wait_warp(&bar->p_full[t], steps[t] & 1, abort, p) &&
+                 wait_warp(&bar->v_full[i % S::RV], (i / S::RV) & 1, abort, p);
             if (!ok) break;
             tc_fence_after();
             const uint32_t pr = tmem + t * TILE;
-            mma_over_tokens<T, DP>(tmem + 256 + t * TILE, pr, pr + 32, sb + S::V_OFF + (i % S::RV) * S::T,
-                                   steps[t] != 0);
-            umma_commit(&bar->o_done[t]);
+            mma_over_tokens<T, DP>(tmem + 256 + t * TILE, pr, pr + 32,
+                                   desc_tokens(sb + S::V_OFF + (i % S::RV) * S::T), steps[t] != 0 ? 1u : 0u);
+            commit_warp(&bar->o_done[t]);
             ++steps[t];
           }
           // over the probabilities just used: the tensor pipe runs in order
           if (i + 1 < n && sees(t, beg + i + 1)) ok = scores(t, i + 1);
         }
         if (!ok) break;
-        umma_commit(&bar->v_empty[i % S::RV]);
-        if (i + 1 < n) umma_commit(&bar->k_empty[(i + 1) % S::RK]);
+        commit_warp(&bar->v_empty[i % S::RV]);
+        if (i + 1 < n) commit_warp(&bar->k_empty[(i + 1) % S::RK]);
       }
       if (!ok) {
-        umma_commit(&bar->drain);
-        mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
+        commit_warp(&bar->drain);
+        if (lane == 0) mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
+        __syncwarp();
       }
     }
-    __syncwarp();
-  } else if (warp >= CTRL_WARPS && w.ok) {
-    // ------------------------------------------------ softmax, output
-    const int t = (warp - CTRL_WARPS) >> 2, quad = warp & 3;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t s_at = tmem + lanes + t * TILE, o_at = tmem + lanes + 256 + t * TILE;
-    const int q0 = i0 + t * TILE, q = q0 + quad * 32 + lane;
-    const int off = w.nk - w.nq;
-    const float c = p.scale * LOG2E;
-    float top = -INFINITY;                         // the scores' reference, before scaling
-    F2 sum2 = f2_make(0.f, 0.f);
-    bool ok = true;
-    const int cnt = r[t].count;
-    for (int i = 0; i < cnt; ++i) {
-      const int j0 = (r[t].first + i) * TILE;
-      float v[TILE];
-      ok = wait_warp(&bar->s_full[t], i & 1, abort, p);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < TILE; k += 32) tmem_ld32(s_at + k, v + k);
-      tmem_ld_wait();
-      if (j0 + TILE > w.nk ||
-          (p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window)))) {
-        int lo = 0, hi = w.nk - j0;
-        if (p.causal) {
-          hi = min(hi, q + off + 1 - j0);
-          if (p.window > 0) lo = q + off - p.window + 1 - j0;
-        }
-#pragma unroll
-        for (int k = 0; k < TILE; ++k)
-          if (k < lo || k >= hi) v[k] = -INFINITY;
-      }
-      float m[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-      for (int k = 4; k < TILE; k += 8) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = k + 4 + e < TILE ? fmaxf(fmaxf(m[e], v[k + e]), v[k + 4 + e]) : fmaxf(m[e], v[k + e]);
-      }
-      const float mt = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-      if (i == 0) {
-        top = mt;
-      } else {
-        const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
-        if (__any_sync(0xffffffffu, up)) {
-          ok = wait_warp(&bar->o_done[t], (i - 1) & 1, abort, p);
-          if (!ok) break;
-          tc_fence_after();
-          const float f = !up ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - mt) * c);
-          if (up) top = mt;
-          sum2 = f2_mul(sum2, f2_make(f, f));
-#pragma unroll 1
-          for (int k = 0; k < DP; k += 32) {
-            float o[32];
-            tmem_ld32(o_at + k, o);
-            tmem_ld_wait();
-            uint32_t* u = reinterpret_cast<uint32_t*>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(o_at + k, u);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (w.ok) {
+      // ------------------------------------------------ softmax, output
+      const int t = (warp - CTRL_WARPS) >> 2, quad = warp & 3;
+      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+      const uint32_t s_at = tmem + lanes + t * TILE, o_at = tmem + lanes + 256 + t * TILE;
+      const int q0 = i0 + t * TILE, q = q0 + quad * 32 + lane;
+      const int off = w.nk - w.nq;
+      const float c = p.scale * LOG2E;
+      float top = -INFINITY;                         // the scores' reference, before scaling
+      F2 sum2 = f2_make(0.f, 0.f);
+      bool ok = true;
+      const int cnt = r[t].count;
+      for (int i = 0; i < cnt; ++i) {
+        const int j0 = (r[t].first + i) * TILE;
+        float v[TILE];
+        ok = wait_warp(&bar->s_full[t], i & 1, abort, p);
+        if (!ok) break;
+        tc_fence_after();
+  #pragma unroll
+        for (int k = 0; k < TILE; k += 32) tmem_ld32(s_at + k, v + k);
+        tmem_ld_wait();
+        if (j0 + TILE > w.nk ||
+            (p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window)))) {
+          int lo = 0, hi = w.nk - j0;
+          if (p.causal) {
+            hi = min(hi, q + off + 1 - j0);
+            if (p.window > 0) lo = q + off - p.window + 1 - j0;
           }
-          tmem_st_wait();
+  #pragma unroll
+          for (int k = 0; k < TILE; ++k)
+            if (k < lo || k >= hi) v[k] = -INFINITY;
         }
-      }
-      const float ref = top == -INFINITY ? 0.f : -top * c;
-      const F2 cc = f2_make(c, c), rr = f2_make(ref, ref);
-#pragma unroll
-      for (int k = 0; k < TILE; k += 64) {
-#pragma unroll
-        for (int e = k; e < k + 64; e += 2) {
-          const float2 a = f2_split(f2_fma(f2_make(v[e], v[e + 1]), cc, rr));
-          v[e] = exp2_fast(a.x);
-          v[e + 1] = exp2_fast(a.y);
-          sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
+        float m[4] = {v[0], v[1], v[2], v[3]};
+  #pragma unroll
+        for (int k = 4; k < TILE; k += 8) {
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) m[e] = k + 4 + e < TILE ? fmaxf(fmaxf(m[e], v[k + e]), v[k + 4 + e]) : fmaxf(m[e], v[k + e]);
         }
-        store_half<T>(s_at + k / 2, v + k);
+        const float mt = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        if (i == 0) {
+          top = mt;
+        } else {
+          const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
+          if (__any_sync(0xffffffffu, up)) {
+            ok = wait_warp(&bar->o_done[t], (i - 1) & 1, abort, p);
+            if (!ok) break;
+            tc_fence_after();
+            const float f = !up ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - mt) * c);
+            if (up) top = mt;
+            sum2 = f2_mul(sum2, f2_make(f, f));
+  #pragma unroll 1
+            for (int k = 0; k < DP; k += 32) {
+              float o[32];
+              tmem_ld32(o_at + k, o);
+              tmem_ld_wait();
+              uint32_t* u = reinterpret_cast<uint32_t*>(o);
+  #pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(o_at + k, u);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float ref = top == -INFINITY ? 0.f : -top * c;
+        const F2 cc = f2_make(c, c), rr = f2_make(ref, ref);
+  #pragma unroll
+        for (int k = 0; k < TILE; k += 64) {
+  #pragma unroll
+          for (int e = k; e < k + 64; e += 2) {
+            const float2 a = f2_split(f2_fma(f2_make(v[e], v[e + 1]), cc, rr));
+            v[e] = exp2_fast(a.x);
+            v[e + 1] = exp2_fast(a.y);
+            sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
+          }
+          store_half<T>(s_at + k / 2, v + k);
+        }
+        warp_arrive(&bar->p_full[t]);
       }
-      warp_arrive(&bar->p_full[t]);
-    }
-    if (ok && cnt > 0) {
-      ok = wait_warp(&bar->o_done[t], (cnt - 1) & 1, abort, p);
-      tc_fence_after();
-    }
-    if (ok) {
-      const float2 s2 = f2_split(sum2);
-      const float sum = s2.x + s2.y;
-      T* row = q < w.nq ? static_cast<T*>(p.out) + w.b * p.ob + static_cast<long long>(w.q0 + q) * p.os + w.h * p.oh
-                        : nullptr;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (cnt > 0) {
-#pragma unroll 1
-        for (int k = 0; k < DP; k += 32) store_cols32<T>(o_at + k, row, k, p.dim, inv);
-      } else if (row != nullptr) {
-        for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+      if (ok && cnt > 0) {
+        ok = wait_warp(&bar->o_done[t], (cnt - 1) & 1, abort, p);
+        tc_fence_after();
       }
-      if (row != nullptr)
-        p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + q] =
-            sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
+      if (ok) {
+        const float2 s2 = f2_split(sum2);
+        const float sum = s2.x + s2.y;
+        T* row = q < w.nq ? static_cast<T*>(p.out) + w.b * p.ob + static_cast<long long>(w.q0 + q) * p.os + w.h * p.oh
+                          : nullptr;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (cnt > 0) {
+  #pragma unroll 1
+          for (int k = 0; k < DP; k += 32) store_cols32<T>(o_at + k, row, k, p.dim, inv);
+        } else if (row != nullptr) {
+          for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (row != nullptr)
+          p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + q] =
+              sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
+      }
     }
   }
   tc_fence_before();

@@ -141,6 +141,38 @@ AttnParams attn_params(muon_handle_t h, const muon_attention_t& a) {
   return p;
 }
 
+// Map of [rows][cols], row stride ld elements of `size` bytes (bf16 or
+// bytes), in boxes of 64 rows and one 128-byte swizzle row of columns.
+bool rows_map(muon_handle_t h, CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int size,
+              uint32_t box_cols) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1};
+  const cuuint64_t pitch = static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(size);
+  cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[3] = {box_cols, 64, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return h->encode(map, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scratch of a weight gradient: the splits' partial results, then dy with
+// padded rows where TMA cannot read it in place.
+struct WgradPlan {
+  int splits;
+  uint64_t part_bytes, pad_bytes;
+  uint64_t bytes() const { return part_bytes + pad_bytes; }
+};
+
+WgradPlan wgrad_plan(muon_handle_t h, const void* dy, int64_t lddy, int64_t rows, int64_t cols, int64_t out) {
+  WgradPlan w{};
+  w.splits = wgrad_splits(rows, static_cast<int>(cols), static_cast<int>(out), h->num_sms / 2);
+  if (w.splits > 1) w.part_bytes = round256(static_cast<uint64_t>(w.splits) * out * cols * 4);
+  if (rows > 0 && ((rows > 1 && lddy % 8 != 0) || !aligned(dy, 16)))
+    w.pad_bytes = round256(static_cast<uint64_t>(rows) * ((out + 7) / 8 * 8) * 2);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -360,14 +392,13 @@ muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t l
   });
 }
 
-muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, int64_t rows, int64_t cols, int64_t out, int64_t lddy,
-                                              uint64_t* bytes) {
+muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, const void* dy, int64_t lddy, int64_t rows,
+                                              int64_t cols, int64_t out, uint64_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded([&]() -> muon_status_t {
     MUON_CHECK(rows >= 0 && rows <= kMaxTokens && cols >= 0 && cols <= kMaxTokens && out >= 0 && out <= kMaxTokens,
                "negative or oversized shape");
-    (void)lddy;
-    *bytes = 0;
+    *bytes = cols == 0 || out == 0 ? 0 : wgrad_plan(h, dy, lddy, rows, cols, out).bytes();
     return MUON_OK;
   });
 }
@@ -378,23 +409,58 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
                                     void* workspace, size_t workspace_bytes, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded([&]() -> muon_status_t {
-    uint64_t need = 0;
-    muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
-    if (st == MUON_OK) st = muon_act8_weight_grad_workspace(h, rows, cols, out, lddy, &need);
+    const muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
     if (st != MUON_OK) return st;
+    MUON_CHECK(out >= 0 && out <= kMaxTokens, "negative or oversized shape");
     MUON_CHECK(odtype == MUON_F32 || odtype == MUON_BF16, "odtype must be MUON_F32 or MUON_BF16");
     if (cols == 0 || out == 0) return MUON_OK;
     MUON_CHECK(dw != nullptr && (lddw >= cols || out == 1), "dw is NULL or its row stride is below cols");
     MUON_CHECK(add == nullptr || ldadd >= cols || out == 1, "add's row stride is below cols");
     MUON_CHECK(rows == 0 || (dy != nullptr && (lddy >= out || rows == 1)), "dy is NULL or its row stride is below out");
-    MUON_CHECK(need == 0 || (workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256)),
+    const WgradPlan plan = wgrad_plan(h, dy, lddy, rows, cols, out);
+    MUON_CHECK(plan.bytes() == 0 ||
+                   (workspace != nullptr && workspace_bytes >= plan.bytes() && aligned(workspace, 256)),
                "the workspace is too small or not 256-byte aligned");
     DeviceGuard guard(h->device);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
-    const WgradParams p{static_cast<const __nv_bfloat16*>(dy), codes, scales, add, dw, rows, lddy, ldc, lds, ldadd,
-                        lddw, static_cast<int>(cols), static_cast<int>(out), odtype};
+    WgradParams p{};
+    p.codes = codes;
+    p.scales = scales;
+    p.add = add;
+    p.dw = dw;
+    p.part = static_cast<float*>(workspace);
+    p.rows = rows;
+    p.ldc = ldc;
+    p.lds = lds;
+    p.ldadd = ldadd;
+    p.ldw = lddw;
+    p.cols = static_cast<int>(cols);
+    p.out = static_cast<int>(out);
+    p.odtype = odtype;
+    p.splits = plan.splits;
+    p.err = h->err;
+    p.timeout_ns = h->timeout_ns;
     h->prof_tag = -1;
-    MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, stream), "weight gradient launch");
+    CUtensorMap maps[2] = {};
+    if (rows > 0) {
+      const void* base = dy;
+      int64_t ld = lddy;
+      if (plan.pad_bytes > 0) {
+        __nv_bfloat16* pad = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + plan.part_bytes);
+        ld = (out + 7) / 8 * 8;
+        MUON_LAUNCH(MUON_K_WGRAD, launch_pad_rows(static_cast<const __nv_bfloat16*>(dy), lddy, pad, ld, rows, p.out,
+                                                  h->num_sms, stream),
+                    "row padding launch");
+        base = pad;
+      }
+      if (rows == 1) ld = (out + 7) / 8 * 8;
+      if (!rows_map(h, &maps[0], base, out, rows, ld, 2, 64) ||
+          !rows_map(h, &maps[1], codes, (cols + 127) / 128 * 128, rows, ldc, 1, 128))
+        return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
+    }
+    MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, maps, h->num_sms / 2, stream), "weight gradient launch");
+    if (p.splits > 1)
+      MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad_join(p, h->num_sms, stream), "weight gradient join launch");
     return MUON_OK;
   });
 }

@@ -353,7 +353,8 @@ def act8_weight_grad(dy, codes, scales, *, add=None, out=None, dtype=None, handl
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=dev)
         need = ctypes.c_uint64()
-        c.check(c.lib.muon_act8_weight_grad_workspace(c.h.ptr, rows, cols, shape[0], ldy, ctypes.byref(need)),
+        c.check(c.lib.muon_act8_weight_grad_workspace(c.h.ptr, dyr.data_ptr(), ldy, rows, cols, shape[0],
+                                                      ctypes.byref(need)),
                 "muon_act8_weight_grad_workspace")
         ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
         c.check(c.lib.muon_act8_weight_grad(

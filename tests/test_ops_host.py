@@ -100,7 +100,7 @@ def test_operators_reject_a_null_handle(lib):
                                      None) == 1
     assert lib.muon_layer_norm_workspace(None, 1, 1, ctypes.byref(out)) == 1
     assert lib.muon_attention_workspace(None, ctypes.byref(a), ctypes.byref(out)) == 1
-    assert lib.muon_act8_weight_grad_workspace(None, 1, 1, 1, 1, ctypes.byref(out)) == 1
+    assert lib.muon_act8_weight_grad_workspace(None, None, 1, 1, 1, 1, ctypes.byref(out)) == 1
 
 
 def test_operators_refuse_host_tensors():
