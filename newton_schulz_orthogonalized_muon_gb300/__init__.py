@@ -30,7 +30,8 @@ def __getattr__(name):
         return getattr(optim, name)
     if name in _OPS_NAMES:
         from . import ops
-        return getattr(ops, name)
+        globals()[name] = getattr(ops, name)     # found directly from now on
+        return globals()[name]
     raise AttributeError(name)
 
 

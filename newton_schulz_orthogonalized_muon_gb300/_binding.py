@@ -113,9 +113,9 @@ def load_library(path: str | None = None):
             "muon_layer_norm_backward": (i32, [vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, i32, i32,
                                                vp, ctypes.c_size_t, vp]),
             "muon_layer_norm_workspace": (i32, [vp, i64, i64, ctypes.POINTER(u64)]),
-            "muon_attention_forward": (i32, [vp, ctypes.POINTER(MuonAttentionC), vp]),
-            "muon_attention_backward": (i32, [vp, ctypes.POINTER(MuonAttentionC), vp, ctypes.c_size_t, vp]),
-            "muon_attention_workspace": (i32, [vp, ctypes.POINTER(MuonAttentionC), ctypes.POINTER(u64)]),
+            "muon_attention_forward": (i32, [vp, ctypes.c_char_p, vp]),
+            "muon_attention_backward": (i32, [vp, ctypes.c_char_p, vp, ctypes.c_size_t, vp]),
+            "muon_attention_workspace": (i32, [vp, ctypes.c_char_p, ctypes.POINTER(u64)]),
             "muon_act8_store": (i32, [vp, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_restore": (i32, [vp, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp,

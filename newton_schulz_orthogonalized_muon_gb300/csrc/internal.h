@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace muon {
 
 // Programmatic dependent launch of the library's kernels, from the
@@ -33,6 +35,20 @@ cudaError_t launch_k(bool pdl, void (*kern)(Params...), dim3 grid, dim3 block, s
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
+// Lets `kern` use `bytes` of dynamic shared memory: the attribute is set once
+// for each kernel and device (`done`, one bit a device, is the caller's static
+// of that kernel).
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit != 0 && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 struct SrcEntry;

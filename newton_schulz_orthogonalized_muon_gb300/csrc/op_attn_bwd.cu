@@ -549,8 +549,9 @@ cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, int part, cud
   }
   auto dkv = attn_dkv_kernel<T, DP>;
   auto dq = attn_dq_kernel<T, DP>;
-  const void* f = part == 1 ? reinterpret_cast<const void*>(dkv) : reinterpret_cast<const void*>(dq);
-  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP>::BYTES);
+  static std::atomic<unsigned long long> done[2];
+  const cudaError_t e = part == 1 ? allow_smem(reinterpret_cast<const void*>(dkv), Smem<DP>::BYTES, done[0])
+                                  : allow_smem(reinterpret_cast<const void*>(dq), Smem<DP>::BYTES, done[1]);
   if (e != cudaSuccess) return e;
   if (part == 1)
     dkv<<<static_cast<unsigned>(nk), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(kt),

@@ -310,7 +310,8 @@ cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, cudaStream_t 
   const long long items = tiles * p.heads * (packed ? 1 : p.batch);
   if (items > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   auto kern = attn_fwd_kernel<T, DP>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP>::BYTES);
+  static std::atomic<unsigned long long> done;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(items), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], p, static_cast<int>(tiles));
   return cudaGetLastError();

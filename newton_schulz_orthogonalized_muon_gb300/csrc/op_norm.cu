@@ -313,7 +313,8 @@ cudaError_t launch_cfg(const NormParams& p, int parts, cudaStream_t s) {
     constexpr int smem = (NormCfg<TPR>::GROUPS > 1 || !kReg) ? 2 * TPR * EPT * 4 : 0;
     auto kern = norm_bwd_kernel<T, VEC, TPR, EPT, kReg>;
     if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      static std::atomic<unsigned long long> done;
+      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
       if (e != cudaSuccess) return e;
     }
     kern<<<parts, NormCfg<TPR>::THREADS, smem, s>>>(p);

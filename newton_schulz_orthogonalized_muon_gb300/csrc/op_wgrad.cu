@@ -546,7 +546,8 @@ cudaError_t launch_act8_wgrad(const WgradParams& q, const CUtensorMap* maps, int
   const long long es = p.odtype == DT_F32 ? 4 : 2;
   p.vec = reinterpret_cast<uintptr_t>(p.dw) % (4 * es) == 0 && p.ldw % 4 == 0;
   p.vec_add = reinterpret_cast<uintptr_t>(p.add) % 16 == 0 && p.ldadd * es % 16 == 0;
-  const cudaError_t e = cudaFuncSetAttribute(act8_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  static std::atomic<unsigned long long> done;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(act8_wgrad_kernel), SMEM, done);
   if (e != cudaSuccess) return e;
   act8_wgrad_kernel<<<2 * static_cast<unsigned>(items < pairs ? items : pairs), THREADS, SMEM, s>>>(maps[0], maps[1], p);
   return cudaGetLastError();

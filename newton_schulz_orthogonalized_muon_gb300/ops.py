@@ -13,7 +13,9 @@ written on another stream have to be ready there, as for any call.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
+import struct
 
 import torch
 
@@ -25,64 +27,63 @@ BLOCK = 128                       # columns that share one scale
 _CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16, torch.float16: MUON_F16}
 
 
-def _code(t: torch.Tensor, what: str, allowed=(torch.float32, torch.bfloat16, torch.float16)) -> int:
-    if t.dtype not in allowed:
-        raise ValueError(f"{what} must be one of {', '.join(str(d) for d in allowed)}, not {t.dtype}")
-    return _CODE[t.dtype]
+def _code(t: torch.Tensor, what: str, allowed=tuple(_CODE)) -> int:
+    dtype = t.dtype
+    if dtype not in allowed:
+        raise ValueError(f"{what} must be one of {', '.join(str(d) for d in allowed)}, not {dtype}")
+    return _CODE[dtype]
 
 
-def _cuda(what: str, *tensors):
-    """Every tensor (None aside) on one CUDA device."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{what} must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{what} must be on one device")
+def _device(what: str, first, *rest) -> int:
+    """The index of the CUDA device that all the tensors (None aside) are on."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError(f"{what} must be CUDA tensors")
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != dev):
+            raise ValueError(f"{what} must be CUDA tensors on one device")
     return dev
 
 
-class _Call:
-    """The handle and the stream of one call; scratch and outputs are
-    allocated inside it, so that torch ties them to that stream."""
+# the current stream of a device as an integer; the private call skips the
+# construction of a Stream object (2 us of a 20 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("h", "lib", "stream", "_ctx")
 
-    def __init__(self, dev, handle, stream):
-        self.h = handle or _binding.default_handle(dev.index)
-        if self.h.device != dev.index:
-            raise ValueError(f"the handle is on device {self.h.device}, the tensors on {dev.index}")
-        self.lib = self.h._lib
-        self._ctx = None if stream is None else torch.cuda.stream(stream)
-        self.stream = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+def _handle(dev: int, handle):
+    if handle is None:
+        return _binding.default_handle(dev)
+    if handle.device != dev:
+        raise ValueError(f"the handle is on device {handle.device}, the tensors on {dev}")
+    return handle
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-
-    def check(self, status: int, what: str):
-        if status != 0:
-            self.h._raise(status, what)
+def _on_stream(fn):
+    """``stream=``: the call runs with that stream current, so that torch ties
+    outputs and scratch to it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _rows(t: torch.Tensor, what: str):
     """(tensor, rows, row stride) of [.., cols] seen as rows: the last
     dimension contiguous, the others with one stride between rows.  Anything
     else is copied once."""
-    if t.dim() == 0:
+    shape = t.shape
+    if len(shape) == 0:
         raise ValueError(f"{what} must have at least one dimension")
-    cols = t.shape[-1]
-    if t.dim() == 2 and (t.stride(1) == 1 or cols <= 1) and (t.stride(0) >= cols or t.shape[0] <= 1):
-        return t, t.shape[0], max(t.stride(0), cols)
+    cols = shape[-1]
+    if len(shape) == 2:
+        ld, one = t.stride()
+        if one == 1 or cols <= 1:
+            if ld >= cols or shape[0] <= 1:
+                return t, shape[0], max(ld, cols)
     if not t.is_contiguous():
         try:
             flat = t.view(-1, cols)
@@ -96,113 +97,136 @@ def _rows(t: torch.Tensor, what: str):
 
 # ---------------------------------------------------------------- layer norm
 def _affine(t, what, x, cols):
+    """Pointer and type code of a weight or bias vector."""
     if t is None:
-        return None
+        return None, MUON_F32
     if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {cols} elements")
-    if t.dtype not in (torch.float32, x.dtype):
+    if t.dtype is not torch.float32 and t.dtype is not x.dtype:
         raise ValueError(f"{what} must be float32 or {x.dtype}")
-    return t
+    return t.data_ptr(), _CODE[t.dtype]
 
 
-def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, handle=None, stream=None):
+@_on_stream
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, handle=None):
     """Layer norm over the last dimension: ``(y, mean, rstd)``.
 
     x: [.., cols] fp32, bf16 or fp16, cols up to 16384; weight and bias:
     [cols], fp32 or x's type, or None (ones, zeros).  y has x's type and
     shape, mean and rstd (fp32, x.shape[:-1]) are what the backward pass
     takes."""
-    dev = _cuda("x, weight and bias", x, weight, bias)
+    dev = _device("x, weight and bias", x, weight, bias)
     code = _code(x, "x")
-    cols = x.shape[-1] if x.dim() else 0
-    weight, bias = _affine(weight, "weight", x, cols), _affine(bias, "bias", x, cols)
-    w = weight if weight is not None else bias
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+    xr, rows, ldx = _rows(x, "x")
+    shape = x.shape
+    cols = shape[-1]
+    wptr, wcode = _affine(weight, "weight", x, cols)
+    bptr, bcode = _affine(bias, "bias", x, cols)
+    if wptr is not None and bptr is not None and wcode != bcode:
         raise ValueError("weight and bias must have one type")
-    with _Call(dev, handle, stream) as c:
-        xr, rows, ldx = _rows(x, "x")
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        c.check(c.lib.muon_layer_norm_forward(
-            c.h.ptr, xr.data_ptr(), ldx, weight.data_ptr() if weight is not None else None,
-            bias.data_ptr() if bias is not None else None, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), rows,
-            cols, code, _CODE[w.dtype] if w is not None else MUON_F32, eps, c.stream), "muon_layer_norm_forward")
+    h = _handle(dev, handle)
+    y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    st = h._lib.muon_layer_norm_forward(h.ptr, xr.data_ptr(), ldx, wptr, bptr, y.data_ptr(), cols, mean.data_ptr(),
+                                        rstd.data_ptr(), rows, cols, code, bcode if wptr is None else wcode, eps,
+                                        _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_layer_norm_forward")
     return y, mean, rstd
 
 
-def layer_norm_backward(dy, x, mean, rstd, weight=None, *, handle=None, stream=None):
+@_on_stream
+def layer_norm_backward(dy, x, mean, rstd, weight=None, *, handle=None):
     """``(dx, dweight, dbias)`` of layer_norm: dx in x's type, dweight and
     dbias fp32 [cols], summed over all rows in a fixed order."""
-    dev = _cuda("dy, x, mean, rstd and weight", dy, x, mean, rstd, weight)
+    dev = _device("x, dy, mean, rstd and weight", x, dy, mean, rstd, weight)
     code = _code(x, "x")
-    if dy.shape != x.shape or dy.dtype != x.dtype:
+    shape = x.shape
+    if dy.shape != shape or dy.dtype != x.dtype:
         raise ValueError("dy must have x's shape and type")
+    xr, rows, ldx = _rows(x, "x")
+    gr, _, ldg = _rows(dy, "dy")
     for t, what in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous float32 of shape {tuple(x.shape[:-1])}")
-    cols = x.shape[-1]
-    weight = _affine(weight, "weight", x, cols)
-    with _Call(dev, handle, stream) as c:
-        xr, rows, ldx = _rows(x, "x")
-        gr, _, ldg = _rows(dy, "dy")
-        need = ctypes.c_uint64()
-        c.check(c.lib.muon_layer_norm_workspace(c.h.ptr, rows, cols, ctypes.byref(need)), "muon_layer_norm_workspace")
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        dwb = torch.empty((2, cols), dtype=torch.float32, device=dev)
-        c.check(c.lib.muon_layer_norm_backward(
-            c.h.ptr, gr.data_ptr(), ldg, xr.data_ptr(), ldx, mean.data_ptr(), rstd.data_ptr(),
-            weight.data_ptr() if weight is not None else None, dx.data_ptr(), cols, dwb.data_ptr(),
-            dwb.data_ptr() + 4 * cols, rows, cols, code, _CODE[weight.dtype] if weight is not None else MUON_F32,
-            ws.data_ptr(), need.value, c.stream), "muon_layer_norm_backward")
-    return dx, dwb[0], dwb[1]
+        if t.dtype != torch.float32 or t.shape != shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous float32 of shape {tuple(shape[:-1])}")
+    cols = shape[-1]
+    wptr, wcode = _affine(weight, "weight", x, cols)
+    h = _handle(dev, handle)
+    lib, need, where = h._lib, ctypes.c_uint64(), x.device
+    st = lib.muon_layer_norm_workspace(h.ptr, rows, cols, ctypes.byref(need))
+    if st:
+        h._raise(st, "muon_layer_norm_workspace")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=where)
+    dx = torch.empty(shape, dtype=x.dtype, device=where)
+    dw = torch.empty(cols, dtype=torch.float32, device=where)
+    db = torch.empty_like(dw)
+    st = lib.muon_layer_norm_backward(h.ptr, gr.data_ptr(), ldg, xr.data_ptr(), ldx, mean.data_ptr(), rstd.data_ptr(),
+                                      wptr, dx.data_ptr(), cols, dw.data_ptr(), db.data_ptr(), rows, cols, code,
+                                      wcode, ws.data_ptr(), need.value, _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_layer_norm_backward")
+    return dx, dw, db
 
 
 # ----------------------------------------------------------------- attention
-def _heads(t, what, packed):
+def _strides(t, what, packed):
     """Strides (batch, token, head) of [batch, token, head, dim], or of
     [token, head, dim] when packed."""
-    want = 3 if packed else 4
-    if t.dim() != want:
-        raise ValueError(f"{what} must have {want} dimensions")
     st = t.stride()
+    if len(st) != (3 if packed else 4):
+        raise ValueError(f"{what} must have {3 if packed else 4} dimensions")
     if st[-1] != 1 and t.shape[-1] != 1:
         raise ValueError(f"{what} must be contiguous in its last dimension")
     return (0, st[0], st[1]) if packed else st[:3]
 
 
-def _attention_args(q, k, v, causal, window, scale, cu_q, cu_k):
-    packed = cu_q is not None or cu_k is not None
-    code = _code(q, "q", (torch.bfloat16, torch.float16))
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("q, k and v must have one type")
-    a = MuonAttentionC()
-    a.q_stride[:], a.k_stride[:], a.v_stride[:] = (_heads(t, n, packed) for t, n in ((q, "q"), (k, "k"), (v, "v")))
-    if k.shape != v.shape or q.shape[-1] != k.shape[-1] or (not packed and q.shape[0] != k.shape[0]):
-        raise ValueError(f"shapes do not go together: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    if packed:
-        if cu_q is None or cu_k is None:
-            raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
-        for t, what in ((cu_q, "cu_seqlens_q"), (cu_k, "cu_seqlens_k")):
-            if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < 1 or not t.is_contiguous():
-                raise ValueError(f"{what} must be a contiguous int32 vector of at least one element")
-        if cu_q.shape != cu_k.shape:
-            raise ValueError("cu_seqlens_q and cu_seqlens_k must have one length")
-        a.batch = cu_q.shape[0] - 1
-        a.cu_seqlens_q, a.cu_seqlens_k = cu_q.data_ptr(), cu_k.data_ptr()
-    else:
-        a.batch = q.shape[0]
-    a.sq, a.heads, a.dim = q.shape[-3:]
-    a.sk, a.kv_heads = k.shape[-3:-1]
-    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.causal, a.window, a.dtype = 1 if causal else 0, int(window), code
-    a.scale = 1.0 / math.sqrt(a.dim) if scale is None and a.dim else float(scale or 0.0)
-    return a, packed
+# muon_attention_t: eleven pointers, eight times three strides, nine integers, the scale
+_ATTENTION = struct.Struct("@11P24q9if")
+assert _ATTENTION.size == ctypes.sizeof(MuonAttentionC)
 
 
+class _Attention:
+    """The checked arguments of an attention call."""
+
+    __slots__ = ("packed", "strides", "ints", "scale", "cu", "lse_shape")
+
+    def __init__(self, q, k, v, causal, window, scale, cu_q, cu_k):
+        packed = self.packed = cu_q is not None or cu_k is not None
+        code = _code(q, "q", (torch.bfloat16, torch.float16))
+        if k.dtype is not q.dtype or v.dtype is not q.dtype:
+            raise ValueError("q, k and v must have one type")
+        self.strides = (*_strides(q, "q", packed), *_strides(k, "k", packed), *_strides(v, "v", packed))
+        qs, ks = q.shape, k.shape
+        if ks != v.shape or qs[-1] != ks[-1] or (not packed and qs[0] != ks[0]):
+            raise ValueError(f"shapes do not go together: q {tuple(qs)}, k {tuple(ks)}, v {tuple(v.shape)}")
+        if packed:
+            if cu_q is None or cu_k is None:
+                raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
+            for t, what in ((cu_q, "cu_seqlens_q"), (cu_k, "cu_seqlens_k")):
+                if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < 1 or not t.is_contiguous():
+                    raise ValueError(f"{what} must be a contiguous int32 vector of at least one element")
+            if cu_q.shape != cu_k.shape:
+                raise ValueError("cu_seqlens_q and cu_seqlens_k must have one length")
+            batch = cu_q.shape[0] - 1
+            self.cu = (cu_q.data_ptr(), cu_k.data_ptr())
+        else:
+            batch = qs[0]
+            self.cu = (0, 0)
+        sq, heads, dim = qs[-3:]
+        self.lse_shape = (heads, sq) if packed else (batch, heads, sq)
+        self.ints = (batch, sq, ks[-3], heads, ks[-2], dim, 1 if causal else 0, int(window), code)
+        if max(self.ints) >= 1 << 31 or min(self.ints) < 0:
+            raise ValueError("negative or oversized shape or window")
+        self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(dim) if dim else 0.0
+
+    def pack(self, pointers, strides):
+        return _ATTENTION.pack(*pointers, *self.cu, *self.strides, *strides, *self.ints, self.scale)
+
+
+@_on_stream
 def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None,
-              handle=None, stream=None):
+              handle=None):
     """Attention, ``(o, lse)``.
 
     q: [batch, sq, heads, dim], k and v: [batch, sk, kv_heads, dim], bf16 or
@@ -212,58 +236,65 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_
     more than sequences) the tensors are [tokens, heads, dim], sequences one
     after another.  Query i stands at place i + sk - sq of its sequence;
     ``causal``: it sees keys up to its place, with ``window`` only the last
-    ``window`` of them.  scale: 1 / sqrt(dim) by default.
+    ``window`` of them.  scale (above 0): 1 / sqrt(dim) by default.
     o has q's shape and type (a query that sees no key: 0); lse is fp32
     [batch, heads, sq] or [heads, tokens] (there: -inf)."""
-    dev = _cuda("q, k, v and the offsets", q, k, v, cu_seqlens_q, cu_seqlens_k)
-    a, packed = _attention_args(q, k, v, causal, window, scale, cu_seqlens_q, cu_seqlens_k)
-    with _Call(dev, handle, stream) as c:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        lse = torch.empty((a.heads, a.sq) if packed else (a.batch, a.heads, a.sq), dtype=torch.float32, device=dev)
-        a.o, a.lse = o.data_ptr(), lse.data_ptr()
-        a.o_stride[:] = _heads(o, "o", packed)
-        c.check(c.lib.muon_attention_forward(c.h.ptr, ctypes.byref(a), c.stream), "muon_attention_forward")
+    dev = _device("q, k, v and the offsets", q, k, v, cu_seqlens_q, cu_seqlens_k)
+    a = _Attention(q, k, v, causal, window, scale, cu_seqlens_q, cu_seqlens_k)
+    h = _handle(dev, handle)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(a.lse_shape, dtype=torch.float32, device=q.device)
+    args = a.pack((q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0),
+                  _strides(o, "o", a.packed) + _NO_STRIDES)
+    st = h._lib.muon_attention_forward(h.ptr, args, _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_attention_forward")
     return o, lse
 
 
+_NO_STRIDES = (0,) * 12
+
+
+@_on_stream
 def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int = 0, scale=None, cu_seqlens_q=None,
-                       cu_seqlens_k=None, handle=None, stream=None):
+                       cu_seqlens_k=None, handle=None):
     """``(dq, dk, dv)`` of attention, from its output and lse: the
     probabilities are recomputed, nothing of size sq x sk is kept.  dk and dv
     are summed over the query heads that share them, in a fixed order."""
-    dev = _cuda("do, q, k, v, o, lse and the offsets", do, q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
-    a, packed = _attention_args(q, k, v, causal, window, scale, cu_seqlens_q, cu_seqlens_k)
+    dev = _device("q, k, v, do, o, lse and the offsets", q, k, v, do, o, lse, cu_seqlens_q, cu_seqlens_k)
+    a = _Attention(q, k, v, causal, window, scale, cu_seqlens_q, cu_seqlens_k)
+    dtype, where = q.dtype, q.device
     for t, what in ((do, "do"), (o, "o")):
-        if t.shape != q.shape or t.dtype != q.dtype:
+        if t.shape != q.shape or t.dtype is not dtype:
             raise ValueError(f"{what} must have q's shape and type")
-    if lse.dtype != torch.float32 or lse.shape != ((a.heads, a.sq) if packed else (a.batch, a.heads, a.sq)) \
-            or not lse.is_contiguous():
+    if lse.dtype is not torch.float32 or lse.shape != a.lse_shape or not lse.is_contiguous():
         raise ValueError("lse must be the contiguous float32 tensor that attention returned")
-    with _Call(dev, handle, stream) as c:
-        if do.stride(-1) != 1 or any(s % 8 for s in do.stride()[:-1]):
-            do = do.contiguous()         # autograd hands over expanded gradients
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        a.o, a.lse, a.dout = o.data_ptr(), lse.data_ptr(), do.data_ptr()
-        a.dq, a.dk, a.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
-        a.o_stride[:], a.dout_stride[:] = _heads(o, "o", packed), _heads(do, "do", packed)
-        a.dq_stride[:], a.dk_stride[:], a.dv_stride[:] = (_heads(t, "", packed) for t in (dq, dk, dv))
-        need = ctypes.c_uint64()
-        c.check(c.lib.muon_attention_workspace(c.h.ptr, ctypes.byref(a), ctypes.byref(need)),
-                "muon_attention_workspace")
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        c.check(c.lib.muon_attention_backward(c.h.ptr, ctypes.byref(a), ws.data_ptr(), need.value, c.stream),
-                "muon_attention_backward")
+    h = _handle(dev, handle)
+    st = do.stride()
+    if st[-1] != 1 or 0 in st or any(s % 8 for s in st[:-1]):
+        do = do.contiguous()             # autograd hands over expanded gradients
+    dq = torch.empty(q.shape, dtype=dtype, device=where)
+    dk = torch.empty(k.shape, dtype=dtype, device=where)
+    dv = torch.empty_like(dk)
+    kv = _strides(dk, "dk", a.packed)
+    args = a.pack((q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
+                   dq.data_ptr(), dk.data_ptr(), dv.data_ptr()),
+                  (*_strides(o, "o", a.packed), *_strides(do, "do", a.packed), *_strides(dq, "dq", a.packed), *kv, *kv))
+    lib = h._lib
+    need = ctypes.c_uint64()
+    st = lib.muon_attention_workspace(h.ptr, args, ctypes.byref(need))
+    if st:
+        h._raise(st, "muon_attention_workspace")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=where)
+    st = lib.muon_attention_backward(h.ptr, args, ws.data_ptr(), need.value, _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_attention_backward")
     return dq, dk, dv
 
 
 # --------------------------------------------------- activations in 8 bits
-def _blocks(cols: int) -> int:
-    return -(-cols // BLOCK)
-
-
-def act8_store(x, *, handle=None, stream=None):
+@_on_stream
+def act8_store(x, *, handle=None):
     """x [rows, cols] (fp32, bf16, fp16) in 8 bits: ``(codes, scales)``.
 
     codes: float8_e4m3fn [rows, cols]; scales: uint8 [ceil(cols / 128),
@@ -274,92 +305,105 @@ def act8_store(x, *, handle=None, stream=None):
     padded storage (whole blocks, 16 rows), which act8_weight_grad reads in
     place; copies in other layouts are taken too, at the cost of one more
     copy."""
-    dev = _cuda("x", x)
+    dev = _device("x", x)
     code = _code(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
-    with _Call(dev, handle, stream) as c:
-        xr, rows, ldx = _rows(x, "x")
-        cols = x.shape[1]
-        ldc, lds = _blocks(cols) * BLOCK, -(-rows // 16) * 16
-        codes = torch.empty((rows, ldc), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((_blocks(cols), lds), dtype=torch.uint8, device=dev)
-        c.check(c.lib.muon_act8_store(c.h.ptr, xr.data_ptr(), ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds,
-                                      rows, cols, code, c.stream), "muon_act8_store")
-    return codes[:, :cols], scales[:, :rows]
+    xr, rows, ldx = _rows(x, "x")
+    cols = x.shape[1]
+    h = _handle(dev, handle)
+    blocks, lds = -(-cols // BLOCK), -(-rows // 16) * 16
+    ldc = blocks * BLOCK
+    codes = torch.empty((rows, ldc), dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty((blocks, lds), dtype=torch.uint8, device=x.device)
+    st = h._lib.muon_act8_store(h.ptr, xr.data_ptr(), ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, rows, cols,
+                                code, _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_act8_store")
+    return codes if ldc == cols else codes[:, :cols], scales if lds == rows else scales[:, :rows]
 
 
 def _act8_operands(codes, scales):
     """codes and scales as the kernels read them (padded rows), copied if
-    they come in another layout, and their row strides."""
-    if codes.dim() != 2 or codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    they come in another layout, their shape and row strides."""
+    if codes.dim() != 2 or (codes.dtype is not torch.float8_e4m3fn and codes.dtype is not torch.uint8):
         raise ValueError("codes must be 2-D float8_e4m3fn")
     rows, cols = codes.shape
-    if scales.dtype != torch.uint8 or tuple(scales.shape) != (_blocks(cols), rows):
-        raise ValueError(f"scales must be uint8 of shape {(_blocks(cols), rows)}")
+    blocks = -(-cols // BLOCK)
+    if scales.dtype is not torch.uint8 or scales.shape != (blocks, rows):
+        raise ValueError(f"scales must be uint8 of shape {(blocks, rows)}")
+    ldc, lds = codes.stride(), scales.stride()
     if rows and cols:
-        if codes.stride(1) != 1 or codes.stride(0) % BLOCK or codes.stride(0) < cols or codes.data_ptr() % 16:
-            wide = torch.zeros((rows, _blocks(cols) * BLOCK), dtype=torch.uint8, device=codes.device)
-            wide[:, :cols] = codes.view(torch.uint8) if codes.dtype != torch.uint8 else codes
-            codes = wide
-        if scales.stride(1) != 1 or scales.stride(0) % 16 or scales.stride(0) < rows or scales.data_ptr() % 16:
-            tall = torch.zeros((scales.shape[0], -(-rows // 16) * 16), dtype=torch.uint8, device=codes.device)
+        if ldc[1] != 1 or ldc[0] % BLOCK or ldc[0] < cols or codes.data_ptr() % 16:
+            wide = torch.zeros((rows, blocks * BLOCK), dtype=torch.uint8, device=codes.device)
+            wide[:, :cols] = codes.view(torch.uint8) if codes.dtype is not torch.uint8 else codes
+            codes, ldc = wide, wide.stride()
+        if lds[1] != 1 or lds[0] % 16 or lds[0] < rows or scales.data_ptr() % 16:
+            tall = torch.zeros((blocks, -(-rows // 16) * 16), dtype=torch.uint8, device=codes.device)
             tall[:, :rows] = scales
-            scales = tall
-    return codes, scales, rows, cols, codes.stride(0), scales.stride(0) if scales.dim() == 2 else 0
+            scales, lds = tall, tall.stride()
+    return codes, scales, rows, cols, ldc[0], lds[0]
 
 
-def act8_restore(codes, scales, *, dtype=torch.bfloat16, handle=None, stream=None):
+@_on_stream
+def act8_restore(codes, scales, *, dtype=torch.bfloat16, handle=None):
     """The values that act8_store kept, [rows, cols] in ``dtype``."""
-    dev = _cuda("codes and scales", codes, scales)
+    dev = _device("codes and scales", codes, scales)
     if dtype not in _CODE:
         raise ValueError(f"unsupported dtype {dtype}")
-    with _Call(dev, handle, stream) as c:
-        codes, scales, rows, cols, ldc, lds = _act8_operands(codes, scales)
-        out = torch.empty((rows, cols), dtype=dtype, device=dev)
-        c.check(c.lib.muon_act8_restore(c.h.ptr, codes.data_ptr(), ldc, scales.data_ptr(), lds, out.data_ptr(), cols,
-                                        rows, cols, _CODE[dtype], c.stream), "muon_act8_restore")
+    h = _handle(dev, handle)
+    codes, scales, rows, cols, ldc, lds = _act8_operands(codes, scales)
+    out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    st = h._lib.muon_act8_restore(h.ptr, codes.data_ptr(), ldc, scales.data_ptr(), lds, out.data_ptr(), cols, rows,
+                                  cols, _CODE[dtype], _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_act8_restore")
     return out
 
 
-def act8_weight_grad(dy, codes, scales, *, add=None, out=None, dtype=None, handle=None, stream=None):
+@_on_stream
+def act8_weight_grad(dy, codes, scales, *, add=None, out=None, dtype=None, handle=None):
     """dw [out, cols] = dy^T x (+ add) of a linear layer y = x w^T whose
     input x is kept in 8 bits.
 
     dy: bf16 [rows, out]; add: the gradient so far; out: where dw is written
     (``out=add`` adds in place); dtype: float32 (default) or bfloat16, that
     of add and out if they are given."""
-    dev = _cuda("dy, codes, scales, add and out", dy, codes, scales, add, out)
+    dev = _device("dy, codes, scales, add and out", dy, codes, scales, add, out)
     _code(dy, "dy", (torch.bfloat16,))
     if dy.dim() != 2 or codes.dim() != 2 or dy.shape[0] != codes.shape[0]:
         raise ValueError("dy must be [rows, out] and codes [rows, cols]")
     shape = (dy.shape[1], codes.shape[1])
-    for t, what in ((add, "add"), (out, "out")):
+    ld = [shape[1], shape[1]]
+    for i, (t, what) in enumerate(((add, "add"), (out, "out"))):
         if t is None:
             continue
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{what} must have shape {shape}")
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise ValueError(f"{what} must have type {dtype}")
         dtype = t.dtype
-        if t.stride(1) != 1 and shape[1] > 1 or t.stride(0) < shape[1] and shape[0] > 1:
+        st = t.stride()
+        if st[1] != 1 and shape[1] > 1 or st[0] < shape[1] and shape[0] > 1:
             raise ValueError(f"{what} must have contiguous rows")
+        ld[i] = max(st[0], shape[1])
     dtype = torch.float32 if dtype is None else dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError("dtype must be float32 or bfloat16")
-    with _Call(dev, handle, stream) as c:
-        dyr, _, ldy = _rows(dy, "dy")
-        xc, sc, rows, cols, ldc, lds = _act8_operands(codes, scales)
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        need = ctypes.c_uint64()
-        c.check(c.lib.muon_act8_weight_grad_workspace(c.h.ptr, dyr.data_ptr(), ldy, rows, cols, shape[0],
-                                                      ctypes.byref(need)),
-                "muon_act8_weight_grad_workspace")
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        c.check(c.lib.muon_act8_weight_grad(
-            c.h.ptr, dyr.data_ptr(), ldy, xc.data_ptr(), ldc, sc.data_ptr(), lds,
-            add.data_ptr() if add is not None else None, max(add.stride(0), cols) if add is not None else cols,
-            out.data_ptr(), max(out.stride(0), cols), rows, cols, shape[0], _CODE[dtype],
-            ws.data_ptr() if ws is not None else None, need.value, c.stream), "muon_act8_weight_grad")
+    h = _handle(dev, handle)
+    dyr, _, ldy = _rows(dy, "dy")
+    xc, sc, rows, cols, ldc, lds = _act8_operands(codes, scales)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dy.device)
+    lib, need = h._lib, ctypes.c_uint64()
+    st = lib.muon_act8_weight_grad_workspace(h.ptr, dyr.data_ptr(), ldy, rows, cols, shape[0], ctypes.byref(need))
+    if st:
+        h._raise(st, "muon_act8_weight_grad_workspace")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dy.device) if need.value else None
+    st = lib.muon_act8_weight_grad(h.ptr, dyr.data_ptr(), ldy, xc.data_ptr(), ldc, sc.data_ptr(), lds,
+                                   add.data_ptr() if add is not None else None, ld[0], out.data_ptr(), ld[1], rows,
+                                   cols, shape[0], _CODE[dtype], ws.data_ptr() if ws is not None else None,
+                                   need.value, _raw_stream(dev))
+    if st:
+        h._raise(st, "muon_act8_weight_grad")
     return out

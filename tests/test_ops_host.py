@@ -88,18 +88,18 @@ def test_attention_struct_layout_matches_the_c_compiler(tmp_path):
 
 def test_operators_reject_a_null_handle(lib):
     from newton_schulz_orthogonalized_muon_gb300._binding import MuonAttentionC
-    a, out = MuonAttentionC(), ctypes.c_uint64()
+    a, out = bytes(MuonAttentionC()), ctypes.c_uint64()
     assert lib.muon_layer_norm_forward(None, None, 1, None, None, None, 1, None, None, 1, 1, 0, 0, 1e-5, None) == 1
     assert lib.muon_layer_norm_backward(None, None, 1, None, 1, None, None, None, None, 1, None, None, 1, 1, 0, 0, None,
                                         0, None) == 1
-    assert lib.muon_attention_forward(None, ctypes.byref(a), None) == 1
-    assert lib.muon_attention_backward(None, ctypes.byref(a), None, 0, None) == 1
+    assert lib.muon_attention_forward(None, a, None) == 1
+    assert lib.muon_attention_backward(None, a, None, 0, None) == 1
     assert lib.muon_act8_store(None, None, 1, None, 128, None, 16, 1, 1, 0, None) == 1
     assert lib.muon_act8_restore(None, None, 128, None, 16, None, 1, 1, 1, 0, None) == 1
     assert lib.muon_act8_weight_grad(None, None, 1, None, 128, None, 16, None, 1, None, 1, 1, 1, 1, 0, None, 0,
                                      None) == 1
     assert lib.muon_layer_norm_workspace(None, 1, 1, ctypes.byref(out)) == 1
-    assert lib.muon_attention_workspace(None, ctypes.byref(a), ctypes.byref(out)) == 1
+    assert lib.muon_attention_workspace(None, a, ctypes.byref(out)) == 1
     assert lib.muon_act8_weight_grad_workspace(None, None, 1, 1, 1, 1, ctypes.byref(out)) == 1
 
 
