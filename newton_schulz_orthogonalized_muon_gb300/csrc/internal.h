@@ -298,10 +298,12 @@ struct NormParams {
   int cols, dtype, wdtype;
   int wvec;                // set by the launcher: weight and bias are 16-byte aligned
   float eps;
+  unsigned* err;           // the handle's error word
+  unsigned long long timeout_ns;
 };
 constexpr int kNormMaxCols = 16384;
-int norm_threads(int cols);                             // threads that share a row
-int norm_parts(long long rows, int cols, int sms);      // CTAs of a pass = partial rows of dw and db
+int norm_parts(const NormParams& p, bool bwd, int sms);          // CTAs of a pass = partial rows of dw and db
+int norm_max_parts(long long rows, int cols, int sms);          // the most that a pass of this size has
 cudaError_t launch_norm_fwd(const NormParams& p, int parts, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams& p, int parts, cudaStream_t s);
 cudaError_t launch_norm_join(const NormParams& p, int parts, float* dw, float* db, cudaStream_t s);

@@ -204,8 +204,10 @@ muon_status_t muon_layer_norm_forward(muon_handle_t h, const void* x, int64_t ld
     p.dtype = dtype;
     p.wdtype = wdtype;
     p.eps = eps;
+    p.err = h->err;
+    p.timeout_ns = h->timeout_ns;
     h->prof_tag = -1;
-    MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_fwd(p, norm_parts(rows, p.cols, h->num_sms), stream),
+    MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_fwd(p, norm_parts(p, false, h->num_sms), stream),
                 "layer norm launch");
     return MUON_OK;
   });
@@ -216,7 +218,7 @@ muon_status_t muon_layer_norm_workspace(muon_handle_t h, int64_t rows, int64_t c
   return guarded([&]() -> muon_status_t {
     const muon_status_t st = check_norm(h, rows, cols, MUON_F32, MUON_F32);
     if (st != MUON_OK) return st;
-    *bytes = round256(static_cast<uint64_t>(norm_parts(rows, static_cast<int>(cols), h->num_sms)) * 2 * cols * 4);
+    *bytes = round256(static_cast<uint64_t>(norm_max_parts(rows, static_cast<int>(cols), h->num_sms)) * 2 * cols * 4);
     return MUON_OK;
   });
 }
@@ -235,7 +237,6 @@ muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t 
     MUON_CHECK(dweight != nullptr && dbias != nullptr, "dweight or dbias is NULL");
     NormParams p{};
     p.cols = static_cast<int>(cols);
-    const int parts = norm_parts(rows, p.cols, h->num_sms);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
     if (rows > 0) {
       MUON_CHECK(dy != nullptr && x != nullptr && dx != nullptr && mean != nullptr && rstd != nullptr,
@@ -252,6 +253,8 @@ muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t 
     p.mean = const_cast<float*>(mean);
     p.rstd = const_cast<float*>(rstd);
     p.part = static_cast<float*>(workspace);
+    p.err = h->err;
+    p.timeout_ns = h->timeout_ns;
     p.rows = rows;
     p.ldx = ldx;
     p.ldy = lddx;
@@ -259,6 +262,7 @@ muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t 
     p.dtype = dtype;
     p.wdtype = wdtype;
     h->prof_tag = -1;
+    const int parts = norm_parts(p, true, h->num_sms);
     if (rows > 0) MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_bwd(p, parts, stream), "layer norm backward launch");
     MUON_LAUNCH(MUON_K_LAYER_NORM, launch_norm_join(p, parts, dweight, dbias, stream), "layer norm join launch");
     return MUON_OK;
