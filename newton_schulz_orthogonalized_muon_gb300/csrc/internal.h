@@ -351,7 +351,7 @@ struct AttnParams {
                            // b * lse_b + h * lse_h + s
   void *out;               // forward: o
   void *dq, *dk, *dv;      // backward
-  float* stat_lse;         // backward, scratch: lse log2(e) and rowsum(dO * O), 128 values a query tile:
+  float* stat_lse;         // backward, scratch: -lse log2(e) and -rowsum(dO * O), 128 values a query tile:
   float* stat_delta;       // tile t of (b, h) at ((b * heads + h) * qtiles + t) * 128
   long long qb, qs, qh, kb, ks, kh, vb, vs, vh, ob, os, oh, dob, dos, doh;   // strides in elements
   long long dqb, dqs, dqh, dkb, dks, dkh, dvb, dvs, dvh;
@@ -368,8 +368,8 @@ struct AttnParams {
   unsigned long long timeout_ns;
 };
 int attn_qtiles(int sq, int batch, bool packed);
-// m: 4-D tensor maps {dim, head, token, batch} with boxes of 64 columns and
-// 128 tokens, 128-byte swizzle: q, k, v (and do).
+// m: 4-D tensor maps {dim, head, token, batch} of q, k, v (and do) with boxes
+// of 64 columns and 128 tokens (64 backward with dim <= 64), 128-byte swizzle.
 cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s);
 // part 0: statistics; 1: dk and dv; 2: dq
 cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s);

@@ -1,10 +1,9 @@
 // What the attention kernels share: how a work item finds its sequence, the
 // operand tiles in shared memory, and the tensor-core and TMEM access.
 //
-// A tile is 128 rows (tokens of one head) by DP = 64 or 128 columns of 16-bit
-// elements, in boxes of 128 rows x 64 columns (128-byte rows, 128-byte
-// swizzle, 16 KB), as TMA writes them from a 4-D map {dim, head, token,
-// batch}.  Columns past `dim` and, in the batched form, rows past the
+// A tile is 64 or 128 rows (tokens of one head) by DP = 64 or 128 columns of
+// 16-bit elements, in boxes of 64 columns (128-byte rows, 128-byte swizzle),
+// as TMA writes them from a 4-D map {dim, head, token, batch}.  Columns past `dim` and, in the batched form, rows past the
 // sequence are filled with zeros.  One such tile serves both as a K-major
 // operand (the product runs over dim) and as an MN-major one (over tokens).
 #pragma once
@@ -135,7 +134,9 @@ struct Range {
   int first, count;
 };
 
-// Key tiles that the queries [i0, i1] of a sequence see (count 0: none).
+// Key tiles of ROWS rows that the queries [i0, i1] of a sequence see (count
+// 0: none).
+template <int ROWS = TILE>
 __device__ __forceinline__ Range key_tiles(const AttnParams& p, const Work& w, int i0, int i1) {
   int beg = 0, end = w.nk;
   if (p.causal) {
@@ -144,10 +145,11 @@ __device__ __forceinline__ Range key_tiles(const AttnParams& p, const Work& w, i
     if (p.window > 0) beg = max(0, i0 + off - p.window + 1);
   }
   if (end <= beg) return Range{0, 0};
-  return Range{beg / TILE, (end + TILE - 1) / TILE - beg / TILE};
+  return Range{beg / ROWS, (end + ROWS - 1) / ROWS - beg / ROWS};
 }
 
 // Query tiles that see any of the keys [j0, j1].
+template <int ROWS>
 __device__ __forceinline__ Range query_tiles(const AttnParams& p, const Work& w, int j0, int j1) {
   int beg = 0, end = w.nq;
   if (p.causal) {
@@ -156,7 +158,7 @@ __device__ __forceinline__ Range query_tiles(const AttnParams& p, const Work& w,
     if (p.window > 0) end = static_cast<int>(min(static_cast<long long>(end), static_cast<long long>(j1) - off + p.window));
   }
   if (end <= beg) return Range{0, 0};
-  return Range{beg / TILE, (end + TILE - 1) / TILE - beg / TILE};
+  return Range{beg / ROWS, (end + ROWS - 1) / ROWS - beg / ROWS};
 }
 
 // ------------------------------------------------------------------- waits
@@ -197,12 +199,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
       : "memory");
 }
-// Loads a tile whose rows start at token `row`, by one lane, signalled on
-// `bar` (which the caller has armed with the tile's bytes).
-template <int DP>
+// Loads a tile of ROWS rows that starts at token `row`, by one lane, signalled
+// on `bar` (which the caller has armed with the tile's bytes); the map's boxes
+// have BOX rows.
+template <int DP, int ROWS = TILE, int BOX = TILE>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int h, int row, int b) {
 #pragma unroll
-  for (int x = 0; x < DP / 64; ++x) tma_load_4d(dst + x * BOX_BYTES, map, bar, 64 * x, h, row, b);
+  for (int x = 0; x < DP / 64; ++x)
+#pragma unroll
+    for (int y = 0; y < ROWS; y += BOX) tma_load_4d(dst + (x * ROWS + y) * 128, map, bar, 64 * x, h, row + y, b);
 }
 
 // The same by a whole warp for a packed sequence that ends inside the tile:
@@ -210,21 +215,21 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 // zeros, so that a NaN or an infinity there has no part in a product with a
 // zero probability.  `edge` is the warp's own barrier; on return the tile is
 // complete for the async proxy.
-template <int DP>
+template <int DP, int ROWS = TILE, int BOX = TILE>
 __device__ __forceinline__ bool load_edge_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* edge, uint32_t& phase,
                                                int h, int row, int valid, volatile int* abort, const AttnParams& p) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) {
-    mbar_arrive_expect_tx(edge, tile_bytes<DP>());
-    load_tile<DP>(smem_u32(dst), map, edge, h, row, 0);
+    mbar_arrive_expect_tx(edge, DP / 64 * ROWS * 128);
+    load_tile<DP, ROWS, BOX>(smem_u32(dst), map, edge, h, row, 0);
   }
   __syncwarp();
   if (!wait_warp(edge, phase & 1u, abort, p)) return false;
   ++phase;
 #pragma unroll
   for (int x = 0; x < DP / 64; ++x)
-    for (int i = valid * 8 + lane; i < TILE * 8; i += 32)
-      *reinterpret_cast<uint4*>(dst + x * BOX_BYTES + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = valid * 8 + lane; i < ROWS * 8; i += 32)
+      *reinterpret_cast<uint4*>(dst + x * ROWS * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
   return true;
@@ -239,30 +244,58 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, int b_mn_major) {
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(TILE >> 4) << 24);
 }
 // The products are issued by one warp whose lanes stay together: every value
-// is warp-uniform and the instruction itself picks one lane.  Issued from a
-// branch that one lane takes, with descriptors rebuilt each time, a product
-// of 64 cycles took about 100 to issue.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// is warp-uniform and the instructions themselves pick one lane, once for
+// four products.  (Issued from a branch that one lane takes, with descriptors
+// rebuilt each time, a product of 64 cycles took about 100 to issue.)
+//
+// Four products of 16 along the summed index; SS: A from shared memory, its
+// descriptor 32 bytes further each time, and so B's (K-major).
+__device__ __forceinline__ void umma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n"
-      " .reg .pred p, q;\n"
+      " .reg .pred p, q, t;\n"
+      " .reg .b64 a1, a2, a3, b1, b2, b3;\n"
       " elect.sync _|q, 0xffffffff;\n"
       " setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " add.s64 a1, %1, 2;\n"
+      " add.s64 b1, %2, 2;\n"
+      " add.s64 a2, %1, 4;\n"
+      " add.s64 b2, %2, 4;\n"
+      " add.s64 a3, %1, 6;\n"
+      " add.s64 b3, %2, 6;\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n"
       "}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-// A from TMEM
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// A from TMEM: 16 tokens are eight columns; after two products `skip` more
+// columns to the next 32 tokens.  B MN-major: 16 rows, 2 KB, further each time.
+template <int SKIP>
+__device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n"
-      " .reg .pred p, q;\n"
+      " .reg .pred p, q, t;\n"
+      " .reg .b32 a1, a2, a3;\n"
+      " .reg .b64 b1, b2, b3;\n"
       " elect.sync _|q, 0xffffffff;\n"
       " setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " add.s32 a1, %1, 8;\n"
+      " add.s64 b1, %2, 128;\n"
+      " add.s32 a2, %1, %5;\n"
+      " add.s64 b2, %2, 256;\n"
+      " add.s32 a3, %1, %6;\n"
+      " add.s64 b3, %2, 384;\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
       "}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "r"(a), "l"(b), "r"(id), "r"(acc), "n"(16 + SKIP), "n"(24 + SKIP)
       : "memory");
 }
 // arrives on `bar` when every product issued so far by this warp is done
@@ -275,29 +308,30 @@ __device__ __forceinline__ void commit_warp(uint64_t* bar) {
       "}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-// Descriptors of a tile: K-major (over dim) and MN-major (over tokens).  A
-// step along either adds its byte offset / 16.
+// Descriptors of a tile of ROWS rows: K-major (over dim) and MN-major (over
+// tokens).  A step along either adds its byte offset / 16.
 __device__ __forceinline__ uint64_t desc_dim(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
-__device__ __forceinline__ uint64_t desc_tokens(uint32_t tile) { return sdesc_sw128(tile, BOX_BYTES, 1024); }
+template <int ROWS = TILE>
+__device__ __forceinline__ uint64_t desc_tokens(uint32_t tile) { return sdesc_sw128(tile, ROWS * 128, 1024); }
 
-// D[128 x 128] = A B^T over dim: both tiles K-major.
-template <typename T, int DP>
+// D[128 x N] = A B^T over dim: both tiles K-major, B of N rows.
+template <typename T, int DP, int N = TILE>
 __device__ __forceinline__ void mma_over_dim(uint32_t d, uint64_t a, uint64_t b) {
-  constexpr uint32_t id = idesc<T>(TILE, 0);
+  constexpr uint32_t id = idesc<T>(N, 0);
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
-    const uint32_t off = ((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4;
-    umma_ss(d, a + off, b + off, id, kk != 0 ? 1u : 0u);
-  }
+  for (int x = 0; x < DP / 64; ++x) umma_ss4(d, a + x * (TILE * 128 >> 4), b + x * (N * 128 >> 4), id, x != 0 ? 1u : 0u);
 }
-// D[128 x DP] (+)= A B over 128 tokens: A 16-bit in TMEM, 64 tokens in 32
-// columns from `a0` and the other 64 from `a1`; B a tile read MN-major.
-template <typename T, int DP>
-__device__ __forceinline__ void mma_over_tokens(uint32_t d, uint32_t a0, uint32_t a1, uint64_t b, uint32_t acc) {
+// D[128 x DP] (+)= A B over N tokens: A 16-bit in TMEM, CHUNK tokens (two a
+// column) at a time with CHUNK columns from one chunk to the next; B a tile
+// of N rows read MN-major.
+template <typename T, int DP, int CHUNK, int N = TILE>
+__device__ __forceinline__ void mma_over_tokens(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+  static_assert(CHUNK == 32 || CHUNK == N, "chunks of a warp's columns, or of a row");
   constexpr uint32_t id = idesc<T>(DP, 1);
+  constexpr int kSkip = CHUNK == 32 ? 16 : 0;
 #pragma unroll
-  for (int kk = 0; kk < TILE / 16; ++kk)
-    umma_ts(d, kk < 4 ? a0 + kk * 8 : a1 + (kk - 4) * 8, b + kk * (2048 >> 4), id, kk != 0 ? 1u : acc);
+  for (int k = 0; k < N / 64; ++k)
+    umma_ts4<kSkip>(d, a + k * (32 + 2 * kSkip), b + k * (4 * 2048 >> 4), id, k != 0 ? 1u : acc);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -311,6 +345,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+// 16 rows x 32 columns, spread over the warp as the matrix instructions'
+// accumulators are: v[4 j ..] of thread t are columns 8 j + 2 (t % 4) + {0, 1}
+// of row t / 4, then of row t / 4 + 8.  (A value that belongs to a column is
+// then wanted by a quarter of the threads, not by all.)
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// The same values in 16 bits, two a column: r[2 j] is column 4 j + t % 4 of
+// row t / 4, r[2 j + 1] of row t / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -320,6 +373,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -365,13 +426,16 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int n) {
   }
 }
 
-// 64 values of a row, rounded to T, into 32 TMEM columns.
-template <typename T>
-__device__ __forceinline__ void store_half(uint32_t taddr, const float* v) {
-  uint32_t r[32];
+// 2 N values of a row, rounded to T, into N = 16 or 32 TMEM columns.
+template <typename T, int N>
+__device__ __forceinline__ void store_rounded(uint32_t taddr, const float* v) {
+  uint32_t r[N];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) r[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
-  tmem_st32(taddr, r);
+  for (int k = 0; k < N; ++k) r[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+  if constexpr (N == 32)
+    tmem_st32(taddr, r);
+  else
+    tmem_st16(taddr, r);
   tmem_st_wait();
 }
 

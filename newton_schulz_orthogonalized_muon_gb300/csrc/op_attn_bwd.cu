@@ -14,8 +14,8 @@
 //
 // Both are bound by the tensor cores and the exponentials: per tile pair of
 // 128 x 128 with dim 128 the products take 1024 (768) cycles of the tensor
-// pipe at its full rate.  One CTA an SM, warp-specialised: warp 0 loads tiles
-// by TMA, warp 1 issues every tcgen05.mma, warps 4 - 11 turn
+// pipe at its full rate.  Warp-specialised: warp 0 loads tiles by TMA,
+// warp 1 issues every tcgen05.mma, the other warps turn
 // scores into p and ds.  p and ds never leave the SM: each warp writes its 16
 // bit values over the fp32 scores (or dP) that it read, and the next product
 // takes them from TMEM as its A operand.  Scores are transposed in the dkv
@@ -29,13 +29,27 @@ namespace {
 
 using namespace attn;
 
-constexpr int CTRL_WARPS = 4;
-constexpr int CALC_WARPS = 8;                     // two warps a TMEM lane quadrant, 64 columns each
-constexpr int THREADS = 32 * (CTRL_WARPS + CALC_WARPS);
+constexpr int CTRL_WARPS = 2;
+constexpr int COLS = 32;                          // scores of a row that a warp has
+
+// The tile that stays has 128 rows; the walked ones 128 with dim up to 128
+// and 64 with dim up to 64, where 256 of the SM's 512 TMEM columns and under
+// half of its shared memory are enough, so that two CTAs share an SM and each
+// fills the other's waits.
+template <int DP>
+struct Shape {
+  static constexpr int WT = DP;                             // rows of a walked tile
+  static constexpr int PARTS = WT / COLS;                   // warps of a TMEM lane quadrant
+  static constexpr int CALC = 4 * PARTS;
+  static constexpr int THREADS = 32 * (CTRL_WARPS + CALC);
+  static constexpr int CTAS = DP == 64 ? 2 : 1;             // of an SM
+  static constexpr uint32_t TMEM = DP == 64 ? 256 : 512;    // columns
+};
 
 // ------------------------------------------------------------ statistics
-// lse log2(e) and delta of one tile of queries, 128 values each, padded: rows
-// past the sequence and rows that see no key get +inf, so that their p is 0.
+// -lse log2(e) and -delta of one tile of queries, 128 values each (the sign
+// that two-wide additions want), padded: rows past the sequence and rows that
+// see no key get -inf, so that their p is 0.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int tiles) {
   __shared__ Work sw;
@@ -48,28 +62,34 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int 
   if (!w.ok) return;
   const int l = threadIdx.x & 15, r = threadIdx.x >> 4;
   const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE;
+  uint4 a[8], b[8];
+  float lse[8];
 #pragma unroll
-  for (int k = 0; k < TILE; k += 16) {
-    const int i = w.tile * TILE + k + r;
-    float s = 0.f;
-    if (i < w.nq && 8 * l < p.dim) {
+  for (int k = 0; k < 8; ++k) {
+    const int i = w.tile * TILE + 16 * k + r;
+    a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+    lse[k] = -INFINITY;
+    if (i < w.nq) {
       const long long t = w.q0 + i;
-      float a[8], b[8];
-      unpack16<T>(ld_stream16(static_cast<const T*>(p.o) + w.b * p.ob + t * p.os + w.h * p.oh + 8 * l), a);
-      unpack16<T>(ld_stream16(static_cast<const T*>(p.dout) + w.b * p.dob + t * p.dos + w.h * p.doh + 8 * l), b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+      if (8 * l < p.dim) {
+        a[k] = ld_stream16(static_cast<const T*>(p.o) + w.b * p.ob + t * p.os + w.h * p.oh + 8 * l);
+        b[k] = ld_stream16(static_cast<const T*>(p.dout) + w.b * p.dob + t * p.dos + w.h * p.doh + 8 * l);
+      }
+      if (l == 0) lse[k] = p.lse[w.b * p.lse_b + w.h * p.lse_h + t];
     }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float x[8], y[8], s = 0.f;
+    unpack16<T>(a[k], x);
+    unpack16<T>(b[k], y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (l == 0) {
-      float e = INFINITY;
-      if (i < w.nq) {
-        const float lse = p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + i];
-        if (lse != -INFINITY) e = lse * LOG2E;
-      }
-      p.stat_lse[at + k + r] = e;
-      p.stat_delta[at + k + r] = i < w.nq ? s : 0.f;
+      p.stat_lse[at + 16 * k + r] = lse[k] == -INFINITY ? -INFINITY : -lse[k] * LOG2E;
+      p.stat_delta[at + 16 * k + r] = -s;
     }
   }
 }
@@ -79,16 +99,18 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int 
 // walked: three of the operand that two products a step read, two of the other.
 template <int DP>
 struct Smem {
-  static constexpr int T = tile_bytes<DP>();
+  static constexpr int WT = Shape<DP>::WT;
+  static constexpr int OWN = tile_bytes<DP>();    // a tile that stays
+  static constexpr int T = OWN / TILE * WT;       // a walked one
   static constexpr int RA = 3;
   static constexpr int RB = DP == 128 ? 2 : 3;
-  static constexpr int STAT = 2 * TILE * 4;       // lse and delta of one query tile
-  static constexpr int A_OFF = 2 * T;
+  static constexpr int STAT = 2 * WT * 4;         // lse and delta of one walked query tile
+  static constexpr int A_OFF = 2 * OWN;
   static constexpr int B_OFF = A_OFF + RA * T;
   static constexpr int STAT_OFF = B_OFF + RB * T;
   static constexpr int BAR_OFF = STAT_OFF + RB * STAT;
   static constexpr int BYTES = BAR_OFF + 256;
-  static_assert(BYTES <= 232448, "shared memory");
+  static_assert(BYTES * Shape<DP>::CTAS <= 232448 - 1024 * (Shape<DP>::CTAS - 1), "shared memory");
 };
 
 struct Bars {
@@ -105,11 +127,11 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-__device__ __forceinline__ void init_bars(Bars* s) {
+__device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&s->own[i], 1);
     mbar_init(&s->dp_full[i], 1);
-    mbar_init(&s->ds_full[i], CALC_WARPS);
+    mbar_init(&s->ds_full[i], calc_warps);
   }
   for (int i = 0; i < 3; ++i) {
     mbar_init(&s->a_full[i], 1);
@@ -118,43 +140,28 @@ __device__ __forceinline__ void init_bars(Bars* s) {
     mbar_init(&s->b_empty[i], 1);
   }
   mbar_init(&s->s_full, 1);
-  mbar_init(&s->s_free, CALC_WARPS);
-  mbar_init(&s->p_full, CALC_WARPS);
+  mbar_init(&s->s_free, calc_warps);
+  mbar_init(&s->p_full, calc_warps);
   mbar_init(&s->done, 1);
   mbar_init(&s->edge, 1);
   s->abort = 0;
   fence_mbar_init();
 }
 
-// 64 scores of a row to probabilities: v <- 2^(v c - e[col]), e the columns'
-// values in shared memory; columns outside [lo, hi) get 0.
-template <bool MASK>
-__device__ __forceinline__ void probs_by_col(float* v, float c, const float* e, int lo, int hi) {
-  const F2 cc = f2_make(c, c);
-#pragma unroll
-  for (int k = 0; k < 64; k += 4) {
-    const float4 l4 = *reinterpret_cast<const float4*>(e + k);
-    const float2 a = f2_split(f2_fma(f2_make(v[k], v[k + 1]), cc, f2_make(-l4.x, -l4.y)));
-    const float2 b = f2_split(f2_fma(f2_make(v[k + 2], v[k + 3]), cc, f2_make(-l4.z, -l4.w)));
-    v[k] = exp2_fast(a.x);
-    v[k + 1] = exp2_fast(a.y);
-    v[k + 2] = exp2_fast(b.x);
-    v[k + 3] = exp2_fast(b.y);
-    if (MASK) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (k + i < lo || k + i >= hi) v[k + i] = 0.f;
-    }
-  }
-}
-
 // ------------------------------------------------------------- dk and dv
+// A warp has 32 keys (TMEM rows) by 32 queries; thread t of it the keys t / 4
+// + 8 k, k = 0 .. 3, and the queries 8 j + 2 (t % 4) + {0, 1}, j = 0 .. 3.
+// Value (k, j, e) is v[16 (k / 2) + 4 j + 2 (k % 2) + e].  The queries'
+// statistics are columns here: with one row a thread every thread read all of
+// them, and shared memory's bandwidth, which the products need, bound the
+// step (2970 cycles with dim 128 against 2048 of products).
 template <typename T, int DP>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                     const AttnParams p, int tiles, int qtiles) {
   using S = Smem<DP>;
+  constexpr int WT = S::WT, BOX = DP == 64 ? 64 : TILE;      // rows of a walked tile, of a map's box
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -164,62 +171,62 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Work w = find_work(p, false, TILE, p.kv_heads, tiles, blockIdx.x);
     if (lane == 0) {
       bar->work = w;
-      init_bars(bar);
+      init_bars(bar, Shape<DP>::CALC);
     }
   }
-  if (warp == 1) tmem_alloc(&bar->tmem, 512);
+  if (warp == 1) tmem_alloc(&bar->tmem, Shape<DP>::TMEM);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const Work w = bar->work;
   volatile int* abort = &bar->abort;
   const uint32_t tmem = bar->tmem;
-  constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 256 + DP;
+  constexpr uint32_t S_COL = 0, DP_COL = WT, DV_COL = 2 * WT, DK_COL = 2 * WT + DP;
   const int group = p.heads / p.kv_heads;
   const int j0 = w.tile * TILE;
   Range r{0, 0};
-  if (w.ok) r = query_tiles(p, w, j0, min(j0 + TILE, w.nk) - 1);
+  if (w.ok) r = query_tiles<WT>(p, w, j0, min(j0 + TILE, w.nk) - 1);
   const int n = r.count * group;                   // steps: the group's heads one after another
 
   if (warp == 0 && n > 0) {
     // ---------------------------------------------------------- loads
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar->own[0], S::T);
-      load_tile<DP>(sb, &mk, &bar->own[0], w.h, w.k0 + j0, w.b);
-      mbar_arrive_expect_tx(&bar->own[1], S::T);
-      load_tile<DP>(sb + S::T, &mv, &bar->own[1], w.h, w.k0 + j0, w.b);
+      mbar_arrive_expect_tx(&bar->own[0], S::OWN);
+      load_tile<DP, TILE, BOX>(sb, &mk, &bar->own[0], w.h, w.k0 + j0, w.b);
+      mbar_arrive_expect_tx(&bar->own[1], S::OWN);
+      load_tile<DP, TILE, BOX>(sb + S::OWN, &mv, &bar->own[1], w.h, w.k0 + j0, w.b);
     }
     uint32_t edges = 0;
     int ia = 0, ib = 0;
     bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
       const int hq = w.h * group + i / r.count, tq = r.first + i % r.count;
-      const int row = w.q0 + tq * TILE, valid = w.nq - tq * TILE;
-      const bool edge = p.cu_q != nullptr && valid < TILE;
+      const int row = w.q0 + tq * WT, valid = w.nq - tq * WT;
+      const bool edge = p.cu_q != nullptr && valid < WT;
       const int sa = i % S::RA, sbuf = i % S::RB;
       if (i >= S::RA && !wait_warp(&bar->a_empty[sa], (i / S::RA - 1) & 1, abort, p)) break;
       if (edge) {
-        ok = load_edge_tile<DP>(smem + S::A_OFF + sa * S::T, &mq, &bar->edge, edges, hq, row, valid, abort, p);
+        ok = load_edge_tile<DP, WT, BOX>(smem + S::A_OFF + sa * S::T, &mq, &bar->edge, edges, hq, row, valid, abort, p);
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bar->a_full[sa]);
       } else if (lane == 0) {
         mbar_arrive_expect_tx(&bar->a_full[sa], S::T);
-        load_tile<DP>(sb + S::A_OFF + sa * S::T, &mq, &bar->a_full[sa], hq, row, w.b);
+        load_tile<DP, WT, BOX>(sb + S::A_OFF + sa * S::T, &mq, &bar->a_full[sa], hq, row, w.b);
       }
       ++ia;
       if (i >= S::RB && !wait_warp(&bar->b_empty[sbuf], (i / S::RB - 1) & 1, abort, p)) break;
       if (edge) {
-        ok = load_edge_tile<DP>(smem + S::B_OFF + sbuf * S::T, &mdo, &bar->edge, edges, hq, row, valid, abort, p);
+        ok = load_edge_tile<DP, WT, BOX>(smem + S::B_OFF + sbuf * S::T, &mdo, &bar->edge, edges, hq, row, valid, abort, p);
         if (!ok) break;
       }
       if (lane == 0) {
         const long long at =
-            ((static_cast<long long>(w.b) * p.heads + hq) * qtiles + w.qtile + tq) * TILE;
+            ((static_cast<long long>(w.b) * p.heads + hq) * qtiles + w.qtile) * TILE + tq * WT;
         const uint32_t st = sb + S::STAT_OFF + sbuf * S::STAT;
         mbar_arrive_expect_tx(&bar->b_full[sbuf], S::STAT + (edge ? 0 : S::T));
-        bulk_load(st, p.stat_lse + at, TILE * 4, &bar->b_full[sbuf]);
-        bulk_load(st + TILE * 4, p.stat_delta + at, TILE * 4, &bar->b_full[sbuf]);
-        if (!edge) load_tile<DP>(sb + S::B_OFF + sbuf * S::T, &mdo, &bar->b_full[sbuf], hq, row, w.b);
+        bulk_load(st, p.stat_lse + at, WT * 4, &bar->b_full[sbuf]);
+        bulk_load(st + WT * 4, p.stat_delta + at, WT * 4, &bar->b_full[sbuf]);
+        if (!edge) load_tile<DP, WT, BOX>(sb + S::B_OFF + sbuf * S::T, &mdo, &bar->b_full[sbuf], hq, row, w.b);
       }
       ++ib;
     }
@@ -232,92 +239,123 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1 && n > 0) {
     // -------------------------------------------------------- products
-    const uint64_t k_d = desc_dim(sb), v_d = desc_dim(sb + S::T);
+    const uint64_t k_d = desc_dim(sb), v_d = desc_dim(sb + S::OWN);
     auto scores = [&](int i) {
-      if (!wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
-      tc_fence_after();
-      mma_over_dim<T, DP>(tmem + S_COL, k_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
+      mma_over_dim<T, DP, WT>(tmem + S_COL, k_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
       commit_warp(&bar->s_full);
-      return true;
     };
     auto dprobs = [&](int i) {
-      if (!wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
-      tc_fence_after();
-      mma_over_dim<T, DP>(tmem + DP_COL, v_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
+      mma_over_dim<T, DP, WT>(tmem + DP_COL, v_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
       commit_warp(&bar->dp_full[0]);
-      return true;
     };
-    bool ok = wait_warp(&bar->own[0], 0, abort, p) && scores(0) && wait_warp(&bar->own[1], 0, abort, p) && dprobs(0);
+    // a step's tiles are waited for before the probabilities, so that
+    // products follow one another without a wait in between
+    auto wait_a = [&](int i) { return wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p); };
+    auto wait_b = [&](int i) { return wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p); };
+    bool ok = wait_warp(&bar->own[0], 0, abort, p) && wait_a(0);
+    if (ok) {
+      tc_fence_after();
+      scores(0);
+      ok = wait_warp(&bar->own[1], 0, abort, p) && wait_b(0);
+    }
+    if (ok) {
+      tc_fence_after();
+      dprobs(0);
+    }
     for (int i = 0; ok && i < n; ++i) {
-      ok = wait_warp(&bar->p_full, i & 1, abort, p);
+      const bool more = i + 1 < n;
+      ok = (!more || wait_a(i + 1)) && wait_warp(&bar->p_full, i & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
-      mma_over_tokens<T, DP>(tmem + DV_COL, tmem + S_COL, tmem + S_COL + 64,
-                             desc_tokens(sb + S::B_OFF + (i % S::RB) * S::T), i != 0 ? 1u : 0u);
+      mma_over_tokens<T, DP, COLS, WT>(tmem + DV_COL, tmem + S_COL, desc_tokens<WT>(sb + S::B_OFF + (i % S::RB) * S::T),
+                                   i != 0 ? 1u : 0u);
       commit_warp(&bar->b_empty[i % S::RB]);     // dP(i), issued earlier, has read this dO tile too
       // the next scores overwrite the probabilities: the tensor pipe runs in order
-      if (i + 1 < n) ok = scores(i + 1);
-      ok = ok && wait_warp(&bar->ds_full[0], i & 1, abort, p);
+      if (more) scores(i + 1);
+      ok = (!more || wait_b(i + 1)) && wait_warp(&bar->ds_full[0], i & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
-      mma_over_tokens<T, DP>(tmem + DK_COL, tmem + DP_COL, tmem + DP_COL + 64,
-                             desc_tokens(sb + S::A_OFF + (i % S::RA) * S::T), i != 0 ? 1u : 0u);
+      mma_over_tokens<T, DP, COLS, WT>(tmem + DK_COL, tmem + DP_COL, desc_tokens<WT>(sb + S::A_OFF + (i % S::RA) * S::T),
+                                   i != 0 ? 1u : 0u);
       commit_warp(&bar->a_empty[i % S::RA]);
-      if (i + 1 < n) ok = dprobs(i + 1);
+      if (more) dprobs(i + 1);
     }
     commit_warp(&bar->done);
     if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
     __syncwarp();
   } else if (warp >= CTRL_WARPS && w.ok) {
     // --------------------------------------- probabilities, then outputs
-    const int quad = warp & 3, half = (warp - CTRL_WARPS) >> 2, c0 = 64 * half;
+    const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2, c0 = COLS * part;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const int j = j0 + quad * 32 + lane;           // this thread's key
+    const int j = j0 + quad * 32 + (lane >> 2);    // the first of this thread's keys
+    const int c1 = c0 + 2 * (lane & 3);            // and queries of a tile
     const float c = p.scale * LOG2E;
+    const F2 cc = f2_make(c, c);
     const int off = w.nk - w.nq;
     bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
-      const int q0 = (r.first + i % r.count) * TILE;
-      const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + (i % S::RB) * S::STAT) + c0;
-      // queries q0 .. q0 + 127 against keys j0 .. j0 + 127: does everyone see everything?
-      const bool mask = p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window));
-      float v[64];
+      const int q0 = (r.first + i % r.count) * WT;
+      const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + (i % S::RB) * S::STAT) + c1;
+      // queries q0 .. q0 + WT - 1 against keys j0 .. j0 + 127: does everyone see everything?
+      const bool mask = p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + WT - 1 + off - j0 >= p.window));
+      float v[COLS], d[COLS];
+      uint32_t r16[COLS / 2];
       ok = wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p) && wait_warp(&bar->s_full, i & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
-      tmem_ld32(tmem + lanes + S_COL + c0, v);
-      tmem_ld32(tmem + lanes + S_COL + c0 + 32, v + 32);
+      tmem_ld_16x32(tmem + lanes + S_COL + c0, v);
+      tmem_ld_16x32(tmem + lanes + (16u << 16) + S_COL + c0, v + 16);
+      float2 e[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) e[q] = *reinterpret_cast<const float2*>(st + 8 * q);
       tmem_ld_wait();
-      if (mask) {
-        const int lo = j - off - q0 - c0;          // first query (column) that sees key j
-        probs_by_col<true>(v, c, st, lo, p.window > 0 ? lo + p.window : 64);
-      } else {
-        probs_by_col<false>(v, c, st, 0, 64);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float* u = v + 16 * (k >> 1) + 4 * q + 2 * (k & 1);
+          const float2 x = f2_split(f2_fma(f2_make(u[0], u[1]), cc, f2_make(e[q].x, e[q].y)));
+          u[0] = exp2_fast(x.x);
+          u[1] = exp2_fast(x.y);
+        }
       }
-      store_half<T>(tmem + lanes + S_COL + c0, v);
+      if (mask) {
+        // the queries (columns) that see key j + 8 k: [lo, hi)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int lo = j + 8 * k - off - q0 - c1, hi = p.window > 0 ? lo + p.window : WT;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float* u = v + 16 * (k >> 1) + 4 * q + 2 * (k & 1);
+            if (8 * q < lo || 8 * q >= hi) u[0] = 0.f;
+            if (8 * q + 1 < lo || 8 * q + 1 >= hi) u[1] = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < COLS / 2; ++k) r16[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+      tmem_st_16x16(tmem + lanes + S_COL + c0, r16);
+      tmem_st_16x16(tmem + lanes + (16u << 16) + S_COL + c0, r16 + 8);
+      tmem_st_wait();
       warp_arrive(&bar->p_full);
       ok = wait_warp(&bar->dp_full[0], i & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
+      tmem_ld_16x32(tmem + lanes + DP_COL + c0, d);
+      tmem_ld_16x32(tmem + lanes + (16u << 16) + DP_COL + c0, d + 16);
 #pragma unroll
-      for (int k0 = 0; k0 < 64; k0 += 32) {
-        float d[32];
-        tmem_ld32(tmem + lanes + DP_COL + c0 + k0, d);
-        tmem_ld_wait();
+      for (int q = 0; q < 4; ++q) e[q] = *reinterpret_cast<const float2*>(st + WT + 8 * q);
+      tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float4 dl = *reinterpret_cast<const float4*>(st + TILE + k0 + k);
-          const F2 a = f2_mul(f2_make(v[k0 + k], v[k0 + k + 1]), f2_add(f2_make(d[k], d[k + 1]), f2_make(-dl.x, -dl.y)));
-          const F2 b = f2_mul(f2_make(v[k0 + k + 2], v[k0 + k + 3]),
-                              f2_add(f2_make(d[k + 2], d[k + 3]), f2_make(-dl.z, -dl.w)));
-          const float2 x = f2_split(a), y = f2_split(b);
-          v[k0 + k] = x.x;
-          v[k0 + k + 1] = x.y;
-          v[k0 + k + 2] = y.x;
-          v[k0 + k + 3] = y.y;
-        }
+      for (int k = 0; k < COLS; k += 2) {
+        const int q = (k >> 2) & 3;
+        const float2 x =
+            f2_split(f2_mul(f2_make(v[k], v[k + 1]), f2_add(f2_make(d[k], d[k + 1]), f2_make(e[q].x, e[q].y))));
+        r16[k >> 1] = pack2<T>(x.x, x.y);
       }
-      store_half<T>(tmem + lanes + DP_COL + c0, v);
+      tmem_st_16x16(tmem + lanes + DP_COL + c0, r16);
+      tmem_st_16x16(tmem + lanes + (16u << 16) + DP_COL + c0, r16 + 8);
+      tmem_st_wait();
       warp_arrive(&bar->ds_full[0]);
     }
     if (ok && n > 0) {
@@ -325,16 +363,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
     }
     if (ok) {
-      // dv by the first four warps, dk by the others
-      const long long t = w.k0 + j;
-      T* row = half == 0 ? static_cast<T*>(p.dv) + w.b * p.dvb + t * p.dvs + w.h * p.dvh
-                         : static_cast<T*>(p.dk) + w.b * p.dkb + t * p.dks + w.h * p.dkh;
-      if (j >= w.nk) row = nullptr;
+      // dv by the first half of the warps, dk by the others, 64 columns a warp
+      const bool is_dv = part < Shape<DP>::PARTS / 2;
+      const int key = j0 + quad * 32 + lane;
+      const long long t = w.k0 + key;
+      T* row = is_dv ? static_cast<T*>(p.dv) + w.b * p.dvb + t * p.dvs + w.h * p.dvh
+                     : static_cast<T*>(p.dk) + w.b * p.dkb + t * p.dks + w.h * p.dkh;
+      if (key >= w.nk) row = nullptr;
+      const int d0 = part % (Shape<DP>::PARTS / 2) * 64;
       if (n > 0) {
-#pragma unroll
-        for (int k = 0; k < DP; k += 32)
-          store_cols32<T>(tmem + lanes + (half == 0 ? DV_COL : DK_COL) + k, row, k, p.dim, half == 0 ? 1.f : p.scale);
-      } else if (row != nullptr) {
+#pragma unroll 1
+        for (int k = d0; k < d0 + 64; k += 32)
+          store_cols32<T>(tmem + lanes + (is_dv ? DV_COL : DK_COL) + k, row, k, p.dim, is_dv ? 1.f : p.scale);
+      } else if (row != nullptr && d0 == 0) {
         for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
@@ -342,16 +383,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, Shape<DP>::TMEM);
 }
 
 // -------------------------------------------------------------------- dq
 template <typename T, int DP>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     attn_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                    const AttnParams p, int tiles) {
   using S = Smem<DP>;
+  constexpr int WT = S::WT, BOX = DP == 64 ? 64 : TILE;      // rows of a walked tile, of a map's box
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -361,10 +403,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Work w = find_work(p, true, TILE, p.heads, tiles, blockIdx.x);
     if (lane == 0) {
       bar->work = w;
-      init_bars(bar);
+      init_bars(bar, Shape<DP>::CALC);
     }
   }
-  if (warp == 1) tmem_alloc(&bar->tmem, 512);
+  if (warp == 1) tmem_alloc(&bar->tmem, Shape<DP>::TMEM);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -372,46 +414,46 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort = &bar->abort;
   const uint32_t tmem = bar->tmem;
   // dP is kept twice, so that the next tile's products need not wait for this tile's ds
-  constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 384;
+  constexpr uint32_t S_COL = 0, DP_COL = WT, DQ_COL = 3 * WT;
   const int hk = w.h / (p.heads / p.kv_heads);
   const int i0 = w.tile * TILE;
   Range r{0, 0};
-  if (w.ok) r = key_tiles(p, w, i0, min(i0 + TILE, w.nq) - 1);
+  if (w.ok) r = key_tiles<WT>(p, w, i0, min(i0 + TILE, w.nq) - 1);
   const int n = r.count;
 
   if (warp == 0 && n > 0) {
     // ---------------------------------------------------------- loads
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar->own[0], S::T);
-      load_tile<DP>(sb, &mq, &bar->own[0], w.h, w.q0 + i0, w.b);
-      mbar_arrive_expect_tx(&bar->own[1], S::T);
-      load_tile<DP>(sb + S::T, &mdo, &bar->own[1], w.h, w.q0 + i0, w.b);
+      mbar_arrive_expect_tx(&bar->own[0], S::OWN);
+      load_tile<DP, TILE, BOX>(sb, &mq, &bar->own[0], w.h, w.q0 + i0, w.b);
+      mbar_arrive_expect_tx(&bar->own[1], S::OWN);
+      load_tile<DP, TILE, BOX>(sb + S::OWN, &mdo, &bar->own[1], w.h, w.q0 + i0, w.b);
     }
     uint32_t edges = 0;
     int ia = 0, ib = 0;
     bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
-      const int j = (r.first + i) * TILE, row = w.k0 + j, valid = w.nk - j;
-      const bool edge = p.cu_q != nullptr && valid < TILE;
+      const int j = (r.first + i) * WT, row = w.k0 + j, valid = w.nk - j;
+      const bool edge = p.cu_q != nullptr && valid < WT;
       const int sa = i % S::RA, sbuf = i % S::RB;
       if (i >= S::RA && !wait_warp(&bar->a_empty[sa], (i / S::RA - 1) & 1, abort, p)) break;
       if (edge) {
-        ok = load_edge_tile<DP>(smem + S::A_OFF + sa * S::T, &mk, &bar->edge, edges, hk, row, valid, abort, p);
+        ok = load_edge_tile<DP, WT, BOX>(smem + S::A_OFF + sa * S::T, &mk, &bar->edge, edges, hk, row, valid, abort, p);
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bar->a_full[sa]);
       } else if (lane == 0) {
         mbar_arrive_expect_tx(&bar->a_full[sa], S::T);
-        load_tile<DP>(sb + S::A_OFF + sa * S::T, &mk, &bar->a_full[sa], hk, row, w.b);
+        load_tile<DP, WT, BOX>(sb + S::A_OFF + sa * S::T, &mk, &bar->a_full[sa], hk, row, w.b);
       }
       ++ia;
       if (i >= S::RB && !wait_warp(&bar->b_empty[sbuf], (i / S::RB - 1) & 1, abort, p)) break;
       if (edge) {
-        ok = load_edge_tile<DP>(smem + S::B_OFF + sbuf * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p);
+        ok = load_edge_tile<DP, WT, BOX>(smem + S::B_OFF + sbuf * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p);
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bar->b_full[sbuf]);
       } else if (lane == 0) {
         mbar_arrive_expect_tx(&bar->b_full[sbuf], S::T);
-        load_tile<DP>(sb + S::B_OFF + sbuf * S::T, &mv, &bar->b_full[sbuf], hk, row, w.b);
+        load_tile<DP, WT, BOX>(sb + S::B_OFF + sbuf * S::T, &mv, &bar->b_full[sbuf], hk, row, w.b);
       }
       ++ib;
     }
@@ -424,32 +466,42 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1 && n > 0) {
     // -------------------------------------------------------- products
-    const uint64_t q_d = desc_dim(sb), do_d = desc_dim(sb + S::T);
+    const uint64_t q_d = desc_dim(sb), do_d = desc_dim(sb + S::OWN);
     auto scores = [&](int i) {
-      if (!wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p)) return false;
-      tc_fence_after();
-      mma_over_dim<T, DP>(tmem + S_COL, q_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
+      mma_over_dim<T, DP, WT>(tmem + S_COL, q_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
       commit_warp(&bar->s_full);
-      return true;
     };
     auto dprobs = [&](int i) {
-      if (!wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p)) return false;
-      tc_fence_after();
-      mma_over_dim<T, DP>(tmem + DP_COL + (i & 1) * 128, do_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
+      mma_over_dim<T, DP, WT>(tmem + DP_COL + (i & 1) * WT, do_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
       commit_warp(&bar->dp_full[i & 1]);
       commit_warp(&bar->b_empty[i % S::RB]);
-      return true;
     };
-    bool ok = wait_warp(&bar->own[0], 0, abort, p) && scores(0) && wait_warp(&bar->own[1], 0, abort, p) && dprobs(0);
+    auto wait_a = [&](int i) { return wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p); };
+    auto wait_b = [&](int i) { return wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p); };
+    bool ok = wait_warp(&bar->own[0], 0, abort, p) && wait_a(0);
+    if (ok) {
+      tc_fence_after();
+      scores(0);
+      ok = wait_warp(&bar->own[1], 0, abort, p) && wait_b(0);
+    }
+    if (ok) {
+      tc_fence_after();
+      dprobs(0);
+    }
     for (int i = 0; ok && i < n; ++i) {
       // the next tile's scores and dP (over ds(i - 1), which dq(i - 1) has read: the tensor pipe runs in order)
-      if (i + 1 < n) ok = wait_warp(&bar->s_free, i & 1, abort, p) && scores(i + 1) && dprobs(i + 1);
-      ok = ok && wait_warp(&bar->ds_full[i & 1], (i >> 1) & 1, abort, p);
+      if (i + 1 < n) {
+        ok = wait_a(i + 1) && wait_b(i + 1) && wait_warp(&bar->s_free, i & 1, abort, p);
+        if (!ok) break;
+        tc_fence_after();
+        scores(i + 1);
+        dprobs(i + 1);
+      }
+      ok = wait_warp(&bar->ds_full[i & 1], (i >> 1) & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t ds = tmem + DP_COL + (i & 1) * 128;
-      mma_over_tokens<T, DP>(tmem + DQ_COL, ds, ds + 64, desc_tokens(sb + S::A_OFF + (i % S::RA) * S::T),
-                             i != 0 ? 1u : 0u);
+      mma_over_tokens<T, DP, COLS, WT>(tmem + DQ_COL, tmem + DP_COL + (i & 1) * WT,
+                                   desc_tokens<WT>(sb + S::A_OFF + (i % S::RA) * S::T), i != 0 ? 1u : 0u);
       commit_warp(&bar->a_empty[i % S::RA]);
     }
     commit_warp(&bar->done);
@@ -457,29 +509,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp >= CTRL_WARPS && w.ok) {
     // --------------------------------------- probabilities, then outputs
-    const int quad = warp & 3, half = (warp - CTRL_WARPS) >> 2, c0 = 64 * half;
+    const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2, c0 = COLS * part;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const int q = i0 + quad * 32 + lane;           // this thread's query
     const float c = p.scale * LOG2E;
     const int off = w.nk - w.nq;
     const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE + quad * 32 + lane;
     const float lse = n > 0 ? p.stat_lse[at] : 0.f, delta = n > 0 ? p.stat_delta[at] : 0.f;
-    const F2 cc = f2_make(c, c), ll = f2_make(-lse, -lse), dd = f2_make(-delta, -delta);
+    const F2 cc = f2_make(c, c), ll = f2_make(lse, lse), dd = f2_make(delta, delta);
     bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
-      const int j0 = (r.first + i) * TILE;
-      const bool mask = j0 + TILE > w.nk ||
-                        (p.causal && (j0 + TILE - 1 > i0 + off || (p.window > 0 && i0 + TILE - 1 + off - j0 >= p.window)));
-      float v[64];
+      const int j0 = (r.first + i) * WT;
+      const bool mask = j0 + WT > w.nk ||
+                        (p.causal && (j0 + WT - 1 > i0 + off || (p.window > 0 && i0 + TILE - 1 + off - j0 >= p.window)));
+      float v[COLS];
       ok = wait_warp(&bar->s_full, i & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
       tmem_ld32(tmem + lanes + S_COL + c0, v);
-      tmem_ld32(tmem + lanes + S_COL + c0 + 32, v + 32);
       tmem_ld_wait();
       warp_arrive(&bar->s_free);
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
+      for (int k = 0; k < COLS; k += 2) {
         const float2 a = f2_split(f2_fma(f2_make(v[k], v[k + 1]), cc, ll));
         v[k] = exp2_fast(a.x);
         v[k + 1] = exp2_fast(a.y);
@@ -492,26 +543,23 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (p.window > 0) lo = q + off - p.window + 1 - j0 - c0;
         }
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
+        for (int k = 0; k < COLS; ++k)
           if (k < lo || k >= hi) v[k] = 0.f;
       }
       ok = wait_warp(&bar->dp_full[i & 1], (i >> 1) & 1, abort, p);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t dp = tmem + lanes + DP_COL + (i & 1) * 128 + c0;
+      const uint32_t dp = tmem + lanes + DP_COL + (i & 1) * WT + c0;
+      float d[COLS];
+      tmem_ld32(dp, d);
+      tmem_ld_wait();
 #pragma unroll
-      for (int k0 = 0; k0 < 64; k0 += 32) {
-        float d[32];
-        tmem_ld32(dp + k0, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float2 x = f2_split(f2_mul(f2_make(v[k0 + k], v[k0 + k + 1]), f2_add(f2_make(d[k], d[k + 1]), dd)));
-          v[k0 + k] = x.x;
-          v[k0 + k + 1] = x.y;
-        }
+      for (int k = 0; k < COLS; k += 2) {
+        const float2 x = f2_split(f2_mul(f2_make(v[k], v[k + 1]), f2_add(f2_make(d[k], d[k + 1]), dd)));
+        v[k] = x.x;
+        v[k + 1] = x.y;
       }
-      store_half<T>(dp, v);
+      store_rounded<T, COLS / 2>(dp, v);
       warp_arrive(&bar->ds_full[i & 1]);
     }
     if (ok && n > 0) {
@@ -522,10 +570,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       T* row = q < w.nq ? static_cast<T*>(p.dq) + w.b * p.dqb + static_cast<long long>(w.q0 + q) * p.dqs + w.h * p.dqh
                         : nullptr;
       if (n > 0) {
-#pragma unroll
-        for (int k = 0; k < DP / 2; k += 32)
-          store_cols32<T>(tmem + lanes + DQ_COL + half * (DP / 2) + k, row, half * (DP / 2) + k, p.dim, p.scale);
-      } else if (row != nullptr && half == 0) {
+        store_cols32<T>(tmem + lanes + DQ_COL + c0, row, c0, p.dim, p.scale);
+      } else if (row != nullptr && part == 0) {
         for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
@@ -533,7 +579,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, Shape<DP>::TMEM);
 }
 
 long long seqs(const AttnParams& p) { return p.cu_q != nullptr ? 1 : p.batch; }
@@ -554,10 +600,10 @@ cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, int part, cud
                                   : allow_smem(reinterpret_cast<const void*>(dq), Smem<DP>::BYTES, done[1]);
   if (e != cudaSuccess) return e;
   if (part == 1)
-    dkv<<<static_cast<unsigned>(nk), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(kt),
+    dkv<<<static_cast<unsigned>(nk), Shape<DP>::THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(kt),
                                                                     static_cast<int>(qt));
   else
-    dq<<<static_cast<unsigned>(nq), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(qt));
+    dq<<<static_cast<unsigned>(nq), Shape<DP>::THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(qt));
   return cudaGetLastError();
 }
 

@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t pr = tmem + t * TILE;
-            mma_over_tokens<T, DP>(tmem + 256 + t * TILE, pr, pr + 32,
-                                   desc_tokens(sb + S::V_OFF + (i % S::RV) * S::T), steps[t] != 0 ? 1u : 0u);
+            mma_over_tokens<T, DP, TILE>(tmem + 256 + t * TILE, pr,
+                                           desc_tokens(sb + S::V_OFF + (i % S::RV) * S::T), steps[t] != 0 ? 1u : 0u);
             commit_warp(&bar->o_done[t]);
             ++steps[t];
           }
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             v[e + 1] = exp2_fast(a.y);
             sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
           }
-          store_half<T>(s_at + k / 2, v + k);
+          store_rounded<T, 32>(s_at + k / 2, v + k);
         }
         warp_arrive(&bar->p_full[t]);
       }

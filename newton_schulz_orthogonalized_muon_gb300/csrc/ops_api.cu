@@ -84,16 +84,16 @@ bool bad_operand(const void* p, const int64_t* st, const int64_t* size) {
   return bad;
 }
 
-// Map of an operand [batch][token][head][dim] with boxes of one head, 128
+// Map of an operand [batch][token][head][dim] with boxes of one head, `tokens`
 // tokens and 64 columns (a whole 128-byte swizzle row).
 bool attn_map(muon_handle_t h, CUtensorMap* map, const void* base, const int64_t* st, const int64_t* size, int dim,
-              int dtype) {
+              int dtype, uint32_t tokens) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(size[2]),
                         static_cast<cuuint64_t>(size[1]), static_cast<cuuint64_t>(size[0])};
   cuuint64_t strides[3];
   for (int i = 0; i < 3; ++i)
     strides[i] = size[2 - i] > 1 ? static_cast<cuuint64_t>(st[2 - i]) * 2 : static_cast<cuuint64_t>(dim) * 2;
-  cuuint32_t box[4] = {64, 1, 128, 1};
+  cuuint32_t box[4] = {64, 1, tokens, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return h->encode(map, dtype == MUON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                    const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -287,10 +287,10 @@ muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a,
     AttnParams p = attn_params(h, *a);
     p.out = a->o;
     CUtensorMap m[3] = {};
-    bool ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype);
+    bool ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype, 128);
     if (a->sk > 0)
-      ok = ok && attn_map(h, &m[1], a->k, a->k_stride, kn, a->dim, a->dtype) &&
-           attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype);
+      ok = ok && attn_map(h, &m[1], a->k, a->k_stride, kn, a->dim, a->dtype, 128) &&
+           attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype, 128);
     if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
     MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_fwd(p, m, stream), "attention launch");
@@ -341,13 +341,14 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
     p.stat_lse = static_cast<float*>(workspace);
     p.stat_delta = p.stat_lse + attn_workspace(*a) / 8;
     CUtensorMap m[4] = {};
+    const uint32_t tokens = a->dim <= 64 ? 64 : 128;
     bool ok = true;
     if (a->sq > 0)
-      ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype) &&
-           attn_map(h, &m[3], a->dout, a->dout_stride, qn, a->dim, a->dtype);
+      ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype, tokens) &&
+           attn_map(h, &m[3], a->dout, a->dout_stride, qn, a->dim, a->dtype, tokens);
     if (a->sk > 0)
-      ok = ok && attn_map(h, &m[1], a->k, a->k_stride, kn, a->dim, a->dtype) &&
-           attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype);
+      ok = ok && attn_map(h, &m[1], a->k, a->k_stride, kn, a->dim, a->dtype, tokens) &&
+           attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype, tokens);
     if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
     if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 0, stream), "attention statistics launch");
