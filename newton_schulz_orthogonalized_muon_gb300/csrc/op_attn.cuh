@@ -164,8 +164,7 @@ __device__ __forceinline__ Range query_tiles(const AttnParams& p, const Work& w,
 // ------------------------------------------------------------------- waits
 // Every lane polls; the warp leaves together.  Gives up (and says so in the
 // error word) after the time limit, or when another warp gave up.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const AttnParams& p) {
-  const uint32_t a = smem_u32(bar);
+__device__ __forceinline__ bool wait_warp(uint32_t a, uint32_t parity, volatile int* abort, const AttnParams& p) {
   if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -191,19 +190,19 @@ __device__ __forceinline__ bool swizzle_aligned(uint32_t base, const AttnParams&
 }
 
 // -------------------------------------------------------------------- TMA
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             int u) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
       "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
       : "memory");
 }
 // Loads a tile of ROWS rows that starts at token `row`, by one lane, signalled
 // on `bar` (which the caller has armed with the tile's bytes); the map's boxes
 // have BOX rows.
 template <int DP, int ROWS = TILE, int BOX = TILE>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int h, int row, int b) {
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int h, int row, int b) {
 #pragma unroll
   for (int x = 0; x < DP / 64; ++x)
 #pragma unroll
@@ -216,12 +215,12 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 // zero probability.  `edge` is the warp's own barrier; on return the tile is
 // complete for the async proxy.
 template <int DP, int ROWS = TILE, int BOX = TILE>
-__device__ __forceinline__ bool load_edge_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* edge, uint32_t& phase,
+__device__ __forceinline__ bool load_edge_tile(uint32_t dst, const CUtensorMap* map, uint32_t edge, uint32_t& phase,
                                                int h, int row, int valid, volatile int* abort, const AttnParams& p) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) {
-    mbar_arrive_expect_tx(edge, DP / 64 * ROWS * 128);
-    load_tile<DP, ROWS, BOX>(smem_u32(dst), map, edge, h, row, 0);
+    mbar_expect_at(edge, DP / 64 * ROWS * 128);
+    load_tile<DP, ROWS, BOX>(dst, map, edge, h, row, 0);
   }
   __syncwarp();
   if (!wait_warp(edge, phase & 1u, abort, p)) return false;
@@ -229,7 +228,7 @@ __device__ __forceinline__ bool load_edge_tile(uint8_t* dst, const CUtensorMap* 
 #pragma unroll
   for (int x = 0; x < DP / 64; ++x)
     for (int i = valid * 8 + lane; i < ROWS * 8; i += 32)
-      *reinterpret_cast<uint4*>(dst + x * ROWS * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * ROWS * 128 + i * 16), "r"(0u) : "memory");
   fence_proxy_async_smem();
   __syncwarp();
   return true;
@@ -299,13 +298,13 @@ __device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint64_t b, uin
       : "memory");
 }
 // arrives on `bar` when every product issued so far by this warp is done
-__device__ __forceinline__ void commit_warp(uint64_t* bar) {
+__device__ __forceinline__ void commit_warp(uint32_t bar) {
   asm volatile(
       "{\n"
       " .reg .pred q;\n"
       " elect.sync _|q, 0xffffffff;\n"
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
-      "}\n" ::"r"(smem_u32(bar))
+      "}\n" ::"r"(bar)
       : "memory");
 }
 // Descriptors of a tile of ROWS rows: K-major (over dim) and MN-major (over
@@ -410,10 +409,10 @@ __device__ __forceinline__ void store_cols32(uint32_t taddr, T* dst, int c0, int
 }
 
 // one arrival of a warp whose lanes' TMEM accesses are complete
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
   tc_fence_before();
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  if ((threadIdx.x & 31) == 0) mbar_arrive_at(bar);
 }
 
 // After a wait ran out: no copy may still be in flight when the CTA's shared

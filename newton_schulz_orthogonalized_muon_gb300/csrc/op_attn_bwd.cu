@@ -20,6 +20,8 @@
 // bit values over the fp32 scores (or dP) that it read, and the next product
 // takes them from TMEM as its A operand.  Scores are transposed in the dkv
 // kernel (rows are keys), so that p and ds are that operand as they stand.
+#include <cstddef>
+
 #include "common.cuh"
 #include "internal.h"
 #include "op_attn.cuh"
@@ -126,6 +128,8 @@ struct Bars {
   Work work;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
+// shared-memory address of a barrier; `bb` is the block's
+#define BAR(f) (bb + static_cast<uint32_t>(offsetof(Bars, f)))
 
 __device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
   for (int i = 0; i < 2; ++i) {
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t sb = smem_u32(smem);
+  const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
   if (!swizzle_aligned(sb, p)) return;
   if (warp == 0) {
     const Work w = find_work(p, false, TILE, p.kv_heads, tiles, blockIdx.x);
@@ -191,44 +195,51 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   if (warp == 0 && n > 0) {
     // ---------------------------------------------------------- loads
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar->own[0], S::OWN);
-      load_tile<DP, TILE, BOX>(sb, &mk, &bar->own[0], w.h, w.k0 + j0, w.b);
-      mbar_arrive_expect_tx(&bar->own[1], S::OWN);
-      load_tile<DP, TILE, BOX>(sb + S::OWN, &mv, &bar->own[1], w.h, w.k0 + j0, w.b);
+      mbar_expect_at(BAR(own), S::OWN);
+      load_tile<DP, TILE, BOX>(sb, &mk, BAR(own), w.h, w.k0 + j0, w.b);
+      mbar_expect_at(BAR(own) + 8, S::OWN);
+      load_tile<DP, TILE, BOX>(sb + S::OWN, &mv, BAR(own) + 8, w.h, w.k0 + j0, w.b);
     }
     uint32_t edges = 0;
     int ia = 0, ib = 0;
+    Ring<S::RA> ra;
+    Ring<S::RB> rb;
     bool ok = true;
-    for (int i = 0; ok && i < n; ++i) {
-      const int hq = w.h * group + i / r.count, tq = r.first + i % r.count;
-      const int row = w.q0 + tq * WT, valid = w.nq - tq * WT;
-      const bool edge = p.cu_q != nullptr && valid < WT;
-      const int sa = i % S::RA, sbuf = i % S::RB;
-      if (i >= S::RA && !wait_warp(&bar->a_empty[sa], (i / S::RA - 1) & 1, abort, p)) break;
-      if (edge) {
-        ok = load_edge_tile<DP, WT, BOX>(smem + S::A_OFF + sa * S::T, &mq, &bar->edge, edges, hq, row, valid, abort, p);
+    for (int hq = w.h * group; ok && hq < (w.h + 1) * group; ++hq) {
+      const long long stat = ((static_cast<long long>(w.b) * p.heads + hq) * qtiles + w.qtile) * TILE;
+      for (int i0 = r.first * WT; i0 < (r.first + r.count) * WT; i0 += WT) {
+        const int row = w.q0 + i0, valid = w.nq - i0;
+        const bool edge = p.cu_q != nullptr && valid < WT;
+        const uint32_t at = sb + S::A_OFF + ra.s * S::T, bt = sb + S::B_OFF + rb.s * S::T;
+        const uint32_t fa = BAR(a_full) + 8 * ra.s, fb = BAR(b_full) + 8 * rb.s;
+        ok = wait_warp(BAR(a_empty) + 8 * ra.s, ra.ph ^ 1u, abort, p);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&bar->a_full[sa]);
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(&bar->a_full[sa], S::T);
-        load_tile<DP, WT, BOX>(sb + S::A_OFF + sa * S::T, &mq, &bar->a_full[sa], hq, row, w.b);
-      }
-      ++ia;
-      if (i >= S::RB && !wait_warp(&bar->b_empty[sbuf], (i / S::RB - 1) & 1, abort, p)) break;
-      if (edge) {
-        ok = load_edge_tile<DP, WT, BOX>(smem + S::B_OFF + sbuf * S::T, &mdo, &bar->edge, edges, hq, row, valid, abort, p);
+        if (edge) {
+          ok = load_edge_tile<DP, WT, BOX>(at, &mq, BAR(edge), edges, hq, row, valid, abort, p);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_at(fa);
+        } else if (lane == 0) {
+          mbar_expect_at(fa, S::T);
+          load_tile<DP, WT, BOX>(at, &mq, fa, hq, row, w.b);
+        }
+        ++ia;
+        ra.next();
+        ok = wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p);
         if (!ok) break;
+        if (edge) {
+          ok = load_edge_tile<DP, WT, BOX>(bt, &mdo, BAR(edge), edges, hq, row, valid, abort, p);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          const uint32_t st = sb + S::STAT_OFF + rb.s * S::STAT;
+          mbar_expect_at(fb, S::STAT + (edge ? 0 : S::T));
+          bulk_load(st, p.stat_lse + stat + i0, WT * 4, fb);
+          bulk_load(st + WT * 4, p.stat_delta + stat + i0, WT * 4, fb);
+          if (!edge) load_tile<DP, WT, BOX>(bt, &mdo, fb, hq, row, w.b);
+        }
+        ++ib;
+        rb.next();
       }
-      if (lane == 0) {
-        const long long at =
-            ((static_cast<long long>(w.b) * p.heads + hq) * qtiles + w.qtile) * TILE + tq * WT;
-        const uint32_t st = sb + S::STAT_OFF + sbuf * S::STAT;
-        mbar_arrive_expect_tx(&bar->b_full[sbuf], S::STAT + (edge ? 0 : S::T));
-        bulk_load(st, p.stat_lse + at, WT * 4, &bar->b_full[sbuf]);
-        bulk_load(st + WT * 4, p.stat_delta + at, WT * 4, &bar->b_full[sbuf]);
-        if (!edge) load_tile<DP, WT, BOX>(sb + S::B_OFF + sbuf * S::T, &mdo, &bar->b_full[sbuf], hq, row, w.b);
-      }
-      ++ib;
     }
     if (*abort != 0 && lane == 0) {
       mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
@@ -240,47 +251,51 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   } else if (warp == 1 && n > 0) {
     // -------------------------------------------------------- products
     const uint64_t k_d = desc_dim(sb), v_d = desc_dim(sb + S::OWN);
-    auto scores = [&](int i) {
-      mma_over_dim<T, DP, WT>(tmem + S_COL, k_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
-      commit_warp(&bar->s_full);
+    Ring<S::RA> ra, na;                            // this step's Q tile, and the next one's
+    Ring<S::RB> rb, nb;
+    auto scores = [&]() {
+      mma_over_dim<T, DP, WT>(tmem + S_COL, k_d, desc_dim(sb + S::A_OFF + na.s * S::T));
+      commit_warp(BAR(s_full));
+      na.next();
     };
-    auto dprobs = [&](int i) {
-      mma_over_dim<T, DP, WT>(tmem + DP_COL, v_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
-      commit_warp(&bar->dp_full[0]);
+    auto dprobs = [&]() {
+      mma_over_dim<T, DP, WT>(tmem + DP_COL, v_d, desc_dim(sb + S::B_OFF + nb.s * S::T));
+      commit_warp(BAR(dp_full));
+      nb.next();
     };
     // a step's tiles are waited for before the probabilities, so that
     // products follow one another without a wait in between
-    auto wait_a = [&](int i) { return wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p); };
-    auto wait_b = [&](int i) { return wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p); };
-    bool ok = wait_warp(&bar->own[0], 0, abort, p) && wait_a(0);
+    auto wait_a = [&]() { return wait_warp(BAR(a_full) + 8 * na.s, na.ph, abort, p); };
+    auto wait_b = [&]() { return wait_warp(BAR(b_full) + 8 * nb.s, nb.ph, abort, p); };
+    bool ok = wait_warp(BAR(own), 0, abort, p) && wait_a();
     if (ok) {
       tc_fence_after();
-      scores(0);
-      ok = wait_warp(&bar->own[1], 0, abort, p) && wait_b(0);
+      scores();
+      ok = wait_warp(BAR(own) + 8, 0, abort, p) && wait_b();
     }
     if (ok) {
       tc_fence_after();
-      dprobs(0);
+      dprobs();
     }
-    for (int i = 0; ok && i < n; ++i) {
-      const bool more = i + 1 < n;
-      ok = (!more || wait_a(i + 1)) && wait_warp(&bar->p_full, i & 1, abort, p);
+    uint32_t ph = 0, acc = 0;
+    for (int left = n - 1; ok && left >= 0; --left, ph ^= 1u, acc = 1) {
+      ok = (left == 0 || wait_a()) && wait_warp(BAR(p_full), ph, abort, p);
       if (!ok) break;
       tc_fence_after();
-      mma_over_tokens<T, DP, COLS, WT>(tmem + DV_COL, tmem + S_COL, desc_tokens<WT>(sb + S::B_OFF + (i % S::RB) * S::T),
-                                   i != 0 ? 1u : 0u);
-      commit_warp(&bar->b_empty[i % S::RB]);     // dP(i), issued earlier, has read this dO tile too
+      mma_over_tokens<T, DP, COLS, WT>(tmem + DV_COL, tmem + S_COL, desc_tokens<WT>(sb + S::B_OFF + rb.s * S::T), acc);
+      commit_warp(BAR(b_empty) + 8 * rb.s);        // dP, issued earlier, has read this dO tile too
+      rb.next();
       // the next scores overwrite the probabilities: the tensor pipe runs in order
-      if (more) scores(i + 1);
-      ok = (!more || wait_b(i + 1)) && wait_warp(&bar->ds_full[0], i & 1, abort, p);
+      if (left > 0) scores();
+      ok = (left == 0 || wait_b()) && wait_warp(BAR(ds_full), ph, abort, p);
       if (!ok) break;
       tc_fence_after();
-      mma_over_tokens<T, DP, COLS, WT>(tmem + DK_COL, tmem + DP_COL, desc_tokens<WT>(sb + S::A_OFF + (i % S::RA) * S::T),
-                                   i != 0 ? 1u : 0u);
-      commit_warp(&bar->a_empty[i % S::RA]);
-      if (more) dprobs(i + 1);
+      mma_over_tokens<T, DP, COLS, WT>(tmem + DK_COL, tmem + DP_COL, desc_tokens<WT>(sb + S::A_OFF + ra.s * S::T), acc);
+      commit_warp(BAR(a_empty) + 8 * ra.s);
+      ra.next();
+      if (left > 0) dprobs();
     }
-    commit_warp(&bar->done);
+    commit_warp(BAR(done));
     if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
     __syncwarp();
   } else if (warp >= CTRL_WARPS && w.ok) {
@@ -292,19 +307,24 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     const float c = p.scale * LOG2E;
     const F2 cc = f2_make(c, c);
     const int off = w.nk - w.nq;
+    const uint32_t s_at = tmem + lanes + S_COL + c0, dp_at = tmem + lanes + DP_COL + c0;
+    constexpr uint32_t ROWS16 = 16u << 16;         // the warp's second 16 TMEM rows
+    Ring<S::RB> rb;
+    uint32_t ph = 0;
     bool ok = true;
-    for (int i = 0; ok && i < n; ++i) {
-      const int q0 = (r.first + i % r.count) * WT;
-      const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + (i % S::RB) * S::STAT) + c1;
+    int q0 = r.first * WT;
+    const int q_end = (r.first + r.count) * WT;
+    for (int i = 0; i < n; ++i) {
+      const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + rb.s * S::STAT) + c1;
       // queries q0 .. q0 + WT - 1 against keys j0 .. j0 + 127: does everyone see everything?
       const bool mask = p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + WT - 1 + off - j0 >= p.window));
       float v[COLS], d[COLS];
       uint32_t r16[COLS / 2];
-      ok = wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p) && wait_warp(&bar->s_full, i & 1, abort, p);
+      ok = wait_warp(BAR(b_full) + 8 * rb.s, rb.ph, abort, p) && wait_warp(BAR(s_full), ph, abort, p);
       if (!ok) break;
       tc_fence_after();
-      tmem_ld_16x32(tmem + lanes + S_COL + c0, v);
-      tmem_ld_16x32(tmem + lanes + (16u << 16) + S_COL + c0, v + 16);
+      tmem_ld_16x32(s_at, v);
+      tmem_ld_16x32(s_at + ROWS16, v + 16);
       float2 e[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) e[q] = *reinterpret_cast<const float2*>(st + 8 * q);
@@ -334,15 +354,15 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
       }
 #pragma unroll
       for (int k = 0; k < COLS / 2; ++k) r16[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
-      tmem_st_16x16(tmem + lanes + S_COL + c0, r16);
-      tmem_st_16x16(tmem + lanes + (16u << 16) + S_COL + c0, r16 + 8);
+      tmem_st_16x16(s_at, r16);
+      tmem_st_16x16(s_at + ROWS16, r16 + 8);
       tmem_st_wait();
-      warp_arrive(&bar->p_full);
-      ok = wait_warp(&bar->dp_full[0], i & 1, abort, p);
+      warp_arrive(BAR(p_full));
+      ok = wait_warp(BAR(dp_full), ph, abort, p);
       if (!ok) break;
       tc_fence_after();
-      tmem_ld_16x32(tmem + lanes + DP_COL + c0, d);
-      tmem_ld_16x32(tmem + lanes + (16u << 16) + DP_COL + c0, d + 16);
+      tmem_ld_16x32(dp_at, d);
+      tmem_ld_16x32(dp_at + ROWS16, d + 16);
 #pragma unroll
       for (int q = 0; q < 4; ++q) e[q] = *reinterpret_cast<const float2*>(st + WT + 8 * q);
       tmem_ld_wait();
@@ -353,13 +373,17 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
             f2_split(f2_mul(f2_make(v[k], v[k + 1]), f2_add(f2_make(d[k], d[k + 1]), f2_make(e[q].x, e[q].y))));
         r16[k >> 1] = pack2<T>(x.x, x.y);
       }
-      tmem_st_16x16(tmem + lanes + DP_COL + c0, r16);
-      tmem_st_16x16(tmem + lanes + (16u << 16) + DP_COL + c0, r16 + 8);
+      tmem_st_16x16(dp_at, r16);
+      tmem_st_16x16(dp_at + ROWS16, r16 + 8);
       tmem_st_wait();
-      warp_arrive(&bar->ds_full[0]);
+      warp_arrive(BAR(ds_full));
+      rb.next();
+      ph ^= 1u;
+      q0 += WT;
+      if (q0 == q_end) q0 = r.first * WT;          // the group's next head
     }
     if (ok && n > 0) {
-      ok = wait_warp(&bar->done, 0, abort, p);
+      ok = wait_warp(BAR(done), 0, abort, p);
       tc_fence_after();
     }
     if (ok) {
@@ -397,7 +421,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t sb = smem_u32(smem);
+  const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
   if (!swizzle_aligned(sb, p)) return;
   if (warp == 0) {
     const Work w = find_work(p, true, TILE, p.heads, tiles, blockIdx.x);
@@ -424,38 +448,40 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   if (warp == 0 && n > 0) {
     // ---------------------------------------------------------- loads
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar->own[0], S::OWN);
-      load_tile<DP, TILE, BOX>(sb, &mq, &bar->own[0], w.h, w.q0 + i0, w.b);
-      mbar_arrive_expect_tx(&bar->own[1], S::OWN);
-      load_tile<DP, TILE, BOX>(sb + S::OWN, &mdo, &bar->own[1], w.h, w.q0 + i0, w.b);
+      mbar_expect_at(BAR(own), S::OWN);
+      load_tile<DP, TILE, BOX>(sb, &mq, BAR(own), w.h, w.q0 + i0, w.b);
+      mbar_expect_at(BAR(own) + 8, S::OWN);
+      load_tile<DP, TILE, BOX>(sb + S::OWN, &mdo, BAR(own) + 8, w.h, w.q0 + i0, w.b);
     }
     uint32_t edges = 0;
     int ia = 0, ib = 0;
-    bool ok = true;
-    for (int i = 0; ok && i < n; ++i) {
-      const int j = (r.first + i) * WT, row = w.k0 + j, valid = w.nk - j;
+    Ring<S::RA> ra;
+    Ring<S::RB> rb;
+    for (int j = r.first * WT; j < (r.first + r.count) * WT; j += WT) {
+      const int row = w.k0 + j, valid = w.nk - j;
       const bool edge = p.cu_q != nullptr && valid < WT;
-      const int sa = i % S::RA, sbuf = i % S::RB;
-      if (i >= S::RA && !wait_warp(&bar->a_empty[sa], (i / S::RA - 1) & 1, abort, p)) break;
+      const uint32_t at = sb + S::A_OFF + ra.s * S::T, bt = sb + S::B_OFF + rb.s * S::T;
+      const uint32_t fa = BAR(a_full) + 8 * ra.s, fb = BAR(b_full) + 8 * rb.s;
+      if (!wait_warp(BAR(a_empty) + 8 * ra.s, ra.ph ^ 1u, abort, p)) break;
       if (edge) {
-        ok = load_edge_tile<DP, WT, BOX>(smem + S::A_OFF + sa * S::T, &mk, &bar->edge, edges, hk, row, valid, abort, p);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&bar->a_full[sa]);
+        if (!load_edge_tile<DP, WT, BOX>(at, &mk, BAR(edge), edges, hk, row, valid, abort, p)) break;
+        if (lane == 0) mbar_arrive_at(fa);
       } else if (lane == 0) {
-        mbar_arrive_expect_tx(&bar->a_full[sa], S::T);
-        load_tile<DP, WT, BOX>(sb + S::A_OFF + sa * S::T, &mk, &bar->a_full[sa], hk, row, w.b);
+        mbar_expect_at(fa, S::T);
+        load_tile<DP, WT, BOX>(at, &mk, fa, hk, row, w.b);
       }
       ++ia;
-      if (i >= S::RB && !wait_warp(&bar->b_empty[sbuf], (i / S::RB - 1) & 1, abort, p)) break;
+      ra.next();
+      if (!wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p)) break;
       if (edge) {
-        ok = load_edge_tile<DP, WT, BOX>(smem + S::B_OFF + sbuf * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&bar->b_full[sbuf]);
+        if (!load_edge_tile<DP, WT, BOX>(bt, &mv, BAR(edge), edges, hk, row, valid, abort, p)) break;
+        if (lane == 0) mbar_arrive_at(fb);
       } else if (lane == 0) {
-        mbar_arrive_expect_tx(&bar->b_full[sbuf], S::T);
-        load_tile<DP, WT, BOX>(sb + S::B_OFF + sbuf * S::T, &mv, &bar->b_full[sbuf], hk, row, w.b);
+        mbar_expect_at(fb, S::T);
+        load_tile<DP, WT, BOX>(bt, &mv, fb, hk, row, w.b);
       }
       ++ib;
+      rb.next();
     }
     if (*abort != 0 && lane == 0) {
       mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
@@ -467,44 +493,53 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   } else if (warp == 1 && n > 0) {
     // -------------------------------------------------------- products
     const uint64_t q_d = desc_dim(sb), do_d = desc_dim(sb + S::OWN);
-    auto scores = [&](int i) {
-      mma_over_dim<T, DP, WT>(tmem + S_COL, q_d, desc_dim(sb + S::A_OFF + (i % S::RA) * S::T));
-      commit_warp(&bar->s_full);
+    Ring<S::RA> ra, na;                            // this step's K tile, and the next one's
+    Ring<S::RB> nb;
+    Ring<2> buf, next;                             // the two places of dP
+    auto scores = [&]() {
+      mma_over_dim<T, DP, WT>(tmem + S_COL, q_d, desc_dim(sb + S::A_OFF + na.s * S::T));
+      commit_warp(BAR(s_full));
+      na.next();
     };
-    auto dprobs = [&](int i) {
-      mma_over_dim<T, DP, WT>(tmem + DP_COL + (i & 1) * WT, do_d, desc_dim(sb + S::B_OFF + (i % S::RB) * S::T));
-      commit_warp(&bar->dp_full[i & 1]);
-      commit_warp(&bar->b_empty[i % S::RB]);
+    auto dprobs = [&]() {
+      mma_over_dim<T, DP, WT>(tmem + DP_COL + next.s * WT, do_d, desc_dim(sb + S::B_OFF + nb.s * S::T));
+      commit_warp(BAR(dp_full) + 8 * next.s);
+      commit_warp(BAR(b_empty) + 8 * nb.s);
+      nb.next();
+      next.next();
     };
-    auto wait_a = [&](int i) { return wait_warp(&bar->a_full[i % S::RA], (i / S::RA) & 1, abort, p); };
-    auto wait_b = [&](int i) { return wait_warp(&bar->b_full[i % S::RB], (i / S::RB) & 1, abort, p); };
-    bool ok = wait_warp(&bar->own[0], 0, abort, p) && wait_a(0);
+    auto wait_a = [&]() { return wait_warp(BAR(a_full) + 8 * na.s, na.ph, abort, p); };
+    auto wait_b = [&]() { return wait_warp(BAR(b_full) + 8 * nb.s, nb.ph, abort, p); };
+    bool ok = wait_warp(BAR(own), 0, abort, p) && wait_a();
     if (ok) {
       tc_fence_after();
-      scores(0);
-      ok = wait_warp(&bar->own[1], 0, abort, p) && wait_b(0);
+      scores();
+      ok = wait_warp(BAR(own) + 8, 0, abort, p) && wait_b();
     }
     if (ok) {
       tc_fence_after();
-      dprobs(0);
+      dprobs();
     }
-    for (int i = 0; ok && i < n; ++i) {
-      // the next tile's scores and dP (over ds(i - 1), which dq(i - 1) has read: the tensor pipe runs in order)
-      if (i + 1 < n) {
-        ok = wait_a(i + 1) && wait_b(i + 1) && wait_warp(&bar->s_free, i & 1, abort, p);
+    uint32_t ph = 0, acc = 0;
+    for (int left = n - 1; ok && left >= 0; --left, ph ^= 1u, acc = 1) {
+      // the next tile's scores and dP (over the ds before last, which dq has read: the tensor pipe runs in order)
+      if (left > 0) {
+        ok = wait_a() && wait_b() && wait_warp(BAR(s_free), ph, abort, p);
         if (!ok) break;
         tc_fence_after();
-        scores(i + 1);
-        dprobs(i + 1);
+        scores();
+        dprobs();
       }
-      ok = wait_warp(&bar->ds_full[i & 1], (i >> 1) & 1, abort, p);
+      ok = wait_warp(BAR(ds_full) + 8 * buf.s, buf.ph, abort, p);
       if (!ok) break;
       tc_fence_after();
-      mma_over_tokens<T, DP, COLS, WT>(tmem + DQ_COL, tmem + DP_COL + (i & 1) * WT,
-                                   desc_tokens<WT>(sb + S::A_OFF + (i % S::RA) * S::T), i != 0 ? 1u : 0u);
-      commit_warp(&bar->a_empty[i % S::RA]);
+      mma_over_tokens<T, DP, COLS, WT>(tmem + DQ_COL, tmem + DP_COL + buf.s * WT,
+                                       desc_tokens<WT>(sb + S::A_OFF + ra.s * S::T), acc);
+      commit_warp(BAR(a_empty) + 8 * ra.s);
+      ra.next();
+      buf.next();
     }
-    commit_warp(&bar->done);
+    commit_warp(BAR(done));
     if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
     __syncwarp();
   } else if (warp >= CTRL_WARPS && w.ok) {
@@ -517,18 +552,19 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE + quad * 32 + lane;
     const float lse = n > 0 ? p.stat_lse[at] : 0.f, delta = n > 0 ? p.stat_delta[at] : 0.f;
     const F2 cc = f2_make(c, c), ll = f2_make(lse, lse), dd = f2_make(delta, delta);
+    Ring<2> buf;
+    uint32_t ph = 0;
     bool ok = true;
-    for (int i = 0; ok && i < n; ++i) {
-      const int j0 = (r.first + i) * WT;
+    for (int j0 = r.first * WT; j0 < (r.first + r.count) * WT; j0 += WT) {
       const bool mask = j0 + WT > w.nk ||
                         (p.causal && (j0 + WT - 1 > i0 + off || (p.window > 0 && i0 + TILE - 1 + off - j0 >= p.window)));
       float v[COLS];
-      ok = wait_warp(&bar->s_full, i & 1, abort, p);
+      ok = wait_warp(BAR(s_full), ph, abort, p);
       if (!ok) break;
       tc_fence_after();
       tmem_ld32(tmem + lanes + S_COL + c0, v);
       tmem_ld_wait();
-      warp_arrive(&bar->s_free);
+      warp_arrive(BAR(s_free));
 #pragma unroll
       for (int k = 0; k < COLS; k += 2) {
         const float2 a = f2_split(f2_fma(f2_make(v[k], v[k + 1]), cc, ll));
@@ -546,10 +582,10 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
         for (int k = 0; k < COLS; ++k)
           if (k < lo || k >= hi) v[k] = 0.f;
       }
-      ok = wait_warp(&bar->dp_full[i & 1], (i >> 1) & 1, abort, p);
+      ok = wait_warp(BAR(dp_full) + 8 * buf.s, buf.ph, abort, p);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t dp = tmem + lanes + DP_COL + (i & 1) * WT + c0;
+      const uint32_t dp = tmem + lanes + DP_COL + buf.s * WT + c0;
       float d[COLS];
       tmem_ld32(dp, d);
       tmem_ld_wait();
@@ -560,10 +596,12 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
         v[k + 1] = x.y;
       }
       store_rounded<T, COLS / 2>(dp, v);
-      warp_arrive(&bar->ds_full[i & 1]);
+      warp_arrive(BAR(ds_full) + 8 * buf.s);
+      buf.next();
+      ph ^= 1u;
     }
     if (ok && n > 0) {
-      ok = wait_warp(&bar->done, 0, abort, p);
+      ok = wait_warp(BAR(done), 0, abort, p);
       tc_fence_after();
     }
     if (ok) {

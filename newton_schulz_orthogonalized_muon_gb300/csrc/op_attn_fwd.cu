@@ -17,6 +17,8 @@
 //
 // Bound by the tensor cores and the exponentials alike: a 128 x 128 tile
 // pair with dim 128 takes 512 cycles of products and 16 K exponentials.
+#include <cstddef>
+
 #include "common.cuh"
 #include "internal.h"
 #include "op_attn.cuh"
@@ -53,6 +55,8 @@ struct Bars {
   Work work;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
+// shared-memory address of a barrier; `bb` is the block's
+#define BAR(f) (bb + static_cast<uint32_t>(offsetof(Bars, f)))
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t sb = smem_u32(smem);
+  const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
   if (!swizzle_aligned(sb, p)) return;
   if (warp == 0) {
     const Work w = find_work(p, true, ROWS, p.heads, tiles, blockIdx.x);
@@ -120,8 +124,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (r[t].count > 0) {
-            mbar_arrive_expect_tx(&bar->q_full[t], S::T);
-            load_tile<DP>(sb + t * S::T, &mq, &bar->q_full[t], w.h, w.q0 + i0 + t * TILE, w.b);
+            mbar_expect_at(BAR(q_full) + 8 * (t), S::T);
+            load_tile<DP>(sb + t * S::T, &mq, BAR(q_full) + 8 * (t), w.h, w.q0 + i0 + t * TILE, w.b);
           }
         }
       }
@@ -130,20 +134,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < n; ++i) {
         const int j = (beg + i) * TILE, row = w.k0 + j, valid = w.nk - j;
         const int sk = i % S::RK, sv = i % S::RV;
-        if (i >= S::RK && !wait_warp(&bar->k_empty[sk], (i / S::RK - 1) & 1, abort, p)) break;
+        if (i >= S::RK && !wait_warp(BAR(k_empty) + 8 * (sk), (i / S::RK - 1) & 1, abort, p)) break;
         if (lane == 0) {
           // rows past the sequence give scores that are masked, whatever they hold
-          mbar_arrive_expect_tx(&bar->k_full[sk], S::T);
-          load_tile<DP>(sb + S::K_OFF + sk * S::T, &mk, &bar->k_full[sk], hk, row, w.b);
+          mbar_expect_at(BAR(k_full) + 8 * (sk), S::T);
+          load_tile<DP>(sb + S::K_OFF + sk * S::T, &mk, BAR(k_full) + 8 * (sk), hk, row, w.b);
         }
         ++ik;
-        if (i >= S::RV && !wait_warp(&bar->v_empty[sv], (i / S::RV - 1) & 1, abort, p)) break;
+        if (i >= S::RV && !wait_warp(BAR(v_empty) + 8 * (sv), (i / S::RV - 1) & 1, abort, p)) break;
         if (p.cu_q != nullptr && valid < TILE) {
-          if (!load_edge_tile<DP>(smem + S::V_OFF + sv * S::T, &mv, &bar->edge, edges, hk, row, valid, abort, p)) break;
-          if (lane == 0) mbar_arrive(&bar->v_full[sv]);
+          if (!load_edge_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, BAR(edge), edges, hk, row, valid, abort, p)) break;
+          if (lane == 0) mbar_arrive_at(BAR(v_full) + 8 * (sv));
         } else if (lane == 0) {
-          mbar_arrive_expect_tx(&bar->v_full[sv], S::T);
-          load_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, &bar->v_full[sv], hk, row, w.b);
+          mbar_expect_at(BAR(v_full) + 8 * (sv), S::T);
+          load_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, BAR(v_full) + 8 * (sv), hk, row, w.b);
         }
         ++iv;
       }
@@ -156,41 +160,56 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     } else if (warp == 1 && n > 0) {
       // -------------------------------------------------------- products
-      int steps[2] = {0, 0};                       // key tiles done, of each query tile
-      auto scores = [&](int t, int i) {
-        if (!wait_warp(&bar->k_full[i % S::RK], (i / S::RK) & 1, abort, p)) return false;
-        if (steps[t] == 0 && !wait_warp(&bar->q_full[t], 0, abort, p)) return false;
-        tc_fence_after();
-        mma_over_dim<T, DP>(tmem + t * TILE, desc_dim(sb + t * S::T), desc_dim(sb + S::K_OFF + (i % S::RK) * S::T));
-        commit_warp(&bar->s_full[t]);
-        return true;
+      Ring<S::RK> rk;                              // the K tile of the scores to come
+      Ring<S::RV> rv;
+      uint32_t ph[2] = {0u, 0u}, acc[2] = {0u, 0u};
+      auto scores = [&](int t) {
+        mma_over_dim<T, DP>(tmem + t * TILE, desc_dim(sb + t * S::T), desc_dim(sb + S::K_OFF + rk.s * S::T));
+        commit_warp(BAR(s_full) + 8 * t);
       };
-      bool ok = true;
-      for (int t = 0; t < 2; ++t)
-        if (ok && sees(t, beg)) ok = scores(t, 0);
-      if (ok) commit_warp(&bar->k_empty[0]);
-      for (int i = 0; ok && i < n; ++i) {
-        for (int t = 0; ok && t < 2; ++t) {
-          if (sees(t, beg + i)) {
-            ok = wait_warp(&bar->p_full[t], steps[t] & 1, abort, p) &&
-                 wait_warp(&bar->v_full[i % S::RV], (i / S::RV) & 1, abort, p);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t pr = tmem + t * TILE;
-            mma_over_tokens<T, DP, TILE>(tmem + 256 + t * TILE, pr,
-                                           desc_tokens(sb + S::V_OFF + (i % S::RV) * S::T), steps[t] != 0 ? 1u : 0u);
-            commit_warp(&bar->o_done[t]);
-            ++steps[t];
+      bool ok = wait_warp(BAR(k_full), 0, abort, p);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (ok && r[t].count > 0) ok = wait_warp(BAR(q_full) + 8 * t, 0, abort, p);
+        if (ok && sees(t, beg)) {
+          tc_fence_after();
+          scores(t);
+        }
+      }
+      if (ok) commit_warp(BAR(k_empty));
+      rk.next();
+      for (int tile = beg; ok && tile < end; ++tile) {
+        const bool more = tile + 1 < end;
+        // this step's tiles before the probabilities, so that no wait stands between products
+        ok = wait_warp(BAR(v_full) + 8 * rv.s, rv.ph, abort, p) &&
+             (!more || wait_warp(BAR(k_full) + 8 * rk.s, rk.ph, abort, p));
+        if (!ok) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && sees(t, tile)) {
+            ok = wait_warp(BAR(p_full) + 8 * t, ph[t], abort, p);
+            if (ok) {
+              tc_fence_after();
+              mma_over_tokens<T, DP, TILE>(tmem + 256 + t * TILE, tmem + t * TILE,
+                                           desc_tokens(sb + S::V_OFF + rv.s * S::T), acc[t]);
+              commit_warp(BAR(o_done) + 8 * t);
+              ph[t] ^= 1u;
+              acc[t] = 1u;
+            }
           }
           // over the probabilities just used: the tensor pipe runs in order
-          if (i + 1 < n && sees(t, beg + i + 1)) ok = scores(t, i + 1);
+          if (ok && more && sees(t, tile + 1)) scores(t);
         }
         if (!ok) break;
-        commit_warp(&bar->v_empty[i % S::RV]);
-        if (i + 1 < n) commit_warp(&bar->k_empty[(i + 1) % S::RK]);
+        commit_warp(BAR(v_empty) + 8 * rv.s);
+        rv.next();
+        if (more) {
+          commit_warp(BAR(k_empty) + 8 * rk.s);
+          rk.next();
+        }
       }
       if (!ok) {
-        commit_warp(&bar->drain);
+        commit_warp(BAR(drain));
         if (lane == 0) mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
         __syncwarp();
       }
@@ -212,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < cnt; ++i) {
         const int j0 = (r[t].first + i) * TILE;
         float v[TILE];
-        ok = wait_warp(&bar->s_full[t], i & 1, abort, p);
+        ok = wait_warp(BAR(s_full) + 8 * t, i & 1, abort, p);
         if (!ok) break;
         tc_fence_after();
   #pragma unroll
@@ -241,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
           if (__any_sync(0xffffffffu, up)) {
-            ok = wait_warp(&bar->o_done[t], (i - 1) & 1, abort, p);
+            ok = wait_warp(BAR(o_done) + 8 * t, (i - 1) & 1, abort, p);
             if (!ok) break;
             tc_fence_after();
             const float f = !up ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - mt) * c);
@@ -273,10 +292,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           store_rounded<T, 32>(s_at + k / 2, v + k);
         }
-        warp_arrive(&bar->p_full[t]);
+        warp_arrive(BAR(p_full) + 8 * t);
       }
       if (ok && cnt > 0) {
-        ok = wait_warp(&bar->o_done[t], (cnt - 1) & 1, abort, p);
+        ok = wait_warp(BAR(o_done) + 8 * t, (cnt - 1) & 1, abort, p);
         tc_fence_after();
       }
       if (ok) {

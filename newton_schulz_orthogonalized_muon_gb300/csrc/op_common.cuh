@@ -118,6 +118,28 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
   return r;
 }
 
+// A place in a ring: its index and the phase bit of its next use.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int by = 1) {
+    s += by;
+    if (s >= N) {
+      s -= N;
+      ph ^= 1u;
+    }
+  }
+};
+
+// Barriers by their shared-memory address.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // 16 bytes of shared memory
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
@@ -125,9 +147,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return v;
 }
 // Untiled copy: both addresses and the size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
 

@@ -410,10 +410,10 @@ __device__ __forceinline__ void copy_batches(const NormParams& p, uint32_t ring,
       const T* src = static_cast<const T*>(a == 0 ? p.x : p.dy);
       const long long ld = a == 0 ? p.ldx : p.lddy;
       if (ld == p.cols) {
-        if (lane == a) bulk_load(dst + a * B * row_bytes, src + row * ld, n * row_bytes, &full[slot]);
+        if (lane == a) bulk_load(dst + a * B * row_bytes, src + row * ld, n * row_bytes, smem_u32(&full[slot]));
       } else {
         for (int k = lane; k < n; k += 32)
-          bulk_load(dst + (a * B + k) * row_bytes, src + (row + k) * ld, row_bytes, &full[slot]);
+          bulk_load(dst + (a * B + k) * row_bytes, src + (row + k) * ld, row_bytes, smem_u32(&full[slot]));
       }
     }
     if (++slot == depth) {

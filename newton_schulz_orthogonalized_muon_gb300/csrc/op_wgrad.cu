@@ -65,20 +65,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-// A place in a ring: its index and the phase bit of its next use.
-template <int N>
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next(int by = 1) {
-    s += by;
-    if (s >= N) {
-      s -= N;
-      ph ^= 1u;
-    }
-  }
-};
-
 // Pair products issued by a warp whose lanes stay together (see op_attn.cuh).
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
@@ -313,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const long long t0 = static_cast<long long>(k) * BK;
                 const uint32_t bytes = p.rows - t0 >= BK ? BK : static_cast<uint32_t>((p.rows - t0 + 15) / 16 * 16);
                 mbar_arrive_expect_tx(cf, bytes);
-                bulk_load(sb + SCALE_OFF + rc.s * BK, from + t0, bytes, cf);
+                bulk_load(sb + SCALE_OFF + rc.s * BK, from + t0, bytes, smem_u32(cf));
               } else {
                 mbar_arrive(cf);
               }
