@@ -371,7 +371,7 @@ int attn_qtiles(int sq, int batch, bool packed);
 // m: 4-D tensor maps {dim, head, token, batch} of q, k, v (and do) with boxes
 // of 64 columns and 128 tokens (64 backward with dim <= 64), 128-byte swizzle.
 cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s);
-// part 0: statistics; 1: dk and dv; 2: dq
-cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s);
+// prep: the statistics (sq > 0); else, after it on the stream, the gradients
+cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s);
 
 }  // namespace muon

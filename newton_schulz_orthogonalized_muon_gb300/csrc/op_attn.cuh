@@ -108,19 +108,20 @@ __device__ __forceinline__ Work find_packed(const AttnParams& p, bool by_q, int 
 // Work item `item` of a grid of tiles of `rows` rows x (heads x batch), heads fastest.  The
 // longest items of a causal grid come first: the key tiles in their order,
 // the query tiles (`tiles` of them at most) from the last.
-__device__ __forceinline__ Work find_work(const AttnParams& p, bool by_q, int rows, int heads, int tiles, long long item) {
-  const long long hb = static_cast<long long>(heads) * (p.cu_q != nullptr ? 1 : p.batch);
+__device__ __forceinline__ Work find_work(const AttnParams& p, bool by_q, int rows, int heads, int tiles,
+                                          uint32_t item) {
+  const uint32_t hb = static_cast<uint32_t>(heads) * (p.cu_q != nullptr ? 1u : static_cast<uint32_t>(p.batch));
   int tile = static_cast<int>(item / hb);
-  const int r = static_cast<int>(item % hb);
+  const uint32_t r = item % hb;
   if (by_q) tile = tiles - 1 - tile;
   Work w;
   if (p.cu_q != nullptr) {
     w = find_packed(p, by_q, rows, tile);
     w.b = 0;
   } else {
-    w = Work{0, p.sq, 0, p.sk, tile, 0, r / heads, 0, 1};
+    w = Work{0, p.sq, 0, p.sk, tile, 0, static_cast<int>(r / heads), 0, 1};
   }
-  w.h = r % heads;
+  w.h = static_cast<int>(r % heads);
   return w;
 }
 
@@ -390,22 +391,38 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// 32 consecutive fp32 TMEM columns of this warp's rows, times `mul`, rounded
-// to T, into columns c0 .. c0 + 31 of row `dst` (nullptr: nowhere).
-template <typename T>
-__device__ __forceinline__ void store_cols32(uint32_t taddr, T* dst, int c0, int dim, float mul) {
-  float v[32];
-  tmem_ld32(taddr, v);
-  tmem_ld_wait();
-  if (dst == nullptr) return;
+// NC = 32 or 64 fp32 TMEM columns of this warp's 32 rows, times `mul`, rounded
+// to T, out to `dst` (row 0, column 0; `rows` rows and `cols` columns of it
+// exist).  By way of the warp's rows of a box [128][64] in shared memory that
+// nothing reads any more, so that lanes next to each other write one row:
+// a row a lane took 1.7 us for a 128 x 64 tile.
+template <typename T, int NC>
+__device__ __forceinline__ void store_block(uint32_t taddr, uint32_t box, int r0, int chunk0, T* dst, long long stride,
+                                            int rows, int cols, float mul) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (c0 + 8 * q < dim) {
+  for (int c = 0; c < NC; c += 32) {
+    float v[32];
+    tmem_ld32(taddr + c, v);
+    tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * q + e] *= mul;
-      *reinterpret_cast<uint4*>(dst + c0 + 8 * q) = pack16<T>(v + 8 * q);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = pack2<T>(v[8 * q + 2 * e] * mul, v[8 * q + 2 * e + 1] * mul);
+      sts16(box + (r0 + lane) * 128 + (((chunk0 + c / 8 + q) ^ (lane & 7)) << 4), r);
     }
   }
+  __syncwarp();
+  constexpr int LPR = NC / 8;                    // lanes of a row
+  const int q = lane % LPR;
+#pragma unroll
+  for (int i = 0; i < LPR; ++i) {
+    const int r = i * (32 / LPR) + lane / LPR;
+    if (r < rows && 8 * q < cols)
+      *reinterpret_cast<uint4*>(dst + r * stride + 8 * q) = lds16(box + (r0 + r) * 128 + (((chunk0 + q) ^ (r & 7)) << 4));
+  }
+  __syncwarp();
 }
 
 // one arrival of a warp whose lanes' TMEM accesses are complete

@@ -4,11 +4,11 @@
 //   dv_j = sum_i p_ij do_i,   ds_ij = p_ij (do_i . v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
 //
-// Three kernels.  attn_prep_kernel writes lse_i log2(e) and delta_i, tile by
-// tile (HBM-bound: it reads o and do).  attn_dkv_kernel owns a tile of 128
-// keys, walks the query tiles that see them (of every query head that shares
-// the key head) and keeps dk and dv in TMEM; attn_dq_kernel owns a tile of
-// 128 queries, walks its key tiles and keeps dq in TMEM.  No value is added
+// attn_prep_kernel writes lse_i log2(e) and delta_i, tile by tile (HBM-bound:
+// it reads o and do).  attn_bwd_kernel has two kinds of items.  One owns a
+// tile of 128 keys, walks the query tiles that see them (of every query head
+// that shares the key head) and keeps dk and dv in TMEM; the other owns a
+// tile of 128 queries, walks its key tiles and keeps dq in TMEM.  No value is added
 // by atomics, so results do not change from call to call; the price is that
 // scores and dP are formed twice, seven products a tile pair instead of five.
 //
@@ -52,9 +52,12 @@ struct Shape {
 // -lse log2(e) and -delta of one tile of queries, 128 values each (the sign
 // that two-wide additions want), padded: rows past the sequence and rows that
 // see no key get -inf, so that their p is 0.
-template <typename T>
+template <typename T, int DP>
 __global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int tiles) {
+  constexpr int LPR = DP / 8;                     // lanes of a row, 16 bytes each
+  constexpr int N = TILE * LPR / 256;             // rows of a thread
   __shared__ Work sw;
+  pdl_launch_dependents();
   if (threadIdx.x < 32) {
     const Work w = find_work(p, true, TILE, p.heads, tiles, blockIdx.x);
     if (threadIdx.x == 0) sw = w;
@@ -62,36 +65,39 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int 
   __syncthreads();
   const Work w = sw;
   if (!w.ok) return;
-  const int l = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE;
-  uint4 a[8], b[8];
-  float lse[8];
+  const int l = threadIdx.x % LPR, r0 = w.tile * TILE + threadIdx.x / LPR;
+  const T* o = static_cast<const T*>(p.o) + w.b * p.ob + static_cast<long long>(w.q0) * p.os + w.h * p.oh + 8 * l;
+  const T* g = static_cast<const T*>(p.dout) + w.b * p.dob + static_cast<long long>(w.q0) * p.dos + w.h * p.doh + 8 * l;
+  const float* lse = p.lse + w.b * p.lse_b + w.h * p.lse_h + w.q0;
+  const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile) * TILE;
+  uint4 a[N], b[N];
+  float e[N];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = w.tile * TILE + 16 * k + r;
+  for (int k = 0; k < N; ++k) {
+    const int i = r0 + k * (256 / LPR);
     a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
-    lse[k] = -INFINITY;
+    e[k] = -INFINITY;
     if (i < w.nq) {
-      const long long t = w.q0 + i;
       if (8 * l < p.dim) {
-        a[k] = ld_stream16(static_cast<const T*>(p.o) + w.b * p.ob + t * p.os + w.h * p.oh + 8 * l);
-        b[k] = ld_stream16(static_cast<const T*>(p.dout) + w.b * p.dob + t * p.dos + w.h * p.doh + 8 * l);
+        a[k] = ld_stream16(o + static_cast<long long>(i) * p.os);
+        b[k] = ld_stream16(g + static_cast<long long>(i) * p.dos);
       }
-      if (l == 0) lse[k] = p.lse[w.b * p.lse_b + w.h * p.lse_h + t];
+      if (l == 0) e[k] = lse[i];
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < N; ++k) {
     float x[8], y[8], s = 0.f;
     unpack16<T>(a[k], x);
     unpack16<T>(b[k], y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+    for (int c = 0; c < 8; ++c) s = fmaf(x[c], y[c], s);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int c = LPR / 2; c > 0; c >>= 1) s += __shfl_xor_sync(0xffffffffu, s, c);
     if (l == 0) {
-      p.stat_lse[at + 16 * k + r] = lse[k] == -INFINITY ? -INFINITY : -lse[k] * LOG2E;
-      p.stat_delta[at + 16 * k + r] = -s;
+      const int i = r0 + k * (256 / LPR);
+      p.stat_lse[at + i] = e[k] == -INFINITY ? -INFINITY : -e[k] * LOG2E;
+      p.stat_delta[at + i] = -s;
     }
   }
 }
@@ -160,10 +166,9 @@ __device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
 // them, and shared memory's bandwidth, which the products need, bound the
 // step (2970 cycles with dim 128 against 2048 of products).
 template <typename T, int DP>
-__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
-    attn_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
-                    const AttnParams p, int tiles, int qtiles) {
+__device__ __forceinline__ void dkv_item(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                         const CUtensorMap& mdo, const AttnParams& p, int tiles, int qtiles,
+                                         uint32_t item) {
   using S = Smem<DP>;
   constexpr int WT = S::WT, BOX = DP == 64 ? 64 : TILE;      // rows of a walked tile, of a map's box
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
   if (!swizzle_aligned(sb, p)) return;
   if (warp == 0) {
-    const Work w = find_work(p, false, TILE, p.kv_heads, tiles, blockIdx.x);
+    const Work w = find_work(p, false, TILE, p.kv_heads, tiles, item);
     if (lane == 0) {
       bar->work = w;
       init_bars(bar, Shape<DP>::CALC);
@@ -197,9 +202,8 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     if (lane == 0) {
       mbar_expect_at(BAR(own), S::OWN);
       load_tile<DP, TILE, BOX>(sb, &mk, BAR(own), w.h, w.k0 + j0, w.b);
-      mbar_expect_at(BAR(own) + 8, S::OWN);
-      load_tile<DP, TILE, BOX>(sb + S::OWN, &mv, BAR(own) + 8, w.h, w.k0 + j0, w.b);
     }
+    bool first = true;
     uint32_t edges = 0;
     int ia = 0, ib = 0;
     Ring<S::RA> ra;
@@ -224,6 +228,14 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
         }
         ++ia;
         ra.next();
+        if (first) {                               // after what the first scores want
+          first = false;
+          if (lane == 0) {
+            mbar_expect_at(BAR(own) + 8, S::OWN);
+            load_tile<DP, TILE, BOX>(sb + S::OWN, &mv, BAR(own) + 8, w.h, w.k0 + j0, w.b);
+          }
+          pdl_wait();                              // the statistics are the previous kernel's
+        }
         ok = wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p);
         if (!ok) break;
         if (edge) {
@@ -243,7 +255,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     }
     if (*abort != 0 && lane == 0) {
       mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
-      mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
+      if (!first) mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
       drain_ring<S::RA>(bar->a_full, ia);
       drain_ring<S::RB>(bar->b_full, ib);
     }
@@ -387,20 +399,20 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
       tc_fence_after();
     }
     if (ok) {
-      // dv by the first half of the warps, dk by the others, 64 columns a warp
+      // dv by the first half of the warps, dk by the others, 64 columns a warp,
+      // through K's and V's places in shared memory
       const bool is_dv = part < Shape<DP>::PARTS / 2;
-      const int key = j0 + quad * 32 + lane;
-      const long long t = w.k0 + key;
-      T* row = is_dv ? static_cast<T*>(p.dv) + w.b * p.dvb + t * p.dvs + w.h * p.dvh
-                     : static_cast<T*>(p.dk) + w.b * p.dkb + t * p.dks + w.h * p.dkh;
-      if (key >= w.nk) row = nullptr;
-      const int d0 = part % (Shape<DP>::PARTS / 2) * 64;
+      const int x = part % (Shape<DP>::PARTS / 2), first = j0 + quad * 32;
+      const long long stride = is_dv ? p.dvs : p.dks, t = w.k0 + first;
+      T* out = (is_dv ? static_cast<T*>(p.dv) + w.b * p.dvb + w.h * p.dvh : static_cast<T*>(p.dk) + w.b * p.dkb + w.h * p.dkh) +
+               t * stride + 64 * x;
       if (n > 0) {
-#pragma unroll 1
-        for (int k = d0; k < d0 + 64; k += 32)
-          store_cols32<T>(tmem + lanes + (is_dv ? DV_COL : DK_COL) + k, row, k, p.dim, is_dv ? 1.f : p.scale);
-      } else if (row != nullptr && d0 == 0) {
-        for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+        store_block<T, 64>(tmem + lanes + (is_dv ? DV_COL : DK_COL) + 64 * x,
+                           sb + (is_dv ? S::OWN : 0) + x * BOX_BYTES, quad * 32, 0, out, stride, w.nk - first,
+                           p.dim - 64 * x, is_dv ? 1.f : p.scale);
+      } else if (first + lane < w.nk) {
+        for (int k = 0; k < 64 && 64 * x + k < p.dim; k += 8)
+          *reinterpret_cast<uint4*>(out + lane * stride + k) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
   }
@@ -412,10 +424,8 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
 
 // -------------------------------------------------------------------- dq
 template <typename T, int DP>
-__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
-    attn_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
-                   const AttnParams p, int tiles) {
+__device__ __forceinline__ void dq_item(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                        const CUtensorMap& mdo, const AttnParams& p, int tiles, uint32_t item) {
   using S = Smem<DP>;
   constexpr int WT = S::WT, BOX = DP == 64 ? 64 : TILE;      // rows of a walked tile, of a map's box
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -424,7 +434,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
   if (!swizzle_aligned(sb, p)) return;
   if (warp == 0) {
-    const Work w = find_work(p, true, TILE, p.heads, tiles, blockIdx.x);
+    const Work w = find_work(p, true, TILE, p.heads, tiles, item);
     if (lane == 0) {
       bar->work = w;
       init_bars(bar, Shape<DP>::CALC);
@@ -450,9 +460,8 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     if (lane == 0) {
       mbar_expect_at(BAR(own), S::OWN);
       load_tile<DP, TILE, BOX>(sb, &mq, BAR(own), w.h, w.q0 + i0, w.b);
-      mbar_expect_at(BAR(own) + 8, S::OWN);
-      load_tile<DP, TILE, BOX>(sb + S::OWN, &mdo, BAR(own) + 8, w.h, w.q0 + i0, w.b);
     }
+    bool first = true;
     uint32_t edges = 0;
     int ia = 0, ib = 0;
     Ring<S::RA> ra;
@@ -472,6 +481,13 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
       }
       ++ia;
       ra.next();
+      if (first) {                                 // after what the first scores want
+        first = false;
+        if (lane == 0) {
+          mbar_expect_at(BAR(own) + 8, S::OWN);
+          load_tile<DP, TILE, BOX>(sb + S::OWN, &mdo, BAR(own) + 8, w.h, w.q0 + i0, w.b);
+        }
+      }
       if (!wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p)) break;
       if (edge) {
         if (!load_edge_tile<DP, WT, BOX>(bt, &mv, BAR(edge), edges, hk, row, valid, abort, p)) break;
@@ -485,7 +501,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     }
     if (*abort != 0 && lane == 0) {
       mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
-      mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
+      if (!first) mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
       drain_ring<S::RA>(bar->a_full, ia);
       drain_ring<S::RB>(bar->b_full, ib);
     }
@@ -550,6 +566,7 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     const float c = p.scale * LOG2E;
     const int off = w.nk - w.nq;
     const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE + quad * 32 + lane;
+    pdl_wait();                                    // the statistics are the previous kernel's
     const float lse = n > 0 ? p.stat_lse[at] : 0.f, delta = n > 0 ? p.stat_delta[at] : 0.f;
     const F2 cc = f2_make(c, c), ll = f2_make(lse, lse), dd = f2_make(delta, delta);
     Ring<2> buf;
@@ -605,12 +622,15 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
       tc_fence_after();
     }
     if (ok) {
-      T* row = q < w.nq ? static_cast<T*>(p.dq) + w.b * p.dqb + static_cast<long long>(w.q0 + q) * p.dqs + w.h * p.dqh
-                        : nullptr;
+      // 32 columns a warp, through Q's place in shared memory
+      const int first = i0 + quad * 32;
+      T* out = static_cast<T*>(p.dq) + w.b * p.dqb + static_cast<long long>(w.q0 + first) * p.dqs + w.h * p.dqh + c0;
       if (n > 0) {
-        store_cols32<T>(tmem + lanes + DQ_COL + c0, row, c0, p.dim, p.scale);
-      } else if (row != nullptr && part == 0) {
-        for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+        store_block<T, COLS>(tmem + lanes + DQ_COL + c0, sb + c0 / 64 * BOX_BYTES, quad * 32, c0 % 64 / 8, out, p.dqs,
+                             w.nq - first, p.dim - c0, p.scale);
+      } else if (q < w.nq) {
+        for (int k = 0; k < COLS && c0 + k < p.dim; k += 8)
+          *reinterpret_cast<uint4*>(out + lane * p.dqs + k) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
   }
@@ -620,41 +640,59 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   if (warp == 1) tmem_dealloc(tmem, Shape<DP>::TMEM);
 }
 
-long long seqs(const AttnParams& p) { return p.cu_q != nullptr ? 1 : p.batch; }
+// Items [0, nk) are key tiles (dk, dv), the rest query tiles (dq): one launch,
+// so that the short items of one kind fill the SMs beside the last long ones
+// of the other.
+template <typename T, int DP>
+__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                    const AttnParams p, uint32_t nk, int ktiles, int qtiles) {
+  if (threadIdx.x < 32) {
+    if ((threadIdx.x & 31) == 0) {
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+      tma_prefetch_map(&mdo);
+    }
+    __syncwarp();
+  }
+  if (blockIdx.x < nk)
+    dkv_item<T, DP>(mq, mk, mv, mdo, p, ktiles, qtiles, blockIdx.x);
+  else
+    dq_item<T, DP>(mq, mk, mv, mdo, p, qtiles, blockIdx.x - nk);
+}
 
 template <typename T, int DP>
-cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s) {
-  const long long qt = p.qtiles, kt = tile_bound(p.sk, TILE, p.batch, p.cu_q != nullptr);
-  const long long nq = qt * p.heads * seqs(p), nk = kt * p.kv_heads * seqs(p);
-  if (nq > 0x7FFFFFFFll || nk > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  if (part == 0) {
-    attn_prep_kernel<T><<<static_cast<unsigned>(nq), 256, 0, s>>>(p, static_cast<int>(qt));
+cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s) {
+  const bool packed = p.cu_q != nullptr;
+  const long long seqs = packed ? 1 : p.batch;
+  const long long qt = p.qtiles, kt = tile_bound(p.sk, TILE, p.batch, packed);
+  const long long nq = p.sq > 0 ? qt * p.heads * seqs : 0, nk = p.sk > 0 ? kt * p.kv_heads * seqs : 0;
+  if (nq + nk > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  if (prep) {
+    attn_prep_kernel<T, DP><<<static_cast<unsigned>(nq), 256, 0, s>>>(p, static_cast<int>(qt));
     return cudaGetLastError();
   }
-  auto dkv = attn_dkv_kernel<T, DP>;
-  auto dq = attn_dq_kernel<T, DP>;
-  static std::atomic<unsigned long long> done[2];
-  const cudaError_t e = part == 1 ? allow_smem(reinterpret_cast<const void*>(dkv), Smem<DP>::BYTES, done[0])
-                                  : allow_smem(reinterpret_cast<const void*>(dq), Smem<DP>::BYTES, done[1]);
+  auto kern = attn_bwd_kernel<T, DP>;
+  static std::atomic<unsigned long long> done;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
   if (e != cudaSuccess) return e;
-  if (part == 1)
-    dkv<<<static_cast<unsigned>(nk), Shape<DP>::THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(kt),
-                                                                    static_cast<int>(qt));
-  else
-    dq<<<static_cast<unsigned>(nq), Shape<DP>::THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], m[3], p, static_cast<int>(qt));
-  return cudaGetLastError();
+  // its prologue overlaps the statistics kernel (the wait for them is in the items); without that one, no overlap
+  e = launch_k(p.sq > 0, kern, dim3(static_cast<unsigned>(nq + nk)), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0],
+               m[1], m[2], m[3], p, static_cast<uint32_t>(nk), static_cast<int>(kt), static_cast<int>(qt));
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_part(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s) {
-  return p.dim <= 64 ? launch_dims<T, 64>(p, m, part, s) : launch_dims<T, 128>(p, m, part, s);
+cudaError_t launch_type(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s) {
+  return p.dim <= 64 ? launch_dims<T, 64>(p, m, prep, s) : launch_dims<T, 128>(p, m, prep, s);
 }
 
 }  // namespace
 
-// part 0: statistics; 1: dk and dv; 2: dq.  m: maps of q, k, v, do.
-cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, int part, cudaStream_t s) {
-  return p.dtype == DT_BF16 ? launch_part<__nv_bfloat16>(p, m, part, s) : launch_part<__half>(p, m, part, s);
+cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s) {
+  return p.dtype == DT_BF16 ? launch_type<__nv_bfloat16>(p, m, prep, s) : launch_type<__half>(p, m, prep, s);
 }
 
 }  // namespace muon

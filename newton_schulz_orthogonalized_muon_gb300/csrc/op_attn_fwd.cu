@@ -301,16 +301,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (ok) {
         const float2 s2 = f2_split(sum2);
         const float sum = s2.x + s2.y;
-        T* row = q < w.nq ? static_cast<T*>(p.out) + w.b * p.ob + static_cast<long long>(w.q0 + q) * p.os + w.h * p.oh
-                          : nullptr;
+        const int first = q0 + quad * 32;          // of the warp's queries
+        T* out = static_cast<T*>(p.out) + w.b * p.ob + static_cast<long long>(w.q0 + first) * p.os + w.h * p.oh;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (cnt > 0) {
-  #pragma unroll 1
-          for (int k = 0; k < DP; k += 32) store_cols32<T>(o_at + k, row, k, p.dim, inv);
-        } else if (row != nullptr) {
-          for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(row + k) = make_uint4(0u, 0u, 0u, 0u);
+          // through this tile's Q, which every product has read
+#pragma unroll
+          for (int x = 0; x < DP / 64; ++x)
+            store_block<T, 64>(o_at + 64 * x, sb + t * S::T + x * BOX_BYTES, quad * 32, 0, out + 64 * x, p.os,
+                               w.nq - first, p.dim - 64 * x, inv);
+        } else if (q < w.nq) {
+          for (int k = 0; k < p.dim; k += 8)
+            *reinterpret_cast<uint4*>(out + lane * p.os + k) = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (row != nullptr)
+        if (q < w.nq)
           p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + q] =
               sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
       }

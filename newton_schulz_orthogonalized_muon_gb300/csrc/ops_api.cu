@@ -351,9 +351,8 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
            attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype, tokens);
     if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
-    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 0, stream), "attention statistics launch");
-    if (a->sk > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 1, stream), "attention dk, dv launch");
-    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, 2, stream), "attention dq launch");
+    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, true, stream), "attention statistics launch");
+    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, false, stream), "attention backward launch");
     return MUON_OK;
   });
 }
