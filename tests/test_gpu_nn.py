@@ -1,0 +1,98 @@
+"""The autograd wrappers of the training operators, and the example that
+trains with them.
+
+Gradients are compared with torch's autograd in fp64 on the same (bf16)
+values.  A bf16 result is rounded at every operator, each rounding at most
+2^-8 of its value; through the few operators of these tests the relative
+error of a whole gradient stays below 2^-5 (norm against norm)."""
+import os
+import sys
+
+import pytest
+import torch
+
+from _margins import record
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def nn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    from newton_schulz_orthogonalized_muon_gb300 import nn as mod
+    return mod
+
+
+def near(name, got, ref, tol=2.0 ** -5):
+    err = ((got.double() - ref.double()).norm() / ref.double().norm()).item()
+    record(name, err, tol)
+    assert err < tol, (name, err)
+
+
+def leaf(t, dtype=None):
+    return t.detach().to(dtype or t.dtype).clone().requires_grad_(True)
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(BF, torch.float32), (torch.float16, torch.float16),
+                                          (torch.float32, torch.float32)])
+def test_layer_norm_gradients(nn, dtype, wdtype):
+    torch.manual_seed(1)
+    x, w, b = (torch.randn(3, 50, 96, device="cuda") + 1).to(dtype), torch.rand(96, device="cuda").to(wdtype), \
+        torch.randn(96, device="cuda").to(wdtype)
+    g = torch.randn(3, 50, 96, device="cuda").to(dtype)
+    mine = [leaf(t) for t in (x, w, b)]
+    nn.layer_norm(*mine).backward(g)
+    ref = [leaf(t, torch.float64) for t in (x, w, b)]
+    torch.nn.functional.layer_norm(ref[0], (96,), ref[1], ref[2]).backward(g.double())
+    for n, a, r in zip(("x", "weight", "bias"), mine, ref):
+        assert a.grad.dtype == a.dtype
+        near(f"nn layer norm {dtype} {n}", a.grad, r.grad, 2.0 ** -18 if dtype == torch.float32 else 2.0 ** -8)
+
+
+def test_attention_gradients_and_expanded_heads(nn):
+    torch.manual_seed(2)
+    q, k, v = (torch.randn(2, 150, h, 64, device="cuda").to(BF) for h in (4, 2, 2))
+    mine = [leaf(t) for t in (q, k, v)]
+    nn.attention(*mine, causal=True).sum().backward()          # the gradient of a sum has stride 0
+    ref = [leaf(t, torch.float64) for t in (q, k, v)]
+    qq = ref[0].transpose(1, 2)
+    kk, vv = (t.transpose(1, 2).repeat_interleave(2, 1) for t in ref[1:])
+    s = (qq @ kk.transpose(-1, -2)) / 8.0
+    s = s.masked_fill(torch.ones(150, 150, device="cuda").triu(1).bool(), -torch.inf)
+    (torch.softmax(s, -1) @ vv).sum().backward()
+    for n, a, r in zip("qkv", mine, ref):
+        near(f"nn attention d{n}", a.grad, r.grad)
+
+
+def test_linear8_gradients(nn):
+    torch.manual_seed(3)
+    import newton_schulz_orthogonalized_muon_gb300 as muon
+    x, w = torch.randn(5, 40, 200, device="cuda").to(BF), torch.randn(72, 200, device="cuda").to(BF)
+    g = torch.randn(5, 40, 72, device="cuda").to(BF)
+    a, b = leaf(x), leaf(w)
+    y = nn.linear8(a, b)
+    assert torch.equal(y, x @ w.t())
+    y.backward(g)
+    kept = muon.act8_restore(*muon.act8_store(x.flatten(0, 1)), dtype=torch.float32).double()
+    near("linear8 dx", a.grad, g.double() @ w.double(), 2.0 ** -8)
+    near("linear8 dw of the kept input", b.grad, g.flatten(0, 1).double().t() @ kept, 2.0 ** -8)
+    # against the unrounded input: the codes' own error, at most 2^-4 of a value and about 2^-5.4 in the mean
+    near("linear8 dw", b.grad, g.flatten(0, 1).double().t() @ x.flatten(0, 1).double(), 2.0 ** -4)
+    with pytest.raises(ValueError):
+        nn.linear8(x.float(), w.float())
+
+
+def test_example_trains(nn):
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import train_block
+    finally:
+        sys.path.pop(0)
+    losses = train_block.train(steps=60, log=None)
+    assert all(v == v for v in losses)
+    # a uniform guess over 64 tokens is 4.16; copying is learned within the run
+    assert losses[0] > 3.5 and min(losses[-5:]) < 1.0, losses[::10]
