@@ -363,6 +363,7 @@ struct AttnParams {
   int causal, window;      // window > 0: a query sees at most the last `window` keys up to its own place
   int dtype;
   float scale;
+  unsigned* counter;       // backward, scratch: items taken, or nullptr (no statistics kernel to set it to 0)
   int qtiles;              // query tiles of 128 rows of a (batch, head): a bound when packed
   unsigned* err;           // the handle's error word
   unsigned long long timeout_ns;
@@ -372,6 +373,6 @@ int attn_qtiles(int sq, int batch, bool packed);
 // of 64 columns and 128 tokens (64 backward with dim <= 64), 128-byte swizzle.
 cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s);
 // prep: the statistics (sq > 0); else, after it on the stream, the gradients
-cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s);
+cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, int sms, cudaStream_t s);
 
 }  // namespace muon

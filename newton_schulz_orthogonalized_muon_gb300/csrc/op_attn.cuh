@@ -210,20 +210,15 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     for (int y = 0; y < ROWS; y += BOX) tma_load_4d(dst + (x * ROWS + y) * 128, map, bar, 64 * x, h, row + y, b);
 }
 
-// The same by a whole warp for a packed sequence that ends inside the tile:
-// the next sequence's rows are loaded with it and then overwritten with
-// zeros, so that a NaN or an infinity there has no part in a product with a
-// zero probability.  `edge` is the warp's own barrier; on return the tile is
-// complete for the async proxy.
-template <int DP, int ROWS = TILE, int BOX = TILE>
-__device__ __forceinline__ bool load_edge_tile(uint32_t dst, const CUtensorMap* map, uint32_t edge, uint32_t& phase,
-                                               int h, int row, int valid, volatile int* abort, const AttnParams& p) {
+// The same tile, of a packed sequence that ends inside it, once it is loaded
+// (signalled on `edge`, a barrier of the loading warp): the next sequence's
+// rows, which were loaded with it, are overwritten with zeros, so that a NaN
+// or an infinity there has no part in a product with a zero probability.  By
+// the whole warp; on return the tile is complete for the async proxy.
+template <int DP, int ROWS = TILE>
+__device__ __forceinline__ bool finish_edge_tile(uint32_t dst, uint32_t edge, uint32_t& phase, int valid,
+                                                 volatile int* abort, const AttnParams& p) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) {
-    mbar_expect_at(edge, DP / 64 * ROWS * 128);
-    load_tile<DP, ROWS, BOX>(dst, map, edge, h, row, 0);
-  }
-  __syncwarp();
   if (!wait_warp(edge, phase & 1u, abort, p)) return false;
   ++phase;
 #pragma unroll
@@ -423,6 +418,48 @@ __device__ __forceinline__ void store_block(uint32_t taddr, uint32_t box, int r0
       *reinterpret_cast<uint4*>(dst + r * stride + 8 * q) = lds16(box + (r0 + r) * 128 + (((chunk0 + q) ^ (r & 7)) << 4));
   }
   __syncwarp();
+}
+
+// 32 x 32 fp32 TMEM values of this warp's rows, times `mul`, rounded to T, out
+// to `dst` (row 0, column 0; `rows` rows and `cols` columns of it exist).
+// Read in the accumulators' layout, and four lanes trade their words, so that
+// they write 64 bytes of a row: a row a lane, 16 bytes at a time, took twice
+// as long.
+template <typename T>
+__device__ __forceinline__ void store_rows(uint32_t taddr, T* dst, long long stride, int rows, int cols, float mul) {
+  if (cols <= 0) return;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  float v[32];
+  tmem_ld_16x32(taddr, v);
+  tmem_ld_16x32(taddr + (16u << 16), v + 16);
+  tmem_ld_wait();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {              // row lane / 4 + 8 k
+    uint32_t w[4];                           // word q: columns 8 q + 2 c, + 1
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* u = v + 16 * (k >> 1) + 4 * q + 2 * (k & 1);
+      w[q] = pack2<T>(u[0] * mul, u[1] * mul);
+    }
+    // transposed over the four lanes: lane c gets columns 8 c .. 8 c + 7
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      const bool up = (c & o) != 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if ((q & o) == 0) {
+          const uint32_t send = up ? w[q] : w[q | o];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, send, o);
+          if (up)
+            w[q] = got;
+          else
+            w[q | o] = got;
+        }
+      }
+    }
+    const int r = (lane >> 2) + 8 * k;
+    if (r < rows && 8 * c < cols) *reinterpret_cast<uint4*>(dst + r * stride + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // one arrival of a warp whose lanes' TMEM accesses are complete

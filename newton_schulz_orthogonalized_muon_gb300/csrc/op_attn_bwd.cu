@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AttnParams p, int 
   }
   __syncthreads();
   const Work w = sw;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0u;      // of the gradient kernel's items
   if (!w.ok) return;
   const int l = threadIdx.x % LPR, r0 = w.tile * TILE + threadIdx.x / LPR;
   const T* o = static_cast<const T*>(p.o) + w.b * p.ob + static_cast<long long>(w.q0) * p.os + w.h * p.oh + 8 * l;
@@ -117,31 +118,40 @@ struct Smem {
   static constexpr int B_OFF = A_OFF + RA * T;
   static constexpr int STAT_OFF = B_OFF + RB * T;
   static constexpr int BAR_OFF = STAT_OFF + RB * STAT;
-  static constexpr int BYTES = BAR_OFF + 256;
+  static constexpr int BYTES = BAR_OFF + 320;
   static_assert(BYTES * Shape<DP>::CTAS <= 232448 - 1024 * (Shape<DP>::CTAS - 1), "shared memory");
 };
 
+// Every barrier's phases are counted by the warps that wait on it, on through
+// the items of a CTA.
 struct Bars {
-  uint64_t own[2];          // the two tiles that stay
-  uint64_t a_full[3], a_empty[3];
+  uint64_t own[2], own_empty[2];      // the two tiles that stay: loaded, and read by their last product
+  uint64_t a_full[3], a_empty[3];     // walked tiles
   uint64_t b_full[3], b_empty[3];
-  uint64_t s_full, s_free;  // scores: written, and read into registers
-  uint64_t p_full;
-  uint64_t dp_full[2], ds_full[2];
-  uint64_t done, edge;
+  uint64_t s_full, s_free;            // scores: formed; read into registers (dq)
+  uint64_t p_full;                    // dk, dv: probabilities written
+  uint64_t dpk_full, dsk_full;        //   dP formed, ds written
+  uint64_t dp_full[2], ds_full[2];    // dq: the same, twice
+  uint64_t done, acc_free;            // an item's sums formed; read
+  uint64_t edge[2];
+  uint64_t id_full[2], id_empty[2];   // the items that the loading warp announces
+  uint32_t id[2];
   uint32_t tmem;
   int abort;
-  Work work;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 320, "barrier block");
 // shared-memory address of a barrier; `bb` is the block's
 #define BAR(f) (bb + static_cast<uint32_t>(offsetof(Bars, f)))
 
 __device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&s->own[i], 1);
+    mbar_init(&s->own_empty[i], 1);
     mbar_init(&s->dp_full[i], 1);
     mbar_init(&s->ds_full[i], calc_warps);
+    mbar_init(&s->edge[i], 1);
+    mbar_init(&s->id_full[i], 1);
+    mbar_init(&s->id_empty[i], 1 + calc_warps);
   }
   for (int i = 0; i < 3; ++i) {
     mbar_init(&s->a_full[i], 1);
@@ -152,188 +162,334 @@ __device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
   mbar_init(&s->s_full, 1);
   mbar_init(&s->s_free, calc_warps);
   mbar_init(&s->p_full, calc_warps);
+  mbar_init(&s->dpk_full, 1);
+  mbar_init(&s->dsk_full, calc_warps);
   mbar_init(&s->done, 1);
-  mbar_init(&s->edge, 1);
+  mbar_init(&s->acc_free, calc_warps);
   s->abort = 0;
   fence_mbar_init();
 }
 
-// ------------------------------------------------------------- dk and dv
-// A warp has 32 keys (TMEM rows) by 32 queries; thread t of it the keys t / 4
-// + 8 k, k = 0 .. 3, and the queries 8 j + 2 (t % 4) + {0, 1}, j = 0 .. 3.
-// Value (k, j, e) is v[16 (k / 2) + 4 j + 2 (k % 2) + e].  The queries'
-// statistics are columns here: with one row a thread every thread read all of
-// them, and shared memory's bandwidth, which the products need, bound the
-// step (2970 cycles with dim 128 against 2048 of products).
+// What every warp knows of the launch.
+struct Grid {
+  const CUtensorMap *mq, *mk, *mv, *mdo;
+  uint32_t nk, total;        // items of dk and dv, and all
+  int ktiles, qtiles;
+};
+
+// The items that the loading warp announced, for another warp of the CTA.
+struct Items {
+  Ring<2> at;
+  __device__ __forceinline__ bool next(uint32_t bb, const Bars* bar, const Grid& g, volatile int* abort,
+                                       const AttnParams& p, uint32_t* id) {
+    if (!wait_warp(BAR(id_full) + 8 * at.s, at.ph, abort, p)) return false;
+    *id = *const_cast<const volatile uint32_t*>(&bar->id[at.s]);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_at(BAR(id_empty) + 8 * at.s);
+    at.next();
+    return *id < g.total;
+  }
+};
+
+// One item: what it owns and what it walks.
+struct Item {
+  bool dkv;
+  Work w;
+  int own;                   // first row of the tile that stays, in its sequence
+  Range r;                   // walked tiles (of every head of the group: dk, dv)
+  int n;                     // steps
+};
+
+template <int WT>
+__device__ __forceinline__ Item find_item(const AttnParams& p, const Grid& g, uint32_t id) {
+  Item t;
+  t.dkv = id < g.nk;
+  t.w = t.dkv ? find_work(p, false, TILE, p.kv_heads, g.ktiles, id)
+              : find_work(p, true, TILE, p.heads, g.qtiles, id - g.nk);
+  t.own = t.w.tile * TILE;
+  t.r = Range{0, 0};
+  if (t.w.ok)
+    t.r = t.dkv ? query_tiles<WT>(p, t.w, t.own, min(t.own + TILE, t.w.nk) - 1)
+                : key_tiles<WT>(p, t.w, t.own, min(t.own + TILE, t.w.nq) - 1);
+  t.n = t.r.count * (t.dkv ? p.heads / p.kv_heads : 1);
+  return t;
+}
+
+// ----------------------------------------------------------------- loads
 template <typename T, int DP>
-__device__ __forceinline__ void dkv_item(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                         const CUtensorMap& mdo, const AttnParams& p, int tiles, int qtiles,
-                                         uint32_t item) {
+__device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, uint32_t sb, uint32_t bb, Bars* bar) {
+  volatile int* abort = &bar->abort;
   using S = Smem<DP>;
   constexpr int WT = S::WT, BOX = DP == 64 ? 64 : TILE;      // rows of a walked tile, of a map's box
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
-  if (!swizzle_aligned(sb, p)) return;
-  if (warp == 0) {
-    const Work w = find_work(p, false, TILE, p.kv_heads, tiles, item);
+  const int lane = threadIdx.x & 31;
+  Ring<S::RA> ra;
+  Ring<S::RB> rb;
+  uint32_t edges[2] = {0u, 0u}, own_ph = 1u;                 // the first item finds its places free
+  // The CTA's first item is its own number; the next ones are taken from a
+  // counter (which the statistics kernel sets to 0) while an item is under
+  // way, so that long and short items even out.  Which CTA computes an item
+  // changes nothing in its result.
+  Ring<2> ids;
+  uint32_t id = blockIdx.x, next_id = 0;
+  auto take = [&]() {
+    if (lane == 0) next_id = p.counter != nullptr ? gridDim.x + atomicAdd(p.counter, 1u) : id + gridDim.x;
+  };
+  bool ok = true, waited = false;
+  for (;; id = __shfl_sync(0xffffffffu, next_id, 0)) {
+    ok = ok && wait_warp(BAR(id_empty) + 8 * ids.s, ids.ph ^ 1u, abort, p);
+    if (!ok) break;
     if (lane == 0) {
-      bar->work = w;
-      init_bars(bar, Shape<DP>::CALC);
+      *const_cast<volatile uint32_t*>(&bar->id[ids.s]) = id;
+      mbar_arrive_at(BAR(id_full) + 8 * ids.s);
     }
-  }
-  if (warp == 1) tmem_alloc(&bar->tmem, Shape<DP>::TMEM);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const Work w = bar->work;
-  volatile int* abort = &bar->abort;
-  const uint32_t tmem = bar->tmem;
-  constexpr uint32_t S_COL = 0, DP_COL = WT, DV_COL = 2 * WT, DK_COL = 2 * WT + DP;
-  const int group = p.heads / p.kv_heads;
-  const int j0 = w.tile * TILE;
-  Range r{0, 0};
-  if (w.ok) r = query_tiles<WT>(p, w, j0, min(j0 + TILE, w.nk) - 1);
-  const int n = r.count * group;                   // steps: the group's heads one after another
-
-  if (warp == 0 && n > 0) {
-    // ---------------------------------------------------------- loads
+    ids.next();
+    if (id >= g.total) break;
+    const Item t = find_item<WT>(p, g, id);
+    if (t.n == 0) {
+      if (!waited) pdl_wait();
+      waited = true;
+      take();
+      continue;
+    }
+    const Work& w = t.w;
+    // dk, dv: K and V stay, Q and dO are walked; dq: Q and dO stay, K and V are walked
+    const CUtensorMap* own0 = t.dkv ? g.mk : g.mq;
+    const CUtensorMap* own1 = t.dkv ? g.mv : g.mdo;
+    const CUtensorMap* walk_a = t.dkv ? g.mq : g.mk;
+    const CUtensorMap* walk_b = t.dkv ? g.mdo : g.mv;
+    const int own_row = (t.dkv ? w.k0 : w.q0) + t.own, group = p.heads / p.kv_heads;
+    const int first = t.dkv ? w.q0 : w.k0, len = t.dkv ? w.nq : w.nk;
+    const int h0 = t.dkv ? w.h * group : w.h / group, h1 = t.dkv ? h0 + group : h0 + 1;
+    ok = wait_warp(BAR(own_empty), own_ph, abort, p);
+    if (!ok) break;
     if (lane == 0) {
       mbar_expect_at(BAR(own), S::OWN);
-      load_tile<DP, TILE, BOX>(sb, &mk, BAR(own), w.h, w.k0 + j0, w.b);
+      load_tile<DP, TILE, BOX>(sb, own0, BAR(own), w.h, own_row, w.b);
     }
-    bool first = true;
-    uint32_t edges = 0;
-    int ia = 0, ib = 0;
-    Ring<S::RA> ra;
-    Ring<S::RB> rb;
-    bool ok = true;
-    for (int hq = w.h * group; ok && hq < (w.h + 1) * group; ++hq) {
-      const long long stat = ((static_cast<long long>(w.b) * p.heads + hq) * qtiles + w.qtile) * TILE;
-      for (int i0 = r.first * WT; i0 < (r.first + r.count) * WT; i0 += WT) {
-        const int row = w.q0 + i0, valid = w.nq - i0;
+    bool second = true;                                      // the other own tile is still to come
+    for (int h = h0; ok && h < h1; ++h) {
+      const long long stat = ((static_cast<long long>(w.b) * p.heads + h) * g.qtiles + w.qtile) * TILE;
+      for (int i0 = t.r.first * WT; i0 < (t.r.first + t.r.count) * WT; i0 += WT) {
+        const int row = first + i0, valid = len - i0;
         const bool edge = p.cu_q != nullptr && valid < WT;
         const uint32_t at = sb + S::A_OFF + ra.s * S::T, bt = sb + S::B_OFF + rb.s * S::T;
         const uint32_t fa = BAR(a_full) + 8 * ra.s, fb = BAR(b_full) + 8 * rb.s;
         ok = wait_warp(BAR(a_empty) + 8 * ra.s, ra.ph ^ 1u, abort, p);
         if (!ok) break;
-        if (edge) {
-          ok = load_edge_tile<DP, WT, BOX>(at, &mq, BAR(edge), edges, hq, row, valid, abort, p);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_at(fa);
-        } else if (lane == 0) {
-          mbar_expect_at(fa, S::T);
-          load_tile<DP, WT, BOX>(at, &mq, fa, hq, row, w.b);
+        if (lane == 0) {
+          if (!edge) mbar_expect_at(fa, S::T);
+          else mbar_expect_at(BAR(edge), S::T);
+          load_tile<DP, WT, BOX>(at, walk_a, edge ? BAR(edge) : fa, h, row, w.b);
         }
-        ++ia;
-        ra.next();
-        if (first) {                               // after what the first scores want
-          first = false;
+        if (second) {                                        // after what the first scores want
+          second = false;
+          ok = wait_warp(BAR(own_empty) + 8, own_ph, abort, p);
+          if (!ok) break;
           if (lane == 0) {
             mbar_expect_at(BAR(own) + 8, S::OWN);
-            load_tile<DP, TILE, BOX>(sb + S::OWN, &mv, BAR(own) + 8, w.h, w.k0 + j0, w.b);
+            load_tile<DP, TILE, BOX>(sb + S::OWN, own1, BAR(own) + 8, w.h, own_row, w.b);
           }
-          pdl_wait();                              // the statistics are the previous kernel's
+          if (!waited) pdl_wait();                           // statistics and counter are the previous kernel's
+          waited = true;
+          take();
         }
         ok = wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p);
         if (!ok) break;
+        if (lane == 0) {
+          if (!edge) mbar_expect_at(fb, S::T + (t.dkv ? S::STAT : 0));
+          else mbar_expect_at(BAR(edge) + 8, S::T + (t.dkv ? S::STAT : 0));
+          const uint32_t to = edge ? BAR(edge) + 8 : fb;
+          load_tile<DP, WT, BOX>(bt, walk_b, to, h, row, w.b);
+          if (t.dkv) {
+            const uint32_t st = sb + S::STAT_OFF + rb.s * S::STAT;
+            bulk_load(st, p.stat_lse + stat + i0, WT * 4, to);
+            bulk_load(st + WT * 4, p.stat_delta + stat + i0, WT * 4, to);
+          }
+        }
         if (edge) {
-          ok = load_edge_tile<DP, WT, BOX>(bt, &mdo, BAR(edge), edges, hq, row, valid, abort, p);
+          // a packed sequence ends inside the tile: the next one's rows become zeros, so that a NaN
+          // or an infinity there has no part in a product with a zero probability
+          ok = finish_edge_tile<DP, WT>(at, BAR(edge), edges[0], valid, abort, p);
+          if (ok && lane == 0) mbar_arrive_at(fa);
+          ok = ok && finish_edge_tile<DP, WT>(bt, BAR(edge) + 8, edges[1], valid, abort, p);
+          if (ok && lane == 0) mbar_arrive_at(fb);
           if (!ok) break;
         }
-        if (lane == 0) {
-          const uint32_t st = sb + S::STAT_OFF + rb.s * S::STAT;
-          mbar_expect_at(fb, S::STAT + (edge ? 0 : S::T));
-          bulk_load(st, p.stat_lse + stat + i0, WT * 4, fb);
-          bulk_load(st + WT * 4, p.stat_delta + stat + i0, WT * 4, fb);
-          if (!edge) load_tile<DP, WT, BOX>(bt, &mdo, fb, hq, row, w.b);
-        }
-        ++ib;
+        ra.next();
         rb.next();
       }
     }
-    if (*abort != 0 && lane == 0) {
-      mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
-      if (!first) mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
-      drain_ring<S::RA>(bar->a_full, ia);
-      drain_ring<S::RB>(bar->b_full, ib);
+    own_ph ^= 1u;
+  }
+  // after a wait ran out: a millisecond for copies in flight to land
+  if (*abort != 0 && lane == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
     }
-    __syncwarp();
-  } else if (warp == 1 && n > 0) {
-    // -------------------------------------------------------- products
-    const uint64_t k_d = desc_dim(sb), v_d = desc_dim(sb + S::OWN);
-    Ring<S::RA> ra, na;                            // this step's Q tile, and the next one's
-    Ring<S::RB> rb, nb;
-    auto scores = [&]() {
-      mma_over_dim<T, DP, WT>(tmem + S_COL, k_d, desc_dim(sb + S::A_OFF + na.s * S::T));
-      commit_warp(BAR(s_full));
-      na.next();
-    };
-    auto dprobs = [&]() {
-      mma_over_dim<T, DP, WT>(tmem + DP_COL, v_d, desc_dim(sb + S::B_OFF + nb.s * S::T));
-      commit_warp(BAR(dp_full));
+  }
+  __syncwarp();
+}
+
+// -------------------------------------------------------------- products
+template <typename T, int DP>
+__device__ __forceinline__ void product_role(const AttnParams& p, const Grid& g, uint32_t sb, uint32_t bb,
+                                             uint32_t tmem, Bars* bar) {
+  using S = Smem<DP>;
+  constexpr int WT = S::WT;
+  constexpr uint32_t S_COL = 0, DP_COL = WT;
+  constexpr uint32_t DV_COL = 2 * WT, DK_COL = 2 * WT + DP;          // dk, dv
+  constexpr uint32_t DQ_COL = 3 * WT;                                // dq: dP twice
+  volatile int* abort = &bar->abort;
+  const uint64_t own0 = desc_dim(sb), own1 = desc_dim(sb + S::OWN);
+  Ring<S::RA> ra, na;                        // this step's walked tile, and the next one's
+  Ring<S::RB> rb, nb;
+  Ring<2> buf, next;                         // the two places of dP (dq)
+  uint32_t own_ph = 0, k_ph = 0, s_ph = 0, acc_ph = 1;
+  auto wait_a = [&]() { return wait_warp(BAR(a_full) + 8 * na.s, na.ph, abort, p); };
+  auto wait_b = [&]() { return wait_warp(BAR(b_full) + 8 * nb.s, nb.ph, abort, p); };
+  auto scores = [&](bool last) {
+    mma_over_dim<T, DP, WT>(tmem + S_COL, own0, desc_dim(sb + S::A_OFF + na.s * S::T));
+    commit_warp(BAR(s_full));
+    if (last) commit_warp(BAR(own_empty));
+    na.next();
+  };
+  auto dprobs = [&](uint32_t col, uint32_t full, bool last) {
+    mma_over_dim<T, DP, WT>(tmem + col, own1, desc_dim(sb + S::B_OFF + nb.s * S::T));
+    commit_warp(full);
+    if (last) commit_warp(BAR(own_empty) + 8);
+  };
+  bool ok = true, was_dkv = false;
+  Items items;
+  for (uint32_t id; ok && items.next(bb, bar, g, abort, p, &id);) {
+    const Item t = find_item<WT>(p, g, id);
+    if (t.n == 0) continue;
+    // an item's first products go ahead of the previous item's outputs; its
+    // sums wait for them.  From dk, dv to dq the places differ: wait at once.
+    bool sums_free = false;
+    if (!t.dkv && was_dkv) {
+      ok = wait_warp(BAR(acc_free), acc_ph, abort, p);
+      sums_free = true;
+    }
+    was_dkv = t.dkv;
+    ok = ok && wait_warp(BAR(own), own_ph, abort, p) && wait_a();
+    if (!ok) break;
+    tc_fence_after();
+    scores(t.n == 1);
+    ok = wait_warp(BAR(own) + 8, own_ph, abort, p) && wait_b();
+    if (!ok) break;
+    own_ph ^= 1u;
+    tc_fence_after();
+    uint32_t acc = 0;
+    if (t.dkv) {
+      dprobs(DP_COL, BAR(dpk_full), t.n == 1);
       nb.next();
-    };
-    // a step's tiles are waited for before the probabilities, so that
-    // products follow one another without a wait in between
-    auto wait_a = [&]() { return wait_warp(BAR(a_full) + 8 * na.s, na.ph, abort, p); };
-    auto wait_b = [&]() { return wait_warp(BAR(b_full) + 8 * nb.s, nb.ph, abort, p); };
-    bool ok = wait_warp(BAR(own), 0, abort, p) && wait_a();
-    if (ok) {
-      tc_fence_after();
-      scores();
-      ok = wait_warp(BAR(own) + 8, 0, abort, p) && wait_b();
+      for (int left = t.n - 1; left >= 0; --left, k_ph ^= 1u, acc = 1) {
+        // a step's tiles are waited for before the probabilities, so that
+        // products follow one another without a wait in between
+        ok = (left == 0 || wait_a()) && wait_warp(BAR(p_full), k_ph, abort, p) &&
+             (acc != 0 || wait_warp(BAR(acc_free), acc_ph, abort, p));
+        if (!ok) break;
+        tc_fence_after();
+        mma_over_tokens<T, DP, COLS, WT>(tmem + DV_COL, tmem + S_COL, desc_tokens<WT>(sb + S::B_OFF + rb.s * S::T), acc);
+        commit_warp(BAR(b_empty) + 8 * rb.s);      // dP, issued earlier, has read this dO tile too
+        rb.next();
+        // the next scores overwrite the probabilities: the tensor pipe runs in order
+        if (left > 0) scores(left == 1);
+        ok = (left == 0 || wait_b()) && wait_warp(BAR(dsk_full), k_ph, abort, p);
+        if (!ok) break;
+        tc_fence_after();
+        mma_over_tokens<T, DP, COLS, WT>(tmem + DK_COL, tmem + DP_COL, desc_tokens<WT>(sb + S::A_OFF + ra.s * S::T), acc);
+        commit_warp(BAR(a_empty) + 8 * ra.s);
+        ra.next();
+        if (left > 0) {
+          dprobs(DP_COL, BAR(dpk_full), left == 1);
+          nb.next();
+        }
+      }
+    } else {
+      auto ahead = [&](bool last) {
+        dprobs(DP_COL + next.s * WT, BAR(dp_full) + 8 * next.s, last);
+        commit_warp(BAR(b_empty) + 8 * nb.s);
+        nb.next();
+        rb.next();
+        next.next();
+      };
+      ahead(t.n == 1);
+      for (int left = t.n - 1; left >= 0; --left, s_ph ^= 1u, acc = 1) {
+        // the next tile's scores and dP (over the ds before last, which dq has read: the tensor pipe runs in order)
+        if (left > 0) {
+          ok = wait_a() && wait_b() && wait_warp(BAR(s_free), s_ph, abort, p);
+          if (!ok) break;
+          tc_fence_after();
+          scores(left == 1);
+          ahead(left == 1);
+        }
+        ok = wait_warp(BAR(ds_full) + 8 * buf.s, buf.ph, abort, p) &&
+             (acc != 0 || sums_free || wait_warp(BAR(acc_free), acc_ph, abort, p));
+        if (!ok) break;
+        tc_fence_after();
+        mma_over_tokens<T, DP, COLS, WT>(tmem + DQ_COL, tmem + DP_COL + buf.s * WT,
+                                         desc_tokens<WT>(sb + S::A_OFF + ra.s * S::T), acc);
+        commit_warp(BAR(a_empty) + 8 * ra.s);
+        ra.next();
+        buf.next();
+      }
+      // the last step's scores were read too: their phase is over
     }
-    if (ok) {
-      tc_fence_after();
-      dprobs();
-    }
-    uint32_t ph = 0, acc = 0;
-    for (int left = n - 1; ok && left >= 0; --left, ph ^= 1u, acc = 1) {
-      ok = (left == 0 || wait_a()) && wait_warp(BAR(p_full), ph, abort, p);
-      if (!ok) break;
-      tc_fence_after();
-      mma_over_tokens<T, DP, COLS, WT>(tmem + DV_COL, tmem + S_COL, desc_tokens<WT>(sb + S::B_OFF + rb.s * S::T), acc);
-      commit_warp(BAR(b_empty) + 8 * rb.s);        // dP, issued earlier, has read this dO tile too
-      rb.next();
-      // the next scores overwrite the probabilities: the tensor pipe runs in order
-      if (left > 0) scores();
-      ok = (left == 0 || wait_b()) && wait_warp(BAR(ds_full), ph, abort, p);
-      if (!ok) break;
-      tc_fence_after();
-      mma_over_tokens<T, DP, COLS, WT>(tmem + DK_COL, tmem + DP_COL, desc_tokens<WT>(sb + S::A_OFF + ra.s * S::T), acc);
-      commit_warp(BAR(a_empty) + 8 * ra.s);
-      ra.next();
-      if (left > 0) dprobs();
-    }
+    if (!ok) break;
     commit_warp(BAR(done));
-    if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
-    __syncwarp();
-  } else if (warp >= CTRL_WARPS && w.ok) {
-    // --------------------------------------- probabilities, then outputs
-    const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2, c0 = COLS * part;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const int j = j0 + quad * 32 + (lane >> 2);    // the first of this thread's keys
+    acc_ph ^= 1u;
+  }
+  if (*abort != 0) {
+    // the products in flight end by themselves: a millisecond for them
+    if ((threadIdx.x & 31) == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// --------------------------------------------- probabilities and outputs
+template <typename T, int DP>
+struct Calc {
+  using S = Smem<DP>;
+  static constexpr int WT = S::WT;
+  const AttnParams& p;
+  uint8_t* smem;
+  uint32_t bb, tmem, lanes;
+  volatile int* abort;
+  int quad, part, c0, lane;
+  Ring<S::RB> rb;
+  Ring<2> buf;
+  uint32_t s_ph = 0, k_ph = 0, done_ph = 0;
+
+  // dk and dv.  A warp has 32 keys (TMEM rows) by 32 queries; thread t of it
+  // the keys t / 4 + 8 k, k = 0 .. 3, and the queries 8 j + 2 (t % 4) + {0,
+  // 1}, j = 0 .. 3.  Value (k, j, e) is v[16 (k / 2) + 4 j + 2 (k % 2) + e].
+  // The queries' statistics are columns here: with one row a thread every
+  // thread read all of them, and shared memory's bandwidth, which the
+  // products need, bound the step.
+  __device__ __forceinline__ bool dkv_steps(const Item& t) {
+    constexpr uint32_t ROWS16 = 16u << 16;         // the warp's second 16 TMEM rows
+    const int j = t.own + quad * 32 + (lane >> 2); // the first of this thread's keys
     const int c1 = c0 + 2 * (lane & 3);            // and queries of a tile
     const float c = p.scale * LOG2E;
     const F2 cc = f2_make(c, c);
-    const int off = w.nk - w.nq;
-    const uint32_t s_at = tmem + lanes + S_COL + c0, dp_at = tmem + lanes + DP_COL + c0;
-    constexpr uint32_t ROWS16 = 16u << 16;         // the warp's second 16 TMEM rows
-    Ring<S::RB> rb;
-    uint32_t ph = 0;
-    bool ok = true;
-    int q0 = r.first * WT;
-    const int q_end = (r.first + r.count) * WT;
-    for (int i = 0; i < n; ++i) {
+    const int off = t.w.nk - t.w.nq;
+    const uint32_t s_at = tmem + lanes + c0, dp_at = tmem + lanes + WT + c0;
+    int q0 = t.r.first * WT;
+    const int q_end = (t.r.first + t.r.count) * WT;
+    for (int i = 0; i < t.n; ++i) {
       const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + rb.s * S::STAT) + c1;
-      // queries q0 .. q0 + WT - 1 against keys j0 .. j0 + 127: does everyone see everything?
-      const bool mask = p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + WT - 1 + off - j0 >= p.window));
+      // queries q0 .. q0 + WT - 1 against keys own .. own + 127: does everyone see everything?
+      const bool mask =
+          p.causal && (t.own + TILE - 1 > q0 + off || (p.window > 0 && q0 + WT - 1 + off - t.own >= p.window));
       float v[COLS], d[COLS];
       uint32_t r16[COLS / 2];
-      ok = wait_warp(BAR(b_full) + 8 * rb.s, rb.ph, abort, p) && wait_warp(BAR(s_full), ph, abort, p);
-      if (!ok) break;
+      if (!wait_warp(BAR(b_full) + 8 * rb.s, rb.ph, abort, p) || !wait_warp(BAR(s_full), s_ph, abort, p)) return false;
+      s_ph ^= 1u;
       tc_fence_after();
       tmem_ld_16x32(s_at, v);
       tmem_ld_16x32(s_at + ROWS16, v + 16);
@@ -370,8 +526,8 @@ __device__ __forceinline__ void dkv_item(const CUtensorMap& mq, const CUtensorMa
       tmem_st_16x16(s_at + ROWS16, r16 + 8);
       tmem_st_wait();
       warp_arrive(BAR(p_full));
-      ok = wait_warp(BAR(dp_full), ph, abort, p);
-      if (!ok) break;
+      if (!wait_warp(BAR(dpk_full), k_ph, abort, p)) return false;
+      k_ph ^= 1u;
       tc_fence_after();
       tmem_ld_16x32(dp_at, d);
       tmem_ld_16x32(dp_at + ROWS16, d + 16);
@@ -388,198 +544,33 @@ __device__ __forceinline__ void dkv_item(const CUtensorMap& mq, const CUtensorMa
       tmem_st_16x16(dp_at, r16);
       tmem_st_16x16(dp_at + ROWS16, r16 + 8);
       tmem_st_wait();
-      warp_arrive(BAR(ds_full));
+      warp_arrive(BAR(dsk_full));
       rb.next();
-      ph ^= 1u;
       q0 += WT;
-      if (q0 == q_end) q0 = r.first * WT;          // the group's next head
+      if (q0 == q_end) q0 = t.r.first * WT;        // the group's next head
     }
-    if (ok && n > 0) {
-      ok = wait_warp(BAR(done), 0, abort, p);
-      tc_fence_after();
-    }
-    if (ok) {
-      // dv by the first half of the warps, dk by the others, 64 columns a warp,
-      // through K's and V's places in shared memory
-      const bool is_dv = part < Shape<DP>::PARTS / 2;
-      const int x = part % (Shape<DP>::PARTS / 2), first = j0 + quad * 32;
-      const long long stride = is_dv ? p.dvs : p.dks, t = w.k0 + first;
-      T* out = (is_dv ? static_cast<T*>(p.dv) + w.b * p.dvb + w.h * p.dvh : static_cast<T*>(p.dk) + w.b * p.dkb + w.h * p.dkh) +
-               t * stride + 64 * x;
-      if (n > 0) {
-        store_block<T, 64>(tmem + lanes + (is_dv ? DV_COL : DK_COL) + 64 * x,
-                           sb + (is_dv ? S::OWN : 0) + x * BOX_BYTES, quad * 32, 0, out, stride, w.nk - first,
-                           p.dim - 64 * x, is_dv ? 1.f : p.scale);
-      } else if (first + lane < w.nk) {
-        for (int k = 0; k < 64 && 64 * x + k < p.dim; k += 8)
-          *reinterpret_cast<uint4*>(out + lane * stride + k) = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
+    return true;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, Shape<DP>::TMEM);
-}
 
-// -------------------------------------------------------------------- dq
-template <typename T, int DP>
-__device__ __forceinline__ void dq_item(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                        const CUtensorMap& mdo, const AttnParams& p, int tiles, uint32_t item) {
-  using S = Smem<DP>;
-  constexpr int WT = S::WT, BOX = DP == 64 ? 64 : TILE;      // rows of a walked tile, of a map's box
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
-  if (!swizzle_aligned(sb, p)) return;
-  if (warp == 0) {
-    const Work w = find_work(p, true, TILE, p.heads, tiles, item);
-    if (lane == 0) {
-      bar->work = w;
-      init_bars(bar, Shape<DP>::CALC);
-    }
-  }
-  if (warp == 1) tmem_alloc(&bar->tmem, Shape<DP>::TMEM);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const Work w = bar->work;
-  volatile int* abort = &bar->abort;
-  const uint32_t tmem = bar->tmem;
-  // dP is kept twice, so that the next tile's products need not wait for this tile's ds
-  constexpr uint32_t S_COL = 0, DP_COL = WT, DQ_COL = 3 * WT;
-  const int hk = w.h / (p.heads / p.kv_heads);
-  const int i0 = w.tile * TILE;
-  Range r{0, 0};
-  if (w.ok) r = key_tiles<WT>(p, w, i0, min(i0 + TILE, w.nq) - 1);
-  const int n = r.count;
-
-  if (warp == 0 && n > 0) {
-    // ---------------------------------------------------------- loads
-    if (lane == 0) {
-      mbar_expect_at(BAR(own), S::OWN);
-      load_tile<DP, TILE, BOX>(sb, &mq, BAR(own), w.h, w.q0 + i0, w.b);
-    }
-    bool first = true;
-    uint32_t edges = 0;
-    int ia = 0, ib = 0;
-    Ring<S::RA> ra;
-    Ring<S::RB> rb;
-    for (int j = r.first * WT; j < (r.first + r.count) * WT; j += WT) {
-      const int row = w.k0 + j, valid = w.nk - j;
-      const bool edge = p.cu_q != nullptr && valid < WT;
-      const uint32_t at = sb + S::A_OFF + ra.s * S::T, bt = sb + S::B_OFF + rb.s * S::T;
-      const uint32_t fa = BAR(a_full) + 8 * ra.s, fb = BAR(b_full) + 8 * rb.s;
-      if (!wait_warp(BAR(a_empty) + 8 * ra.s, ra.ph ^ 1u, abort, p)) break;
-      if (edge) {
-        if (!load_edge_tile<DP, WT, BOX>(at, &mk, BAR(edge), edges, hk, row, valid, abort, p)) break;
-        if (lane == 0) mbar_arrive_at(fa);
-      } else if (lane == 0) {
-        mbar_expect_at(fa, S::T);
-        load_tile<DP, WT, BOX>(at, &mk, fa, hk, row, w.b);
-      }
-      ++ia;
-      ra.next();
-      if (first) {                                 // after what the first scores want
-        first = false;
-        if (lane == 0) {
-          mbar_expect_at(BAR(own) + 8, S::OWN);
-          load_tile<DP, TILE, BOX>(sb + S::OWN, &mdo, BAR(own) + 8, w.h, w.q0 + i0, w.b);
-        }
-      }
-      if (!wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p)) break;
-      if (edge) {
-        if (!load_edge_tile<DP, WT, BOX>(bt, &mv, BAR(edge), edges, hk, row, valid, abort, p)) break;
-        if (lane == 0) mbar_arrive_at(fb);
-      } else if (lane == 0) {
-        mbar_expect_at(fb, S::T);
-        load_tile<DP, WT, BOX>(bt, &mv, fb, hk, row, w.b);
-      }
-      ++ib;
-      rb.next();
-    }
-    if (*abort != 0 && lane == 0) {
-      mbar_wait_bounded(&bar->own[0], 0, nullptr, DRAIN_NS);
-      if (!first) mbar_wait_bounded(&bar->own[1], 0, nullptr, DRAIN_NS);
-      drain_ring<S::RA>(bar->a_full, ia);
-      drain_ring<S::RB>(bar->b_full, ib);
-    }
-    __syncwarp();
-  } else if (warp == 1 && n > 0) {
-    // -------------------------------------------------------- products
-    const uint64_t q_d = desc_dim(sb), do_d = desc_dim(sb + S::OWN);
-    Ring<S::RA> ra, na;                            // this step's K tile, and the next one's
-    Ring<S::RB> nb;
-    Ring<2> buf, next;                             // the two places of dP
-    auto scores = [&]() {
-      mma_over_dim<T, DP, WT>(tmem + S_COL, q_d, desc_dim(sb + S::A_OFF + na.s * S::T));
-      commit_warp(BAR(s_full));
-      na.next();
-    };
-    auto dprobs = [&]() {
-      mma_over_dim<T, DP, WT>(tmem + DP_COL + next.s * WT, do_d, desc_dim(sb + S::B_OFF + nb.s * S::T));
-      commit_warp(BAR(dp_full) + 8 * next.s);
-      commit_warp(BAR(b_empty) + 8 * nb.s);
-      nb.next();
-      next.next();
-    };
-    auto wait_a = [&]() { return wait_warp(BAR(a_full) + 8 * na.s, na.ph, abort, p); };
-    auto wait_b = [&]() { return wait_warp(BAR(b_full) + 8 * nb.s, nb.ph, abort, p); };
-    bool ok = wait_warp(BAR(own), 0, abort, p) && wait_a();
-    if (ok) {
-      tc_fence_after();
-      scores();
-      ok = wait_warp(BAR(own) + 8, 0, abort, p) && wait_b();
-    }
-    if (ok) {
-      tc_fence_after();
-      dprobs();
-    }
-    uint32_t ph = 0, acc = 0;
-    for (int left = n - 1; ok && left >= 0; --left, ph ^= 1u, acc = 1) {
-      // the next tile's scores and dP (over the ds before last, which dq has read: the tensor pipe runs in order)
-      if (left > 0) {
-        ok = wait_a() && wait_b() && wait_warp(BAR(s_free), ph, abort, p);
-        if (!ok) break;
-        tc_fence_after();
-        scores();
-        dprobs();
-      }
-      ok = wait_warp(BAR(ds_full) + 8 * buf.s, buf.ph, abort, p);
-      if (!ok) break;
-      tc_fence_after();
-      mma_over_tokens<T, DP, COLS, WT>(tmem + DQ_COL, tmem + DP_COL + buf.s * WT,
-                                       desc_tokens<WT>(sb + S::A_OFF + ra.s * S::T), acc);
-      commit_warp(BAR(a_empty) + 8 * ra.s);
-      ra.next();
-      buf.next();
-    }
-    commit_warp(BAR(done));
-    if (!ok && lane == 0) mbar_wait_bounded(&bar->done, 0, nullptr, DRAIN_NS);
-    __syncwarp();
-  } else if (warp >= CTRL_WARPS && w.ok) {
-    // --------------------------------------- probabilities, then outputs
-    const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2, c0 = COLS * part;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const int q = i0 + quad * 32 + lane;           // this thread's query
+  // dq: one query a thread, 32 keys of it
+  __device__ __forceinline__ bool dq_steps(const Item& t, int qtiles) {
+    const int q = t.own + quad * 32 + lane;
     const float c = p.scale * LOG2E;
-    const int off = w.nk - w.nq;
-    const long long at = ((static_cast<long long>(w.b) * p.heads + w.h) * tiles + w.qtile + w.tile) * TILE + quad * 32 + lane;
+    const int off = t.w.nk - t.w.nq;
+    const long long at =
+        ((static_cast<long long>(t.w.b) * p.heads + t.w.h) * qtiles + t.w.qtile + t.w.tile) * TILE + quad * 32 + lane;
     pdl_wait();                                    // the statistics are the previous kernel's
-    const float lse = n > 0 ? p.stat_lse[at] : 0.f, delta = n > 0 ? p.stat_delta[at] : 0.f;
+    const float lse = p.stat_lse[at], delta = p.stat_delta[at];
     const F2 cc = f2_make(c, c), ll = f2_make(lse, lse), dd = f2_make(delta, delta);
-    Ring<2> buf;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int j0 = r.first * WT; j0 < (r.first + r.count) * WT; j0 += WT) {
-      const bool mask = j0 + WT > w.nk ||
-                        (p.causal && (j0 + WT - 1 > i0 + off || (p.window > 0 && i0 + TILE - 1 + off - j0 >= p.window)));
-      float v[COLS];
-      ok = wait_warp(BAR(s_full), ph, abort, p);
-      if (!ok) break;
+    for (int j0 = t.r.first * WT; j0 < (t.r.first + t.r.count) * WT; j0 += WT) {
+      const bool mask =
+          j0 + WT > t.w.nk ||
+          (p.causal && (j0 + WT - 1 > t.own + off || (p.window > 0 && t.own + TILE - 1 + off - j0 >= p.window)));
+      float v[COLS], d[COLS];
+      if (!wait_warp(BAR(s_full), s_ph, abort, p)) return false;
+      s_ph ^= 1u;
       tc_fence_after();
-      tmem_ld32(tmem + lanes + S_COL + c0, v);
+      tmem_ld32(tmem + lanes + c0, v);
       tmem_ld_wait();
       warp_arrive(BAR(s_free));
 #pragma unroll
@@ -590,7 +581,7 @@ __device__ __forceinline__ void dq_item(const CUtensorMap& mq, const CUtensorMap
       }
       if (mask) {
         // keys (columns) [lo, hi) are seen by query q
-        int lo = 0, hi = w.nk - j0 - c0;
+        int lo = 0, hi = t.w.nk - j0 - c0;
         if (p.causal) {
           hi = min(hi, q + off + 1 - j0 - c0);
           if (p.window > 0) lo = q + off - p.window + 1 - j0 - c0;
@@ -599,11 +590,9 @@ __device__ __forceinline__ void dq_item(const CUtensorMap& mq, const CUtensorMap
         for (int k = 0; k < COLS; ++k)
           if (k < lo || k >= hi) v[k] = 0.f;
       }
-      ok = wait_warp(BAR(dp_full) + 8 * buf.s, buf.ph, abort, p);
-      if (!ok) break;
+      if (!wait_warp(BAR(dp_full) + 8 * buf.s, buf.ph, abort, p)) return false;
       tc_fence_after();
-      const uint32_t dp = tmem + lanes + DP_COL + buf.s * WT + c0;
-      float d[COLS];
+      const uint32_t dp = tmem + lanes + WT + buf.s * WT + c0;
       tmem_ld32(dp, d);
       tmem_ld_wait();
 #pragma unroll
@@ -615,23 +604,95 @@ __device__ __forceinline__ void dq_item(const CUtensorMap& mq, const CUtensorMap
       store_rounded<T, COLS / 2>(dp, v);
       warp_arrive(BAR(ds_full) + 8 * buf.s);
       buf.next();
-      ph ^= 1u;
     }
-    if (ok && n > 0) {
-      ok = wait_warp(BAR(done), 0, abort, p);
-      tc_fence_after();
+    return true;
+  }
+
+  // The sums of an item, 64 columns a warp (dk, dv) or 32 (dq), to memory.
+  __device__ __forceinline__ bool outputs(const Item& t) {
+    const Work& w = t.w;
+    const int first = t.own + quad * 32;
+    T* out;
+    long long stride;
+    int col, rows;
+    uint32_t at;
+    float mul = p.scale;
+    if (t.dkv) {
+      // dv by the first half of the warps, dk by the others
+      const bool is_dv = part < Shape<DP>::PARTS / 2;
+      col = part % (Shape<DP>::PARTS / 2) * 64;
+      stride = is_dv ? p.dvs : p.dks;
+      out = is_dv ? static_cast<T*>(p.dv) + w.b * p.dvb + w.h * p.dvh : static_cast<T*>(p.dk) + w.b * p.dkb + w.h * p.dkh;
+      out += (w.k0 + first) * stride + col;
+      rows = w.nk - first;
+      at = tmem + lanes + 2 * WT + (is_dv ? 0 : DP) + col;
+      if (is_dv) mul = 1.f;
+    } else {
+      col = c0;
+      stride = p.dqs;
+      out = static_cast<T*>(p.dq) + w.b * p.dqb + w.h * p.dqh + (w.q0 + first) * stride + col;
+      rows = w.nq - first;
+      at = tmem + lanes + 3 * WT + col;
     }
-    if (ok) {
-      // 32 columns a warp, through Q's place in shared memory
-      const int first = i0 + quad * 32;
-      T* out = static_cast<T*>(p.dq) + w.b * p.dqb + static_cast<long long>(w.q0 + first) * p.dqs + w.h * p.dqh + c0;
-      if (n > 0) {
-        store_block<T, COLS>(tmem + lanes + DQ_COL + c0, sb + c0 / 64 * BOX_BYTES, quad * 32, c0 % 64 / 8, out, p.dqs,
-                             w.nq - first, p.dim - c0, p.scale);
-      } else if (q < w.nq) {
-        for (int k = 0; k < COLS && c0 + k < p.dim; k += 8)
-          *reinterpret_cast<uint4*>(out + lane * p.dqs + k) = make_uint4(0u, 0u, 0u, 0u);
-      }
+    if (t.n == 0) {
+      const int width = t.dkv ? 64 : COLS;
+      if (lane < rows)
+        for (int k = 0; k < width && col + k < p.dim; k += 8)
+          *reinterpret_cast<uint4*>(out + lane * stride + k) = make_uint4(0u, 0u, 0u, 0u);
+      return true;
+    }
+    if (!wait_warp(BAR(done), done_ph, abort, p)) return false;
+    done_ph ^= 1u;
+    tc_fence_after();
+    store_rows<T>(at, out, stride, rows, p.dim - col, mul);
+    if (t.dkv) store_rows<T>(at + 32, out + 32, stride, rows, p.dim - col - 32, mul);
+    warp_arrive(BAR(acc_free));
+    return true;
+  }
+};
+
+// Items [0, nk) are key tiles (dk, dv), the rest query tiles (dq), each kind
+// from its longest to its shortest.  CTAs stay
+// on their SMs and take item after item: an item's tiles are loaded, and its
+// first products formed, while the previous one ends.  (A CTA an item spent
+// 5 us on start, first loads and outputs, beside about 1.2 us a step.)
+template <typename T, int DP>
+__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                    const AttnParams p, uint32_t nk, uint32_t total, int ktiles, int qtiles) {
+  using S = Smem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
+  if (!swizzle_aligned(sb, p)) return;
+  const Grid g{&mq, &mk, &mv, &mdo, nk, total, ktiles, qtiles};
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&mq);
+    tma_prefetch_map(&mk);
+    tma_prefetch_map(&mv);
+    tma_prefetch_map(&mdo);
+    init_bars(bar, Shape<DP>::CALC);
+  }
+  if (warp == 1) tmem_alloc(&bar->tmem, Shape<DP>::TMEM);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  if (warp == 0) {
+    load_role<T, DP>(p, g, sb, bb, bar);
+  } else if (warp == 1) {
+    product_role<T, DP>(p, g, sb, bb, tmem, bar);
+  } else {
+    const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2;
+    Calc<T, DP> calc{p, smem, bb, tmem, static_cast<uint32_t>(quad * 32) << 16, &bar->abort, quad, part, COLS * part, lane};
+    Items items;
+    for (uint32_t id; items.next(bb, bar, g, &bar->abort, p, &id);) {
+      const Item t = find_item<S::WT>(p, g, id);
+      if (!t.w.ok) continue;
+      const bool ok = t.n == 0 || (t.dkv ? calc.dkv_steps(t) : calc.dq_steps(t, qtiles));
+      if (!ok || !calc.outputs(t)) break;
     }
   }
   tc_fence_before();
@@ -640,31 +701,8 @@ __device__ __forceinline__ void dq_item(const CUtensorMap& mq, const CUtensorMap
   if (warp == 1) tmem_dealloc(tmem, Shape<DP>::TMEM);
 }
 
-// Items [0, nk) are key tiles (dk, dv), the rest query tiles (dq): one launch,
-// so that the short items of one kind fill the SMs beside the last long ones
-// of the other.
 template <typename T, int DP>
-__global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
-                    const AttnParams p, uint32_t nk, int ktiles, int qtiles) {
-  if (threadIdx.x < 32) {
-    if ((threadIdx.x & 31) == 0) {
-      tma_prefetch_map(&mq);
-      tma_prefetch_map(&mk);
-      tma_prefetch_map(&mv);
-      tma_prefetch_map(&mdo);
-    }
-    __syncwarp();
-  }
-  if (blockIdx.x < nk)
-    dkv_item<T, DP>(mq, mk, mv, mdo, p, ktiles, qtiles, blockIdx.x);
-  else
-    dq_item<T, DP>(mq, mk, mv, mdo, p, qtiles, blockIdx.x - nk);
-}
-
-template <typename T, int DP>
-cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s) {
+cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, bool prep, int sms, cudaStream_t s) {
   const bool packed = p.cu_q != nullptr;
   const long long seqs = packed ? 1 : p.batch;
   const long long qt = p.qtiles, kt = tile_bound(p.sk, TILE, p.batch, packed);
@@ -678,21 +716,24 @@ cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, bool prep, cu
   static std::atomic<unsigned long long> done;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
   if (e != cudaSuccess) return e;
-  // its prologue overlaps the statistics kernel (the wait for them is in the items); without that one, no overlap
-  e = launch_k(p.sq > 0, kern, dim3(static_cast<unsigned>(nq + nk)), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0],
-               m[1], m[2], m[3], p, static_cast<uint32_t>(nk), static_cast<int>(kt), static_cast<int>(qt));
+  const long long slots = static_cast<long long>(sms) * Shape<DP>::CTAS;
+  const unsigned grid = static_cast<unsigned>(nq + nk < slots ? nq + nk : slots);
+  // its prologue overlaps the statistics kernel (the wait for them is in the roles); without that one, no overlap
+  e = launch_k(p.sq > 0, kern, dim3(grid), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0], m[1], m[2], m[3], p,
+               static_cast<uint32_t>(nk), static_cast<uint32_t>(nq + nk), static_cast<int>(kt), static_cast<int>(qt));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_type(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s) {
-  return p.dim <= 64 ? launch_dims<T, 64>(p, m, prep, s) : launch_dims<T, 128>(p, m, prep, s);
+cudaError_t launch_type(const AttnParams& p, const CUtensorMap* m, bool prep, int sms, cudaStream_t s) {
+  return p.dim <= 64 ? launch_dims<T, 64>(p, m, prep, sms, s) : launch_dims<T, 128>(p, m, prep, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, cudaStream_t s) {
-  return p.dtype == DT_BF16 ? launch_type<__nv_bfloat16>(p, m, prep, s) : launch_type<__half>(p, m, prep, s);
+cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, int sms, cudaStream_t s) {
+  return p.dtype == DT_BF16 ? launch_type<__nv_bfloat16>(p, m, prep, sms, s)
+                            : launch_type<__half>(p, m, prep, sms, s);
 }
 
 }  // namespace muon

@@ -142,12 +142,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         ++ik;
         if (i >= S::RV && !wait_warp(BAR(v_empty) + 8 * (sv), (i / S::RV - 1) & 1, abort, p)) break;
-        if (p.cu_q != nullptr && valid < TILE) {
-          if (!load_edge_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, BAR(edge), edges, hk, row, valid, abort, p)) break;
-          if (lane == 0) mbar_arrive_at(BAR(v_full) + 8 * (sv));
-        } else if (lane == 0) {
-          mbar_expect_at(BAR(v_full) + 8 * (sv), S::T);
-          load_tile<DP>(sb + S::V_OFF + sv * S::T, &mv, BAR(v_full) + 8 * (sv), hk, row, w.b);
+        const bool edge = p.cu_q != nullptr && valid < TILE;
+        const uint32_t vt = sb + S::V_OFF + sv * S::T, fv = BAR(v_full) + 8 * sv;
+        if (lane == 0) {
+          mbar_expect_at(edge ? BAR(edge) : fv, S::T);
+          load_tile<DP>(vt, &mv, edge ? BAR(edge) : fv, hk, row, w.b);
+        }
+        if (edge) {
+          if (!finish_edge_tile<DP>(vt, BAR(edge), edges, valid, abort, p)) break;
+          if (lane == 0) mbar_arrive_at(fv);
         }
         ++iv;
       }

@@ -55,11 +55,14 @@ muon_status_t check_act8(muon_handle_t h, const uint8_t* codes, int64_t ldc, con
   return MUON_OK;
 }
 
-uint64_t attn_workspace(const muon_attention_t& a) {
+// Two statistics of every query, by tiles of 128, then a counter.
+uint64_t attn_stat_bytes(const muon_attention_t& a) {
   const bool packed = a.cu_seqlens_q != nullptr;
   const uint64_t b = packed ? 1 : static_cast<uint64_t>(a.batch);
   return 2 * 512 * b * static_cast<uint64_t>(a.heads) * static_cast<uint64_t>(attn_qtiles(a.sq, a.batch, packed));
 }
+
+uint64_t attn_workspace(const muon_attention_t& a) { return a.sq > 0 ? attn_stat_bytes(a) + 256 : 0; }
 
 muon_status_t check_attention(muon_handle_t h, const muon_attention_t* a) {
   MUON_CHECK(a != nullptr, "a is NULL");
@@ -339,7 +342,8 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
     p.dk = a->dk;
     p.dv = a->dv;
     p.stat_lse = static_cast<float*>(workspace);
-    p.stat_delta = p.stat_lse + attn_workspace(*a) / 8;
+    p.stat_delta = p.stat_lse + attn_stat_bytes(*a) / 8;
+    p.counter = a->sq > 0 ? reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + attn_stat_bytes(*a)) : nullptr;
     CUtensorMap m[4] = {};
     const uint32_t tokens = a->dim <= 64 ? 64 : 128;
     bool ok = true;
@@ -351,8 +355,8 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
            attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype, tokens);
     if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
-    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, true, stream), "attention statistics launch");
-    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, false, stream), "attention backward launch");
+    if (a->sq > 0) MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, true, h->num_sms, stream), "attention statistics launch");
+    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_bwd(p, m, false, h->num_sms, stream), "attention backward launch");
     return MUON_OK;
   });
 }
