@@ -3,9 +3,10 @@
 //
 // A tile is 64 or 128 rows (tokens of one head) by DP = 64 or 128 columns of
 // 16-bit elements, in boxes of 64 columns (128-byte rows, 128-byte swizzle),
-// as TMA writes them from a 4-D map {dim, head, token, batch}.  Columns past `dim` and, in the batched form, rows past the
-// sequence are filled with zeros.  One such tile serves both as a K-major
-// operand (the product runs over dim) and as an MN-major one (over tokens).
+// as TMA writes them from a 4-D map {dim, head, token, batch}.  Columns past
+// `dim` and, in the batched form, rows past the sequence are filled with
+// zeros.  One such tile serves both as a K-major operand (the product runs
+// over dim) and as an MN-major one (over tokens).
 #pragma once
 
 #include "common.cuh"
@@ -37,11 +38,11 @@ struct Work {
 };
 
 // Packed sequences: finds the sequence that tile `tile` (of `rows` rows) of
-// the query (by_q) or key axis belongs to.  Every sequence has
-// ceil(length / rows) tiles; the
-// tokens before the first offset and after the last form sequences of their
-// own that see nothing.  Offsets are device data and not trusted: they are
-// clamped to the axis and to the largest before them.  All 32 lanes call it.
+// the query (by_q) or key axis belongs to.  Every sequence has ceil(length /
+// rows) tiles; the tokens before the first offset and after the last form
+// sequences of their own that see nothing.  Offsets are device data and not
+// trusted: they are clamped to the axis and to the largest before them.  All
+// 32 lanes call it.
 __device__ __forceinline__ Work find_packed(const AttnParams& p, bool by_q, int rows, int tile) {
   const int lane = threadIdx.x & 31;
   const int n = p.batch;
@@ -105,9 +106,9 @@ __device__ __forceinline__ Work find_packed(const AttnParams& p, bool by_q, int 
   return w;
 }
 
-// Work item `item` of a grid of tiles of `rows` rows x (heads x batch), heads fastest.  The
-// longest items of a causal grid come first: the key tiles in their order,
-// the query tiles (`tiles` of them at most) from the last.
+// Work item `item` of a grid of tiles of `rows` rows x (heads x batch), heads
+// fastest.  The longest items of a causal grid come first: the key tiles in
+// their order, the query tiles (`tiles` of them at most) from the last.
 __device__ __forceinline__ Work find_work(const AttnParams& p, bool by_q, int rows, int heads, int tiles,
                                           uint32_t item) {
   const uint32_t hb = static_cast<uint32_t>(heads) * (p.cu_q != nullptr ? 1u : static_cast<uint32_t>(p.batch));
@@ -135,8 +136,8 @@ struct Range {
   int first, count;
 };
 
-// Key tiles of ROWS rows that the queries [i0, i1] of a sequence see (count
-// 0: none).
+// Key tiles of ROWS rows that the queries [i0, i1] of a sequence see (count 0:
+// none).
 template <int ROWS = TILE>
 __device__ __forceinline__ Range key_tiles(const AttnParams& p, const Work& w, int i0, int i1) {
   int beg = 0, end = w.nk;
@@ -182,6 +183,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t a, uint32_t parity, volatile 
     }
   }
 }
+
 // The swizzled tiles need shared memory that starts on a 1 KB boundary, which
 // a kernel without static shared memory gets.
 __device__ __forceinline__ bool swizzle_aligned(uint32_t base, const AttnParams& p) {
@@ -386,17 +388,17 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// NC = 32 or 64 fp32 TMEM columns of this warp's 32 rows, times `mul`, rounded
-// to T, out to `dst` (row 0, column 0; `rows` rows and `cols` columns of it
-// exist).  By way of the warp's rows of a box [128][64] in shared memory that
-// nothing reads any more, so that lanes next to each other write one row:
-// a row a lane took 1.7 us for a 128 x 64 tile.
-template <typename T, int NC>
-__device__ __forceinline__ void store_block(uint32_t taddr, uint32_t box, int r0, int chunk0, T* dst, long long stride,
-                                            int rows, int cols, float mul) {
+// 64 fp32 TMEM columns of this warp's 32 rows, times `mul`, rounded to T, out
+// to `dst` (row 0, column 0; `rows` rows and `cols` columns of it exist).  By
+// way of the warp's rows, from r0, of a box [128][64] in shared memory that
+// nothing reads any more, so that lanes next to each other write one row: a
+// row a lane took 1.7 us for a 128 x 64 tile.
+template <typename T>
+__device__ __forceinline__ void store_block(uint32_t taddr, uint32_t box, int r0, T* dst, long long stride, int rows,
+                                            int cols, float mul) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int c = 0; c < NC; c += 32) {
+  for (int c = 0; c < 64; c += 32) {
     float v[32];
     tmem_ld32(taddr + c, v);
     tmem_ld_wait();
@@ -405,17 +407,16 @@ __device__ __forceinline__ void store_block(uint32_t taddr, uint32_t box, int r0
       uint32_t r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[e] = pack2<T>(v[8 * q + 2 * e] * mul, v[8 * q + 2 * e + 1] * mul);
-      sts16(box + (r0 + lane) * 128 + (((chunk0 + c / 8 + q) ^ (lane & 7)) << 4), r);
+      sts16(box + (r0 + lane) * 128 + (((c / 8 + q) ^ (lane & 7)) << 4), r);
     }
   }
   __syncwarp();
-  constexpr int LPR = NC / 8;                    // lanes of a row
-  const int q = lane % LPR;
+  const int q = lane & 7;
 #pragma unroll
-  for (int i = 0; i < LPR; ++i) {
-    const int r = i * (32 / LPR) + lane / LPR;
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
     if (r < rows && 8 * q < cols)
-      *reinterpret_cast<uint4*>(dst + r * stride + 8 * q) = lds16(box + (r0 + r) * 128 + (((chunk0 + q) ^ (r & 7)) << 4));
+      *reinterpret_cast<uint4*>(dst + r * stride + 8 * q) = lds16(box + (r0 + r) * 128 + ((q ^ (r & 7)) << 4));
   }
   __syncwarp();
 }

@@ -4,22 +4,31 @@
 //   dv_j = sum_i p_ij do_i,   ds_ij = p_ij (do_i . v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
 //
-// attn_prep_kernel writes lse_i log2(e) and delta_i, tile by tile (HBM-bound:
+// attn_prep_kernel writes -lse_i log2(e) and -delta_i, tile by tile (HBM-bound:
 // it reads o and do).  attn_bwd_kernel has two kinds of items.  One owns a
 // tile of 128 keys, walks the query tiles that see them (of every query head
 // that shares the key head) and keeps dk and dv in TMEM; the other owns a
-// tile of 128 queries, walks its key tiles and keeps dq in TMEM.  No value is added
-// by atomics, so results do not change from call to call; the price is that
-// scores and dP are formed twice, seven products a tile pair instead of five.
+// tile of 128 queries, walks its key tiles and keeps dq in TMEM.  No value is
+// added by atomics, so results do not change from call to call; the price is
+// that scores and dP are formed twice, seven products a tile pair, not five.
 //
-// Both are bound by the tensor cores and the exponentials: per tile pair of
-// 128 x 128 with dim 128 the products take 1024 (768) cycles of the tensor
-// pipe at its full rate.  Warp-specialised: warp 0 loads tiles by TMA,
-// warp 1 issues every tcgen05.mma, the other warps turn
-// scores into p and ds.  p and ds never leave the SM: each warp writes its 16
-// bit values over the fp32 scores (or dP) that it read, and the next product
-// takes them from TMEM as its A operand.  Scores are transposed in the dkv
-// kernel (rows are keys), so that p and ds are that operand as they stand.
+// Warp-specialised: warp 0 loads tiles by TMA, warp 1 issues every
+// tcgen05.mma, the other warps turn scores into p and ds.  p and ds never
+// leave the SM: each warp writes its 16-bit values over the fp32 scores (or
+// dP) that it read, and the next product takes them from TMEM as its A
+// operand.  For dk and dv the scores are transposed (rows are keys), so that
+// p and ds are that operand as they stand.
+//
+// With dim 128 the products bind: 2048 (dk, dv) and 1536 (dq) cycles of the
+// tensor pipe for 128 x 128 pairs, measured 2600 to 2900 and 2030, as shared
+// memory, from which N = 128 products take 128 bytes a cycle, is as busy.
+// 8192 causal tokens of 32 heads (8 of keys), bf16: 1.09 ms, 1270 TFLOP/s of
+// the five products that the gradient needs, 1770 of the seven.  With short
+// sequences and dim 64 the way of a tile through the element-wise warps
+// binds: 8 x 1024 causal tokens of 12 heads take 74 us, 440 TFLOP/s of five,
+// with 46% of the issue slots and 30% of the tensor pipe used.  (p and ds of
+// a tile in one go, with half the barriers, took 82 us: no product then runs
+// beside them.)
 #include <cstddef>
 
 #include "common.cuh"
@@ -434,7 +443,6 @@ __device__ __forceinline__ void product_role(const AttnParams& p, const Grid& g,
         ra.next();
         buf.next();
       }
-      // the last step's scores were read too: their phase is over
     }
     if (!ok) break;
     commit_warp(BAR(done));
@@ -652,10 +660,10 @@ struct Calc {
 };
 
 // Items [0, nk) are key tiles (dk, dv), the rest query tiles (dq), each kind
-// from its longest to its shortest.  CTAs stay
-// on their SMs and take item after item: an item's tiles are loaded, and its
-// first products formed, while the previous one ends.  (A CTA an item spent
-// 5 us on start, first loads and outputs, beside about 1.2 us a step.)
+// from its longest to its shortest.  CTAs stay on their SMs and take item after
+// item: an item's tiles are loaded, and its first products formed, while the
+// previous one ends.  (A CTA an item spent 5 us on start, first loads and
+// outputs, beside about 1.2 us a step.)
 template <typename T, int DP>
 __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,

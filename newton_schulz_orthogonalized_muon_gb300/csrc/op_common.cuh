@@ -151,26 +151,6 @@ __device__ __forceinline__ void sts16(uint32_t addr, const uint32_t* r) {
                : "memory");
 }
 
-// 128 values of `add` from (o, n), zeros outside it: what a running sum
-// starts from, read while the first products run.
-__device__ __forceinline__ void load_add(const WgradParams& p, int o, int n, float* v) {
-  const bool any = p.add != nullptr && p.splits == 1 && o < p.out;
-  const long long at = static_cast<long long>(o) * p.ldadd + n;
-#pragma unroll
-  for (int k = 0; k < 128; k += 8) {
-    if (any && p.vec_add && n + k + 8 <= p.cols) {
-      if (p.odtype == DT_F32) {
-        unpack16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + at + k), v + k);
-        unpack16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + at + k + 4), v + k + 4);
-      } else {
-        unpack16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.add) + at + k), v + k);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[k + e] = any && n + k + e < p.cols ? load_f32(p.add, at + k + e, p.odtype) : 0.f;
-    }
-  }
-}
 // Untiled copy: both addresses and the size are multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),

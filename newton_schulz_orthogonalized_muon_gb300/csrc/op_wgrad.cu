@@ -172,6 +172,27 @@ __device__ __forceinline__ void store4(const WgradParams& p, float* part, int o,
     if (n + k < p.cols) store_from_f32(p.dw, at + k, p.odtype, f[k]);
 }
 
+// 128 values of `add` from (o, n), zeros outside it: what a running sum
+// starts from, read while the first products run.
+__device__ __forceinline__ void load_add(const WgradParams& p, int o, int n, float* v) {
+  const bool any = p.add != nullptr && p.splits == 1 && o < p.out;
+  const long long at = static_cast<long long>(o) * p.ldadd + n;
+#pragma unroll
+  for (int k = 0; k < 128; k += 8) {
+    if (any && p.vec_add && n + k + 8 <= p.cols) {
+      if (p.odtype == DT_F32) {
+        unpack16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + at + k), v + k);
+        unpack16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + at + k + 4), v + k + 4);
+      } else {
+        unpack16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.add) + at + k), v + k);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k + e] = any && n + k + e < p.cols ? load_f32(p.add, at + k + e, p.odtype) : 0.f;
+    }
+  }
+}
+
 struct Item {
   int o, n;              // tile indices
   int k0, k1;            // steps [k0, k1)
