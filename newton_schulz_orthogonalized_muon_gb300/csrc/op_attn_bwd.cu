@@ -122,13 +122,27 @@ struct Smem {
   static constexpr int T = OWN / TILE * WT;       // a walked one
   static constexpr int RA = 3;
   static constexpr int RB = DP == 128 ? 2 : 3;
-  static constexpr int STAT = 2 * WT * 4;         // lse and delta of one walked query tile
+  static constexpr int STAT = 2 * TILE * 4;       // lse and delta of a walked query tile, or of the one that stays
   static constexpr int A_OFF = 2 * OWN;
   static constexpr int B_OFF = A_OFF + RA * T;
   static constexpr int STAT_OFF = B_OFF + RB * T;
   static constexpr int BAR_OFF = STAT_OFF + RB * STAT;
-  static constexpr int BYTES = BAR_OFF + 320;
+  static constexpr int BYTES = BAR_OFF + 448;
   static_assert(BYTES * Shape<DP>::CTAS <= 232448 - 1024 * (Shape<DP>::CTAS - 1), "shared memory");
+};
+
+// One item.  The loading warp finds it and announces it: where it lies costs
+// several divisions and, with packed sequences, a walk through their offsets,
+// 1200 cycles that no other warp spends.
+enum Kind : int { DQ = 0, DKV = 1, NO_MORE = 2 };
+struct Item {
+  int kind;
+  int n;                     // steps
+  int own;                   // first row of the tile that stays, in its sequence
+  int rows;                  // rows from there to the sequence's end
+  int first, last;           // walked rows: whole tiles, those of a head
+  int nk, off;               // keys of the sequence; the position of query 0 among them
+  void* out[2];              // that first row of dq, or of dv and dk
 };
 
 // Every barrier's phases are counted by the warps that wait on it, on through
@@ -141,14 +155,15 @@ struct Bars {
   uint64_t p_full;                    // dk, dv: probabilities written
   uint64_t dpk_full, dsk_full;        //   dP formed, ds written
   uint64_t dp_full[2], ds_full[2];    // dq: the same, twice
-  uint64_t done, acc_free;            // an item's sums formed; read
+  uint64_t dv_done, done, acc_free;   // an item's dv formed; all its sums; read
   uint64_t edge[2];
-  uint64_t id_full[2], id_empty[2];   // the items that the loading warp announces
-  uint32_t id[2];
+  uint64_t stat[2];                   // dq: statistics of an item's queries, by turns
+  uint64_t item_full[2], item_empty[2];
+  Item item[2];                       // announced by the loading warp
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 320, "barrier block");
+static_assert(sizeof(Bars) <= 448, "barrier block");
 // shared-memory address of a barrier; `bb` is the block's
 #define BAR(f) (bb + static_cast<uint32_t>(offsetof(Bars, f)))
 
@@ -159,8 +174,9 @@ __device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
     mbar_init(&s->dp_full[i], 1);
     mbar_init(&s->ds_full[i], calc_warps);
     mbar_init(&s->edge[i], 1);
-    mbar_init(&s->id_full[i], 1);
-    mbar_init(&s->id_empty[i], 1 + calc_warps);
+    mbar_init(&s->stat[i], 1);
+    mbar_init(&s->item_full[i], 1);
+    mbar_init(&s->item_empty[i], 1 + calc_warps);
   }
   for (int i = 0; i < 3; ++i) {
     mbar_init(&s->a_full[i], 1);
@@ -173,56 +189,37 @@ __device__ __forceinline__ void init_bars(Bars* s, int calc_warps) {
   mbar_init(&s->p_full, calc_warps);
   mbar_init(&s->dpk_full, 1);
   mbar_init(&s->dsk_full, calc_warps);
+  mbar_init(&s->dv_done, 1);
   mbar_init(&s->done, 1);
   mbar_init(&s->acc_free, calc_warps);
   s->abort = 0;
   fence_mbar_init();
 }
 
-// What every warp knows of the launch.
+// The loading warp's view of the launch.
 struct Grid {
   const CUtensorMap *mq, *mk, *mv, *mdo;
   uint32_t nk, total;        // items of dk and dv, and all
   int ktiles, qtiles;
 };
 
-// The items that the loading warp announced, for another warp of the CTA.
+// The announced items, for another warp of the CTA: next() waits for one,
+// free() gives its place back.
 struct Items {
+  uint32_t bb;
+  const Bars* bar;
   Ring<2> at;
-  __device__ __forceinline__ bool next(uint32_t bb, const Bars* bar, const Grid& g, volatile int* abort,
-                                       const AttnParams& p, uint32_t* id) {
-    if (!wait_warp(BAR(id_full) + 8 * at.s, at.ph, abort, p)) return false;
-    *id = *const_cast<const volatile uint32_t*>(&bar->id[at.s]);
+  __device__ __forceinline__ const Item* next(volatile int* abort, const AttnParams& p) {
+    if (!wait_warp(BAR(item_full) + 8 * at.s, at.ph, abort, p)) return nullptr;
+    const Item* t = &bar->item[at.s];
+    return t->kind == NO_MORE ? nullptr : t;
+  }
+  __device__ __forceinline__ void free() {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_at(BAR(id_empty) + 8 * at.s);
+    if ((threadIdx.x & 31) == 0) mbar_arrive_at(BAR(item_empty) + 8 * at.s);
     at.next();
-    return *id < g.total;
   }
 };
-
-// One item: what it owns and what it walks.
-struct Item {
-  bool dkv;
-  Work w;
-  int own;                   // first row of the tile that stays, in its sequence
-  Range r;                   // walked tiles (of every head of the group: dk, dv)
-  int n;                     // steps
-};
-
-template <int WT>
-__device__ __forceinline__ Item find_item(const AttnParams& p, const Grid& g, uint32_t id) {
-  Item t;
-  t.dkv = id < g.nk;
-  t.w = t.dkv ? find_work(p, false, TILE, p.kv_heads, g.ktiles, id)
-              : find_work(p, true, TILE, p.heads, g.qtiles, id - g.nk);
-  t.own = t.w.tile * TILE;
-  t.r = Range{0, 0};
-  if (t.w.ok)
-    t.r = t.dkv ? query_tiles<WT>(p, t.w, t.own, min(t.own + TILE, t.w.nk) - 1)
-                : key_tiles<WT>(p, t.w, t.own, min(t.own + TILE, t.w.nq) - 1);
-  t.n = t.r.count * (t.dkv ? p.heads / p.kv_heads : 1);
-  return t;
-}
 
 // ----------------------------------------------------------------- loads
 template <typename T, int DP>
@@ -238,37 +235,63 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
   // counter (which the statistics kernel sets to 0) while an item is under
   // way, so that long and short items even out.  Which CTA computes an item
   // changes nothing in its result.
-  Ring<2> ids;
+  Ring<2> items, stats;
   uint32_t id = blockIdx.x, next_id = 0;
+  bool ok = true, waited = false;
+  auto wait_stats = [&]() {                                  // statistics and counter are the previous kernel's
+    if (!waited) pdl_wait();
+    waited = true;
+  };
   auto take = [&]() {
+    wait_stats();
     if (lane == 0) next_id = p.counter != nullptr ? gridDim.x + atomicAdd(p.counter, 1u) : id + gridDim.x;
   };
-  bool ok = true, waited = false;
+  const int group = p.heads / p.kv_heads;
   for (;; id = __shfl_sync(0xffffffffu, next_id, 0)) {
-    ok = ok && wait_warp(BAR(id_empty) + 8 * ids.s, ids.ph ^ 1u, abort, p);
+    Item t;
+    Work w{};
+    const bool end = id >= g.total, dkv = id < g.nk;
+    t.kind = end ? NO_MORE : dkv ? DKV : DQ;
+    if (!end) {
+      w = dkv ? find_work(p, false, TILE, p.kv_heads, g.ktiles, id) : find_work(p, true, TILE, p.heads, g.qtiles, id - g.nk);
+      if (!w.ok) {
+        take();
+        continue;
+      }
+      t.own = w.tile * TILE;
+      t.rows = (dkv ? w.nk : w.nq) - t.own;
+      const Range r = dkv ? query_tiles<WT>(p, w, t.own, min(t.own + TILE, w.nk) - 1)
+                          : key_tiles<WT>(p, w, t.own, min(t.own + TILE, w.nq) - 1);
+      t.n = r.count * (dkv ? group : 1);
+      t.first = r.first * WT;
+      t.last = (r.first + r.count) * WT;
+      t.nk = w.nk;
+      t.off = w.nk - w.nq;
+      const long long k0 = w.k0 + t.own, q0 = w.q0 + t.own;
+      t.out[0] = dkv ? static_cast<T*>(p.dv) + w.b * p.dvb + w.h * p.dvh + k0 * p.dvs
+                     : static_cast<T*>(p.dq) + w.b * p.dqb + w.h * p.dqh + q0 * p.dqs;
+      t.out[1] = static_cast<T*>(p.dk) + w.b * p.dkb + w.h * p.dkh + k0 * p.dks;
+    }
+    ok = ok && wait_warp(BAR(item_empty) + 8 * items.s, items.ph ^ 1u, abort, p);
     if (!ok) break;
     if (lane == 0) {
-      *const_cast<volatile uint32_t*>(&bar->id[ids.s]) = id;
-      mbar_arrive_at(BAR(id_full) + 8 * ids.s);
+      bar->item[items.s] = t;
+      mbar_arrive_at(BAR(item_full) + 8 * items.s);
     }
-    ids.next();
-    if (id >= g.total) break;
-    const Item t = find_item<WT>(p, g, id);
+    items.next();
+    if (end) break;
     if (t.n == 0) {
-      if (!waited) pdl_wait();
-      waited = true;
       take();
       continue;
     }
-    const Work& w = t.w;
     // dk, dv: K and V stay, Q and dO are walked; dq: Q and dO stay, K and V are walked
-    const CUtensorMap* own0 = t.dkv ? g.mk : g.mq;
-    const CUtensorMap* own1 = t.dkv ? g.mv : g.mdo;
-    const CUtensorMap* walk_a = t.dkv ? g.mq : g.mk;
-    const CUtensorMap* walk_b = t.dkv ? g.mdo : g.mv;
-    const int own_row = (t.dkv ? w.k0 : w.q0) + t.own, group = p.heads / p.kv_heads;
-    const int first = t.dkv ? w.q0 : w.k0, len = t.dkv ? w.nq : w.nk;
-    const int h0 = t.dkv ? w.h * group : w.h / group, h1 = t.dkv ? h0 + group : h0 + 1;
+    const CUtensorMap* own0 = dkv ? g.mk : g.mq;
+    const CUtensorMap* own1 = dkv ? g.mv : g.mdo;
+    const CUtensorMap* walk_a = dkv ? g.mq : g.mk;
+    const CUtensorMap* walk_b = dkv ? g.mdo : g.mv;
+    const int own_row = (dkv ? w.k0 : w.q0) + t.own;
+    const int first = dkv ? w.q0 : w.k0, len = dkv ? w.nq : w.nk;
+    const int h0 = dkv ? w.h * group : w.h / group, h1 = dkv ? h0 + group : h0 + 1;
     ok = wait_warp(BAR(own_empty), own_ph, abort, p);
     if (!ok) break;
     if (lane == 0) {
@@ -277,8 +300,9 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
     }
     bool second = true;                                      // the other own tile is still to come
     for (int h = h0; ok && h < h1; ++h) {
-      const long long stat = ((static_cast<long long>(w.b) * p.heads + h) * g.qtiles + w.qtile) * TILE;
-      for (int i0 = t.r.first * WT; i0 < (t.r.first + t.r.count) * WT; i0 += WT) {
+      // statistics: of each walked tile, or of the one that stays, with the first walked tile
+      const long long stat = ((static_cast<long long>(w.b) * p.heads + (dkv ? h : w.h)) * g.qtiles + w.qtile) * TILE;
+      for (int i0 = t.first; i0 < t.last; i0 += WT) {
         const int row = first + i0, valid = len - i0;
         const bool edge = p.cu_q != nullptr && valid < WT;
         const uint32_t at = sb + S::A_OFF + ra.s * S::T, bt = sb + S::B_OFF + rb.s * S::T;
@@ -298,21 +322,24 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
             mbar_expect_at(BAR(own) + 8, S::OWN);
             load_tile<DP, TILE, BOX>(sb + S::OWN, own1, BAR(own) + 8, w.h, own_row, w.b);
           }
-          if (!waited) pdl_wait();                           // statistics and counter are the previous kernel's
-          waited = true;
           take();
         }
         ok = wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p);
         if (!ok) break;
         if (lane == 0) {
-          if (!edge) mbar_expect_at(fb, S::T + (t.dkv ? S::STAT : 0));
-          else mbar_expect_at(BAR(edge) + 8, S::T + (t.dkv ? S::STAT : 0));
           const uint32_t to = edge ? BAR(edge) + 8 : fb;
+          const uint32_t st = sb + S::STAT_OFF + rb.s * S::STAT;
+          mbar_expect_at(to, S::T + (dkv ? 2 * WT * 4 : 0));
           load_tile<DP, WT, BOX>(bt, walk_b, to, h, row, w.b);
-          if (t.dkv) {
-            const uint32_t st = sb + S::STAT_OFF + rb.s * S::STAT;
+          if (dkv) {
             bulk_load(st, p.stat_lse + stat + i0, WT * 4, to);
-            bulk_load(st + WT * 4, p.stat_delta + stat + i0, WT * 4, to);
+            bulk_load(st + TILE * 4, p.stat_delta + stat + i0, WT * 4, to);
+          } else if (i0 == t.first) {
+            // a barrier of their own: the walked tiles get further ahead of the warps that read these
+            const uint32_t bs = BAR(stat) + 8 * stats.s;
+            mbar_expect_at(bs, 2 * TILE * 4);
+            bulk_load(st, p.stat_lse + stat + t.own, TILE * 4, bs);
+            bulk_load(st + TILE * 4, p.stat_delta + stat + t.own, TILE * 4, bs);
           }
         }
         if (edge) {
@@ -329,6 +356,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
       }
     }
     own_ph ^= 1u;
+    if (!dkv) stats.next();
   }
   // after a wait ran out: a millisecond for copies in flight to land
   if (*abort != 0 && lane == 0) {
@@ -341,8 +369,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
 
 // -------------------------------------------------------------- products
 template <typename T, int DP>
-__device__ __forceinline__ void product_role(const AttnParams& p, const Grid& g, uint32_t sb, uint32_t bb,
-                                             uint32_t tmem, Bars* bar) {
+__device__ __forceinline__ void product_role(const AttnParams& p, uint32_t sb, uint32_t bb, uint32_t tmem, Bars* bar) {
   using S = Smem<DP>;
   constexpr int WT = S::WT;
   constexpr uint32_t S_COL = 0, DP_COL = WT;
@@ -368,31 +395,35 @@ __device__ __forceinline__ void product_role(const AttnParams& p, const Grid& g,
     if (last) commit_warp(BAR(own_empty) + 8);
   };
   bool ok = true, was_dkv = false;
-  Items items;
-  for (uint32_t id; ok && items.next(bb, bar, g, abort, p, &id);) {
-    const Item t = find_item<WT>(p, g, id);
-    if (t.n == 0) continue;
+  Items items{bb, bar, {}};
+  while (ok) {
+    const Item* t = items.next(abort, p);
+    if (t == nullptr) break;
+    const int n = t->n;
+    const bool dkv = t->kind == DKV;
+    items.free();
+    if (n == 0) continue;
     // an item's first products go ahead of the previous item's outputs; its
     // sums wait for them.  From dk, dv to dq the places differ: wait at once.
     bool sums_free = false;
-    if (!t.dkv && was_dkv) {
+    if (!dkv && was_dkv) {
       ok = wait_warp(BAR(acc_free), acc_ph, abort, p);
       sums_free = true;
     }
-    was_dkv = t.dkv;
+    was_dkv = dkv;
     ok = ok && wait_warp(BAR(own), own_ph, abort, p) && wait_a();
     if (!ok) break;
     tc_fence_after();
-    scores(t.n == 1);
+    scores(n == 1);
     ok = wait_warp(BAR(own) + 8, own_ph, abort, p) && wait_b();
     if (!ok) break;
     own_ph ^= 1u;
     tc_fence_after();
     uint32_t acc = 0;
-    if (t.dkv) {
-      dprobs(DP_COL, BAR(dpk_full), t.n == 1);
+    if (dkv) {
+      dprobs(DP_COL, BAR(dpk_full), n == 1);
       nb.next();
-      for (int left = t.n - 1; left >= 0; --left, k_ph ^= 1u, acc = 1) {
+      for (int left = n - 1; left >= 0; --left, k_ph ^= 1u, acc = 1) {
         // a step's tiles are waited for before the probabilities, so that
         // products follow one another without a wait in between
         ok = (left == 0 || wait_a()) && wait_warp(BAR(p_full), k_ph, abort, p) &&
@@ -401,6 +432,7 @@ __device__ __forceinline__ void product_role(const AttnParams& p, const Grid& g,
         tc_fence_after();
         mma_over_tokens<T, DP, COLS, WT>(tmem + DV_COL, tmem + S_COL, desc_tokens<WT>(sb + S::B_OFF + rb.s * S::T), acc);
         commit_warp(BAR(b_empty) + 8 * rb.s);      // dP, issued earlier, has read this dO tile too
+        if (left == 0) commit_warp(BAR(dv_done));
         rb.next();
         // the next scores overwrite the probabilities: the tensor pipe runs in order
         if (left > 0) scores(left == 1);
@@ -423,8 +455,8 @@ __device__ __forceinline__ void product_role(const AttnParams& p, const Grid& g,
         rb.next();
         next.next();
       };
-      ahead(t.n == 1);
-      for (int left = t.n - 1; left >= 0; --left, s_ph ^= 1u, acc = 1) {
+      ahead(n == 1);
+      for (int left = n - 1; left >= 0; --left, s_ph ^= 1u, acc = 1) {
         // the next tile's scores and dP (over the ds before last, which dq has read: the tensor pipe runs in order)
         if (left > 0) {
           ok = wait_a() && wait_b() && wait_warp(BAR(s_free), s_ph, abort, p);
@@ -470,8 +502,13 @@ struct Calc {
   volatile int* abort;
   int quad, part, c0, lane;
   Ring<S::RB> rb;
-  Ring<2> buf;
-  uint32_t s_ph = 0, k_ph = 0, done_ph = 0;
+  Ring<2> buf, stats;
+  uint32_t s_ph = 0, k_ph = 0, dv_ph = 0, done_ph = 0;
+
+  // bits [lo, hi) of 32
+  static __device__ __forceinline__ uint32_t seen(int lo, int hi) {
+    return __funnelshift_lc(0u, ~0u, max(lo, 0)) & ~__funnelshift_lc(0u, ~0u, max(hi, 0));
+  }
 
   // dk and dv.  A warp has 32 keys (TMEM rows) by 32 queries; thread t of it
   // the keys t / 4 + 8 k, k = 0 .. 3, and the queries 8 j + 2 (t % 4) + {0,
@@ -485,15 +522,13 @@ struct Calc {
     const int c1 = c0 + 2 * (lane & 3);            // and queries of a tile
     const float c = p.scale * LOG2E;
     const F2 cc = f2_make(c, c);
-    const int off = t.w.nk - t.w.nq;
+    const int n = t.n, own = t.own, off = t.off, first = t.first, last = t.last;
     const uint32_t s_at = tmem + lanes + c0, dp_at = tmem + lanes + WT + c0;
-    int q0 = t.r.first * WT;
-    const int q_end = (t.r.first + t.r.count) * WT;
-    for (int i = 0; i < t.n; ++i) {
+    int q0 = first;
+    for (int i = 0; i < n; ++i) {
       const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + rb.s * S::STAT) + c1;
       // queries q0 .. q0 + WT - 1 against keys own .. own + 127: does everyone see everything?
-      const bool mask =
-          p.causal && (t.own + TILE - 1 > q0 + off || (p.window > 0 && q0 + WT - 1 + off - t.own >= p.window));
+      const bool mask = p.causal && (own + TILE - 1 > q0 + off || (p.window > 0 && q0 + WT - 1 + off - own >= p.window));
       float v[COLS], d[COLS];
       uint32_t r16[COLS / 2];
       if (!wait_warp(BAR(b_full) + 8 * rb.s, rb.ph, abort, p) || !wait_warp(BAR(s_full), s_ph, abort, p)) return false;
@@ -519,12 +554,13 @@ struct Calc {
         // the queries (columns) that see key j + 8 k: [lo, hi)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int lo = j + 8 * k - off - q0 - c1, hi = p.window > 0 ? lo + p.window : WT;
+          const int lo = j + 8 * k - off - q0 - c1;
+          const uint32_t m = seen(lo, p.window > 0 ? lo + p.window : COLS);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float* u = v + 16 * (k >> 1) + 4 * q + 2 * (k & 1);
-            if (8 * q < lo || 8 * q >= hi) u[0] = 0.f;
-            if (8 * q + 1 < lo || 8 * q + 1 >= hi) u[1] = 0.f;
+            if (!(m & (1u << (8 * q)))) u[0] = 0.f;
+            if (!(m & (2u << (8 * q)))) u[1] = 0.f;
           }
         }
       }
@@ -532,6 +568,9 @@ struct Calc {
       for (int k = 0; k < COLS / 2; ++k) r16[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
       tmem_st_16x16(s_at, r16);
       tmem_st_16x16(s_at + ROWS16, r16 + 8);
+      // delta now: once dv has read its tiles, the place of the statistics is filled again
+#pragma unroll
+      for (int q = 0; q < 4; ++q) e[q] = *reinterpret_cast<const float2*>(st + TILE + 8 * q);
       tmem_st_wait();
       warp_arrive(BAR(p_full));
       if (!wait_warp(BAR(dpk_full), k_ph, abort, p)) return false;
@@ -539,8 +578,6 @@ struct Calc {
       tc_fence_after();
       tmem_ld_16x32(dp_at, d);
       tmem_ld_16x32(dp_at + ROWS16, d + 16);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) e[q] = *reinterpret_cast<const float2*>(st + WT + 8 * q);
       tmem_ld_wait();
 #pragma unroll
       for (int k = 0; k < COLS; k += 2) {
@@ -555,25 +592,26 @@ struct Calc {
       warp_arrive(BAR(dsk_full));
       rb.next();
       q0 += WT;
-      if (q0 == q_end) q0 = t.r.first * WT;        // the group's next head
+      if (q0 == last) q0 = first;                  // the group's next head
     }
     return true;
   }
 
   // dq: one query a thread, 32 keys of it
-  __device__ __forceinline__ bool dq_steps(const Item& t, int qtiles) {
-    const int q = t.own + quad * 32 + lane;
+  __device__ __forceinline__ bool dq_steps(const Item& t) {
     const float c = p.scale * LOG2E;
-    const int off = t.w.nk - t.w.nq;
-    const long long at =
-        ((static_cast<long long>(t.w.b) * p.heads + t.w.h) * qtiles + t.w.qtile + t.w.tile) * TILE + quad * 32 + lane;
-    pdl_wait();                                    // the statistics are the previous kernel's
-    const float lse = p.stat_lse[at], delta = p.stat_delta[at];
+    const int own = t.own, off = t.off, nk = t.nk, first = t.first, last = t.last;
+    const int q = own + quad * 32 + lane;
+    // the statistics came with the first walked tile; nothing is loaded over
+    // them before every warp has let its first scores go
+    if (!wait_warp(BAR(stat) + 8 * stats.s, stats.ph, abort, p)) return false;
+    stats.next();
+    const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + rb.s * S::STAT) + quad * 32 + lane;
+    const float lse = st[0], delta = st[TILE];
     const F2 cc = f2_make(c, c), ll = f2_make(lse, lse), dd = f2_make(delta, delta);
-    for (int j0 = t.r.first * WT; j0 < (t.r.first + t.r.count) * WT; j0 += WT) {
-      const bool mask =
-          j0 + WT > t.w.nk ||
-          (p.causal && (j0 + WT - 1 > t.own + off || (p.window > 0 && t.own + TILE - 1 + off - j0 >= p.window)));
+    for (int j0 = first; j0 < last; j0 += WT) {
+      const bool mask = j0 + WT > nk || (p.causal && (j0 + WT - 1 > own + off ||
+                                                      (p.window > 0 && own + TILE - 1 + off - j0 >= p.window)));
       float v[COLS], d[COLS];
       if (!wait_warp(BAR(s_full), s_ph, abort, p)) return false;
       s_ph ^= 1u;
@@ -589,14 +627,15 @@ struct Calc {
       }
       if (mask) {
         // keys (columns) [lo, hi) are seen by query q
-        int lo = 0, hi = t.w.nk - j0 - c0;
+        int lo = 0, hi = nk - j0 - c0;
         if (p.causal) {
           hi = min(hi, q + off + 1 - j0 - c0);
           if (p.window > 0) lo = q + off - p.window + 1 - j0 - c0;
         }
+        const uint32_t m = seen(lo, hi);
 #pragma unroll
         for (int k = 0; k < COLS; ++k)
-          if (k < lo || k >= hi) v[k] = 0.f;
+          if (!(m & (1u << k))) v[k] = 0.f;
       }
       if (!wait_warp(BAR(dp_full) + 8 * buf.s, buf.ph, abort, p)) return false;
       tc_fence_after();
@@ -612,48 +651,33 @@ struct Calc {
       store_rounded<T, COLS / 2>(dp, v);
       warp_arrive(BAR(ds_full) + 8 * buf.s);
       buf.next();
+      rb.next();
     }
     return true;
   }
 
   // The sums of an item, 64 columns a warp (dk, dv) or 32 (dq), to memory.
+  // dv goes while dk's last product runs.
   __device__ __forceinline__ bool outputs(const Item& t) {
-    const Work& w = t.w;
-    const int first = t.own + quad * 32;
-    T* out;
-    long long stride;
-    int col, rows;
-    uint32_t at;
-    float mul = p.scale;
-    if (t.dkv) {
-      // dv by the first half of the warps, dk by the others
-      const bool is_dv = part < Shape<DP>::PARTS / 2;
-      col = part % (Shape<DP>::PARTS / 2) * 64;
-      stride = is_dv ? p.dvs : p.dks;
-      out = is_dv ? static_cast<T*>(p.dv) + w.b * p.dvb + w.h * p.dvh : static_cast<T*>(p.dk) + w.b * p.dkb + w.h * p.dkh;
-      out += (w.k0 + first) * stride + col;
-      rows = w.nk - first;
-      at = tmem + lanes + 2 * WT + (is_dv ? 0 : DP) + col;
-      if (is_dv) mul = 1.f;
-    } else {
-      col = c0;
-      stride = p.dqs;
-      out = static_cast<T*>(p.dq) + w.b * p.dqb + w.h * p.dqh + (w.q0 + first) * stride + col;
-      rows = w.nq - first;
-      at = tmem + lanes + 3 * WT + col;
-    }
+    constexpr int HALF = Shape<DP>::PARTS / 2;     // dv by the first half of the warps, dk by the others
+    const bool dkv = t.kind == DKV, is_dk = part >= HALF, is_dv = dkv && !is_dk;
+    const int width = dkv ? 64 : COLS, col = dkv ? part % HALF * 64 : c0, rows = t.rows - quad * 32;
+    const long long stride = dkv ? (is_dk ? p.dks : p.dvs) : p.dqs;
+    T* out = static_cast<T*>(t.out[dkv && is_dk]) + quad * 32 * stride + col;
     if (t.n == 0) {
-      const int width = t.dkv ? 64 : COLS;
       if (lane < rows)
         for (int k = 0; k < width && col + k < p.dim; k += 8)
           *reinterpret_cast<uint4*>(out + lane * stride + k) = make_uint4(0u, 0u, 0u, 0u);
       return true;
     }
-    if (!wait_warp(BAR(done), done_ph, abort, p)) return false;
+    if (!wait_warp(is_dv ? BAR(dv_done) : BAR(done), is_dv ? dv_ph : done_ph, abort, p)) return false;
     done_ph ^= 1u;
+    if (dkv) dv_ph ^= 1u;
     tc_fence_after();
-    store_rows<T>(at, out, stride, rows, p.dim - col, mul);
-    if (t.dkv) store_rows<T>(at + 32, out + 32, stride, rows, p.dim - col - 32, mul);
+    const uint32_t at = tmem + lanes + (dkv ? 2 * WT + (is_dk ? DP : 0) : 3 * WT) + col;
+#pragma unroll 1
+    for (int k = 0; k < width; k += 32)
+      store_rows<T>(at + k, out + k, stride, rows, p.dim - col - k, is_dv ? 1.f : p.scale);
     warp_arrive(BAR(acc_free));
     return true;
   }
@@ -691,16 +715,15 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   if (warp == 0) {
     load_role<T, DP>(p, g, sb, bb, bar);
   } else if (warp == 1) {
-    product_role<T, DP>(p, g, sb, bb, tmem, bar);
+    product_role<T, DP>(p, sb, bb, tmem, bar);
   } else {
     const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2;
     Calc<T, DP> calc{p, smem, bb, tmem, static_cast<uint32_t>(quad * 32) << 16, &bar->abort, quad, part, COLS * part, lane};
-    Items items;
-    for (uint32_t id; items.next(bb, bar, g, &bar->abort, p, &id);) {
-      const Item t = find_item<S::WT>(p, g, id);
-      if (!t.w.ok) continue;
-      const bool ok = t.n == 0 || (t.dkv ? calc.dkv_steps(t) : calc.dq_steps(t, qtiles));
-      if (!ok || !calc.outputs(t)) break;
+    Items items{bb, bar, {}};
+    while (const Item* t = items.next(&bar->abort, p)) {
+      const bool ok = t->n == 0 || (t->kind == DKV ? calc.dkv_steps(*t) : calc.dq_steps(*t));
+      if (!ok || !calc.outputs(*t)) break;
+      items.free();
     }
   }
   tc_fence_before();
