@@ -13,7 +13,6 @@ written on another stream have to be ready there, as for any call.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import struct
 
@@ -25,23 +24,28 @@ from ._binding import MUON_BF16, MUON_F16, MUON_F32, MuonAttentionC
 BLOCK = 128                       # columns that share one scale
 
 _CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16, torch.float16: MUON_F16}
+_CODE16 = {torch.bfloat16: MUON_BF16, torch.float16: MUON_F16}
+_CODE_BF16 = {torch.bfloat16: MUON_BF16}
 
 
-def _code(t: torch.Tensor, what: str, allowed=tuple(_CODE)) -> int:
-    dtype = t.dtype
-    if dtype not in allowed:
-        raise ValueError(f"{what} must be one of {', '.join(str(d) for d in allowed)}, not {dtype}")
-    return _CODE[dtype]
+def _code(t: torch.Tensor, what: str, allowed=_CODE) -> int:
+    code = allowed.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be one of {', '.join(str(d) for d in allowed)}, not {t.dtype}")
+    return code
 
 
 def _device(what: str, first, *rest) -> int:
     """The index of the CUDA device that all the tensors (None aside) are on."""
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise ValueError(f"{what} must be CUDA tensors")
-    dev = first.get_device()
-    for t in rest:
-        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != dev):
-            raise ValueError(f"{what} must be CUDA tensors on one device")
+    try:
+        dev = first.get_device()         # -1: not on a GPU
+        for t in rest:
+            if t is not None and t.get_device() != dev:
+                dev = -1
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        raise ValueError(f"{what} must be CUDA tensors on one device")
     return dev
 
 
@@ -57,18 +61,6 @@ def _handle(dev: int, handle):
     if handle.device != dev:
         raise ValueError(f"the handle is on device {handle.device}, the tensors on {dev}")
     return handle
-
-
-def _on_stream(fn):
-    """``stream=``: the call runs with that stream current, so that torch ties
-    outputs and scratch to it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
 
 
 def _rows(t: torch.Tensor, what: str):
@@ -96,37 +88,41 @@ def _rows(t: torch.Tensor, what: str):
 
 
 # ---------------------------------------------------------------- layer norm
-def _affine(t, what, x, cols):
+def _affine(t, what, dtype, cols):
     """Pointer and type code of a weight or bias vector."""
     if t is None:
         return None, MUON_F32
-    if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
+    if t.shape != (cols,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {cols} elements")
-    if t.dtype is not torch.float32 and t.dtype is not x.dtype:
-        raise ValueError(f"{what} must be float32 or {x.dtype}")
-    return t.data_ptr(), _CODE[t.dtype]
+    own = t.dtype
+    if own is not torch.float32 and own is not dtype:
+        raise ValueError(f"{what} must be float32 or {dtype}")
+    return t.data_ptr(), _CODE[own]
 
 
-@_on_stream
-def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, handle=None):
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, handle=None, stream=None):
     """Layer norm over the last dimension: ``(y, mean, rstd)``.
 
     x: [.., cols] fp32, bf16 or fp16, cols up to 16384; weight and bias:
     [cols], fp32 or x's type, or None (ones, zeros).  y has x's type and
     shape, mean and rstd (fp32, x.shape[:-1]) are what the backward pass
     takes."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return layer_norm(x, weight, bias, eps=eps, handle=handle)
     dev = _device("x, weight and bias", x, weight, bias)
     code = _code(x, "x")
     xr, rows, ldx = _rows(x, "x")
-    shape = x.shape
+    shape, dtype = x.shape, x.dtype
     cols = shape[-1]
-    wptr, wcode = _affine(weight, "weight", x, cols)
-    bptr, bcode = _affine(bias, "bias", x, cols)
+    wptr, wcode = _affine(weight, "weight", dtype, cols)
+    bptr, bcode = _affine(bias, "bias", dtype, cols)
     if wptr is not None and bptr is not None and wcode != bcode:
         raise ValueError("weight and bias must have one type")
     h = _handle(dev, handle)
-    y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    where = x.device
+    y = torch.empty(shape, dtype=dtype, device=where)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=where)
     rstd = torch.empty_like(mean)
     st = h._lib.muon_layer_norm_forward(h.ptr, xr.data_ptr(), ldx, wptr, bptr, y.data_ptr(), cols, mean.data_ptr(),
                                         rstd.data_ptr(), rows, cols, code, bcode if wptr is None else wcode, eps,
@@ -136,10 +132,12 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, handle=None):
     return y, mean, rstd
 
 
-@_on_stream
-def layer_norm_backward(dy, x, mean, rstd, weight=None, *, handle=None):
+def layer_norm_backward(dy, x, mean, rstd, weight=None, *, handle=None, stream=None):
     """``(dx, dweight, dbias)`` of layer_norm: dx in x's type, dweight and
     dbias fp32 [cols], summed over all rows in a fixed order."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return layer_norm_backward(dy, x, mean, rstd, weight, handle=handle)
     dev = _device("x, dy, mean, rstd and weight", x, dy, mean, rstd, weight)
     code = _code(x, "x")
     shape = x.shape
@@ -147,23 +145,26 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, handle=None):
         raise ValueError("dy must have x's shape and type")
     xr, rows, ldx = _rows(x, "x")
     gr, _, ldg = _rows(dy, "dy")
+    outer = shape[:-1]
     for t, what in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or t.shape != shape[:-1] or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous float32 of shape {tuple(shape[:-1])}")
+        if t.dtype is not torch.float32 or t.shape != outer or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous float32 of shape {tuple(outer)}")
     cols = shape[-1]
-    wptr, wcode = _affine(weight, "weight", x, cols)
+    wptr, wcode = _affine(weight, "weight", x.dtype, cols)
     h = _handle(dev, handle)
-    lib, need, where = h._lib, ctypes.c_uint64(), x.device
+    lib, need = h._lib, ctypes.c_uint64()
     st = lib.muon_layer_norm_workspace(h.ptr, rows, cols, ctypes.byref(need))
     if st:
         h._raise(st, "muon_layer_norm_workspace")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=where)
+    need = need.value
+    where = x.device
+    ws = torch.empty(need, dtype=torch.uint8, device=where)
     dx = torch.empty(shape, dtype=x.dtype, device=where)
     dw = torch.empty(cols, dtype=torch.float32, device=where)
     db = torch.empty_like(dw)
     st = lib.muon_layer_norm_backward(h.ptr, gr.data_ptr(), ldg, xr.data_ptr(), ldx, mean.data_ptr(), rstd.data_ptr(),
                                       wptr, dx.data_ptr(), cols, dw.data_ptr(), db.data_ptr(), rows, cols, code,
-                                      wcode, ws.data_ptr(), need.value, _raw_stream(dev))
+                                      wcode, ws.data_ptr(), need, _raw_stream(dev))
     if st:
         h._raise(st, "muon_layer_norm_backward")
     return dx, dw, db
@@ -189,11 +190,11 @@ assert _ATTENTION.size == ctypes.sizeof(MuonAttentionC)
 class _Attention:
     """The checked arguments of an attention call."""
 
-    __slots__ = ("packed", "strides", "ints", "scale", "cu", "lse_shape")
+    __slots__ = ("packed", "strides", "ints", "scale", "cu", "like_q", "like_k", "lse_shape")
 
     def __init__(self, q, k, v, causal, window, scale, cu_q, cu_k):
         packed = self.packed = cu_q is not None or cu_k is not None
-        code = _code(q, "q", (torch.bfloat16, torch.float16))
+        code = _code(q, "q", _CODE16)
         if k.dtype is not q.dtype or v.dtype is not q.dtype:
             raise ValueError("q, k and v must have one type")
         self.strides = (*_strides(q, "q", packed), *_strides(k, "k", packed), *_strides(v, "v", packed))
@@ -214,8 +215,14 @@ class _Attention:
             batch = qs[0]
             self.cu = (0, 0)
         sq, heads, dim = qs[-3:]
+        sk, kv_heads = ks[-3], ks[-2]
+        # strides of contiguous outputs
+        row = heads * dim
+        self.like_q = (sq * row, row, dim)
+        row = kv_heads * dim
+        self.like_k = (sk * row, row, dim)
         self.lse_shape = (heads, sq) if packed else (batch, heads, sq)
-        self.ints = (batch, sq, ks[-3], heads, ks[-2], dim, 1 if causal else 0, int(window), code)
+        self.ints = (batch, sq, sk, heads, kv_heads, dim, 1 if causal else 0, int(window), code)
         if max(self.ints) >= 1 << 31 or min(self.ints) < 0:
             raise ValueError("negative or oversized shape or window")
         self.scale = float(scale) if scale is not None else 1.0 / math.sqrt(dim) if dim else 0.0
@@ -224,9 +231,8 @@ class _Attention:
         return _ATTENTION.pack(*pointers, *self.cu, *self.strides, *strides, *self.ints, self.scale)
 
 
-@_on_stream
 def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None,
-              handle=None):
+              handle=None, stream=None):
     """Attention, ``(o, lse)``.
 
     q: [batch, sq, heads, dim], k and v: [batch, sk, kv_heads, dim], bf16 or
@@ -239,13 +245,18 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_
     ``window`` of them.  scale (above 0): 1 / sqrt(dim) by default.
     o has q's shape and type (a query that sees no key: 0); lse is fp32
     [batch, heads, sq] or [heads, tokens] (there: -inf)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return attention(q, k, v, causal=causal, window=window, scale=scale, cu_seqlens_q=cu_seqlens_q,
+                             cu_seqlens_k=cu_seqlens_k, handle=handle)
     dev = _device("q, k, v and the offsets", q, k, v, cu_seqlens_q, cu_seqlens_k)
     a = _Attention(q, k, v, causal, window, scale, cu_seqlens_q, cu_seqlens_k)
     h = _handle(dev, handle)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(a.lse_shape, dtype=torch.float32, device=q.device)
+    where = q.device
+    o = torch.empty(q.shape, dtype=q.dtype, device=where)
+    lse = torch.empty(a.lse_shape, dtype=torch.float32, device=where)
     args = a.pack((q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), 0, 0, 0, 0),
-                  _strides(o, "o", a.packed) + _NO_STRIDES)
+                  a.like_q + _NO_STRIDES)
     st = h._lib.muon_attention_forward(h.ptr, args, _raw_stream(dev))
     if st:
         h._raise(st, "muon_attention_forward")
@@ -255,46 +266,49 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_
 _NO_STRIDES = (0,) * 12
 
 
-@_on_stream
 def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int = 0, scale=None, cu_seqlens_q=None,
-                       cu_seqlens_k=None, handle=None):
+                       cu_seqlens_k=None, handle=None, stream=None):
     """``(dq, dk, dv)`` of attention, from its output and lse: the
     probabilities are recomputed, nothing of size sq x sk is kept.  dk and dv
     are summed over the query heads that share them, in a fixed order."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return attention_backward(do, q, k, v, o, lse, causal=causal, window=window, scale=scale,
+                                      cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, handle=handle)
     dev = _device("q, k, v, do, o, lse and the offsets", q, k, v, do, o, lse, cu_seqlens_q, cu_seqlens_k)
     a = _Attention(q, k, v, causal, window, scale, cu_seqlens_q, cu_seqlens_k)
-    dtype, where = q.dtype, q.device
-    for t, what in ((do, "do"), (o, "o")):
-        if t.shape != q.shape or t.dtype is not dtype:
-            raise ValueError(f"{what} must have q's shape and type")
+    shape, dtype = q.shape, q.dtype
+    if do.shape != shape or o.shape != shape or do.dtype is not dtype or o.dtype is not dtype:
+        raise ValueError("do and o must have q's shape and type")
     if lse.dtype is not torch.float32 or lse.shape != a.lse_shape or not lse.is_contiguous():
         raise ValueError("lse must be the contiguous float32 tensor that attention returned")
     h = _handle(dev, handle)
-    st = do.stride()
-    if st[-1] != 1 or 0 in st or any(s % 8 for s in st[:-1]):
-        do = do.contiguous()             # autograd hands over expanded gradients
-    dq = torch.empty(q.shape, dtype=dtype, device=where)
+    if not do.is_contiguous():
+        st = do.stride()
+        if st[-1] != 1 or 0 in st or any(s % 8 for s in st[:-1]):
+            do = do.contiguous()         # autograd hands over expanded gradients
+    where = q.device
+    dq = torch.empty(shape, dtype=dtype, device=where)
     dk = torch.empty(k.shape, dtype=dtype, device=where)
     dv = torch.empty_like(dk)
-    kv = _strides(dk, "dk", a.packed)
     args = a.pack((q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
                    dq.data_ptr(), dk.data_ptr(), dv.data_ptr()),
-                  (*_strides(o, "o", a.packed), *_strides(do, "do", a.packed), *_strides(dq, "dq", a.packed), *kv, *kv))
+                  (*_strides(o, "o", a.packed), *_strides(do, "do", a.packed), *a.like_q, *a.like_k, *a.like_k))
     lib = h._lib
     need = ctypes.c_uint64()
     st = lib.muon_attention_workspace(h.ptr, args, ctypes.byref(need))
     if st:
         h._raise(st, "muon_attention_workspace")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=where)
-    st = lib.muon_attention_backward(h.ptr, args, ws.data_ptr(), need.value, _raw_stream(dev))
+    need = need.value
+    ws = torch.empty(need, dtype=torch.uint8, device=where)
+    st = lib.muon_attention_backward(h.ptr, args, ws.data_ptr(), need, _raw_stream(dev))
     if st:
         h._raise(st, "muon_attention_backward")
     return dq, dk, dv
 
 
 # --------------------------------------------------- activations in 8 bits
-@_on_stream
-def act8_store(x, *, handle=None):
+def act8_store(x, *, handle=None, stream=None):
     """x [rows, cols] (fp32, bf16, fp16) in 8 bits: ``(codes, scales)``.
 
     codes: float8_e4m3fn [rows, cols]; scales: uint8 [ceil(cols / 128),
@@ -305,6 +319,9 @@ def act8_store(x, *, handle=None):
     padded storage (whole blocks, 16 rows), which act8_weight_grad reads in
     place; copies in other layouts are taken too, at the cost of one more
     copy."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return act8_store(x, handle=handle)
     dev = _device("x", x)
     code = _code(x, "x")
     if x.dim() != 2:
@@ -314,13 +331,14 @@ def act8_store(x, *, handle=None):
     h = _handle(dev, handle)
     blocks, lds = -(-cols // BLOCK), -(-rows // 16) * 16
     ldc = blocks * BLOCK
-    codes = torch.empty((rows, ldc), dtype=torch.float8_e4m3fn, device=x.device)
-    scales = torch.empty((blocks, lds), dtype=torch.uint8, device=x.device)
+    where = x.device
+    codes = torch.empty((rows, ldc), dtype=torch.float8_e4m3fn, device=where)
+    scales = torch.empty((blocks, lds), dtype=torch.uint8, device=where)
     st = h._lib.muon_act8_store(h.ptr, xr.data_ptr(), ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, rows, cols,
                                 code, _raw_stream(dev))
     if st:
         h._raise(st, "muon_act8_store")
-    return codes if ldc == cols else codes[:, :cols], scales if lds == rows else scales[:, :rows]
+    return codes if ldc == cols else codes.narrow(1, 0, cols), scales if lds == rows else scales.narrow(1, 0, rows)
 
 
 def _act8_operands(codes, scales):
@@ -345,32 +363,37 @@ def _act8_operands(codes, scales):
     return codes, scales, rows, cols, ldc[0], lds[0]
 
 
-@_on_stream
-def act8_restore(codes, scales, *, dtype=torch.bfloat16, handle=None):
+def act8_restore(codes, scales, *, dtype=torch.bfloat16, handle=None, stream=None):
     """The values that act8_store kept, [rows, cols] in ``dtype``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return act8_restore(codes, scales, dtype=dtype, handle=handle)
     dev = _device("codes and scales", codes, scales)
-    if dtype not in _CODE:
+    code = _CODE.get(dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {dtype}")
     h = _handle(dev, handle)
     codes, scales, rows, cols, ldc, lds = _act8_operands(codes, scales)
-    out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    out = torch.empty((rows, cols), dtype=dtype, device=scales.device)
     st = h._lib.muon_act8_restore(h.ptr, codes.data_ptr(), ldc, scales.data_ptr(), lds, out.data_ptr(), cols, rows,
-                                  cols, _CODE[dtype], _raw_stream(dev))
+                                  cols, code, _raw_stream(dev))
     if st:
         h._raise(st, "muon_act8_restore")
     return out
 
 
-@_on_stream
-def act8_weight_grad(dy, codes, scales, *, add=None, out=None, dtype=None, handle=None):
+def act8_weight_grad(dy, codes, scales, *, add=None, out=None, dtype=None, handle=None, stream=None):
     """dw [out, cols] = dy^T x (+ add) of a linear layer y = x w^T whose
     input x is kept in 8 bits.
 
     dy: bf16 [rows, out]; add: the gradient so far; out: where dw is written
     (``out=add`` adds in place); dtype: float32 (default) or bfloat16, that
     of add and out if they are given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return act8_weight_grad(dy, codes, scales, add=add, out=out, dtype=dtype, handle=handle)
     dev = _device("dy, codes, scales, add and out", dy, codes, scales, add, out)
-    _code(dy, "dy", (torch.bfloat16,))
+    _code(dy, "dy", _CODE_BF16)
     if dy.dim() != 2 or codes.dim() != 2 or dy.shape[0] != codes.shape[0]:
         raise ValueError("dy must be [rows, out] and codes [rows, cols]")
     shape = (dy.shape[1], codes.shape[1])
