@@ -142,53 +142,61 @@ __device__ __forceinline__ void convert16(const uint4& c, float unit, uint32_t* 
   }
 }
 
-// Four outputs of row o from column n (n < cols): partial results as they
-// are, final ones rounded to their type.
-__device__ __forceinline__ void store4(const WgradParams& p, float* part, int o, int n, float4 v) {
-  if (part != nullptr) {
-    float* d = part + static_cast<long long>(o) * p.cols + n;
-    if ((p.cols & 3) == 0) {
-      *reinterpret_cast<float4*>(d) = v;
-      return;
-    }
-    const float f[4] = {v.x, v.y, v.z, v.w};
+// A 32 x 32 block of fp32 values in a warp's slot of shared memory, its
+// 16-byte chunks swizzled: lanes read and write either a row each or, eight
+// lanes a row, parts of rows that are next to each other in memory.
+__device__ __forceinline__ uint32_t slot_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// The block of `add` from (o, n) into the slot, zeros outside it.
+__device__ __forceinline__ void load_block(const WgradParams& p, uint8_t* slot, int o, int n, int lane) {
+  const int r = lane >> 3, q = lane & 7;
+  const long long at = static_cast<long long>(o + r) * p.ldadd + n + 4 * q;
+  const bool inside = p.vec_add && o + 32 <= p.out && n + 32 <= p.cols;
+  if (inside && p.odtype == DT_F32) {
+    float4 x[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (n + k < p.cols) d[k] = f[k];
+    for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.add) + at + 4 * i * p.ldadd);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(slot + slot_at(r + 4 * i, q)) = x[i];
     return;
   }
-  const float f[4] = {v.x, v.y, v.z, v.w};
-  const long long at = static_cast<long long>(o) * p.ldw + n;
-  if (p.vec && n + 3 < p.cols) {
-    if (p.odtype == DT_F32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at) = make_float4(f[0], f[1], f[2], f[3]);
-    else
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dw) + at) =
-          make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-    return;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    float* to = reinterpret_cast<float*>(slot + slot_at(r + 4 * i, q));
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e)
+      to[e] = o + r + 4 * i < p.out && n + 4 * q + e < p.cols ? load_f32(p.add, at + 4 * i * p.ldadd + e, p.odtype) : 0.f;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (n + k < p.cols) store_from_f32(p.dw, at + k, p.odtype, f[k]);
 }
 
-// 128 values of `add` from (o, n), zeros outside it: what a running sum
-// starts from, read while the first products run.
-__device__ __forceinline__ void load_add(const WgradParams& p, int o, int n, float* v) {
-  const bool any = p.add != nullptr && p.splits == 1 && o < p.out;
-  const long long at = static_cast<long long>(o) * p.ldadd + n;
+// The slot out to the block of dw (or of a split's partial results) from (o, n).
+__device__ __forceinline__ void store_block(const WgradParams& p, float* part, const uint8_t* slot, int o, int n, int lane) {
+  const int r = lane >> 3, q = lane & 7;
+  const int dtype = part != nullptr ? DT_F32 : p.odtype;
+  const long long ld = part != nullptr ? p.cols : p.ldw;
+  void* out = part != nullptr ? part : p.dw;
+  const long long at = static_cast<long long>(o + r) * ld + n + 4 * q;
+  const bool vec = part != nullptr ? (p.cols & 3) == 0 : p.vec != 0;
+  if (vec && n + 32 <= p.cols && dtype == DT_F32) {
 #pragma unroll
-  for (int k = 0; k < 128; k += 8) {
-    if (any && p.vec_add && n + k + 8 <= p.cols) {
-      if (p.odtype == DT_F32) {
-        unpack16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + at + k), v + k);
-        unpack16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(p.add) + at + k + 4), v + k + 4);
-      } else {
-        unpack16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.add) + at + k), v + k);
-      }
+    for (int i = 0; i < 8; ++i)
+      if (o + r + 4 * i < p.out)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at + 4 * i * ld) =
+            *reinterpret_cast<const float4*>(slot + slot_at(r + 4 * i, q));
+    return;
+  }
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    if (o + r + 4 * i >= p.out) break;
+    const float4 v = *reinterpret_cast<const float4*>(slot + slot_at(r + 4 * i, q));
+    if (vec && n + 32 <= p.cols) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at + 4 * i * ld) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     } else {
+      const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k + e] = any && n + k + e < p.cols ? load_f32(p.add, at + k + e, p.odtype) : 0.f;
+      for (int e = 0; e < 4; ++e)
+        if (n + 4 * q + e < p.cols) store_from_f32(out, at + 4 * i * ld + e, dtype, f[e]);
     }
   }
 }
@@ -421,8 +429,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Item t = item_of(p, i);
       const int o0 = t.o * PT + static_cast<int>(rank) * 128 + quad * 32;
       const int n0 = t.n * PT + half * 128;
+      // a running sum starts from `add`, read while the first products run
       float v[128];
-      load_add(p, o0 + lane, n0, v);
+      const bool add = p.add != nullptr && p.splits == 1;
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        if (add) {
+          __syncwarp();
+          load_block(p, slot, o0, n0 + c, lane);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float4 x = add ? *reinterpret_cast<const float4*>(slot + slot_at(lane, q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[c + 4 * q] = x.x;
+          v[c + 4 * q + 1] = x.y;
+          v[c + 4 * q + 2] = x.z;
+          v[c + 4 * q + 3] = x.w;
+        }
+      }
       for (int k0 = t.k0; k0 < t.k1; k0 += STEPS_SUM) {
         ok = wait_warp<500>(&bar->tfull[acc], acc_ph, abort, p);
         if (!ok) break;
@@ -442,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (acc == 0) acc_ph ^= 1u;
       }
       if (!ok) break;
-      // out through shared memory, 32 x 32 at a time: eight lanes a row
+      // out through shared memory, 32 x 32 at a time
       float* part = p.splits > 1 ? p.part + static_cast<long long>(t.split) * p.out * p.cols : nullptr;
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
@@ -450,16 +475,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(slot + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+          *reinterpret_cast<float4*>(slot + slot_at(lane, q)) =
               make_float4(v[c + 4 * q], v[c + 4 * q + 1], v[c + 4 * q + 2], v[c + 4 * q + 3]);
         __syncwarp();
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int rr = 4 * it + (lane >> 3), q = lane & 7;
-          const int o = o0 + rr, n = n0 + c + 4 * q;
-          if (o < p.out && n < p.cols)
-            store4(p, part, o, n, *reinterpret_cast<const float4*>(slot + rr * 128 + ((q ^ (rr & 7)) << 4)));
-        }
+        store_block(p, part, slot, o0, n0 + c, lane);
       }
     }
   }
