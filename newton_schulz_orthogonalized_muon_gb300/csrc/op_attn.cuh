@@ -19,7 +19,6 @@ namespace attn {
 constexpr int TILE = 128;                    // rows of a tile
 constexpr int BOX_BYTES = 128 * 128;         // 128 rows x 64 16-bit columns
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr unsigned long long DRAIN_NS = 1000000000ull;
 
 template <int DP>
 __host__ __device__ constexpr int tile_bytes() {
@@ -382,52 +381,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// bits [lo, hi) of 32
+__device__ __forceinline__ uint32_t bits32(int lo, int hi) {
+  return __funnelshift_lc(0u, ~0u, max(lo, 0)) & ~__funnelshift_lc(0u, ~0u, max(hi, 0));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// 64 fp32 TMEM columns of this warp's 32 rows, times `mul`, rounded to T, out
-// to `dst` (row 0, column 0; `rows` rows and `cols` columns of it exist).  By
-// way of the warp's rows, from r0, of a box [128][64] in shared memory that
-// nothing reads any more, so that lanes next to each other write one row: a
-// row a lane took 1.7 us for a 128 x 64 tile.
-template <typename T>
-__device__ __forceinline__ void store_block(uint32_t taddr, uint32_t box, int r0, T* dst, long long stride, int rows,
-                                            int cols, float mul) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int c = 0; c < 64; c += 32) {
-    float v[32];
-    tmem_ld32(taddr + c, v);
-    tmem_ld_wait();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t r[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = pack2<T>(v[8 * q + 2 * e] * mul, v[8 * q + 2 * e + 1] * mul);
-      sts16(box + (r0 + lane) * 128 + (((c / 8 + q) ^ (lane & 7)) << 4), r);
-    }
-  }
-  __syncwarp();
-  const int q = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    if (r < rows && 8 * q < cols)
-      *reinterpret_cast<uint4*>(dst + r * stride + 8 * q) = lds16(box + (r0 + r) * 128 + ((q ^ (r & 7)) << 4));
-  }
-  __syncwarp();
-}
-
-// 32 x 32 fp32 TMEM values of this warp's rows, times `mul`, rounded to T, out
-// to `dst` (row 0, column 0; `rows` rows and `cols` columns of it exist).
+// 32 x 32 fp32 TMEM values of this warp's rows, rounded to T, out to `dst` (row
+// 0, column 0; `rows` rows and `cols` columns of it exist), the rows lane / 4 +
+// 8 k of a lane times mul[k].
 // Read in the accumulators' layout, and four lanes trade their words, so that
 // they write 64 bytes of a row: a row a lane, 16 bytes at a time, took twice
 // as long.
 template <typename T>
-__device__ __forceinline__ void store_rows(uint32_t taddr, T* dst, long long stride, int rows, int cols, float mul) {
+__device__ __forceinline__ void store_rows(uint32_t taddr, T* dst, long long stride, int rows, int cols, const float* mul) {
   if (cols <= 0) return;
   const int lane = threadIdx.x & 31, c = lane & 3;
   float v[32];
@@ -440,7 +412,7 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, T* dst, long long str
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float* u = v + 16 * (k >> 1) + 4 * q + 2 * (k & 1);
-      w[q] = pack2<T>(u[0] * mul, u[1] * mul);
+      w[q] = pack2<T>(u[0] * mul[k], u[1] * mul[k]);
     }
     // transposed over the four lanes: lane c gets columns 8 c .. 8 c + 7
 #pragma unroll
@@ -468,16 +440,6 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive_at(bar);
-}
-
-// After a wait ran out: no copy may still be in flight when the CTA's shared
-// memory goes away.  `n` tiles were issued into a ring of R.
-template <int R>
-__device__ __forceinline__ void drain_ring(uint64_t* full, int n) {
-  for (int s = 0; s < R && s < n; ++s) {
-    const int uses = (n - 1 - s) / R;
-    mbar_wait_bounded(&full[s], static_cast<uint32_t>(uses & 1), nullptr, DRAIN_NS);
-  }
 }
 
 // 2 N values of a row, rounded to T, into N = 16 or 32 TMEM columns.

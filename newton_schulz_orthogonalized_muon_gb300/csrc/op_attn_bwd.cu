@@ -505,11 +505,6 @@ struct Calc {
   Ring<2> buf, stats;
   uint32_t s_ph = 0, k_ph = 0, dv_ph = 0, done_ph = 0;
 
-  // bits [lo, hi) of 32
-  static __device__ __forceinline__ uint32_t seen(int lo, int hi) {
-    return __funnelshift_lc(0u, ~0u, max(lo, 0)) & ~__funnelshift_lc(0u, ~0u, max(hi, 0));
-  }
-
   // dk and dv.  A warp has 32 keys (TMEM rows) by 32 queries; thread t of it
   // the keys t / 4 + 8 k, k = 0 .. 3, and the queries 8 j + 2 (t % 4) + {0,
   // 1}, j = 0 .. 3.  Value (k, j, e) is v[16 (k / 2) + 4 j + 2 (k % 2) + e].
@@ -555,7 +550,7 @@ struct Calc {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int lo = j + 8 * k - off - q0 - c1;
-          const uint32_t m = seen(lo, p.window > 0 ? lo + p.window : COLS);
+          const uint32_t m = bits32(lo, p.window > 0 ? lo + p.window : COLS);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float* u = v + 16 * (k >> 1) + 4 * q + 2 * (k & 1);
@@ -632,7 +627,7 @@ struct Calc {
           hi = min(hi, q + off + 1 - j0 - c0);
           if (p.window > 0) lo = q + off - p.window + 1 - j0 - c0;
         }
-        const uint32_t m = seen(lo, hi);
+        const uint32_t m = bits32(lo, hi);
 #pragma unroll
         for (int k = 0; k < COLS; ++k)
           if (!(m & (1u << k))) v[k] = 0.f;
@@ -675,9 +670,9 @@ struct Calc {
     if (dkv) dv_ph ^= 1u;
     tc_fence_after();
     const uint32_t at = tmem + lanes + (dkv ? 2 * WT + (is_dk ? DP : 0) : 3 * WT) + col;
+    const float m = is_dv ? 1.f : p.scale, mul[4] = {m, m, m, m};
 #pragma unroll 1
-    for (int k = 0; k < width; k += 32)
-      store_rows<T>(at + k, out + k, stride, rows, p.dim - col - k, is_dv ? 1.f : p.scale);
+    for (int k = 0; k < width; k += 32) store_rows<T>(at + k, out + k, stride, rows, p.dim - col - k, mul);
     warp_arrive(BAR(acc_free));
     return true;
   }

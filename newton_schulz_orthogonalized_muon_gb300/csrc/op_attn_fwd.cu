@@ -1,15 +1,18 @@
 // Attention, forward: o_i = sum_j p_ij v_j, p_ij = exp(scale q_i . k_j -
 // lse_i), in one pass over the keys with a running maximum and sum.
 //
-// A CTA owns two tiles of 128 queries of one head and walks the key tiles
+// An item is two tiles of 128 queries of one head, which walk the key tiles
 // that they see.  Warp 0 loads by TMA, warp 1 issues every tcgen05.mma, and
 // each tile has a warpgroup of its own (warps 4 - 7, 8 - 11) with one thread a
 // query: while one tile's scores go through the exponential, the tensor pipe
-// works for the other.  The scores (fp32) and o
-// stay in TMEM; the probabilities are rounded to the operands' 16-bit type
-// and written over the scores, from where the second product takes them as
-// its A operand.  The row sum is taken from the probabilities before they
-// are rounded.
+// works for the other.  The scores (fp32) and o stay in TMEM; the
+// probabilities are rounded to the operands' 16-bit type and written over the
+// scores, from where the second product takes them as its A operand.  The row
+// sum is taken from the probabilities before they are rounded.
+//
+// A CTA that is done with its item takes over one that has not started yet
+// (a cluster launch control request), and loads it and forms its first scores
+// while the last item's outputs are written.
 //
 // The maximum that a row's exponents are taken against is raised only when a
 // new score passes it by more than 2^8 (in exp2 units): o and the sum are
@@ -19,7 +22,7 @@
 // Bound by the tensor cores and the exponentials alike: a 128 x 128 tile
 // pair with dim 128 takes 1024 cycles of products and 16384 exponentials.
 // Measured: 8192 causal tokens of 32 heads (8 of keys), dim 128, bf16, in
-// 371 us, 1480 TFLOP/s of the visible pairs' products.
+// 363 us, 1510 TFLOP/s of the visible pairs' products.
 #include <cstddef>
 
 #include "common.cuh"
@@ -44,22 +47,366 @@ struct Smem {
   static constexpr int K_OFF = 2 * T;
   static constexpr int V_OFF = K_OFF + RK * T;
   static constexpr int BAR_OFF = V_OFF + RV * T;
-  static constexpr int BYTES = BAR_OFF + 256;
+  static constexpr int BYTES = BAR_OFF + 512;
   static_assert(BYTES <= 232448, "shared memory");
 };
 
+struct Item {
+  int more;                  // 0: there is none, the CTA is done
+  int beg, end;              // key tiles of both query tiles
+  Range r[2];                // and of each
+  int i0, rows;              // the first query, and queries from there to the sequence's end
+  int nk, off;               // keys of the sequence; the position of query 0 among them
+  void* out;                 // the first query's row of o
+  float* lse;
+};
+
+// Phases are counted by the warps that wait, on through the items of a CTA.
 struct Bars {
-  uint64_t q_full[2];
+  uint64_t q_full[2], q_empty[2];
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
-  uint64_t s_full[2], p_full[2], o_done[2];
-  uint64_t drain, edge;
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t edge, asked;
+  uint64_t item_full[2], item_empty[2];
+  alignas(16) uint4 answer;           // to a request for another item
+  Item item[2];                       // announced by the loading warp
   uint32_t tmem;
   int abort;
-  Work work;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 512, "barrier block");
 // shared-memory address of a barrier; `bb` is the block's
 #define BAR(f) (bb + static_cast<uint32_t>(offsetof(Bars, f)))
+
+// Asks for a CTA of this grid that has not started; the answer is 16 bytes.
+__device__ __forceinline__ void ask_next(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+// Its number, or -1 when all have started.
+__device__ __forceinline__ int answered(uint32_t answer) {
+  int id;
+  asm volatile(
+      "{\n"
+      " .reg .b128 a;\n"
+      " .reg .pred p;\n"
+      " .reg .b32 x;\n"
+      " ld.shared.b128 a, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
+      " mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 x, a;\n"
+      " @p mov.b32 %0, x;\n"
+      "}\n"
+      : "=r"(id)
+      : "r"(answer)
+      : "memory");
+  return id;
+}
+
+// ----------------------------------------------------------------- loads
+template <typename T, int DP>
+__device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap* mq, const CUtensorMap* mk,
+                                          const CUtensorMap* mv, int tiles, uint32_t sb, uint32_t bb, Bars* bar) {
+  using S = Smem<DP>;
+  volatile int* abort = &bar->abort;
+  const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
+  Ring<S::RK> rk;
+  Ring<S::RV> rv;
+  Ring<2> items;
+  uint32_t q_ph[2] = {1u, 1u}, ask_ph = 0, edges = 0;
+  bool ok = true;
+  for (int id = static_cast<int>(blockIdx.x); ok;) {
+    __syncwarp();
+    if (lane == 0 && id >= 0) {
+      fence_proxy_async_smem();                    // every lane has read the last answer
+      mbar_expect_at(BAR(asked), 16);
+      ask_next(BAR(answer), BAR(asked));
+    }
+    Item t;
+    Work w{};
+    t.more = id >= 0;
+    if (id >= 0) {
+      w = find_work(p, true, ROWS, p.heads, tiles, static_cast<uint32_t>(id));
+      t.i0 = w.tile * ROWS;
+      t.rows = w.nq - t.i0;
+      t.nk = w.nk;
+      t.off = w.nk - w.nq;
+      t.beg = t.end = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        t.r[k] = Range{0, 0};
+        if (w.ok && k * TILE < t.rows) t.r[k] = key_tiles(p, w, t.i0 + k * TILE, min(t.i0 + (k + 1) * TILE, w.nq) - 1);
+      }
+      if (t.r[0].count > 0 || t.r[1].count > 0) {
+        t.beg = t.r[0].count == 0 ? t.r[1].first : t.r[1].count == 0 ? t.r[0].first : min(t.r[0].first, t.r[1].first);
+        t.end = max(t.r[0].first + t.r[0].count, t.r[1].first + t.r[1].count);
+      }
+      const long long q0 = w.q0 + t.i0;
+      t.out = static_cast<T*>(p.out) + w.b * p.ob + q0 * p.os + w.h * p.oh;
+      t.lse = p.lse + w.b * p.lse_b + w.h * p.lse_h + q0;
+    }
+    if (w.ok || id < 0) {
+      ok = wait_warp(BAR(item_empty) + 8 * items.s, items.ph ^ 1u, abort, p);
+      if (!ok) break;
+      if (lane == 0) {
+        bar->item[items.s] = t;
+        mbar_arrive_at(BAR(item_full) + 8 * items.s);
+      }
+      items.next();
+    }
+    if (id < 0) break;
+    if (t.end > t.beg) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (ok && t.r[k].count > 0) {
+          ok = wait_warp(BAR(q_empty) + 8 * k, q_ph[k], abort, p);
+          q_ph[k] ^= 1u;
+          if (ok && lane == 0) {
+            mbar_expect_at(BAR(q_full) + 8 * k, S::T);
+            load_tile<DP>(sb + k * S::T, mq, BAR(q_full) + 8 * k, w.h, w.q0 + t.i0 + k * TILE, w.b);
+          }
+        }
+      }
+      const int hk = w.h / group;
+      for (int tile = t.beg; ok && tile < t.end; ++tile) {
+        const int row = w.k0 + tile * TILE, valid = w.nk - tile * TILE;
+        ok = wait_warp(BAR(k_empty) + 8 * rk.s, rk.ph ^ 1u, abort, p);
+        if (!ok) break;
+        if (lane == 0) {
+          // rows past the sequence give scores that are masked, whatever they hold
+          mbar_expect_at(BAR(k_full) + 8 * rk.s, S::T);
+          load_tile<DP>(sb + S::K_OFF + rk.s * S::T, mk, BAR(k_full) + 8 * rk.s, hk, row, w.b);
+        }
+        rk.next();
+        ok = wait_warp(BAR(v_empty) + 8 * rv.s, rv.ph ^ 1u, abort, p);
+        if (!ok) break;
+        const bool edge = p.cu_q != nullptr && valid < TILE;
+        const uint32_t vt = sb + S::V_OFF + rv.s * S::T, fv = BAR(v_full) + 8 * rv.s;
+        if (lane == 0) {
+          mbar_expect_at(edge ? BAR(edge) : fv, S::T);
+          load_tile<DP>(vt, mv, edge ? BAR(edge) : fv, hk, row, w.b);
+        }
+        if (edge) {
+          ok = finish_edge_tile<DP>(vt, BAR(edge), edges, valid, abort, p);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_at(fv);
+        }
+        rv.next();
+      }
+    }
+    ok = ok && wait_warp(BAR(asked), ask_ph, abort, p);
+    if (!ok) break;
+    ask_ph ^= 1u;
+    id = answered(BAR(answer));
+  }
+  // after a wait ran out: a millisecond for copies in flight to land
+  if (*abort != 0 && lane == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  __syncwarp();
+}
+
+// -------------------------------------------------------------- products
+template <typename T, int DP>
+__device__ __forceinline__ void product_role(const AttnParams& p, uint32_t sb, uint32_t bb, uint32_t tmem, Bars* bar) {
+  using S = Smem<DP>;
+  volatile int* abort = &bar->abort;
+  Ring<S::RK> rk;                                // the K tile of the scores to come
+  Ring<S::RV> rv;
+  Ring<2> items;
+  uint32_t q_ph[2] = {0u, 0u}, p_ph[2] = {0u, 0u}, free_ph[2] = {1u, 1u};
+  bool ok = true;
+  while (ok && wait_warp(BAR(item_full) + 8 * items.s, items.ph, abort, p)) {
+    const Item& t = bar->item[items.s];
+    const bool more = t.more != 0;
+    const int beg = t.beg, end = t.end, first[2] = {t.r[0].first, t.r[1].first},
+              last[2] = {t.r[0].first + t.r[0].count - 1, t.r[1].first + t.r[1].count - 1};
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_at(BAR(item_empty) + 8 * items.s);
+    items.next();
+    if (!more) break;
+    if (end <= beg) continue;
+    auto sees = [&](int k, int tile) { return tile >= first[k] && tile <= last[k]; };
+    auto scores = [&](int k, int tile) {
+      mma_over_dim<T, DP>(tmem + k * TILE, desc_dim(sb + k * S::T), desc_dim(sb + S::K_OFF + rk.s * S::T));
+      commit_warp(BAR(s_full) + 8 * k);
+      if (tile == last[k]) commit_warp(BAR(q_empty) + 8 * k);
+    };
+    uint32_t acc[2] = {0u, 0u};
+    ok = wait_warp(BAR(k_full) + 8 * rk.s, rk.ph, abort, p);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (ok && last[k] >= first[k]) {
+        ok = wait_warp(BAR(q_full) + 8 * k, q_ph[k], abort, p);
+        q_ph[k] ^= 1u;
+      }
+      if (ok && sees(k, beg)) {
+        tc_fence_after();
+        scores(k, beg);
+      }
+    }
+    if (ok) commit_warp(BAR(k_empty) + 8 * rk.s);
+    rk.next();
+    for (int tile = beg; ok && tile < end; ++tile) {
+      const bool next = tile + 1 < end;
+      // this step's tiles before the probabilities, so that no wait stands between products
+      ok = wait_warp(BAR(v_full) + 8 * rv.s, rv.ph, abort, p) &&
+           (!next || wait_warp(BAR(k_full) + 8 * rk.s, rk.ph, abort, p));
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (ok && sees(k, tile)) {
+          ok = wait_warp(BAR(p_full) + 8 * k, p_ph[k], abort, p);
+          p_ph[k] ^= 1u;
+          if (ok && acc[k] == 0u) {              // over the last item's o
+            ok = wait_warp(BAR(o_free) + 8 * k, free_ph[k], abort, p);
+            free_ph[k] ^= 1u;
+          }
+          if (ok) {
+            tc_fence_after();
+            mma_over_tokens<T, DP, TILE>(tmem + 256 + k * TILE, tmem + k * TILE,
+                                         desc_tokens(sb + S::V_OFF + rv.s * S::T), acc[k]);
+            commit_warp(BAR(o_done) + 8 * k);
+            acc[k] = 1u;
+          }
+        }
+        // over the probabilities just used: the tensor pipe runs in order
+        if (ok && next && sees(k, tile + 1)) scores(k, tile + 1);
+      }
+      if (!ok) break;
+      commit_warp(BAR(v_empty) + 8 * rv.s);
+      rv.next();
+      if (next) {
+        commit_warp(BAR(k_empty) + 8 * rk.s);
+        rk.next();
+      }
+    }
+  }
+  // after a wait ran out: the products in flight end by themselves, a millisecond for them
+  if (*abort != 0 && (threadIdx.x & 31) == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------- softmax, output
+template <typename T, int DP>
+__device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, uint32_t tmem, Bars* bar) {
+  volatile int* abort = &bar->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = (warp - CTRL_WARPS) >> 2, quad = warp & 3;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t s_at = tmem + lanes + t * TILE, o_at = tmem + lanes + 256 + t * TILE;
+  const float c = p.scale * LOG2E;
+  const F2 cc = f2_make(c, c);
+  Ring<2> items;
+  uint32_t steps = 0;                              // of this tile so far: the phases of its barriers
+  while (wait_warp(BAR(item_full) + 8 * items.s, items.ph, abort, p)) {
+    const Item& it = bar->item[items.s];
+    if (it.more == 0) break;
+    const int cnt = it.r[t].count, i0 = it.i0, nk = it.nk, off = it.off, first = it.r[t].first;
+    const int q0 = i0 + t * TILE, q = q0 + quad * 32 + lane;
+    float top = -INFINITY;                         // the scores' reference, before scaling
+    F2 sum2 = f2_make(0.f, 0.f);
+    bool ok = true;
+    for (int i = 0; i < cnt; ++i, ++steps) {
+      const int j0 = (first + i) * TILE;
+      float v[TILE];
+      ok = wait_warp(BAR(s_full) + 8 * t, steps & 1u, abort, p);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < TILE; k += 32) tmem_ld32(s_at + k, v + k);
+      tmem_ld_wait();
+      if (j0 + TILE > nk ||
+          (p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window)))) {
+        int lo = 0, hi = nk - j0;
+        if (p.causal) {
+          hi = min(hi, q + off + 1 - j0);
+          if (p.window > 0) lo = q + off - p.window + 1 - j0;
+        }
+#pragma unroll
+        for (int k = 0; k < TILE; k += 32) {
+          const uint32_t m = bits32(lo - k, hi - k);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(m & (1u << e))) v[k + e] = -INFINITY;
+        }
+      }
+      float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int k = 4; k < TILE; k += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = k + 4 + e < TILE ? fmaxf(fmaxf(m[e], v[k + e]), v[k + 4 + e]) : fmaxf(m[e], v[k + e]);
+      }
+      const float mt = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+      if (i == 0) {
+        top = mt;
+      } else {
+        const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
+        if (__any_sync(0xffffffffu, up)) {
+          ok = wait_warp(BAR(o_done) + 8 * t, (steps - 1) & 1u, abort, p);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = !up ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - mt) * c);
+          if (up) top = mt;
+          sum2 = f2_mul(sum2, f2_make(f, f));
+#pragma unroll 1
+          for (int k = 0; k < DP; k += 32) {
+            float o[32];
+            tmem_ld32(o_at + k, o);
+            tmem_ld_wait();
+            uint32_t* u = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(o_at + k, u);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float ref = top == -INFINITY ? 0.f : -top * c;
+      const F2 rr = f2_make(ref, ref);
+#pragma unroll
+      for (int k = 0; k < TILE; k += 64) {
+#pragma unroll
+        for (int e = k; e < k + 64; e += 2) {
+          const float2 a = f2_split(f2_fma(f2_make(v[e], v[e + 1]), cc, rr));
+          v[e] = exp2_fast(a.x);
+          v[e + 1] = exp2_fast(a.y);
+          sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
+        }
+        store_rounded<T, 32>(s_at + k / 2, v + k);
+      }
+      warp_arrive(BAR(p_full) + 8 * t);
+    }
+    if (ok && cnt > 0) ok = wait_warp(BAR(o_done) + 8 * t, (steps - 1) & 1u, abort, p);
+    if (!ok) break;
+    tc_fence_after();
+    const float2 s2 = f2_split(sum2);
+    const float sum = s2.x + s2.y, inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int row = t * TILE + quad * 32, rows = it.rows - row;      // the warp's first query, and queries from it on
+    T* out = static_cast<T*>(it.out) + row * p.os;
+    if (lane < rows) it.lse[row + lane] = sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
+    if (cnt > 0) {
+      float mul[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mul[k] = __shfl_sync(0xffffffffu, inv, (lane >> 2) + 8 * k);
+#pragma unroll 1
+      for (int k = 0; k < DP; k += 32) store_rows<T>(o_at + k, out + k, p.os, rows, p.dim - k, mul);
+      warp_arrive(BAR(o_free) + 8 * t);
+    } else if (lane < rows) {
+      for (int k = 0; k < p.dim; k += 8) *reinterpret_cast<uint4*>(out + lane * p.os + k) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(BAR(item_empty) + 8 * items.s);
+    items.next();
+  }
+}
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -71,260 +418,42 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sb = smem_u32(smem), bb = sb + S::BAR_OFF;
   if (!swizzle_aligned(sb, p)) return;
-  if (warp == 0) {
-    const Work w = find_work(p, true, ROWS, p.heads, tiles, blockIdx.x);
-    if (lane == 0) {
-      bar->work = w;
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&bar->q_full[i], 1);
-        mbar_init(&bar->s_full[i], 1);
-        mbar_init(&bar->p_full[i], 4);
-        mbar_init(&bar->o_done[i], 1);
-      }
-      for (int i = 0; i < 3; ++i) {
-        mbar_init(&bar->k_full[i], 1);
-        mbar_init(&bar->k_empty[i], 1);
-        mbar_init(&bar->v_full[i], 1);
-        mbar_init(&bar->v_empty[i], 1);
-      }
-      mbar_init(&bar->drain, 1);
-      mbar_init(&bar->edge, 1);
-      bar->abort = 0;
-      fence_mbar_init();
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->q_full[i], 1);
+      mbar_init(&bar->q_empty[i], 1);
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->o_done[i], 1);
+      mbar_init(&bar->o_free[i], 4);
+      mbar_init(&bar->item_full[i], 1);
+      mbar_init(&bar->item_empty[i], 1 + 8);
     }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
+    }
+    mbar_init(&bar->edge, 1);
+    mbar_init(&bar->asked, 1);
+    bar->abort = 0;
+    fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&bar->tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Work w = bar->work;
-  volatile int* abort = &bar->abort;
   const uint32_t tmem = bar->tmem;
-  const int hk = w.h / (p.heads / p.kv_heads);
-  const int i0 = w.tile * ROWS;
-  // key tiles of each query tile, and of both
-  Range r[2] = {{0, 0}, {0, 0}};
-  if (w.ok) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (i0 + t * TILE < w.nq) r[t] = key_tiles(p, w, i0 + t * TILE, min(i0 + (t + 1) * TILE, w.nq) - 1);
-  }
-  int beg = 0, end = 0;
-  if (r[0].count > 0 || r[1].count > 0) {
-    beg = r[0].count == 0 ? r[1].first : r[1].count == 0 ? r[0].first : min(r[0].first, r[1].first);
-    end = max(r[0].first + r[0].count, r[1].first + r[1].count);
-  }
-  const int n = end - beg;
-  auto sees = [&](int t, int tile) { return tile >= r[t].first && tile < r[t].first + r[t].count; };
-
   // a softmax thread holds a row of 128 scores: registers move from the
   // control warps (4 x 32 x 88 + 8 x 32 x 200 of the 384 x 168 at launch)
   if (warp < CTRL_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0 && n > 0) {
-      // ---------------------------------------------------------- loads
-      if (lane == 0) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (r[t].count > 0) {
-            mbar_expect_at(BAR(q_full) + 8 * t, S::T);
-            load_tile<DP>(sb + t * S::T, &mq, BAR(q_full) + 8 * t, w.h, w.q0 + i0 + t * TILE, w.b);
-          }
-        }
-      }
-      uint32_t edges = 0;
-      int ik = 0, iv = 0;
-      for (int i = 0; i < n; ++i) {
-        const int j = (beg + i) * TILE, row = w.k0 + j, valid = w.nk - j;
-        const int sk = i % S::RK, sv = i % S::RV;
-        if (i >= S::RK && !wait_warp(BAR(k_empty) + 8 * sk, (i / S::RK - 1) & 1, abort, p)) break;
-        if (lane == 0) {
-          // rows past the sequence give scores that are masked, whatever they hold
-          mbar_expect_at(BAR(k_full) + 8 * sk, S::T);
-          load_tile<DP>(sb + S::K_OFF + sk * S::T, &mk, BAR(k_full) + 8 * sk, hk, row, w.b);
-        }
-        ++ik;
-        if (i >= S::RV && !wait_warp(BAR(v_empty) + 8 * sv, (i / S::RV - 1) & 1, abort, p)) break;
-        const bool edge = p.cu_q != nullptr && valid < TILE;
-        const uint32_t vt = sb + S::V_OFF + sv * S::T, fv = BAR(v_full) + 8 * sv;
-        if (lane == 0) {
-          mbar_expect_at(edge ? BAR(edge) : fv, S::T);
-          load_tile<DP>(vt, &mv, edge ? BAR(edge) : fv, hk, row, w.b);
-        }
-        if (edge) {
-          if (!finish_edge_tile<DP>(vt, BAR(edge), edges, valid, abort, p)) break;
-          if (lane == 0) mbar_arrive_at(fv);
-        }
-        ++iv;
-      }
-      if (*abort != 0 && lane == 0) {
-        for (int t = 0; t < 2; ++t)
-          if (r[t].count > 0) mbar_wait_bounded(&bar->q_full[t], 0, nullptr, DRAIN_NS);
-        drain_ring<S::RK>(bar->k_full, ik);
-        drain_ring<S::RV>(bar->v_full, iv);
-      }
-      __syncwarp();
-    } else if (warp == 1 && n > 0) {
-      // -------------------------------------------------------- products
-      Ring<S::RK> rk;                              // the K tile of the scores to come
-      Ring<S::RV> rv;
-      uint32_t ph[2] = {0u, 0u}, acc[2] = {0u, 0u};
-      auto scores = [&](int t) {
-        mma_over_dim<T, DP>(tmem + t * TILE, desc_dim(sb + t * S::T), desc_dim(sb + S::K_OFF + rk.s * S::T));
-        commit_warp(BAR(s_full) + 8 * t);
-      };
-      bool ok = wait_warp(BAR(k_full), 0, abort, p);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (ok && r[t].count > 0) ok = wait_warp(BAR(q_full) + 8 * t, 0, abort, p);
-        if (ok && sees(t, beg)) {
-          tc_fence_after();
-          scores(t);
-        }
-      }
-      if (ok) commit_warp(BAR(k_empty));
-      rk.next();
-      for (int tile = beg; ok && tile < end; ++tile) {
-        const bool more = tile + 1 < end;
-        // this step's tiles before the probabilities, so that no wait stands between products
-        ok = wait_warp(BAR(v_full) + 8 * rv.s, rv.ph, abort, p) &&
-             (!more || wait_warp(BAR(k_full) + 8 * rk.s, rk.ph, abort, p));
-        if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (ok && sees(t, tile)) {
-            ok = wait_warp(BAR(p_full) + 8 * t, ph[t], abort, p);
-            if (ok) {
-              tc_fence_after();
-              mma_over_tokens<T, DP, TILE>(tmem + 256 + t * TILE, tmem + t * TILE,
-                                           desc_tokens(sb + S::V_OFF + rv.s * S::T), acc[t]);
-              commit_warp(BAR(o_done) + 8 * t);
-              ph[t] ^= 1u;
-              acc[t] = 1u;
-            }
-          }
-          // over the probabilities just used: the tensor pipe runs in order
-          if (ok && more && sees(t, tile + 1)) scores(t);
-        }
-        if (!ok) break;
-        commit_warp(BAR(v_empty) + 8 * rv.s);
-        rv.next();
-        if (more) {
-          commit_warp(BAR(k_empty) + 8 * rk.s);
-          rk.next();
-        }
-      }
-      if (!ok) {
-        commit_warp(BAR(drain));
-        if (lane == 0) mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
-        __syncwarp();
-      }
-    }
+    if (warp == 0) load_role<T, DP>(p, &mq, &mk, &mv, tiles, sb, bb, bar);
+    if (warp == 1) product_role<T, DP>(p, sb, bb, tmem, bar);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    if (w.ok) {
-      // ------------------------------------------------ softmax, output
-      const int t = (warp - CTRL_WARPS) >> 2, quad = warp & 3;
-      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-      const uint32_t s_at = tmem + lanes + t * TILE, o_at = tmem + lanes + 256 + t * TILE;
-      const int q0 = i0 + t * TILE, q = q0 + quad * 32 + lane;
-      const int off = w.nk - w.nq;
-      const float c = p.scale * LOG2E;
-      float top = -INFINITY;                         // the scores' reference, before scaling
-      F2 sum2 = f2_make(0.f, 0.f);
-      bool ok = true;
-      const int cnt = r[t].count;
-      for (int i = 0; i < cnt; ++i) {
-        const int j0 = (r[t].first + i) * TILE;
-        float v[TILE];
-        ok = wait_warp(BAR(s_full) + 8 * t, i & 1, abort, p);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < TILE; k += 32) tmem_ld32(s_at + k, v + k);
-        tmem_ld_wait();
-        if (j0 + TILE > w.nk ||
-            (p.causal && (j0 + TILE - 1 > q0 + off || (p.window > 0 && q0 + TILE - 1 + off - j0 >= p.window)))) {
-          int lo = 0, hi = w.nk - j0;
-          if (p.causal) {
-            hi = min(hi, q + off + 1 - j0);
-            if (p.window > 0) lo = q + off - p.window + 1 - j0;
-          }
-#pragma unroll
-          for (int k = 0; k < TILE; ++k)
-            if (k < lo || k >= hi) v[k] = -INFINITY;
-        }
-        float m[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int k = 4; k < TILE; k += 8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m[e] = k + 4 + e < TILE ? fmaxf(fmaxf(m[e], v[k + e]), v[k + 4 + e]) : fmaxf(m[e], v[k + e]);
-        }
-        const float mt = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        if (i == 0) {
-          top = mt;
-        } else {
-          const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
-          if (__any_sync(0xffffffffu, up)) {
-            ok = wait_warp(BAR(o_done) + 8 * t, (i - 1) & 1, abort, p);
-            if (!ok) break;
-            tc_fence_after();
-            const float f = !up ? 1.f : top == -INFINITY ? 0.f : exp2_fast((top - mt) * c);
-            if (up) top = mt;
-            sum2 = f2_mul(sum2, f2_make(f, f));
-#pragma unroll 1
-            for (int k = 0; k < DP; k += 32) {
-              float o[32];
-              tmem_ld32(o_at + k, o);
-              tmem_ld_wait();
-              uint32_t* u = reinterpret_cast<uint32_t*>(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(o_at + k, u);
-            }
-            tmem_st_wait();
-          }
-        }
-        const float ref = top == -INFINITY ? 0.f : -top * c;
-        const F2 cc = f2_make(c, c), rr = f2_make(ref, ref);
-#pragma unroll
-        for (int k = 0; k < TILE; k += 64) {
-#pragma unroll
-          for (int e = k; e < k + 64; e += 2) {
-            const float2 a = f2_split(f2_fma(f2_make(v[e], v[e + 1]), cc, rr));
-            v[e] = exp2_fast(a.x);
-            v[e + 1] = exp2_fast(a.y);
-            sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
-          }
-          store_rounded<T, 32>(s_at + k / 2, v + k);
-        }
-        warp_arrive(BAR(p_full) + 8 * t);
-      }
-      if (ok && cnt > 0) {
-        ok = wait_warp(BAR(o_done) + 8 * t, (cnt - 1) & 1, abort, p);
-        tc_fence_after();
-      }
-      if (ok) {
-        const float2 s2 = f2_split(sum2);
-        const float sum = s2.x + s2.y;
-        const int first = q0 + quad * 32;          // of the warp's queries
-        T* out = static_cast<T*>(p.out) + w.b * p.ob + static_cast<long long>(w.q0 + first) * p.os + w.h * p.oh;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (cnt > 0) {
-          // through this tile's Q, which every product has read
-#pragma unroll
-          for (int x = 0; x < DP / 64; ++x)
-            store_block<T>(o_at + 64 * x, sb + t * S::T + x * BOX_BYTES, quad * 32, out + 64 * x, p.os, w.nq - first,
-                           p.dim - 64 * x, inv);
-        } else if (q < w.nq) {
-          for (int k = 0; k < p.dim; k += 8)
-            *reinterpret_cast<uint4*>(out + lane * p.os + k) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (q < w.nq)
-          p.lse[w.b * p.lse_b + w.h * p.lse_h + w.q0 + q] =
-              sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
-      }
-    }
+    softmax_role<T, DP>(p, bb, tmem, bar);
   }
   tc_fence_before();
   __syncthreads();
