@@ -236,6 +236,12 @@ __device__ __forceinline__ void store_partial(const NormParams& p, const float* 
   if (grp == 0) store_sums<T, VEC, TPR, EPT>(p, acc, t);
 }
 
+// mean(d^2) about a mean that is `off` too small: not below 0, NaN stays.
+__device__ __forceinline__ float variance(float sq, float off) {
+  const float v = fmaf(-off, off, sq);
+  return v < 0.f ? 0.f : v;
+}
+
 // ---------------------------------------------------------- row kernels
 // One row at a time and CTA (of TPR threads; four rows of a warp each when
 // one warp is enough), for rows that the batch kernels do not take.
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(RowCfg<TPR>::THREADS) norm_row_fwd_kernel(cons
     // differences, the variance and the mean itself
     group_sum<TPR, 2>(s, red[grp][1], grp);
     const float off = s[1] * inv;
-    const float r = rsqrtf(fmaxf(fmaf(-off, off, s[0] * inv), 0.f) + p.eps);
+    const float r = rsqrtf(variance(s[0] * inv, off) + p.eps);
     float w[EPT];
     load_affine<VEC, TPR, EPT, T>(p, p.weight, 1.f, t, w);
 #pragma unroll
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(CALC + 32, 1) norm_batch_kernel(const NormPara
           if (row >= p.rows) break;
           // what the sum's rounding left in mu, as in the row kernel
           const float off = s[2 * r + 1] * inv;
-          const float rs = rsqrtf(fmaxf(fmaf(-off, off, s[2 * r] * inv), 0.f) + p.eps);
+          const float rs = rsqrtf(variance(s[2 * r] * inv, off) + p.eps);
           const F2 no = f2_make(-off, -off), rr = f2_make(rs, rs);
 #pragma unroll
           for (int e = 0; e < H; ++e) v[r][e] = f2_fma(f2_mul(f2_add(v[r][e], no), rr), w[e], b[e]);

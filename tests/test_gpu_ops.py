@@ -151,6 +151,16 @@ def test_layer_norm_nan_stays_in_its_row(muon):
     assert got[2].isnan().all() and torch.equal(got[[0, 1, 3, 4]], want[[0, 1, 3, 4]])
 
 
+@pytest.mark.parametrize("cols", [512, 513])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_layer_norm_statistics_of_a_row_that_is_not_finite(muon, cols, value):
+    x = rand(12, 3, cols, dtype=BF)
+    x[1, 5] = value
+    _, mean, rstd = muon.layer_norm(x)
+    assert mean[1].isnan() and rstd[1].isnan()
+    assert mean[[0, 2]].isfinite().all() and rstd[[0, 2]].isfinite().all()
+
+
 # ----------------------------------------------------------------- attention
 ATTN = [  # batch, sq, sk, heads, kv_heads, dim, causal, window, dtype
     (1, 1, 1, 1, 1, 8, True, 0, BF), (2, 61, 61, 3, 3, 64, True, 0, BF), (1, 128, 128, 2, 1, 128, True, 0, BF),
