@@ -369,11 +369,12 @@ muon_status_t muon_attention_workspace(muon_handle_t h, const muon_attention_t* 
  * with a 2^-e <= 448.  The scale byte is e + 127.  A block with a NaN or an
  * infinity gets the byte 255 and codes 0, which stand for NaN.
  *   x       dtype, [rows][cols], row stride ldx
- *   codes   [rows], row stride ldc bytes: a multiple of 128, >= cols; the
- *           codes past the last column up to the block's end are set to 0;
- *           16-byte aligned
- *   scales  [ceil(cols / 128)], lds bytes apart: a multiple of 16, >= rows;
- *           one byte a row; 16-byte aligned */
+ *   codes   [rows][cols], row stride ldc bytes: a multiple of 128, >= cols;
+ *           16-byte aligned; nothing past the last column is written
+ *   scales  [ceil(cols / 128)][rows], lds bytes apart: a multiple of 16, >=
+ *           rows; one byte a row; 16-byte aligned.  Both are read in whole
+ *           groups of 8 (codes) and 16 (scales) bytes: bytes past the last
+ *           row or column in such a group are loaded, and have no part. */
 muon_status_t muon_act8_store(muon_handle_t h, const void* x, int64_t ldx, uint8_t* codes, int64_t ldc,
                               uint8_t* scales, int64_t lds, int64_t rows, int64_t cols, int32_t dtype, void* stream);
 /* out[r][c] = code 2^e, rounded to dtype (exact in fp32, and in bf16 below

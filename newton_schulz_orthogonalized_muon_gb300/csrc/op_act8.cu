@@ -15,7 +15,7 @@
 // handles its 16 rows of one block column two at a time, and 16 lanes write
 // the rows' scale bytes at once (scales lie block column by block column,
 // one byte a row, as the weight-gradient kernel reads them).  Measured at
-// 16384 x 14336 bf16: stored in 117 us (6.0 TB/s), restored in 106 us (6.6).
+// 16384 x 14336 bf16: stored in 119 us (5.9 TB/s), restored in 106 us (6.6).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -107,13 +107,11 @@ __device__ __forceinline__ void e4m3x4_values(uint32_t w, float unit, float* f) 
 }
 
 // A warp takes AROWS rows of one block column, two rows at a time, with the
-// loads of AHEAD row pairs in flight: 2 pairs took 132 us, 4 117 us, 8 (with
+// loads of AHEAD row pairs in flight: 2 pairs took 132 us, 4 119 us, 8 (with
 // fewer warps on an SM) 126 us at 16384 x 14336.  The instructions count as
-// well: with the maximum taken one value at a time 4 pairs took 130 us.  Rows of codes are padded to whole
-// blocks, so a lane always writes its eight bytes; columns past the last get
-// code 0.
+// well: with the maximum taken one value at a time 4 pairs took 130 us.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(AWARPS * 32) act8_store_kernel(const Act8Params p, int blocks) {
+__global__ void __launch_bounds__(AWARPS * 32, VEC && sizeof(T) == 2 ? 6 : 4) act8_store_kernel(const Act8Params p, int blocks) {
   constexpr int AHEAD = 4;
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   const long long groups = (p.rows + AROWS - 1) / AROWS;
@@ -122,6 +120,7 @@ __global__ void __launch_bounds__(AWARPS * 32) act8_store_kernel(const Act8Param
   const int blk = static_cast<int>(item % blocks);
   const long long r0 = item / blocks * AROWS;
   const int c = blk * ABLK + l * 8;
+  const long long rows = c < p.cols ? p.rows : 0;      // that this lane has codes of
   int mine = 0;                       // an even lane's: scale byte of row r0 + l + half
 #pragma unroll
   for (int i0 = 0; i0 < AROWS; i0 += 2 * AHEAD) {
@@ -149,7 +148,15 @@ __global__ void __launch_bounds__(AWARPS * 32) act8_store_kernel(const Act8Param
         f[k + 1] = v.y;
       }
       const uint32_t lo = e4m3x4(f), hi = e4m3x4(f + 4);
-      if (r < p.rows) *reinterpret_cast<uint2*>(p.codes + r * p.ldc + c) = fine ? make_uint2(lo, hi) : make_uint2(0u, 0u);
+      const uint2 code = fine ? make_uint2(lo, hi) : make_uint2(0u, 0u);
+      if (r < rows) {
+        uint8_t* to = p.codes + r * p.ldc + c;
+        if (VEC || c + 8 <= p.cols) {
+          *reinterpret_cast<uint2*>(to) = code;
+        } else {
+          for (int k = 0; c + k < p.cols; ++k) to[k] = static_cast<uint8_t>((k < 4 ? code.x : code.y) >> (8 * (k & 3)));
+        }
+      }
       if (l == i) mine = e;
     }
   }
@@ -157,8 +164,12 @@ __global__ void __launch_bounds__(AWARPS * 32) act8_store_kernel(const Act8Param
   if (l % 2 == 0 && r < p.rows) p.scales[blk * p.lds + r] = static_cast<uint8_t>(mine);
 }
 
+// Rows that 16-byte stores do not fit go by way of shared memory, so that a
+// warp's lanes write elements next to each other: 16384 x 14330 bf16 took 644
+// us with eight elements a lane.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(AWARPS * 32) act8_restore_kernel(const Act8Params p, int blocks) {
+  __shared__ __align__(16) T rows[VEC ? 1 : AWARPS][2][VEC ? 8 : ABLK];
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   const long long groups = (p.rows + AROWS - 1) / AROWS;
   const long long item = static_cast<long long>(blockIdx.x) * AWARPS + (threadIdx.x >> 5);
@@ -166,33 +177,45 @@ __global__ void __launch_bounds__(AWARPS * 32) act8_restore_kernel(const Act8Par
   const int blk = static_cast<int>(item % blocks);
   const long long r0 = item / blocks * AROWS;
   const int c = blk * ABLK + l * 8;
-  if (c >= p.cols) return;
+  const bool live = c < p.cols;
   uint2 w[AROWS / 2];
   int e[AROWS / 2];
 #pragma unroll
   for (int j = 0; j < AROWS / 2; ++j) {
     const long long r = r0 + 2 * j + half;
-    const bool in = r < p.rows;
+    const bool in = live && r < p.rows;
     w[j] = in ? *reinterpret_cast<const uint2*>(p.codes + r * p.ldc + c) : make_uint2(0u, 0u);
     e[j] = in ? p.scales[blk * p.lds + r] : 0;
   }
+  T* out = static_cast<T*>(p.out);
 #pragma unroll
   for (int j = 0; j < AROWS / 2; ++j) {
-    const long long r = r0 + 2 * j + half;
+    const long long r = r0 + 2 * j;
     if (r >= p.rows) break;
     float f[8];
     const float unit = __int_as_float(e[j] << 23);              // 255: infinity, times code 0: NaN
     e4m3x4_values(w[j].x, unit, f);
     e4m3x4_values(w[j].y, unit, f + 4);
-    T* row = static_cast<T*>(p.out) + r * p.ldx;
+    constexpr int kStep = 16 / static_cast<int>(sizeof(T));
     if constexpr (VEC) {
+      if (live && r + half < p.rows) {
 #pragma unroll
-      for (int i = 0; i < 8; i += 16 / static_cast<int>(sizeof(T)))
-        *reinterpret_cast<uint4*>(row + c + i) = pack16<T>(f + i);
+        for (int i = 0; i < 8; i += kStep) *reinterpret_cast<uint4*>(out + (r + half) * p.ldx + c + i) = pack16<T>(f + i);
+      }
     } else {
+      T(*to)[ABLK] = rows[threadIdx.x >> 5];
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < p.cols) row[c + i] = from_f32<T>(f[i]);
+      for (int i = 0; i < 8; i += kStep) *reinterpret_cast<uint4*>(&to[half][l * 8 + i]) = pack16<T>(f + i);
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (r + h >= p.rows) break;
+        T* row = out + (r + h) * p.ldx + blk * ABLK;
+#pragma unroll
+        for (int i = lane; i < ABLK; i += 32)
+          if (blk * ABLK + i < p.cols) row[i] = to[h][i];
+      }
     }
   }
 }

@@ -298,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 mbar_arrive_expect_tx(cf, BOX);
                 tma_load_3d(sb + CODE_OFF + rc.s * BOX, &mcode, cf, blk * 128, k * BK, 0);
               } else if (live) {
-                // the step's scale bytes, whole 16-byte groups (storage is padded to them)
+                // the step's scale bytes, whole 16-byte groups (lds is a multiple of them)
                 const long long t0 = static_cast<long long>(k) * BK;
                 const uint32_t bytes = p.rows - t0 >= BK ? BK : static_cast<uint32_t>((p.rows - t0 + 15) / 16 * 16);
                 mbar_arrive_expect_tx(cf, bytes);

@@ -463,7 +463,7 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
       }
       if (rows == 1) ld = (out + 7) / 8 * 8;
       if (!rows_map(h, &maps[0], base, out, rows, ld, 2, 64) ||
-          !rows_map(h, &maps[1], codes, (cols + 127) / 128 * 128, rows, ldc, 1, 128))
+          !rows_map(h, &maps[1], codes, cols, rows, ldc, 1, 128))
         return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     }
     MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, maps, h->num_sms / 2, stream), "weight gradient launch");

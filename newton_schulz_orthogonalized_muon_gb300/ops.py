@@ -315,10 +315,9 @@ def act8_store(x, *, handle=None, stream=None):
     rows], one exponent a row and 128 columns: the stored value is code times
     2^(scale - 127), with the smallest power of two that fits the block's
     largest value (at least 2^-111).  A block with a NaN or an infinity is
-    stored as scale 255, codes 0 and stands for NaN.  Both are views of
-    padded storage (whole blocks, 16 rows), which act8_weight_grad reads in
-    place; copies in other layouts are taken too, at the cost of one more
-    copy."""
+    stored as scale 255, codes 0 and stands for NaN.  Both have padded row
+    strides (whole blocks, 16 rows), which act8_weight_grad reads in place;
+    copies in other layouts are taken too, at the cost of one more copy."""
     if stream is not None:
         with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
             return act8_store(x, handle=handle)
@@ -332,13 +331,13 @@ def act8_store(x, *, handle=None, stream=None):
     blocks, lds = -(-cols // BLOCK), -(-rows // 16) * 16
     ldc = blocks * BLOCK
     where = x.device
-    codes = torch.empty((rows, ldc), dtype=torch.float8_e4m3fn, device=where)
-    scales = torch.empty((blocks, lds), dtype=torch.uint8, device=where)
+    codes = torch.empty_strided((rows, cols), (ldc, 1), dtype=torch.float8_e4m3fn, device=where)
+    scales = torch.empty_strided((blocks, rows), (lds, 1), dtype=torch.uint8, device=where)
     st = h._lib.muon_act8_store(h.ptr, xr.data_ptr(), ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, rows, cols,
                                 code, _raw_stream(dev))
     if st:
         h._raise(st, "muon_act8_store")
-    return codes if ldc == cols else codes.narrow(1, 0, cols), scales if lds == rows else scales.narrow(1, 0, rows)
+    return codes, scales
 
 
 def _act8_operands(codes, scales):

@@ -366,6 +366,22 @@ def test_act8_codes_are_exact(muon, rows, cols, pad, dtype):
         assert np.array_equal(host(got), ref, equal_nan=True), out
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 5), (17, 128), (6, 1001)])
+def test_act8_writes_its_codes_and_scales_alone(muon, rows, cols):
+    x = rand(83, rows, cols, dtype=BF)
+    want = muon.act8_store(x)
+    ldc, lds, blocks = -(-cols // 128) * 128 + 128, -(-rows // 16) * 16 + 16, -(-cols // 128)
+    codes = torch.full((rows + 1, ldc), 77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((blocks + 1, lds), 77, dtype=torch.uint8, device="cuda")
+    h = muon.default_handle()
+    st = h._lib.muon_act8_store(h.ptr, x.data_ptr(), cols, codes.data_ptr(), ldc, scales.data_ptr(), lds, rows, cols,
+                                muon._binding.MUON_BF16, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert torch.equal(codes[:rows, :cols], want[0].view(torch.uint8)) and torch.equal(scales[:blocks, :rows], want[1])
+    codes[:rows, :cols] = scales[:blocks, :rows] = 77
+    assert (codes == 77).all() and (scales == 77).all()
+
+
 def test_act8_error_is_a_sixteenth(muon):
     x = rand(82, 64, 512, dtype=BF)
     codes, scales = muon.act8_store(x)
