@@ -21,6 +21,11 @@
 // a floor of 119: a row's reduction is a chain of about 1500 cycles.  Other
 // rows (row kernels) are loaded into registers one row ahead.
 //
+// 32768 x 4096 bf16: 98 us forward (5.5 TB/s), 135 us backward (6.0) and 8 us
+// for the join, half of it beside the main kernel; 32768 x 4096 fp32 5.9 and
+// 6.2 TB/s.  Row kernels: 32768 x 4095 bf16 2.2 and 3.6 TB/s (an element at a
+// time), 8192 x 16384 bf16 3.6 and 2.8 (sums in shared memory).
+//
 // The backward pass keeps its share of dw and db in registers over all its
 // rows (in shared memory above 8192 columns).  Each CTA writes one partial
 // row of dw and db, and a second kernel adds the partial rows in a fixed

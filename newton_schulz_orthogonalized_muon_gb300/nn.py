@@ -15,6 +15,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -28,6 +29,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = ops.layer_norm_backward(dy, x, mean, rstd, weight)
@@ -63,6 +65,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse = ctx.saved_tensors
         return (*ops.attention_backward(do, q, k, v, o, lse, **ctx.options), None)
@@ -83,6 +86,7 @@ class _Linear8(torch.autograd.Function):
         return x @ weight.t()
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         codes, scales, weight = ctx.saved_tensors
         dw = ops.act8_weight_grad(dy.reshape(-1, dy.shape[-1]), codes, scales, dtype=weight.dtype) \

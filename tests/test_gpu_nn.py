@@ -96,3 +96,13 @@ def test_example_trains(nn):
     assert all(v == v for v in losses)
     # a uniform guess over 64 tokens is 4.16; copying is learned within the run
     assert losses[0] > 3.5 and min(losses[-5:]) < 1.0, losses[::10]
+
+
+def test_second_derivatives_are_refused(nn):
+    x, w = leaf(torch.randn(4, 64, device="cuda")), leaf(torch.rand(64, device="cuda"))
+    q = leaf(torch.randn(1, 8, 1, 64, device="cuda").to(BF))
+    a, b = leaf(torch.randn(8, 64, device="cuda").to(BF)), leaf(torch.randn(32, 64, device="cuda").to(BF))
+    for out, arg in ((nn.layer_norm(x, w), x), (nn.attention(q, q, q, causal=True), q), (nn.linear8(a, b), b)):
+        grad, = torch.autograd.grad(out.float().square().sum(), arg, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(grad.float().sum(), arg)

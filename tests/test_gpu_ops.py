@@ -213,6 +213,45 @@ def test_attention(muon, batch, sq, sk, heads, kv, dim, causal, window, dtype):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("batch,seq,heads,dim,window", [
+    (8, 1024, 16, 128, 0), (8, 1024, 12, 64, 0), (70, 130, 16, 128, 0), (90, 65, 16, 64, 0), (9, 700, 16, 128, 150)])
+def test_attention_of_many_items(muon, batch, seq, heads, dim, window):
+    """More work items than CTAs: a head is computed as it is alone."""
+    q, k, v, do = (rand(24 + i, batch, seq, heads, dim, dtype=BF) for i in range(4))
+    kw = dict(causal=True, window=window)
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    assert muon.default_handle().check() == 0
+    for b, h in ((0, 0), (batch // 2, heads - 1), (batch - 1, 3)):
+        at = (slice(b, b + 1), slice(None), slice(h, h + 1))
+        one, one_lse = muon.attention(q[at], k[at], v[at], **kw)
+        assert torch.equal(one, o[at]) and torch.equal(one_lse, lse[b:b + 1, h:h + 1])
+        for a, g in zip(muon.attention_backward(do[at], q[at], k[at], v[at], one, one_lse, **kw), grads):
+            assert torch.equal(a, g[at])
+    b, h = batch - 1, slice(1, 2)
+    check_attention(f"attention {batch}x{seq} h{heads} d{dim}", BF, dim ** -0.5, True, window, [(0, 0, seq, 0, seq)],
+                    *(t[b:, :, h] for t in (q, k, v, do, o)), lse[b:, h], [g[b:, :, h] for g in grads])
+
+
+def test_packed_documents_of_many_items(muon):
+    lengths = [1, 107, 429, 532, 881, 175, 906, 40, 575, 54, 246, 96, 128, 14, 256, 1735, 58, 0, 501]
+    cuts = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    q, k, v, do = (rand(28 + i, cuts[-1], 16, 128, dtype=HF) for i in range(4))
+    cu = torch.tensor(cuts, dtype=torch.int32).cuda()
+    kw = dict(causal=True, cu_seqlens_q=cu, cu_seqlens_k=cu)
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    assert muon.default_handle().check() == 0
+    for a, b in zip(cuts, cuts[1:]):
+        if a == b:
+            continue
+        at = (slice(a, b), slice(5, 7))
+        one, one_lse = muon.attention(*(t[at][None] for t in (q, k, v)), causal=True)
+        assert torch.equal(one[0], o[at]) and torch.equal(one_lse[0], lse[5:7, a:b])
+        for x, g in zip(muon.attention_backward(*(t[at][None] for t in (do, q, k, v)), one, one_lse, causal=True), grads):
+            assert torch.equal(x[0], g[at])
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cuts_q,cuts_k", [
     ([0, 0, 1, 130, 130, 386, 391, 647], None), ([0, 300], None), ([0, 5, 135, 140], [0, 200, 210, 210]),
