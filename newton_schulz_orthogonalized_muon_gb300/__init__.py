@@ -5,7 +5,8 @@ Newton-Schulz GEMMs, fused momentum/norm and AdamW kernels) behind the C ABI
 in ``include/muon.h``.  This package is a thin ctypes binding over it; the
 binding is loaded on first use and raises if the library was not built.
 ``ops`` (and ``nn`` for autograd) holds the training operators whose
-gradients the step takes: layer norm, attention, activations in 8 bits.
+gradients the step takes: layer norm, attention, activations in 8 bits; their
+calls go through an extension module over the same C ABI.
 """
 __version__ = "1.0.0"
 

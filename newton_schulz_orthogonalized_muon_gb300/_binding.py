@@ -189,6 +189,11 @@ class MuonHandle:
     def ptr(self):
         return self._h
 
+    @property
+    def address(self) -> int:
+        """The handle's pointer as an integer (0 once it is closed)."""
+        return self._h.value if self._h is not None else 0
+
     def set_workspace_limit(self, nbytes: int):
         self._raise(self._lib.muon_handle_set_workspace_limit(self._h, int(nbytes)), "set_workspace_limit")
 

@@ -1,14 +1,18 @@
-"""Build libmuon_gb300.so in-tree with nvcc for sm_103a (GB300).
+"""Build libmuon_gb300.so in-tree with nvcc for sm_103a (GB300), and the
+extension module that calls it on torch tensors.
 
-The CUDA translation units compile in parallel; the shared library
-links the CUDA runtime statically and resolves the tensor-map encoder from
-the driver at run time, so it needs no -lcuda.
+The translation units compile in parallel; the shared library links the CUDA
+runtime statically and resolves the tensor-map encoder from the driver at run
+time, so it needs no -lcuda.  The module (host code) links that library and
+torch's; its object's name carries torch's version, so that another torch
+gets another build.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +25,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["muon_api.cu", "kernels_tc.cu", "kernels_tc2.cu", "kernels_elem.cu", "kernels_simt.cu", "noalloc.cu",
            "ops_api.cu", "op_norm.cu", "op_act8.cu", "op_wgrad.cu", "op_attn_fwd.cu", "op_attn_bwd.cu"]
 HEADERS = ["common.cuh", "internal.h", "tc_common.cuh", "launch_opts.h", "handle.h", "op_common.cuh", "op_attn.cuh"]
+MODULE_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
+MODULE_PATH = os.path.join(HERE, "_torch_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE]
 
@@ -32,6 +38,22 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: set CUDA_HOME or put nvcc on PATH")
 
 
+def _module_commands(nvcc: str):
+    """(object, compile command, link command) of the extension module."""
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    dirs = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda, INCLUDE]
+    obj = os.path.join(BUILD_DIR, f"torch_ops-{torch.__version__}.o")
+    cxx = shutil.which("g++") or "c++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *[f for d in dirs for f in ("-isystem" if d != INCLUDE else "-I", d)], "-c", MODULE_SOURCE, "-o", obj]
+    link = [cxx, "-shared", obj, "-o", MODULE_PATH, LIB_PATH, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return obj, compile_, link
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -40,8 +62,8 @@ def _stale(target: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every translation unit (in parallel) and link the library.
-    Returns the path of the shared library."""
+    """Compile every translation unit (in parallel), link the library and the
+    extension module.  Returns the path of the shared library."""
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "muon.h")]
@@ -53,13 +75,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs.append(o)
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
+    mod_obj, mod_compile, mod_link = _module_commands(nvcc)
+    if force or _stale(mod_obj, [MODULE_SOURCE, os.path.join(INCLUDE, "muon.h")]):
+        jobs.append(mod_compile)
 
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
@@ -67,7 +92,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             list(ex.map(run, jobs))
     if force or jobs or _stale(LIB_PATH, objs):
-        run([nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", LIB_PATH])
+        run([nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-Xlinker", f"-soname={LIB_NAME}", "-o", LIB_PATH])
+    if force or _stale(MODULE_PATH, [mod_obj, LIB_PATH]):
+        run(mod_link)
     return LIB_PATH
 
 

@@ -111,3 +111,14 @@ def test_operators_refuse_host_tensors():
                  lambda: muon.layer_norm_backward(x, x, x[:, 0].float(), x[:, 0].float())):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_extension_module_loads_and_checks_its_arguments(lib):
+    from newton_schulz_orthogonalized_muon_gb300 import _torch_ops as native
+    x = torch.zeros(4, 8)
+    for call in (lambda: native.layer_norm(0, 0), lambda: native.layer_norm(0, 0, x, None, None, 1e-5),
+                 lambda: native.act8_store(0, 0, "x"), lambda: native.attention(0, 0, x, x, x, True, 0, None, None, None)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        native.act8_store("handle", 0, x)
