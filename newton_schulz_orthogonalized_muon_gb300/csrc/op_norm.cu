@@ -248,18 +248,20 @@ __device__ __forceinline__ float variance(float sq, float off) {
 }
 
 // ---------------------------------------------------------- row kernels
-// One row at a time and CTA (of TPR threads; four rows of a warp each when
-// one warp is enough), for rows that the batch kernels do not take.
-template <int TPR>
+// One row at a time and group of TPR threads, for rows that the batch kernels
+// do not take.  Backward a CTA of several groups has one partial row of dw and
+// db: 4099 x 1023 fp32 with 128 threads a CTA took 16.4 us, with 512 14.5 (a
+// group of one warp: 4 and 16 groups the same or worse).
+template <int TPR, bool BWD>
 struct RowCfg {
-  static constexpr int THREADS = TPR == 32 ? 128 : TPR;
+  static constexpr int THREADS = TPR == 32 ? 128 : BWD && TPR < 512 ? 512 : TPR;
   static constexpr int GROUPS = THREADS / TPR;
 };
 
 template <typename T, int VEC, int TPR, int EPT>
-__global__ void __launch_bounds__(RowCfg<TPR>::THREADS) norm_row_fwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(RowCfg<TPR, false>::THREADS) norm_row_fwd_kernel(const NormParams p) {
   using Part = RowPart<T, VEC, TPR, EPT>;
-  constexpr int G = RowCfg<TPR>::GROUPS;
+  constexpr int G = RowCfg<TPR, false>::GROUPS;
   __shared__ float red[G][2][2 * TPR / 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int cols = p.cols;
@@ -309,9 +311,9 @@ __global__ void __launch_bounds__(RowCfg<TPR>::THREADS) norm_row_fwd_kernel(cons
 // thread its own columns, no barrier), for rows so wide that the registers
 // would spill.
 template <typename T, int VEC, int TPR, int EPT, bool ACC_REG>
-__global__ void __launch_bounds__(RowCfg<TPR>::THREADS) norm_row_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(RowCfg<TPR, true>::THREADS) norm_row_bwd_kernel(const NormParams p) {
   using Part = RowPart<T, VEC, TPR, EPT>;
-  constexpr int G = RowCfg<TPR>::GROUPS;
+  constexpr int G = RowCfg<TPR, true>::GROUPS;
   extern __shared__ __align__(128) float acc[];        // [2][TPR * EPT], element e of thread t at e TPR + t
   __shared__ float red[G][2][2 * TPR / 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(32 * JOIN) norm_join_kernel(const float* part,
 
 template <typename T, int VEC, int TPR, int EPT, bool BWD>
 cudaError_t launch_rows(const NormParams& p, int parts, cudaStream_t s) {
-  constexpr int kThreads = RowCfg<TPR>::THREADS;
+  constexpr int kThreads = RowCfg<TPR, BWD>::THREADS;
   if constexpr (BWD) {
     constexpr bool kReg = EPT <= 8;
     constexpr int kSmem = 2 * TPR * EPT * 4;
@@ -738,17 +740,17 @@ int norm_parts(const NormParams& p, bool bwd, int sms) {
     const int b = rows * (p.cols > 4096 ? 1 : norm_rows_at_once(p.dtype == DT_F32 ? 4 : 2, bwd));
     want = (p.rows + b - 1) / b;
   } else {
-    const int tpr = p.cols <= 256 ? 128 : p.cols <= 1024 ? 128 : p.cols <= 2048 ? 256 : p.cols <= 4096 ? 512 : 1024;
-    const int b = p.cols <= 256 ? 4 : 1;
+    const int tpr = p.cols <= 256 ? 32 : p.cols <= 1024 ? 128 : p.cols <= 2048 ? 256 : p.cols <= 4096 ? 512 : 1024;
+    const int threads = tpr == 32 ? 128 : bwd && tpr < 512 ? 512 : tpr, b = threads / tpr;
     want = (p.rows + b - 1) / b;
-    most = static_cast<long long>(sms) * (1024 / tpr);
+    most = static_cast<long long>(sms) * (1024 / threads);
   }
   return static_cast<int>(want < most ? want : most);
 }
 
 // Partial rows that a pass over this many rows can have, whatever its types and alignment.
 int norm_max_parts(long long rows, int cols, int sms) {
-  const long long most = static_cast<long long>(sms) * (cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1);
+  const long long most = static_cast<long long>(sms) * (cols <= 256 ? 8 : cols <= 4096 ? 2 : 1);
   return static_cast<int>(rows < most ? rows : most);
 }
 
