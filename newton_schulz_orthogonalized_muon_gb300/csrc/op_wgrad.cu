@@ -213,18 +213,24 @@ struct Item {
 };
 
 // Tiles go eight output blocks at a time, the pairs that run together share
-// dy and x panels in L2; splits of one tile are neighbours.
-__device__ __forceinline__ Item item_of(const WgradParams& p, int i) {
-  Item t;
-  t.split = i % p.splits;
-  i /= p.splits;
-  const int band = i / (8 * p.tiles_n), in = i - band * 8 * p.tiles_n;
-  const int rows = min(8, p.tiles_o - band * 8);
-  t.o = band * 8 + in % rows;
-  t.n = in / rows;
-  const int steps = static_cast<int>((p.rows + BK - 1) / BK);
-  t.k0 = static_cast<int>(static_cast<long long>(steps) * t.split / p.splits);
-  t.k1 = static_cast<int>(static_cast<long long>(steps) * (t.split + 1) / p.splits);
+// dy and x panels in L2; splits of one tile are neighbours.  (In 32 bits, and
+// without divisions by splits that there are not: every warp starts with this,
+// and 64-bit divisions held the first load for 3000 cycles.)
+__device__ __forceinline__ Item item_of(const WgradParams& p, uint32_t i) {
+  Item t{0, 0, 0, static_cast<int>((p.rows + BK - 1) / BK), 0};
+  if (p.splits > 1) {
+    // steps * splits stays below 2^32: at most 2^24 steps, and fewer splits than SMs
+    const uint32_t n = static_cast<uint32_t>(p.splits), steps = static_cast<uint32_t>(t.k1), split = i % n;
+    i /= n;
+    t.split = static_cast<int>(split);
+    t.k0 = static_cast<int>(steps * split / n);
+    t.k1 = static_cast<int>(steps * (split + 1) / n);
+  }
+  const uint32_t per = 8u * static_cast<uint32_t>(p.tiles_n), band = i / per, in = i - band * per;
+  const uint32_t rows = min(8u, static_cast<uint32_t>(p.tiles_o) - band * 8u);
+  const uint32_t n = rows == 8u ? in >> 3 : in / rows;
+  t.n = static_cast<int>(n);
+  t.o = static_cast<int>(band * 8u + in - n * rows);
   return t;
 }
 
