@@ -249,7 +249,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
     const bool end = id >= g.total, dkv = id < g.nk;
     t.kind = end ? NO_MORE : dkv ? DKV : DQ;
     if (!end) {
-      w = dkv ? find_work(p, false, TILE, p.kv_heads, g.ktiles, id) : find_work(p, true, TILE, p.heads, g.qtiles, id - g.nk);
+      w = find_work(p, !dkv, TILE, dkv ? p.kv_heads : p.heads, dkv ? g.ktiles : g.qtiles, dkv ? id : id - g.nk);
       if (!w.ok) {
         take();
         continue;
