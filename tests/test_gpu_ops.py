@@ -468,6 +468,38 @@ def test_act8_weight_grad_carries_nan(muon):
 
 
 # ------------------------------------------------- streams, refusals, errors
+def test_offsets_past_32_bits(muon):
+    """Rows and tokens 2^30 elements apart."""
+    step, n = 1 << 30, 3
+    store = torch.empty((n - 1) * step + 1024, dtype=BF, device="cuda")
+
+    def apart(t, at=0):                               # t's rows (first dimension), far from each other
+        size = t.shape[1:].numel()
+        view = store.as_strided((n, size), (step, 1), at)
+        view.copy_(t.reshape(n, size))
+        return view.view(n, *t.shape[1:])
+
+    x, dy = rand(84, n, 256, dtype=BF), rand(85, n, 256, dtype=BF)
+    y, mean, rstd = muon.layer_norm(x)
+    far_x, far_dy = apart(x), apart(dy, 256)
+    assert far_x.stride(0) == step
+    assert torch.equal(muon.layer_norm(far_x)[0], y)
+    for a, b in zip(muon.layer_norm_backward(far_dy, far_x, mean, rstd), muon.layer_norm_backward(dy, x, mean, rstd)):
+        assert torch.equal(a, b)
+    for a, b in zip(muon.act8_store(far_x), muon.act8_store(x)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    codes, scales = muon.act8_store(x)
+    assert torch.equal(muon.act8_weight_grad(far_dy, codes, scales), muon.act8_weight_grad(dy, codes, scales))
+    q, k, v, do = (rand(86 + i, n, 2, 64, dtype=BF) for i in range(4))
+    o, lse = muon.attention(q[None], k[None], v[None], causal=True)
+    want = muon.attention_backward(do[None], q[None], k[None], v[None], o, lse, causal=True)
+    far = [apart(t, 128 * i)[None] for i, t in enumerate((q, k, v, do, o[0]))]
+    assert torch.equal(muon.attention(*far[:3], causal=True)[0], o)
+    for a, b in zip(muon.attention_backward(far[3], *far[:3], far[4], lse, causal=True), want):
+        assert torch.equal(a, b)
+    assert muon.default_handle().check() == 0
+
+
 def test_operators_on_a_side_stream_and_in_a_graph(muon):
     x, dy = rand(90, 64, 512, dtype=BF), rand(91, 64, 64, dtype=BF)
     q = rand(92, 1, 200, 2, 64, dtype=BF)
