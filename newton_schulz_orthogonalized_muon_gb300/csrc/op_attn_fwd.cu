@@ -19,10 +19,14 @@
 // then scaled down in TMEM.  Below that the probabilities stay under 256,
 // exact in the same relative precision, and o is left alone.
 //
-// Bound by the tensor cores and the exponentials alike: a 128 x 128 tile
-// pair with dim 128 takes 1024 cycles of products and 16384 exponentials.
-// Measured: 8192 causal tokens of 32 heads (8 of keys), dim 128, bf16, in
-// 363 us, 1510 TFLOP/s of the visible pairs' products.
+// Bound by the products together with what feeds them: two 128 x 128 tile
+// pairs with dim 128 take 2048 cycles of the tensor pipe, and as many of
+// shared memory, from which the score products take 128 bytes a cycle beside
+// the loads of K and V; 32768 exponentials run next to them.  Measured: 8192
+// causal tokens of 32 heads (8 of keys), dim 128, bf16, in 363 us, 1510
+// TFLOP/s of the visible pairs' products, about 3180 cycles a step.  (Two
+// warps a row's half each, 16 for the softmax, took 439 us: a meeting a step
+// and registers that spill cost more than the shorter way saves.)
 #include <cstddef>
 
 #include "common.cuh"

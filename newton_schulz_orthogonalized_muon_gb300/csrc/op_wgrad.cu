@@ -21,9 +21,9 @@
 // Few tiles and many tokens: the tokens are split over several pairs, whose
 // fp32 partial results a second kernel adds in a fixed order.
 //
-// 16384 tokens, 4096 columns, 14336 outputs in 1.15 ms, 1670 TFLOP/s, bound by
-// the products (and, in long runs, by the power limit: 1.29 ms); 1001 x 2048 x
-// 1408 with `add` in 21 us, of which 15 are a CTA's start, first loads and
+// 16384 tokens, 4096 columns, 14336 outputs in 1.14 ms, 1680 TFLOP/s, bound by
+// the products (and, in long runs, by the power limit: 1.27 ms); 1001 x 2048 x
+// 1408 with `add` in 21 us, of which 14 are a CTA's start, first loads and
 // epilogue.
 #include <cuda_fp8.h>
 
