@@ -321,13 +321,12 @@ cudaError_t launch_act8_store(const Act8Params& p, cudaStream_t s);
 cudaError_t launch_act8_restore(const Act8Params& p, cudaStream_t s);
 
 struct WgradParams {
-  const __nv_bfloat16* dy; // [rows], row stride ldy elements
   const uint8_t* codes;    // as above
   const uint8_t* scales;
   const void* add;         // [out][cols] of odtype, row stride ldw, or nullptr
   void* dw;                // [out][cols] of odtype, row stride ldw
   float* part;             // [splits][out][cols] partial results when splits > 1
-  long long rows, ldy, ldc, lds, ldadd, ldw;
+  long long rows, ldc, lds, ldadd, ldw;
   int cols, out, odtype;
   int splits;              // parts that the rows are cut into
   unsigned* err;           // the handle's error word
@@ -336,8 +335,8 @@ struct WgradParams {
 };
 int wgrad_splits(long long rows, int cols, int out, int pairs);
 // maps, 3-D with 128-byte swizzle: {out, rows, 1} of dy in boxes of 64 columns and 64 rows, {columns, rows, 1} of
-// the codes in boxes of 128 columns and 64 rows
-cudaError_t launch_act8_wgrad(const WgradParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s);
+// the codes in boxes of 128 columns and 64 rows.  padded: dy comes from launch_pad_rows, right before this on the stream
+cudaError_t launch_act8_wgrad(const WgradParams& p, const CUtensorMap* maps, bool padded, int pairs, cudaStream_t s);
 cudaError_t launch_act8_wgrad_join(const WgradParams& p, int sms, cudaStream_t s);
 cudaError_t launch_pad_rows(const __nv_bfloat16* src, long long lds, __nv_bfloat16* dst, long long ldd, long long rows,
                             int cols, int sms, cudaStream_t s);

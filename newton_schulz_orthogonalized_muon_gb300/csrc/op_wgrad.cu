@@ -265,6 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (bar->abort) atomicOr(p.err, ERRBIT_TIMEOUT);
     fence_mbar_init();
   }
+  pdl_launch_dependents();
   if (warp == 0) tmem_alloc_pair(&bar->tmem, 512);
   tc_fence_before();
   cluster_sync_all();
@@ -282,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         Ring<DY_STAGES> rd;
         Ring<CODE_STAGES> rc;
         bool ok = true, issued = false;
+        if (warp == 0) pdl_wait();                 // dy may come from the padding kernel
         const uint32_t lead = mapa_shared(smem_u32(&bar->dy_full[0]), 0);
         for (int i = pair; ok && i < items; i += npairs) {
           const Item t = item_of(p, i);
@@ -500,27 +502,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
-// dw = add + the splits' partial results, in their order.
+// dw = add + the splits' partial results, in their order.  (Splits are for few
+// tiles: outputs fit 32 bits.)
 __global__ void __launch_bounds__(256) act8_wgrad_join_kernel(const WgradParams p) {
-  const long long count = static_cast<long long>(p.out) * p.cols;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < count;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const long long o = i / p.cols, n = i - o * p.cols;
+  const uint32_t cols = static_cast<uint32_t>(p.cols), count = static_cast<uint32_t>(p.out) * cols;
+  pdl_wait();                            // launched while the partial results are still being formed
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < count; i += gridDim.x * 256u) {
+    const uint32_t o = i / cols, n = i - o * cols;
     float v = 0.f;
-    for (int s = 0; s < p.splits; ++s) v += p.part[s * count + i];
+#pragma unroll 8
+    for (int s = 0; s < p.splits; ++s) v += p.part[static_cast<long long>(s) * count + i];
     if (p.add != nullptr) v += load_f32(p.add, o * p.ldadd + n, p.odtype);
     store_from_f32(p.dw, o * p.ldw + n, p.odtype, v);
   }
 }
 
-// dy with rows on 16-byte boundaries, for TMA.
+// dy with rows on 16-byte boundaries, for TMA: a warp a row, eight elements a lane.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const __nv_bfloat16* src, long long lds, __nv_bfloat16* dst,
                                                        long long ldd, long long rows, int cols) {
-  const long long count = rows * cols;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < count;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const long long r = i / cols, c = i - r * cols;
-    dst[r * ldd + c] = src[r * lds + c];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  for (long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows;
+       r += static_cast<long long>(gridDim.x) * 8) {
+    const __nv_bfloat16* from = src + r * lds;
+    for (int c = lane * 8; c < cols; c += 256) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = c + k < cols ? to_f32(from[c + k]) : 0.f;
+      *reinterpret_cast<uint4*>(dst + r * ldd + c) = pack16<__nv_bfloat16>(f);
+    }
   }
 }
 
@@ -537,13 +547,13 @@ int wgrad_splits(long long rows, int cols, int out, int pairs) {
 
 cudaError_t launch_pad_rows(const __nv_bfloat16* src, long long lds, __nv_bfloat16* dst, long long ldd, long long rows,
                             int cols, int sms, cudaStream_t s) {
-  const long long want = (rows * cols + 255) / 256;
+  const long long want = (rows + 7) / 8;
   pad_rows_kernel<<<static_cast<unsigned>(want < sms * 8LL ? want : sms * 8LL), 256, 0, s>>>(src, lds, dst, ldd, rows,
                                                                                              cols);
   return cudaGetLastError();
 }
 
-cudaError_t launch_act8_wgrad(const WgradParams& q, const CUtensorMap* maps, int pairs, cudaStream_t s) {
+cudaError_t launch_act8_wgrad(const WgradParams& q, const CUtensorMap* maps, bool padded, int pairs, cudaStream_t s) {
   WgradParams p = q;
   p.tiles_o = (p.out + PT - 1) / PT;
   p.tiles_n = (p.cols + PT - 1) / PT;
@@ -555,14 +565,16 @@ cudaError_t launch_act8_wgrad(const WgradParams& q, const CUtensorMap* maps, int
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(act8_wgrad_kernel), SMEM, done);
   if (e != cudaSuccess) return e;
-  act8_wgrad_kernel<<<2 * static_cast<unsigned>(items < pairs ? items : pairs), THREADS, SMEM, s>>>(maps[0], maps[1], p);
-  return cudaGetLastError();
+  const cudaError_t l = launch_k(padded, act8_wgrad_kernel, dim3(2 * static_cast<unsigned>(items < pairs ? items : pairs)),
+                                 dim3(THREADS), SMEM, s, maps[0], maps[1], p);
+  return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 cudaError_t launch_act8_wgrad_join(const WgradParams& p, int sms, cudaStream_t s) {
   const long long want = (static_cast<long long>(p.out) * p.cols + 255) / 256;
-  act8_wgrad_join_kernel<<<static_cast<unsigned>(want < sms * 8LL ? want : sms * 8LL), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = launch_k(true, act8_wgrad_join_kernel, dim3(static_cast<unsigned>(want < sms * 8LL ? want : sms * 8LL)),
+                                 dim3(256), 0, s, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace muon

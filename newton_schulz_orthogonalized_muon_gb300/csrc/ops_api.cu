@@ -466,7 +466,7 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
           !rows_map(h, &maps[1], codes, cols, rows, ldc, 1, 128))
         return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     }
-    MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, maps, h->num_sms / 2, stream), "weight gradient launch");
+    MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, maps, rows > 0 && plan.pad_bytes > 0, h->num_sms / 2, stream), "weight gradient launch");
     if (p.splits > 1)
       MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad_join(p, h->num_sms, stream), "weight gradient join launch");
     return MUON_OK;
