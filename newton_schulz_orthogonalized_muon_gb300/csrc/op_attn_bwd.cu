@@ -243,13 +243,16 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
     if (lane == 0) next_id = p.counter != nullptr ? gridDim.x + atomicAdd(p.counter, 1u) : id + gridDim.x;
   };
   const int group = p.heads / p.kv_heads;
+  PackedIndex index;
+  if (p.cu_q != nullptr) index.fill(p, TILE);
   for (;; id = __shfl_sync(0xffffffffu, next_id, 0)) {
     Item t;
     Work w{};
     const bool end = id >= g.total, dkv = id < g.nk;
     t.kind = end ? NO_MORE : dkv ? DKV : DQ;
     if (!end) {
-      w = find_work(p, !dkv, TILE, dkv ? p.kv_heads : p.heads, dkv ? g.ktiles : g.qtiles, dkv ? id : id - g.nk);
+      w = find_work(p, !dkv, TILE, dkv ? p.kv_heads : p.heads, dkv ? g.ktiles : g.qtiles, dkv ? id : id - g.nk,
+                    &index);
       if (!w.ok) {
         take();
         continue;

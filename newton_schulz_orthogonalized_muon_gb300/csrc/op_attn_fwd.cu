@@ -120,6 +120,8 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap
   Ring<2> items;
   uint32_t q_ph[2] = {1u, 1u}, ask_ph = 0, edges = 0;
   bool ok = true;
+  PackedIndex index;
+  if (p.cu_q != nullptr) index.fill(p, ROWS);
   for (int id = static_cast<int>(blockIdx.x); ok;) {
     __syncwarp();
     if (lane == 0 && id >= 0) {
@@ -131,7 +133,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap
     Work w{};
     t.more = id >= 0;
     if (id >= 0) {
-      w = find_work(p, true, ROWS, p.heads, tiles, static_cast<uint32_t>(id));
+      w = find_work(p, true, ROWS, p.heads, tiles, static_cast<uint32_t>(id), &index);
       t.i0 = w.tile * ROWS;
       t.rows = w.nq - t.i0;
       t.nk = w.nk;

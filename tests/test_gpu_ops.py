@@ -233,8 +233,10 @@ def test_attention_of_many_items(muon, batch, seq, heads, dim, window):
                     *(t[b:, :, h] for t in (q, k, v, do, o)), lse[b:, h], [g[b:, :, h] for g in grads])
 
 
-def test_packed_documents_of_many_items(muon):
-    lengths = [1, 107, 429, 532, 881, 175, 906, 40, 575, 54, 246, 96, 128, 14, 256, 1735, 58, 0, 501]
+@pytest.mark.parametrize("lengths", [
+    [1, 107, 429, 532, 881, 175, 906, 40, 575, 54, 246, 96, 128, 14, 256, 1735, 58, 0, 501],
+    [30 * (i % 7) + i for i in range(75)], [3] * 31, [200] * 32])
+def test_packed_documents_of_many_items(muon, lengths):
     cuts = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
     q, k, v, do = (rand(28 + i, cuts[-1], 16, 128, dtype=HF) for i in range(4))
     cu = torch.tensor(cuts, dtype=torch.int32).cuda()
