@@ -58,23 +58,28 @@ class LayerNorm(torch.nn.Module):
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, options):
-        o, lse = ops.attention(q, k, v, **options)
-        ctx.save_for_backward(q, k, v, o, lse)
+    def forward(ctx, q, k, v, cu_seqlens_q, cu_seqlens_k, options):
+        o, lse = ops.attention(q, k, v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, **options)
+        # the offsets too: the backward pass reads them on the device, and only
+        # saved tensors are watched for a write in between
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
         ctx.options = options
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
-        return (*ops.attention_backward(do, q, k, v, o, lse, **ctx.options), None)
+        q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k = ctx.saved_tensors
+        grads = ops.attention_backward(do, q, k, v, o, lse, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k,
+                                       **ctx.options)
+        return (*grads, None, None, None)
 
 
 def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_seqlens_q=None, cu_seqlens_k=None):
-    """Differentiable attention (see ops.attention); returns the output."""
-    return _Attention.apply(q, k, v, dict(causal=causal, window=window, scale=scale, cu_seqlens_q=cu_seqlens_q,
-                                          cu_seqlens_k=cu_seqlens_k))
+    """Differentiable attention (see ops.attention); returns the output.  The
+    offsets are kept for the backward pass like the other inputs: writing to
+    them before it raises."""
+    return _Attention.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, dict(causal=causal, window=window, scale=scale))
 
 
 class _Linear8(torch.autograd.Function):

@@ -106,3 +106,28 @@ def test_second_derivatives_are_refused(nn):
         grad, = torch.autograd.grad(out.float().square().sum(), arg, create_graph=True)
         with pytest.raises(RuntimeError):
             torch.autograd.grad(grad.float().sum(), arg)
+
+
+def test_attention_offsets_are_kept_like_the_other_inputs(nn):
+    """Offsets that are refilled before the backward pass raise; offsets that a saved-tensor hook moves are the ones
+    that the backward pass takes."""
+    torch.manual_seed(4)
+    base = [torch.randn(300, 2, 64, device="cuda").to(BF) for _ in range(3)]
+    g = torch.randn(300, 2, 64, device="cuda").to(BF)
+    cu = torch.tensor([0, 100, 161, 300], dtype=torch.int32, device="cuda")
+    want = [leaf(t) for t in base]
+    nn.attention(*want, causal=True, cu_seqlens_q=cu, cu_seqlens_k=cu).backward(g)
+    late = [leaf(t) for t in base]
+    buf = cu.clone()
+    o = nn.attention(*late, causal=True, cu_seqlens_q=buf, cu_seqlens_k=buf)
+    buf.copy_(torch.tensor([0, 50, 60, 300], dtype=torch.int32))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.backward(g)
+    kept = [leaf(t) for t in base]
+    buf = cu.clone()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), lambda t: t):
+        o = nn.attention(*kept, causal=True, cu_seqlens_q=buf, cu_seqlens_k=buf)
+    buf.zero_()
+    o.backward(g)
+    for a, b in zip(want, kept):
+        assert torch.equal(a.grad, b.grad)
