@@ -392,7 +392,8 @@ struct BatchCfg {
   static constexpr int SUMS = SHARED_SUMS ? 2 * TPR * EPT * 4 : 0;
   static constexpr int B = G * R;          // rows of a batch: row r G + g of group g
   static constexpr int RED = G * 2 * 2 * R * (TPR / 32) * 4;
-  static constexpr int OFF_RED = 2 * RING_MAX * 8;
+  static constexpr int OFF_LATE = 2 * RING_MAX * 8;      // a wait ran out
+  static constexpr int OFF_RED = OFF_LATE + 16;
   static constexpr int OFF_SUMS = (OFF_RED + RED + 127) / 128 * 128;
   static constexpr int OFF_RING = OFF_SUMS + SUMS;
   static constexpr int RING = RING_BYTES - SUMS;
@@ -403,14 +404,18 @@ struct BatchCfg {
 // slot (x, then dy).  Rows without a gap go in one copy.
 template <typename T, int B, bool BWD>
 __device__ __forceinline__ void copy_batches(const NormParams& p, uint32_t ring, uint64_t* full, uint64_t* empty,
-                                             int depth, int row_bytes) {
+                                             volatile int* late, int depth, int row_bytes) {
   const int lane = threadIdx.x & 31;
   const long long batches = (p.rows + B - 1) / B;
   int slot = 0;
   uint32_t parity = 1;                     // the first round finds every slot free
   for (long long i = blockIdx.x; i < batches; i += gridDim.x) {
-    if (!mbar_wait_bounded(&empty[slot], parity, nullptr, p.timeout_ns)) {
-      if (lane == 0) atomicOr(p.err, ERRBIT_TIMEOUT);
+    // the lanes leave together: they meet again below
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], parity, late, p.timeout_ns))) {
+      if (lane == 0) {
+        if (*late == 0) atomicOr(p.err, ERRBIT_TIMEOUT);
+        *late = 1;
+      }
       return;
     }
     const long long row = i * B;
@@ -445,6 +450,7 @@ __global__ void __launch_bounds__(CALC + 32, 1) norm_batch_kernel(const NormPara
   extern __shared__ __align__(128) uint8_t dyn[];
   uint64_t* full = reinterpret_cast<uint64_t*>(dyn);
   uint64_t* empty = full + RING_MAX;
+  volatile int* late = reinterpret_cast<int*>(dyn + C::OFF_LATE);
   const uint32_t ring = smem_u32(dyn + C::OFF_RING);
   const int cols = p.cols, row_bytes = cols * static_cast<int>(sizeof(T));
   const int slot_bytes = (BWD ? 2 : 1) * B * row_bytes;
@@ -454,6 +460,7 @@ __global__ void __launch_bounds__(CALC + 32, 1) norm_batch_kernel(const NormPara
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], CALC / 32);
     }
+    *late = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(CALC + 32, 1) norm_batch_kernel(const NormPara
   F2* sums = reinterpret_cast<F2*>(dyn + C::OFF_SUMS);
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   if (threadIdx.x >= CALC) {
-    copy_batches<T, B, BWD>(p, ring, full, empty, depth, row_bytes);
+    copy_batches<T, B, BWD>(p, ring, full, empty, late, depth, row_bytes);
   } else {
     float* red = reinterpret_cast<float*>(dyn + C::OFF_RED) + grp * (2 * 2 * R * (TPR / 32));
     const int lane = threadIdx.x & 31;
@@ -495,11 +502,13 @@ __global__ void __launch_bounds__(CALC + 32, 1) norm_batch_kernel(const NormPara
     if (BWD && blockIdx.x < batches) stats(blockIdx.x);
     int slot = 0, turn = 0;
     uint32_t parity = 0;
-    bool late = false;                     // a wait ran out: no further waits, the error word tells
+    // A wait ran out: no further waits, the error word tells.  No thread leaves: its group meets at barriers.
+    bool gave_up = false;
     for (long long i = blockIdx.x; i < batches; i += gridDim.x, turn ^= 1) {
-      if (!late && !mbar_wait_bounded(&full[slot], parity, nullptr, p.timeout_ns)) {
-        atomicOr(p.err, ERRBIT_TIMEOUT);
-        late = true;
+      if (!gave_up && !mbar_wait_bounded(&full[slot], parity, late, p.timeout_ns)) {
+        if (*late == 0) atomicOr(p.err, ERRBIT_TIMEOUT);
+        *late = 1;
+        gave_up = true;
       }
       const uint32_t at = ring + slot * slot_bytes;
       Part x[R], dy[BWD ? R : 1];
@@ -611,8 +620,15 @@ __global__ void __launch_bounds__(CALC + 32, 1) norm_batch_kernel(const NormPara
       }
     }
   }
-  if constexpr (BWD) {
-    __syncthreads();                       // every batch is read: the ring's place takes the sums
+  __syncthreads();                         // every batch is read
+  // after a wait ran out, copies may still be in flight, and none is issued
+  // any more: a millisecond for them to land, in which the CTA's memory is kept
+  if (threadIdx.x == CALC && *late != 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  if constexpr (BWD) {                     // the ring's place takes the sums
     if (kRegSums || grp < G) {             // the copying warp has no sums of its own in shared memory
       float dwf[EPT], dbf[EPT];
 #pragma unroll

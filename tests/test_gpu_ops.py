@@ -573,3 +573,32 @@ def test_refusals(muon):
             call()
             raise AssertionError(f"call {i} was not refused")
     assert muon.default_handle().launch_count() == n0
+
+
+# ------------------------------------------------------------ bounded waits
+def run_with_short_waits(muon, call):
+    """Calls under a wait limit of a nanosecond.  A wait that is still open after its first polls then gives up: the
+    call ends, the error word tells, and the next call is whole again.  (Data mostly arrives within the polls.)"""
+    h = muon.default_handle()
+    want = call()
+    assert h.check() == 0
+    seen = set()
+    try:
+        h.set_timeout_ns(1)
+        for _ in range(8):
+            got = call()
+            seen.add(h.check())
+            if seen == {0}:
+                assert all(torch.equal(a, b) for a, b in zip(want, got))
+    finally:
+        h.set_timeout_ns(4_000_000_000)
+    assert seen <= {0, 6}
+    assert all(torch.equal(a, b) for a, b in zip(want, call())) and h.check() == 0
+    return seen
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(8000, 4096, BF), (40000, 256, BF), (3000, 8192, FP)])
+def test_layer_norm_waits_end(muon, rows, cols, dtype):
+    x, dy = rand(110, rows, cols, dtype=dtype), rand(111, rows, cols, dtype=dtype)
+    y, mean, rstd = muon.layer_norm(x)
+    run_with_short_waits(muon, lambda: (*muon.layer_norm(x), *muon.layer_norm_backward(dy, x, mean, rstd)))
