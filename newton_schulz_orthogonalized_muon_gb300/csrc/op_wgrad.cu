@@ -282,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // all three took 1000 cycles a step, twice what the products take.)
         Ring<DY_STAGES> rd;
         Ring<CODE_STAGES> rc;
-        bool ok = true, issued = false;
+        bool ok = true;
         if (warp == 0) pdl_wait();                 // dy may come from the padding kernel
         const uint32_t lead = mapa_shared(smem_u32(&bar->dy_full[0]), 0);
         for (int i = pair; ok && i < items; i += npairs) {
@@ -297,7 +297,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               if (rank == 0) mbar_arrive_expect_tx(&bar->dy_full[rd.s], 4 * BOX);
               tma_load_3d_pair(sb + rd.s * 2 * BOX, &mdy, fb, o0, k * BK, 0);
               tma_load_3d_pair(sb + rd.s * 2 * BOX + BOX, &mdy, fb, o0 + 64, k * BK, 0);
-              issued = true;
               rd.next();
             }
           } else {
@@ -319,16 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               } else {
                 mbar_arrive(cf);
               }
-              issued = true;
               rc.next();
             }
-          }
-        }
-        // after a wait ran out: copies in flight signal barriers that may
-        // never complete (the peer's part missing); a millisecond to land
-        if (!ok && issued) {
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 1000000ull) {
           }
         }
       }
@@ -497,6 +488,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // after a wait ran out, whichever warp's it was: copies in flight (their
+  // barriers may never complete, the peer's part missing) get a millisecond
+  // to land before the pair's memory is given up; none is issued any more
+  if (threadIdx.x == 0 && *abort != 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  __syncwarp();
   cluster_sync_all();
   tc_fence_after();
   if (warp == 0) tmem_dealloc_pair(tmem, 512);

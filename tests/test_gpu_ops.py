@@ -602,3 +602,9 @@ def test_layer_norm_waits_end(muon, rows, cols, dtype):
     x, dy = rand(110, rows, cols, dtype=dtype), rand(111, rows, cols, dtype=dtype)
     y, mean, rstd = muon.layer_norm(x)
     run_with_short_waits(muon, lambda: (*muon.layer_norm(x), *muon.layer_norm_backward(dy, x, mean, rstd)))
+
+
+@pytest.mark.parametrize("rows,cols,out", [(5000, 2048, 2048), (1000, 3000, 20000), (20000, 256, 250)])
+def test_act8_weight_grad_waits_end(muon, rows, cols, out):
+    dy, kept = rand(112, rows, out, dtype=BF), muon.act8_store(rand(113, rows, cols, dtype=BF))
+    run_with_short_waits(muon, lambda: (muon.act8_weight_grad(dy, *kept),))
