@@ -439,6 +439,17 @@ __device__ __forceinline__ uint32_t bits32(int lo, int hi) {
   return __funnelshift_lc(0u, ~0u, max(lo, 0)) & ~__funnelshift_lc(0u, ~0u, max(hi, 0));
 }
 
+// Probabilities are rounded to T times 2^N, taken back from what they are
+// summed to: fp16 has few bits left below 2^-14 and none below 2^-25, and
+// over many keys such probabilities add up.  (bf16 has fp32's range: N = 0.)
+// Backward they reach about 1.
+template <typename T>
+__host__ __device__ constexpr int lift_backward() {
+  return std::is_same<T, __half>::value ? 14 : 0;
+}
+// 2^-n
+__host__ __device__ constexpr float lowered(int n) { return 1.f / static_cast<float>(1 << n); }
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

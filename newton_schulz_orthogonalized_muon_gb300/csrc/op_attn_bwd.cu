@@ -5,7 +5,8 @@
 //   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i
 //
 // attn_prep_kernel writes -lse_i log2(e) and -delta_i, tile by tile (HBM-bound:
-// it reads o and do).  attn_bwd_kernel has two kinds of items.  One owns a
+// it reads o and do).  fp16: the first 14 above, the second 2^-14 as large, so
+// that p comes out lifted by 2^14 and ds as it is (see op_attn.cuh).  attn_bwd_kernel has two kinds of items.  One owns a
 // tile of 128 keys, walks the query tiles that see them (of every query head
 // that shares the key head) and keeps dk and dv in TMEM; the other owns a
 // tile of 128 queries, walks its key tiles and keeps dq in TMEM.  No value is
@@ -59,7 +60,7 @@ struct Shape {
 
 // ------------------------------------------------------------ statistics
 // -lse log2(e) and -delta of one tile of queries, 128 values each (the sign
-// that two-wide additions want), padded: rows past the sequence and rows that
+// that two-wide additions want; lifted and lowered), padded: rows past the sequence and rows that
 // see no key get -inf, so that their p is 0.  8192 tokens of 32 heads of 128:
 // 31 us, 4.3 TB/s.
 constexpr int PREP = 512;                         // threads
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(PREP) attn_prep_kernel(const AttnParams p, int
     for (int c = LPR / 2; c > 0; c >>= 1) s += __shfl_xor_sync(0xffffffffu, s, c);
     if (l == 0) {
       const int i = r0 + k * (PREP / LPR);
-      p.stat_lse[at + i] = e[k] == -INFINITY ? -INFINITY : -e[k] * LOG2E;
-      p.stat_delta[at + i] = -s;
+      p.stat_lse[at + i] = e[k] == -INFINITY ? -INFINITY : fmaf(-e[k], LOG2E, static_cast<float>(lift_backward<T>()));
+      p.stat_delta[at + i] = -s * lowered(lift_backward<T>());
     }
   }
 }
@@ -504,6 +505,13 @@ struct Calc {
   Ring<2> buf, stats;
   uint32_t s_ph = 0, k_ph = 0, dv_ph = 0, done_ph = 0;
 
+  // dP - delta (of two), lowered as far as p is lifted
+  static __device__ __forceinline__ F2 dp_less_delta(float a, float b, F2 delta) {
+    if constexpr (lift_backward<T>() == 0) return f2_add(f2_make(a, b), delta);
+    constexpr float k = lowered(lift_backward<T>());
+    return f2_fma(f2_make(a, b), f2_make(k, k), delta);
+  }
+
   // dk and dv.  A warp has 32 keys (TMEM rows) by 32 queries; thread t of it
   // the keys t / 4 + 8 k, k = 0 .. 3, and the queries 8 j + 2 (t % 4) + {0,
   // 1}, j = 0 .. 3.  Value (k, j, e) is v[16 (k / 2) + 4 j + 2 (k % 2) + e].
@@ -576,8 +584,7 @@ struct Calc {
 #pragma unroll
       for (int k = 0; k < COLS; k += 2) {
         const int q = (k >> 2) & 3;
-        const float2 x =
-            f2_split(f2_mul(f2_make(v[k], v[k + 1]), f2_add(f2_make(d[k], d[k + 1]), f2_make(e[q].x, e[q].y))));
+        const float2 x = f2_split(f2_mul(f2_make(v[k], v[k + 1]), dp_less_delta(d[k], d[k + 1], f2_make(e[q].x, e[q].y))));
         r16[k >> 1] = pack2<T>(x.x, x.y);
       }
       tmem_st_16x16(dp_at, r16);
@@ -638,7 +645,7 @@ struct Calc {
       tmem_ld_wait();
 #pragma unroll
       for (int k = 0; k < COLS; k += 2) {
-        const float2 x = f2_split(f2_mul(f2_make(v[k], v[k + 1]), f2_add(f2_make(d[k], d[k + 1]), dd)));
+        const float2 x = f2_split(f2_mul(f2_make(v[k], v[k + 1]), dp_less_delta(d[k], d[k + 1], dd)));
         v[k] = x.x;
         v[k + 1] = x.y;
       }
@@ -669,7 +676,7 @@ struct Calc {
     if (dkv) dv_ph ^= 1u;
     tc_fence_after();
     const uint32_t at = tmem + lanes + (dkv ? 2 * WT + (is_dk ? DP : 0) : 3 * WT) + col;
-    const float m = is_dv ? 1.f : p.scale, mul[4] = {m, m, m, m};
+    const float m = is_dv ? lowered(lift_backward<T>()) : p.scale, mul[4] = {m, m, m, m};
 #pragma unroll 1
     for (int k = 0; k < width; k += 32) store_rows<T>(at + k, out + k, stride, rows, p.dim - col - k, mul);
     warp_arrive(BAR(acc_free));

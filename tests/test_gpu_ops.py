@@ -608,3 +608,53 @@ def test_layer_norm_waits_end(muon, rows, cols, dtype):
 def test_act8_weight_grad_waits_end(muon, rows, cols, out):
     dy, kept = rand(112, rows, out, dtype=BF), muon.act8_store(rand(113, rows, cols, dtype=BF))
     run_with_short_waits(muon, lambda: (muon.act8_weight_grad(dy, *kept),))
+
+
+# ------------------------------------------- attention over very many keys
+def attention_reference(q, k, v, do):
+    """One sequence whose heads share one key head, in fp64 on the GPU: o, lse, (dq, dk, dv), and the magnitudes of
+    the products that are summed into o and into each gradient (|do||v| + |do||o| in the place of their difference)."""
+    q, k, v, do = q.double(), k.double()[:, 0], v.double()[:, 0], do.double()
+    o, dq, mo, mq = (torch.zeros_like(q) for _ in range(4))
+    dk, dv, mk, mv = (torch.zeros_like(k) for _ in range(4))
+    lse = torch.zeros(q.shape[1], q.shape[0], dtype=torch.float64, device="cuda")
+    scale, step = q.shape[2] ** -0.5, max(1, (1 << 25) // len(k))
+    for h in range(q.shape[1]):
+        for i in range(0, len(q), step):
+            at = (slice(i, i + step), h)
+            s = (q[at] @ k.T) * scale
+            z = torch.logsumexp(s, 1)
+            p = torch.exp(s - z[:, None])
+            o[at], mo[at], lse[h, i:i + step] = p @ v, p @ v.abs(), z
+            g = do[at]
+            ds = p * (g @ v.T - (g * o[at]).sum(1, keepdim=True)) * scale
+            wide = p * (g.abs() @ v.abs().T + (g * o[at]).abs().sum(1, keepdim=True)) * scale
+            dq[at], mq[at] = ds @ k, wide @ k.abs()
+            dv += p.T @ g
+            mv += p.T @ g.abs()
+            dk += ds.T @ q[at]
+            mk += wide.T @ q[at].abs()
+    return o, lse, (dq, dk[:, None], dv[:, None]), mo, (mq, mk[:, None], mv[:, None])
+
+
+def near_on_gpu(name, got, ref, tol):
+    ratio = ((got.double() - ref).abs() / tol.clamp(min=1e-30)).max().item()
+    record(name, ratio, 1.0)
+    assert ratio <= 1.0, (name, ratio)
+
+
+# The tolerance of attn_tol.  fp16 results are themselves rounded in steps of 2^-24 at least.
+def gpu_tol(u, ref, mag, wide):
+    return u * ref.abs() + 1.02 * u * mag + 2.0 ** -15 * wide + 2.0 ** -25
+
+
+def test_fp16_gradient_of_a_flat_softmax(muon):
+    """2^18 keys with probabilities of 2^-18."""
+    n = 1 << 18
+    q, do = rand(120, 1, 64, 1, 64, dtype=HF, scale=0.5), rand(121, 1, 64, 1, 64, dtype=HF, scale=64.0)
+    k, v = rand(122, 1, n, 1, 64, dtype=HF), rand(123, 1, n, 1, 64, dtype=HF)
+    o, lse = muon.attention(q, k, v)
+    grads = muon.attention_backward(do, q, k, v, o, lse)
+    _, _, (_, _, rv), _, (_, _, mv) = attention_reference(q[0], k[0], v[0], do[0])
+    near_on_gpu("small probabilities dv", grads[2][0], rv, gpu_tol(U[HF], rv, mv, mv))
+    assert muon.default_handle().check() == 0
