@@ -354,6 +354,17 @@ typedef struct {
 
 muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a, void* stream);
 
+/* The forward pass over very many keys (more than 8192 in fp16, 65536 in bf16,
+ * within a window if there is one): o is summed in parts of that many keys,
+ * which are added up in fp32 in `workspace`.  Without one (workspace NULL, or
+ * muon_attention_forward) the tensor core's accumulator takes all keys; it
+ * truncates, so values of one sign come out too small, by 4e-4 of themselves
+ * over 65536 keys and 3e-3 over 524288.  For fewer keys the two calls are one
+ * and no workspace is needed. */
+muon_status_t muon_attention_forward_ex(muon_handle_t h, const muon_attention_t* a, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+muon_status_t muon_attention_forward_workspace(muon_handle_t h, const muon_attention_t* a, uint64_t* bytes);
+
 /* The backward pass, which recomputes the probabilities p_ij = exp(s_ij -
  * lse_i): with delta_i = dout_i . o_i,
  *   dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - delta_i),

@@ -32,6 +32,7 @@ EXPORTS = ("muon_handle_create", "muon_handle_destroy", "muon_handle_set_workspa
            "muon_noalloc_check", "muon_noalloc_set_timeout_ns",
            "muon_layer_norm_forward", "muon_layer_norm_backward", "muon_layer_norm_workspace",
            "muon_attention_forward", "muon_attention_backward", "muon_attention_workspace",
+           "muon_attention_forward_ex", "muon_attention_forward_workspace",
            "muon_act8_store", "muon_act8_restore", "muon_act8_weight_grad", "muon_act8_weight_grad_workspace")
 KERNEL_CLASSES = ("prepare", "norm", "syrk", "poly", "update", "final", "apply", "adamw", "layer_norm", "attention",
                   "act8", "wgrad")
@@ -114,6 +115,8 @@ def load_library(path: str | None = None):
                                                vp, ctypes.c_size_t, vp]),
             "muon_layer_norm_workspace": (i32, [vp, i64, i64, ctypes.POINTER(u64)]),
             "muon_attention_forward": (i32, [vp, ctypes.c_char_p, vp]),
+            "muon_attention_forward_ex": (i32, [vp, ctypes.c_char_p, vp, ctypes.c_size_t, vp]),
+            "muon_attention_forward_workspace": (i32, [vp, ctypes.c_char_p, ctypes.POINTER(u64)]),
             "muon_attention_backward": (i32, [vp, ctypes.c_char_p, vp, ctypes.c_size_t, vp]),
             "muon_attention_workspace": (i32, [vp, ctypes.c_char_p, ctypes.POINTER(u64)]),
             "muon_act8_store": (i32, [vp, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),

@@ -362,15 +362,23 @@ struct AttnParams {
   int causal, window;      // window > 0: a query sees at most the last `window` keys up to its own place
   int dtype;
   float scale;
-  unsigned* counter;       // backward, scratch: items taken, or nullptr (no statistics kernel to set it to 0)
+  unsigned* counter;       // scratch, items taken: backward, or nullptr (no statistics kernel to set it to 0);
+                           // forward, with part, set to 0 before the launch
   int qtiles;              // query tiles of 128 rows of a (batch, head): a bound when packed
   unsigned* err;           // the handle's error word
   unsigned long long timeout_ns;
+  float* part;             // scratch of walks over more than attn_sum_rows rows: attn_part_floats for each CTA; or
+                           // nullptr (no walk is longer, or its sums stay in one accumulator)
 };
+// Rows of a walk that one tensor-core accumulator takes (see op_attn.cuh).
+constexpr int attn_sum_rows(bool bf16) { return bf16 ? 65536 : 8192; }
 int attn_qtiles(int sq, int batch, bool packed);
+// CTAs of a pass whose walks are handed over in parts, at most, and floats of scratch for each
+inline int attn_part_ctas(int dim, bool bwd, int sms) { return bwd && dim <= 64 ? 2 * sms : sms; }
+inline int attn_part_floats(int dim) { return 256 * (dim <= 64 ? 64 : 128); }
 // m: 4-D tensor maps {dim, head, token, batch} of q, k, v (and do) with boxes
 // of 64 columns and 128 tokens (64 backward with dim <= 64), 128-byte swizzle.
-cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s);
+cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, int sms, cudaStream_t s);
 // prep: the statistics (sq > 0); else, after it on the stream, the gradients
 cudaError_t launch_attn_bwd(const AttnParams& p, const CUtensorMap* m, bool prep, int sms, cudaStream_t s);
 

@@ -20,6 +20,17 @@ constexpr int TILE = 128;                    // rows of a tile
 constexpr int BOX_BYTES = 128 * 128;         // 128 rows x 64 16-bit columns
 constexpr float LOG2E = 1.4426950408889634f;
 
+// The tensor core adds each product of 16 rows to its fp32 accumulator with
+// truncation, so a sum of one sign comes out too small the more the longer
+// (walks of 8192, 65536 and 524288 rows: by 5e-5, 4e-4 and 3e-3 of itself).  The results' rounding is up to 2^-12 in fp16 and 2^-9 in bf16, five
+// times that of 8192 and 65536 rows.  Walks over more rows are handed over in
+// parts of as many, which are added up in fp32 with rounding, in scratch
+// memory of the CTA (p.part): each value is read back by the thread that wrote
+// it.  (Kernels of their own: the hot loops took 3 to 4% longer with the code
+// for parts beside them.)
+template <typename T>
+constexpr int SUM_ROWS = attn_sum_rows(std::is_same<T, __nv_bfloat16>::value);
+
 template <int DP>
 __host__ __device__ constexpr int tile_bytes() {
   return DP / 64 * BOX_BYTES;
@@ -462,14 +473,29 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // Read in the accumulators' layout, and four lanes trade their words, so that
 // they write 64 bytes of a row: a row a lane, 16 bytes at a time, took twice
 // as long.
-template <typename T>
-__device__ __forceinline__ void store_rows(uint32_t taddr, T* dst, long long stride, int rows, int cols, const float* mul) {
+// parts: SUM_ADD, the values in `sums` (32 x 32 of this warp's) are added
+// first; SUM_KEEP, the result goes there instead, as it is.
+enum : int { SUM_ADD = 1, SUM_KEEP = 2 };
+template <typename T, bool PARTS = false>
+__device__ __forceinline__ void store_rows(uint32_t taddr, T* dst, long long stride, int rows, int cols, const float* mul,
+                                           int parts = 0, float* sums = nullptr) {
   if (cols <= 0) return;
   const int lane = threadIdx.x & 31, c = lane & 3;
   float v[32];
   tmem_ld_16x32(taddr, v);
   tmem_ld_16x32(taddr + (16u << 16), v + 16);
   tmem_ld_wait();
+  if constexpr (PARTS) {
+    if (parts & SUM_ADD) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] += sums[e * 32 + lane];
+    }
+    if (parts & SUM_KEEP) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) sums[e * 32 + lane] = v[e];
+      return;
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {              // row lane / 4 + 8 k
     uint32_t w[4];                           // word q: columns 8 q + 2 c, + 1

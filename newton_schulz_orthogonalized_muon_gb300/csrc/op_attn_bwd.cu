@@ -135,6 +135,8 @@ enum Kind : int { DQ = 0, DKV = 1, NO_MORE = 2 };
 struct Item {
   int kind;
   int n;                     // steps
+  int start;                 // walked row of the first of them
+  int parts;                 // a walk in parts, each an item: SUM_ADD: not the first, SUM_KEEP: not the last
   int own;                   // first row of the tile that stays, in its sequence
   int rows;                  // rows from there to the sequence's end
   int first, last;           // walked rows: whole tiles, those of a head
@@ -219,7 +221,7 @@ struct Items {
 };
 
 // ----------------------------------------------------------------- loads
-template <typename T, int DP>
+template <typename T, int DP, bool PARTS>
 __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, uint32_t sb, uint32_t bb, Bars* bar) {
   volatile int* abort = &bar->abort;
   using S = Smem<DP>;
@@ -249,6 +251,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
   for (;; id = __shfl_sync(0xffffffffu, next_id, 0)) {
     Item t;
     Work w{};
+    int steps = 0;
     const bool end = id >= g.total, dkv = id < g.nk;
     t.kind = end ? NO_MORE : dkv ? DKV : DQ;
     if (!end) {
@@ -262,7 +265,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
       t.rows = (dkv ? w.nk : w.nq) - t.own;
       const Range r = dkv ? query_tiles<WT>(p, w, t.own, min(t.own + TILE, w.nk) - 1)
                           : key_tiles<WT>(p, w, t.own, min(t.own + TILE, w.nq) - 1);
-      t.n = r.count * (dkv ? group : 1);
+      steps = r.count * (dkv ? group : 1);
       t.first = r.first * WT;
       t.last = (r.first + r.count) * WT;
       t.nk = w.nk;
@@ -272,18 +275,6 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
                      : static_cast<T*>(p.dq) + w.b * p.dqb + w.h * p.dqh + q0 * p.dqs;
       t.out[1] = static_cast<T*>(p.dk) + w.b * p.dkb + w.h * p.dkh + k0 * p.dks;
     }
-    ok = ok && wait_warp(BAR(item_empty) + 8 * items.s, items.ph ^ 1u, abort, p);
-    if (!ok) break;
-    if (lane == 0) {
-      bar->item[items.s] = t;
-      mbar_arrive_at(BAR(item_full) + 8 * items.s);
-    }
-    items.next();
-    if (end) break;
-    if (t.n == 0) {
-      take();
-      continue;
-    }
     // dk, dv: K and V stay, Q and dO are walked; dq: Q and dO stay, K and V are walked
     const CUtensorMap* own0 = dkv ? g.mk : g.mq;
     const CUtensorMap* own1 = dkv ? g.mv : g.mdo;
@@ -291,18 +282,30 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
     const CUtensorMap* walk_b = dkv ? g.mdo : g.mv;
     const int own_row = (dkv ? w.k0 : w.q0) + t.own;
     const int first = dkv ? w.q0 : w.k0, len = dkv ? w.nq : w.nk;
-    const int h0 = dkv ? w.h * group : w.h / group, h1 = dkv ? h0 + group : h0 + 1;
-    ok = wait_warp(BAR(own_empty), own_ph, abort, p);
-    if (!ok) break;
-    if (lane == 0) {
-      mbar_expect_at(BAR(own), S::OWN);
-      load_tile<DP, TILE, BOX>(sb, own0, BAR(own), w.h, own_row, w.b);
-    }
-    bool second = true;                                      // the other own tile is still to come
-    for (int h = h0; ok && h < h1; ++h) {
-      // statistics: of each walked tile, or of the one that stays, with the first walked tile
-      const long long stat = ((static_cast<long long>(w.b) * p.heads + (dkv ? h : w.h)) * g.qtiles + w.qtile) * TILE;
-      for (int i0 = t.first; i0 < t.last; i0 += WT) {
+    int h = dkv ? w.h * group : w.h / group, i0 = t.first;
+    for (int done = 0; ok;) {                                // the walk's parts, mostly one
+      t.n = PARTS ? min(steps - done, SUM_ROWS<T> / WT) : steps;
+      t.start = i0;
+      t.parts = (done > 0 ? SUM_ADD : 0) | (done + t.n < steps ? SUM_KEEP : 0);
+      ok = wait_warp(BAR(item_empty) + 8 * items.s, items.ph ^ 1u, abort, p);
+      if (!ok) break;
+      if (lane == 0) {
+        bar->item[items.s] = t;
+        mbar_arrive_at(BAR(item_full) + 8 * items.s);
+      }
+      items.next();
+      if (end) break;
+      if (steps == 0) {
+        take();
+        break;
+      }
+      ok = wait_warp(BAR(own_empty), own_ph, abort, p);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_expect_at(BAR(own), S::OWN);
+        load_tile<DP, TILE, BOX>(sb, own0, BAR(own), w.h, own_row, w.b);
+      }
+      for (int k = 0; k < t.n; ++k) {
         const int row = first + i0, valid = len - i0;
         const bool edge = p.cu_q != nullptr && valid < WT;
         const uint32_t at = sb + S::A_OFF + ra.s * S::T, bt = sb + S::B_OFF + rb.s * S::T;
@@ -314,27 +317,28 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
           else mbar_expect_at(BAR(edge), S::T);
           load_tile<DP, WT, BOX>(at, walk_a, edge ? BAR(edge) : fa, h, row, w.b);
         }
-        if (second) {                                        // after what the first scores want
-          second = false;
+        if (k == 0) {                                        // the other own tile, after what the first scores want
           ok = wait_warp(BAR(own_empty) + 8, own_ph, abort, p);
           if (!ok) break;
           if (lane == 0) {
             mbar_expect_at(BAR(own) + 8, S::OWN);
             load_tile<DP, TILE, BOX>(sb + S::OWN, own1, BAR(own) + 8, w.h, own_row, w.b);
           }
-          take();
+          if (done == 0) take();
         }
         ok = wait_warp(BAR(b_empty) + 8 * rb.s, rb.ph ^ 1u, abort, p);
         if (!ok) break;
         if (lane == 0) {
           const uint32_t to = edge ? BAR(edge) + 8 : fb;
           const uint32_t st = sb + S::STAT_OFF + rb.s * S::STAT;
+          // statistics: of each walked tile, or of the one that stays, with the first walked tile
+          const long long stat = ((static_cast<long long>(w.b) * p.heads + (dkv ? h : w.h)) * g.qtiles + w.qtile) * TILE;
           mbar_expect_at(to, S::T + (dkv ? 2 * WT * 4 : 0));
           load_tile<DP, WT, BOX>(bt, walk_b, to, h, row, w.b);
           if (dkv) {
             bulk_load(st, p.stat_lse + stat + i0, WT * 4, to);
             bulk_load(st + TILE * 4, p.stat_delta + stat + i0, WT * 4, to);
-          } else if (i0 == t.first) {
+          } else if (k == 0) {
             // a barrier of their own: the walked tiles get further ahead of the warps that read these
             const uint32_t bs = BAR(stat) + 8 * stats.s;
             mbar_expect_at(bs, 2 * TILE * 4);
@@ -353,10 +357,18 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const Grid& g, ui
         }
         ra.next();
         rb.next();
+        i0 += WT;
+        if (i0 == t.last) {                                  // on to the group's next head
+          i0 = t.first;
+          ++h;
+        }
       }
+      own_ph ^= 1u;
+      if (!dkv) stats.next();
+      done += t.n;
+      if (!PARTS || done == steps) break;
     }
-    own_ph ^= 1u;
-    if (!dkv) stats.next();
+    if (!ok || end) break;
   }
   // after a wait ran out: a millisecond for copies in flight to land
   if (*abort != 0 && lane == 0) {
@@ -492,7 +504,7 @@ __device__ __forceinline__ void product_role(const AttnParams& p, uint32_t sb, u
 }
 
 // --------------------------------------------- probabilities and outputs
-template <typename T, int DP>
+template <typename T, int DP, bool PARTS>
 struct Calc {
   using S = Smem<DP>;
   static constexpr int WT = S::WT;
@@ -526,7 +538,7 @@ struct Calc {
     const F2 cc = f2_make(c, c);
     const int n = t.n, own = t.own, off = t.off, first = t.first, last = t.last;
     const uint32_t s_at = tmem + lanes + c0, dp_at = tmem + lanes + WT + c0;
-    int q0 = first;
+    int q0 = t.start;
     for (int i = 0; i < n; ++i) {
       const float* st = reinterpret_cast<const float*>(smem + S::STAT_OFF + rb.s * S::STAT) + c1;
       // queries q0 .. q0 + WT - 1 against keys own .. own + 127: does everyone see everything?
@@ -601,7 +613,7 @@ struct Calc {
   // dq: one query a thread, 32 keys of it
   __device__ __forceinline__ bool dq_steps(const Item& t) {
     const float c = p.scale * LOG2E;
-    const int own = t.own, off = t.off, nk = t.nk, first = t.first, last = t.last;
+    const int own = t.own, off = t.off, nk = t.nk, first = t.start, last = t.start + t.n * WT;
     const int q = own + quad * 32 + lane;
     // the statistics came with the first walked tile; nothing is loaded over
     // them before every warp has let its first scores go
@@ -657,7 +669,8 @@ struct Calc {
     return true;
   }
 
-  // The sums of an item, 64 columns a warp (dk, dv) or 32 (dq), to memory.
+  // The sums of an item, 64 columns a warp (dk, dv) or 32 (dq), to memory; of a
+  // part of a walk, added up in the CTA's scratch.
   // dv goes while dk's last product runs.
   __device__ __forceinline__ bool outputs(const Item& t) {
     constexpr int HALF = Shape<DP>::PARTS / 2;     // dv by the first half of the warps, dk by the others
@@ -676,9 +689,11 @@ struct Calc {
     if (dkv) dv_ph ^= 1u;
     tc_fence_after();
     const uint32_t at = tmem + lanes + (dkv ? 2 * WT + (is_dk ? DP : 0) : 3 * WT) + col;
+    float* sums = p.part + static_cast<long long>(blockIdx.x) * (2 * TILE * DP) + ((part * 4 + quad) * 64) * 32;
     const float m = is_dv ? lowered(lift_backward<T>()) : p.scale, mul[4] = {m, m, m, m};
 #pragma unroll 1
-    for (int k = 0; k < width; k += 32) store_rows<T>(at + k, out + k, stride, rows, p.dim - col - k, mul);
+    for (int k = 0; k < width; k += 32)
+      store_rows<T, PARTS>(at + k, out + k, stride, rows, p.dim - col - k, mul, t.parts, sums + 32 * k);
     warp_arrive(BAR(acc_free));
     return true;
   }
@@ -689,7 +704,7 @@ struct Calc {
 // item: an item's tiles are loaded, and its first products formed, while the
 // previous one ends.  (A CTA an item spent 5 us on start, first loads and
 // outputs, beside about 1.2 us a step.)
-template <typename T, int DP>
+template <typename T, int DP, bool PARTS>
 __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
@@ -714,12 +729,12 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
   if (warp == 0) {
-    load_role<T, DP>(p, g, sb, bb, bar);
+    load_role<T, DP, PARTS>(p, g, sb, bb, bar);
   } else if (warp == 1) {
     product_role<T, DP>(p, sb, bb, tmem, bar);
   } else {
     const int quad = warp & 3, part = (warp - CTRL_WARPS) >> 2;
-    Calc<T, DP> calc{p, smem, bb, tmem, static_cast<uint32_t>(quad * 32) << 16, &bar->abort, quad, part, COLS * part, lane};
+    Calc<T, DP, PARTS> calc{p, smem, bb, tmem, static_cast<uint32_t>(quad * 32) << 16, &bar->abort, quad, part, COLS * part, lane};
     Items items{bb, bar, {}};
     while (const Item* t = items.next(&bar->abort, p)) {
       const bool ok = t->n == 0 || (t->kind == DKV ? calc.dkv_steps(*t) : calc.dq_steps(*t));
@@ -733,6 +748,19 @@ __global__ void __launch_bounds__(Shape<DP>::THREADS, Shape<DP>::CTAS)
   if (warp == 1) tmem_dealloc(tmem, Shape<DP>::TMEM);
 }
 
+template <typename T, int DP, bool PARTS>
+cudaError_t launch_items(const AttnParams& p, const CUtensorMap* m, unsigned grid, long long nk, long long total,
+                         long long ktiles, long long qtiles, cudaStream_t s) {
+  auto kern = attn_bwd_kernel<T, DP, PARTS>;
+  static std::atomic<unsigned long long> done;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
+  if (e != cudaSuccess) return e;
+  // its prologue overlaps the statistics kernel (the wait for them is in the roles); without that one, no overlap
+  e = launch_k(p.sq > 0, kern, dim3(grid), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0], m[1], m[2], m[3], p,
+               static_cast<uint32_t>(nk), static_cast<uint32_t>(total), static_cast<int>(ktiles), static_cast<int>(qtiles));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <typename T, int DP>
 cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, bool prep, int sms, cudaStream_t s) {
   const bool packed = p.cu_q != nullptr;
@@ -744,16 +772,10 @@ cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, bool prep, in
     attn_prep_kernel<T, DP><<<static_cast<unsigned>(nq), PREP, 0, s>>>(p, static_cast<int>(qt));
     return cudaGetLastError();
   }
-  auto kern = attn_bwd_kernel<T, DP>;
-  static std::atomic<unsigned long long> done;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
-  if (e != cudaSuccess) return e;
   const long long slots = static_cast<long long>(sms) * Shape<DP>::CTAS;
   const unsigned grid = static_cast<unsigned>(nq + nk < slots ? nq + nk : slots);
-  // its prologue overlaps the statistics kernel (the wait for them is in the roles); without that one, no overlap
-  e = launch_k(p.sq > 0, kern, dim3(grid), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0], m[1], m[2], m[3], p,
-               static_cast<uint32_t>(nk), static_cast<uint32_t>(nq + nk), static_cast<int>(kt), static_cast<int>(qt));
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return p.part != nullptr ? launch_items<T, DP, true>(p, m, grid, nk, nq + nk, kt, qt, s)
+                           : launch_items<T, DP, false>(p, m, grid, nk, nq + nk, kt, qt, s);
 }
 
 template <typename T>

@@ -10,6 +10,9 @@
 // scores, from where the second product takes them as its A operand.  The row
 // sum is taken from the probabilities before they are rounded.
 //
+// o of a walk over very many keys is handed over in parts to fp32 sums in
+// memory (see op_attn.cuh), which follow the same maximum.
+//
 // A CTA that is done with its item takes over one that has not started yet
 // (a cluster launch control request), and loads it and forms its first scores
 // while the last item's outputs are written.
@@ -42,6 +45,8 @@ constexpr int CTRL_WARPS = 4;
 constexpr int THREADS = 32 * (CTRL_WARPS + 8);
 constexpr int ROWS = 2 * TILE;
 constexpr float RAISE = 8.f;
+template <typename T>
+constexpr int SUM_TILES = SUM_ROWS<T> / TILE;        // key tiles between handovers of o (PARTS)
 
 template <int DP>
 struct Smem {
@@ -109,9 +114,9 @@ __device__ __forceinline__ int answered(uint32_t answer) {
 }
 
 // ----------------------------------------------------------------- loads
-template <typename T, int DP>
+template <typename T, int DP, bool PARTS>
 __device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap* mq, const CUtensorMap* mk,
-                                          const CUtensorMap* mv, int tiles, uint32_t sb, uint32_t bb, Bars* bar) {
+                                          const CUtensorMap* mv, int tiles, int total, uint32_t sb, uint32_t bb, Bars* bar) {
   using S = Smem<DP>;
   volatile int* abort = &bar->abort;
   const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
@@ -119,15 +124,20 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap
   Ring<S::RV> rv;
   Ring<2> items;
   uint32_t q_ph[2] = {1u, 1u}, ask_ph = 0, edges = 0;
+  unsigned taken = 0;
   bool ok = true;
   PackedIndex index;
   if (p.cu_q != nullptr) index.fill(p, ROWS);
   for (int id = static_cast<int>(blockIdx.x); ok;) {
     __syncwarp();
     if (lane == 0 && id >= 0) {
-      fence_proxy_async_smem();                    // every lane has read the last answer
-      mbar_expect_at(BAR(asked), 16);
-      ask_next(BAR(answer), BAR(asked));
+      if constexpr (PARTS) {
+        taken = atomicAdd(p.counter, 1u);
+      } else {
+        fence_proxy_async_smem();                  // every lane has read the last answer
+        mbar_expect_at(BAR(asked), 16);
+        ask_next(BAR(answer), BAR(asked));
+      }
     }
     Item t;
     Work w{};
@@ -201,10 +211,15 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap
         rv.next();
       }
     }
-    ok = ok && wait_warp(BAR(asked), ask_ph, abort, p);
-    if (!ok) break;
-    ask_ph ^= 1u;
-    id = answered(BAR(answer));
+    if constexpr (PARTS) {                         // as many CTAs as there is scratch for, which take from a counter
+      const unsigned next = gridDim.x + __shfl_sync(0xffffffffu, taken, 0);
+      id = next < static_cast<unsigned>(total) ? static_cast<int>(next) : -1;
+    } else {
+      ok = ok && wait_warp(BAR(asked), ask_ph, abort, p);
+      if (!ok) break;
+      ask_ph ^= 1u;
+      id = answered(BAR(answer));
+    }
   }
   // after a wait ran out: a millisecond for copies in flight to land
   if (*abort != 0 && lane == 0) {
@@ -216,7 +231,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const CUtensorMap
 }
 
 // -------------------------------------------------------------- products
-template <typename T, int DP>
+template <typename T, int DP, bool PARTS>
 __device__ __forceinline__ void product_role(const AttnParams& p, uint32_t sb, uint32_t bb, uint32_t tmem, Bars* bar) {
   using S = Smem<DP>;
   volatile int* abort = &bar->abort;
@@ -273,6 +288,10 @@ __device__ __forceinline__ void product_role(const AttnParams& p, uint32_t sb, u
           }
           if (ok) {
             tc_fence_after();
+            // a new part: the softmax warps have taken o before they wrote these probabilities
+            if constexpr (PARTS) {
+              if ((tile - first[k]) % SUM_TILES<T> == 0) acc[k] = 0u;
+            }
             mma_over_tokens<T, DP, TILE>(tmem + 256 + k * TILE, tmem + k * TILE,
                                          desc_tokens(sb + S::V_OFF + rv.s * S::T), acc[k]);
             commit_warp(BAR(o_done) + 8 * k);
@@ -301,7 +320,17 @@ __device__ __forceinline__ void product_role(const AttnParams& p, uint32_t sb, u
 }
 
 // ------------------------------------------------------- softmax, output
-template <typename T, int DP>
+// A row's sums of o from its walk's parts, column k at [32 k] ...
+template <int DP>
+__device__ __forceinline__ float* part_sums(const AttnParams& p, int t, int quad, int lane) {
+  return p.part + ((static_cast<long long>(blockIdx.x) * 2 + t) * 4 + quad) * (32 * DP) + lane;
+}
+// ... and the factor that brings them from reference `base` to `top`.
+__device__ __forceinline__ float rescale(float base, float top, float c) {
+  return base == top ? 1.f : exp2_fast((base - top) * c);
+}
+
+template <typename T, int DP, bool PARTS>
 __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, uint32_t tmem, Bars* bar) {
   volatile int* abort = &bar->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -319,9 +348,29 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
     const int q0 = i0 + t * TILE, q = q0 + quad * 32 + lane;
     float top = -INFINITY;                         // the scores' reference, before scaling
     F2 sum2 = f2_make(0.f, 0.f);
+    [[maybe_unused]] float base = top;             // PARTS: the reference of the handed over sums
     bool ok = true;
     for (int i = 0; i < cnt; ++i, ++steps) {
       const int j0 = (first + i) * TILE;
+      if constexpr (PARTS) {
+        if (i > 0 && i % SUM_TILES<T> == 0) {
+          ok = wait_warp(BAR(o_done) + 8 * t, (steps - 1) & 1u, abort, p);
+          if (!ok) break;
+          tc_fence_after();
+          float* sums = part_sums<DP>(p, t, quad, lane);
+          const float f = rescale(base, top, c);
+#pragma unroll 1
+          for (int k = 0; k < DP; k += 32) {
+            float o[32];
+            tmem_ld32(o_at + k, o);
+            tmem_ld_wait();
+            float* at = sums + 32 * k;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) at[32 * e] = i == SUM_TILES<T> ? o[e] : fmaf(at[32 * e], f, o[e]);
+          }
+          base = top;
+        }
+      }
       float v[TILE];
       ok = wait_warp(BAR(s_full) + 8 * t, steps & 1u, abort, p);
       if (!ok) break;
@@ -393,6 +442,23 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
     if (ok && cnt > 0) ok = wait_warp(BAR(o_done) + 8 * t, (steps - 1) & 1u, abort, p);
     if (!ok) break;
     tc_fence_after();
+    if constexpr (PARTS) {
+      if (cnt > SUM_TILES<T>) {                    // the last part's o joins the others
+        const float* sums = part_sums<DP>(p, t, quad, lane);
+        const float f = rescale(base, top, c);
+#pragma unroll 1
+        for (int k = 0; k < DP; k += 32) {
+          float o[32];
+          tmem_ld32(o_at + k, o);
+          tmem_ld_wait();
+          const float* at = sums + 32 * k;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(at[32 * e], f, o[e]);
+          tmem_st32(o_at + k, reinterpret_cast<const uint32_t*>(o));
+        }
+        tmem_st_wait();
+      }
+    }
     const float2 s2 = f2_split(sum2);
     const float sum = s2.x + s2.y, inv = sum == 0.f ? 0.f : 1.f / sum;
     const int row = t * TILE + quad * 32, rows = it.rows - row;      // the warp's first query, and queries from it on
@@ -414,10 +480,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const AttnParams p, int tiles) {
+                    const __grid_constant__ CUtensorMap mv, const AttnParams p, int tiles, int total) {
   using S = Smem<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + S::BAR_OFF);
@@ -455,11 +521,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   // control warps (4 x 32 x 88 + 8 x 32 x 200 of the 384 x 168 at launch)
   if (warp < CTRL_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0) load_role<T, DP>(p, &mq, &mk, &mv, tiles, sb, bb, bar);
-    if (warp == 1) product_role<T, DP>(p, sb, bb, tmem, bar);
+    if (warp == 0) load_role<T, DP, PARTS>(p, &mq, &mk, &mv, tiles, total, sb, bb, bar);
+    if (warp == 1) product_role<T, DP, PARTS>(p, sb, bb, tmem, bar);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    softmax_role<T, DP>(p, bb, tmem, bar);
+    softmax_role<T, DP, PARTS>(p, bb, tmem, bar);
   }
   tc_fence_before();
   __syncthreads();
@@ -467,31 +533,42 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+template <typename T, int DP, bool PARTS>
+cudaError_t launch_items(const AttnParams& p, const CUtensorMap* m, long long grid, long long tiles, long long items,
+                         cudaStream_t s) {
+  auto kern = attn_fwd_kernel<T, DP, PARTS>;
+  static std::atomic<unsigned long long> done;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(grid), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], p, static_cast<int>(tiles),
+                                                                     static_cast<int>(items));
+  return cudaGetLastError();
+}
+
 template <typename T, int DP>
-cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
+cudaError_t launch_dims(const AttnParams& p, const CUtensorMap* m, int sms, cudaStream_t s) {
   const bool packed = p.cu_q != nullptr;
   const long long tiles = tile_bound(p.sq, ROWS, p.batch, packed);
   const long long items = tiles * p.heads * (packed ? 1 : p.batch);
   if (items > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  auto kern = attn_fwd_kernel<T, DP>;
-  static std::atomic<unsigned long long> done;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
+  if (p.part == nullptr) return launch_items<T, DP, false>(p, m, items, tiles, items, s);
+  const cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(unsigned), s);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(items), THREADS, Smem<DP>::BYTES, s>>>(m[0], m[1], m[2], p, static_cast<int>(tiles));
-  return cudaGetLastError();
+  const long long ctas = attn_part_ctas(p.dim, false, sms);
+  return launch_items<T, DP, true>(p, m, items < ctas ? items : ctas, tiles, items, s);
 }
 
 template <typename T>
-cudaError_t launch_type(const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
-  return p.dim <= 64 ? launch_dims<T, 64>(p, m, s) : launch_dims<T, 128>(p, m, s);
+cudaError_t launch_type(const AttnParams& p, const CUtensorMap* m, int sms, cudaStream_t s) {
+  return p.dim <= 64 ? launch_dims<T, 64>(p, m, sms, s) : launch_dims<T, 128>(p, m, sms, s);
 }
 
 }  // namespace
 
 int attn_qtiles(int sq, int batch, bool packed) { return static_cast<int>(tile_bound(sq, TILE, batch, packed)); }
 
-cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
-  return p.dtype == DT_BF16 ? launch_type<__nv_bfloat16>(p, m, s) : launch_type<__half>(p, m, s);
+cudaError_t launch_attn_fwd(const AttnParams& p, const CUtensorMap* m, int sms, cudaStream_t s) {
+  return p.dtype == DT_BF16 ? launch_type<__nv_bfloat16>(p, m, sms, s) : launch_type<__half>(p, m, sms, s);
 }
 
 }  // namespace muon

@@ -1,5 +1,6 @@
 // C ABI of the training operators (see include/muon.h): checks of the
 // arguments, workspace layout and launches.  No exception leaves an entry.
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -55,6 +56,16 @@ muon_status_t check_act8(muon_handle_t h, const uint8_t* codes, int64_t ldc, con
   return MUON_OK;
 }
 
+// Scratch of the CTAs whose walks are over more rows than one accumulator
+// takes (a bound when packed: the sequences' lengths are on the device).
+uint64_t attn_part_bytes(muon_handle_t h, const muon_attention_t& a, bool bwd) {
+  if (a.sq == 0 || a.sk == 0) return 0;
+  const int64_t reach = a.window > 0 ? int64_t(a.window) + 128 : kMaxTokens;       // of the rows that a tile sees
+  const int64_t keys = std::min<int64_t>(a.sk, reach), queries = std::min<int64_t>(a.sq, reach) * (a.heads / a.kv_heads);
+  if (std::max<int64_t>(keys, bwd ? queries : 0) <= attn_sum_rows(a.dtype == MUON_BF16)) return 0;
+  return static_cast<uint64_t>(attn_part_ctas(a.dim, bwd, h->num_sms)) * attn_part_floats(a.dim) * 4;
+}
+
 // Two statistics of every query, by tiles of 128, then a counter.
 uint64_t attn_stat_bytes(const muon_attention_t& a) {
   const bool packed = a.cu_seqlens_q != nullptr;
@@ -62,7 +73,9 @@ uint64_t attn_stat_bytes(const muon_attention_t& a) {
   return 2 * 512 * b * static_cast<uint64_t>(a.heads) * static_cast<uint64_t>(attn_qtiles(a.sq, a.batch, packed));
 }
 
-uint64_t attn_workspace(const muon_attention_t& a) { return a.sq > 0 ? attn_stat_bytes(a) + 256 : 0; }
+uint64_t attn_workspace(muon_handle_t h, const muon_attention_t& a) {
+  return a.sq > 0 ? attn_stat_bytes(a) + 256 + attn_part_bytes(h, a, true) : 0;
+}
 
 muon_status_t check_attention(muon_handle_t h, const muon_attention_t* a) {
   MUON_CHECK(a != nullptr, "a is NULL");
@@ -273,10 +286,29 @@ muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t 
 }
 
 muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a, void* stream_arg) {
+  return muon_attention_forward_ex(h, a, nullptr, 0, stream_arg);
+}
+
+muon_status_t muon_attention_forward_workspace(muon_handle_t h, const muon_attention_t* a, uint64_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded([&]() -> muon_status_t {
+    const muon_status_t st = check_attention(h, a);
+    if (st != MUON_OK) return st;
+    const uint64_t part = attn_part_bytes(h, *a, false);
+    *bytes = part > 0 ? part + 256 : 0;            // and a counter
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_attention_forward_ex(muon_handle_t h, const muon_attention_t* a, void* workspace,
+                                        size_t workspace_bytes, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded([&]() -> muon_status_t {
     const muon_status_t st = check_attention(h, a);
     if (st != MUON_OK) return st;
+    const uint64_t part = attn_part_bytes(h, *a, false);
+    MUON_CHECK(workspace == nullptr || part == 0 || (workspace_bytes >= part + 256 && aligned(workspace, 256)),
+               "the workspace is too small or not 256-byte aligned");
     const bool packed = a->cu_seqlens_q != nullptr;
     if (a->sq == 0 || (a->batch == 0 && !packed)) return MUON_OK;
     const int64_t nb = packed ? 1 : a->batch;
@@ -289,6 +321,10 @@ muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a,
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
     AttnParams p = attn_params(h, *a);
     p.out = a->o;
+    if (part > 0 && workspace != nullptr) {
+      p.part = static_cast<float*>(workspace);
+      p.counter = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + part);
+    }
     CUtensorMap m[3] = {};
     bool ok = attn_map(h, &m[0], a->q, a->q_stride, qn, a->dim, a->dtype, 128);
     if (a->sk > 0)
@@ -296,7 +332,7 @@ muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a,
            attn_map(h, &m[2], a->v, a->v_stride, kn, a->dim, a->dtype, 128);
     if (!ok) return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     h->prof_tag = -1;
-    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_fwd(p, m, stream), "attention launch");
+    MUON_LAUNCH(MUON_K_ATTENTION, launch_attn_fwd(p, m, h->num_sms, stream), "attention launch");
     return MUON_OK;
   });
 }
@@ -306,7 +342,7 @@ muon_status_t muon_attention_workspace(muon_handle_t h, const muon_attention_t* 
   return guarded([&]() -> muon_status_t {
     const muon_status_t st = check_attention(h, a);
     if (st != MUON_OK) return st;
-    *bytes = attn_workspace(*a);
+    *bytes = attn_workspace(h, *a);
     return MUON_OK;
   });
 }
@@ -330,7 +366,7 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
                kBadOperand);
     if (a->sq > 0) {
       MUON_CHECK(a->lse != nullptr, "lse is NULL");
-      MUON_CHECK(workspace != nullptr && workspace_bytes >= attn_workspace(*a) && aligned(workspace, 256),
+      MUON_CHECK(workspace != nullptr && workspace_bytes >= attn_workspace(h, *a) && aligned(workspace, 256),
                  "the workspace is too small or not 256-byte aligned");
     }
     DeviceGuard guard(h->device);
@@ -344,6 +380,8 @@ muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a
     p.stat_lse = static_cast<float*>(workspace);
     p.stat_delta = p.stat_lse + attn_stat_bytes(*a) / 8;
     p.counter = a->sq > 0 ? reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + attn_stat_bytes(*a)) : nullptr;
+    if (attn_part_bytes(h, *a, true) > 0)
+      p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_stat_bytes(*a) + 256);
     CUtensorMap m[4] = {};
     const uint32_t tokens = a->dim <= 64 ? 64 : 128;
     bool ok = true;

@@ -307,7 +307,12 @@ PyObject* attention(Args a) {
   p.o = o.data_ptr();
   p.lse = lse.data_ptr<float>();
   set_strides(p.o_stride, o, "o", p.cu_seqlens_q != nullptr);
-  const muon_status_t st = muon_attention_forward(t.h, &p, t.stream());
+  uint64_t need = 0;
+  muon_status_t st = muon_attention_forward_workspace(t.h, &p, &need);
+  if (st != MUON_OK) return PyLong_FromLong(st);
+  at::Tensor ws;
+  if (need > 0) ws = empty({static_cast<int64_t>(need)}, q, at::kByte);
+  st = muon_attention_forward_ex(t.h, &p, need > 0 ? ws.data_ptr() : nullptr, need, t.stream());
   if (st != MUON_OK) return PyLong_FromLong(st);
   return results(std::move(o), std::move(lse), at::Tensor());
 }

@@ -13,6 +13,7 @@ Tolerances, element by element.  u is the unit roundoff of the storage type:
   * The weight gradient multiplies exact bf16 factors and sums in fp32, 16
     products at a time: (rows / 16 + 16) 2^-23 of the terms' magnitudes.
 """
+import ctypes
 import math
 
 import numpy as np
@@ -611,7 +612,7 @@ def test_act8_weight_grad_waits_end(muon, rows, cols, out):
 
 
 # ------------------------------------------- attention over very many keys
-def attention_reference(q, k, v, do):
+def attention_reference(q, k, v, do, causal=False, window=0):
     """One sequence whose heads share one key head, in fp64 on the GPU: o, lse, (dq, dk, dv), and the magnitudes of
     the products that are summed into o and into each gradient (|do||v| + |do||o| in the place of their difference)."""
     q, k, v, do = q.double(), k.double()[:, 0], v.double()[:, 0], do.double()
@@ -623,6 +624,10 @@ def attention_reference(q, k, v, do):
         for i in range(0, len(q), step):
             at = (slice(i, i + step), h)
             s = (q[at] @ k.T) * scale
+            if causal:
+                place = torch.arange(i, i + len(s), device="cuda")[:, None] + (len(k) - len(q))
+                j = torch.arange(len(k), device="cuda")
+                s[(j > place) | (j <= place - window if window else j > place)] = -torch.inf
             z = torch.logsumexp(s, 1)
             p = torch.exp(s - z[:, None])
             o[at], mo[at], lse[h, i:i + step] = p @ v, p @ v.abs(), z
@@ -658,3 +663,73 @@ def test_fp16_gradient_of_a_flat_softmax(muon):
     _, _, (_, _, rv), _, (_, _, mv) = attention_reference(q[0], k[0], v[0], do[0])
     near_on_gpu("small probabilities dv", grads[2][0], rv, gpu_tol(U[HF], rv, mv, mv))
     assert muon.default_handle().check() == 0
+
+
+# Walks over so many rows that the tensor core's truncation shows in values of one sign: the tolerance knows no length.
+@pytest.mark.parametrize("dim,dtype", [(64, HF), (128, HF), (128, BF)])
+@pytest.mark.parametrize("sq,sk,heads,causal,window", [
+    (65536, 128, 8, False, 0), (128, 1 << 19, 1, False, 0), (200, 70001, 3, True, 0), (20011, 20011, 2, True, 0),
+    (20011, 20011, 2, True, 9001)])
+def test_attention_over_many_rows_of_one_sign(muon, sq, sk, heads, causal, window, dim, dtype):
+    q, k = rand(130, 1, sq, heads, dim).abs().to(dtype), rand(131, 1, sk, 1, dim).abs().to(dtype)
+    v, do = (rand(132, 1, sk, 1, dim).abs() + 0.5).to(dtype), (rand(133, 1, sq, heads, dim).abs() + 0.5).to(dtype)
+    kw = dict(causal=causal, window=window)
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    assert muon.default_handle().check() == 0
+    ro, rl, refs, mo, mags = attention_reference(q[0], k[0], v[0], do[0], **kw)
+    tag = f"one sign {sq}x{sk} h{heads} d{dim} w{window} {dtype}"
+    near_on_gpu(tag + " o", o[0], ro, gpu_tol(U[dtype], ro, mo, mo))
+    near_on_gpu(tag + " lse", lse[0], rl, 2.0 ** -17 * (rl.abs() + 1))
+    for n, g, r, m in zip(("dq", "dk", "dv"), grads, refs, mags):
+        near_on_gpu(f"{tag} {n}", g[0], r, gpu_tol(U[dtype], r, m, m))
+    assert torch.equal(o, muon.attention(q, k, v, **kw)[0])
+    for a, b in zip(grads, muon.attention_backward(do, q, k, v, o, lse, **kw)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, HF)])
+def test_long_documents_beside_short_ones(muon, dim, dtype):
+    lengths = [100, 9000, 1, 12001, 300]
+    cuts = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    q, do = rand(134, cuts[-1], 4, dim, dtype=dtype), rand(135, cuts[-1], 4, dim, dtype=dtype)
+    k, v = rand(136, cuts[-1], 2, dim, dtype=dtype), rand(137, cuts[-1], 2, dim, dtype=dtype)
+    cu = torch.tensor(cuts, dtype=torch.int32).cuda()
+    kw = dict(causal=True, cu_seqlens_q=cu, cu_seqlens_k=cu)
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    assert muon.default_handle().check() == 0
+    for a, b in zip(cuts, cuts[1:]):
+        one, one_lse = muon.attention(*(t[None, a:b] for t in (q, k, v)), causal=True)
+        assert torch.equal(one[0], o[a:b]) and torch.equal(one_lse[0], lse[:, a:b])
+        for x, g in zip(muon.attention_backward(*(t[None, a:b] for t in (do, q, k, v)), one, one_lse, causal=True), grads):
+            assert torch.equal(x[0], g[a:b])
+
+
+def test_attention_without_scratch(muon):
+    """The call without a workspace: the same bits up to 8192 keys, one accumulator beyond; a workspace that is too
+    small is refused."""
+    from newton_schulz_orthogonalized_muon_gb300 import _binding
+    h, stream = muon.default_handle(), torch.cuda.current_stream().cuda_stream
+    for sk in (8192, 8200):
+        q, k, v = (rand(138 + i, 1, n, 1, 64, dtype=HF) for i, n in enumerate((130, sk, sk)))
+        o, lse = torch.empty_like(q), torch.empty(1, 1, 130, device="cuda")
+        a = _binding.MuonAttentionC(q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), o=o.data_ptr(), lse=lse.data_ptr(),
+                                    batch=1, sq=130, sk=sk, heads=1, kv_heads=1, dim=64, dtype=_binding.MUON_F16,
+                                    scale=0.125)
+        for n in ("q", "k", "v", "o"):
+            getattr(a, n + "_stride")[:] = [1 << 20, 64, 64]
+        need = ctypes.c_uint64()
+        assert h._lib.muon_attention_forward_workspace(h.ptr, bytes(a), ctypes.byref(need)) == 0
+        assert (need.value > 0) == (sk > 8192)
+        assert h._lib.muon_attention_forward(h.ptr, bytes(a), stream) == 0
+        want, want_lse = muon.attention(q, k, v)
+        if sk == 8192:
+            assert torch.equal(o, want) and torch.equal(lse, want_lse)
+        else:
+            assert (o - want).abs().max().item() < 2.0 ** -8 and torch.equal(lse, want_lse)
+            ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+            assert h._lib.muon_attention_forward_ex(h.ptr, bytes(a), ws.data_ptr(), need.value - 1, stream) == 1
+            assert h._lib.muon_attention_forward_ex(h.ptr, bytes(a), ws.data_ptr(), need.value, stream) == 0
+            assert torch.equal(o, want)
+    assert h.check() == 0
