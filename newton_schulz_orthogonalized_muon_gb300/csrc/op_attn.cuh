@@ -453,7 +453,15 @@ __device__ __forceinline__ uint32_t bits32(int lo, int hi) {
 // Probabilities are rounded to T times 2^N, taken back from what they are
 // summed to: fp16 has few bits left below 2^-14 and none below 2^-25, and
 // over many keys such probabilities add up.  (bf16 has fp32's range: N = 0.)
-// Backward they reach about 1.
+// Forward they reach 2^raise, backward about 1.
+template <typename T>
+__host__ __device__ constexpr int lift_forward() {
+  return std::is_same<T, __half>::value ? 11 : 0;
+}
+template <typename T>
+__host__ __device__ constexpr float raise() {
+  return std::is_same<T, __half>::value ? 4.f : 8.f;
+}
 template <typename T>
 __host__ __device__ constexpr int lift_backward() {
   return std::is_same<T, __half>::value ? 14 : 0;

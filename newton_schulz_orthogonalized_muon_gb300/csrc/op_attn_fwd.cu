@@ -20,7 +20,9 @@
 // The maximum that a row's exponents are taken against is raised only when a
 // new score passes it by more than 2^8 (in exp2 units): o and the sum are
 // then scaled down in TMEM.  Below that the probabilities stay under 256,
-// exact in the same relative precision, and o is left alone.
+// exact in the same relative precision, and o is left alone.  (fp16: 2^4
+// instead of 2^8, and all of them and their sum lifted by 2^11, so that small
+// ones keep their bits; see op_attn.cuh.)
 //
 // Bound by the products together with what feeds them: two 128 x 128 tile
 // pairs with dim 128 take 2048 cycles of the tensor pipe, and as many of
@@ -44,7 +46,6 @@ using namespace attn;
 constexpr int CTRL_WARPS = 4;
 constexpr int THREADS = 32 * (CTRL_WARPS + 8);
 constexpr int ROWS = 2 * TILE;
-constexpr float RAISE = 8.f;
 template <typename T>
 constexpr int SUM_TILES = SUM_ROWS<T> / TILE;        // key tiles between handovers of o (PARTS)
 
@@ -403,7 +404,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
       if (i == 0) {
         top = mt;
       } else {
-        const bool up = mt > top && (top == -INFINITY || (mt - top) * c > RAISE);
+        const bool up = mt > top && (top == -INFINITY || (mt - top) * c > raise<T>());
         if (__any_sync(0xffffffffu, up)) {
           ok = wait_warp(BAR(o_done) + 8 * t, (steps - 1) & 1u, abort, p);
           if (!ok) break;
@@ -424,8 +425,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
           tmem_st_wait();
         }
       }
-      const float ref = top == -INFINITY ? 0.f : -top * c;
+      const float ref = top == -INFINITY ? 0.f : fmaf(-top, c, static_cast<float>(lift_forward<T>()));
       const F2 rr = f2_make(ref, ref);
+      F2 here = f2_make(0.f, 0.f);                 // this tile's sum: small values meet each other first
 #pragma unroll
       for (int k = 0; k < TILE; k += 64) {
 #pragma unroll
@@ -433,10 +435,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
           const float2 a = f2_split(f2_fma(f2_make(v[e], v[e + 1]), cc, rr));
           v[e] = exp2_fast(a.x);
           v[e + 1] = exp2_fast(a.y);
-          sum2 = f2_add(sum2, f2_make(v[e], v[e + 1]));
+          here = f2_add(here, f2_make(v[e], v[e + 1]));
         }
         store_rounded<T, 32>(s_at + k / 2, v + k);
       }
+      sum2 = f2_add(sum2, here);
       warp_arrive(BAR(p_full) + 8 * t);
     }
     if (ok && cnt > 0) ok = wait_warp(BAR(o_done) + 8 * t, (steps - 1) & 1u, abort, p);
@@ -463,7 +466,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, uint32_t bb, u
     const float sum = s2.x + s2.y, inv = sum == 0.f ? 0.f : 1.f / sum;
     const int row = t * TILE + quad * 32, rows = it.rows - row;      // the warp's first query, and queries from it on
     T* out = static_cast<T*>(it.out) + row * p.os;
-    if (lane < rows) it.lse[row + lane] = sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum));
+    if (lane < rows) it.lse[row + lane] = sum == 0.f ? -INFINITY : fmaf(top, p.scale, logf(sum * lowered(lift_forward<T>())));
     if (cnt > 0) {
       float mul[4];
 #pragma unroll

@@ -653,6 +653,20 @@ def gpu_tol(u, ref, mag, wide):
     return u * ref.abs() + 1.02 * u * mag + 2.0 ** -15 * wide + 2.0 ** -25
 
 
+def test_fp16_probabilities_that_are_small_but_many(muon):
+    n = 1 << 18
+    # forward: one key far above 2^18 others, which have 2^-26 of its weight each and 2^-8 together
+    q = torch.zeros(1, 40, 1, 64, dtype=HF, device="cuda")
+    k, v = torch.zeros(1, n + 5, 1, 64, dtype=HF, device="cuda"), torch.ones(1, n + 5, 1, 64, dtype=HF, device="cuda")
+    q[..., 0] = 12.0
+    k[0, 3, 0, 0], v[0, 3] = 12.015625, 0.0                       # score 18.02 = 26 log(2)
+    o, lse = muon.attention(q, k, v)
+    ro, rl, _, mag, _ = attention_reference(q[0], k[0], v[0], q[0])
+    near_on_gpu("many small probabilities o", o[0], ro, gpu_tol(U[HF], ro, mag, mag))
+    near_on_gpu("many small probabilities lse", lse[0], rl, 2.0 ** -17 * (rl.abs() + 1))
+    assert muon.default_handle().check() == 0
+
+
 def test_fp16_gradient_of_a_flat_softmax(muon):
     """2^18 keys with probabilities of 2^-18."""
     n = 1 << 18
