@@ -69,10 +69,13 @@ struct muon_handle_s {
 
 namespace muon {
 
+// The set call is made on the right device too: a thread that has called no
+// CUDA function yet (autograd's, say) has no context before it, and tensor
+// maps are not encoded without one.
 struct DeviceGuard {
   int prev = -1;
   explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) cudaSetDevice(dev);
+    if (cudaGetDevice(&prev) == cudaSuccess) cudaSetDevice(dev);
   }
   ~DeviceGuard() {
     int cur = -1;

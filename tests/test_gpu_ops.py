@@ -747,3 +747,37 @@ def test_attention_without_scratch(muon):
             assert h._lib.muon_attention_forward_ex(h.ptr, bytes(a), ws.data_ptr(), need.value, stream) == 0
             assert torch.equal(o, want)
     assert h.check() == 0
+
+
+# ------------------------------------------------------------------ threads
+def test_first_cuda_call_of_a_thread(muon):
+    """Calls that build tensor maps, from a thread that has used no CUDA function before."""
+    import threading
+    q = rand(150, 1, 200, 2, 64, dtype=BF)
+    o, lse = muon.attention(q, q, q, causal=True)
+    kept, dy = muon.act8_store(rand(151, 200, 256, dtype=BF)), rand(152, 200, 72, dtype=BF)
+    w, g = rand(153, 256, 512, dtype=BF), rand(154, 256, 512, dtype=BF)
+    m = torch.zeros(256, 512, device="cuda")
+    calls = [lambda: muon.attention(q, q, q, causal=True),
+             lambda: muon.attention_backward(q, q, q, q, o, lse, causal=True),
+             lambda: (muon.act8_weight_grad(dy, *kept),),
+             lambda: muon.muon_step([w], [g], [m], lr=0.02, wd=0.1)]
+    want = [call() for call in calls[:3]]
+    calls[3]()
+    for call, ref in zip(calls, want + [None]):
+        got = []
+
+        def work():
+            try:
+                got.append(call())
+            except Exception as e:          # the thread's own: raised below
+                got.append(e)
+        torch.cuda.synchronize()
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        if isinstance(got[0], Exception):
+            raise got[0]
+        if ref is not None:
+            assert all(torch.equal(a, b) for a, b in zip(got[0], ref))
+    assert muon.default_handle().check() == 0
