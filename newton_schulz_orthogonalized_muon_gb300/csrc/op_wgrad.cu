@@ -21,7 +21,7 @@
 // Few tiles and many tokens: the tokens are split over several pairs, whose
 // fp32 partial results a second kernel adds in a fixed order.
 //
-// 16384 tokens, 4096 columns, 14336 outputs in 1.14 ms, 1680 TFLOP/s, bound by
+// 16384 tokens, 4096 columns, 14336 outputs in 1.19 ms, 1620 TFLOP/s, bound by
 // the products (and, in long runs, by the power limit: 1.27 ms); 1001 x 2048 x
 // 1408 with `add` in 21 us, of which 14 are a CTA's start, first loads and
 // epilogue.
@@ -59,10 +59,12 @@ constexpr int SMEM = BAR_OFF + 512;
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
 static_assert(SMEM <= 232448, "shared memory");
 
-struct Bars {
+struct alignas(16) Bars {
   uint64_t dy_full[DY_STAGES], dy_empty[DY_STAGES];         // full: the leader's, for both CTAs
   uint64_t code_full[CODE_STAGES], code_empty[CODE_STAGES]; // each CTA's own
   uint64_t x_full[X_STAGES], x_empty[X_STAGES];             // full: the leader's, for both CTAs
+  uint64_t x_here[X_STAGES];                                // the other CTA's: its half of x is written
+  uint4 token[2];                                           // sent, received (see send_token)
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
@@ -93,13 +95,31 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t cta_mask) {
       : "memory");
 }
 
-// Arrives on a barrier of the pair for shared-memory writes that the fence
-// before it has handed to the async proxy: the tensor core reads them in the
-// SM that wrote them, so nothing has to be released to the other CTA's
-// threads.  (A release at cluster scope here held every conversion step for
-// about 1000 cycles.)
-__device__ __forceinline__ void arrive_operand(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// The leader's product reads what the other CTA's warps wrote to their shared
+// memory, so those writes have to be ordered before it across the CTAs.  Their
+// fence hands them to the async proxy, a barrier of their own CTA collects
+// them, and one warp then sends 16 bytes to the leader, an asynchronous copy
+// that completes on the leader's barrier as a release at cluster scope.  (An
+// arrival with that release by the writing warps held each for 1900 cycles and
+// took 2.4 ms at 16384 x 4096 x 14336, one such arrival by the one warp 2.9;
+// an arrival without it, which orders nothing between CTAs, 1.13.)
+__device__ __forceinline__ void send_token(uint32_t dst, uint32_t src, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
+               "r"(src), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void gave_up(volatile int* abort, unsigned* err) {
@@ -113,15 +133,16 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatil
   return false;
 }
 // a warp; SLEEP: nanoseconds between polls where the wait is long and the
-// issue slots are better left to the code warps
-template <int SLEEP = 0>
+// issue slots are better left to the code warps; PAIR: for what the other CTA did
+template <int SLEEP = 0, bool PAIR = false>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const WgradParams& p) {
   const uint32_t a = smem_u32(bar);
-  if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  auto done = [&]() { return __all_sync(0xffffffffu, PAIR ? try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) != 0; };
+  if (done()) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (SLEEP > 0) __nanosleep(SLEEP);
-    if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    if (done()) return true;
     if ((it & 31u) == 0u) {
       const bool stop = *abort != 0 || globaltimer_ns() - t0 > p.timeout_ns;
       if (__any_sync(0xffffffffu, stop)) {
@@ -253,7 +274,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&bar->code_empty[s], GROUP_WARPS);
     }
     for (int s = 0; s < X_STAGES; ++s) {
-      mbar_init(&bar->x_full[s], 2 * GROUP_WARPS);
+      mbar_init(&bar->x_full[s], GROUP_WARPS);     // and the other CTA's token
+      mbar_init(&bar->x_here[s], GROUP_WARPS);
       mbar_init(&bar->x_empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -261,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&bar->tempty[a], 2 * EPI_WARPS);
     }
     mbar_init(&bar->drain, 1);
+    bar->token[0] = make_uint4(0u, 0u, 0u, 0u);
     bar->abort = (sb & 1023u) != 0u ? 1 : 0;       // the swizzled boxes need 1 KB boundaries
     if (bar->abort) atomicOr(p.err, ERRBIT_TIMEOUT);
     fence_mbar_init();
@@ -323,7 +346,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
       }
-    } else if (rank == 0) {
+    } else if (rank != 0) {
+      // ------------------------------- this CTA's halves of x, reported
+      const uint32_t full = mapa_shared(smem_u32(&bar->x_full[0]), 0), to = mapa_shared(smem_u32(&bar->token[1]), 0);
+      Ring<X_STAGES> rx;
+      bool ok = true;
+      for (int i = pair; ok && i < items; i += npairs) {
+        const Item t = item_of(p, i);
+        for (int k = t.k0; k < t.k1; ++k) {
+          ok = wait_warp(&bar->x_here[rx.s], rx.ph, abort, p);
+          if (!ok) break;
+          if (lane == 0) send_token(to, smem_u32(&bar->token[0]), full + rx.s * 8);
+          __syncwarp();
+          rx.next();
+        }
+      }
+    } else {
       // ----------------------------------------------------- products
       // both operands MN-major; M = 256 over the pair, N = 256
       const uint32_t id = idesc_bf16_f32(PT, PT, 1) | (1u << 15);
@@ -335,13 +373,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int i = pair; ok && i < items; i += npairs) {
         const Item t = item_of(p, i);
         for (int k0 = t.k0; ok && k0 < t.k1; k0 += STEPS_SUM) {
-          ok = wait_warp(&bar->tempty[acc], acc_ph ^ 1u, abort, p);
+          ok = wait_warp<0, true>(&bar->tempty[acc], acc_ph ^ 1u, abort, p);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + acc * PT;
           const int k1 = min(k0 + STEPS_SUM, t.k1);
           for (int k = k0; k < k1; ++k) {
-            ok = wait_warp(&bar->dy_full[rd.s], rd.ph, abort, p) && wait_warp(&bar->x_full[rx.s], rx.ph, abort, p);
+            ok = wait_warp(&bar->dy_full[rd.s], rd.ph, abort, p) && wait_warp<0, true>(&bar->x_full[rx.s], rx.ph, abort, p);
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = sdesc_sw128(sb + rd.s * 2 * BOX, BOX, 1024);
@@ -413,7 +451,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          arrive_operand(mapa_shared(smem_u32(&bar->x_full[rx.s]), 0));
+          if (rank != 0)
+            mbar_arrive(&bar->x_here[rx.s]);
+          else if (cw % GROUP_WARPS == 0)
+            mbar_arrive_expect_tx(&bar->x_full[rx.s], sizeof(uint4));
+          else
+            mbar_arrive(&bar->x_full[rx.s]);
           mbar_arrive(&bar->code_empty[rc.s]);
         }
         rc.next(GROUPS);

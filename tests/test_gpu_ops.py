@@ -780,4 +780,16 @@ def test_first_cuda_call_of_a_thread(muon):
             raise got[0]
         if ref is not None:
             assert all(torch.equal(a, b) for a, b in zip(got[0], ref))
+
+
+# ------------------------------------------------ many steps of a CTA (pair)
+def test_act8_weight_grad_repeats_its_bits(muon):
+    """Both CTAs of a pair write an operand that one of them reads: many steps, the same bits every time."""
+    dy, kept = rand(140, 9000, 2500, dtype=BF), muon.act8_store(rand(141, 9000, 1500, dtype=BF))
+    want = muon.act8_weight_grad(dy, *kept)
+    for _ in range(30):
+        assert torch.equal(muon.act8_weight_grad(dy, *kept), want)
+    ref = torch.mm(dy.double().t(), muon.act8_restore(*kept, dtype=FP).double())
+    mag = torch.mm(dy.double().abs().t(), muon.act8_restore(*kept, dtype=FP).double().abs())
+    near_on_gpu("weight grad 9000x1500x2500", want, ref, U[FP] * ref.abs() + (9000 / 16 + 16) * 2.0 ** -23 * mag)
     assert muon.default_handle().check() == 0
