@@ -360,6 +360,14 @@ PyObject* attention_backward(Args a) {
 // --------------------------------------------------- activations in 8 bits
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+// [rows][cols] bytes with row stride ld, on storage of whole rows: the kernels
+// read codes in groups of 8 and scales in groups of 16, the last ones too.
+at::Tensor padded(int64_t rows, int64_t cols, int64_t ld, const at::Tensor& like, at::ScalarType type) {
+  at::Tensor t = empty({rows, ld}, like, type);
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({rows, cols}), at::IntArrayRef({ld, 1}));
+  return t;
+}
+
 PyObject* act8_store(Args a) {
   const Target t = a.target();
   const at::Tensor& x = *a.tensor(t, "x");
@@ -368,8 +376,7 @@ PyObject* act8_store(Args a) {
   const Rows xr = rows_of(x, "x");
   const int64_t rows = x.size(0), cols = x.size(1), blocks = round_up(cols, kBlock) / kBlock;
   const int64_t ldc = blocks * kBlock, lds = round_up(rows, 16);
-  at::Tensor codes = at::empty_strided({rows, cols}, {ldc, 1}, x.options().dtype(at::kFloat8_e4m3fn));
-  at::Tensor scales = at::empty_strided({blocks, rows}, {lds, 1}, x.options().dtype(at::kByte));
+  at::Tensor codes = padded(rows, cols, ldc, x, at::kFloat8_e4m3fn), scales = padded(blocks, rows, lds, x, at::kByte);
   const muon_status_t st =
       muon_act8_store(t.h, xr.t.data_ptr(), xr.ld, static_cast<uint8_t*>(codes.data_ptr()), ldc,
                       static_cast<uint8_t*>(scales.data_ptr()), lds, rows, cols, type, t.stream());
@@ -394,18 +401,19 @@ Act8 act8_of(const at::Tensor& codes, const at::Tensor& scales) {
     refuse("scales must be uint8 of shape (" + std::to_string(blocks) + ", " + std::to_string(rows) + ")");
   Act8 r{codes, scales, rows, cols, codes.stride(0), scales.stride(0)};
   if (rows == 0 || cols == 0) return r;
-  auto usable = [](const at::Tensor& t, int64_t ld, int64_t unit) {
-    return (t.stride(1) == 1 || t.size(1) == 1) && ld % unit == 0 && ld >= t.size(1) &&
-           reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0;
+  auto usable = [](const at::Tensor& t, int64_t ld, int64_t unit, int64_t group) {
+    if ((t.stride(1) != 1 && t.size(1) != 1) || ld % unit != 0 || ld < t.size(1)) return false;
+    const int64_t end = t.storage_offset() + (t.size(0) - 1) * ld + round_up(t.size(1), group);
+    return end <= static_cast<int64_t>(t.storage().nbytes()) && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0;
   };
-  if (!usable(r.codes, r.ldc, kBlock)) {
+  if (!usable(r.codes, r.ldc, kBlock, 8)) {
     r.ldc = blocks * kBlock;
-    r.codes = at::empty_strided({rows, cols}, {r.ldc, 1}, codes.options().dtype(at::kByte));
+    r.codes = padded(rows, cols, r.ldc, codes, at::kByte);
     r.codes.copy_(codes.scalar_type() == at::kByte ? codes : codes.view(at::kByte));
   }
-  if (!usable(r.scales, r.lds, 16)) {
+  if (!usable(r.scales, r.lds, 16, 16)) {
     r.lds = round_up(rows, 16);
-    r.scales = at::empty_strided({blocks, rows}, {r.lds, 1}, scales.options());
+    r.scales = padded(blocks, rows, r.lds, scales, at::kByte);
     r.scales.copy_(scales);
   }
   return r;

@@ -793,3 +793,27 @@ def test_act8_weight_grad_repeats_its_bits(muon):
     mag = torch.mm(dy.double().abs().t(), muon.act8_restore(*kept, dtype=FP).double().abs())
     near_on_gpu("weight grad 9000x1500x2500", want, ref, U[FP] * ref.abs() + (9000 / 16 + 16) * 2.0 ** -23 * mag)
     assert muon.default_handle().check() == 0
+
+
+# ------------------------------------------------ storage of codes and scales
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (17, 130), (33, 1001)])
+def test_act8_storage_holds_whole_groups(muon, rows, cols):
+    """What the kernels load lies inside the tensors' storage; codes and scales on storage that ends with their last
+    element are taken too."""
+    x, dy = rand(160, rows, cols, dtype=BF), rand(161, rows, 24, dtype=BF)
+    codes, scales = muon.act8_store(x)
+    for t, group in ((codes, 8), (scales, 16)):
+        end = (t.shape[0] - 1) * t.stride(0) + -(-t.shape[1] // group) * group
+        assert t.storage_offset() + end <= t.untyped_storage().nbytes()
+    want = muon.act8_restore(codes, scales), muon.act8_weight_grad(dy, codes, scales)
+
+    def tight(t):
+        ld = t.stride(0)
+        flat = torch.empty((t.shape[0] - 1) * ld + t.shape[1], dtype=torch.uint8, device="cuda")
+        out = flat.as_strided(t.shape, (ld, 1))
+        out.copy_(t.view(torch.uint8))
+        return out.view(t.dtype)
+    tc, ts = tight(codes), tight(scales)
+    assert tc.untyped_storage().nbytes() == (rows - 1) * codes.stride(0) + cols
+    assert torch.equal(muon.act8_restore(tc, ts), want[0])
+    assert torch.equal(muon.act8_weight_grad(dy, tc, ts), want[1])
