@@ -328,13 +328,14 @@ PyObject* attention_backward(Args a) {
     refuse("do and o must have q's shape and type");
   if (lse.scalar_type() != at::kFloat || lse.sizes() != LseShape(p).ref() || !lse.is_contiguous())
     refuse("lse must be the contiguous float32 tensor that attention returned");
+  // autograd hands over expanded gradients, and parts of larger ones that start anywhere
   at::Tensor dout = given;
+  bool copy = reinterpret_cast<uintptr_t>(dout.data_ptr()) % 16 != 0;
   if (!dout.is_contiguous()) {
-    // autograd hands over expanded gradients
-    bool copy = dout.stride(-1) != 1;
+    copy = copy || dout.stride(-1) != 1;
     for (int64_t i = 0; i + 1 < dout.dim(); ++i) copy = copy || dout.stride(i) == 0 || dout.stride(i) % 8 != 0;
-    if (copy) dout = dout.contiguous();
   }
+  if (copy) dout = dout.clone(at::MemoryFormat::Contiguous);
   at::Tensor dq = empty(q.sizes(), q, q.scalar_type()), dk = empty(k.sizes(), k, k.scalar_type()),
              dv = empty(v.sizes(), v, v.scalar_type());
   p.o = o.data_ptr();

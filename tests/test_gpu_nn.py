@@ -131,3 +131,16 @@ def test_attention_offsets_are_kept_like_the_other_inputs(nn):
     o.backward(g)
     for a, b in zip(want, kept):
         assert torch.equal(a.grad, b.grad)
+
+
+def test_attention_gradient_that_starts_anywhere(nn):
+    """The gradient of one part of a concatenation is a view into the whole's, at an odd offset."""
+    torch.manual_seed(5)
+    base = [torch.randn(1, 50, 2, 64, device="cuda").to(BF) for _ in range(3)]
+    g = torch.randn(3 + 50 * 2 * 64, device="cuda").to(BF)
+    mine, want = [leaf(t) for t in base], [leaf(t) for t in base]
+    odd = leaf(torch.zeros(3, device="cuda", dtype=BF))
+    torch.cat([odd, nn.attention(*mine, causal=True).flatten()]).backward(g)
+    nn.attention(*want, causal=True).backward(g[3:].clone().view(1, 50, 2, 64))
+    for a, b in zip(mine, want):
+        assert torch.equal(a.grad, b.grad)
