@@ -33,6 +33,9 @@
  *     anything is enqueued.
  *   - A handle owns its device workspace and a device error word.  Calls on
  *     one handle must be ordered (same stream, or externally synchronised).
+ *     Host threads may call at once: a call holds the handle until it has
+ *     queued its work.  muon_last_error's text is the calling thread's until
+ *     that thread asks again.
  *   - Errors that can only be seen on the device (a bounded wait that timed
  *     out, a non-finite gradient norm) are recorded in the error word and
  *     returned by muon_handle_check().
@@ -274,8 +277,8 @@ muon_status_t muon_noalloc_set_timeout_ns(uint64_t timeout_ns);
  *
  * Conventions, beyond those at the top of this file:
  *   - The last dimension is contiguous; the others have strides in elements.
- *   - Nothing is kept in the handle between calls: calls from one
- *     host thread may run on several streams at once.
+ *   - Nothing is kept in the handle between calls: calls may run on several
+ *     streams at once.
  *   - `workspace` is caller-owned device memory, 256-byte aligned, of at
  *     least the bytes that the matching *_workspace call reports (host only,
  *     from shapes alone; 0 bytes: NULL is fine).  It is scratch: free for

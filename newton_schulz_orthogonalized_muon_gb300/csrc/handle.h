@@ -2,6 +2,7 @@
 // selection, error reporting, and counted, optionally timed launches.
 #pragma once
 
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -11,6 +12,8 @@
 #include "muon.h"
 
 struct muon_handle_s {
+  // of everything below that a call reads or writes on the host (HandleLock)
+  std::recursive_mutex mutex;
   int device = 0;
   int num_sms = 0;
   size_t ws_limit = size_t(16) << 30;
@@ -81,6 +84,21 @@ struct DeviceGuard {
     int cur = -1;
     if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
   }
+};
+
+// Host threads share a handle (the torch calls' default one): each entry point
+// holds it for the length of its call.  Entry points call one another.
+class HandleLock {
+ public:
+  explicit HandleLock(muon_handle_t h) noexcept {
+    try {
+      lock_ = std::unique_lock<std::recursive_mutex>(h->mutex);
+    } catch (...) {          // the lock itself failed: as before there was one
+    }
+  }
+
+ private:
+  std::unique_lock<std::recursive_mutex> lock_;
 };
 
 inline muon_status_t fail(muon_handle_t h, muon_status_t st, const std::string& msg) {

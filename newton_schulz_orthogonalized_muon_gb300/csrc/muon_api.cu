@@ -1141,7 +1141,18 @@ const char* muon_status_string(muon_status_t s) {
   return "unknown status";
 }
 
-const char* muon_last_error(muon_handle_t h) { return h == nullptr ? "null handle" : h->last.c_str(); }
+const char* muon_last_error(muon_handle_t h) {
+  if (h == nullptr) return "null handle";
+  // the thread's own copy: another thread's next error replaces the handle's
+  thread_local std::string mine;
+  HandleLock lock(h);
+  try {
+    mine = h->last;
+  } catch (...) {
+    return "";
+  }
+  return mine.c_str();
+}
 
 int32_t muon_version(void) { return 10000; }
 
@@ -1226,12 +1237,14 @@ muon_status_t muon_handle_destroy(muon_handle_t h) {
 
 muon_status_t muon_handle_set_workspace_limit(muon_handle_t h, size_t bytes) {
   if (h == nullptr || bytes == 0) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   h->ws_limit = bytes;
   return MUON_OK;
 }
 
 muon_status_t muon_handle_set_timeout_ns(muon_handle_t h, uint64_t timeout_ns) {
   if (h == nullptr || timeout_ns == 0) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   h->timeout_ns = timeout_ns;
   return MUON_OK;
 }
@@ -1240,7 +1253,9 @@ muon_status_t muon_handle_check(muon_handle_t h, void* stream) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MUON_CUDA_TRY(cudaStreamSynchronize(s), "stream synchronise");
+  const cudaError_t synced = cudaStreamSynchronize(s);       // without the lock: others go on
+  HandleLock lock(h);
+  MUON_CUDA_TRY(synced, "stream synchronise");
   unsigned word = 0;
   MUON_CUDA_TRY(cudaMemcpy(&word, h->err, sizeof(unsigned), cudaMemcpyDeviceToHost), "error word read");
   MUON_CUDA_TRY(cudaMemset(h->err, 0, sizeof(unsigned)), "error word reset");
@@ -1252,6 +1267,7 @@ muon_status_t muon_handle_check(muon_handle_t h, void* stream) {
 muon_status_t muon_orthogonalize(muon_handle_t h, void* X, int32_t dtype, int64_t batch, int64_t m, int64_t n,
                                  int32_t steps, const float* coeffs, int32_t ns_method, void* stream) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   if (!valid_dtype(dtype)) return fail(h, MUON_ERR_INVALID_ARG, "dtype must be MUON_F32 or MUON_BF16");
   if (batch < 0 || m < 0 || n < 0 || m > kMaxDim || n > kMaxDim || batch > kMaxDim)
     return fail(h, MUON_ERR_INVALID_ARG, "negative or oversized shape");
@@ -1278,6 +1294,7 @@ muon_status_t muon_orthogonalize(muon_handle_t h, void* X, int32_t dtype, int64_
 muon_status_t muon_workspace_size(muon_handle_t h, const muon_param_t* params, int32_t n_params, int32_t ns_method,
                                   int32_t ns_steps, int32_t ns_dtype, uint64_t* bytes) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   if (bytes == nullptr) return fail(h, MUON_ERR_INVALID_ARG, "bytes is NULL");
   *bytes = 0;
   if (n_params < 0) return fail(h, MUON_ERR_INVALID_ARG, "n_params < 0");
@@ -1323,6 +1340,7 @@ muon_status_t muon_workspace_size(muon_handle_t h, const muon_param_t* params, i
 muon_status_t muon_step_ex(muon_handle_t h, const muon_param_t* params, int32_t n_params,
                            const muon_step_options_t* opts, void* stream) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   if (opts == nullptr) return fail(h, MUON_ERR_INVALID_ARG, "opts is NULL");
   const muon_step_options_t o = *opts;
   if (n_params < 0) return fail(h, MUON_ERR_INVALID_ARG, "n_params < 0");
@@ -1378,6 +1396,7 @@ muon_status_t adamw_step(muon_handle_t h, void* const* params, const void* const
                          const int32_t* grad_dtypes, int32_t n, int64_t step, float lr, float beta1, float beta2,
                          float eps, float wd, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   if (n < 0) return fail(h, MUON_ERR_INVALID_ARG, "n < 0");
   if (n == 0) return MUON_OK;
   if (params == nullptr || grads == nullptr || exp_avg == nullptr || exp_avg_sq == nullptr || numel == nullptr ||
@@ -1427,6 +1446,7 @@ muon_status_t adamw_step(muon_handle_t h, void* const* params, const void* const
 
 muon_status_t muon_handle_set_profiling(muon_handle_t h, int32_t enable) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   h->profiling = enable != 0;
   h->prof_used = 0;
   return MUON_OK;
@@ -1434,6 +1454,7 @@ muon_status_t muon_handle_set_profiling(muon_handle_t h, int32_t enable) {
 
 muon_status_t muon_handle_profile(muon_handle_t h, double* ms, int64_t* launches, int32_t n_classes) {
   if (h == nullptr || n_classes < 0 || n_classes > MUON_K_COUNT) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   DeviceGuard guard(h->device);
   for (int32_t c = 0; c < n_classes; ++c) {
     if (ms) ms[c] = 0.0;
@@ -1456,6 +1477,7 @@ muon_status_t muon_handle_profile(muon_handle_t h, double* ms, int64_t* launches
 muon_status_t muon_handle_profile_records(muon_handle_t h, int32_t* cls, int32_t* tag, float* ms, int32_t capacity,
                                           int32_t* count) {
   if (h == nullptr || capacity < 0 || count == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   DeviceGuard guard(h->device);
   *count = static_cast<int32_t>(h->prof_used);
   for (size_t i = 0; i < h->prof_used; ++i) {
@@ -1475,6 +1497,7 @@ muon_status_t muon_handle_profile_records(muon_handle_t h, int32_t* cls, int32_t
 
 muon_status_t muon_handle_launch_count(muon_handle_t h, uint64_t* count) {
   if (h == nullptr || count == nullptr) return MUON_ERR_INVALID_ARG;
+  HandleLock lock(h);
   *count = h->launches;
   return MUON_OK;
 }
@@ -1483,6 +1506,7 @@ muon_status_t muon_selftest_timeout(muon_handle_t h, uint64_t timeout_ns, void* 
   if (h == nullptr || timeout_ns == 0 || timeout_ns > 10000000000ull) return MUON_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  HandleLock lock(h);
   MUON_CUDA_TRY(launch_wait_selftest(timeout_ns, h->err, s), "selftest launch");
   return MUON_OK;
 }

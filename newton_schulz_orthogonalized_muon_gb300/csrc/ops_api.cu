@@ -20,7 +20,8 @@ uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
 bool op_dtype(int32_t t) { return t == MUON_F32 || t == MUON_BF16 || t == MUON_F16; }
 
 template <typename F>
-muon_status_t guarded(F&& f) noexcept {
+muon_status_t guarded(muon_handle_t h, F&& f) noexcept {
+  HandleLock lock(h);
   try {
     return f();
   } catch (...) {
@@ -197,7 +198,7 @@ muon_status_t muon_layer_norm_forward(muon_handle_t h, const void* x, int64_t ld
                                       const void* bias, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows,
                                       int64_t cols, int32_t dtype, int32_t wdtype, float eps, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_norm(h, rows, cols, dtype, wdtype);
     if (st != MUON_OK) return st;
     MUON_CHECK(std::isfinite(eps) && eps >= 0.f, "eps must be finite and not negative");
@@ -231,7 +232,7 @@ muon_status_t muon_layer_norm_forward(muon_handle_t h, const void* x, int64_t ld
 
 muon_status_t muon_layer_norm_workspace(muon_handle_t h, int64_t rows, int64_t cols, uint64_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_norm(h, rows, cols, MUON_F32, MUON_F32);
     if (st != MUON_OK) return st;
     *bytes = round256(static_cast<uint64_t>(norm_max_parts(rows, static_cast<int>(cols), h->num_sms)) * 2 * cols * 4);
@@ -245,7 +246,7 @@ muon_status_t muon_layer_norm_backward(muon_handle_t h, const void* dy, int64_t 
                                        int32_t dtype, int32_t wdtype, void* workspace, size_t workspace_bytes,
                                        void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     uint64_t need = 0;
     muon_status_t st = check_norm(h, rows, cols, dtype, wdtype);
     if (st == MUON_OK) st = muon_layer_norm_workspace(h, rows, cols, &need);
@@ -291,7 +292,7 @@ muon_status_t muon_attention_forward(muon_handle_t h, const muon_attention_t* a,
 
 muon_status_t muon_attention_forward_workspace(muon_handle_t h, const muon_attention_t* a, uint64_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_attention(h, a);
     if (st != MUON_OK) return st;
     const uint64_t part = attn_part_bytes(h, *a, false);
@@ -303,7 +304,7 @@ muon_status_t muon_attention_forward_workspace(muon_handle_t h, const muon_atten
 muon_status_t muon_attention_forward_ex(muon_handle_t h, const muon_attention_t* a, void* workspace,
                                         size_t workspace_bytes, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_attention(h, a);
     if (st != MUON_OK) return st;
     const uint64_t part = attn_part_bytes(h, *a, false);
@@ -339,7 +340,7 @@ muon_status_t muon_attention_forward_ex(muon_handle_t h, const muon_attention_t*
 
 muon_status_t muon_attention_workspace(muon_handle_t h, const muon_attention_t* a, uint64_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_attention(h, a);
     if (st != MUON_OK) return st;
     *bytes = attn_workspace(h, *a);
@@ -350,7 +351,7 @@ muon_status_t muon_attention_workspace(muon_handle_t h, const muon_attention_t* 
 muon_status_t muon_attention_backward(muon_handle_t h, const muon_attention_t* a, void* workspace,
                                       size_t workspace_bytes, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_attention(h, a);
     if (st != MUON_OK) return st;
     const bool packed = a->cu_seqlens_q != nullptr;
@@ -403,7 +404,7 @@ muon_status_t muon_act8_store(muon_handle_t h, const void* x, int64_t ldx, uint8
                               uint8_t* scales, int64_t lds, int64_t rows, int64_t cols, int32_t dtype,
                               void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
     const muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
     if (st != MUON_OK) return st;
@@ -422,7 +423,7 @@ muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t l
                                 int64_t lds, void* out, int64_t ldo, int64_t rows, int64_t cols, int32_t dtype,
                                 void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
     const muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
     if (st != MUON_OK) return st;
@@ -441,7 +442,7 @@ muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t l
 muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, const void* dy, int64_t lddy, int64_t rows,
                                               int64_t cols, int64_t out, uint64_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     MUON_CHECK(rows >= 0 && rows <= kMaxTokens && cols >= 0 && cols <= kMaxTokens && out >= 0 && out <= kMaxTokens,
                "negative or oversized shape");
     *bytes = cols == 0 || out == 0 ? 0 : wgrad_plan(h, dy, lddy, rows, cols, out).bytes();
@@ -454,7 +455,7 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
                                     int64_t lddw, int64_t rows, int64_t cols, int64_t out, int32_t odtype,
                                     void* workspace, size_t workspace_bytes, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  return guarded([&]() -> muon_status_t {
+  return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
     if (st != MUON_OK) return st;
     MUON_CHECK(out >= 0 && out <= kMaxTokens, "negative or oversized shape");

@@ -36,6 +36,20 @@ struct Refusal {
 // An exception that Python has already been told of.
 struct Raised {};
 
+// Other Python threads run while torch allocates and the call queues its work
+// (which waits when the launch queue is full).  Between the arguments and the
+// results nothing is Python's.
+class NoGil {
+ public:
+  NoGil() : state_(PyEval_SaveThread()) {}
+  ~NoGil() { PyEval_RestoreThread(state_); }
+  NoGil(const NoGil&) = delete;
+  NoGil& operator=(const NoGil&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // ---------------------------------------------------------------- arguments
 // The calls' first two arguments.
 struct Target {
@@ -116,7 +130,12 @@ at::Tensor empty(at::IntArrayRef sizes, const at::Tensor& like, at::ScalarType t
   return at::empty(sizes, like.options().dtype(type));
 }
 
-PyObject* results(at::Tensor a, at::Tensor b, at::Tensor c) {
+// The tensors, or the status where it is not MUON_OK.
+PyObject* result(muon_status_t st, at::Tensor a) {
+  return st != MUON_OK ? PyLong_FromLong(st) : THPVariable_Wrap(std::move(a));
+}
+PyObject* results(muon_status_t st, at::Tensor a, at::Tensor b, at::Tensor c) {
+  if (st != MUON_OK) return PyLong_FromLong(st);
   const int n = c.defined() ? 3 : 2;
   PyObject* t = PyTuple_New(n);
   if (t == nullptr) throw Raised{};
@@ -179,18 +198,24 @@ PyObject* layer_norm(Args a) {
   const at::Tensor& x = *a.tensor(t, "x");
   const at::Tensor *weight = a.tensor(t, "weight", true), *bias = a.tensor(t, "bias", true);
   const double eps = a.number();
-  const int type = code(x, "x");
-  const Rows xr = rows_of(x, "x");
-  const int64_t cols = x.size(-1);
-  const Affine w = affine(weight, "weight", x.scalar_type(), cols), b = affine(bias, "bias", x.scalar_type(), cols);
-  if (w.p != nullptr && b.p != nullptr && w.code != b.code) refuse("weight and bias must have one type");
-  const at::IntArrayRef sizes = x.sizes(), outer = sizes.slice(0, sizes.size() - 1);
-  at::Tensor y = empty(sizes, x, x.scalar_type()), mean = empty(outer, x, at::kFloat), rstd = empty(outer, x, at::kFloat);
-  const muon_status_t st = muon_layer_norm_forward(
-      t.h, xr.t.data_ptr(), xr.ld, w.p, b.p, y.data_ptr(), cols, mean.data_ptr<float>(), rstd.data_ptr<float>(),
-      xr.rows, cols, type, w.p == nullptr ? b.code : w.code, static_cast<float>(eps), t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return results(std::move(y), std::move(mean), std::move(rstd));
+  at::Tensor y, mean, rstd;
+  muon_status_t st;
+  {
+    NoGil free;
+    const int type = code(x, "x");
+    const Rows xr = rows_of(x, "x");
+    const int64_t cols = x.size(-1);
+    const Affine w = affine(weight, "weight", x.scalar_type(), cols), b = affine(bias, "bias", x.scalar_type(), cols);
+    if (w.p != nullptr && b.p != nullptr && w.code != b.code) refuse("weight and bias must have one type");
+    const at::IntArrayRef sizes = x.sizes(), outer = sizes.slice(0, sizes.size() - 1);
+    y = empty(sizes, x, x.scalar_type());
+    mean = empty(outer, x, at::kFloat);
+    rstd = empty(outer, x, at::kFloat);
+    st = muon_layer_norm_forward(
+        t.h, xr.t.data_ptr(), xr.ld, w.p, b.p, y.data_ptr(), cols, mean.data_ptr<float>(), rstd.data_ptr<float>(),
+        xr.rows, cols, type, w.p == nullptr ? b.code : w.code, static_cast<float>(eps), t.stream());
+  }
+  return results(st, std::move(y), std::move(mean), std::move(rstd));
 }
 
 PyObject* layer_norm_backward(Args a) {
@@ -198,25 +223,32 @@ PyObject* layer_norm_backward(Args a) {
   const at::Tensor &dy = *a.tensor(t, "dy"), &x = *a.tensor(t, "x"), &mean = *a.tensor(t, "mean"),
                    &rstd = *a.tensor(t, "rstd");
   const at::Tensor* weight = a.tensor(t, "weight", true);
-  const int type = code(x, "x");
-  if (dy.sizes() != x.sizes() || dy.scalar_type() != x.scalar_type()) refuse("dy must have x's shape and type");
-  const Rows xr = rows_of(x, "x"), gr = rows_of(dy, "dy");
-  const int64_t cols = x.size(-1);
-  const at::IntArrayRef sizes = x.sizes(), outer = sizes.slice(0, sizes.size() - 1);
-  for (const at::Tensor* s : {&mean, &rstd})
-    if (s->scalar_type() != at::kFloat || s->sizes() != outer || !s->is_contiguous())
-      refuse("mean and rstd must be contiguous float32 of x's shape without the last dimension");
-  const Affine w = affine(weight, "weight", x.scalar_type(), cols);
-  uint64_t need = 0;
-  muon_status_t st = muon_layer_norm_workspace(t.h, xr.rows, cols, &need);
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  at::Tensor ws = empty({static_cast<int64_t>(need)}, x, at::kByte);
-  at::Tensor dx = empty(sizes, x, x.scalar_type()), dw = empty({cols}, x, at::kFloat), db = empty({cols}, x, at::kFloat);
-  st = muon_layer_norm_backward(t.h, gr.t.data_ptr(), gr.ld, xr.t.data_ptr(), xr.ld, mean.data_ptr<float>(),
-                                rstd.data_ptr<float>(), w.p, dx.data_ptr(), cols, dw.data_ptr<float>(),
-                                db.data_ptr<float>(), xr.rows, cols, type, w.code, ws.data_ptr(), need, t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return results(std::move(dx), std::move(dw), std::move(db));
+  at::Tensor dx, dw, db;
+  muon_status_t st;
+  {
+    NoGil free;
+    const int type = code(x, "x");
+    if (dy.sizes() != x.sizes() || dy.scalar_type() != x.scalar_type()) refuse("dy must have x's shape and type");
+    const Rows xr = rows_of(x, "x"), gr = rows_of(dy, "dy");
+    const int64_t cols = x.size(-1);
+    const at::IntArrayRef sizes = x.sizes(), outer = sizes.slice(0, sizes.size() - 1);
+    for (const at::Tensor* s : {&mean, &rstd})
+      if (s->scalar_type() != at::kFloat || s->sizes() != outer || !s->is_contiguous())
+        refuse("mean and rstd must be contiguous float32 of x's shape without the last dimension");
+    const Affine w = affine(weight, "weight", x.scalar_type(), cols);
+    uint64_t need = 0;
+    st = muon_layer_norm_workspace(t.h, xr.rows, cols, &need);
+    if (st == MUON_OK) {
+      at::Tensor ws = empty({static_cast<int64_t>(need)}, x, at::kByte);
+      dx = empty(sizes, x, x.scalar_type());
+      dw = empty({cols}, x, at::kFloat);
+      db = empty({cols}, x, at::kFloat);
+      st = muon_layer_norm_backward(t.h, gr.t.data_ptr(), gr.ld, xr.t.data_ptr(), xr.ld, mean.data_ptr<float>(),
+                                    rstd.data_ptr<float>(), w.p, dx.data_ptr(), cols, dw.data_ptr<float>(),
+                                    db.data_ptr<float>(), xr.rows, cols, type, w.code, ws.data_ptr(), need, t.stream());
+    }
+  }
+  return results(st, std::move(dx), std::move(dw), std::move(db));
 }
 
 // ---------------------------------------------------------------- attention
@@ -303,18 +335,24 @@ PyObject* attention(Args a) {
   const Target t = a.target();
   const at::Tensor &q = *a.tensor(t, "q"), &k = *a.tensor(t, "k"), &v = *a.tensor(t, "v");
   muon_attention_t p = attention_args(t, a, q, k, v);
-  at::Tensor o = empty(q.sizes(), q, q.scalar_type()), lse = empty(LseShape(p).ref(), q, at::kFloat);
-  p.o = o.data_ptr();
-  p.lse = lse.data_ptr<float>();
-  set_strides(p.o_stride, o, "o", p.cu_seqlens_q != nullptr);
-  uint64_t need = 0;
-  muon_status_t st = muon_attention_forward_workspace(t.h, &p, &need);
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  at::Tensor ws;
-  if (need > 0) ws = empty({static_cast<int64_t>(need)}, q, at::kByte);
-  st = muon_attention_forward_ex(t.h, &p, need > 0 ? ws.data_ptr() : nullptr, need, t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return results(std::move(o), std::move(lse), at::Tensor());
+  at::Tensor o, lse;
+  muon_status_t st;
+  {
+    NoGil free;
+    o = empty(q.sizes(), q, q.scalar_type());
+    lse = empty(LseShape(p).ref(), q, at::kFloat);
+    p.o = o.data_ptr();
+    p.lse = lse.data_ptr<float>();
+    set_strides(p.o_stride, o, "o", p.cu_seqlens_q != nullptr);
+    uint64_t need = 0;
+    st = muon_attention_forward_workspace(t.h, &p, &need);
+    if (st == MUON_OK) {
+      at::Tensor ws;
+      if (need > 0) ws = empty({static_cast<int64_t>(need)}, q, at::kByte);
+      st = muon_attention_forward_ex(t.h, &p, need > 0 ? ws.data_ptr() : nullptr, need, t.stream());
+    }
+  }
+  return results(st, std::move(o), std::move(lse), at::Tensor());
 }
 
 PyObject* attention_backward(Args a) {
@@ -322,40 +360,46 @@ PyObject* attention_backward(Args a) {
   const at::Tensor &given = *a.tensor(t, "do"), &q = *a.tensor(t, "q"), &k = *a.tensor(t, "k"), &v = *a.tensor(t, "v"),
                    &o = *a.tensor(t, "o"), &lse = *a.tensor(t, "lse");
   muon_attention_t p = attention_args(t, a, q, k, v);
-  const bool packed = p.cu_seqlens_q != nullptr;
-  if (given.sizes() != q.sizes() || o.sizes() != q.sizes() || given.scalar_type() != q.scalar_type() ||
-      o.scalar_type() != q.scalar_type())
-    refuse("do and o must have q's shape and type");
-  if (lse.scalar_type() != at::kFloat || lse.sizes() != LseShape(p).ref() || !lse.is_contiguous())
-    refuse("lse must be the contiguous float32 tensor that attention returned");
-  // autograd hands over expanded gradients, and parts of larger ones that start anywhere
-  at::Tensor dout = given;
-  bool copy = reinterpret_cast<uintptr_t>(dout.data_ptr()) % 16 != 0;
-  if (!dout.is_contiguous()) {
-    copy = copy || dout.stride(-1) != 1;
-    for (int64_t i = 0; i + 1 < dout.dim(); ++i) copy = copy || dout.stride(i) == 0 || dout.stride(i) % 8 != 0;
+  at::Tensor dq, dk, dv;
+  muon_status_t st;
+  {
+    NoGil free;
+    const bool packed = p.cu_seqlens_q != nullptr;
+    if (given.sizes() != q.sizes() || o.sizes() != q.sizes() || given.scalar_type() != q.scalar_type() ||
+        o.scalar_type() != q.scalar_type())
+      refuse("do and o must have q's shape and type");
+    if (lse.scalar_type() != at::kFloat || lse.sizes() != LseShape(p).ref() || !lse.is_contiguous())
+      refuse("lse must be the contiguous float32 tensor that attention returned");
+    // autograd hands over expanded gradients, and parts of larger ones that start anywhere
+    at::Tensor dout = given;
+    bool copy = reinterpret_cast<uintptr_t>(dout.data_ptr()) % 16 != 0;
+    if (!dout.is_contiguous()) {
+      copy = copy || dout.stride(-1) != 1;
+      for (int64_t i = 0; i + 1 < dout.dim(); ++i) copy = copy || dout.stride(i) == 0 || dout.stride(i) % 8 != 0;
+    }
+    if (copy) dout = dout.clone(at::MemoryFormat::Contiguous);
+    dq = empty(q.sizes(), q, q.scalar_type());
+    dk = empty(k.sizes(), k, k.scalar_type());
+    dv = empty(v.sizes(), v, v.scalar_type());
+    p.o = o.data_ptr();
+    p.lse = lse.data_ptr<float>();
+    p.dout = dout.data_ptr();
+    p.dq = dq.data_ptr();
+    p.dk = dk.data_ptr();
+    p.dv = dv.data_ptr();
+    set_strides(p.o_stride, o, "o", packed);
+    set_strides(p.dout_stride, dout, "do", packed);
+    set_strides(p.dq_stride, dq, "dq", packed);
+    set_strides(p.dk_stride, dk, "dk", packed);
+    set_strides(p.dv_stride, dv, "dv", packed);
+    uint64_t need = 0;
+    st = muon_attention_workspace(t.h, &p, &need);
+    if (st == MUON_OK) {
+      at::Tensor ws = empty({static_cast<int64_t>(need)}, q, at::kByte);
+      st = muon_attention_backward(t.h, &p, ws.data_ptr(), need, t.stream());
+    }
   }
-  if (copy) dout = dout.clone(at::MemoryFormat::Contiguous);
-  at::Tensor dq = empty(q.sizes(), q, q.scalar_type()), dk = empty(k.sizes(), k, k.scalar_type()),
-             dv = empty(v.sizes(), v, v.scalar_type());
-  p.o = o.data_ptr();
-  p.lse = lse.data_ptr<float>();
-  p.dout = dout.data_ptr();
-  p.dq = dq.data_ptr();
-  p.dk = dk.data_ptr();
-  p.dv = dv.data_ptr();
-  set_strides(p.o_stride, o, "o", packed);
-  set_strides(p.dout_stride, dout, "do", packed);
-  set_strides(p.dq_stride, dq, "dq", packed);
-  set_strides(p.dk_stride, dk, "dk", packed);
-  set_strides(p.dv_stride, dv, "dv", packed);
-  uint64_t need = 0;
-  muon_status_t st = muon_attention_workspace(t.h, &p, &need);
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  at::Tensor ws = empty({static_cast<int64_t>(need)}, q, at::kByte);
-  st = muon_attention_backward(t.h, &p, ws.data_ptr(), need, t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return results(std::move(dq), std::move(dk), std::move(dv));
+  return results(st, std::move(dq), std::move(dk), std::move(dv));
 }
 
 // --------------------------------------------------- activations in 8 bits
@@ -372,17 +416,21 @@ at::Tensor padded(int64_t rows, int64_t cols, int64_t ld, const at::Tensor& like
 PyObject* act8_store(Args a) {
   const Target t = a.target();
   const at::Tensor& x = *a.tensor(t, "x");
-  const int type = code(x, "x");
-  if (x.dim() != 2) refuse("x must be 2-D");
-  const Rows xr = rows_of(x, "x");
-  const int64_t rows = x.size(0), cols = x.size(1), blocks = round_up(cols, kBlock) / kBlock;
-  const int64_t ldc = blocks * kBlock, lds = round_up(rows, 16);
-  at::Tensor codes = padded(rows, cols, ldc, x, at::kFloat8_e4m3fn), scales = padded(blocks, rows, lds, x, at::kByte);
-  const muon_status_t st =
-      muon_act8_store(t.h, xr.t.data_ptr(), xr.ld, static_cast<uint8_t*>(codes.data_ptr()), ldc,
-                      static_cast<uint8_t*>(scales.data_ptr()), lds, rows, cols, type, t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return results(std::move(codes), std::move(scales), at::Tensor());
+  at::Tensor codes, scales;
+  muon_status_t st;
+  {
+    NoGil free;
+    const int type = code(x, "x");
+    if (x.dim() != 2) refuse("x must be 2-D");
+    const Rows xr = rows_of(x, "x");
+    const int64_t rows = x.size(0), cols = x.size(1), blocks = round_up(cols, kBlock) / kBlock;
+    const int64_t ldc = blocks * kBlock, lds = round_up(rows, 16);
+    codes = padded(rows, cols, ldc, x, at::kFloat8_e4m3fn);
+    scales = padded(blocks, rows, lds, x, at::kByte);
+    st = muon_act8_store(t.h, xr.t.data_ptr(), xr.ld, static_cast<uint8_t*>(codes.data_ptr()), ldc,
+                        static_cast<uint8_t*>(scales.data_ptr()), lds, rows, cols, type, t.stream());
+  }
+  return results(st, std::move(codes), std::move(scales), at::Tensor());
 }
 
 // codes and scales as the kernels read them (padded row strides), copied if
@@ -425,12 +473,16 @@ PyObject* act8_restore(Args a) {
   const at::Tensor &codes = *a.tensor(t, "codes"), &scales = *a.tensor(t, "scales");
   const std::optional<at::ScalarType> type = a.dtype();
   if (!type || code_of(*type) < 0) refuse("dtype must be float32, bfloat16 or float16");
-  const Act8 c = act8_of(codes, scales);
-  at::Tensor out = empty({c.rows, c.cols}, codes, *type);
-  const muon_status_t st = muon_act8_restore(t.h, c.code(), c.ldc, c.scale(), c.lds, out.data_ptr(), c.cols, c.rows,
-                                             c.cols, code_of(*type), t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return THPVariable_Wrap(std::move(out));
+  at::Tensor out;
+  muon_status_t st;
+  {
+    NoGil free;
+    const Act8 c = act8_of(codes, scales);
+    out = empty({c.rows, c.cols}, codes, *type);
+    st = muon_act8_restore(t.h, c.code(), c.ldc, c.scale(), c.lds, out.data_ptr(), c.cols, c.rows,
+                                               c.cols, code_of(*type), t.stream());
+  }
+  return result(st, std::move(out));
 }
 
 PyObject* act8_weight_grad(Args a) {
@@ -438,38 +490,43 @@ PyObject* act8_weight_grad(Args a) {
   const at::Tensor &dy = *a.tensor(t, "dy"), &codes = *a.tensor(t, "codes"), &scales = *a.tensor(t, "scales");
   const at::Tensor *add = a.tensor(t, "add", true), *given = a.tensor(t, "out", true);
   std::optional<at::ScalarType> type = a.dtype();
-  if (dy.scalar_type() != at::kBFloat16) refuse("dy must be bfloat16");
-  if (dy.dim() != 2 || codes.dim() != 2 || dy.size(0) != codes.size(0))
-    refuse("dy must be [rows, out] and codes [rows, cols]");
-  const int64_t outs = dy.size(1), cols = codes.size(1);
-  int64_t ld[2] = {cols, cols};
-  const at::Tensor* both[2] = {add, given};
-  for (int i = 0; i < 2; ++i) {
-    const at::Tensor* m = both[i];
-    const std::string what = i == 0 ? "add" : "out";
-    if (m == nullptr) continue;
-    if (m->dim() != 2 || m->size(0) != outs || m->size(1) != cols)
-      refuse(what + " must have shape (" + std::to_string(outs) + ", " + std::to_string(cols) + ")");
-    if (type && m->scalar_type() != *type) refuse(what + " does not have the result's type");
-    type = m->scalar_type();
-    if ((m->stride(1) != 1 && cols > 1) || (m->stride(0) < cols && outs > 1)) refuse(what + " must have contiguous rows");
-    ld[i] = std::max(m->stride(0), cols);
+  at::Tensor out;
+  muon_status_t st;
+  {
+    NoGil free;
+    if (dy.scalar_type() != at::kBFloat16) refuse("dy must be bfloat16");
+    if (dy.dim() != 2 || codes.dim() != 2 || dy.size(0) != codes.size(0))
+      refuse("dy must be [rows, out] and codes [rows, cols]");
+    const int64_t outs = dy.size(1), cols = codes.size(1);
+    int64_t ld[2] = {cols, cols};
+    const at::Tensor* both[2] = {add, given};
+    for (int i = 0; i < 2; ++i) {
+      const at::Tensor* m = both[i];
+      const std::string what = i == 0 ? "add" : "out";
+      if (m == nullptr) continue;
+      if (m->dim() != 2 || m->size(0) != outs || m->size(1) != cols)
+        refuse(what + " must have shape (" + std::to_string(outs) + ", " + std::to_string(cols) + ")");
+      if (type && m->scalar_type() != *type) refuse(what + " does not have the result's type");
+      type = m->scalar_type();
+      if ((m->stride(1) != 1 && cols > 1) || (m->stride(0) < cols && outs > 1)) refuse(what + " must have contiguous rows");
+      ld[i] = std::max(m->stride(0), cols);
+    }
+    if (!type) type = at::kFloat;
+    if (*type != at::kFloat && *type != at::kBFloat16) refuse("dtype must be float32 or bfloat16");
+    const Rows g = rows_of(dy, "dy");
+    const Act8 c = act8_of(codes, scales);
+    out = given != nullptr ? *given : empty({outs, cols}, dy, *type);
+    uint64_t need = 0;
+    st = muon_act8_weight_grad_workspace(t.h, g.t.data_ptr(), g.ld, c.rows, cols, outs, &need);
+    if (st == MUON_OK) {
+      at::Tensor ws;
+      if (need > 0) ws = empty({static_cast<int64_t>(need)}, dy, at::kByte);
+      st = muon_act8_weight_grad(t.h, g.t.data_ptr(), g.ld, c.code(), c.ldc, c.scale(), c.lds,
+                                 add != nullptr ? add->data_ptr() : nullptr, ld[0], out.data_ptr(), ld[1], c.rows, cols, outs,
+                                 code_of(*type), need > 0 ? ws.data_ptr() : nullptr, need, t.stream());
+    }
   }
-  if (!type) type = at::kFloat;
-  if (*type != at::kFloat && *type != at::kBFloat16) refuse("dtype must be float32 or bfloat16");
-  const Rows g = rows_of(dy, "dy");
-  const Act8 c = act8_of(codes, scales);
-  at::Tensor out = given != nullptr ? *given : empty({outs, cols}, dy, *type);
-  uint64_t need = 0;
-  muon_status_t st = muon_act8_weight_grad_workspace(t.h, g.t.data_ptr(), g.ld, c.rows, cols, outs, &need);
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  at::Tensor ws;
-  if (need > 0) ws = empty({static_cast<int64_t>(need)}, dy, at::kByte);
-  st = muon_act8_weight_grad(t.h, g.t.data_ptr(), g.ld, c.code(), c.ldc, c.scale(), c.lds,
-                             add != nullptr ? add->data_ptr() : nullptr, ld[0], out.data_ptr(), ld[1], c.rows, cols, outs,
-                             code_of(*type), need > 0 ? ws.data_ptr() : nullptr, need, t.stream());
-  if (st != MUON_OK) return PyLong_FromLong(st);
-  return THPVariable_Wrap(std::move(out));
+  return result(st, std::move(out));
 }
 
 // ------------------------------------------------------------------- module

@@ -817,3 +817,74 @@ def test_act8_storage_holds_whole_groups(muon, rows, cols):
     assert tc.untyped_storage().nbytes() == (rows - 1) * codes.stride(0) + cols
     assert torch.equal(muon.act8_restore(tc, ts), want[0])
     assert torch.equal(muon.act8_weight_grad(dy, tc, ts), want[1])
+
+
+def test_other_threads_run_while_the_launch_queue_is_full(muon):
+    """Calls that wait for room in the launch queue, behind a kernel of about a second, leave Python to other threads."""
+    import threading
+    import time
+    x = rand(155, 4, 64, dtype=BF)
+    kept = muon.act8_store(x)
+    muon.layer_norm(x), muon.act8_restore(*kept)
+    torch.cuda.synchronize()
+    stamps, done = [], threading.Event()
+
+    def work():
+        torch.cuda._sleep(1_500_000_000)             # device cycles
+        t0 = time.monotonic()
+        for _ in range(1500):
+            muon.layer_norm(x)
+            muon.act8_restore(*kept)
+        stamps.append(time.monotonic() - t0)
+        done.set()
+    t = threading.Thread(target=work)
+    t.start()
+    last, gap = time.monotonic(), 0.0
+    while not done.is_set():
+        time.sleep(0.001)
+        now = time.monotonic()
+        gap, last = max(gap, now - last), now
+    t.join()
+    torch.cuda.synchronize()
+    assert stamps[0] > 0.3                           # the calls did wait
+    assert gap < stamps[0] / 3, (gap, stamps[0])
+
+
+def test_threads_share_a_handle(muon):
+    """Threads in the library at once: every launch is counted, every error is told, every result is right."""
+    import threading
+    h, n = muon.default_handle(), 2000
+    x = rand(156, 8, 64, dtype=BF)
+    want = muon.layer_norm(x)[0]
+    ps = [[torch.ones(64, device="cuda") for _ in range(4)] for _ in range(2)]
+    wrong = []
+
+    def norm():
+        for _ in range(n):
+            if not torch.equal(muon.layer_norm(x)[0], want):
+                wrong.append("layer norm")
+
+    def adam(p, times=n):
+        for i in range(times):
+            muon.adamw_step([p[0]], [p[1]], [p[2]], [p[3]], step=i + 1, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, wd=0.0)
+
+    def refused():
+        for _ in range(n):
+            try:
+                muon.attention(*[x.view(1, 8, 1, 64)] * 3, scale=-1.0)
+                wrong.append("not refused")
+            except muon.MuonError as e:
+                if "scale" not in str(e):
+                    wrong.append(str(e))
+    counts = [h.launch_count()]
+    for call in (lambda: muon.layer_norm(x), lambda: adam(ps[0], 1)):
+        call()
+        counts.append(h.launch_count())
+    threads = [threading.Thread(target=f, args=a) for f, a in ((norm, ()), (adam, (ps[0],)), (adam, (ps[1],)), (refused, ()))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
+    assert h.launch_count() - counts[2] == n * (counts[1] - counts[0]) + 2 * n * (counts[2] - counts[1])
+    assert h.check() == 0
