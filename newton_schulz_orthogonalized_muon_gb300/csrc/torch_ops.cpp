@@ -516,6 +516,7 @@ PyObject* act8_weight_grad(Args a) {
     const Rows g = rows_of(dy, "dy");
     const Act8 c = act8_of(codes, scales);
     out = given != nullptr ? *given : empty({outs, cols}, dy, *type);
+    if (given != nullptr) out.unsafeGetTensorImpl()->bump_version();     // autograd sees the write
     uint64_t need = 0;
     st = muon_act8_weight_grad_workspace(t.h, g.t.data_ptr(), g.ld, c.rows, cols, outs, &need);
     if (st == MUON_OK) {

@@ -144,3 +144,16 @@ def test_attention_gradient_that_starts_anywhere(nn):
     nn.attention(*want, causal=True).backward(g[3:].clone().view(1, 50, 2, 64))
     for a, b in zip(mine, want):
         assert torch.equal(a.grad, b.grad)
+
+
+def test_a_written_out_is_seen_by_autograd(nn):
+    import newton_schulz_orthogonalized_muon_gb300 as muon
+    x, dy = torch.randn(40, 64, device="cuda").to(BF), torch.randn(40, 32, device="cuda").to(BF)
+    kept, out = muon.act8_store(x), torch.ones(32, 64, device="cuda")
+    w = leaf(torch.ones(32, 64, device="cuda"))
+    loss = (w * out).sum()                           # keeps out for w's gradient
+    version = out._version
+    muon.act8_weight_grad(dy, *kept, out=out)
+    assert out._version > version
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
