@@ -85,25 +85,30 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_
 class _Linear8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight):
-        rows = x.reshape(-1, x.shape[-1])
-        codes, scales = ops.act8_store(rows)
-        ctx.save_for_backward(codes, scales, weight)
+        # the input is kept for the weight's gradient, the weight for the input's
+        codes = scales = None
+        if ctx.needs_input_grad[1]:
+            codes, scales = ops.act8_store(x.reshape(-1, x.shape[-1]))
+        ctx.save_for_backward(codes, scales, weight if ctx.needs_input_grad[0] else None)
+        ctx.dtype = weight.dtype
         return x @ weight.t()
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         codes, scales, weight = ctx.saved_tensors
-        dw = ops.act8_weight_grad(dy.reshape(-1, dy.shape[-1]), codes, scales, dtype=weight.dtype) \
-            if ctx.needs_input_grad[1] else None
-        return dy @ weight, dw
+        dw = None if codes is None else \
+            ops.act8_weight_grad(dy.reshape(-1, dy.shape[-1]), codes, scales, dtype=ctx.dtype)
+        return None if weight is None else dy @ weight, dw
 
 
 def linear8(x, weight):
     """x weight^T, both bf16; the input is kept in 8 bits for the weight's
-    gradient (see ops.act8_store for the format)."""
+    gradient (see ops.act8_store for the format), if there will be one."""
     if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
         raise ValueError("linear8 takes bfloat16 inputs and weights")
+    if not torch.is_grad_enabled():
+        return x @ weight.t()
     return _Linear8.apply(x, weight)
 
 

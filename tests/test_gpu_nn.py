@@ -157,3 +157,24 @@ def test_a_written_out_is_seen_by_autograd(nn):
     assert out._version > version
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_linear8_does_no_work_for_gradients_that_nobody_wants(nn, monkeypatch):
+    torch.manual_seed(6)
+    x, w = torch.randn(30, 200, device="cuda").to(BF), torch.randn(72, 200, device="cuda").to(BF)
+    g = torch.randn(30, 72, device="cuda").to(BF)
+    both = leaf(x), leaf(w)
+    nn.linear8(*both).backward(g)
+    stored = []
+    store = nn.ops.act8_store
+    monkeypatch.setattr(nn.ops, "act8_store", lambda t: stored.append(t.shape) or store(t))
+    with torch.no_grad():
+        assert torch.equal(nn.linear8(*both), x @ w.t())
+    frozen = leaf(x)                                 # a frozen weight: nothing is stored
+    nn.linear8(frozen, w).backward(g)
+    assert torch.equal(frozen.grad, both[0].grad) and stored == []
+    first = leaf(w)                                  # a first layer: no product with the weight
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as prof:
+        nn.linear8(x, first).backward(g)
+    assert sum(e.name == "aten::mm" for e in prof.events()) == 1
+    assert torch.equal(first.grad, both[1].grad) and stored == [torch.Size([30, 200])]
