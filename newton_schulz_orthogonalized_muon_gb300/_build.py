@@ -4,8 +4,8 @@ extension module that calls it on torch tensors.
 The translation units compile in parallel; the shared library links the CUDA
 runtime statically and resolves the tensor-map encoder from the driver at run
 time, so it needs no -lcuda.  The module (host code) links that library and
-torch's; its object's name carries torch's version, so that another torch
-gets another build.
+torch's; its object's name carries torch's version and the link command is
+kept, so that another torch gets another build.
 """
 from __future__ import annotations
 
@@ -62,8 +62,8 @@ def _stale(target: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every translation unit (in parallel), link the library and the
-    extension module.  Returns the path of the shared library."""
+    """Compile every translation unit (in parallel), link the library and then
+    the extension module.  Returns the path of the shared library."""
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "muon.h")]
@@ -75,26 +75,50 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs.append(o)
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
-    mod_obj, mod_compile, mod_link = _module_commands(nvcc)
-    if force or _stale(mod_obj, [MODULE_SOURCE, os.path.join(INCLUDE, "muon.h")]):
-        jobs.append(mod_compile)
+    lib_jobs = len(jobs)
+    mod_error = None
+    try:
+        mod_obj, mod_compile, mod_link = _module_commands(nvcc)
+        if force or _stale(mod_obj, [MODULE_SOURCE, os.path.join(INCLUDE, "muon.h")]):
+            jobs.append(mod_compile)
+    except ImportError as e:                     # no torch: the library is built all the same
+        mod_error = e
 
     def run(cmd):
+        """None, or the command's failure."""
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
+        try:
+            r = subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:
+            return RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{e}")
+        if verbose and r.returncode == 0 and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
+        return RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}") if r.returncode else None
 
+    def need(error):
+        if error is not None:
+            raise error
+
+    errors = []
     if jobs:
         with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB_PATH, objs):
-        run([nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-Xlinker", f"-soname={LIB_NAME}", "-o", LIB_PATH])
-    if force or _stale(MODULE_PATH, [mod_obj, LIB_PATH]):
-        run(mod_link)
+            errors = list(ex.map(run, jobs))
+    for e in errors[:lib_jobs]:
+        need(e)
+    if force or lib_jobs or _stale(LIB_PATH, objs):
+        need(run([nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-Xlinker", f"-soname={LIB_NAME}", "-o", LIB_PATH]))
+    # then the module: the library does not depend on torch or on its headers
+    need(mod_error)
+    for e in errors[lib_jobs:]:
+        need(e)
+    # what the module was linked from: an older object of another torch's is not newer than it
+    stamp = os.path.join(BUILD_DIR, "torch_ops.link")
+    last = open(stamp).read() if os.path.exists(stamp) else None
+    if force or last != " ".join(mod_link) or _stale(MODULE_PATH, [mod_obj, LIB_PATH]):
+        need(run(mod_link))
+        with open(stamp, "w") as f:
+            f.write(" ".join(mod_link))
     return LIB_PATH
 
 

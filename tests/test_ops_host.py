@@ -122,3 +122,46 @@ def test_extension_module_loads_and_checks_its_arguments(lib):
             call()
     with pytest.raises(TypeError):
         native.act8_store("handle", 0, x)
+
+
+@pytest.fixture
+def fake_build(tmp_path, monkeypatch):
+    """build() into a folder of its own, with commands that only touch their outputs."""
+    from newton_schulz_orthogonalized_muon_gb300 import _build
+    ran, broken = [], set()
+    monkeypatch.setattr(_build, "BUILD_DIR", str(tmp_path / "build"))
+    monkeypatch.setattr(_build, "LIB_PATH", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(_build, "MODULE_PATH", str(tmp_path / "module.so"))
+    monkeypatch.setattr(_build, "nvcc_path", lambda: "nvcc")
+
+    def run(cmd, **kw):
+        out = cmd[cmd.index("-o") + 1]
+        if any(b in " ".join(cmd) for b in broken):
+            return subprocess.CompletedProcess(cmd, 1, "", "broken")
+        with open(out, "w") as f:
+            f.write(" ".join(cmd))
+        ran.append(os.path.basename(out))
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    return _build, ran, broken, tmp_path
+
+
+def test_module_is_linked_again_for_another_torch(fake_build, monkeypatch):
+    build, ran, _, tmp = fake_build
+    for version in ("1.0", "2.0", "1.0", "1.0"):
+        monkeypatch.setattr(torch, "__version__", version)
+        ran.clear()
+        build.build()
+        assert f"torch_ops-{version}.o" in (tmp / "module.so").read_text()
+    assert ran == []                                 # nothing changed: nothing built
+
+
+def test_library_is_built_where_the_module_is_not(fake_build):
+    build, ran, broken, tmp = fake_build
+    broken.add("torch_ops.cpp")
+    with pytest.raises(RuntimeError, match="torch_ops.cpp"):
+        build.build()
+    assert (tmp / "lib.so").exists() and not (tmp / "module.so").exists()
+    broken.clear()
+    build.build()
+    assert (tmp / "module.so").exists()
