@@ -756,7 +756,7 @@ cudaError_t launch_items(const AttnParams& p, const CUtensorMap* m, unsigned gri
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), Smem<DP>::BYTES, done);
   if (e != cudaSuccess) return e;
   // its prologue overlaps the statistics kernel (the wait for them is in the roles); without that one, no overlap
-  e = launch_k(p.sq > 0, kern, dim3(grid), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0], m[1], m[2], m[3], p,
+  e = launch_k(p.sq > 0 && pdl_level() >= 1, kern, dim3(grid), dim3(Shape<DP>::THREADS), Smem<DP>::BYTES, s, m[0], m[1], m[2], m[3], p,
                static_cast<uint32_t>(nk), static_cast<uint32_t>(total), static_cast<int>(ktiles), static_cast<int>(qtiles));
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -775,7 +775,7 @@ cudaError_t launch_norm_bwd(const NormParams& p, int parts, cudaStream_t s) { re
 
 cudaError_t launch_norm_join(const NormParams& p, int parts, float* dw, float* db, cudaStream_t s) {
   // overlaps its launch with the pass that forms the partial rows
-  const cudaError_t e = launch_k(true, norm_join_kernel, dim3((2 * p.cols + 31) / 32), dim3(32 * JOIN), 0, s,
+  const cudaError_t e = launch_k(pdl_level() >= 1, norm_join_kernel, dim3((2 * p.cols + 31) / 32), dim3(32 * JOIN), 0, s,
                                  static_cast<const float*>(p.part), parts, 2 * p.cols, dw, db);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -608,14 +608,14 @@ cudaError_t launch_act8_wgrad(const WgradParams& q, const CUtensorMap* maps, boo
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(act8_wgrad_kernel), SMEM, done);
   if (e != cudaSuccess) return e;
-  const cudaError_t l = launch_k(padded, act8_wgrad_kernel, dim3(2 * static_cast<unsigned>(items < pairs ? items : pairs)),
+  const cudaError_t l = launch_k(padded && pdl_level() >= 1, act8_wgrad_kernel, dim3(2 * static_cast<unsigned>(items < pairs ? items : pairs)),
                                  dim3(THREADS), SMEM, s, maps[0], maps[1], p);
   return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 cudaError_t launch_act8_wgrad_join(const WgradParams& p, int sms, cudaStream_t s) {
   const long long want = (static_cast<long long>(p.out) * p.cols + 255) / 256;
-  const cudaError_t e = launch_k(true, act8_wgrad_join_kernel, dim3(static_cast<unsigned>(want < sms * 8LL ? want : sms * 8LL)),
+  const cudaError_t e = launch_k(pdl_level() >= 1, act8_wgrad_join_kernel, dim3(static_cast<unsigned>(want < sms * 8LL ? want : sms * 8LL)),
                                  dim3(256), 0, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -15,6 +15,9 @@ Tolerances, element by element.  u is the unit roundoff of the storage type:
 """
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -27,6 +30,7 @@ pytestmark = pytest.mark.gpu
 
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -888,3 +892,48 @@ def test_threads_share_a_handle(muon):
     assert not wrong, wrong[:3]
     assert h.launch_count() - counts[2] == n * (counts[1] - counts[0]) + 2 * n * (counts[2] - counts[1])
     assert h.check() == 0
+
+
+EDGES = """
+import ctypes, sys
+import torch
+import newton_schulz_orthogonalized_muon_gb300 as muon
+g = torch.Generator().manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+x, dy, q = r(2000, 256), r(2000, 250), r(1, 200, 2, 64)
+y, mean, rstd = muon.layer_norm(x)
+kept = muon.act8_store(x)
+o, lse = muon.attention(q, q, q, causal=True)
+calls = [lambda: muon.layer_norm_backward(x, x, mean, rstd), lambda: (muon.act8_weight_grad(dy, *kept),),
+         lambda: muon.attention_backward(q, q, q, q, o, lse, causal=True)]
+rt = ctypes.CDLL("libcudart.so.13")
+out = []
+for call in calls:
+    out += [t.cpu() for t in call()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    raw, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t()
+    assert rt.cudaGraphGetEdges(raw, None, None, None, ctypes.byref(n)) == 0
+    a, b, data = (ctypes.c_void_p * n.value)(), (ctypes.c_void_p * n.value)(), (ctypes.c_ubyte * (8 * n.value))()
+    assert rt.cudaGraphGetEdges(raw, a, b, data, ctypes.byref(n)) == 0
+    print(n.value, sum(data[8 * i + 2] for i in range(n.value)))       # the edge's type: 1 programmatic
+assert muon.default_handle().check() == 0
+torch.save(out, sys.argv[1])
+"""
+
+
+def test_dependent_launches_can_be_switched_off(muon, tmp_path):
+    """MUON_PDL=0: every launch of the operators waits for the one before it, and the bits are the same."""
+    got = {}
+    for level in ("0", "1"):
+        r = subprocess.run([sys.executable, "-c", EDGES, str(tmp_path / level)], cwd=ROOT, capture_output=True, text=True,
+                           env={**os.environ, "MUON_PDL": level})
+        assert r.returncode == 0, r.stdout + r.stderr
+        got[level] = [tuple(map(int, line.split())) for line in r.stdout.split("\n") if line]
+    assert [n for n, _ in got["0"]] == [n for n, _ in got["1"]] and all(n > 0 for n, _ in got["0"])
+    assert all(p == 0 for _, p in got["0"]), got
+    assert all(p > 0 for _, p in got["1"]), got
+    for a, b in zip(torch.load(tmp_path / "0"), torch.load(tmp_path / "1")):
+        assert torch.equal(a, b)
