@@ -937,3 +937,41 @@ def test_dependent_launches_can_be_switched_off(muon, tmp_path):
     assert all(p > 0 for _, p in got["1"]), got
     for a, b in zip(torch.load(tmp_path / "0"), torch.load(tmp_path / "1")):
         assert torch.equal(a, b)
+
+
+# --------------------------- many rows, steps and items of a CTA (or CTA pair)
+# Row kernels with several rows a group, batch kernels whose ring goes round, uneven last batches.
+@pytest.mark.parametrize("rows,cols,pad,dtype", [
+    (40001, 33, 0, BF), (4099, 1023, 6, FP), (9001, 1023, 0, HF), (60007, 256, 0, BF), (60007, 256, 0, FP), (30011, 768, 8, HF),
+    (8003, 4096, 0, BF), (4001, 4096, 0, FP), (1501, 8192, 0, FP), (3001, 8192, 0, BF), (901, 9001, 0, BF),
+    (1201, 16384, 0, BF), (701, 16384, 0, FP)])
+def test_layer_norm_over_many_rows(muon, rows, cols, pad, dtype):
+    """The formulas and tolerances of test_layer_norm, the reference in fp64 on the GPU."""
+    x = (rand(170, rows, cols + pad) * 3 + 5).to(dtype)[:, :cols]
+    dy = rand(171, rows, cols + pad, dtype=dtype)[:, :cols]
+    w, b = 1 + rand(172, cols) * 0.3, rand(173, cols)
+    y, mean, rstd = muon.layer_norm(x, w, b, eps=1e-5)
+    dx, dw, db = muon.layer_norm_backward(dy, x, mean, rstd, w)
+    assert muon.default_handle().check() == 0
+    tag, e = f"layer norm {rows}x{cols} {dtype}", 2.0 ** -19
+    xd, dyd, wd, bd = x.double(), dy.double(), w.double(), b.double()
+    mr = xd.mean(1)
+    rr = (xd - mr[:, None]).square().mean(1).add(1e-5).rsqrt()
+    top, size = e * xd.abs().amax(1) * rr, e * xd.abs().mean(1)
+    off = size * rr
+    near_on_gpu(tag + " mean", mean, mr, size)
+    near_on_gpu(tag + " rstd", rstd, rr, rr * (e + off * off + top))
+    z = (xd - mr[:, None]) * rr[:, None]
+    yr = z * wd + bd
+    inner = off[:, None] + (e + top[:, None]) * z.abs()
+    near_on_gpu(tag + " y", y, yr, U[dtype] * yr.abs() + inner * wd.abs() + e * (z.abs() * wd.abs() + bd.abs()))
+    md, rd = mean.double()[:, None], rstd.double()[:, None]
+    z, g = (xd - md) * rd, dyd * wd
+    ref = rd * (g - g.mean(1, keepdim=True) - z * (g * z).mean(1, keepdim=True))
+    xh, xt, g = (xd.abs() + md.abs()) * rd, z.abs(), g.abs()
+    mag = rd * (g + g.mean(1, keepdim=True) + xh * (g * xt).mean(1, keepdim=True) + xt * (g * xh).mean(1, keepdim=True))
+    near_on_gpu(tag + " dx", dx, ref, U[dtype] * ref.abs() + e * mag)
+    near_on_gpu(tag + " dw", dw, (dyd * z).sum(0), 2.0 ** -18 * (dyd.abs() * xh).sum(0))
+    near_on_gpu(tag + " db", db, dyd.sum(0), 2.0 ** -18 * dyd.abs().sum(0))
+    for a, c in zip((dx, dw, db), muon.layer_norm_backward(dy, x, mean, rstd, w)):
+        assert torch.equal(a, c)
