@@ -975,3 +975,29 @@ def test_layer_norm_over_many_rows(muon, rows, cols, pad, dtype):
     near_on_gpu(tag + " db", db, dyd.sum(0), 2.0 ** -18 * dyd.abs().sum(0))
     for a, c in zip((dx, dw, db), muon.layer_norm_backward(dy, x, mean, rstd, w)):
         assert torch.equal(a, c)
+
+
+# Both accumulators and their phases (more than 2048 tokens, several thousand of them), rings carried from item to item
+# (more tiles than pairs), output bands past the first eight tiles, splits of more than 2048 tokens.
+@pytest.mark.parametrize("rows,cols,out,odtype,add", [
+    (4239, 1500, 4100, FP, False), (4239, 1500, 4100, FP, True), (6273, 1500, 4100, BF, True), (20001, 1024, 2600, FP, False),
+    (70, 3000, 9000, FP, True), (8200, 300, 20000, BF, False), (200001, 200, 136, FP, True), (400003, 300, 250, BF, False)])
+def test_act8_weight_grad_over_many_tokens_and_tiles(muon, rows, cols, out, odtype, add):
+    x, dy = rand(174, rows, cols, dtype=BF) + 0.2, rand(175, rows, out, dtype=BF)
+    kept = muon.act8_store(x)
+    base = rand(176, out, cols, dtype=odtype) if add else None
+    got = muon.act8_weight_grad(dy, *kept, add=base, dtype=odtype)
+    assert muon.default_handle().check() == 0
+    xd, dyd = muon.act8_restore(*kept, dtype=FP).double(), dy.double()
+    ref, mag = dyd.t() @ xd, dyd.abs().t() @ xd.abs()
+    if add:
+        ref, mag = ref + base.double(), mag + base.double().abs()
+    # 16 products an addition, 128 additions an accumulator; then one rounded addition each 2048 tokens, of a split
+    # (its steps of 64 tokens over the splits), and one a split
+    terms = min(rows, 2048) / 16 + rows / 2048 + 16
+    tol = U[odtype] * ref.abs() + terms * 2.0 ** -23 * mag
+    near_on_gpu(f"weight grad {rows}x{cols}x{out} {odtype}", got, ref, tol)
+    assert torch.equal(got, muon.act8_weight_grad(dy, *kept, add=base, dtype=odtype))
+    if add:
+        muon.act8_weight_grad(dy, *kept, add=base, out=base)
+        assert torch.equal(base, got)
