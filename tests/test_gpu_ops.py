@@ -1001,3 +1001,45 @@ def test_act8_weight_grad_over_many_tokens_and_tiles(muon, rows, cols, out, odty
     if add:
         muon.act8_weight_grad(dy, *kept, add=base, out=base)
         assert torch.equal(base, got)
+
+
+# ----------------------------------------------- offsets that are not in order
+def clamped(cuts, axis):
+    """The documented rule: cut to the axis, and raised to the largest before."""
+    out = []
+    for c in cuts:
+        out.append(max(min(max(c, 0), axis), out[-1] if out else 0))
+    return out
+
+
+@pytest.mark.parametrize("cuts_q,cuts_k", [
+    ([10, 200, 390], None), ([0, 200, 100, 5000], None), ([-7, 150, 150], None), ([390, 10, 400], None),
+    ([5, 60, 50, 300], [-3, 130, 260, 100]), ([7], None),
+    ([3 + 9 * i - (40 if i % 13 == 5 else 0) + (9999 if i == 60 else 0) for i in range(64)], None),
+    ([6 * i - (100 if i == 40 else 0) for i in range(50)], [2 ** 31 - 1 if i > 45 else 8 * i - 20 for i in range(50)])])
+def test_packed_offsets_follow_the_rule(muon, cuts_q, cuts_k):
+    n, h, dim = 400, 2, 64
+    cuts_k = cuts_q if cuts_k is None else cuts_k
+    q, k, v, do = (rand(180 + i, n, h, dim, dtype=BF) for i in range(4))
+    kw = dict(causal=True, cu_seqlens_q=torch.tensor(cuts_q, dtype=torch.int32).cuda(),
+              cu_seqlens_k=torch.tensor(cuts_k, dtype=torch.int32).cuda())
+    o, lse = muon.attention(q, k, v, **kw)
+    grads = muon.attention_backward(do, q, k, v, o, lse, **kw)
+    assert muon.default_handle().check() == 0
+    cq, ck = clamped(cuts_q, n), clamped(cuts_k, n)
+    spans = [(None, *s) for s in zip(cq, cq[1:], ck, ck[1:])]
+    check_attention(f"offsets {cuts_q[:4]} {cuts_k[:4]}", BF, dim ** -0.5, True, 0, spans, q, k, v, do, o, lse, grads)
+    for cuts, tensors in ((cq, (o, grads[0], lse.t())), (ck, grads[1:])):
+        outside = torch.ones(n, dtype=torch.bool, device="cuda")
+        outside[cuts[0]:cuts[-1]] = False
+        for t in tensors:
+            want = -math.inf if t.dtype == FP else 0.0
+            assert (t[outside] == want).all()
+
+
+@pytest.mark.parametrize("dim,heads,kv,seq", [(64, 12, 12, 1024), (128, 16, 4, 2048), (128, 1, 1, 9000)])
+def test_attention_waits_end(muon, dim, heads, kv, seq):
+    q, k, v, do = (rand(184 + i, 2, seq, n, dim, dtype=HF) for i, n in enumerate((heads, kv, kv, heads)))
+    o, lse = muon.attention(q, k, v, causal=True)
+    run_with_short_waits(muon, lambda: (*muon.attention(q, k, v, causal=True),
+                                        *muon.attention_backward(do, q, k, v, o, lse, causal=True)))
