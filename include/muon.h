@@ -283,8 +283,11 @@ muon_status_t muon_noalloc_set_timeout_ns(uint64_t timeout_ns);
  *     least the bytes that the matching *_workspace call reports (host only,
  *     from shapes alone; 0 bytes: NULL is fine).  It is scratch: free for
  *     other use once the call's work on `stream` is done.
- *   - Sums, statistics and softmax are held in fp32; each output is rounded
- *     once to its type.  Results do not change from call to call.
+ *   - Sums, statistics and softmax are held in fp32, and each output is
+ *     rounded once to its type.  Beside that, attention rounds factors of its
+ *     products (see there), and sums on the tensor cores are truncated to 24
+ *     bits with each 16 products that are added (see attention and the weight
+ *     gradient).  Results do not change from call to call.
  *   - An operand of an unsupported size, stride or alignment gives
  *     MUON_ERR_INVALID_ARG before anything is enqueued.
  */
@@ -335,7 +338,18 @@ muon_status_t muon_layer_norm_workspace(muon_handle_t h, int64_t rows, int64_t c
  *            dimension of one element is not used); pointers 16-byte aligned
  *   lse      fp32 [batch][heads][sq] ([heads][sq] when packed), contiguous
  * Rows of a sequence are cut at its length: what lies past it, NaN and
- * infinity included, has no part in the result. */
+ * infinity included, has no part in the result.
+ *
+ * The probabilities p_ij, and in the backward pass ds_ij, are factors of
+ * products on the tensor cores and are rounded to dtype for them; row sums and
+ * everything before are fp32.  So an element of o, dv (p), dq or dk (ds) is off
+ * by up to 2^-9 (bf16) or 2^-12 (fp16) of the sum of its products' magnitudes,
+ * beside its own rounding: about 1.4 times the error of its rounding alone.
+ * There is no wider form.  fp16 keeps p's bits down to 2^-25 of the row's
+ * largest (forward) or 2^-28 (backward); ds has fp16's range as it is, so
+ * gradients of o are scaled (as fp16 gradients are) to keep ds between 2^-14
+ * and 2^16.  Sums of one sign are too small by up to 5e-5 (fp16) or 4e-4 (bf16)
+ * of themselves, a fifth of an output's rounding. */
 typedef struct {
   const void* q;
   const void* k;
@@ -404,7 +418,11 @@ muon_status_t muon_act8_restore(muon_handle_t h, const uint8_t* codes, int64_t l
  *            aligned start is read in place, anything else copied first)
  *   add, dw  odtype (MUON_F32 or MUON_BF16) [out][cols], row strides ldadd,
  *            lddw; add may be NULL, or dw itself
- * rows == 0 gives zeros (or add). */
+ * rows == 0 gives zeros (or add).
+ * The factors are exact; 2048 tokens at a time are added up on the tensor
+ * cores, with truncation, and those sums in fp32 with rounding: an error of
+ * up to 2^-16 of the sum of the products' magnitudes (measured 1e-6 of dw and
+ * less). */
 muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t lddy, const uint8_t* codes, int64_t ldc,
                                     const uint8_t* scales, int64_t lds, const void* add, int64_t ldadd, void* dw,
                                     int64_t lddw, int64_t rows, int64_t cols, int64_t out, int32_t odtype,

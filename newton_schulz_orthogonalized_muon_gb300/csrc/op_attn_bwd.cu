@@ -24,10 +24,12 @@
 // tensor pipe for 128 x 128 pairs, measured 2600 to 2900 and 2030, as shared
 // memory, from which N = 128 products take 128 bytes a cycle, is as busy.
 // 8192 causal tokens of 32 heads (8 of keys), bf16: 1.08 ms, 1270 TFLOP/s of
-// the five products that the gradient needs, 1780 of the seven.  With short
-// sequences and dim 64 the way of a tile through the element-wise warps
-// binds: 8 x 1024 causal tokens of 12 heads take 69 us, 465 TFLOP/s of five,
-// with 50% of the issue slots and 35% of the tensor pipe used.  (p and ds of
+// the five products that the gradient needs, 1780 of the seven (this kernel
+// alone; a call takes 1.11 ms, and 1.20 to 1.24 where calls follow one another
+// under the power limit).  With short sequences and dim 64 the way of a tile
+// through the element-wise warps binds: 8 x 1024 causal tokens of 12 heads take
+// 66 us (a call 75), 490 TFLOP/s of five, with 51% of the issue slots and 36%
+// of the tensor pipe used.  (p and ds of
 // a tile in one go, with half the barriers, took 11% longer: no product then
 // runs beside them.)
 #include <cstddef>

@@ -28,10 +28,13 @@
 // pairs with dim 128 take 2048 cycles of the tensor pipe, and as many of
 // shared memory, from which the score products take 128 bytes a cycle beside
 // the loads of K and V; 32768 exponentials run next to them.  Measured: 8192
-// causal tokens of 32 heads (8 of keys), dim 128, bf16, in 363 us, 1510
-// TFLOP/s of the visible pairs' products, about 3180 cycles a step.  (Two
-// warps a row's half each, 16 for the softmax, took 439 us: a meeting a step
-// and registers that spill cost more than the shorter way saves.)
+// causal tokens of 32 heads (8 of keys), dim 128, bf16, in 362 us, 1520
+// TFLOP/s of the visible pairs' products, about 3180 cycles a step (377 to 380
+// us where calls follow one another under the power limit).  dim 64, 8 x 1024
+// causal tokens of 12 heads: 33 us, 390 TFLOP/s, 23% of the tensor pipe, one
+// CTA an SM.  (Two warps a row's half each, 16 for the softmax, took 439 us
+// with dim 128: a meeting a step and registers that spill cost more than the
+// shorter way saves.)
 #include <cstddef>
 
 #include "common.cuh"

@@ -22,9 +22,10 @@
 // fp32 partial results a second kernel adds in a fixed order.
 //
 // 16384 tokens, 4096 columns, 14336 outputs in 1.19 ms, 1620 TFLOP/s, bound by
-// the products (and, in long runs, by the power limit: 1.27 ms); 1001 x 2048 x
-// 1408 with `add` in 21 us, of which 14 are a CTA's start, first loads and
-// epilogue.
+// the products (and, in calls that follow one another, by the power limit: 1.26
+// to 1.28 ms); 1001 x 2048 x 1408 with `add` in 21 us with cold caches (18 in
+// calls that follow one another), of which 14 are a CTA's start, first loads
+// and epilogue.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

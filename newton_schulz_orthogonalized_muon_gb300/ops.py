@@ -5,7 +5,11 @@ probabilities) and activations kept in 8 bits.  Each is a call of the C ABI
 in include/muon.h by way of an extension module (csrc/torch_ops.cpp): the
 tensors are checked, outputs and scratch are allocated by torch on the stream
 that the kernels run on, arguments that do not go together raise ValueError,
-a non-OK status raises MuonError.  ``nn`` wraps them for autograd.
+a non-OK status raises MuonError.
+
+These calls are outside autograd: they take the values of tensors that require
+gradients and return results without a graph (or a tangent).  ``nn`` wraps
+them for autograd.
 
 Every function takes ``stream`` (default: the current stream of the tensors'
 device) and ``handle`` (default: that device's handle).  Inputs that are
@@ -82,7 +86,8 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, cu_
     ``causal``: it sees keys up to its place, with ``window`` only the last
     ``window`` of them.  scale (above 0): 1 / sqrt(dim) by default.
     o has q's shape and type (a query that sees no key: 0); lse is fp32
-    [batch, heads, sq] or [heads, tokens] (there: -inf)."""
+    [batch, heads, sq] or [heads, tokens] (there: -inf).  The softmax is fp32;
+    the probabilities are rounded to q's type for their product with v."""
     if stream is not None:
         with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
             return attention(q, k, v, causal=causal, window=window, scale=scale, cu_seqlens_q=cu_seqlens_q,
@@ -98,7 +103,9 @@ def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int
                        cu_seqlens_k=None, handle=None, stream=None):
     """``(dq, dk, dv)`` of attention, from its output and lse: the
     probabilities are recomputed, nothing of size sq x sk is kept.  dk and dv
-    are summed over the query heads that share them, in a fixed order."""
+    are summed over the query heads that share them, in a fixed order.  The
+    probabilities and the scores' gradients are rounded to q's type for their
+    products; with fp16 `do` has to be scaled so that the latter fit it."""
     if stream is not None:
         with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
             return attention_backward(do, q, k, v, o, lse, causal=causal, window=window, scale=scale, cu_seqlens_q=cu_seqlens_q,
