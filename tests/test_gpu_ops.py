@@ -1043,3 +1043,33 @@ def test_attention_waits_end(muon, dim, heads, kv, seq):
     o, lse = muon.attention(q, k, v, causal=True)
     run_with_short_waits(muon, lambda: (*muon.attention(q, k, v, causal=True),
                                         *muon.attention_backward(do, q, k, v, o, lse, causal=True)))
+
+
+def test_long_attention_in_a_graph_and_on_two_streams(muon):
+    """Walks in parts: scratch and counter are the call's own."""
+    q, do = rand(190, 1, 9001, 2, 64, dtype=HF), rand(191, 1, 9001, 2, 64, dtype=HF)
+    k, v = rand(192, 1, 9001, 1, 64, dtype=HF), rand(193, 1, 9001, 1, 64, dtype=HF)
+
+    def work():
+        o, lse = muon.attention(q, k, v, causal=True)
+        return [o, lse, *muon.attention_backward(do, q, k, v, o, lse, causal=True)]
+    want = work()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(work())
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for _ in range(2):
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held))
+    assert muon.default_handle().check() == 0
