@@ -21,13 +21,14 @@ constexpr int BOX_BYTES = 128 * 128;         // 128 rows x 64 16-bit columns
 constexpr float LOG2E = 1.4426950408889634f;
 
 // The tensor core adds each product of 16 rows to its fp32 accumulator with
-// truncation, so a sum of one sign comes out too small the more the longer
-// (walks of 8192, 65536 and 524288 rows: by 5e-5, 4e-4 and 3e-3 of itself).  The results' rounding is up to 2^-12 in fp16 and 2^-9 in bf16, five
-// times that of 8192 and 65536 rows.  Walks over more rows are handed over in
-// parts of as many, which are added up in fp32 with rounding, in scratch
-// memory of the CTA (p.part): each value is read back by the thread that wrote
-// it.  (Kernels of their own: the hot loops took 3 to 4% longer with the code
-// for parts beside them.)
+// truncation, so a sum of one sign comes out too small, the more the longer
+// (walks of 8192, 65536 and 524288 rows: by 5e-5, 4e-4 and 3e-3 of itself).
+// Results are rounded by up to 2^-12 (fp16) or 2^-9 (bf16), five times what
+// 8192 or 65536 rows lose.  Walks over more rows are handed over in parts of
+// as many, which are added up in fp32 with rounding, in scratch memory of the
+// CTA (p.part): each value is read back by the thread that wrote it.  (Kernels
+// of their own: the hot loops took 3 to 4% longer with the code for parts
+// beside them.)
 template <typename T>
 constexpr int SUM_ROWS = attn_sum_rows(std::is_same<T, __nv_bfloat16>::value);
 
