@@ -431,6 +431,41 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
 muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, const void* dy, int64_t lddy, int64_t rows,
                                               int64_t cols, int64_t out, uint64_t* bytes);
 
+/* Products of a layer of experts, tokens grouped by expert.  Expert e has the
+ * tokens offsets[e] .. offsets[e + 1] - 1 of the token axis (device int32
+ * [experts + 1]; read on the device: an offset outside the axis, or below the
+ * largest before it, is raised or cut to that).
+ *   transpose 0:  y[t] = W[e] x[t],    x [tokens][cols], y [tokens][out]
+ *   transpose 1:  y[t] = W[e]^T x[t],  x [tokens][out], y [tokens][cols]
+ * (the second gives the gradient of the input).  A token of no expert gets
+ * zeros, whatever it holds.
+ *   x, w, y   dtype (MUON_BF16 or MUON_F16); w [experts][out][cols], expert and
+ *             row strides w_expert, ldw
+ *   cols, out multiples of 8; strides of x and w multiples of 8, theirs and y's
+ *             pointers 16-byte aligned
+ *   experts   1 .. 1024
+ * Sums are fp32 on the tensor cores (truncated, as above: up to 6e-5 of
+ * themselves over 16384 products of one sign), rounded once to dtype.
+ * tokens == 0 is a valid no-op. */
+muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                 int64_t w_expert, const int32_t* offsets, void* y, int64_t ldy, int64_t tokens,
+                                 int64_t cols, int64_t out, int64_t experts, int32_t transpose, int32_t dtype,
+                                 void* stream);
+
+/* The gradient of its weight: dw[e] = sum over e's tokens of dy[t] x[t]^T
+ * (+ add[e]); an expert without tokens gets zeros (or add).
+ *   dy, x    dtype, [tokens][out], [tokens][cols]
+ *   add, dw  odtype (MUON_F32 or dtype) [experts][out][cols]; add may be NULL, or
+ *            dw itself with its strides
+ * 2048 tokens at a time are added up on the tensor cores, with truncation, and
+ * those sums in fp32 with rounding, in `workspace`. */
+muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                      const int32_t* offsets, const void* add, int64_t ldadd, int64_t add_expert,
+                                      void* dw, int64_t lddw, int64_t dw_expert, int64_t tokens, int64_t cols,
+                                      int64_t out, int64_t experts, int32_t dtype, int32_t odtype, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, uint64_t* bytes);
+
 /* Kernel classes reported by muon_handle_profile(). */
 enum {
   MUON_K_PREPARE = 0, /* momentum / Nesterov / norm partials / working copy */
@@ -445,7 +480,8 @@ enum {
   MUON_K_ATTENTION = 9,
   MUON_K_ACT8 = 10,   /* store and restore                                  */
   MUON_K_WGRAD = 11,  /* weight gradient from 8-bit activations             */
-  MUON_K_COUNT = 12
+  MUON_K_EXPERTS = 12, /* products by expert                                 */
+  MUON_K_COUNT = 13
 };
 
 /* Enable (1) or disable (0) per-launch CUDA-event timing on the launching

@@ -33,9 +33,10 @@ EXPORTS = ("muon_handle_create", "muon_handle_destroy", "muon_handle_set_workspa
            "muon_layer_norm_forward", "muon_layer_norm_backward", "muon_layer_norm_workspace",
            "muon_attention_forward", "muon_attention_backward", "muon_attention_workspace",
            "muon_attention_forward_ex", "muon_attention_forward_workspace",
-           "muon_act8_store", "muon_act8_restore", "muon_act8_weight_grad", "muon_act8_weight_grad_workspace")
+           "muon_act8_store", "muon_act8_restore", "muon_act8_weight_grad", "muon_act8_weight_grad_workspace",
+           "muon_expert_matmul", "muon_expert_weight_grad", "muon_expert_weight_grad_workspace")
 KERNEL_CLASSES = ("prepare", "norm", "syrk", "poly", "update", "final", "apply", "adamw", "layer_norm", "attention",
-                  "act8", "wgrad")
+                  "act8", "wgrad", "experts")
 
 
 class MuonError(RuntimeError):
@@ -124,6 +125,10 @@ def load_library(path: str | None = None):
             "muon_act8_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp,
                                             ctypes.c_size_t, vp]),
             "muon_act8_weight_grad_workspace": (i32, [vp, vp, i64, i64, i64, i64, ctypes.POINTER(u64)]),
+            "muon_expert_matmul": (i32, [vp, vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
+            "muon_expert_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i64, i64, i64, i64, i64, i32,
+                                              i32, vp, ctypes.c_size_t, vp]),
+            "muon_expert_weight_grad_workspace": (i32, [vp, i64, ctypes.POINTER(u64)]),
             "muon_workspace_size": (i32, [vp, ctypes.POINTER(MuonParamC), i32, i32, i32, i32, ctypes.POINTER(u64)]),
         }
         for name, (res, args) in sig.items():

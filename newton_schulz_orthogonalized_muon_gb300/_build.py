@@ -23,8 +23,10 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libmuon_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["muon_api.cu", "kernels_tc.cu", "kernels_tc2.cu", "kernels_elem.cu", "kernels_simt.cu", "noalloc.cu",
-           "ops_api.cu", "op_norm.cu", "op_act8.cu", "op_wgrad.cu", "op_attn_fwd.cu", "op_attn_bwd.cu"]
-HEADERS = ["common.cuh", "internal.h", "tc_common.cuh", "launch_opts.h", "handle.h", "op_common.cuh", "op_attn.cuh"]
+           "ops_api.cu", "op_norm.cu", "op_act8.cu", "op_wgrad.cu", "op_attn_fwd.cu", "op_attn_bwd.cu",
+           "op_product.cu"]
+HEADERS = ["common.cuh", "internal.h", "tc_common.cuh", "launch_opts.h", "handle.h", "op_common.cuh", "op_attn.cuh",
+           "op_pair.cuh"]
 MODULE_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 MODULE_PATH = os.path.join(HERE, "_torch_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -341,6 +341,30 @@ cudaError_t launch_act8_wgrad_join(const WgradParams& p, int sms, cudaStream_t s
 cudaError_t launch_pad_rows(const __nv_bfloat16* src, long long lds, __nv_bfloat16* dst, long long ldd, long long rows,
                             int cols, int sms, cudaStream_t s);
 
+// ------------------------------------- products by expert and in 8 bits
+enum ProductKind : int { PRODUCT_FORWARD = 0, PRODUCT_INPUT = 1, PRODUCT_WEIGHT = 2 };
+constexpr int kMaxExperts = 1024;
+struct ProductParams {
+  const int* offsets;      // [groups + 1] on the token axis, or nullptr (one group of all tokens)
+  const void* add;         // weight: [groups][n][m] of odtype, or nullptr
+  void* out;               // tokens: [tokens][m]; weight: [groups][n][m]; of odtype
+  long long ldo, out_group, ldadd, add_group;   // row and group strides in elements
+  float* part;             // weight: scratch of product_part_bytes
+  int kind;                // ProductKind
+  int tokens, groups;
+  int m, n, k;             // m: consecutive outputs; n: weight's rows of outputs; k: summed (not weight, whose sums are
+                           // over tokens)
+  int odtype;
+  int f16;                 // the operands are fp16 (else bf16)
+  int vec;                 // set by the launcher: rows of out and add are 16-byte aligned
+  unsigned* err;           // the handle's error word
+  unsigned long long timeout_ns;
+};
+// maps, 3-D with 128-byte swizzle: A and B (see op_product.cu).  K-major: {k, rows, groups or 1} in boxes of 64 k and 128
+// rows (A) or 32 (B); MN-major: {rows, k, groups or 1} in boxes of 64 rows and 64 k.
+uint64_t product_part_bytes(int64_t tokens, int sms);
+cudaError_t launch_product(const ProductParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s);
+
 // ------------------------------------------------------------ attention
 struct AttnParams {
   const void *q, *k, *v;   // element (b, s, h, d) at b * s?b + s * s?s + h * s?h + d

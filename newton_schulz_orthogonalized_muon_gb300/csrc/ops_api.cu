@@ -13,6 +13,7 @@ using namespace muon;
 
 namespace {
 
+constexpr int64_t kMaxSide = int64_t(1) << 20;       // of an expert's weight
 constexpr int64_t kMaxTokens = int64_t(1) << 30;     // token and row counts fit an int with room to spare
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -188,6 +189,38 @@ WgradPlan wgrad_plan(muon_handle_t h, const void* dy, int64_t lddy, int64_t rows
   if (rows > 0 && ((rows > 1 && lddy % 8 != 0) || !aligned(dy, 16)))
     w.pad_bytes = round256(static_cast<uint64_t>(rows) * ((out + 7) / 8 * 8) * 2);
   return w;
+}
+
+// Map of an operand of a product by expert: [groups][rows][cols] of 16-bit
+// elements, the last contiguous, in boxes of 64 columns and `box` rows.
+bool product_map(muon_handle_t h, CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t groups,
+                 int64_t group, int dtype, uint32_t box) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
+  // (the stride of a dimension of one element is not used)
+  const cuuint64_t pitch = static_cast<cuuint64_t>(rows > 1 ? ld : cols) * 2;
+  cuuint64_t strides[2] = {pitch, groups > 1 ? static_cast<cuuint64_t>(group) * 2 : pitch};
+  cuuint32_t boxes[3] = {64, box, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return h->encode(map, dtype == MUON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void*>(base), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+muon_status_t check_experts(muon_handle_t h, const int32_t* offsets, int64_t tokens, int64_t cols, int64_t out,
+                            int64_t experts, int32_t dtype) {
+  MUON_CHECK(dtype == MUON_BF16 || dtype == MUON_F16, "dtype must be MUON_BF16 or MUON_F16");
+  MUON_CHECK(tokens >= 0 && tokens <= kMaxTokens, "tokens must be in [0, 2^30]");
+  MUON_CHECK(cols >= 8 && cols <= kMaxSide && cols % 8 == 0 && out >= 8 && out <= kMaxSide && out % 8 == 0,
+             "cols and out must be multiples of 8 in [8, 2^20]");
+  MUON_CHECK(experts >= 1 && experts <= kMaxExperts, "experts must be in [1, 1024]");
+  MUON_CHECK(offsets != nullptr && aligned(offsets, 4), "offsets is NULL or not aligned");
+  return MUON_OK;
+}
+
+// Rows of 16-bit elements as TMA reads them.
+bool bad_rows(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  return p == nullptr || !aligned(p, 16) || (rows > 1 && (ld < cols || ld % 8 != 0 || ld > (int64_t(1) << 38)));
 }
 
 }  // namespace
@@ -508,6 +541,105 @@ muon_status_t muon_act8_weight_grad(muon_handle_t h, const void* dy, int64_t ldd
     MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad(p, maps, rows > 0 && plan.pad_bytes > 0, h->num_sms / 2, stream), "weight gradient launch");
     if (p.splits > 1)
       MUON_LAUNCH(MUON_K_WGRAD, launch_act8_wgrad_join(p, h->num_sms, stream), "weight gradient join launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                 int64_t w_expert, const int32_t* offsets, void* y, int64_t ldy, int64_t tokens,
+                                 int64_t cols, int64_t out, int64_t experts, int32_t transpose, int32_t dtype,
+                                 void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    const muon_status_t st = check_experts(h, offsets, tokens, cols, out, experts, dtype);
+    if (st != MUON_OK) return st;
+    if (tokens == 0) return MUON_OK;
+    const int64_t in = transpose ? out : cols, to = transpose ? cols : out;
+    MUON_CHECK(!bad_rows(x, ldx, tokens, in) && !bad_rows(w, ldw, out, cols) &&
+                   (experts == 1 || (w_expert % 8 == 0 && w_expert >= (out - 1) * (out > 1 ? ldw : 0) + cols &&
+                                     w_expert <= (int64_t(1) << 38))),
+               kBadOperand);
+    MUON_CHECK(y != nullptr && aligned(y, 16) && (ldy >= to || tokens == 1), "y is NULL, not aligned or its row stride is too small");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    ProductParams p{};
+    p.kind = transpose ? PRODUCT_INPUT : PRODUCT_FORWARD;
+    p.offsets = offsets;
+    p.out = y;
+    p.ldo = ldy;
+    p.tokens = static_cast<int>(tokens);
+    p.groups = static_cast<int>(experts);
+    p.m = static_cast<int>(to);
+    p.k = static_cast<int>(in);
+    p.odtype = dtype;
+    p.f16 = dtype == MUON_F16;
+    p.err = h->err;
+    p.timeout_ns = h->timeout_ns;
+    h->prof_tag = -1;
+    CUtensorMap maps[2] = {};
+    if (!product_map(h, &maps[0], w, cols, out, ldw, experts, w_expert, dtype, transpose ? 64 : 128) ||
+        !product_map(h, &maps[1], x, in, tokens, ldx, 1, 0, dtype, 32))
+      return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
+    MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms / 2, stream), "experts' product launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, uint64_t* bytes) {
+  if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    MUON_CHECK(tokens >= 0 && tokens <= kMaxTokens, "tokens must be in [0, 2^30]");
+    *bytes = product_part_bytes(tokens, h->num_sms);
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                      const int32_t* offsets, const void* add, int64_t ldadd, int64_t add_expert,
+                                      void* dw, int64_t lddw, int64_t dw_expert, int64_t tokens, int64_t cols,
+                                      int64_t out, int64_t experts, int32_t dtype, int32_t odtype, void* workspace,
+                                      size_t workspace_bytes, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    const muon_status_t st = check_experts(h, offsets, tokens, cols, out, experts, dtype);
+    if (st != MUON_OK) return st;
+    const uint64_t need = product_part_bytes(tokens, h->num_sms);
+    MUON_CHECK(need == 0 || (workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256)),
+               "the workspace is too small or not 256-byte aligned");
+    MUON_CHECK(odtype == MUON_F32 || odtype == dtype, "odtype must be MUON_F32 or dtype");
+    MUON_CHECK(tokens == 0 || (!bad_rows(x, ldx, tokens, cols) && !bad_rows(dy, lddy, tokens, out)), kBadOperand);
+    auto whole = [&](const void* p, int64_t ld, int64_t group) {
+      return p != nullptr && aligned(p, odtype == MUON_F32 ? 4 : 2) && (ld >= cols || out == 1) &&
+             (experts == 1 || group >= (out - 1) * ld + cols);
+    };
+    MUON_CHECK(whole(dw, lddw, dw_expert), "dw is NULL, not aligned or its strides are too small");
+    MUON_CHECK(add == nullptr || whole(add, ldadd, add_expert), "add is not aligned or its strides are too small");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    ProductParams p{};
+    p.kind = PRODUCT_WEIGHT;
+    p.offsets = offsets;
+    p.add = add;
+    p.out = dw;
+    p.ldo = lddw;
+    p.out_group = dw_expert;
+    p.ldadd = ldadd;
+    p.add_group = add_expert;
+    p.part = static_cast<float*>(workspace);
+    p.tokens = static_cast<int>(tokens);
+    p.groups = static_cast<int>(experts);
+    p.m = static_cast<int>(cols);
+    p.n = static_cast<int>(out);
+    p.odtype = odtype;
+    p.f16 = dtype == MUON_F16;
+    p.err = h->err;
+    p.timeout_ns = h->timeout_ns;
+    h->prof_tag = -1;
+    CUtensorMap maps[2] = {};
+    if (tokens > 0 && (!product_map(h, &maps[0], x, cols, tokens, ldx, 1, 0, dtype, 64) ||
+                       !product_map(h, &maps[1], dy, out, tokens, lddy, 1, 0, dtype, 64)))
+      return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
+    MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms / 2, stream), "experts' weight gradient launch");
     return MUON_OK;
   });
 }

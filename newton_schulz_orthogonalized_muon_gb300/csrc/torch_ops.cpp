@@ -530,6 +530,105 @@ PyObject* act8_weight_grad(Args a) {
   return result(st, std::move(out));
 }
 
+// ------------------------------------------------------ products by expert
+// [.., rows, cols] of 16-bit elements as the kernels read it: the last dimension
+// contiguous, the other strides multiples of 8 that do not overlap, on a 16-byte
+// boundary.  Anything else is copied once.
+at::Tensor by_rows(const at::Tensor& t) {
+  const int64_t d = t.dim();
+  bool fine = reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && (t.stride(d - 1) == 1 || t.size(d - 1) == 1);
+  int64_t span = t.size(d - 1);
+  for (int64_t i = d - 2; i >= 0; --i) {
+    if (t.size(i) <= 1) continue;
+    fine = fine && t.stride(i) % 8 == 0 && t.stride(i) >= span;
+    span += (t.size(i) - 1) * t.stride(i);
+  }
+  return fine ? t : t.clone(at::MemoryFormat::Contiguous);
+}
+
+const int32_t* expert_offsets(const at::Tensor& t, int64_t experts) {
+  if (t.scalar_type() != at::kInt || t.dim() != 1 || !t.is_contiguous()) refuse("offsets must be a contiguous int32 vector");
+  if (experts >= 0 && t.size(0) != experts + 1)
+    refuse("offsets must have " + std::to_string(experts + 1) + " elements, one more than there are experts");
+  if (t.size(0) < 2) refuse("offsets must have at least two elements");
+  return t.data_ptr<int32_t>();
+}
+
+void need_16_bit(const at::Tensor& t, const char* what) {
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kHalf) refuse(std::string(what) + " must be bfloat16 or float16");
+}
+
+PyObject* expert_matmul(Args a) {
+  const Target t = a.target();
+  const at::Tensor &x = *a.tensor(t, "x"), &weight = *a.tensor(t, "weight"), &offsets = *a.tensor(t, "offsets");
+  const bool transpose = a.truth();
+  at::Tensor y;
+  muon_status_t st;
+  {
+    NoGil free;
+    need_16_bit(x, "x");
+    if (weight.scalar_type() != x.scalar_type()) refuse("weight must have x's type");
+    if (x.dim() != 2 || weight.dim() != 3 || x.size(1) != weight.size(transpose ? 1 : 2))
+      refuse("shapes do not go together: x " + shape(x) + ", weight " + shape(weight));
+    const int64_t experts = weight.size(0), out = weight.size(1), cols = weight.size(2), tokens = x.size(0);
+    const int32_t* at = expert_offsets(offsets, experts);
+    const at::Tensor xr = by_rows(x), w = by_rows(weight);
+    const int64_t to = transpose ? cols : out;
+    y = empty({tokens, to}, x, x.scalar_type());
+    st = muon_expert_matmul(t.h, xr.data_ptr(), xr.stride(0), w.data_ptr(), w.stride(1), w.stride(0), at, y.data_ptr(), to,
+                            tokens, cols, out, experts, transpose ? 1 : 0, code_of(x.scalar_type()), t.stream());
+  }
+  return result(st, std::move(y));
+}
+
+PyObject* expert_weight_grad(Args a) {
+  const Target t = a.target();
+  const at::Tensor &dy = *a.tensor(t, "dy"), &x = *a.tensor(t, "x"), &offsets = *a.tensor(t, "offsets");
+  const at::Tensor *add = a.tensor(t, "add", true), *given = a.tensor(t, "out", true);
+  std::optional<at::ScalarType> type = a.dtype();
+  at::Tensor out;
+  muon_status_t st;
+  {
+    NoGil free;
+    need_16_bit(dy, "dy");
+    if (x.scalar_type() != dy.scalar_type()) refuse("x must have dy's type");
+    if (dy.dim() != 2 || x.dim() != 2 || dy.size(0) != x.size(0)) refuse("dy must be [tokens, out] and x [tokens, cols]");
+    const int32_t* at = expert_offsets(offsets, -1);
+    const int64_t experts = offsets.size(0) - 1, outs = dy.size(1), cols = x.size(1);
+    int64_t ld[2] = {cols, cols}, group[2] = {outs * cols, outs * cols};
+    const at::Tensor* both[2] = {add, given};
+    for (int i = 0; i < 2; ++i) {
+      const at::Tensor* m = both[i];
+      const std::string what = i == 0 ? "add" : "out";
+      if (m == nullptr) continue;
+      if (m->dim() != 3 || m->size(0) != experts || m->size(1) != outs || m->size(2) != cols)
+        refuse(what + " must have shape (" + std::to_string(experts) + ", " + std::to_string(outs) + ", " + std::to_string(cols) + ")");
+      if (type && m->scalar_type() != *type) refuse(what + " does not have the result's type");
+      type = m->scalar_type();
+      const bool rows = m->stride(2) == 1 && (m->stride(1) >= cols || outs == 1);
+      if (!rows || (experts > 1 && m->stride(0) < (outs - 1) * m->stride(1) + cols)) refuse(what + " must have contiguous rows that do not overlap");
+      ld[i] = std::max(m->stride(1), cols);
+      group[i] = m->stride(0);
+    }
+    if (!type) type = at::kFloat;
+    if (*type != at::kFloat && *type != dy.scalar_type()) refuse("dtype must be float32 or dy's type");
+    const at::Tensor g = by_rows(dy), xr = by_rows(x);
+    out = given != nullptr ? *given : empty({experts, outs, cols}, dy, *type);
+    if (given != nullptr) out.unsafeGetTensorImpl()->bump_version();     // autograd sees the write
+    uint64_t need = 0;
+    st = muon_expert_weight_grad_workspace(t.h, dy.size(0), &need);
+    if (st == MUON_OK) {
+      at::Tensor ws;
+      if (need > 0) ws = empty({static_cast<int64_t>(need)}, dy, at::kByte);
+      st = muon_expert_weight_grad(t.h, g.data_ptr(), g.stride(0), xr.data_ptr(), xr.stride(0), at,
+                                   add != nullptr ? add->data_ptr() : nullptr, ld[0], group[0], out.data_ptr(), ld[1], group[1],
+                                   dy.size(0), cols, outs, experts, code_of(dy.scalar_type()), code_of(*type),
+                                   need > 0 ? ws.data_ptr() : nullptr, need, t.stream());
+    }
+  }
+  return result(st, std::move(out));
+}
+
 // ------------------------------------------------------------------- module
 template <PyObject* (*F)(Args)>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -558,6 +657,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&call<f>)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {ENTRY(layer_norm), ENTRY(layer_norm_backward), ENTRY(attention), ENTRY(attention_backward),
                          ENTRY(act8_store), ENTRY(act8_restore), ENTRY(act8_weight_grad),
+                         ENTRY(expert_matmul), ENTRY(expert_weight_grad),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

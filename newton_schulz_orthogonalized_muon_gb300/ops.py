@@ -165,3 +165,41 @@ def act8_weight_grad(dy, codes, scales, *, add=None, out=None, dtype=None, handl
     if type(got) is int:
         h._raise(got, "act8_weight_grad")
     return got
+
+
+def expert_matmul(x, weight, offsets, *, transpose: bool = False, handle=None, stream=None):
+    """The product of a layer of experts: row t of the result is weight[e] x[t]
+    for the expert e with ``offsets[e] <= t < offsets[e + 1]``.
+
+    x: [tokens, cols], weight: [experts, out, cols], both bf16 or fp16, cols and
+    out multiples of 8; offsets: int32 [experts + 1] on the device, rising (an
+    offset below the largest before it is raised to that, one past the last
+    token cut).  The result is [tokens, out]; tokens of no expert get zeros.
+    ``transpose``: x is [tokens, out], the result [tokens, cols], each token
+    times its expert's transposed weight (the gradient of the input).  Strides
+    that are not multiples of 8, or starts off 16-byte boundaries, cost a copy."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return expert_matmul(x, weight, offsets, transpose=transpose, handle=handle)
+    h = _target(x, handle)
+    got = _native.expert_matmul(h.address, h.device, x, weight, offsets, transpose)
+    if type(got) is int:
+        h._raise(got, "expert_matmul")
+    return got
+
+
+def expert_weight_grad(dy, x, offsets, *, add=None, out=None, dtype=None, handle=None, stream=None):
+    """The gradient of expert_matmul's weight, [experts, out, cols]: for each
+    expert the sum over its tokens of dy[t] x[t]^T (+ add).
+
+    dy: [tokens, out], x: [tokens, cols], bf16 or fp16; add: the gradient so
+    far; out: where the result is written (``out=add`` adds in place); dtype:
+    float32 (default) or dy's type, that of add and out if they are given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return expert_weight_grad(dy, x, offsets, add=add, out=out, dtype=dtype, handle=handle)
+    h = _target(dy, handle)
+    got = _native.expert_weight_grad(h.address, h.device, dy, x, offsets, add, out, dtype)
+    if type(got) is int:
+        h._raise(got, "expert_weight_grad")
+    return got

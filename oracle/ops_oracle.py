@@ -134,3 +134,30 @@ def act8_decode(codes, scales):
 def act8_weight_grad(dy, x):
     """dy^T x and the sum of the products' magnitudes."""
     return dy.T @ x, np.abs(dy).T @ np.abs(x)
+
+
+# ------------------------------------------------------ products by expert
+def expert_ranges(offsets, tokens):
+    """[(first, end)] of each expert's tokens: offsets cut to the token axis
+    and raised to the largest before them."""
+    at = np.maximum.accumulate(np.clip(np.asarray(offsets, np.int64), 0, tokens))
+    return list(zip(at[:-1], at[1:]))
+
+
+def expert_matmul(x, w, offsets, transpose=False):
+    """x[t] w[e]^T (or x[t] w[e]) for the tokens of each expert, zeros for the
+    others, and the sum of the products' magnitudes."""
+    y = np.zeros((x.shape[0], w.shape[2 if transpose else 1]))
+    mag = np.zeros_like(y)
+    for e, (a, b) in enumerate(expert_ranges(offsets, x.shape[0])):
+        m = w[e] if transpose else w[e].T
+        y[a:b] = x[a:b] @ m
+        mag[a:b] = np.abs(x[a:b]) @ np.abs(m)
+    return y, mag
+
+
+def expert_weight_grad(dy, x, offsets):
+    """[experts, out, cols]: dy^T x over each expert's tokens, and the sum of
+    the products' magnitudes."""
+    parts = [(dy[a:b].T @ x[a:b], np.abs(dy[a:b]).T @ np.abs(x[a:b])) for a, b in expert_ranges(offsets, x.shape[0])]
+    return np.stack([p for p, _ in parts]), np.stack([m for _, m in parts])
