@@ -466,6 +466,77 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
                                       size_t workspace_bytes, void* stream);
 muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, uint64_t* bytes);
 
+/* A weight in 8 bits, for products with stored activations: each block of 128
+ * x 128 is stored as e4m3 codes of w 2^-e, rounded to nearest even, e the
+ * smallest integer >= -111 with a 2^-e <= 448 for the block's largest magnitude
+ * a.  The scale byte is e + 127.  A block with a NaN or an infinity gets the byte
+ * 255 and codes 0, which stand for NaN.
+ *   w        dtype, [out][cols], row stride ldw
+ *   codes    [out][cols], row stride ldc: a multiple of 128, >= cols; 16-byte
+ *            aligned; nothing past the last column is written
+ *   codes_t  the transpose's codes [cols][out], row stride ldt: a multiple of
+ *            128, >= out; 16-byte aligned; NULL: not written
+ *   scales   [ceil(cols / 128)][ceil(out / 128)] bytes, rows lds apart.  Read
+ *            with its two indices exchanged it belongs to codes_t. */
+muon_status_t muon_act8_store_weight(muon_handle_t h, const void* w, int64_t ldw, uint8_t* codes, int64_t ldc,
+                                     uint8_t* codes_t, int64_t ldt, uint8_t* scales, int64_t lds, int64_t out,
+                                     int64_t cols, int32_t dtype, void* stream);
+/* w[o][c] = code 2^e rounded to dtype, the scale of block (c / 128, o / 128) at
+ * scales[(c / 128) * s_col + (o / 128) * s_row]. */
+muon_status_t muon_act8_restore_weight(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                       int64_t s_col, int64_t s_row, void* w, int64_t ldw, int64_t out, int64_t cols,
+                                       int32_t dtype, void* stream);
+
+/* y[t][o] = sum over c of x[t][c] w[o][c] of stored activations (muon_act8_store:
+ * codes, ldc, scales, lds) and a stored weight (wcodes, ldw, wscales, s_col,
+ * s_row as above).  On the tensor cores, from the codes and scales as they are:
+ * the factors are exact, sums are fp32 (truncated with each 32 products that are
+ * added), rounded once to odtype.  A value stored as NaN makes its token's row,
+ * or its weight's columns, NaN.
+ *   y        odtype [rows][out], row stride ldy
+ * rows, out and cols are free; cols == 0 gives zeros. */
+muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                               const uint8_t* wcodes, int64_t ldw, const uint8_t* wscales, int64_t s_col,
+                               int64_t s_row, void* y, int64_t ldy, int64_t rows, int64_t cols, int64_t out,
+                               int32_t odtype, void* stream);
+
+/* The AdamW step of adamw_step with states in 8 bits, in blocks of 128 elements:
+ *   avg    e4m3 codes of the gradients' average m, scaled by 2^(127 - s), s the
+ *          block's byte in avg_scale (the activations' rule, above)
+ *   root   codes of r = v^(1/2), v the squares' average: 0 is 0, c > 0 is
+ *          (1 + (c & 15) / 16) 2^((c >> 4) - 8) times 2^(s - 127), s the byte in
+ *          root_scale: the smallest >= 16 with which the block's largest is at most
+ *          248.  A root above 0 gets code 1 at least.
+ * (all zero at start).  The step is computed from the states' values in fp32; the
+ * new states are then rounded up where their part past a code plus (b + 1/2) / 256
+ * is 1 or more, b being byte i % 4 of a 32-bit hash of (i / 4 + seed * 0x9E3779B1)
+ * for element i: x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B,
+ * x ^= x >> 16.  (e4m3 below its normal range: steps of 2^-9.)  Calls with other
+ * seeds round apart, so an average that moves by less than half a step moves all
+ * the same; use another one each step.  A NaN or an infinity in a block's new state makes the whole block's
+ * state NaN (byte 255, codes 0).
+ * tensors: a host array, read during the call; a tensor may not be in it twice.
+ * n == 0 is a valid no-op. */
+typedef struct {
+  void* param;            /* param_dtype, updated in place */
+  const void* grad;       /* grad_dtype, read only */
+  uint8_t* avg;           /* [numel], updated in place, as what follows */
+  uint8_t* root;          /* [numel] */
+  uint8_t* avg_scale;     /* [ceil(numel / 128)] */
+  uint8_t* root_scale;    /* [ceil(numel / 128)] */
+  int64_t numel;
+  int32_t param_dtype;    /* MUON_F32 or MUON_BF16 */
+  int32_t grad_dtype;     /* MUON_F32 or MUON_BF16 */
+} muon_adamw8_t;
+
+muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, int32_t n, int64_t step, uint32_t seed,
+                               float lr, float beta1, float beta2, float eps, float wd, void* stream);
+/* The values of states: m into avg[i] and r (not its square) into root[i], both
+ * dtype (MUON_F32: exact; MUON_BF16: exact above 2^-126).  param and grad are not
+ * read. */
+muon_status_t muon_adamw8_restore(muon_handle_t h, const muon_adamw8_t* tensors, void* const* avg, void* const* root,
+                                  int32_t n, int32_t dtype, void* stream);
+
 /* Kernel classes reported by muon_handle_profile(). */
 enum {
   MUON_K_PREPARE = 0, /* momentum / Nesterov / norm partials / working copy */
@@ -475,13 +546,14 @@ enum {
   MUON_K_UPDATE = 4,  /* X = aX + BX                                        */
   MUON_K_FINAL = 5,   /* last update fused with the parameter write         */
   MUON_K_APPLY = 6,   /* parameter write when no NS iteration runs          */
-  MUON_K_ADAMW = 7,   /* AdamW fallback                                     */
+  MUON_K_ADAMW = 7,   /* AdamW fallback, with fp32 or 8-bit states          */
   MUON_K_LAYER_NORM = 8,
   MUON_K_ATTENTION = 9,
-  MUON_K_ACT8 = 10,   /* store and restore                                  */
+  MUON_K_ACT8 = 10,   /* store and restore, activations' and weights'       */
   MUON_K_WGRAD = 11,  /* weight gradient from 8-bit activations             */
   MUON_K_EXPERTS = 12, /* products by expert                                 */
-  MUON_K_COUNT = 13
+  MUON_K_MATMUL8 = 13, /* product of 8-bit operands                          */
+  MUON_K_COUNT = 14
 };
 
 /* Enable (1) or disable (0) per-launch CUDA-event timing on the launching

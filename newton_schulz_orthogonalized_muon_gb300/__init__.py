@@ -19,7 +19,8 @@ _BINDING_NAMES = ("MuonHandle", "MuonError", "muon_orthogonalize", "muon_orthogo
 
 _OPTIM_NAMES = ("Muon", "split_params", "takes_muon")
 _OPS_NAMES = ("layer_norm", "layer_norm_backward", "attention", "attention_backward", "act8_store", "act8_restore",
-              "act8_weight_grad", "expert_matmul", "expert_weight_grad")
+              "act8_weight_grad", "expert_matmul", "expert_weight_grad", "act8_store_weight", "act8_restore_weight",
+              "act8_matmul", "Adamw8State", "adamw8_state", "adamw8_step", "adamw8_restore")
 
 
 def __getattr__(name):

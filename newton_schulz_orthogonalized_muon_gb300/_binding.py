@@ -34,9 +34,11 @@ EXPORTS = ("muon_handle_create", "muon_handle_destroy", "muon_handle_set_workspa
            "muon_attention_forward", "muon_attention_backward", "muon_attention_workspace",
            "muon_attention_forward_ex", "muon_attention_forward_workspace",
            "muon_act8_store", "muon_act8_restore", "muon_act8_weight_grad", "muon_act8_weight_grad_workspace",
-           "muon_expert_matmul", "muon_expert_weight_grad", "muon_expert_weight_grad_workspace")
+           "muon_expert_matmul", "muon_expert_weight_grad", "muon_expert_weight_grad_workspace",
+           "muon_act8_store_weight", "muon_act8_restore_weight", "muon_act8_matmul", "muon_adamw8_step",
+           "muon_adamw8_restore")
 KERNEL_CLASSES = ("prepare", "norm", "syrk", "poly", "update", "final", "apply", "adamw", "layer_norm", "attention",
-                  "act8", "wgrad", "experts")
+                  "act8", "wgrad", "experts", "matmul8")
 
 
 class MuonError(RuntimeError):
@@ -68,6 +70,11 @@ class MuonAttentionC(ctypes.Structure):
                 + [(n, ctypes.c_int32) for n in ("batch", "sq", "sk", "heads", "kv_heads", "dim", "causal", "window",
                                                  "dtype")]
                 + [("scale", ctypes.c_float)])
+
+
+class MuonAdamw8C(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("param", "grad", "avg", "root", "avg_scale", "root_scale")]
+                + [("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)])
 
 
 _lib = None
@@ -129,6 +136,13 @@ def load_library(path: str | None = None):
             "muon_expert_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i64, i64, i64, i64, i64, i32,
                                               i32, vp, ctypes.c_size_t, vp]),
             "muon_expert_weight_grad_workspace": (i32, [vp, i64, ctypes.POINTER(u64)]),
+            "muon_act8_store_weight": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
+            "muon_act8_restore_weight": (i32, [vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, i32, vp]),
+            "muon_act8_matmul": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i64, i64, i32, vp]),
+            "muon_adamw8_step": (i32, [vp, ctypes.POINTER(MuonAdamw8C), i32, i64, ctypes.c_uint32, f32, f32, f32, f32, f32,
+                                       vp]),
+            "muon_adamw8_restore": (i32, [vp, ctypes.POINTER(MuonAdamw8C), ctypes.POINTER(vp), ctypes.POINTER(vp), i32, i32,
+                                          vp]),
             "muon_workspace_size": (i32, [vp, ctypes.POINTER(MuonParamC), i32, i32, i32, i32, ctypes.POINTER(u64)]),
         }
         for name, (res, args) in sig.items():

@@ -24,9 +24,9 @@ LIB_NAME = "libmuon_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["muon_api.cu", "kernels_tc.cu", "kernels_tc2.cu", "kernels_elem.cu", "kernels_simt.cu", "noalloc.cu",
            "ops_api.cu", "op_norm.cu", "op_act8.cu", "op_wgrad.cu", "op_attn_fwd.cu", "op_attn_bwd.cu",
-           "op_product.cu"]
+           "op_product.cu", "op_weight8.cu", "op_adamw8.cu"]
 HEADERS = ["common.cuh", "internal.h", "tc_common.cuh", "launch_opts.h", "handle.h", "op_common.cuh", "op_attn.cuh",
-           "op_pair.cuh"]
+           "op_pair.cuh", "op_code8.cuh"]
 MODULE_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 MODULE_PATH = os.path.join(HERE, "_torch_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -341,14 +341,50 @@ cudaError_t launch_act8_wgrad_join(const WgradParams& p, int sms, cudaStream_t s
 cudaError_t launch_pad_rows(const __nv_bfloat16* src, long long lds, __nv_bfloat16* dst, long long ldd, long long rows,
                             int cols, int sms, cudaStream_t s);
 
+// ------------------------------------------------- weights in 8 bits
+struct Weight8Params {
+  const void* w;           // store: [out][cols], row stride ldw; restore: written
+  uint8_t* codes;          // [out][cols], row stride ldc bytes
+  uint8_t* codes_t;        // [cols][out], row stride ldt bytes, or nullptr
+  uint8_t* scales;         // a byte a 128 x 128 block, at column block * lds + row block * lds_row (store: * 1)
+  long long ldw, ldc, ldt, lds, lds_row;
+  long long out, cols;
+  int dtype;
+};
+cudaError_t launch_weight8(const Weight8Params& p, bool store, cudaStream_t s);
+
+// ------------------------------------------- AdamW with states in 8 bits
+struct Adamw8Tensor {
+  void* p;                 // parameter; restore: the average's values
+  const void* g;           // gradient; restore: the root's values, written
+  uint8_t *m, *r;          // codes of the average and of the root
+  uint8_t *ms, *rs;        // their scales, a byte for 128 elements
+  long long numel;
+  uint32_t chunk0;         // set by the launcher
+  int vec;                 // every pointer but the scales' is 16-byte aligned
+};
+constexpr int kAdamw8Tensors = 112;      // of a launch: its parameters are kept below 8 KB
+struct Adamw8Params {
+  int n, pdtype, gdtype;   // (restore: pdtype is the values' type)
+  uint32_t salt;
+  float omb1, omb2;        // 1 - beta
+  float eps, decay, size;  // as AdamParams
+  Adamw8Tensor t[kAdamw8Tensors];
+};
+cudaError_t launch_adamw8(Adamw8Params& p, cudaStream_t s);
+cudaError_t launch_adamw8_restore(Adamw8Params& p, cudaStream_t s);
+
 // ------------------------------------- products by expert and in 8 bits
-enum ProductKind : int { PRODUCT_FORWARD = 0, PRODUCT_INPUT = 1, PRODUCT_WEIGHT = 2 };
+enum ProductKind : int { PRODUCT_FORWARD = 0, PRODUCT_INPUT = 1, PRODUCT_WEIGHT = 2, PRODUCT_ACT8 = 3 };
 constexpr int kMaxExperts = 1024;
 struct ProductParams {
   const int* offsets;      // [groups + 1] on the token axis, or nullptr (one group of all tokens)
   const void* add;         // weight: [groups][n][m] of odtype, or nullptr
   void* out;               // tokens: [tokens][m]; weight: [groups][n][m]; of odtype
   long long ldo, out_group, ldadd, add_group;   // row and group strides in elements
+  const uint8_t* scales;   // 8 bits: a byte a token and 128 columns, [blocks] rows lds apart
+  const uint8_t* wscales;  // a byte a 128 x 128 block of W, at column block * ws_col + row block * ws_row
+  long long lds, ws_col, ws_row;
   float* part;             // weight: scratch of product_part_bytes
   int kind;                // ProductKind
   int tokens, groups;
@@ -361,7 +397,7 @@ struct ProductParams {
   unsigned long long timeout_ns;
 };
 // maps, 3-D with 128-byte swizzle: A and B (see op_product.cu).  K-major: {k, rows, groups or 1} in boxes of 64 k and 128
-// rows (A) or 32 (B); MN-major: {rows, k, groups or 1} in boxes of 64 rows and 64 k.
+// rows (A) or 32 (B) (8 bits: of 128 k); MN-major: {rows, k, groups or 1} in boxes of 64 rows and 64 k.
 uint64_t product_part_bytes(int64_t tokens, int sms);
 cudaError_t launch_product(const ProductParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s);
 

@@ -16,10 +16,9 @@
 // the rows' scale bytes at once (scales lie block column by block column,
 // one byte a row, as the weight-gradient kernel reads them).  Measured at
 // 16384 x 14336 bf16: stored in 119 us (5.9 TB/s), restored in 106 us (6.6).
-#include <cuda_fp8.h>
-
 #include "common.cuh"
 #include "internal.h"
+#include "op_code8.cuh"
 #include "op_common.cuh"
 
 namespace muon {
@@ -28,15 +27,6 @@ namespace {
 constexpr int ABLK = 128;       // columns of a block
 constexpr int AROWS = 16;       // rows of a warp's work item
 constexpr int AWARPS = 8;
-
-// The scale byte of a block with largest magnitude a (finite, >= 0).
-__device__ __forceinline__ int scale_byte(float a) {
-  // a = m 2^k, 1 <= m < 2 (a below the normal range: k <= -127, clamped)
-  const int bits = __float_as_int(a);
-  const int k = (bits >> 23) - 127;
-  const int e = (bits & 0x7FFFFF) <= 0x600000 ? k - 8 : k - 7;   // 448 = 1.75 * 2^8
-  return max(e + 127, 16);
-}
 
 // Eight consecutive values of a row from column c, as loaded: zeros past the
 // last column and past the last row.
@@ -89,23 +79,6 @@ struct Eight {
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x4(const float* f) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
-}
-
-// The four values of a word of codes, each times `unit`.
-__device__ __forceinline__ void e4m3x4_values(uint32_t w, float unit, float* f) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * k)), __NV_E4M3));
-    const float2 v = __half22float2(h);
-    f[2 * k] = v.x * unit;
-    f[2 * k + 1] = v.y * unit;
-  }
-}
-
 // A warp takes AROWS rows of one block column, two rows at a time, with the
 // loads of AHEAD row pairs in flight: 2 pairs took 132 us, 4 119 us, 8 (with
 // fewer warps on an SM) 126 us at 16384 x 14336.  The instructions count as
@@ -136,7 +109,7 @@ __global__ void __launch_bounds__(AWARPS * 32, VEC && sizeof(T) == 2 ? 6 : 4) ac
       const long long r = r0 + i + half;
       const int top = in[j].block_top();
       const bool fine = top < 0x7F800000;
-      const int e = fine ? scale_byte(__int_as_float(top)) : 255;
+      const int e = fine ? e4m3_scale_byte(top) : 255;
       const float unit = __int_as_float((254 - e) << 23);       // 2^-(e - 127)
       float f[8];
       in[j].get(f);

@@ -1,0 +1,267 @@
+// AdamW over many tensors whose states are kept in 8 bits.
+//
+// A tensor is cut into blocks of 128 elements.  The average m of the gradients
+// is kept as e4m3 codes of m 2^-e, e the smallest integer >= -111 with which
+// the block's largest magnitude is 448 or less; e + 127 in a byte.  Of the
+// average v of their squares the root r is kept, which has half of v's range
+// in powers of two, as codes without a sign: code c > 0 stands for
+//   (1 + (c & 15) / 16) 2^((c >> 4) - 8),  up to 248,  times 2^e,
+// 0 for 0: 16 binades in steps of 1/16 (v itself: 32 binades).  A root that is
+// not 0 gets code 1 at least, since the step divides by it.
+//
+// Rounding.  An average moves by (1 - beta) of the difference, often less than
+// half a step of its codes: rounded to nearest it would never move.  So a
+// value is rounded up where its part past a code plus a number in [0, 1) is 1
+// or more, which keeps it right on average.  The number of element i is
+// (b + 1/2) / 256, b the byte i % 4 of a 32-bit hash of i / 4 and the seed (the
+// finalizer that C. Wellons published as lowbias32): the same call gives the
+// same result.  Both states of an element use one number: errors of one sign
+// in m and r cancel in part in m / r.
+//
+// The step is as adamw_kernel's, on the states' values in fp32:
+//   m <- m + (1 - beta1)(g - m);  v <- r^2 + (1 - beta2)(g^2 - r^2);  r = v^(1/2)
+//   p <- p decay - size m / (eps + r)
+// and only then are m and r rounded to codes.
+//
+// Bound by HBM: 10 bytes an element with bf16 parameters and gradients (fp32
+// states: 22).  A thread has 16 elements, 8 lanes a block.
+#include "common.cuh"
+#include "internal.h"
+#include "op_code8.cuh"
+#include "op_common.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int A8_THREADS = 256, A8_EACH = 16, A8_CHUNK = A8_THREADS * A8_EACH;
+
+__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7FEB352Du;
+  x ^= x >> 15;
+  x *= 0x846CA68Bu;
+  return x ^ (x >> 16);
+}
+
+// The scale byte of roots whose largest has these fp32 bits.
+__device__ __forceinline__ int root_scale_byte(int bits) {
+  const int k = (bits >> 23) - 127;
+  const int e = (bits & 0x7FFFFF) <= 0x780000 ? k - 7 : k - 6;   // 248 = 1.9375 * 2^7
+  return max(e + 127, 16);
+}
+
+// The value of a root's code, before its scale.
+__device__ __forceinline__ float root_value(uint32_t c) { return c == 0u ? 0.f : __uint_as_float((c << 19) + (119u << 23)); }
+
+// 16 elements of type T from `i`; of the tensor's n elements where not VEC.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load16(const void* base, long long i, long long n, float* f) {
+  const T* from = static_cast<const T*>(base) + i;
+  if constexpr (VEC) {
+    constexpr int kStep = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int k = 0; k < 16; k += kStep) unpack16<T>(*reinterpret_cast<const uint4*>(from + k), f + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) f[k] = i + k < n ? to_f32(from[k]) : 0.f;
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store16(void* base, long long i, long long n, const float* f) {
+  T* to = static_cast<T*>(base) + i;
+  if constexpr (VEC) {
+    constexpr int kStep = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int k = 0; k < 16; k += kStep) *reinterpret_cast<uint4*>(to + k) = pack16<T>(f + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (i + k < n) to[k] = from_f32<T>(f[k]);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_codes(const uint8_t* base, long long i, long long n, uint32_t* w) {
+  if constexpr (VEC) {
+    const uint4 v = *reinterpret_cast<const uint4*>(base + i);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint32_t b = i + k < n ? base[i + k] : 0u;
+      w[k >> 2] = (k & 3) == 0 ? b : w[k >> 2] | (b << (8 * (k & 3)));
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* base, long long i, long long n, const uint32_t* w) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uint4*>(base + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (i + k < n) base[i + k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
+  }
+}
+
+__device__ __forceinline__ int block_max(int v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+template <typename TP, typename TG, bool VEC>
+__device__ __forceinline__ void step16(const Adamw8Params& p, const Adamw8Tensor& t, long long i) {
+  const long long n = t.numel, blk = i >> 7;
+  // lanes past the end stay for the block's maxima
+  const bool in = i < n;
+  const long long at = VEC || in ? i : 0, end = VEC ? n : in ? n : 0;
+  float g[16], w[16], m[16], r[16];
+  uint32_t mc[4], rc[4];
+  load16<TG, VEC>(t.g, at, end, g);
+  load16<TP, VEC>(t.p, at, end, w);
+  load_codes<VEC>(t.m, at, end, mc);
+  load_codes<VEC>(t.r, at, end, rc);
+  const float mu = __int_as_float(in ? t.ms[blk] << 23 : 0), ru = __int_as_float(in ? t.rs[blk] << 23 : 0);
+  int mtop = 0, rtop = 0;
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    e4m3x4_values(mc[k >> 2], mu, m + k);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int j = k + q;
+      const float root = root_value((rc[k >> 2] >> (8 * q)) & 255u) * ru, sq = root * root;
+      m[j] = fmaf(p.omb1, g[j] - m[j], m[j]);
+      const float v = fmaf(p.omb2, fmaf(g[j], g[j], -sq), sq);
+      asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j]) : "f"(v));
+      w[j] = fmaf(w[j], p.decay, -p.size * __fdividef(m[j], p.eps + r[j]));
+      mtop = max(mtop, __float_as_int(m[j]) & 0x7FFFFFFF);
+      rtop = max(rtop, __float_as_int(r[j]) & 0x7FFFFFFF);
+    }
+  }
+  store16<TP, VEC>(t.p, at, end, w);
+  mtop = block_max(mtop);
+  rtop = block_max(rtop);
+  const bool mfine = mtop < 0x7F800000, rfine = rtop < 0x7F800000;
+  const int me = mfine ? e4m3_scale_byte(mtop) : 255, re = rfine ? root_scale_byte(rtop) : 255;
+  const float mi = __int_as_float((254 - me) << 23), ri = __int_as_float((254 - re) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t h = hash32(static_cast<uint32_t>(i >> 2) + k + p.salt);
+    uint32_t mw = 0u, rw = 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int j = 4 * k + q;
+      const uint32_t byte = (h >> (8 * q)) & 255u;
+      float y = fabsf(m[j]) * mi;
+      const bool low = y < 0.015625f;              // 2^-6: steps of 2^-9 below
+      y = low ? y + 0.015625f : y;
+      const uint32_t c = (__float_as_uint(y) + (byte << 12) + 0x800u) >> 20;
+      mw |= (min(c - (low ? 968u : 960u), 0x7Eu) | (__float_as_uint(m[j]) >> 31 << 7)) << (8 * q);
+      const float z = r[j] * ri;
+      const int d = static_cast<int>((__float_as_uint(z) + (byte << 11) + 0x400u) >> 19) - 1904;
+      rw |= (z > 0.f ? static_cast<uint32_t>(min(max(d, 1), 255)) : 0u) << (8 * q);
+    }
+    mc[k] = mfine ? mw : 0u;
+    rc[k] = rfine ? rw : 0u;
+  }
+  store_codes<VEC>(t.m, at, end, mc);
+  store_codes<VEC>(t.r, at, end, rc);
+  if ((threadIdx.x & 7) == 0 && in) {
+    t.ms[blk] = static_cast<uint8_t>(me);
+    t.rs[blk] = static_cast<uint8_t>(re);
+  }
+}
+
+// The tensor that the CTA's chunk belongs to.
+__device__ __forceinline__ int tensor_of(const Adamw8Params& p, uint32_t chunk) {
+  int lo = 0, hi = p.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.t[mid].chunk0 <= chunk)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename TP, typename TG>
+__global__ void __launch_bounds__(A8_THREADS) adamw8_kernel(const __grid_constant__ Adamw8Params p) {
+  const Adamw8Tensor& t = p.t[tensor_of(p, blockIdx.x)];
+  const long long i0 = static_cast<long long>(blockIdx.x - t.chunk0) * A8_CHUNK, i = i0 + threadIdx.x * A8_EACH;
+  if (t.vec && i0 + A8_CHUNK <= t.numel)
+    step16<TP, TG, true>(p, t, i);
+  else
+    step16<TP, TG, false>(p, t, i);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(A8_THREADS) adamw8_restore_kernel(const __grid_constant__ Adamw8Params p) {
+  const Adamw8Tensor& t = p.t[tensor_of(p, blockIdx.x)];
+  const long long n = t.numel, i = static_cast<long long>(blockIdx.x - t.chunk0) * A8_CHUNK + threadIdx.x * A8_EACH;
+  if (i >= n) return;
+  const float mu = __int_as_float(t.ms[i >> 7] << 23), ru = __int_as_float(t.rs[i >> 7] << 23);
+  const bool vec = t.vec && i + A8_EACH <= n;
+  uint32_t mc[4], rc[4];
+  float f[16];
+  if (vec) {
+    load_codes<true>(t.m, i, n, mc);
+    load_codes<true>(t.r, i, n, rc);
+  } else {
+    load_codes<false>(t.m, i, n, mc);
+    load_codes<false>(t.r, i, n, rc);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) e4m3x4_values(mc[k], mu, f + 4 * k);
+  if (vec)
+    store16<T, true>(t.p, i, n, f);
+  else
+    store16<T, false>(t.p, i, n, f);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) f[k] = root_value((rc[k >> 2] >> (8 * (k & 3))) & 255u) * ru;
+  if (vec)
+    store16<T, true>(const_cast<void*>(t.g), i, n, f);
+  else
+    store16<T, false>(const_cast<void*>(t.g), i, n, f);
+}
+
+}  // namespace
+
+// Numbers the chunks of q.t[0 .. n - 1]; the number of all.
+static long long number_chunks(Adamw8Params& q) {
+  long long chunks = 0;
+  for (int i = 0; i < q.n; ++i) {
+    q.t[i].chunk0 = static_cast<uint32_t>(chunks);
+    chunks += (q.t[i].numel + A8_CHUNK - 1) / A8_CHUNK;
+  }
+  return chunks;
+}
+
+cudaError_t launch_adamw8(Adamw8Params& q, cudaStream_t s) {
+  const long long chunks = number_chunks(q);
+  if (chunks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(chunks));
+  const bool pb = q.pdtype == DT_BF16, gb = q.gdtype == DT_BF16;
+  if (pb && gb)
+    adamw8_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, A8_THREADS, 0, s>>>(q);
+  else if (pb)
+    adamw8_kernel<__nv_bfloat16, float><<<grid, A8_THREADS, 0, s>>>(q);
+  else if (gb)
+    adamw8_kernel<float, __nv_bfloat16><<<grid, A8_THREADS, 0, s>>>(q);
+  else
+    adamw8_kernel<float, float><<<grid, A8_THREADS, 0, s>>>(q);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adamw8_restore(Adamw8Params& q, cudaStream_t s) {
+  const long long chunks = number_chunks(q);
+  if (chunks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(chunks));
+  if (q.pdtype == DT_BF16)
+    adamw8_restore_kernel<__nv_bfloat16><<<grid, A8_THREADS, 0, s>>>(q);
+  else
+    adamw8_restore_kernel<float><<<grid, A8_THREADS, 0, s>>>(q);
+  return cudaGetLastError();
+}
+
+}  // namespace muon

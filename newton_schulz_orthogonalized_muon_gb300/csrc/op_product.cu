@@ -50,17 +50,25 @@ struct Traits {
   static constexpr bool kTokens = KIND != PRODUCT_WEIGHT;                   // n are tokens
   static constexpr bool kAmn = KIND == PRODUCT_INPUT || KIND == PRODUCT_WEIGHT;   // A is read MN-major
   static constexpr bool kBmn = KIND == PRODUCT_WEIGHT;
-  static constexpr int BK = 64;
-  static constexpr int EPI_WARP0 = 4;
+  static constexpr bool k8 = KIND == PRODUCT_ACT8;
+  static constexpr int BK = k8 ? 128 : 64;                                  // 128 bytes
+  static constexpr int EPI_WARP0 = k8 ? 8 : 4;
   static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-  static constexpr int NT = 256;                                            // most n of a tile
+  // most n of a tile: two accumulators and, for 8 bits, the scales share 512 columns of TMEM
+  static constexpr int NT = k8 ? 224 : 256;
 };
+// The scales in TMEM, by groups of four 128-column blocks: a 32-bit word a row
+// of A (4 columns of 32 lanes) and of B (8), a byte for each block.
+constexpr int SF_SLOTS = 5, SF_COLS = 12;
+static_assert(2 * Traits<PRODUCT_ACT8>::NT + SF_SLOTS * SF_COLS <= 512, "TMEM");
 
 struct alignas(16) Bars {
   uint64_t full[STAGES];                 // the leader's, for both CTAs
   uint64_t empty[STAGES];                // each CTA's own
   uint64_t own[STAGES];                  // weight: this CTA's part of an expert's last step
   uint64_t tfull[2], tempty[2];
+  uint64_t sf_full[SF_SLOTS];            // 8 bits: the leader's, scales written by both CTAs
+  uint64_t sf_empty[SF_SLOTS];
   uint64_t drain;
   uint4 token[2];                        // sent, received (see send_token)
   uint32_t tmem;
@@ -176,6 +184,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Scales of a group of blocks to the 32 TMEM lanes of a warp.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr), "r"(w) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Pair product of e4m3 codes; the scales' columns, a power of two a row and 32 k.
+__device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb,
+                                                uint32_t acc) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p, q;\n"
+      " elect.sync _|q, 0xffffffff;\n"
+      " setp.ne.b32 p, %6, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(acc)
+      : "memory");
 }
 
 __device__ __forceinline__ void store_any(void* base, long long i, int dtype, float v) {
@@ -299,6 +332,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       mbar_init(&bar->tfull[a], 1);
       mbar_init(&bar->tempty[a], 2 * EPI_WARPS);
     }
+    for (int s = 0; s < SF_SLOTS; ++s) {
+      mbar_init(&bar->sf_full[s], 8);
+      mbar_init(&bar->sf_empty[s], 1);
+    }
     mbar_init(&bar->drain, 1);
     bar->token[0] = make_uint4(0u, 0u, 0u, 0u);
     bar->abort = (sb & 1023u) != 0u ? 1 : 0;       // the swizzled boxes need 1 KB boundaries
@@ -349,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
             if (rank == 0) mbar_arrive(&bar->full[r.s]);
           }
           if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], 2 * bytes);
-          if constexpr (KIND == PRODUCT_FORWARD) {
-            tma_load_3d_pair(a, &ma, fb, k * 64, m0, t.e);
+          if constexpr (KIND == PRODUCT_FORWARD || KIND == PRODUCT_ACT8) {
+            tma_load_3d_pair(a, &ma, fb, k * T::BK, m0, t.e);
           } else if constexpr (KIND == PRODUCT_INPUT) {
             tma_load_3d_pair(a, &ma, fb, m0, k * 64, t.e);
             tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, k * 64, t.e);
@@ -362,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
             if constexpr (T::kBmn)
               tma_load_3d_pair(b + c * BOX, &mb, fb, n0 + c * 64, t.t0 + k * 64, 0);
             else
-              tma_load_3d_pair(b + c * (BOX / 2), &mb, fb, k * 64, n0 + c * 32, 0);
+              tma_load_3d_pair(b + c * (BOX / 2), &mb, fb, k * T::BK, n0 + c * 32, 0);
           }
           r.next();
         }
@@ -372,8 +409,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
   } else if (warp == 1) {
     if (rank == 0) {
       // --------------------------------------------------------- products
-      const uint32_t type = p.f16 ? 0u : (1u << 7) | (1u << 10);
-      const uint32_t id0 = (1u << 4) | type | (T::kAmn ? 1u << 15 : 0u) | (T::kBmn ? 1u << 16 : 0u) | ((MT >> 4) << 24);
+      // 16 bits: fp32 results, operands bf16 or fp16.  8 bits: e4m3, scales 2^(byte - 127), the byte of a word at 4 (B)
+      // and 29 (A)
+      const uint32_t type = T::k8 ? 1u << 23 : (1u << 4) | (p.f16 ? 0u : (1u << 7) | (1u << 10));
+      const uint32_t id0 = type | (T::kAmn ? 1u << 15 : 0u) | (T::kBmn ? 1u << 16 : 0u) | ((MT >> 4) << 24);
+      Ring<SF_SLOTS> rs;
       Ring<STAGES> r;
       int acc = 0;
       uint32_t acc_ph = 0;
@@ -386,22 +426,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           ok = wait_warp<0, true>(&bar->tempty[acc], acc_ph ^ 1u, abort, p);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tmem + acc * 256;
+          const uint32_t d = tmem + acc * T::NT;
           const int k1 = min(k0 + part, t.steps);
           for (int k = k0; k < k1; ++k) {
             ok = wait_warp<0, KIND == PRODUCT_WEIGHT>(&bar->full[r.s], r.ph, abort, p);
             if (!ok) break;
+            if constexpr (T::k8) {
+              if ((k & 3) == 0) ok = wait_warp<0, true>(&bar->sf_full[rs.s], rs.ph, abort, p);
+              if (!ok) break;
+            }
             tc_fence_after();
             const uint32_t sa = sb + r.s * STAGE;
             const uint64_t a = T::kAmn ? sdesc_sw128(sa, BOX, 1024) : sdesc_sw128(sa, 16, 1024);
             const uint64_t b = T::kBmn ? sdesc_sw128(sa + 2 * BOX, BOX, 1024) : sdesc_sw128(sa + 2 * BOX, 16, 1024);
             // steps of 16 k: two rows of 8 in an MN-major operand, 32 bytes of a K-major one
             const int kks = KIND == PRODUCT_WEIGHT ? (min(t.len - k * 64, 64) + 15) / 16 : 4;
+            if constexpr (T::k8) {
+              const uint32_t sf = tmem + 2 * T::NT + rs.s * SF_COLS, ids = id | ((k & 3u) << 4) | ((k & 3u) << 29);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < kks)
-                mma_pair(d, a + kk * (T::kAmn ? 2048 >> 4 : 2), b + kk * (T::kBmn ? 2048 >> 4 : 2), id,
-                         kk != 0 || k != k0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_pair_scaled(d, a + kk * 2, b + kk * 2, ids, sf, sf + 4, kk != 0 || k != k0 ? 1u : 0u);
+              if ((k & 3) == 3 || k == k1 - 1) {
+                commit_pair(&bar->sf_empty[rs.s], 0x3);
+                rs.next();
+              }
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (kk < kks)
+                  mma_pair(d, a + kk * (T::kAmn ? 2048 >> 4 : 2), b + kk * (T::kBmn ? 2048 >> 4 : 2), id,
+                           kk != 0 || k != k0 ? 1u : 0u);
+            }
             commit_pair(&bar->empty[r.s], 0x3);
             r.next();
           }
@@ -452,6 +507,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         s = (s + 1) % STAGES;
       }
     }
+  } else if (T::k8 && warp >= 4 && warp < T::EPI_WARP0) {
+    if constexpr (T::k8) {
+      // Scales, four blocks at a time, to this warp's lanes: each row of 32
+      // lanes of TMEM holds all of them.  The product reads its CTA's own copy,
+      // of all n.  Blocks and tokens that are not there get 2^0: their codes
+      // are zeros (an infinity or NaN times them would not be).
+      const uint32_t lead = mapa_shared(smem_u32(&bar->sf_full[0]), 0);
+      const uint32_t at0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * T::NT;
+      Ring<SF_SLOTS> rs;
+      bool ok = true;
+      for (int i = pair; ok && i < tiles.total; i += npairs) {
+        const Tile t = tiles.get(i);
+        const int m0 = t.m0 + static_cast<int>(rank) * 128;
+        const uint8_t* ws = p.wscales + (m0 >> 7) * p.ws_row;
+        for (int k0 = 0; k0 < t.steps; k0 += 4) {
+          uint32_t wa = 0u, wb[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) wb[c] = 0u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int k = k0 + q;
+            const bool in = k < t.steps;
+            wa |= static_cast<uint32_t>(in && m0 < p.m ? ws[k * p.ws_col] : 127) << (8 * q);
+            const uint8_t* xs = p.scales + k * p.lds + t.n0 + lane;
+#pragma unroll
+            for (int c = 0; c < 7; ++c)
+              wb[c] |= static_cast<uint32_t>(in && c * 32 + lane < t.n ? xs[c * 32] : 127) << (8 * q);
+          }
+          ok = wait_warp(&bar->sf_empty[rs.s], rs.ph ^ 1u, abort, p);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st4(at0 + rs.s * SF_COLS, wa);
+          tmem_st8(at0 + rs.s * SF_COLS + 4, wb);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead + rs.s * 8);
+          rs.next();
+        }
+      }
+    }
   } else if (warp >= T::EPI_WARP0) {
     // ----------------------------------------------------------- epilogue
     const int ew = warp - T::EPI_WARP0, quad = warp & 3, half = ew >> 2;
@@ -469,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         ok = wait_warp<100>(&bar->tfull[acc], acc_ph, abort, p);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256;
+        const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::NT;
         for (int c = half * 32; c < t.n; c += 64) {
           float v[32];
           tmem_ld32(from + c, v);
@@ -498,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
             if (!ok) break;
             tc_fence_after();
           }
-          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256;
+          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::NT;
 #pragma unroll 1
           for (int c = half * 32; c < t.n; c += 64) {
             float v[32];
@@ -582,6 +678,7 @@ cudaError_t launch_product(const ProductParams& q, const CUtensorMap* maps, int 
   p.vec = fits(p.out, p.ldo, p.out_group) && (p.add == nullptr || fits(p.add, p.ldadd, p.add_group)) && p.m % 8 == 0;
   switch (p.kind) {
     case PRODUCT_FORWARD: return launch_kind<PRODUCT_FORWARD>(p, maps, pairs, s);
+    case PRODUCT_ACT8: return launch_kind<PRODUCT_ACT8>(p, maps, pairs, s);
     case PRODUCT_INPUT: return launch_kind<PRODUCT_INPUT>(p, maps, pairs, s);
     default: return launch_kind<PRODUCT_WEIGHT>(p, maps, pairs, s);
   }

@@ -3,6 +3,8 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "common.cuh"
 #include "handle.h"
@@ -215,6 +217,66 @@ muon_status_t check_experts(muon_handle_t h, const int32_t* offsets, int64_t tok
              "cols and out must be multiples of 8 in [8, 2^20]");
   MUON_CHECK(experts >= 1 && experts <= kMaxExperts, "experts must be in [1, 1024]");
   MUON_CHECK(offsets != nullptr && aligned(offsets, 4), "offsets is NULL or not aligned");
+  return MUON_OK;
+}
+
+// Map of codes [rows][cols] in boxes of 128 columns and `box` rows.
+bool codes_map(muon_handle_t h, CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows)};
+  cuuint32_t boxes[3] = {128, box, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+muon_status_t check_weight8(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t out, int64_t cols) {
+  MUON_CHECK(out >= 0 && out <= kMaxTokens && cols >= 0 && cols <= kMaxTokens, "negative or oversized shape");
+  if (out == 0 || cols == 0) return MUON_OK;
+  MUON_CHECK(codes != nullptr && scales != nullptr, "codes or scales is NULL");
+  MUON_CHECK(ldc % 128 == 0 && ldc >= cols && aligned(codes, 16),
+             "codes need a row stride that is a multiple of 128 and a 16-byte aligned start");
+  return MUON_OK;
+}
+
+// Some two of the tensors share memory that is written.
+bool share_memory(std::vector<std::pair<uintptr_t, uintptr_t>>& spans) {
+  std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].first < spans[i - 1].second) return true;
+  return false;
+}
+
+// Checks the tensors and launches them, at most kAdamw8Tensors at a time, those
+// of one pair of types together.
+template <typename Launch, typename Fill>
+muon_status_t adamw8_launches(muon_handle_t h, const muon_adamw8_t* tensors, int32_t n, Adamw8Params& p, const char* what,
+                              cudaStream_t stream, Launch&& launch, Fill&& fill) {
+  for (int types = 0; types < 4; ++types) {
+    p.pdtype = types & 1;
+    p.gdtype = types >> 1;
+    p.n = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      const muon_adamw8_t& t = tensors[i];
+      if (t.numel > 0) fill(i, t);
+      if (p.n == kAdamw8Tensors || (i == n - 1 && p.n > 0)) {
+        MUON_LAUNCH(MUON_K_ADAMW, launch(p, stream), what);
+        p.n = 0;
+      }
+    }
+  }
+  return MUON_OK;
+}
+
+muon_status_t check_adamw8(muon_handle_t h, const muon_adamw8_t* tensors, int32_t n) {
+  MUON_CHECK(n >= 0 && (n == 0 || tensors != nullptr), "n is negative or tensors is NULL");
+  for (int32_t i = 0; i < n; ++i) {
+    const muon_adamw8_t& t = tensors[i];
+    MUON_CHECK(t.numel >= 0 && t.numel <= (int64_t(1) << 40), "negative or oversized numel");
+    MUON_CHECK(t.numel == 0 || (t.avg != nullptr && t.root != nullptr && t.avg_scale != nullptr && t.root_scale != nullptr),
+               "NULL state pointer");
+  }
   return MUON_OK;
 }
 
@@ -641,6 +703,168 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms / 2, stream), "experts' weight gradient launch");
     return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_store_weight(muon_handle_t h, const void* w, int64_t ldw, uint8_t* codes, int64_t ldc,
+                                     uint8_t* codes_t, int64_t ldt, uint8_t* scales, int64_t lds, int64_t out,
+                                     int64_t cols, int32_t dtype, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
+    const muon_status_t st = check_weight8(h, codes, ldc, scales, out, cols);
+    if (st != MUON_OK) return st;
+    if (out == 0 || cols == 0) return MUON_OK;
+    MUON_CHECK(codes_t == nullptr || (ldt % 128 == 0 && ldt >= out && aligned(codes_t, 16)),
+               "codes_t needs a row stride that is a multiple of 128 and a 16-byte aligned start");
+    MUON_CHECK(lds >= (out + 127) / 128, "the scales' row stride is too small");
+    MUON_CHECK(w != nullptr && (ldw >= cols || out == 1), "w is NULL or its row stride is below cols");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    const Weight8Params p{w, codes, codes_t, scales, ldw, ldc, ldt, lds, 1, out, cols, dtype};
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_ACT8, launch_weight8(p, true, stream), "weight store launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_restore_weight(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales,
+                                       int64_t s_col, int64_t s_row, void* w, int64_t ldw, int64_t out, int64_t cols,
+                                       int32_t dtype, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    MUON_CHECK(op_dtype(dtype), "dtype must be MUON_F32, MUON_BF16 or MUON_F16");
+    const muon_status_t st = check_weight8(h, codes, ldc, scales, out, cols);
+    if (st != MUON_OK) return st;
+    if (out == 0 || cols == 0) return MUON_OK;
+    MUON_CHECK(s_col >= 0 && s_row >= 0, "negative scale stride");
+    MUON_CHECK(w != nullptr && (ldw >= cols || out == 1), "w is NULL or its row stride is below cols");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    const Weight8Params p{w, const_cast<uint8_t*>(codes), nullptr, const_cast<uint8_t*>(scales), ldw, ldc, 0, s_col, s_row,
+                          out, cols, dtype};
+    h->prof_tag = -1;
+    MUON_LAUNCH(MUON_K_ACT8, launch_weight8(p, false, stream), "weight restore launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                               const uint8_t* wcodes, int64_t ldw, const uint8_t* wscales, int64_t s_col,
+                               int64_t s_row, void* y, int64_t ldy, int64_t rows, int64_t cols, int64_t out,
+                               int32_t odtype, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    MUON_CHECK(op_dtype(odtype), "odtype must be MUON_F32, MUON_BF16 or MUON_F16");
+    muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
+    if (st == MUON_OK) st = check_weight8(h, wcodes, ldw, wscales, out, cols);
+    if (st != MUON_OK) return st;
+    if (rows == 0 || out == 0) return MUON_OK;
+    MUON_CHECK(s_col >= 0 && s_row >= 0, "negative scale stride");
+    MUON_CHECK(y != nullptr && aligned(y, odtype == MUON_F32 ? 4 : 2) && (ldy >= out || rows == 1),
+               "y is NULL, not aligned or its row stride is below out");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    if (cols == 0) {
+      const size_t es = odtype == MUON_F32 ? 4 : 2;
+      MUON_CUDA_TRY(cudaMemset2DAsync(y, static_cast<size_t>(std::max(ldy, out)) * es, 0, static_cast<size_t>(out) * es,
+                                      static_cast<size_t>(rows), stream), "zeros");
+      return MUON_OK;
+    }
+    ProductParams p{};
+    p.kind = PRODUCT_ACT8;
+    p.out = y;
+    p.ldo = ldy;
+    p.scales = scales;
+    p.lds = lds;
+    p.wscales = wscales;
+    p.ws_col = s_col;
+    p.ws_row = s_row;
+    p.tokens = static_cast<int>(rows);
+    p.groups = 1;
+    p.m = static_cast<int>(out);
+    p.k = static_cast<int>(cols);
+    p.odtype = odtype;
+    p.err = h->err;
+    p.timeout_ns = h->timeout_ns;
+    h->prof_tag = -1;
+    CUtensorMap maps[2] = {};
+    if (!codes_map(h, &maps[0], wcodes, cols, out, ldw, 128) || !codes_map(h, &maps[1], codes, cols, rows, ldc, 32))
+      return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
+    MUON_LAUNCH(MUON_K_MATMUL8, launch_product(p, maps, h->num_sms / 2, stream), "8-bit product launch");
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, int32_t n, int64_t step, uint32_t seed,
+                               float lr, float beta1, float beta2, float eps, float wd, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    const muon_status_t st = check_adamw8(h, tensors, n);
+    if (st != MUON_OK) return st;
+    MUON_CHECK(step >= 1, "step counts from 1");
+    MUON_CHECK(beta1 >= 0.f && beta1 < 1.f && beta2 >= 0.f && beta2 < 1.f && std::isfinite(lr) && std::isfinite(eps) &&
+                   std::isfinite(wd), "bad hyper-parameter");
+    std::vector<std::pair<uintptr_t, uintptr_t>> written;
+    written.reserve(5 * static_cast<size_t>(n));
+    for (int32_t i = 0; i < n; ++i) {
+      const muon_adamw8_t& t = tensors[i];
+      if (t.numel == 0) continue;
+      MUON_CHECK(t.param != nullptr && t.grad != nullptr, "NULL tensor pointer");
+      MUON_CHECK((t.param_dtype == MUON_F32 || t.param_dtype == MUON_BF16) &&
+                     (t.grad_dtype == MUON_F32 || t.grad_dtype == MUON_BF16), "bad dtype");
+      const uintptr_t blocks = static_cast<uintptr_t>((t.numel + 127) / 128), k = static_cast<uintptr_t>(t.numel);
+      auto add = [&](const void* q, uintptr_t bytes) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q);
+        written.emplace_back(a, a + bytes);
+      };
+      add(t.param, k * (t.param_dtype == MUON_F32 ? 4 : 2));
+      add(t.avg, k);
+      add(t.root, k);
+      add(t.avg_scale, blocks);
+      add(t.root_scale, blocks);
+    }
+    MUON_CHECK(!share_memory(written), "two tensors, or their states, share memory");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    const double bc1 = 1.0 - std::pow(static_cast<double>(beta1), static_cast<double>(step));
+    const double bc2 = 1.0 - std::pow(static_cast<double>(beta2), static_cast<double>(step));
+    Adamw8Params p{};
+    p.salt = seed * 0x9E3779B1u;
+    p.omb1 = 1.f - beta1;
+    p.omb2 = 1.f - beta2;
+    p.eps = eps;
+    p.decay = static_cast<float>(1.0 - static_cast<double>(lr) * wd);
+    p.size = static_cast<float>(static_cast<double>(lr) * std::sqrt(bc2) / bc1);
+    h->prof_tag = -1;
+    return adamw8_launches(h, tensors, n, p, "adamw8 launch", stream, launch_adamw8, [&](int32_t, const muon_adamw8_t& t) {
+      if (t.param_dtype != p.pdtype || t.grad_dtype != p.gdtype) return;
+      const int vec = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.avg, 16) && aligned(t.root, 16);
+      p.t[p.n++] = Adamw8Tensor{t.param, t.grad, t.avg, t.root, t.avg_scale, t.root_scale, t.numel, 0, vec};
+    });
+  });
+}
+
+muon_status_t muon_adamw8_restore(muon_handle_t h, const muon_adamw8_t* tensors, void* const* avg, void* const* root,
+                                  int32_t n, int32_t dtype, void* stream_arg) {
+  if (h == nullptr) return MUON_ERR_INVALID_ARG;
+  return guarded(h, [&]() -> muon_status_t {
+    const muon_status_t st = check_adamw8(h, tensors, n);
+    if (st != MUON_OK) return st;
+    MUON_CHECK(dtype == MUON_F32 || dtype == MUON_BF16, "dtype must be MUON_F32 or MUON_BF16");
+    MUON_CHECK(n == 0 || (avg != nullptr && root != nullptr), "NULL array");
+    for (int32_t i = 0; i < n; ++i)
+      MUON_CHECK(tensors[i].numel == 0 || (avg[i] != nullptr && root[i] != nullptr), "NULL tensor pointer");
+    DeviceGuard guard(h->device);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
+    Adamw8Params p{};
+    h->prof_tag = -1;
+    return adamw8_launches(h, tensors, n, p, "adamw8 restore launch", stream, launch_adamw8_restore,
+                           [&](int32_t i, const muon_adamw8_t& t) {
+      if (p.pdtype != dtype || p.gdtype != 0) return;
+      const int vec = aligned(avg[i], 16) && aligned(root[i], 16) && aligned(t.avg, 16) && aligned(t.root, 16);
+      p.t[p.n++] = Adamw8Tensor{avg[i], root[i], t.avg, t.root, t.avg_scale, t.root_scale, t.numel, 0, vec};
+    });
   });
 }
 

@@ -21,6 +21,7 @@
 #include <new>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "muon.h"
 
@@ -629,6 +630,219 @@ PyObject* expert_weight_grad(Args a) {
   return result(st, std::move(out));
 }
 
+// --------------------------------------------------------- weights in 8 bits
+// Bytes of scales [column blocks][row blocks] for a weight [out][cols]; the
+// strides are any.
+void check_weight_scales(const at::Tensor& s, int64_t out, int64_t cols) {
+  const int64_t kb = round_up(cols, kBlock) / kBlock, ob = round_up(out, kBlock) / kBlock;
+  if (s.scalar_type() != at::kByte || s.dim() != 2 || s.size(0) != kb || s.size(1) != ob)
+    refuse("the weight's scales must be uint8 of shape (" + std::to_string(kb) + ", " + std::to_string(ob) + ")");
+}
+
+// Codes [rows][cols] as the kernels read them: rows a multiple of 128 bytes apart
+// on a 16-byte boundary.  Anything else is copied once.
+struct Codes {
+  at::Tensor t;
+  int64_t ld;
+  const uint8_t* p() const { return static_cast<const uint8_t*>(t.data_ptr()); }
+};
+
+Codes codes_of(const at::Tensor& t, const char* what) {
+  if (t.dim() != 2 || (t.scalar_type() != at::kFloat8_e4m3fn && t.scalar_type() != at::kByte))
+    refuse(std::string(what) + " must be 2-D float8_e4m3fn");
+  const int64_t rows = t.size(0), cols = t.size(1), ld = t.stride(0);
+  if ((t.stride(1) == 1 || cols == 1) && ld % kBlock == 0 && ld >= cols && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0)
+    return Codes{t, ld};
+  Codes c{padded(rows, cols, round_up(cols, kBlock), t, at::kByte), round_up(cols, kBlock)};
+  c.t.copy_(t.scalar_type() == at::kByte ? t : t.view(at::kByte));
+  return c;
+}
+
+PyObject* act8_store_weight(Args a) {
+  const Target t = a.target();
+  const at::Tensor& w = *a.tensor(t, "w");
+  const bool transposed = a.truth();
+  at::Tensor codes, scales, codes_t;
+  muon_status_t st;
+  {
+    NoGil free;
+    const int type = code(w, "w");
+    if (w.dim() != 2) refuse("w must be 2-D");
+    const Rows wr = rows_of(w, "w");
+    const int64_t out = w.size(0), cols = w.size(1), kb = round_up(cols, kBlock) / kBlock, ob = round_up(out, kBlock) / kBlock;
+    codes = padded(out, cols, kb * kBlock, w, at::kFloat8_e4m3fn);
+    scales = empty({kb, ob}, w, at::kByte);
+    if (transposed) codes_t = padded(cols, out, ob * kBlock, w, at::kFloat8_e4m3fn);
+    st = muon_act8_store_weight(t.h, wr.t.data_ptr(), wr.ld, static_cast<uint8_t*>(codes.data_ptr()), kb * kBlock,
+                                transposed ? static_cast<uint8_t*>(codes_t.data_ptr()) : nullptr, ob * kBlock,
+                                static_cast<uint8_t*>(scales.data_ptr()), ob, out, cols, type, t.stream());
+  }
+  return results(st, std::move(codes), std::move(scales), std::move(codes_t));
+}
+
+PyObject* act8_restore_weight(Args a) {
+  const Target t = a.target();
+  const at::Tensor &codes = *a.tensor(t, "codes"), &scales = *a.tensor(t, "scales");
+  const std::optional<at::ScalarType> type = a.dtype();
+  if (!type || code_of(*type) < 0) refuse("dtype must be float32, bfloat16 or float16");
+  at::Tensor w;
+  muon_status_t st;
+  {
+    NoGil free;
+    const Codes c = codes_of(codes, "codes");
+    const int64_t out = codes.size(0), cols = codes.size(1);
+    check_weight_scales(scales, out, cols);
+    w = empty({out, cols}, codes, *type);
+    st = muon_act8_restore_weight(t.h, c.p(), c.ld, static_cast<const uint8_t*>(scales.data_ptr()), scales.stride(0),
+                                  scales.stride(1), w.data_ptr(), cols, out, cols, code_of(*type), t.stream());
+  }
+  return result(st, std::move(w));
+}
+
+PyObject* act8_matmul(Args a) {
+  const Target t = a.target();
+  const at::Tensor &codes = *a.tensor(t, "codes"), &scales = *a.tensor(t, "scales"), &wcodes = *a.tensor(t, "wcodes"),
+                   &wscales = *a.tensor(t, "wscales");
+  const std::optional<at::ScalarType> type = a.dtype();
+  if (!type || code_of(*type) < 0) refuse("dtype must be float32, bfloat16 or float16");
+  at::Tensor y;
+  muon_status_t st;
+  {
+    NoGil free;
+    const Act8 x = act8_of(codes, scales);
+    const Codes w = codes_of(wcodes, "wcodes");
+    const int64_t out = wcodes.size(0), cols = wcodes.size(1);
+    if (cols != x.cols) refuse("shapes do not go together: codes " + shape(codes) + ", wcodes " + shape(wcodes));
+    check_weight_scales(wscales, out, cols);
+    y = empty({x.rows, out}, codes, *type);
+    st = muon_act8_matmul(t.h, x.code(), x.ldc, x.scale(), x.lds, w.p(), w.ld, static_cast<const uint8_t*>(wscales.data_ptr()),
+                          wscales.stride(0), wscales.stride(1), y.data_ptr(), out, x.rows, cols, out, code_of(*type), t.stream());
+  }
+  return result(st, std::move(y));
+}
+
+// ------------------------------------------------- AdamW with states in 8 bits
+// A list or tuple, held while its items are read.
+struct Items {
+  PyObject* seq;
+  Items(PyObject* o, const char* what) : seq(PySequence_Fast(o, "")) {
+    if (seq == nullptr) {
+      PyErr_Clear();
+      refuse(std::string(what) + " must be a list");
+    }
+  }
+  ~Items() { Py_DECREF(seq); }
+  Items(const Items&) = delete;
+  Items& operator=(const Items&) = delete;
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+  PyObject* at(Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+  // item i, a contiguous tensor on the target's device of one of two types
+  const at::Tensor& tensor(Py_ssize_t i, const Target& t, const std::string& what, at::ScalarType one, at::ScalarType other) const {
+    if (!THPVariable_Check(at(i))) refuse(what + " must be a CUDA tensor");
+    const at::Tensor& v = THPVariable_Unpack(at(i));
+    if (!v.is_cuda() || v.get_device() != t.dev) refuse(what + " must be a CUDA tensor on device " + std::to_string(t.dev));
+    if (!v.is_contiguous()) refuse(what + " must be contiguous");
+    if (v.scalar_type() != one && v.scalar_type() != other) refuse(what + " has a type that is not supported");
+    return v;
+  }
+};
+
+// The states' part of a tensor's entry.
+muon_adamw8_t state_of(const Target& t, PyObject* state, const std::string& what, at::Tensor* shape_of) {
+  const Items s(state, what.c_str());
+  if (s.size() != 4) refuse(what + " must be an Adamw8State");
+  const at::Tensor &avg = s.tensor(0, t, what + ".avg", at::kFloat8_e4m3fn, at::kByte),
+                   &root = s.tensor(1, t, what + ".root", at::kByte, at::kByte),
+                   &as = s.tensor(2, t, what + ".avg_scale", at::kByte, at::kByte),
+                   &rs = s.tensor(3, t, what + ".root_scale", at::kByte, at::kByte);
+  const int64_t n = avg.numel(), blocks = round_up(n, kBlock) / kBlock;
+  if (root.numel() != n || as.numel() != blocks || rs.numel() != blocks)
+    refuse(what + " needs as many roots as averages, and a scale of each for 128 of them");
+  if (shape_of != nullptr) *shape_of = avg;
+  muon_adamw8_t e{};
+  e.avg = static_cast<uint8_t*>(avg.data_ptr());
+  e.root = static_cast<uint8_t*>(root.data_ptr());
+  e.avg_scale = static_cast<uint8_t*>(as.data_ptr());
+  e.root_scale = static_cast<uint8_t*>(rs.data_ptr());
+  e.numel = n;
+  return e;
+}
+
+PyObject* adamw8_step(Args a) {
+  const Target t = a.target();
+  const Items params(a.next(), "params"), grads(a.next(), "grads"), states(a.next(), "states");
+  const int64_t step = a.integer(), seed = a.integer();
+  double hyper[5];
+  for (double& h : hyper) h = a.number();
+  const Py_ssize_t n = params.size();
+  if (grads.size() != n || states.size() != n) refuse("params, grads and states must have the same length");
+  std::vector<muon_adamw8_t> all;
+  std::vector<at::Tensor> written;
+  all.reserve(n);
+  written.reserve(n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const std::string at = "[" + std::to_string(i) + "]";
+    const at::Tensor &p = params.tensor(i, t, "params" + at, at::kFloat, at::kBFloat16),
+                     &g = grads.tensor(i, t, "grads" + at, at::kFloat, at::kBFloat16);
+    muon_adamw8_t e = state_of(t, states.at(i), "states" + at, nullptr);
+    if (g.numel() != p.numel() || e.numel != p.numel()) refuse("grads" + at + " or states" + at + " has the wrong size");
+    e.param = p.data_ptr();
+    e.grad = g.data_ptr();
+    e.param_dtype = code_of(p.scalar_type());
+    e.grad_dtype = code_of(g.scalar_type());
+    all.push_back(e);
+    written.push_back(p);
+  }
+  muon_status_t st;
+  {
+    NoGil free;
+    st = muon_adamw8_step(t.h, all.data(), static_cast<int32_t>(n), step, static_cast<uint32_t>(seed), static_cast<float>(hyper[0]),
+                          static_cast<float>(hyper[1]), static_cast<float>(hyper[2]), static_cast<float>(hyper[3]),
+                          static_cast<float>(hyper[4]), t.stream());
+  }
+  if (st == MUON_OK)
+    for (at::Tensor& p : written) p.unsafeGetTensorImpl()->bump_version();     // autograd sees the write
+  return PyLong_FromLong(st);
+}
+
+PyObject* adamw8_restore(Args a) {
+  const Target t = a.target();
+  const Items states(a.next(), "states");
+  const std::optional<at::ScalarType> type = a.dtype();
+  if (!type || (*type != at::kFloat && *type != at::kBFloat16)) refuse("dtype must be float32 or bfloat16");
+  const Py_ssize_t n = states.size();
+  std::vector<muon_adamw8_t> all;
+  std::vector<at::Tensor> values;
+  std::vector<void*> avg, root;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    at::Tensor like;
+    all.push_back(state_of(t, states.at(i), "states[" + std::to_string(i) + "]", &like));
+    for (std::vector<void*>* to : {&avg, &root}) {
+      values.push_back(empty(like.sizes(), like, *type));
+      to->push_back(values.back().data_ptr());
+    }
+  }
+  muon_status_t st;
+  {
+    NoGil free;
+    st = muon_adamw8_restore(t.h, all.data(), avg.data(), root.data(), static_cast<int32_t>(n), code_of(*type), t.stream());
+  }
+  if (st != MUON_OK) return PyLong_FromLong(st);
+  PyObject* list = PyList_New(n);
+  if (list == nullptr) throw Raised{};
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* pair = nullptr;
+    try {
+      pair = results(st, std::move(values[2 * i]), std::move(values[2 * i + 1]), at::Tensor());
+    } catch (...) {
+      Py_DECREF(list);
+      throw;
+    }
+    PyList_SET_ITEM(list, i, pair);
+  }
+  return list;
+}
+
 // ------------------------------------------------------------------- module
 template <PyObject* (*F)(Args)>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -657,7 +871,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&call<f>)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {ENTRY(layer_norm), ENTRY(layer_norm_backward), ENTRY(attention), ENTRY(attention_backward),
                          ENTRY(act8_store), ENTRY(act8_restore), ENTRY(act8_weight_grad),
-                         ENTRY(expert_matmul), ENTRY(expert_weight_grad),
+                         ENTRY(expert_matmul), ENTRY(expert_weight_grad), ENTRY(act8_store_weight),
+                         ENTRY(act8_restore_weight), ENTRY(act8_matmul), ENTRY(adamw8_step), ENTRY(adamw8_restore),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -17,6 +17,8 @@ written on another stream have to be ready there, as for any call.
 """
 from __future__ import annotations
 
+import typing
+
 import torch
 
 from . import _binding
@@ -202,4 +204,115 @@ def expert_weight_grad(dy, x, offsets, *, add=None, out=None, dtype=None, handle
     got = _native.expert_weight_grad(h.address, h.device, dy, x, offsets, add, out, dtype)
     if type(got) is int:
         h._raise(got, "expert_weight_grad")
+    return got
+
+
+def act8_store_weight(w, *, transposed: bool = False, handle=None, stream=None):
+    """A weight [out, cols] (fp32, bf16, fp16) in 8 bits, for act8_matmul:
+    ``(codes, scales)``, or ``(codes, scales, codes_t)`` with ``transposed``.
+
+    codes: float8_e4m3fn [out, cols]; scales: uint8 [ceil(cols / 128), ceil(out
+    / 128)], one exponent a block of 128 x 128: the stored value is code times
+    2^(scale - 127), by act8_store's rule.  codes_t: the transpose's codes
+    [cols, out], which go with ``scales.t()``; the gradient of a layer's input
+    is taken with those."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return act8_store_weight(w, transposed=transposed, handle=handle)
+    h = _target(w, handle)
+    got = _native.act8_store_weight(h.address, h.device, w, transposed)
+    if type(got) is int:
+        h._raise(got, "act8_store_weight")
+    return got
+
+
+def act8_restore_weight(codes, scales, *, dtype=torch.bfloat16, handle=None, stream=None):
+    """The values that act8_store_weight kept, [out, cols] in ``dtype``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return act8_restore_weight(codes, scales, dtype=dtype, handle=handle)
+    h = _target(codes, handle)
+    got = _native.act8_restore_weight(h.address, h.device, codes, scales, dtype)
+    if type(got) is int:
+        h._raise(got, "act8_restore_weight")
+    return got
+
+
+def act8_matmul(codes, scales, wcodes, wscales, *, dtype=torch.bfloat16, handle=None, stream=None):
+    """x w^T [rows, out] in ``dtype``, of x [rows, cols] kept by act8_store and
+    w [out, cols] kept by act8_store_weight, on the tensor cores in 8 bits.
+
+    The codes and their scales are multiplied as they are, exactly; sums are
+    fp32, rounded once.  What is stored as NaN makes its row (its column) NaN."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return act8_matmul(codes, scales, wcodes, wscales, dtype=dtype, handle=handle)
+    h = _target(codes, handle)
+    got = _native.act8_matmul(h.address, h.device, codes, scales, wcodes, wscales, dtype)
+    if type(got) is int:
+        h._raise(got, "act8_matmul")
+    return got
+
+
+class Adamw8State(typing.NamedTuple):
+    """AdamW's states of one tensor in 8 bits, in blocks of 128 elements.
+
+    avg: float8_e4m3fn, the gradients' average; root: uint8, the square root
+    of their squares' average, 0 for 0 and (1 + (c & 15) / 16) 2^((c >> 4) - 8)
+    for a code c above; both of the tensor's shape.  avg_scale, root_scale:
+    uint8 [ceil(numel / 128)]: a block's values are times 2^(scale - 127)."""
+    avg: torch.Tensor
+    root: torch.Tensor
+    avg_scale: torch.Tensor
+    root_scale: torch.Tensor
+
+
+def adamw8_state(param):
+    """The state that a parameter starts with: zeros."""
+    blocks = -(-param.numel() // 128)
+    kw = dict(dtype=torch.uint8, device=param.device)
+    return Adamw8State(torch.zeros(param.shape, **kw).view(torch.float8_e4m3fn), torch.zeros(param.shape, **kw),
+                       torch.zeros(blocks, **kw), torch.zeros(blocks, **kw))
+
+
+def adamw8_step(params, grads, states, *, step: int, lr: float, beta1: float, beta2: float, eps: float, wd: float, seed=None,
+                handle=None, stream=None):
+    """The AdamW step of adamw_step over lists of tensors whose states are kept
+    in 8 bits (params and states are updated in place).
+
+    params and grads: contiguous, fp32 or bf16; states: an Adamw8State each.
+    The step is computed in fp32 from the states' values; what is kept of them
+    is rounded up or down by a hash of the element's place and ``seed`` (default:
+    ``step``), so that averages move by less than a step of their codes too.
+    The same call gives the same result.  A NaN or an infinity in a gradient
+    makes the state of its 128 elements NaN.  A captured call repeats its
+    ``step`` and ``seed``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return adamw8_step(params, grads, states, step=step, lr=lr, beta1=beta1, beta2=beta2, eps=eps, wd=wd, seed=seed,
+                               handle=handle)
+    if len(params) == 0:
+        if len(grads) or len(states):
+            raise ValueError("params, grads and states must have the same length")
+        return
+    h = _target(params[0], handle)
+    seed = (step if seed is None else int(seed)) & 0xFFFFFFFF
+    got = _native.adamw8_step(h.address, h.device, params, grads, states, step, seed, lr, beta1, beta2, eps, wd)
+    if got != 0:
+        h._raise(got, "adamw8_step")
+
+
+def adamw8_restore(states, *, dtype=torch.float32, handle=None, stream=None):
+    """The values of a list of states: ``[(avg, root), ..]`` in ``dtype``
+    (float32 or bfloat16, both exact down to 2^-126).  root is the square root
+    of adamw_step's exp_avg_sq."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
+            return adamw8_restore(states, dtype=dtype, handle=handle)
+    if len(states) == 0:
+        return []
+    h = _target(states[0][0], handle)
+    got = _native.adamw8_restore(h.address, h.device, states, dtype)
+    if type(got) is int:
+        h._raise(got, "adamw8_restore")
     return got

@@ -161,3 +161,113 @@ def expert_weight_grad(dy, x, offsets):
     the products' magnitudes."""
     parts = [(dy[a:b].T @ x[a:b], np.abs(dy[a:b]).T @ np.abs(x[a:b])) for a, b in expert_ranges(offsets, x.shape[0])]
     return np.stack([p for p, _ in parts]), np.stack([m for _, m in parts])
+
+
+# ------------------------------------------------- weights in 8 bits
+def _nearest_codes(u):
+    """e4m3 codes nearest to u (|u| <= 448), ties to the even code."""
+    pos = e4m3_table()[:0x7F]
+    mid = (pos[1:] + pos[:-1]) / 2
+    a = np.abs(u)
+    lo = np.searchsorted(mid, a, side="left")
+    tie = (lo < len(mid)) & (mid[np.minimum(lo, len(mid) - 1)] == a)
+    return (lo + (tie & (lo % 2 == 1))) | np.where(np.signbit(u), 0x80, 0)
+
+
+def _scale_exponent(top, largest):
+    """The smallest whole e >= -111 with top 2^-e <= largest."""
+    e = -111
+    while top > largest * 2.0 ** e:
+        e += 1
+    return e
+
+
+def act8_encode_weight(w):
+    """(codes, scale bytes [column blocks, row blocks]) of w [out, cols]."""
+    out, cols = w.shape
+    codes = np.zeros(w.shape, np.uint8)
+    scales = np.zeros((-(-cols // BLOCK), -(-out // BLOCK)), np.uint8)
+    for k in range(scales.shape[0]):
+        for o in range(scales.shape[1]):
+            at = np.s_[o * BLOCK:(o + 1) * BLOCK, k * BLOCK:(k + 1) * BLOCK]
+            if not np.isfinite(w[at]).all():
+                scales[k, o] = 255
+                continue
+            e = _scale_exponent(np.abs(w[at]).max(), 448.0)
+            scales[k, o] = e + 127
+            codes[at] = _nearest_codes(w[at] * 2.0 ** -e)
+    return codes, scales
+
+
+def act8_decode_weight(codes, scales):
+    """The values of codes [out, cols] under scale bytes [column blocks, row blocks]."""
+    unit = np.where(scales == 255, np.inf, 2.0 ** (scales.astype(np.float64) - 127))
+    with np.errstate(invalid="ignore"):
+        return e4m3_table()[codes] * np.repeat(np.repeat(unit.T, BLOCK, 0)[:codes.shape[0]], BLOCK, 1)[:, :codes.shape[1]]
+
+
+# --------------------------------------------- AdamW with states in 8 bits
+def root_table():
+    """The value of every code of a root."""
+    c = np.arange(256)
+    return np.where(c == 0, 0.0, (1 + (c & 15) / 16.0) * 2.0 ** ((c >> 4) - 8.0))
+
+
+def adamw8_noise(n, seed):
+    """The number in (0, 1) that each element is rounded with."""
+    x = (np.arange(-(-n // 4), dtype=np.uint64) + np.uint64(seed * 0x9E3779B1 % 2 ** 32)) % np.uint64(2 ** 32)
+    for shift, factor in ((16, 0x7FEB352D), (15, 0x846CA68B)):
+        x = (x ^ (x >> np.uint64(shift))) * np.uint64(factor) % np.uint64(2 ** 32)
+    x ^= x >> np.uint64(16)
+    b = np.stack([(x >> np.uint64(8 * k)) & np.uint64(255) for k in range(4)], 1).reshape(-1)[:n]
+    return (b.astype(np.float64) + 0.5) / 256
+
+
+def _blocks(x):
+    return [x[i:i + BLOCK] for i in range(0, len(x), BLOCK)]
+
+
+def adamw8_decode(avg, root, avg_scale, root_scale):
+    """(m, r) of flat codes and their blocks' scale bytes."""
+    def unit(s):
+        return np.repeat(np.where(s == 255, np.inf, 2.0 ** (s.astype(np.float64) - 127)), BLOCK)[:len(avg)]
+    with np.errstate(invalid="ignore"):
+        return e4m3_table()[avg] * unit(avg_scale), root_table()[root] * unit(root_scale)
+
+
+def adamw8_codes(x, noise, table, largest, least, given=None):
+    """(codes, scale bytes) of magnitudes x by the rounding rule: the largest
+    code whose value is at most u, or the next where (u - value) / (next -
+    value) + noise >= 1; at least `least` for what is not 0.  And how near each
+    was to the other choice, as a part of the step.  given: scale bytes that a
+    block takes where its largest is within 2^-20 of a scale's limit."""
+    codes, scales, near = np.zeros(len(x), np.uint8), [], np.ones(len(x))
+    for i, part in enumerate(_blocks(x)):
+        if not np.isfinite(part).all():
+            scales.append(255)
+            continue
+        top = part.max(initial=0.0)
+        e = _scale_exponent(top, largest)
+        if given is not None and abs(int(given[i]) - 127 - e) == 1:
+            other = int(given[i]) - 127
+            if abs(top / (largest * 2.0 ** min(e, other)) - 1) < 2.0 ** -20:
+                e = other
+        scales.append(e + 127)
+        u = part * 2.0 ** -e
+        lo = np.searchsorted(table, u, side="right") - 1
+        up = np.minimum(lo + 1, len(table) - 1)
+        step = np.where(up > lo, table[up] - table[lo], 1.0)
+        frac = (u - table[lo]) / step
+        z = noise[i * BLOCK:i * BLOCK + len(part)]
+        c = np.where(frac + z >= 1, up, lo)
+        codes[i * BLOCK:i * BLOCK + len(part)] = np.where(u > 0, np.maximum(c, least), 0)
+        near[i * BLOCK:i * BLOCK + len(part)] = np.abs(frac + z - 1)
+    return codes, np.array(scales, np.uint8), near
+
+
+def adamw8_step(p, g, m, r, step, lr, beta1, beta2, eps, wd):
+    """(p, m, r) after the step, before the states are rounded."""
+    m = m + (1 - beta1) * (g - m)
+    r = np.sqrt(r * r + (1 - beta2) * (g * g - r * r))
+    size = lr * np.sqrt(1 - beta2 ** step) / (1 - beta1 ** step)
+    return p * (1 - lr * wd) - size * m / (eps + r), m, r
