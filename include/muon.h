@@ -530,7 +530,7 @@ typedef struct {
 } muon_adamw8_t;
 
 muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, int32_t n, int64_t step, uint32_t seed,
-                               float lr, float beta1, float beta2, float eps, float wd, void* stream);
+                               double lr, double beta1, double beta2, double eps, double wd, void* stream);
 /* The values of states: m into avg[i] and r (not its square) into root[i], both
  * dtype (MUON_F32: exact; MUON_BF16: exact above 2^-126).  param and grad are not
  * read. */

@@ -139,7 +139,7 @@ def load_library(path: str | None = None):
             "muon_act8_store_weight": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_restore_weight": (i32, [vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_matmul": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i64, i64, i32, vp]),
-            "muon_adamw8_step": (i32, [vp, ctypes.POINTER(MuonAdamw8C), i32, i64, ctypes.c_uint32, f32, f32, f32, f32, f32,
+            "muon_adamw8_step": (i32, [vp, ctypes.POINTER(MuonAdamw8C), i32, i64, ctypes.c_uint32, *[ctypes.c_double] * 5,
                                        vp]),
             "muon_adamw8_restore": (i32, [vp, ctypes.POINTER(MuonAdamw8C), ctypes.POINTER(vp), ctypes.POINTER(vp), i32, i32,
                                           vp]),

@@ -396,8 +396,8 @@ struct ProductParams {
   unsigned* err;           // the handle's error word
   unsigned long long timeout_ns;
 };
-// maps, 3-D with 128-byte swizzle: A and B (see op_product.cu).  K-major: {k, rows, groups or 1} in boxes of 64 k and 128
-// rows (A) or 32 (B) (8 bits: of 128 k); MN-major: {rows, k, groups or 1} in boxes of 64 rows and 64 k.
+// maps, 3-D with 128-byte swizzle: A, B and B again (see op_product.cu).  K-major: {k, rows, groups or 1} in boxes of 64 k
+// (8 bits: 128) and 128 rows, or 32 in the third; MN-major: {rows, k, groups or 1} in boxes of 64 rows and 64 k.
 uint64_t product_part_bytes(int64_t tokens, int sms);
 cudaError_t launch_product(const ProductParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s);
 

@@ -313,7 +313,8 @@ __device__ __forceinline__ void zero_rows(const ProductParams& p, int from, int 
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREADS, 1)
-    product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const ProductParams p) {
+    product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                   const __grid_constant__ CUtensorMap mb32, const ProductParams p) {
   using T = Traits<KIND>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + BAR_OFF);
@@ -351,55 +352,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
   volatile int* abort = &bar->abort;
   Tiles<KIND> tiles(p, at);
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     if (lane == 0) {
       // ------------------------------------------------------------ loads
+      // Warp 0 loads A and says what is to come, warp 3 loads B, in few large
+      // boxes: a thread issues a load in some 200 cycles, a step's products
+      // take 512.
+      const bool is_a = warp == 0;
       const uint32_t lead = mapa_shared(smem_u32(&bar->full[0]), 0);
       Ring<STAGES> r;
       bool ok = true;
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
         const int m0 = t.m0 + static_cast<int>(rank) * 128;
+        // of B, this CTA's half: boxes of 128 or 32 tokens, or of 64 outputs
         const int half = (t.n + 31) / 32 * 16, n0 = t.n0 + static_cast<int>(rank) * half;
-        // of B, this CTA's half: boxes of 32 tokens, or of 64 outputs
-        const int boxes = T::kBmn ? (half + 63) / 64 : (half + 31) / 32;
-        const uint32_t bytes = 2 * BOX + boxes * (T::kBmn ? BOX : BOX / 2);
+        const bool one = !T::kBmn && half > 64;
+        const int boxes = one ? 1 : T::kBmn ? (half + 63) / 64 : (half + 31) / 32;
+        const uint32_t bytes = 2 * BOX + boxes * (one ? 2 * BOX : T::kBmn ? BOX : BOX / 2);
         for (int k = 0; k < t.steps; ++k) {
           ok = wait_one(&bar->empty[r.s], r.ph ^ 1u, abort, p);
           if (!ok) break;
-          const uint32_t a = sb + r.s * STAGE, b = a + 2 * BOX;
-          uint32_t fb = lead + r.s * 8;
+          const uint32_t a = sb + r.s * STAGE, b = a + 2 * BOX, fb = lead + r.s * 8;
           if constexpr (KIND == PRODUCT_WEIGHT) {
-            const bool mend = k == t.steps - 1 && (t.len & 15) != 0;
-            if (mend) {
+            const int row = t.t0 + k * 64;
+            if (k == t.steps - 1 && (t.len & 15) != 0) {
               // an expert's last tokens: to this CTA's own warp, which clears
               // what follows them (see below)
-              mbar_arrive_expect_tx(&bar->own[r.s], bytes);
-              if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], sizeof(uint4));
-              const int row = t.t0 + k * 64;
-              tma_load_3d(a, &ma, &bar->own[r.s], m0, row, 0);
-              tma_load_3d(a + BOX, &ma, &bar->own[r.s], m0 + 64, row, 0);
-              for (int c = 0; c < boxes; ++c) tma_load_3d(b + c * BOX, &mb, &bar->own[r.s], n0 + c * 64, row, 0);
-              r.next();
-              continue;
+              uint64_t* own = &bar->own[r.s];
+              if (is_a) {
+                mbar_arrive_expect_tx(own, bytes);
+                if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], sizeof(uint4));
+                tma_load_3d(a, &ma, own, m0, row, 0);
+                tma_load_3d(a + BOX, &ma, own, m0 + 64, row, 0);
+              } else {
+                for (int c = 0; c < boxes; ++c) tma_load_3d(b + c * BOX, &mb, own, n0 + c * 64, row, 0);
+              }
+            } else if (is_a) {
+              if (rank == 0) {
+                mbar_arrive(&bar->full[r.s]);
+                mbar_arrive_expect_tx(&bar->full[r.s], 2 * bytes);
+              }
+              tma_load_3d_pair(a, &ma, fb, m0, row, 0);
+              tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, row, 0);
+            } else {
+              for (int c = 0; c < boxes; ++c) tma_load_3d_pair(b + c * BOX, &mb, fb, n0 + c * 64, row, 0);
             }
-            if (rank == 0) mbar_arrive(&bar->full[r.s]);
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], 2 * bytes);
-          if constexpr (KIND == PRODUCT_FORWARD || KIND == PRODUCT_ACT8) {
-            tma_load_3d_pair(a, &ma, fb, k * T::BK, m0, t.e);
-          } else if constexpr (KIND == PRODUCT_INPUT) {
-            tma_load_3d_pair(a, &ma, fb, m0, k * 64, t.e);
-            tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, k * 64, t.e);
+          } else if (is_a) {
+            if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], 2 * bytes);
+            if constexpr (T::kAmn) {
+              tma_load_3d_pair(a, &ma, fb, m0, k * T::BK, t.e);
+              tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, k * T::BK, t.e);
+            } else {
+              tma_load_3d_pair(a, &ma, fb, k * T::BK, m0, t.e);
+            }
+          } else if (one) {
+            tma_load_3d_pair(b, &mb, fb, k * T::BK, n0, 0);
           } else {
-            tma_load_3d_pair(a, &ma, fb, m0, t.t0 + k * 64, 0);
-            tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, t.t0 + k * 64, 0);
-          }
-          for (int c = 0; c < boxes; ++c) {
-            if constexpr (T::kBmn)
-              tma_load_3d_pair(b + c * BOX, &mb, fb, n0 + c * 64, t.t0 + k * 64, 0);
-            else
-              tma_load_3d_pair(b + c * (BOX / 2), &mb, fb, k * T::BK, n0 + c * 32, 0);
+            for (int c = 0; c < boxes; ++c) tma_load_3d_pair(b + c * (BOX / 2), &mb32, fb, k * T::BK, n0 + c * 32, 0);
           }
           r.next();
         }
@@ -511,8 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     if constexpr (T::k8) {
       // Scales, four blocks at a time, to this warp's lanes: each row of 32
       // lanes of TMEM holds all of them.  The product reads its CTA's own copy,
-      // of all n.  Blocks and tokens that are not there get 2^0: their codes
-      // are zeros (an infinity or NaN times them would not be).
+      // of all n.
       const uint32_t lead = mapa_shared(smem_u32(&bar->sf_full[0]), 0);
       const uint32_t at0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * T::NT;
       Ring<SF_SLOTS> rs;
@@ -520,26 +529,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
         const int m0 = t.m0 + static_cast<int>(rank) * 128;
-        const uint8_t* ws = p.wscales + (m0 >> 7) * p.ws_row;
+        const uint8_t* ws = p.wscales + (min(m0, p.m - 1) >> 7) * p.ws_row;
+        const int last = t.n - 1 - lane;
         for (int k0 = 0; k0 < t.steps; k0 += 4) {
-          uint32_t wa = 0u, wb[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) wb[c] = 0u;
+          // loads first, all of them: past the last block, token or output those
+          // of the last, which no result is stored of
+          uint32_t wa[4], wb[4][7];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int k = k0 + q;
-            const bool in = k < t.steps;
-            wa |= static_cast<uint32_t>(in && m0 < p.m ? ws[k * p.ws_col] : 127) << (8 * q);
+            const int k = min(k0 + q, t.steps - 1);
+            wa[q] = ws[k * p.ws_col];
             const uint8_t* xs = p.scales + k * p.lds + t.n0 + lane;
 #pragma unroll
-            for (int c = 0; c < 7; ++c)
-              wb[c] |= static_cast<uint32_t>(in && c * 32 + lane < t.n ? xs[c * 32] : 127) << (8 * q);
+            for (int c = 0; c < 7; ++c) wb[q][c] = xs[min(c * 32, last)];
           }
+          uint32_t word[8];
+#pragma unroll
+          for (int c = 0; c < 7; ++c) word[c] = wb[0][c] | wb[1][c] << 8 | wb[2][c] << 16 | wb[3][c] << 24;
+          word[7] = 0u;
           ok = wait_warp(&bar->sf_empty[rs.s], rs.ph ^ 1u, abort, p);
           if (!ok) break;
           tc_fence_after();
-          tmem_st4(at0 + rs.s * SF_COLS, wa);
-          tmem_st8(at0 + rs.s * SF_COLS + 4, wb);
+          tmem_st4(at0 + rs.s * SF_COLS, wa[0] | wa[1] << 8 | wa[2] << 16 | wa[3] << 24);
+          tmem_st8(at0 + rs.s * SF_COLS + 4, word);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -659,7 +671,8 @@ cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pai
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(product_kernel<KIND>), SMEM, done);
   if (e != cudaSuccess) return e;
   const long long some = mt * nt < 1 ? 1 : mt * nt < pairs ? mt * nt : pairs;
-  product_kernel<KIND><<<dim3(2 * static_cast<unsigned>(some)), Traits<KIND>::THREADS, SMEM, s>>>(maps[0], maps[1], p);
+  product_kernel<KIND><<<dim3(2 * static_cast<unsigned>(some)), Traits<KIND>::THREADS, SMEM, s>>>(maps[0], maps[1],
+                                                                                                    maps[2], p);
   return cudaGetLastError();
 }
 

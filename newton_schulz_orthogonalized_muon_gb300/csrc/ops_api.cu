@@ -638,9 +638,10 @@ muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, co
     p.err = h->err;
     p.timeout_ns = h->timeout_ns;
     h->prof_tag = -1;
-    CUtensorMap maps[2] = {};
+    CUtensorMap maps[3] = {};
     if (!product_map(h, &maps[0], w, cols, out, ldw, experts, w_expert, dtype, transpose ? 64 : 128) ||
-        !product_map(h, &maps[1], x, in, tokens, ldx, 1, 0, dtype, 32))
+        !product_map(h, &maps[1], x, in, tokens, ldx, 1, 0, dtype, 128) ||
+        !product_map(h, &maps[2], x, in, tokens, ldx, 1, 0, dtype, 32))
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms / 2, stream), "experts' product launch");
     return MUON_OK;
@@ -697,7 +698,7 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
     p.err = h->err;
     p.timeout_ns = h->timeout_ns;
     h->prof_tag = -1;
-    CUtensorMap maps[2] = {};
+    CUtensorMap maps[3] = {};
     if (tokens > 0 && (!product_map(h, &maps[0], x, cols, tokens, ldx, 1, 0, dtype, 64) ||
                        !product_map(h, &maps[1], dy, out, tokens, lddy, 1, 0, dtype, 64)))
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
@@ -788,8 +789,9 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
     p.err = h->err;
     p.timeout_ns = h->timeout_ns;
     h->prof_tag = -1;
-    CUtensorMap maps[2] = {};
-    if (!codes_map(h, &maps[0], wcodes, cols, out, ldw, 128) || !codes_map(h, &maps[1], codes, cols, rows, ldc, 32))
+    CUtensorMap maps[3] = {};
+    if (!codes_map(h, &maps[0], wcodes, cols, out, ldw, 128) || !codes_map(h, &maps[1], codes, cols, rows, ldc, 128) ||
+        !codes_map(h, &maps[2], codes, cols, rows, ldc, 32))
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
     MUON_LAUNCH(MUON_K_MATMUL8, launch_product(p, maps, h->num_sms / 2, stream), "8-bit product launch");
     return MUON_OK;
@@ -797,13 +799,13 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
 }
 
 muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, int32_t n, int64_t step, uint32_t seed,
-                               float lr, float beta1, float beta2, float eps, float wd, void* stream_arg) {
+                               double lr, double beta1, double beta2, double eps, double wd, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded(h, [&]() -> muon_status_t {
     const muon_status_t st = check_adamw8(h, tensors, n);
     if (st != MUON_OK) return st;
     MUON_CHECK(step >= 1, "step counts from 1");
-    MUON_CHECK(beta1 >= 0.f && beta1 < 1.f && beta2 >= 0.f && beta2 < 1.f && std::isfinite(lr) && std::isfinite(eps) &&
+    MUON_CHECK(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && std::isfinite(lr) && std::isfinite(eps) &&
                    std::isfinite(wd), "bad hyper-parameter");
     std::vector<std::pair<uintptr_t, uintptr_t>> written;
     written.reserve(5 * static_cast<size_t>(n));
@@ -827,15 +829,14 @@ muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, in
     MUON_CHECK(!share_memory(written), "two tensors, or their states, share memory");
     DeviceGuard guard(h->device);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
-    const double bc1 = 1.0 - std::pow(static_cast<double>(beta1), static_cast<double>(step));
-    const double bc2 = 1.0 - std::pow(static_cast<double>(beta2), static_cast<double>(step));
+    const double bc1 = 1.0 - std::pow(beta1, static_cast<double>(step)), bc2 = 1.0 - std::pow(beta2, static_cast<double>(step));
     Adamw8Params p{};
     p.salt = seed * 0x9E3779B1u;
-    p.omb1 = 1.f - beta1;
-    p.omb2 = 1.f - beta2;
-    p.eps = eps;
-    p.decay = static_cast<float>(1.0 - static_cast<double>(lr) * wd);
-    p.size = static_cast<float>(static_cast<double>(lr) * std::sqrt(bc2) / bc1);
+    p.omb1 = static_cast<float>(1.0 - beta1);
+    p.omb2 = static_cast<float>(1.0 - beta2);
+    p.eps = static_cast<float>(eps);
+    p.decay = static_cast<float>(1.0 - lr * wd);
+    p.size = static_cast<float>(lr * std::sqrt(bc2) / bc1);
     h->prof_tag = -1;
     return adamw8_launches(h, tensors, n, p, "adamw8 launch", stream, launch_adamw8, [&](int32_t, const muon_adamw8_t& t) {
       if (t.param_dtype != p.pdtype || t.grad_dtype != p.gdtype) return;

@@ -796,9 +796,8 @@ PyObject* adamw8_step(Args a) {
   muon_status_t st;
   {
     NoGil free;
-    st = muon_adamw8_step(t.h, all.data(), static_cast<int32_t>(n), step, static_cast<uint32_t>(seed), static_cast<float>(hyper[0]),
-                          static_cast<float>(hyper[1]), static_cast<float>(hyper[2]), static_cast<float>(hyper[3]),
-                          static_cast<float>(hyper[4]), t.stream());
+    st = muon_adamw8_step(t.h, all.data(), static_cast<int32_t>(n), step, static_cast<uint32_t>(seed), hyper[0], hyper[1],
+                          hyper[2], hyper[3], hyper[4], t.stream());
   }
   if (st == MUON_OK)
     for (at::Tensor& p : written) p.unsafeGetTensorImpl()->bump_version();     // autograd sees the write
