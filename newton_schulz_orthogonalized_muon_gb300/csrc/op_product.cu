@@ -40,7 +40,10 @@ constexpr int STEPS_SUM = 32;            // weight: steps of 64 tokens an accumu
 constexpr int PART_WARP = 4 * 1024;      // floats of scratch of an epilogue warp
 constexpr int EPI_OFF = STAGES * STAGE;
 constexpr int GROUP_OFF = EPI_OFF + EPI_WARPS * SLOT;
-constexpr int BAR_OFF = GROUP_OFF + 2 * 4 * (kMaxExperts + 4);
+// 8 bits: the tokens' scales on their way, 256 of each of four blocks
+constexpr int SB_SLOTS = 4, SB_SLOT = 4 * 256;
+constexpr int SB_OFF = GROUP_OFF + 2 * 4 * (kMaxExperts + 4);
+constexpr int BAR_OFF = SB_OFF + SB_SLOTS * SB_SLOT;
 constexpr int SMEM = BAR_OFF + 512;
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
 static_assert(SMEM <= 232448, "shared memory");
@@ -69,12 +72,13 @@ struct alignas(16) Bars {
   uint64_t tfull[2], tempty[2];
   uint64_t sf_full[SF_SLOTS];            // 8 bits: the leader's, scales written by both CTAs
   uint64_t sf_empty[SF_SLOTS];
+  uint64_t sb_full[SB_SLOTS], sb_empty[SB_SLOTS];   // 8 bits: each CTA's own, scales as they are in memory
   uint64_t drain;
   uint4 token[2];                        // sent, received (see send_token)
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= 512 && SB_OFF % 16 == 0, "barrier block");
 
 // n of the tiles that a row of `len` is cut into: as few tiles as there can be,
 // of about one size where the last would be small.
@@ -106,23 +110,28 @@ struct Tiles {
     total = Traits<KIND>::kTokens ? pre[p.groups] : p.groups * mt * ((p.n + nsize() - 1) / nsize());
   }
   __device__ __forceinline__ int nsize() const { return tile_n<Traits<KIND>::NT>(p.n, false); }
+  // A group's tiles go eight m at a time: the pairs that run together share
+  // panels of A and of B in L2.
+  __device__ __forceinline__ void place(int in, int nt, int& m0, int& n0, int size) const {
+    const int band = in / (8 * nt), r = in - band * 8 * nt, rows = min(8, mt - band * 8), j = r / rows;
+    m0 = (band * 8 + r - j * rows) * MT;
+    n0 = j * size;
+  }
   __device__ __forceinline__ Tile get(int i) {
     Tile t;
     if constexpr (Traits<KIND>::kTokens) {
       while (pre[e + 1] <= i) ++e;
-      const int in = i - pre[e], len = at[e + 1] - at[e], size = tile_n<Traits<KIND>::NT>(len, true), j = in / mt;
+      const int len = at[e + 1] - at[e], size = tile_n<Traits<KIND>::NT>(len, true);
       t.e = e;
-      t.m0 = (in - j * mt) * MT;
-      t.n0 = at[e] + j * size;
+      place(i - pre[e], (len + size - 1) / size, t.m0, t.n0, size);
+      t.n0 += at[e];
       t.n = min(size, at[e + 1] - t.n0);
       t.steps = (p.k + Traits<KIND>::BK - 1) / Traits<KIND>::BK;
       t.t0 = t.len = 0;
     } else {
       const int size = nsize(), per = mt * ((p.n + size - 1) / size);
       t.e = i / per;
-      const int in = i - t.e * per, j = in / mt;
-      t.m0 = (in - j * mt) * MT;
-      t.n0 = j * size;
+      place(i - t.e * per, per / mt, t.m0, t.n0, size);
       t.n = min(size, p.n - t.n0);
       t.t0 = at[t.e];
       t.len = at[t.e + 1] - t.t0;
@@ -337,6 +346,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       mbar_init(&bar->sf_full[s], 8);
       mbar_init(&bar->sf_empty[s], 1);
     }
+    for (int s = 0; s < SB_SLOTS; ++s) {
+      mbar_init(&bar->sb_full[s], 1);
+      mbar_init(&bar->sb_empty[s], 4);
+    }
     mbar_init(&bar->drain, 1);
     bar->token[0] = make_uint4(0u, 0u, 0u, 0u);
     bar->abort = (sb & 1023u) != 0u ? 1 : 0;       // the swizzled boxes need 1 KB boundaries
@@ -480,6 +493,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       if (lane == 0) mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
     }
     __syncwarp();
+  } else if (warp == 2 && T::k8) {
+    if constexpr (T::k8) {
+      // The tokens' scales, 256 bytes for each of four blocks.  (Loaded by the
+      // warps that use them, one group ahead, they were waited for 2700 cycles a
+      // group, whose products take 1800.)
+      Ring<SB_SLOTS> rb;
+      bool ok = true;
+      for (int i = pair; ok && i < tiles.total; i += npairs) {
+        const Tile t = tiles.get(i);
+        const uint32_t bytes = static_cast<uint32_t>(min(256, (p.tokens - t.n0 + 15) / 16 * 16));
+        for (int k0 = 0; k0 < t.steps; k0 += 4) {
+          ok = wait_warp(&bar->sb_empty[rb.s], rb.ph ^ 1u, abort, p);
+          if (!ok) break;
+          const int live = min(4, t.steps - k0);
+          if (lane == 0) mbar_arrive_expect_tx(&bar->sb_full[rb.s], bytes * live);
+          __syncwarp();
+          if (lane < live)
+            bulk_load(sb + SB_OFF + rb.s * SB_SLOT + lane * 256, p.scales + (k0 + lane) * p.lds + t.n0, bytes,
+                      smem_u32(&bar->sb_full[rb.s]));
+          rb.next();
+        }
+      }
+      __syncwarp();
+    }
   } else if (warp == 2) {
     if constexpr (KIND == PRODUCT_WEIGHT) {
       // Tokens behind an expert's last one are another's.  Products take 16 at
@@ -521,36 +558,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     if constexpr (T::k8) {
       // Scales, four blocks at a time, to this warp's lanes: each row of 32
       // lanes of TMEM holds all of them.  The product reads its CTA's own copy,
-      // of all n.
+      // of all n.  (What is behind the last token or block is of no meaning: no
+      // result of such n is stored, no product takes such a byte.)
+      const int ksteps = (p.k + T::BK - 1) / T::BK;
       const uint32_t lead = mapa_shared(smem_u32(&bar->sf_full[0]), 0);
       const uint32_t at0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * T::NT;
       Ring<SF_SLOTS> rs;
-      bool ok = true;
-      for (int i = pair; ok && i < tiles.total; i += npairs) {
-        const Tile t = tiles.get(i);
+      Ring<SB_SLOTS> rb;
+      // The weight's bytes, one a lane for 32 blocks, loaded 32 blocks ahead.
+      Tile t;
+      int i = pair;                      // of the blocks that are loaded next
+      int k = 0;
+      uint32_t next = 0u, now = 0u;
+      auto load = [&]() {
+        if (i >= tiles.total) return;
+        if (k == 0) t = tiles.get(i);
         const int m0 = t.m0 + static_cast<int>(rank) * 128;
-        const uint8_t* ws = p.wscales + (min(m0, p.m - 1) >> 7) * p.ws_row;
-        const int last = t.n - 1 - lane;
-        for (int k0 = 0; k0 < t.steps; k0 += 4) {
-          // loads first, all of them: past the last block, token or output those
-          // of the last, which no result is stored of
-          uint32_t wa[4], wb[4][7];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int k = min(k0 + q, t.steps - 1);
-            wa[q] = ws[k * p.ws_col];
-            const uint8_t* xs = p.scales + k * p.lds + t.n0 + lane;
-#pragma unroll
-            for (int c = 0; c < 7; ++c) wb[q][c] = xs[min(c * 32, last)];
+        next = k + lane < t.steps && m0 < p.m ? p.wscales[(k + lane) * p.ws_col + (m0 >> 7) * p.ws_row] : 127u;
+        k += 32;
+        if (k >= t.steps) {
+          k = 0;
+          i += npairs;
+        }
+      };
+      load();
+      bool ok = true;
+      for (int j = pair; ok && j < tiles.total; j += npairs) {
+        for (int k0 = 0; k0 < ksteps; k0 += 4) {
+          if ((k0 & 31) == 0) {
+            now = next;
+            load();
           }
+          ok = wait_warp(&bar->sb_full[rb.s], rb.ph, abort, p);
+          if (!ok) break;
           uint32_t word[8];
+          const uint8_t* from = smem + SB_OFF + rb.s * SB_SLOT + lane;
 #pragma unroll
-          for (int c = 0; c < 7; ++c) word[c] = wb[0][c] | wb[1][c] << 8 | wb[2][c] << 16 | wb[3][c] << 24;
+          for (int c = 0; c < 7; ++c)
+            word[c] = from[c * 32] | from[256 + c * 32] << 8 | from[512 + c * 32] << 16 | static_cast<uint32_t>(from[768 + c * 32]) << 24;
           word[7] = 0u;
+          uint32_t wword = 0u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) wword |= __shfl_sync(0xffffffffu, now, (k0 & 31) + q) << (8 * q);
+          if (lane == 0) mbar_arrive(&bar->sb_empty[rb.s]);
+          rb.next();
           ok = wait_warp(&bar->sf_empty[rs.s], rs.ph ^ 1u, abort, p);
           if (!ok) break;
           tc_fence_after();
-          tmem_st4(at0 + rs.s * SF_COLS, wa[0] | wa[1] << 8 | wa[2] << 16 | wa[3] << 24);
+          tmem_st4(at0 + rs.s * SF_COLS, wword);
           tmem_st8(at0 + rs.s * SF_COLS + 4, word);
           tmem_wait_st();
           tc_fence_before();
