@@ -392,6 +392,7 @@ struct ProductParams {
                            // over tokens)
   int odtype;
   int f16;                 // the operands are fp16 (else bf16)
+  int most;                // set by the launcher: n of a tile, at most
   int vec;                 // set by the launcher: rows of out and add are 16-byte aligned
   unsigned* err;           // the handle's error word
   unsigned long long timeout_ns;

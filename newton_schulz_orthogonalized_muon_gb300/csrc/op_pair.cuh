@@ -62,12 +62,30 @@ __device__ __forceinline__ void gave_up(volatile int* abort, unsigned* err) {
   if (*abort == 0) atomicOr(err, ERRBIT_TIMEOUT);
   *abort = 1;
 }
+// The clock is read after 32 polls at the earliest: reading it takes longer than
+// most waits last.
+struct WaitClock {
+  uint64_t t0 = 0;
+  // at polls 32, 64, ..: whether the limit has passed
+  __device__ __forceinline__ bool over(uint64_t limit) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    return now - t0 > limit;
+  }
+};
 // one thread
 template <typename P>
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, const P& p) {
-  if (mbar_wait_bounded(bar, parity, abort, p.timeout_ns)) return true;
-  gave_up(abort, p.err);
-  return false;
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  WaitClock clock;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(a, parity)) return true;
+    if ((it & 31u) == 0u && (*abort != 0 || clock.over(p.timeout_ns))) {
+      gave_up(abort, p.err);
+      return false;
+    }
+  }
 }
 // a warp; SLEEP: nanoseconds between polls where the wait is long and the
 // issue slots are better left to the code warps; PAIR: for what the other CTA did
@@ -76,12 +94,12 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   const uint32_t a = smem_u32(bar);
   auto done = [&]() { return __all_sync(0xffffffffu, PAIR ? try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) != 0; };
   if (done()) return true;
-  const uint64_t t0 = globaltimer_ns();
+  WaitClock clock;
   for (uint32_t it = 1;; ++it) {
     if (SLEEP > 0) __nanosleep(SLEEP);
     if (done()) return true;
     if ((it & 31u) == 0u) {
-      const bool stop = *abort != 0 || globaltimer_ns() - t0 > p.timeout_ns;
+      const bool stop = *abort != 0 || clock.over(p.timeout_ns);
       if (__any_sync(0xffffffffu, stop)) {
         if ((threadIdx.x & 31) == 0) gave_up(abort, p.err);
         return false;

@@ -12,15 +12,23 @@
 //   input      columns (W)          tokens (dy)        outputs
 //   weight     columns (x)          outputs (dy)       tokens
 //   8 bits     outputs (W's codes)  tokens (x's codes) columns
-// A CTA pair forms 256 m (128 a CTA) by up to 256 n (tcgen05.mma.cta_group::2).
+// A CTA pair forms 256 m (128 a CTA) by up to 512 n (tcgen05.mma.cta_group::2).
 // The ragged dimension, tokens, is n: the tensor core takes n in steps of 32,
 // so an expert's last tile costs what it has, where rows of m would be padded
-// to 256 (17% of the work at 768 tokens an expert).  Operands come by TMA with
-// 128-byte swizzle, K-major or MN-major as they lie in memory, through a ring
-// of five stages; two accumulators in TMEM, so that a tile's results leave
-// while the next is formed.  Eight epilogue warps turn 32 x 32 blocks around
-// through shared memory (a lane holds one m), so that rows leave in whole
-// sectors.
+// to 256 (17% of the work at 768 tokens an expert).
+//
+// More than 256 n (224 with 8 bits) are two halves with an accumulator each,
+// that share A in shared memory: a step brings 48 KB for 1024 cycles of
+// products where two tiles bring 64.  Both accumulators (all of TMEM) are then
+// one tile's.  So that the products need not wait while one is read out, the
+// second half runs LAG steps behind the first: the first is read out while the
+// second's last steps run, the second while the next tile's first half starts.
+// Tiles of one half alternate between the accumulators.
+//
+// Operands come by TMA with 128-byte swizzle, K-major or MN-major as they lie in
+// memory, through two rings of 16 KB slots, A's and B's.  Eight epilogue warps
+// turn 32 x 32 blocks around through shared memory (a lane holds one m), so that
+// rows leave in whole sectors.
 //
 // The groups' offsets are device data: every CTA clamps them (to the token
 // axis and the largest before them) and counts the tiles for itself.
@@ -34,14 +42,18 @@ namespace {
 
 constexpr int MT = 256;                  // m of a pair's tile
 constexpr int BOX = 64 * 128;            // 64 rows of 128 bytes
-constexpr int STAGES = 5, STAGE = 4 * BOX;
-constexpr int EPI_WARPS = 8, SLOT = 4096;
+constexpr int STAGE = 2 * BOX;           // a step's part of an operand: 128 rows of 128 bytes, or 64 of 256
+constexpr int A_SLOTS = 6, B_SLOTS = 6;
+constexpr int LAG = 2;                   // steps that a tile's second half runs behind its first
+static_assert(A_SLOTS >= LAG + B_SLOTS / 2, "a slot of A is free when the slots of B that are loaded with it are");
+constexpr int EPI_WARPS = 8, SLOT = 2048;
 constexpr int STEPS_SUM = 32;            // weight: steps of 64 tokens an accumulator takes
-constexpr int PART_WARP = 4 * 1024;      // floats of scratch of an epilogue warp
-constexpr int EPI_OFF = STAGES * STAGE;
+constexpr int PART_WARP = 2 * 4 * 1024;  // floats of scratch of an epilogue warp
+constexpr int B_OFF = A_SLOTS * STAGE;
+constexpr int EPI_OFF = B_OFF + B_SLOTS * STAGE;
 constexpr int GROUP_OFF = EPI_OFF + EPI_WARPS * SLOT;
-// 8 bits: the tokens' scales on their way, 256 of each of four blocks
-constexpr int SB_SLOTS = 4, SB_SLOT = 4 * 256;
+// 8 bits: the tokens' scales on their way, those of a tile for each of four blocks
+constexpr int SB_SLOTS = 3, SB_ROW = 448, SB_SLOT = 4 * SB_ROW;
 constexpr int SB_OFF = GROUP_OFF + 2 * 4 * (kMaxExperts + 4);
 constexpr int BAR_OFF = SB_OFF + SB_SLOTS * SB_SLOT;
 constexpr int SMEM = BAR_OFF + 512;
@@ -57,18 +69,19 @@ struct Traits {
   static constexpr int BK = k8 ? 128 : 64;                                  // 128 bytes
   static constexpr int EPI_WARP0 = k8 ? 8 : 4;
   static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-  // most n of a tile: two accumulators and, for 8 bits, the scales share 512 columns of TMEM
+  // most n of an accumulator: two and, for 8 bits, the scales share 512 columns of TMEM
   static constexpr int NT = k8 ? 224 : 256;
 };
 // The scales in TMEM, by groups of four 128-column blocks: a 32-bit word a row
-// of A (4 columns of 32 lanes) and of B (8), a byte for each block.
-constexpr int SF_SLOTS = 5, SF_COLS = 12;
+// of A (4 columns of 32 lanes) and of each half of B (8), a byte for each block.
+constexpr int SF_SLOTS = 3, SF_COLS = 20;
 static_assert(2 * Traits<PRODUCT_ACT8>::NT + SF_SLOTS * SF_COLS <= 512, "TMEM");
 
 struct alignas(16) Bars {
-  uint64_t full[STAGES];                 // the leader's, for both CTAs
-  uint64_t empty[STAGES];                // each CTA's own
-  uint64_t own[STAGES];                  // weight: this CTA's part of an expert's last step
+  // of B's slots, that of a step's first for all that it loads
+  uint64_t full[B_SLOTS];                // the leader's, for both CTAs
+  uint64_t empty[B_SLOTS];               // each CTA's own
+  uint64_t own[B_SLOTS];                 // weight: this CTA's part of an expert's last step
   uint64_t tfull[2], tempty[2];
   uint64_t sf_full[SF_SLOTS];            // 8 bits: the leader's, scales written by both CTAs
   uint64_t sf_empty[SF_SLOTS];
@@ -80,21 +93,27 @@ struct alignas(16) Bars {
 };
 static_assert(sizeof(Bars) <= 512 && SB_OFF % 16 == 0, "barrier block");
 
-// n of the tiles that a row of `len` is cut into: as few tiles as there can be,
-// of about one size where the last would be small.
-template <int NT>
-__host__ __device__ __forceinline__ int tile_n(int len, bool even) {
-  const int tiles = (len + NT - 1) / NT, rest = len % NT;
-  if (tiles <= 1) return NT;
-  if (!even && (rest == 0 || rest >= NT / 2)) return NT;
+// n of the tiles that a row of `len` is cut into, at most `most`: as few tiles as
+// there can be, of about one size (all but the last `most`, where that one is
+// not small and they need not be even).
+__host__ __device__ __forceinline__ int tile_n(int len, int most, bool even) {
+  const int tiles = (len + most - 1) / most, rest = len % most;
+  if (tiles <= 1) return most;
+  if (!even && (rest == 0 || rest >= most / 2)) return most;
   return ((len + tiles - 1) / tiles + 31) / 32 * 32;
 }
 
 struct Tile {
   int e, m0, n0;       // group, first m, first n (of the token axis, or of the outputs)
   int n;               // that exist
+  int first;           // of them in the first half (n: there is no second)
   int t0, len;         // weight: the group's first token and tokens
   int steps;
+
+  __device__ __forceinline__ int halves() const { return first < n ? 2 : 1; }
+  // of half h: how many n, and the n that the product takes
+  __device__ __forceinline__ int count(int h) const { return h == 0 ? first : n - first; }
+  __device__ __forceinline__ int padded(int h) const { return (count(h) + 31) / 32 * 32; }
 };
 
 // The tiles in order of their groups; a thread asks for rising numbers.
@@ -109,7 +128,7 @@ struct Tiles {
     mt = (p.m + MT - 1) / MT;
     total = Traits<KIND>::kTokens ? pre[p.groups] : p.groups * mt * ((p.n + nsize() - 1) / nsize());
   }
-  __device__ __forceinline__ int nsize() const { return tile_n<Traits<KIND>::NT>(p.n, false); }
+  __device__ __forceinline__ int nsize() const { return tile_n(p.n, p.most, false); }
   // A group's tiles go eight m at a time: the pairs that run together share
   // panels of A and of B in L2.
   __device__ __forceinline__ void place(int in, int nt, int& m0, int& n0, int size) const {
@@ -117,11 +136,12 @@ struct Tiles {
     m0 = (band * 8 + r - j * rows) * MT;
     n0 = j * size;
   }
+  // (by way of shuffles: one tile for the warp)
   __device__ __forceinline__ Tile get(int i) {
     Tile t;
     if constexpr (Traits<KIND>::kTokens) {
       while (pre[e + 1] <= i) ++e;
-      const int len = at[e + 1] - at[e], size = tile_n<Traits<KIND>::NT>(len, true);
+      const int len = at[e + 1] - at[e], size = tile_n(len, p.most, true);
       t.e = e;
       place(i - pre[e], (len + size - 1) / size, t.m0, t.n0, size);
       t.n0 += at[e];
@@ -137,6 +157,14 @@ struct Tiles {
       t.len = at[t.e + 1] - t.t0;
       t.steps = (t.len + Traits<KIND>::BK - 1) / Traits<KIND>::BK;
     }
+    t.n = __shfl_sync(0xffffffffu, t.n, 0);
+    t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);
+    t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+    t.e = __shfl_sync(0xffffffffu, t.e, 0);
+    t.t0 = __shfl_sync(0xffffffffu, t.t0, 0);
+    t.len = __shfl_sync(0xffffffffu, t.len, 0);
+    t.steps = __shfl_sync(0xffffffffu, t.steps, 0);
+    t.first = t.n <= Traits<KIND>::NT ? t.n : ((t.n + 1) / 2 + 31) / 32 * 32;
     return t;
   }
 };
@@ -162,7 +190,7 @@ __device__ __forceinline__ void count_tiles(const ProductParams& p, int* at) {
     if constexpr (Traits<KIND>::kTokens) {
       const int len = v - before;
       if (len > 0) {
-        const int size = tile_n<Traits<KIND>::NT>(len, true);
+        const int size = tile_n(len, p.most, true);
         c = (len + size - 1) / size * mt;
       }
 #pragma unroll
@@ -195,6 +223,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// An arrival on a barrier of the pair that orders no memory: the accumulator has
+// been read into registers.  (With a release it waited 950 cycles for the stores
+// of the results before.)
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Scales of a group of blocks to the 32 TMEM lanes of a warp.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t w) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr), "r"(w) : "memory");
@@ -206,17 +241,148 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* w) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Pair product of e4m3 codes; the scales' columns, a power of two a row and 32 k.
-__device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb,
-                                                uint32_t acc) {
+// What a whole warp issues, by one of its lanes: the lanes stay together, so that
+// addresses and coordinates are kept in uniform registers, which these
+// instructions take.  (Loops of a single lane took 550 cycles a step and more.)
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
   asm volatile(
       "{\n"
-      " .reg .pred p, q;\n"
+      " .reg .pred q;\n"
       " elect.sync _|q, 0xffffffff;\n"
-      " setp.ne.b32 p, %6, 0;\n"
-      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n"
+      " @q mbarrier.arrive.shared::cta.b64 _, [%0];\n"
+      "}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void warp_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n"
+      " .reg .pred q;\n"
+      " elect.sync _|q, 0xffffffff;\n"
+      " @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+      "}\n" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+// PAIR: `bar` is the leader's (a shared::cluster address), else this CTA's
+template <bool PAIR>
+__device__ __forceinline__ void warp_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n"
+        " .reg .pred q;\n"
+        " elect.sync _|q, 0xffffffff;\n"
+        " @q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];\n"
+        "}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "{\n"
+        " .reg .pred q;\n"
+        " elect.sync _|q, 0xffffffff;\n"
+        " @q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
+        "}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Commits of the products so far to one or two barriers, of both CTAs.
+template <bool TWO>
+__device__ __forceinline__ void warp_commit(uint32_t bar, uint32_t other) {
+  asm volatile(
+      "{\n"
+      " .reg .pred q;\n"
+      " .reg .b16 m;\n"
+      " elect.sync _|q, 0xffffffff;\n"
+      " mov.b16 m, 3;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n"
+      "}\n" ::"r"(bar)
+      : "memory");
+  if constexpr (TWO) warp_commit<false>(other, 0u);
+}
+
+// A step's products of a pair, up to four of 32 bytes of k.  Descriptors by their
+// low words (the high ones do not change); ADV: from one product's operands to
+// the next, in their units of 16 bytes.
+template <int ADV_A, int ADV_B, bool RAGGED>
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi, uint32_t id,
+                                         uint32_t acc, int count) {
+  if constexpr (RAGGED) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, q, t, q1, q2, q3;\n"
+        " .reg .b64 a, b;\n"
+        " elect.sync _|q, 0xffffffff;\n"
+        " setp.ne.b32 p, %6, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n"
+        " setp.gt.and.s32 q1, %7, 1, q;\n"
+        " setp.gt.and.s32 q2, %7, 2, q;\n"
+        " setp.gt.and.s32 q3, %7, 3, q;\n"
+        " mov.b64 a, {%1, %2};\n"
+        " mov.b64 b, {%3, %4};\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n"
+        " add.s64 a, a, %8;\n"
+        " add.s64 b, b, %9;\n"
+        " @q1 tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+        " add.s64 a, a, %8;\n"
+        " add.s64 b, b, %9;\n"
+        " @q2 tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+        " add.s64 a, a, %8;\n"
+        " add.s64 b, b, %9;\n"
+        " @q3 tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(id), "r"(acc), "r"(count), "n"(ADV_A), "n"(ADV_B)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, q, t;\n"
+        " .reg .b64 a, b;\n"
+        " elect.sync _|q, 0xffffffff;\n"
+        " setp.ne.b32 p, %6, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n"
+        " mov.b64 a, {%1, %2};\n"
+        " mov.b64 b, {%3, %4};\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n"
+        " add.s64 a, a, %7;\n"
+        " add.s64 b, b, %8;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+        " add.s64 a, a, %7;\n"
+        " add.s64 b, b, %8;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+        " add.s64 a, a, %7;\n"
+        " add.s64 b, b, %8;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(id), "r"(acc), "n"(ADV_A), "n"(ADV_B)
+        : "memory");
+  }
+}
+// The same of e4m3 codes, with the scales in TMEM columns sa and sb, a power of
+// two a row and 32 k.
+__device__ __forceinline__ void mma_step_scaled(uint32_t d, uint32_t a, uint32_t ahi, uint32_t b, uint32_t bhi, uint32_t id,
+                                                uint32_t sa, uint32_t sb, uint32_t acc) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p, q, t;\n"
+      " .reg .b64 a, b;\n"
+      " elect.sync _|q, 0xffffffff;\n"
+      " setp.ne.b32 p, %8, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %2};\n"
+      " mov.b64 b, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], a, b, %5, [%6], [%7], p;\n"
+      " add.s64 a, a, 2;\n"
+      " add.s64 b, b, 2;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], a, b, %5, [%6], [%7], t;\n"
+      " add.s64 a, a, 2;\n"
+      " add.s64 b, b, 2;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], a, b, %5, [%6], [%7], t;\n"
+      " add.s64 a, a, 2;\n"
+      " add.s64 b, b, 2;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], a, b, %5, [%6], [%7], t;\n"
       "}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(acc)
+      "r"(a), "r"(ahi), "r"(b), "r"(bhi), "r"(id), "r"(sa), "r"(sb), "r"(acc)
       : "memory");
 }
 
@@ -242,51 +408,84 @@ __device__ __forceinline__ void load4(const void* base, long long i, int dtype, 
   }
 }
 
-// A 32 x 32 block of results to rows `rows` of 32 m from (out, add): lane l
-// holds m = l, v[j] is row j.  Rows past `rows` and m past `ms` are not there.
-// 16-bit results without `add` go through shared memory as pairs: lanes 2i and
-// 2i + 1 exchange, so that each has two consecutive m of one row.
+// 32 m (TMEM lanes) x 32 n (columns) of results, spread over the warp in 8 x 8
+// tiles as the matrix instructions' accumulators are, rounded to T, two n in a
+// register: w[8 a + 2 j + b] of thread t is m = 16 a + 8 b + t / 4, n = 8 j + 2
+// (t % 4) and the next.
+template <typename T>
+__device__ __forceinline__ void tmem_block(uint32_t taddr, uint32_t* w) {
+  float v[2][16];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[a][0]), "=f"(v[a][1]), "=f"(v[a][2]), "=f"(v[a][3]), "=f"(v[a][4]), "=f"(v[a][5]), "=f"(v[a][6]),
+          "=f"(v[a][7]), "=f"(v[a][8]), "=f"(v[a][9]), "=f"(v[a][10]), "=f"(v[a][11]), "=f"(v[a][12]), "=f"(v[a][13]),
+          "=f"(v[a][14]), "=f"(v[a][15])
+        : "r"(taddr + (static_cast<uint32_t>(16 * a) << 16)));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[8 * a + j] = pack2<T>(v[a][2 * j], v[a][2 * j + 1]);
+}
+
+// Such a block to `rows` rows (n) of 32 m at `to`: tiles are stored to shared
+// memory transposed, rows of 64 bytes with their 16-byte parts swizzled.
+__device__ __forceinline__ void store_packed(uint32_t slot, const uint32_t* w, uint16_t* to, long long ld, int rows, int lane) {
+  __syncwarp();
+  // w[8 a + 2 j + b]: the tile of m 16 a + 8 b .., n 8 j ..; a lane gives row
+  // lane % 8 (n) of tile lane / 8 of the four that an instruction stores
+  const int b = (lane >> 3) & 1, j = lane >> 4;
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int n = 16 * h + 8 * j + (lane & 7), part = 2 * a + b;
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                       slot + n * 64 + ((part ^ ((n >> 1) & 3)) << 4)),
+                   "r"(w[8 * a + 4 * h]), "r"(w[8 * a + 4 * h + 1]), "r"(w[8 * a + 4 * h + 2]), "r"(w[8 * a + 4 * h + 3])
+                   : "memory");
+    }
+  __syncwarp();
+  const int r = lane >> 2, q = lane & 3;
+  uint4 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = lds16(slot + (r + 8 * i) * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (r + 8 * i < rows) *reinterpret_cast<uint4*>(to + (r + 8 * i) * ld + q * 8) = x[i];
+}
+
+// The block in fp32, v[j] row j, to rows of 32 m from (out, add), of any type and
+// place.  Rows past `rows` and m past `ms` are not there.
 __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slot, const float* v, long long out,
                                             long long add, int rows, int ms, int lane) {
   const uint32_t s = smem_u32(slot);
   __syncwarp();
-  if (p.vec && ms >= 32 && p.odtype != DT_F32 && p.add == nullptr) {
-    const uint32_t to = s + (lane & 1) * 64 + (lane >> 1) * 4, sel = lane & 1 ? 0x3276u : 0x5410u;
-    const bool bf = p.odtype == DT_BF16;
+  // 16 rows at a time
+  const bool wide = p.vec && ms >= 32;
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const uint32_t w = bf ? pack2<__nv_bfloat16>(v[j], v[j + 1]) : pack2<__half>(v[j], v[j + 1]);
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + j * 64), "r"(__byte_perm(w, o, sel)) : "memory");
-    }
+  for (int h = 0; h < 32; h += 16) {
+    if (h > 0) __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s + j * 128 + lane * 4), "f"(v[h + j]) : "memory");
     __syncwarp();
-    const int r = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      if (r + i < rows)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out + (r + i) * p.ldo + q * 8) = lds16(s + (r + i) * 64 + q * 16);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 32; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s + j * 128 + lane * 4), "f"(v[j]) : "memory");
-  __syncwarp();
-  if (p.vec && ms >= 32) {
-    const int r = lane >> 3, q = lane & 7;
-#pragma unroll
-    for (int h = 0; h < 32; h += 16) {
+    if (wide) {
+      const int r = h + (lane >> 3), q = lane & 7;
       float f[4][4];
       if (p.add != nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (r + h + 4 * i < rows) load4(p.add, add + (r + h + 4 * i) * p.ldadd + q * 4, p.odtype, f[i]);
+          if (r + 4 * i < rows) load4(p.add, add + (r + 4 * i) * p.ldadd + q * 4, p.odtype, f[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (r + h + 4 * i >= rows) break;
-        const uint4 raw = lds16(s + (r + h + 4 * i) * 128 + q * 16);
+        if (r + 4 * i >= rows) break;
+        const uint4 raw = lds16(s + (r - h + 4 * i) * 128 + q * 16);
         float4 x = make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w));
         if (p.add != nullptr) x.x += f[i][0], x.y += f[i][1], x.z += f[i][2], x.w += f[i][3];
-        const long long to = out + (r + h + 4 * i) * p.ldo + q * 4;
+        const long long to = out + (r + 4 * i) * p.ldo + q * 4;
         if (p.odtype == DT_F32)
           *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = x;
         else
@@ -294,16 +493,14 @@ __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slo
               p.odtype == DT_BF16 ? make_uint2(pack2<__nv_bfloat16>(x.x, x.y), pack2<__nv_bfloat16>(x.z, x.w))
                                   : make_uint2(pack2<__half>(x.x, x.y), pack2<__half>(x.z, x.w));
       }
-    }
-    return;
-  }
-  if (lane < ms) {
+    } else if (lane < ms) {
 #pragma unroll 1
-    for (int j = 0; j < 32 && j < rows; ++j) {
-      float x;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(s + j * 128 + lane * 4));
-      if (p.add != nullptr) x += load_f32(p.add, add + j * p.ldadd + lane, p.odtype);
-      store_any(p.out, out + j * p.ldo + lane, p.odtype, x);
+      for (int j = h; j < h + 16 && j < rows; ++j) {
+        float x;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(s + (j - h) * 128 + lane * 4));
+        if (p.add != nullptr) x += load_f32(p.add, add + j * p.ldadd + lane, p.odtype);
+        store_any(p.out, out + j * p.ldo + lane, p.odtype, x);
+      }
     }
   }
 }
@@ -320,6 +517,49 @@ __device__ __forceinline__ void zero_rows(const ProductParams& p, int from, int 
   }
 }
 
+// The order of a tile's products.  Step s loads the first half's part k = s of
+// A and B and the second half's part k = s - LAG of B (A's is there), a slot of B
+// each.  Steps go in runs of n that are alike: f(first, second, k0, k1, n), with
+// constants that say which halves have products and their first k, says whether to
+// go on.  LAST: a half's last step is a run of its own.  EVERY: a run ends where a
+// half's k is a multiple of it (0: nowhere).
+template <bool LAST, int EVERY, typename F>
+__device__ __forceinline__ void runs_of(const Tile& t, F&& f) {
+  const bool two = t.halves() == 2;
+  const int end = two && t.steps > 0 ? t.steps + LAG : t.steps;
+  for (int s = 0; s < end;) {
+    const bool first = s < t.steps, second = two && s >= LAG;
+    const int k1 = s - LAG;
+    int n = first ? t.steps - s : end - s;
+    if (two && s < LAG) n = min(n, LAG - s);
+    if (LAST && n > 1 && ((first && s + n == t.steps) || (second && k1 + n == t.steps))) --n;
+    if constexpr (EVERY > 0) {
+      if (first) n = min(n, EVERY - s % EVERY);
+      if (second) n = min(n, EVERY - k1 % EVERY);
+    }
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
+    bool ok = true;
+    if (first && second)
+      ok = f(Yes{}, Yes{}, s, k1, n);
+    else if (first)
+      ok = f(Yes{}, No{}, s, k1, n);
+    else if (second)
+      ok = f(No{}, Yes{}, s, k1, n);
+    if (!ok) return;
+    s += n;
+  }
+}
+// Slots of B that a tile's steps before s take.
+__device__ __forceinline__ int slots_before(const Tile& t, int s) {
+  return min(s, t.steps) + (t.halves() == 2 ? max(0, s - LAG) : 0);
+}
+
+// An expert's last tokens, where the products take some that are not its own.
+template <int KIND>
+__device__ __forceinline__ bool mended(const Tile& t, int k) {
+  return KIND == PRODUCT_WEIGHT && k == t.steps - 1 && (t.len & 15) != 0;
+}
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
@@ -328,12 +568,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + BAR_OFF);
   int* at = reinterpret_cast<int*>(smem + GROUP_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (by way of a shuffle: known to be one for the warp, so that what follows from
+  // it is kept in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(cluster_id_x()), npairs = static_cast<int>(num_clusters_x());
   const uint32_t sb = smem_u32(smem);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < B_SLOTS; ++s) {
       mbar_init(&bar->full[s], KIND == PRODUCT_WEIGHT ? 2 : 1);
       mbar_init(&bar->empty[s], 1);
       mbar_init(&bar->own[s], 1);
@@ -361,74 +603,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = bar->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
   volatile int* abort = &bar->abort;
   Tiles<KIND> tiles(p, at);
 
   if (warp == 0 || warp == 3) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ loads
-      // Warp 0 loads A and says what is to come, warp 3 loads B, in few large
-      // boxes: a thread issues a load in some 200 cycles, a step's products
-      // take 512.
-      const bool is_a = warp == 0;
-      const uint32_t lead = mapa_shared(smem_u32(&bar->full[0]), 0);
-      Ring<STAGES> r;
-      bool ok = true;
-      for (int i = pair; ok && i < tiles.total; i += npairs) {
-        const Tile t = tiles.get(i);
-        const int m0 = t.m0 + static_cast<int>(rank) * 128;
-        // of B, this CTA's half: boxes of 128 or 32 tokens, or of 64 outputs
-        const int half = (t.n + 31) / 32 * 16, n0 = t.n0 + static_cast<int>(rank) * half;
-        const bool one = !T::kBmn && half > 64;
-        const int boxes = one ? 1 : T::kBmn ? (half + 63) / 64 : (half + 31) / 32;
-        const uint32_t bytes = 2 * BOX + boxes * (one ? 2 * BOX : T::kBmn ? BOX : BOX / 2);
-        for (int k = 0; k < t.steps; ++k) {
-          ok = wait_one(&bar->empty[r.s], r.ph ^ 1u, abort, p);
-          if (!ok) break;
-          const uint32_t a = sb + r.s * STAGE, b = a + 2 * BOX, fb = lead + r.s * 8;
-          if constexpr (KIND == PRODUCT_WEIGHT) {
-            const int row = t.t0 + k * 64;
-            if (k == t.steps - 1 && (t.len & 15) != 0) {
-              // an expert's last tokens: to this CTA's own warp, which clears
-              // what follows them (see below)
-              uint64_t* own = &bar->own[r.s];
-              if (is_a) {
-                mbar_arrive_expect_tx(own, bytes);
-                if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], sizeof(uint4));
-                tma_load_3d(a, &ma, own, m0, row, 0);
-                tma_load_3d(a + BOX, &ma, own, m0 + 64, row, 0);
-              } else {
-                for (int c = 0; c < boxes; ++c) tma_load_3d(b + c * BOX, &mb, own, n0 + c * 64, row, 0);
-              }
-            } else if (is_a) {
-              if (rank == 0) {
-                mbar_arrive(&bar->full[r.s]);
-                mbar_arrive_expect_tx(&bar->full[r.s], 2 * bytes);
-              }
-              tma_load_3d_pair(a, &ma, fb, m0, row, 0);
-              tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, row, 0);
-            } else {
-              for (int c = 0; c < boxes; ++c) tma_load_3d_pair(b + c * BOX, &mb, fb, n0 + c * 64, row, 0);
-            }
-          } else if (is_a) {
-            if (rank == 0) mbar_arrive_expect_tx(&bar->full[r.s], 2 * bytes);
-            if constexpr (T::kAmn) {
-              tma_load_3d_pair(a, &ma, fb, m0, k * T::BK, t.e);
-              tma_load_3d_pair(a + BOX, &ma, fb, m0 + 64, k * T::BK, t.e);
-            } else {
-              tma_load_3d_pair(a, &ma, fb, k * T::BK, m0, t.e);
-            }
-          } else if (one) {
-            tma_load_3d_pair(b, &mb, fb, k * T::BK, n0, 0);
-          } else {
-            for (int c = 0; c < boxes; ++c) tma_load_3d_pair(b + c * (BOX / 2), &mb32, fb, k * T::BK, n0 + c * 32, 0);
-          }
-          r.next();
+    // -------------------------------------------------------------- loads
+    // Warp 0 loads A and says what a step brings, warp 3 loads B, in few large
+    // boxes.
+    const uint32_t lead = mapa_shared(smem_u32(&bar->full[0]), 0), here = smem_u32(&bar->full[0]),
+                   owns = smem_u32(&bar->own[0]);
+    Ring<A_SLOTS> ra;
+    Ring<B_SLOTS> r;
+    bool ok = true;
+    for (int i = pair; ok && i < tiles.total; i += npairs) {
+      const Tile t = tiles.get(i);
+      // of B, this CTA's part of a half, in boxes of 128 or 32 tokens, or of 64 outputs
+      const int part0 = t.padded(0) / 2, part1 = t.padded(1) / 2;
+      const int n0 = t.n0 + static_cast<int>(rank) * part0, n1 = t.n0 + t.first + static_cast<int>(rank) * part1;
+      auto bytes = [&](int part) {
+        return static_cast<uint32_t>(T::kBmn ? (part + 63) / 64 * BOX : part > 64 ? 2 * BOX : (part + 31) / 32 * (BOX / 2));
+      };
+      const uint32_t b0 = STAGE + bytes(part0), b1 = bytes(part1);       // a step's for each half, A with the first
+      const int m0 = t.m0 + static_cast<int>(rank) * 128;
+      auto load_b = [&](auto own, int part, int at, int k, uint32_t to, uint32_t fb) {
+        constexpr bool PAIR = !decltype(own)::value;
+        if constexpr (T::kBmn) {
+          for (int c = 0; c < part; c += 64) warp_load<PAIR>(to + c * 128, &mb, fb, at + c, t.t0 + k * 64, 0);
+        } else if (part > 64) {
+          warp_load<PAIR>(to, &mb, fb, k * T::BK, at, 0);
+        } else {
+          for (int c = 0; c < part; c += 32) warp_load<PAIR>(to + c * 128, &mb32, fb, k * T::BK, at + c, 0);
         }
-      }
+      };
+      auto load_a = [&](auto own, int k, uint32_t to, uint32_t fb) {
+        constexpr bool PAIR = !decltype(own)::value;
+        if constexpr (T::kAmn) {
+          const int row = KIND == PRODUCT_WEIGHT ? t.t0 + k * 64 : k * 64, e = KIND == PRODUCT_WEIGHT ? 0 : t.e;
+          warp_load<PAIR>(to, &ma, fb, m0, row, e);
+          warp_load<PAIR>(to + BOX, &ma, fb, m0 + 64, row, e);
+        } else {
+          warp_load<PAIR>(to, &ma, fb, k * T::BK, m0, t.e);
+        }
+      };
+      using Own = std::integral_constant<bool, true>;
+      using Pair = std::integral_constant<bool, false>;
+      runs_of<KIND == PRODUCT_WEIGHT, 0>(t, [&](auto first, auto second, int k0, int k1, int n) {
+        constexpr bool D0 = decltype(first)::value, D1 = decltype(second)::value;
+        // an expert's last tokens go to this CTA's own warp, which clears what
+        // follows them (see below)
+        const bool own0 = D0 && mended<KIND>(t, k0), own1 = D1 && mended<KIND>(t, k1);
+        const uint32_t mine = (own0 ? b0 : 0u) + (own1 ? b1 : 0u);
+        const uint32_t both = 2 * ((D0 ? b0 : 0u) + (D1 ? b1 : 0u) - mine) + (mine > 0 ? static_cast<uint32_t>(sizeof(uint4)) : 0u);
+#pragma unroll 1
+        for (; n > 0; --n) {
+          ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
+          if (!ok) return false;
+          const uint32_t fb = lead + r.s * 8, ob = owns + r.s * 8, to0 = sb + B_OFF + r.s * STAGE;
+          if (warp == 0) {
+            if (KIND == PRODUCT_WEIGHT && mine > 0) warp_expect(ob, mine);
+            if (rank == 0) {
+              // (the weight's barriers count two arrivals, one of them the clearing warp's)
+              if (KIND == PRODUCT_WEIGHT && mine == 0) warp_arrive(here + r.s * 8);
+              warp_expect(here + r.s * 8, both);
+            }
+            if constexpr (D0) {
+              if (KIND == PRODUCT_WEIGHT && own0)
+                load_a(Own{}, k0, sb + ra.s * STAGE, ob);
+              else
+                load_a(Pair{}, k0, sb + ra.s * STAGE, fb);
+              ra.next();
+            }
+          } else if constexpr (D0) {
+            if (KIND == PRODUCT_WEIGHT && own0)
+              load_b(Own{}, part0, n0, k0, to0, ob);
+            else
+              load_b(Pair{}, part0, n0, k0, to0, fb);
+          }
+          if constexpr (D0) r.next();
+          if constexpr (D1) {
+            uint32_t to1 = to0;
+            if constexpr (D0) {
+              ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
+              if (!ok) return false;
+              to1 = sb + B_OFF + r.s * STAGE;
+              if (warp == 0 && rank == 0) {
+                warp_arrive(here + r.s * 8);       // nothing waits for it: its phase goes on
+                if (KIND == PRODUCT_WEIGHT) warp_arrive(here + r.s * 8);
+              }
+            }
+            if (warp == 3) {
+              if (KIND == PRODUCT_WEIGHT && own1)
+                load_b(Own{}, part1, n1, k1, to1, ob);
+              else
+                load_b(Pair{}, part1, n1, k1, to1, fb);
+            }
+            r.next();
+          }
+          ++k0;
+          ++k1;
+        }
+        return true;
+      });
     }
-    __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       // --------------------------------------------------------- products
@@ -436,57 +713,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // and 29 (A)
       const uint32_t type = T::k8 ? 1u << 23 : (1u << 4) | (p.f16 ? 0u : (1u << 7) | (1u << 10));
       const uint32_t id0 = type | (T::kAmn ? 1u << 15 : 0u) | (T::kBmn ? 1u << 16 : 0u) | ((MT >> 4) << 24);
-      Ring<SF_SLOTS> rs;
-      Ring<STAGES> r;
-      int acc = 0;
-      uint32_t acc_ph = 0;
+      // a ring's place for each half: A's slots and the scales' are used by both
+      Ring<SF_SLOTS> rs[2];
+      Ring<A_SLOTS> ra[2];
+      Ring<B_SLOTS> rb;
+      const uint64_t a0 = T::kAmn ? sdesc_sw128(sb, BOX, 1024) : sdesc_sw128(sb, 16, 1024);
+      const uint64_t b0 = T::kBmn ? sdesc_sw128(sb + B_OFF, BOX, 1024) : sdesc_sw128(sb + B_OFF, 16, 1024);
+      const uint32_t alo = static_cast<uint32_t>(a0), ahi = static_cast<uint32_t>(a0 >> 32), blo = static_cast<uint32_t>(b0),
+                     bhi = static_cast<uint32_t>(b0 >> 32), empty0 = smem_u32(&bar->empty[0]);
+      int cur = 0;                       // the accumulator of the tile's first half
+      uint32_t ph = 0u;                  // the accumulators' phases, a bit each
       bool ok = true;
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
-        const uint32_t id = id0 | (static_cast<uint32_t>((t.n + 31) / 32 * 4) << 17);
-        const int part = KIND == PRODUCT_WEIGHT ? STEPS_SUM : t.steps;
-        for (int k0 = 0; ok && k0 < t.steps; k0 += part) {
-          ok = wait_warp<0, true>(&bar->tempty[acc], acc_ph ^ 1u, abort, p);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + acc * T::NT;
-          const int k1 = min(k0 + part, t.steps);
-          for (int k = k0; k < k1; ++k) {
-            ok = wait_warp<0, KIND == PRODUCT_WEIGHT>(&bar->full[r.s], r.ph, abort, p);
-            if (!ok) break;
-            if constexpr (T::k8) {
-              if ((k & 3) == 0) ok = wait_warp<0, true>(&bar->sf_full[rs.s], rs.ph, abort, p);
-              if (!ok) break;
-            }
-            tc_fence_after();
-            const uint32_t sa = sb + r.s * STAGE;
-            const uint64_t a = T::kAmn ? sdesc_sw128(sa, BOX, 1024) : sdesc_sw128(sa, 16, 1024);
-            const uint64_t b = T::kBmn ? sdesc_sw128(sa + 2 * BOX, BOX, 1024) : sdesc_sw128(sa + 2 * BOX, 16, 1024);
-            // steps of 16 k: two rows of 8 in an MN-major operand, 32 bytes of a K-major one
-            const int kks = KIND == PRODUCT_WEIGHT ? (min(t.len - k * 64, 64) + 15) / 16 : 4;
-            if constexpr (T::k8) {
-              const uint32_t sf = tmem + 2 * T::NT + rs.s * SF_COLS, ids = id | ((k & 3u) << 4) | ((k & 3u) << 29);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_pair_scaled(d, a + kk * 2, b + kk * 2, ids, sf, sf + 4, kk != 0 || k != k0 ? 1u : 0u);
-              if ((k & 3) == 3 || k == k1 - 1) {
-                commit_pair(&bar->sf_empty[rs.s], 0x3);
-                rs.next();
-              }
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                if (kk < kks)
-                  mma_pair(d, a + kk * (T::kAmn ? 2048 >> 4 : 2), b + kk * (T::kBmn ? 2048 >> 4 : 2), id,
-                           kk != 0 || k != k0 ? 1u : 0u);
-            }
-            commit_pair(&bar->empty[r.s], 0x3);
-            r.next();
+        const bool two = t.halves() == 2;
+        const uint32_t ids[2] = {id0 | (static_cast<uint32_t>(t.padded(0) >> 3) << 17),
+                                 id0 | (static_cast<uint32_t>(t.padded(1) >> 3) << 17)};
+        constexpr int PART = KIND == PRODUCT_WEIGHT ? STEPS_SUM : 1 << 30;   // steps that an accumulator takes
+        // part k of half h from the slot of B at rb
+        auto products = [&](auto half, int k) {
+          constexpr int h = decltype(half)::value;
+          const uint32_t d = tmem + (cur ^ h) * T::NT, a = alo + ra[h].s * (STAGE >> 4), b = blo + rb.s * (STAGE >> 4);
+          // of 16 k: two rows of 8 in an MN-major operand, 32 bytes of a K-major one
+          if constexpr (T::k8) {
+            const uint32_t sf = tmem + 2 * T::NT + rs[h].s * SF_COLS;
+            mma_step_scaled(d, a, ahi, b, bhi, ids[h] | ((k & 3u) << 4) | ((k & 3u) << 29), sf, sf + 4 + 8 * h, k);
+          } else {
+            mma_step<T::kAmn ? 2048 >> 4 : 2, T::kBmn ? 2048 >> 4 : 2, KIND == PRODUCT_WEIGHT>(
+                d, a, ahi, b, bhi, ids[h], k % PART, (min(t.len - k * 64, 64) + 15) / 16);
           }
-          if (!ok) break;
-          commit_pair(&bar->tfull[acc], 0x3);
-          acc ^= 1;
-          if (acc == 0) acc_ph ^= 1u;
+          ra[h].next();
+        };
+        // a part's first products wait for the accumulator, its last hand it over
+        auto begins = [&](int h, int k) {
+          if (k % PART != 0) return true;
+          const bool ready = wait_warp<0, true>(&bar->tempty[cur ^ h], ((ph >> (cur ^ h)) & 1u) ^ 1u, abort, p);
+          tc_fence_after();
+          return ready;
+        };
+        auto ends = [&](auto half, int k) {
+          constexpr int h = decltype(half)::value;
+          if constexpr (T::k8) {
+            if ((k & 3) == 0 || k == t.steps) {    // the scales of a group of blocks are used
+              if (h == 1 || !two) warp_commit<false>(smem_u32(&bar->sf_empty[rs[h].s]), 0u);
+              rs[h].next();
+            }
+          }
+          if (k % PART != 0 && k != t.steps) return;
+          warp_commit<false>(smem_u32(&bar->tfull[cur ^ h]), 0u);
+          ph ^= 1u << (cur ^ h);
+        };
+        runs_of<false, KIND == PRODUCT_WEIGHT ? PART : T::k8 ? 4 : 0>(t, [&](auto first, auto second, int k0, int k1, int n) {
+          constexpr bool D0 = decltype(first)::value, D1 = decltype(second)::value;
+          if constexpr (D0) ok = begins(0, k0);
+          if constexpr (D1) ok = ok && begins(1, k1);
+          if constexpr (T::k8 && D0) {
+            if (ok && (k0 & 3) == 0) {
+              ok = wait_warp<0, true>(&bar->sf_full[rs[0].s], rs[0].ph, abort, p);
+              tc_fence_after();
+            }
+          }
+#pragma unroll 1
+          for (; ok && n > 0; --n) {
+            ok = wait_warp<0, KIND == PRODUCT_WEIGHT>(&bar->full[rb.s], rb.ph, abort, p);
+            if (!ok) break;
+            const uint32_t free0 = empty0 + rb.s * 8;
+            if constexpr (D0) {
+              products(std::integral_constant<int, 0>{}, k0);
+              rb.next();
+            }
+            if constexpr (D1) {
+              const uint32_t free1 = empty0 + rb.s * 8;
+              products(std::integral_constant<int, 1>{}, k1);
+              rb.next();
+              warp_commit<D0>(free0, free1);
+            } else {
+              warp_commit<false>(free0, 0u);
+            }
+            ++k0;
+            ++k1;
+          }
+          if (!ok) return false;
+          if constexpr (D0) ends(std::integral_constant<int, 0>{}, k0);
+          if constexpr (D1) ends(std::integral_constant<int, 1>{}, k1);
+          return true;
+        });
+        if (!two) {
+          ra[1] = ra[0];
+          rs[1] = rs[0];
+          if (t.steps > 0) cur ^= 1;
         }
       }
       commit_pair(&bar->drain, 0x1);
@@ -495,14 +810,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     __syncwarp();
   } else if (warp == 2 && T::k8) {
     if constexpr (T::k8) {
-      // The tokens' scales, 256 bytes for each of four blocks.  (Loaded by the
+      // The tokens' scales, SB_ROW bytes for each of four blocks.  (Loaded by the
       // warps that use them, one group ahead, they were waited for 2700 cycles a
       // group, whose products take 1800.)
       Ring<SB_SLOTS> rb;
       bool ok = true;
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
-        const uint32_t bytes = static_cast<uint32_t>(min(256, (p.tokens - t.n0 + 15) / 16 * 16));
+        const uint32_t bytes = static_cast<uint32_t>(min(SB_ROW, (p.tokens - t.n0 + 15) / 16 * 16));
         for (int k0 = 0; k0 < t.steps; k0 += 4) {
           ok = wait_warp(&bar->sb_empty[rb.s], rb.ph ^ 1u, abort, p);
           if (!ok) break;
@@ -510,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           if (lane == 0) mbar_arrive_expect_tx(&bar->sb_full[rb.s], bytes * live);
           __syncwarp();
           if (lane < live)
-            bulk_load(sb + SB_OFF + rb.s * SB_SLOT + lane * 256, p.scales + (k0 + lane) * p.lds + t.n0, bytes,
+            bulk_load(sb + SB_OFF + rb.s * SB_SLOT + lane * SB_ROW, p.scales + (k0 + lane) * p.lds + t.n0, bytes,
                       smem_u32(&bar->sb_full[rb.s]));
           rb.next();
         }
@@ -524,23 +839,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // cleared, in both operands: what they hold may be infinite or NaN.
       const uint32_t full = mapa_shared(smem_u32(&bar->full[0]), 0), to = mapa_shared(smem_u32(&bar->token[1]), 0);
       uint32_t phases = 0;               // of own[], a bit each
-      int s = 0;                         // the tile's first stage
+      int sa = 0, sbb = 0;               // the tile's first slots
       bool ok = true;
+      auto clear = [&](uint32_t base, int boxes, int rest) {
+        const int rows = 16 - (rest & 15);
+        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+        for (int c = lane; c < rows * boxes * 8; c += 32) {
+          const int box = c / (rows * 8), in = c - box * rows * 8;
+          sts16(base + box * BOX + rest * 128 + in * 16, zero);
+        }
+      };
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
         if (t.steps == 0) continue;
-        s = (s + t.steps - 1) % STAGES;
-        const int rest = t.len & 63, first = rest;
-        if ((rest & 15) != 0) {
+        for (int h = 0; ok && h < t.halves() && mended<KIND>(t, t.steps - 1); ++h) {
+          const int s = (sbb + slots_before(t, t.steps - 1 + h * LAG)) % B_SLOTS, rest = t.len & 63;
           ok = wait_warp(&bar->own[s], (phases >> s) & 1u, abort, p);
           if (!ok) break;
           phases ^= 1u << s;
-          const int rows = 16 - (rest & 15), boxes = 2 + ((t.n + 31) / 32 * 16 + 63) / 64;
-          const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-          for (int c = lane; c < rows * boxes * 8; c += 32) {
-            const int box = c / (rows * 8), in = c - box * rows * 8;
-            sts16(sb + s * STAGE + box * BOX + first * 128 + in * 16, zero);
-          }
+          if (h == 0) clear(sb + (sa + t.steps - 1) % A_SLOTS * STAGE, 2, rest);
+          clear(sb + B_OFF + s * STAGE, (t.padded(h) / 2 + 63) / 64, rest);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -551,7 +869,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           }
           __syncwarp();
         }
-        s = (s + 1) % STAGES;
+        sa = (sa + t.steps) % A_SLOTS;
+        sbb = (sbb + t.halves() * t.steps) % B_SLOTS;
       }
     }
   } else if (T::k8 && warp >= 4 && warp < T::EPI_WARP0) {
@@ -560,7 +879,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // lanes of TMEM holds all of them.  The product reads its CTA's own copy,
       // of all n.  (What is behind the last token or block is of no meaning: no
       // result of such n is stored, no product takes such a byte.)
-      const int ksteps = (p.k + T::BK - 1) / T::BK;
       const uint32_t lead = mapa_shared(smem_u32(&bar->sf_full[0]), 0);
       const uint32_t at0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * T::NT;
       Ring<SF_SLOTS> rs;
@@ -584,19 +902,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       load();
       bool ok = true;
       for (int j = pair; ok && j < tiles.total; j += npairs) {
-        for (int k0 = 0; k0 < ksteps; k0 += 4) {
+        const Tile of = tiles.get(j);
+        const int behind = of.halves() == 2 ? of.first : 0;        // tokens of the first half
+        for (int k0 = 0; k0 < of.steps; k0 += 4) {
           if ((k0 & 31) == 0) {
             now = next;
             load();
           }
           ok = wait_warp(&bar->sb_full[rb.s], rb.ph, abort, p);
           if (!ok) break;
-          uint32_t word[8];
+          uint32_t word[2][8];
           const uint8_t* from = smem + SB_OFF + rb.s * SB_SLOT + lane;
 #pragma unroll
-          for (int c = 0; c < 7; ++c)
-            word[c] = from[c * 32] | from[256 + c * 32] << 8 | from[512 + c * 32] << 16 | static_cast<uint32_t>(from[768 + c * 32]) << 24;
-          word[7] = 0u;
+          for (int h = 0; h < 2; ++h) {
+            // (the second half's columns hold nothing of use where there is none)
+            const uint8_t* f = from + (h == 0 ? 0 : behind);
+#pragma unroll
+            for (int c = 0; c < 7; ++c)
+              word[h][c] = f[c * 32] | f[SB_ROW + c * 32] << 8 | f[2 * SB_ROW + c * 32] << 16 |
+                           static_cast<uint32_t>(f[3 * SB_ROW + c * 32]) << 24;
+            word[h][7] = 0u;
+          }
           uint32_t wword = 0u;
 #pragma unroll
           for (int q = 0; q < 4; ++q) wword |= __shfl_sync(0xffffffffu, now, (k0 & 31) + q) << (8 * q);
@@ -606,7 +932,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           if (!ok) break;
           tc_fence_after();
           tmem_st4(at0 + rs.s * SF_COLS, wword);
-          tmem_st8(at0 + rs.s * SF_COLS + 4, word);
+          tmem_st8(at0 + rs.s * SF_COLS + 4, word[0]);
+          tmem_st8(at0 + rs.s * SF_COLS + 12, word[1]);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -617,81 +944,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     }
   } else if (warp >= T::EPI_WARP0) {
     // ----------------------------------------------------------- epilogue
+    // Two warps for each quarter of an accumulator's m, every other 32 n each.
     const int ew = warp - T::EPI_WARP0, quad = warp & 3, half = ew >> 2;
     uint8_t* slot = smem + EPI_OFF + ew * SLOT;
     const uint32_t te[2] = {mapa_shared(smem_u32(&bar->tempty[0]), 0), mapa_shared(smem_u32(&bar->tempty[1]), 0)};
-    int acc = 0;
-    uint32_t acc_ph = 0;
+    const bool packed = p.vec && p.odtype != DT_F32 && p.add == nullptr;
+    int cur = 0;                         // the accumulator of the tile's first half
+    uint32_t ph = 0u;                    // the accumulators' phases, a bit each
     bool ok = true;
     for (int i = pair; ok && i < tiles.total; i += npairs) {
       const Tile t = tiles.get(i);
       const int m0 = t.m0 + static_cast<int>(rank) * 128 + quad * 32, ms = p.m - m0;
-      const long long out = (T::kTokens ? 0 : t.e * p.out_group) + t.n0 * p.ldo + m0;
-      const long long add = (T::kTokens ? 0 : t.e * p.add_group) + t.n0 * p.ldadd + m0;
-      if constexpr (T::kTokens) {
-        ok = wait_warp<100>(&bar->tfull[acc], acc_ph, abort, p);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::NT;
-        for (int c = half * 32; c < t.n; c += 64) {
-          float v[32];
-          tmem_ld32(from + c, v);
-          if (c + 64 >= t.n) {           // this warp's last block: the accumulator is read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(te[acc]);
-          }
-          if (ms > 0) store_block(p, slot, v, out + c * p.ldo, add, t.n - c, ms, lane);
+      const bool some = T::kTokens || t.steps > 0;
+      // weight: tokens past an accumulator's part are added in fp32, in scratch
+      // that each thread reads back what it wrote to
+      const int parts = T::kTokens ? 1 : max(1, (t.steps + STEPS_SUM - 1) / STEPS_SUM);
+      for (int jh = 0; jh < parts * t.halves(); ++jh) {
+        const int j = t.halves() == 2 ? jh >> 1 : jh, h = t.halves() == 2 ? jh & 1 : 0;
+        const int acc = cur ^ h, n = t.count(h), n0 = t.n0 + (h == 0 ? 0 : t.first);
+        const long long out = (T::kTokens ? 0 : t.e * p.out_group) + n0 * p.ldo + m0;
+        const long long add = (T::kTokens ? 0 : t.e * p.add_group) + n0 * p.ldadd + m0;
+        if (some) {
+          ok = wait_warp<32>(&bar->tfull[acc], (ph >> acc) & 1u, abort, p);
+          if (!ok) break;
+          ph ^= 1u << acc;
+          tc_fence_after();
         }
-        if (half * 32 >= t.n) {
+        const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::NT;
+        auto read = [&]() {              // the accumulator may be written again
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(te[acc]);
-        }
-        acc ^= 1;
-        if (acc == 0) acc_ph ^= 1u;
-      } else {
-        // Tokens past an accumulator's part are added in fp32, in scratch that
-        // each thread reads back what it wrote to.
-        float* part = p.part + (static_cast<long long>(pair * 2 + rank) * EPI_WARPS + ew) * PART_WARP + lane;
-        for (int k0 = 0; k0 < t.steps || k0 == 0; k0 += STEPS_SUM) {
-          const bool last = k0 + STEPS_SUM >= t.steps;
-          if (t.steps > 0) {
-            ok = wait_warp<100>(&bar->tfull[acc], acc_ph, abort, p);
-            if (!ok) break;
-            tc_fence_after();
+          if (lane == 0) arrive_relaxed(te[acc]);
+        };
+        if (packed && some && ms >= 32 && parts == 1) {
+          // all of this warp's blocks to registers first, rounded: the next
+          // products wait for this
+          uint32_t w[4][16];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int c = half * 32 + b * 64;
+            if (c < n) {
+              if (p.odtype == DT_BF16)
+                tmem_block<__nv_bfloat16>(from + c, w[b]);
+              else
+                tmem_block<__half>(from + c, w[b]);
+            }
           }
-          const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::NT;
+          read();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int c = half * 32 + b * 64;
+            if (c < n) store_packed(smem_u32(slot), w[b], static_cast<uint16_t*>(p.out) + out + c * p.ldo, p.ldo, n - c, lane);
+          }
+          continue;
+        }
 #pragma unroll 1
-          for (int c = half * 32; c < t.n; c += 64) {
-            float v[32];
-            if (t.steps > 0) {
-              tmem_ld32(from + c, v);
-            } else {
+        for (int c = half * 32; c < n; c += 64) {
+          float v[32];
+          if (some) {
+            tmem_ld32(from + c, v);
+          } else {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] = 0.f;
-            }
-            float* own = part + (c >> 6) * 1024;
-            if (k0 > 0) {
+            for (int q = 0; q < 32; ++q) v[q] = 0.f;
+          }
+          if (some && c + 64 >= n) read();
+          if constexpr (!T::kTokens) {
+            if (parts > 1) {
+              float* own = p.part + (static_cast<long long>(pair * 2 + static_cast<int>(rank)) * EPI_WARPS + ew) * PART_WARP +
+                           h * (PART_WARP / 2) + (c >> 6) * 1024 + lane;
+              if (j > 0) {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] += own[q * 32];
-            }
-            if (!last) {
+                for (int q = 0; q < 32; ++q) v[q] += own[q * 32];
+              }
+              if (j < parts - 1) {
 #pragma unroll
-              for (int q = 0; q < 32; ++q) own[q * 32] = v[q];
-            } else if (ms > 0) {
-              store_block(p, slot, v, out + c * p.ldo, add + c * p.ldadd, t.n - c, ms, lane);
+                for (int q = 0; q < 32; ++q) own[q * 32] = v[q];
+                continue;
+              }
             }
           }
-          if (t.steps > 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(te[acc]);
-            acc ^= 1;
-            if (acc == 0) acc_ph ^= 1u;
-          }
+          if (ms > 0) store_block(p, slot, v, out + c * p.ldo, add + c * p.ldadd, n - c, ms, lane);
         }
+        if (some && half * 32 >= n) read();
       }
+      if (t.halves() == 1 && t.steps > 0) cur ^= 1;
     }
     if constexpr (T::kTokens) {
       const int w = (pair * 2 + static_cast<int>(rank)) * EPI_WARPS + ew, warps = npairs * 2 * EPI_WARPS;
@@ -719,7 +1055,7 @@ cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pai
   const long long mt = (p.m + MT - 1) / MT;
   // tiles, at most: the tokens' experts are on the device
   const long long nt = Traits<KIND>::kTokens
-                           ? p.tokens / Traits<KIND>::NT + (p.tokens < p.groups ? p.tokens : p.groups)
+                           ? p.tokens / p.most + (p.tokens < p.groups ? p.tokens : p.groups)
                            : static_cast<long long>(p.groups) * ((p.n + 31) / 32);
   if (mt * nt > 0x3FFFFFFFll) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done;
@@ -744,6 +1080,7 @@ cudaError_t launch_product(const ProductParams& q, const CUtensorMap* maps, int 
     return reinterpret_cast<uintptr_t>(at) % 16 == 0 && ld * es % 16 == 0 && group * es % 16 == 0;
   };
   p.vec = fits(p.out, p.ldo, p.out_group) && (p.add == nullptr || fits(p.add, p.ldadd, p.add_group)) && p.m % 8 == 0;
+  p.most = p.kind == PRODUCT_ACT8 ? 2 * Traits<PRODUCT_ACT8>::NT : 2 * Traits<PRODUCT_FORWARD>::NT;
   switch (p.kind) {
     case PRODUCT_FORWARD: return launch_kind<PRODUCT_FORWARD>(p, maps, pairs, s);
     case PRODUCT_ACT8: return launch_kind<PRODUCT_ACT8>(p, maps, pairs, s);
