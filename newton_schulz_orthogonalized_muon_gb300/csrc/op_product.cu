@@ -32,6 +32,8 @@
 //
 // The groups' offsets are device data: every CTA clamps them (to the token
 // axis and the largest before them) and counts the tiles for itself.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "op_common.cuh"
@@ -1067,6 +1069,31 @@ cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pai
   return cudaGetLastError();
 }
 
+// The most n of a tile.  Wide tiles bring less to shared memory for each product;
+// narrow ones give every pair of SMs something to do, down to a step's 330 cycles
+// of issue, which 160 n take: 1001 x 2042 x 1411 in 8 bits takes 31 us with tiles
+// of 448 and 21.5 with what this gives.  Two halves pay in 8 bits
+// alone: 16384 x 4096 x 14336 in 672 us against 762, but 64 experts of 768 rows,
+// 1408 -> 2048 in 217 against 205, since two halves of 16 bits are finished in
+// turn where two tiles overlap.
+int most_n(const ProductParams& p, int pairs) {
+  const bool k8 = p.kind == PRODUCT_ACT8, weight = p.kind == PRODUCT_WEIGHT;
+  const long long mt = (p.m + MT - 1) / MT, each = (p.tokens + p.groups - 1) / p.groups;
+  const long long len = weight ? p.n : each, steps = weight ? (each + 63) / 64 : (p.k + (k8 ? 127 : 63)) / (k8 ? 128 : 64);
+  int best = 0;
+  long long least = 0;
+  for (int most = 32; most <= (k8 ? 448 : 256); most = most == 224 && k8 ? 448 : most + 32) {
+    const long long size = tile_n(static_cast<int>(len < 1 ? 1 : len), most, !weight), n = size < len ? size : len;
+    const long long tiles = p.groups * mt * ((len + size - 1) / size), turns = (tiles + pairs - 1) / pairs;
+    const long long cost = turns * (steps * std::max<long long>(330, 2 * ((n + 31) / 32 * 32)) + 2500);
+    if (best == 0 || cost <= least) {
+      best = most;
+      least = cost;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 uint64_t product_part_bytes(int64_t tokens, int sms) {
@@ -1080,7 +1107,7 @@ cudaError_t launch_product(const ProductParams& q, const CUtensorMap* maps, int 
     return reinterpret_cast<uintptr_t>(at) % 16 == 0 && ld * es % 16 == 0 && group * es % 16 == 0;
   };
   p.vec = fits(p.out, p.ldo, p.out_group) && (p.add == nullptr || fits(p.add, p.ldadd, p.add_group)) && p.m % 8 == 0;
-  p.most = p.kind == PRODUCT_ACT8 ? 2 * Traits<PRODUCT_ACT8>::NT : 2 * Traits<PRODUCT_FORWARD>::NT;
+  p.most = most_n(p, pairs);
   switch (p.kind) {
     case PRODUCT_FORWARD: return launch_kind<PRODUCT_FORWARD>(p, maps, pairs, s);
     case PRODUCT_ACT8: return launch_kind<PRODUCT_ACT8>(p, maps, pairs, s);
