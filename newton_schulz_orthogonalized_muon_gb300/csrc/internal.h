@@ -361,7 +361,7 @@ struct Adamw8Tensor {
   uint8_t *ms, *rs;        // their scales, a byte for 128 elements
   long long numel;
   uint32_t chunk0;         // set by the launcher
-  int vec;                 // every pointer but the scales' is 16-byte aligned
+  int vec;                 // every pointer but the scales' is aligned: values' to 32 bytes, codes' to 16
 };
 constexpr int kAdamw8Tensors = 112;      // of a launch: its parameters are kept below 8 KB
 struct Adamw8Params {

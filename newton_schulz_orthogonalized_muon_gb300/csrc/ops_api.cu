@@ -840,7 +840,7 @@ muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, in
     h->prof_tag = -1;
     return adamw8_launches(h, tensors, n, p, "adamw8 launch", stream, launch_adamw8, [&](int32_t, const muon_adamw8_t& t) {
       if (t.param_dtype != p.pdtype || t.grad_dtype != p.gdtype) return;
-      const int vec = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.avg, 16) && aligned(t.root, 16);
+      const int vec = aligned(t.param, 32) && aligned(t.grad, 32) && aligned(t.avg, 16) && aligned(t.root, 16);
       p.t[p.n++] = Adamw8Tensor{t.param, t.grad, t.avg, t.root, t.avg_scale, t.root_scale, t.numel, 0, vec};
     });
   });
@@ -863,7 +863,7 @@ muon_status_t muon_adamw8_restore(muon_handle_t h, const muon_adamw8_t* tensors,
     return adamw8_launches(h, tensors, n, p, "adamw8 restore launch", stream, launch_adamw8_restore,
                            [&](int32_t i, const muon_adamw8_t& t) {
       if (p.pdtype != dtype || p.gdtype != 0) return;
-      const int vec = aligned(avg[i], 16) && aligned(root[i], 16) && aligned(t.avg, 16) && aligned(t.root, 16);
+      const int vec = aligned(avg[i], 32) && aligned(root[i], 32) && aligned(t.avg, 16) && aligned(t.root, 16);
       p.t[p.n++] = Adamw8Tensor{avg[i], root[i], t.avg, t.root, t.avg_scale, t.root_scale, t.numel, 0, vec};
     });
   });
