@@ -464,7 +464,8 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
                                       void* dw, int64_t lddw, int64_t dw_expert, int64_t tokens, int64_t cols,
                                       int64_t out, int64_t experts, int32_t dtype, int32_t odtype, void* workspace,
                                       size_t workspace_bytes, void* stream);
-muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, uint64_t* bytes);
+muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, int64_t cols, int64_t out,
+                                                int64_t experts, uint64_t* bytes);
 
 /* A weight in 8 bits, for products with stored activations: each block of 128
  * x 128 is stored as e4m3 codes of w 2^-e, rounded to nearest even, e the

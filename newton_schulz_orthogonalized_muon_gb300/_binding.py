@@ -135,7 +135,7 @@ def load_library(path: str | None = None):
             "muon_expert_matmul": (i32, [vp, vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i64, i64, i32, i32, vp]),
             "muon_expert_weight_grad": (i32, [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i64, i64, i64, i64, i64, i32,
                                               i32, vp, ctypes.c_size_t, vp]),
-            "muon_expert_weight_grad_workspace": (i32, [vp, i64, ctypes.POINTER(u64)]),
+            "muon_expert_weight_grad_workspace": (i32, [vp, i64, i64, i64, i64, ctypes.POINTER(u64)]),
             "muon_act8_store_weight": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_restore_weight": (i32, [vp, vp, i64, vp, i64, i64, vp, i64, i64, i64, i32, vp]),
             "muon_act8_matmul": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i64, i64, i32, vp]),

@@ -381,7 +381,7 @@ struct ProductParams {
   const int* offsets;      // [groups + 1] on the token axis, or nullptr (one group of all tokens)
   const void* add;         // weight: [groups][n][m] of odtype, or nullptr
   void* out;               // tokens: [tokens][m]; weight: [groups][n][m]; of odtype
-  long long ldo, out_group, ldadd, add_group;   // row and group strides in elements
+  long long ldo, out_group, out_split, ldadd, add_group;   // row and group strides in elements
   const uint8_t* scales;   // 8 bits: a byte a token and 128 columns, [blocks] rows lds apart
   const uint8_t* wscales;  // a byte a 128 x 128 block of W, at column block * ws_col + row block * ws_row
   long long lds, ws_col, ws_row;
@@ -393,14 +393,16 @@ struct ProductParams {
   int odtype;
   int f16;                 // the operands are fp16 (else bf16)
   int most;                // set by the launcher: n of a tile, at most
+  int splits;              // weight, set by the launcher: parts of an expert's tokens, results out_split apart
   int vec;                 // set by the launcher: rows of out and add are 16-byte aligned
   unsigned* err;           // the handle's error word
   unsigned long long timeout_ns;
 };
 // maps, 3-D with 128-byte swizzle: A, B and B again (see op_product.cu).  K-major: {k, rows, groups or 1} in boxes of 64 k
 // (8 bits: 128) and 128 rows, or 32 in the third; MN-major: {rows, k, groups or 1} in boxes of 64 rows and 64 k.
-uint64_t product_part_bytes(int64_t tokens, int sms);
-cudaError_t launch_product(const ProductParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s);
+uint64_t product_part_bytes(int64_t tokens, int cols, int out, int groups, int sms);
+// launches: how many kernels were launched
+cudaError_t launch_product(const ProductParams& p, const CUtensorMap* maps, int sms, cudaStream_t s, int* launches);
 
 // ------------------------------------------------------------ attention
 struct AttnParams {

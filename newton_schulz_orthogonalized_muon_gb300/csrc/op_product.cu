@@ -109,7 +109,8 @@ struct Tile {
   int e, m0, n0;       // group, first m, first n (of the token axis, or of the outputs)
   int n;               // that exist
   int first;           // of them in the first half (n: there is no second)
-  int t0, len;         // weight: the group's first token and tokens
+  int t0, len;         // weight: first token and tokens of the group, or of its split
+  int split;
   int steps;
 
   __device__ __forceinline__ int halves() const { return first < n ? 2 : 1; }
@@ -128,7 +129,7 @@ struct Tiles {
 
   __device__ __forceinline__ Tiles(const ProductParams& q, const int* a) : p(q), at(a), pre(a + kMaxExperts + 4) {
     mt = (p.m + MT - 1) / MT;
-    total = Traits<KIND>::kTokens ? pre[p.groups] : p.groups * mt * ((p.n + nsize() - 1) / nsize());
+    total = Traits<KIND>::kTokens ? pre[p.groups] : p.groups * mt * ((p.n + nsize() - 1) / nsize()) * p.splits;
   }
   __device__ __forceinline__ int nsize() const { return tile_n(p.n, p.most, false); }
   // A group's tiles go eight m at a time: the pairs that run together share
@@ -149,15 +150,26 @@ struct Tiles {
       t.n0 += at[e];
       t.n = min(size, at[e + 1] - t.n0);
       t.steps = (p.k + Traits<KIND>::BK - 1) / Traits<KIND>::BK;
-      t.t0 = t.len = 0;
+      t.t0 = t.len = t.split = 0;
     } else {
       const int size = nsize(), per = mt * ((p.n + size - 1) / size);
+      t.split = 0;
+      if (p.splits > 1) {                // splits of a tile are neighbours
+        t.split = i % p.splits;
+        i /= p.splits;
+      }
       t.e = i / per;
       place(i - t.e * per, per / mt, t.m0, t.n0, size);
       t.n = min(size, p.n - t.n0);
       t.t0 = at[t.e];
       t.len = at[t.e + 1] - t.t0;
       t.steps = (t.len + Traits<KIND>::BK - 1) / Traits<KIND>::BK;
+      if (p.splits > 1) {                // below 2^32: 2^24 steps, fewer splits than SMs
+        const uint32_t steps = t.steps, k0 = steps * t.split / p.splits, k1 = steps * (t.split + 1) / p.splits;
+        t.t0 += static_cast<int>(k0 * Traits<KIND>::BK);
+        t.len = min(t.len, static_cast<int>(k1 * Traits<KIND>::BK)) - static_cast<int>(k0 * Traits<KIND>::BK);
+        t.steps = static_cast<int>(k1 - k0);
+      }
     }
     t.n = __shfl_sync(0xffffffffu, t.n, 0);
     t.m0 = __shfl_sync(0xffffffffu, t.m0, 0);
@@ -165,6 +177,7 @@ struct Tiles {
     t.e = __shfl_sync(0xffffffffu, t.e, 0);
     t.t0 = __shfl_sync(0xffffffffu, t.t0, 0);
     t.len = __shfl_sync(0xffffffffu, t.len, 0);
+    t.split = __shfl_sync(0xffffffffu, t.split, 0);
     t.steps = __shfl_sync(0xffffffffu, t.steps, 0);
     t.first = t.n <= Traits<KIND>::NT ? t.n : ((t.n + 1) / 2 + 31) / 32 * 32;
     return t;
@@ -964,7 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       for (int jh = 0; jh < parts * t.halves(); ++jh) {
         const int j = t.halves() == 2 ? jh >> 1 : jh, h = t.halves() == 2 ? jh & 1 : 0;
         const int acc = cur ^ h, n = t.count(h), n0 = t.n0 + (h == 0 ? 0 : t.first);
-        const long long out = (T::kTokens ? 0 : t.e * p.out_group) + n0 * p.ldo + m0;
+        const long long out = (T::kTokens ? 0 : t.e * p.out_group + t.split * p.out_split) + n0 * p.ldo + m0;
         const long long add = (T::kTokens ? 0 : t.e * p.add_group) + n0 * p.ldadd + m0;
         if (some) {
           ok = wait_warp<32>(&bar->tfull[acc], (ph >> acc) & 1u, abort, p);
@@ -1058,7 +1071,7 @@ cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pai
   // tiles, at most: the tokens' experts are on the device
   const long long nt = Traits<KIND>::kTokens
                            ? p.tokens / p.most + (p.tokens < p.groups ? p.tokens : p.groups)
-                           : static_cast<long long>(p.groups) * ((p.n + 31) / 32);
+                           : static_cast<long long>(p.groups) * ((p.n + 31) / 32) * p.splits;
   if (mt * nt > 0x3FFFFFFFll) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(product_kernel<KIND>), SMEM, done);
@@ -1069,26 +1082,51 @@ cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pai
   return cudaGetLastError();
 }
 
-// The most n of a tile.  Wide tiles bring less to shared memory for each product;
-// narrow ones give every pair of SMs something to do, down to a step's 330 cycles
+// dw = add + the splits' partial results, in their order.
+__global__ void __launch_bounds__(256) product_join_kernel(const ProductParams p, const float* part) {
+  const long long each = static_cast<long long>(p.n) * p.m, count = p.groups * each;
+  pdl_wait();                            // launched while the partial results are still being formed
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
+    const long long e = i / each, in = i - e * each;
+    const int n = static_cast<int>(in / p.m), m = static_cast<int>(in - static_cast<long long>(n) * p.m);
+    float v = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) v += part[s * count + i];
+    if (p.add != nullptr) v += load_f32(p.add, e * p.add_group + n * p.ldadd + m, p.odtype);
+    store_any(p.out, e * p.out_group + n * p.ldo + m, p.odtype, v);
+  }
+}
+
+// How a problem is cut: the most n of a tile and, for the weight's gradient, the
+// parts that an expert's tokens are split into (a second kernel adds their
+// results).  Wide tiles bring less to shared memory for each product; narrow ones
+// and splits give every pair of SMs something to do, down to a step's 330 cycles
 // of issue, which 160 n take: 1001 x 2042 x 1411 in 8 bits takes 31 us with tiles
-// of 448 and 21.5 with what this gives.  Two halves pay in 8 bits
+// of 448 and 21.5 with what this gives; the gradient of one weight 192 x 2088 over
+// 46894 rows 211 us without splits and 64 with them.  Two halves pay in 8 bits
 // alone: 16384 x 4096 x 14336 in 672 us against 762, but 64 experts of 768 rows,
 // 1408 -> 2048 in 217 against 205, since two halves of 16 bits are finished in
 // turn where two tiles overlap.
-int most_n(const ProductParams& p, int pairs) {
-  const bool k8 = p.kind == PRODUCT_ACT8, weight = p.kind == PRODUCT_WEIGHT;
-  const long long mt = (p.m + MT - 1) / MT, each = (p.tokens + p.groups - 1) / p.groups;
-  const long long len = weight ? p.n : each, steps = weight ? (each + 63) / 64 : (p.k + (k8 ? 127 : 63)) / (k8 ? 128 : 64);
-  int best = 0;
+struct Plan {
+  int most, splits;
+};
+Plan plan_of(int kind, long long tokens, int groups, int m, int n, int k, int pairs) {
+  const bool k8 = kind == PRODUCT_ACT8, weight = kind == PRODUCT_WEIGHT;
+  const long long mt = (m + MT - 1) / MT, each = (tokens + groups - 1) / groups;
+  const long long len = weight ? n : each, steps = weight ? (each + 63) / 64 : (k + (k8 ? 127 : 63)) / (k8 ? 128 : 64);
+  Plan best{};
   long long least = 0;
   for (int most = 32; most <= (k8 ? 448 : 256); most = most == 224 && k8 ? 448 : most + 32) {
-    const long long size = tile_n(static_cast<int>(len < 1 ? 1 : len), most, !weight), n = size < len ? size : len;
-    const long long tiles = p.groups * mt * ((len + size - 1) / size), turns = (tiles + pairs - 1) / pairs;
-    const long long cost = turns * (steps * std::max<long long>(330, 2 * ((n + 31) / 32 * 32)) + 2500);
-    if (best == 0 || cost <= least) {
-      best = most;
-      least = cost;
+    const long long size = tile_n(static_cast<int>(len < 1 ? 1 : len), most, !weight), rows = size < len ? size : len;
+    const long long tiles = groups * mt * ((len + size - 1) / size), step = std::max<long long>(330, 2 * ((rows + 31) / 32 * 32));
+    for (int splits = 1; splits == 1 || (weight && tiles * splits <= pairs && steps / splits >= 8); ++splits) {
+      // cycles: a turn of tiles, and for splits a launch and what they write and read
+      const long long turns = (tiles * splits + pairs - 1) / pairs, join = splits > 1 ? 6000 + groups * (1ll * n * m) * splits / 400 : 0;
+      const long long cost = turns * ((steps + splits - 1) / splits * step + 2500) + join;
+      if (best.most == 0 || cost <= least) {
+        best = Plan{most, splits};
+        least = cost;
+      }
     }
   }
   return best;
@@ -1096,24 +1134,56 @@ int most_n(const ProductParams& p, int pairs) {
 
 }  // namespace
 
-uint64_t product_part_bytes(int64_t tokens, int sms) {
+namespace {
+// Scratch of the weight's gradient: the CTAs' sums over more tokens than an
+// accumulator takes, then the splits' results.
+uint64_t sums_bytes(int64_t tokens, int sms) {
   return tokens > STEPS_SUM * 64 ? static_cast<uint64_t>(sms) * EPI_WARPS * PART_WARP * 4 : 0;
 }
+}  // namespace
 
-cudaError_t launch_product(const ProductParams& q, const CUtensorMap* maps, int pairs, cudaStream_t s) {
+uint64_t product_part_bytes(int64_t tokens, int cols, int out, int groups, int sms) {
+  const Plan plan = plan_of(PRODUCT_WEIGHT, tokens, groups, cols, out, 0, sms / 2);
+  const uint64_t split = plan.splits > 1 ? static_cast<uint64_t>(plan.splits) * groups * out * cols * 4 : 0;
+  return sums_bytes(tokens, sms) + split;
+}
+
+cudaError_t launch_product(const ProductParams& q, const CUtensorMap* maps, int sms, cudaStream_t s, int* launches) {
   ProductParams p = q;
+  const Plan plan = plan_of(p.kind, p.tokens, p.groups, p.m, p.n, p.k, sms / 2);
+  p.most = plan.most;
+  p.splits = plan.splits;
+  *launches = 1;
+  float* split = nullptr;
+  if (p.splits > 1) {
+    split = p.part + sums_bytes(p.tokens, sms) / 4;
+    p.out = split;
+    p.add = nullptr;
+    p.odtype = DT_F32;
+    p.ldo = p.m;
+    p.out_group = static_cast<long long>(p.n) * p.m;
+    p.out_split = p.groups * p.out_group;
+  }
   const int es = p.odtype == DT_F32 ? 4 : 2;
   auto fits = [es](const void* at, long long ld, long long group) {
     return reinterpret_cast<uintptr_t>(at) % 16 == 0 && ld * es % 16 == 0 && group * es % 16 == 0;
   };
   p.vec = fits(p.out, p.ldo, p.out_group) && (p.add == nullptr || fits(p.add, p.ldadd, p.add_group)) && p.m % 8 == 0;
-  p.most = most_n(p, pairs);
+  cudaError_t e;
   switch (p.kind) {
-    case PRODUCT_FORWARD: return launch_kind<PRODUCT_FORWARD>(p, maps, pairs, s);
-    case PRODUCT_ACT8: return launch_kind<PRODUCT_ACT8>(p, maps, pairs, s);
-    case PRODUCT_INPUT: return launch_kind<PRODUCT_INPUT>(p, maps, pairs, s);
-    default: return launch_kind<PRODUCT_WEIGHT>(p, maps, pairs, s);
+    case PRODUCT_FORWARD: e = launch_kind<PRODUCT_FORWARD>(p, maps, sms / 2, s); break;
+    case PRODUCT_ACT8: e = launch_kind<PRODUCT_ACT8>(p, maps, sms / 2, s); break;
+    case PRODUCT_INPUT: e = launch_kind<PRODUCT_INPUT>(p, maps, sms / 2, s); break;
+    default: e = launch_kind<PRODUCT_WEIGHT>(p, maps, sms / 2, s);
   }
+  if (e != cudaSuccess || p.splits == 1) return e;
+  *launches = 2;
+  ProductParams j = q;
+  j.splits = p.splits;
+  const long long want = (p.out_split + 255) / 256;
+  e = launch_k(pdl_level() >= 1, product_join_kernel, dim3(static_cast<unsigned>(want < sms * 8ll ? want : sms * 8ll)), dim3(256), 0,
+               s, j, static_cast<const float*>(split));
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace muon

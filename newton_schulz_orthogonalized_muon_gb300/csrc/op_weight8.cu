@@ -23,63 +23,9 @@ constexpr int BLK = 128;
 constexpr int WTHREADS = 256;
 constexpr int PASSES = BLK / (WTHREADS / 16);      // rows a thread has
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(WTHREADS) weight8_store_kernel(const Weight8Params p, int blocks_c) {
-  // word w of row r at w ^ 4 ((r >> 4) & 7): the transposing reads, 8 bands of
-  // 16 rows by 4 neighbouring words, then fall on 32 different banks
-  __shared__ __align__(16) uint32_t tile[BLK][BLK / 4];
-  __shared__ int tops[WTHREADS / 32];
-  const int kb = blockIdx.x % blocks_c, ob = blockIdx.x / blocks_c;
-  const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4, c = kb * BLK + l * 8;
-  const long long o0 = static_cast<long long>(ob) * BLK;
-  const T* w = static_cast<const T*>(p.w);
-  float f[PASSES][8];
-  int top = 0;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const long long o = o0 + r0 + 16 * i;
-    const bool in = o < p.out;
-    if constexpr (VEC) {
-      constexpr int kStep = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-      for (int k = 0; k < 8; k += kStep)
-        unpack16<T>(in && c < p.cols ? ld_stream16(w + o * p.ldw + c + k) : make_uint4(0u, 0u, 0u, 0u), f[i] + k);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[i][k] = in && c + k < p.cols ? to_f32(w[o * p.ldw + c + k]) : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, __float_as_int(f[i][k]) & 0x7FFFFFFF);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < WTHREADS / 32; ++i) top = max(top, tops[i]);
-  const bool fine = top < 0x7F800000;
-  const int e = fine ? e4m3_scale_byte(top) : 255;
-  const float unit = __int_as_float((254 - e) << 23);
-  if (threadIdx.x == 0) p.scales[kb * p.lds + ob] = static_cast<uint8_t>(e);
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = r0 + 16 * i;
-    const long long o = o0 + r;
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = f[i][k] * unit;
-    const uint2 code = fine ? make_uint2(e4m3x4(v), e4m3x4(v + 4)) : make_uint2(0u, 0u);
-    if (o < p.out && c < p.cols) {
-      uint8_t* to = p.codes + o * p.ldc + c;
-      if (c + 8 <= p.cols)
-        *reinterpret_cast<uint2*>(to) = code;
-      else
-        for (int k = 0; c + k < p.cols; ++k) to[k] = static_cast<uint8_t>((k < 4 ? code.x : code.y) >> (8 * (k & 3)));
-    }
-    if (p.codes_t != nullptr) *reinterpret_cast<uint2*>(&tile[r][(2 * l) ^ (4 * ((r >> 4) & 7))]) = code;
-  }
-  if (p.codes_t == nullptr) return;
-  __syncthreads();
-  // 16 rows (band) by 4 columns a thread, turned around as 4 x 4 bytes
+// The transpose's codes from the tile of codes, 16 rows (band) by 4 columns a
+// thread, turned around as 4 x 4 bytes.
+__device__ __forceinline__ void store_transposed(const Weight8Params& p, const uint32_t (*tile)[BLK / 4], long long o0, int c0) {
   const int band = threadIdx.x & 7, word = threadIdx.x >> 3;
   uint32_t t[4][4];                                  // column, four rows a word
 #pragma unroll
@@ -97,7 +43,7 @@ __global__ void __launch_bounds__(WTHREADS) weight8_store_kernel(const Weight8Pa
   const long long o = o0 + band * 16;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int cc = kb * BLK + word * 4 + k;
+    const int cc = c0 + word * 4 + k;
     if (cc >= p.cols || o >= p.out) continue;
     uint8_t* to = p.codes_t + cc * p.ldt + o;
     if (o + 16 <= p.out)
@@ -109,6 +55,114 @@ __global__ void __launch_bounds__(WTHREADS) weight8_store_kernel(const Weight8Pa
   }
 }
 
+// Eight codes of row o from column c.
+__device__ __forceinline__ void store_eight(const Weight8Params& p, long long o, int c, uint2 code) {
+  if (o >= p.out || c >= p.cols) return;
+  uint8_t* to = p.codes + o * p.ldc + c;
+  if (c + 8 <= p.cols)
+    *reinterpret_cast<uint2*>(to) = code;
+  else
+    for (int k = 0; c + k < p.cols; ++k) to[k] = static_cast<uint8_t>((k < 4 ? code.x : code.y) >> (8 * (k & 3)));
+}
+
+// The block's scale byte from each thread's largest magnitude, as bits.
+__device__ __forceinline__ int block_scale(int top, int* tops) {
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WTHREADS / 32; ++i) top = max(top, tops[i]);
+  return top < 0x7F800000 ? e4m3_scale_byte(top) : 255;
+}
+
+// The tile of codes in shared memory: word w of row r at w ^ 4 ((r >> 4) & 7).
+// The transposing reads, 8 bands of 16 rows by 4 neighbouring words, then fall on
+// 32 different banks.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 4 : 2) weight8_store_kernel(const Weight8Params p, int blocks_c) {
+  __shared__ __align__(16) uint32_t tile[BLK][BLK / 4];
+  __shared__ int tops[WTHREADS / 32];
+  const int kb = blockIdx.x % blocks_c, ob = blockIdx.x / blocks_c;
+  const long long o0 = static_cast<long long>(ob) * BLK;
+  const T* w = static_cast<const T*>(p.w);
+  int top = 0, e;
+  if constexpr (VEC) {
+    constexpr int kStep = 16 / static_cast<int>(sizeof(T)), NV = 8 / kStep;
+    const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4, c = kb * BLK + l * 8;
+    uint4 raw[PASSES][NV];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const long long o = o0 + r0 + 16 * i;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        raw[i][v] = o < p.out && c < p.cols ? ld_stream16(w + o * p.ldw + c + v * kStep) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[kStep];
+        unpack16<T>(raw[i][v], f);
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) top = max(top, __float_as_int(f[k]) & 0x7FFFFFFF);
+      }
+    e = block_scale(top, tops);
+    const float unit = __int_as_float((254 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = r0 + 16 * i;
+      float f[8];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) unpack16<T>(raw[i][v], f + v * kStep);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= unit;
+      const uint2 code = e != 255 ? make_uint2(e4m3x4(f), e4m3x4(f + 4)) : make_uint2(0u, 0u);
+      store_eight(p, o0 + r, c, code);
+      if (p.codes_t != nullptr) *reinterpret_cast<uint2*>(&tile[r][(2 * l) ^ (4 * ((r >> 4) & 7))]) = code;
+    }
+  } else {
+    // rows without common alignment: a warp's lanes read elements next to each
+    // other, every second row a thread, and the codes leave by way of the tile
+    // (2612 x 6570 bf16, both ways round and back: 154 us with eight elements a
+    // lane)
+    const int lc = threadIdx.x & 127, r0 = threadIdx.x >> 7, c = kb * BLK + lc;
+    T raw[BLK / 2];
+#pragma unroll
+    for (int i = 0; i < BLK / 2; ++i) {
+      const long long o = o0 + r0 + 2 * i;
+      raw[i] = o < p.out && c < p.cols ? w[o * p.ldw + c] : from_f32<T>(0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < BLK / 2; ++i) top = max(top, __float_as_int(to_f32(raw[i])) & 0x7FFFFFFF);
+    e = block_scale(top, tops);
+    const float unit = __int_as_float((254 - e) << 23);
+    uint8_t* bytes = reinterpret_cast<uint8_t*>(tile);
+#pragma unroll
+    for (int i = 0; i < BLK / 2; i += 4) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = to_f32(raw[i + k]) * unit;
+      const uint32_t code = e != 255 ? e4m3x4(f) : 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 2 * (i + k);
+        bytes[r * BLK + (((lc >> 2) ^ (4 * ((r >> 4) & 7))) << 2) + (lc & 3)] = static_cast<uint8_t>(code >> (8 * k));
+      }
+    }
+    __syncthreads();
+    const int l = threadIdx.x & 15;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = (threadIdx.x >> 4) + 16 * i;
+      store_eight(p, o0 + r, kb * BLK + l * 8, *reinterpret_cast<const uint2*>(&tile[r][(2 * l) ^ (4 * ((r >> 4) & 7))]));
+    }
+  }
+  if (threadIdx.x == 0) p.scales[kb * p.lds + ob] = static_cast<uint8_t>(e);
+  if (p.codes_t == nullptr) return;
+  __syncthreads();
+  store_transposed(p, tile, o0, kb * BLK);
+}
+
 // A half warp takes 128 columns of a row, 8 a lane; rows a block apart share a scale.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(WTHREADS) weight8_restore_kernel(const Weight8Params p, int blocks_c) {
@@ -117,13 +171,14 @@ __global__ void __launch_bounds__(WTHREADS) weight8_restore_kernel(const Weight8
   const long long o0 = static_cast<long long>(ob) * BLK;
   const float unit = __int_as_float(p.scales[kb * p.lds + ob * p.lds_row] << 23);      // 255: infinity, times 0: NaN
   T* w = static_cast<T*>(const_cast<void*>(p.w));
-  if (c >= p.cols) return;
+  __shared__ T rows[VEC ? 1 : 16][VEC ? 1 : BLK + 2];
+  if (VEC && c >= p.cols) return;
   uint2 code[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const long long o = o0 + r0 + 16 * i;
     code[i] = make_uint2(0u, 0u);
-    if (o < p.out) {
+    if (o < p.out && c < p.cols) {
       const uint8_t* from = p.codes + o * p.ldc + c;
       if (c + 8 <= p.cols) {
         code[i] = *reinterpret_cast<const uint2*>(from);
@@ -135,19 +190,24 @@ __global__ void __launch_bounds__(WTHREADS) weight8_restore_kernel(const Weight8
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const long long o = o0 + r0 + 16 * i;
-    if (o >= p.out) break;
+    if (VEC && o >= p.out) break;
     float f[8];
     e4m3x4_values(code[i].x, unit, f);
     e4m3x4_values(code[i].y, unit, f + 4);
-    T* to = w + o * p.ldw + c;
     if constexpr (VEC) {
       constexpr int kStep = 16 / static_cast<int>(sizeof(T));
+      T* to = w + o * p.ldw + c;
 #pragma unroll
       for (int k = 0; k < 8; k += kStep) *reinterpret_cast<uint4*>(to + k) = pack16<T>(f + k);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < p.cols) to[k] = from_f32<T>(f[k]);
+      for (int k = 0; k < 8; ++k) rows[r0][l * 8 + k] = from_f32<T>(f[k]);
+      __syncthreads();
+      // a warp's lanes write elements next to each other
+      const int cc = kb * BLK + (threadIdx.x & 127);
+      for (int r = threadIdx.x >> 7; r < 16; r += 2)
+        if (cc < p.cols && o0 + 16 * i + r < p.out) w[(o0 + 16 * i + r) * p.ldw + cc] = rows[r][threadIdx.x & 127];
+      __syncthreads();
     }
   }
 }

@@ -209,14 +209,12 @@ bool product_map(muon_handle_t h, CUtensorMap* map, const void* base, int64_t co
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-muon_status_t check_experts(muon_handle_t h, const int32_t* offsets, int64_t tokens, int64_t cols, int64_t out,
-                            int64_t experts, int32_t dtype) {
+muon_status_t check_experts(muon_handle_t h, int64_t tokens, int64_t cols, int64_t out, int64_t experts, int32_t dtype) {
   MUON_CHECK(dtype == MUON_BF16 || dtype == MUON_F16, "dtype must be MUON_BF16 or MUON_F16");
   MUON_CHECK(tokens >= 0 && tokens <= kMaxTokens, "tokens must be in [0, 2^30]");
   MUON_CHECK(cols >= 8 && cols <= kMaxSide && cols % 8 == 0 && out >= 8 && out <= kMaxSide && out % 8 == 0,
              "cols and out must be multiples of 8 in [8, 2^20]");
   MUON_CHECK(experts >= 1 && experts <= kMaxExperts, "experts must be in [1, 1024]");
-  MUON_CHECK(offsets != nullptr && aligned(offsets, 4), "offsets is NULL or not aligned");
   return MUON_OK;
 }
 
@@ -613,8 +611,9 @@ muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, co
                                  void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded(h, [&]() -> muon_status_t {
-    const muon_status_t st = check_experts(h, offsets, tokens, cols, out, experts, dtype);
+    const muon_status_t st = check_experts(h, tokens, cols, out, experts, dtype);
     if (st != MUON_OK) return st;
+    MUON_CHECK(offsets != nullptr && aligned(offsets, 4), "offsets is NULL or not aligned");
     if (tokens == 0) return MUON_OK;
     const int64_t in = transpose ? out : cols, to = transpose ? cols : out;
     MUON_CHECK(!bad_rows(x, ldx, tokens, in) && !bad_rows(w, ldw, out, cols) &&
@@ -643,16 +642,19 @@ muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, co
         !product_map(h, &maps[1], x, in, tokens, ldx, 1, 0, dtype, 128) ||
         !product_map(h, &maps[2], x, in, tokens, ldx, 1, 0, dtype, 32))
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
-    MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms / 2, stream), "experts' product launch");
+    int launches = 0;
+    MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms, stream, &launches), "experts' product launch");
     return MUON_OK;
   });
 }
 
-muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, uint64_t* bytes) {
+muon_status_t muon_expert_weight_grad_workspace(muon_handle_t h, int64_t tokens, int64_t cols, int64_t out,
+                                                int64_t experts, uint64_t* bytes) {
   if (h == nullptr || bytes == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded(h, [&]() -> muon_status_t {
-    MUON_CHECK(tokens >= 0 && tokens <= kMaxTokens, "tokens must be in [0, 2^30]");
-    *bytes = product_part_bytes(tokens, h->num_sms);
+    const muon_status_t st = check_experts(h, tokens, cols, out, experts, MUON_BF16);
+    if (st != MUON_OK) return st;
+    *bytes = product_part_bytes(tokens, static_cast<int>(cols), static_cast<int>(out), static_cast<int>(experts), h->num_sms);
     return MUON_OK;
   });
 }
@@ -664,9 +666,11 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
                                       size_t workspace_bytes, void* stream_arg) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   return guarded(h, [&]() -> muon_status_t {
-    const muon_status_t st = check_experts(h, offsets, tokens, cols, out, experts, dtype);
+    const muon_status_t st = check_experts(h, tokens, cols, out, experts, dtype);
     if (st != MUON_OK) return st;
-    const uint64_t need = product_part_bytes(tokens, h->num_sms);
+    MUON_CHECK(offsets != nullptr && aligned(offsets, 4), "offsets is NULL or not aligned");
+    const uint64_t need =
+        product_part_bytes(tokens, static_cast<int>(cols), static_cast<int>(out), static_cast<int>(experts), h->num_sms);
     MUON_CHECK(need == 0 || (workspace != nullptr && workspace_bytes >= need && aligned(workspace, 256)),
                "the workspace is too small or not 256-byte aligned");
     MUON_CHECK(odtype == MUON_F32 || odtype == dtype, "odtype must be MUON_F32 or dtype");
@@ -702,7 +706,9 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
     if (tokens > 0 && (!product_map(h, &maps[0], x, cols, tokens, ldx, 1, 0, dtype, 64) ||
                        !product_map(h, &maps[1], dy, out, tokens, lddy, 1, 0, dtype, 64)))
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
-    MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms / 2, stream), "experts' weight gradient launch");
+    int launches = 0;
+    MUON_LAUNCH(MUON_K_EXPERTS, launch_product(p, maps, h->num_sms, stream, &launches), "experts' weight gradient launch");
+    h->launches += launches - 1;
     return MUON_OK;
   });
 }
@@ -793,7 +799,8 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
     if (!codes_map(h, &maps[0], wcodes, cols, out, ldw, 128) || !codes_map(h, &maps[1], codes, cols, rows, ldc, 128) ||
         !codes_map(h, &maps[2], codes, cols, rows, ldc, 32))
       return fail(h, MUON_ERR_CUDA, "tensor map encoding failed");
-    MUON_LAUNCH(MUON_K_MATMUL8, launch_product(p, maps, h->num_sms / 2, stream), "8-bit product launch");
+    int launches = 0;
+    MUON_LAUNCH(MUON_K_MATMUL8, launch_product(p, maps, h->num_sms, stream, &launches), "8-bit product launch");
     return MUON_OK;
   });
 }

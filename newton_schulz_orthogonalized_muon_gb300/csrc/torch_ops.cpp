@@ -617,7 +617,7 @@ PyObject* expert_weight_grad(Args a) {
     out = given != nullptr ? *given : empty({experts, outs, cols}, dy, *type);
     if (given != nullptr) out.unsafeGetTensorImpl()->bump_version();     // autograd sees the write
     uint64_t need = 0;
-    st = muon_expert_weight_grad_workspace(t.h, dy.size(0), &need);
+    st = muon_expert_weight_grad_workspace(t.h, dy.size(0), cols, outs, experts, &need);
     if (st == MUON_OK) {
       at::Tensor ws;
       if (need > 0) ws = empty({static_cast<int64_t>(need)}, dy, at::kByte);
@@ -811,14 +811,29 @@ PyObject* adamw8_restore(Args a) {
   if (!type || (*type != at::kFloat && *type != at::kBFloat16)) refuse("dtype must be float32 or bfloat16");
   const Py_ssize_t n = states.size();
   std::vector<muon_adamw8_t> all;
-  std::vector<at::Tensor> values;
+  std::vector<at::Tensor> values, likes;
   std::vector<void*> avg, root;
+  std::vector<int64_t> bytes;
+  int64_t total = 0;
   for (Py_ssize_t i = 0; i < n; ++i) {
     at::Tensor like;
     all.push_back(state_of(t, states.at(i), "states[" + std::to_string(i) + "]", &like));
-    for (std::vector<void*>* to : {&avg, &root}) {
-      values.push_back(empty(like.sizes(), like, *type));
-      to->push_back(values.back().data_ptr());
+    likes.push_back(std::move(like));
+    // each on a boundary of 256 bytes
+    bytes.push_back(total);
+    total += round_up(all.back().numel * static_cast<int64_t>(c10::elementSize(*type)), 256) * 2;
+  }
+  // one storage for all: an allocation for each took 1 us, most of a small call
+  const at::Tensor whole = n > 0 ? empty({total}, likes[0], at::kByte) : at::Tensor();
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    for (int k = 0; k < 2; ++k) {
+      const int64_t from = bytes[i] + k * round_up(all[i].numel * static_cast<int64_t>(c10::elementSize(*type)), 256);
+      at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                              c10::scalarTypeToTypeMeta(*type));
+      v.unsafeGetTensorImpl()->set_storage_offset(from / static_cast<int64_t>(c10::elementSize(*type)));
+      v.unsafeGetTensorImpl()->set_sizes_contiguous(likes[i].sizes());
+      (k == 0 ? avg : root).push_back(v.data_ptr());
+      values.push_back(std::move(v));
     }
   }
   muon_status_t st;

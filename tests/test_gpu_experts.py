@@ -142,6 +142,25 @@ def test_many_experts_and_long_sums(muon):
     close("70 K tokens", muon.expert_weight_grad(dy, x, ints([0, 1, 70000])), ref, (sums(2048) + 40 * 2.0 ** -24) * mag)
 
 
+@pytest.mark.parametrize("dtype,odtype,add", [(BF, FP, True), (HF, HF, False)])
+@pytest.mark.parametrize("lens,cols,out", [([6001], 136, 72), ([900, 0, 3001], 256, 200), ([0, 2999], 520, 24), ([11000, 1], 64, 8)])
+def test_weight_grad_of_few_tiles(muon, lens, cols, out, dtype, odtype, add):
+    """Tokens of an expert in splits: ends inside steps, splits without tokens, and an expert that has none."""
+    x, dy = rand(30, sum(lens) + 3, cols, dtype=dtype), rand(31, sum(lens) + 3, out, dtype=dtype, scale=0.1)
+    x[sum(lens):], dy[sum(lens):] = float("inf"), float("nan")
+    so_far = rand(32, len(lens), out, cols, dtype=odtype) if add else None
+    at = offsets_of(lens)
+    got = muon.expert_weight_grad(dy, x, at, add=so_far, dtype=odtype)
+    ref, mag = oo.expert_weight_grad(host(dy), host(x), at.cpu().numpy())
+    if add:
+        ref, mag = ref + host(so_far), mag + np.abs(host(so_far))
+    close(f"experts dw splits {lens} {cols}x{out} {odtype}", got, ref, rounded(odtype, ref) + (sums(2048) + 16 * 2.0 ** -24) * mag)
+    assert torch.equal(got, muon.expert_weight_grad(dy, x, at, add=so_far, dtype=odtype))
+    wide = torch.zeros(len(lens), out, cols + 5, dtype=odtype, device="cuda")[:, :, 2:2 + cols]
+    muon.expert_weight_grad(dy, x, at, add=so_far, out=wide)
+    assert torch.equal(got, wide)
+
+
 def test_strides_and_places(muon):
     lens, cols, out = [40, 25], 64, 48
     wide, wdy = rand(17, 70, 3 * cols), rand(18, 70, out + 16)
