@@ -46,7 +46,7 @@ constexpr int MT = 256;                  // m of a pair's tile
 constexpr int BOX = 64 * 128;            // 64 rows of 128 bytes
 constexpr int STAGE = 2 * BOX;           // a step's part of an operand: 128 rows of 128 bytes, or 64 of 256
 constexpr int A_SLOTS = 6, B_SLOTS = 6;
-constexpr int LAG = 2;                   // steps that a tile's second half runs behind its first
+constexpr int LAG = 3;                   // steps that a tile's second half runs behind its first
 static_assert(A_SLOTS >= LAG + B_SLOTS / 2, "a slot of A is free when the slots of B that are loaded with it are");
 constexpr int EPI_WARPS = 8, SLOT = 2048;
 constexpr int STEPS_SUM = 32;            // weight: steps of 64 tokens an accumulator takes
@@ -474,12 +474,20 @@ __device__ __forceinline__ void store_packed(uint32_t slot, const uint32_t* w, u
 
 // The block in fp32, v[j] row j, to rows of 32 m from (out, add), of any type and
 // place.  Rows past `rows` and m past `ms` are not there.
+template <bool ADD>
 __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slot, const float* v, long long out,
                                             long long add, int rows, int ms, int lane) {
   const uint32_t s = smem_u32(slot);
   __syncwarp();
-  // 16 rows at a time
+  // 16 rows at a time; what is added is asked for first
   const bool wide = p.vec && ms >= 32;
+  const int wr = lane >> 3, wq = lane & 7;
+  float f[8][4];
+  if (wide && ADD && p.add != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (wr + 4 * i < rows) load4(p.add, add + (wr + 4 * i) * p.ldadd + wq * 4, p.odtype, f[i]);
+  }
 #pragma unroll
   for (int h = 0; h < 32; h += 16) {
     if (h > 0) __syncwarp();
@@ -487,19 +495,13 @@ __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slo
     for (int j = 0; j < 16; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s + j * 128 + lane * 4), "f"(v[h + j]) : "memory");
     __syncwarp();
     if (wide) {
-      const int r = h + (lane >> 3), q = lane & 7;
-      float f[4][4];
-      if (p.add != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (r + 4 * i < rows) load4(p.add, add + (r + 4 * i) * p.ldadd + q * 4, p.odtype, f[i]);
-      }
+      const int r = h + wr, q = wq;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (r + 4 * i >= rows) break;
         const uint4 raw = lds16(s + (r - h + 4 * i) * 128 + q * 16);
         float4 x = make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w));
-        if (p.add != nullptr) x.x += f[i][0], x.y += f[i][1], x.z += f[i][2], x.w += f[i][3];
+        if (ADD && p.add != nullptr) x.x += f[h / 4 + i][0], x.y += f[h / 4 + i][1], x.z += f[h / 4 + i][2], x.w += f[h / 4 + i][3];
         const long long to = out + (r + 4 * i) * p.ldo + q * 4;
         if (p.odtype == DT_F32)
           *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = x;
@@ -513,7 +515,7 @@ __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slo
       for (int j = h; j < h + 16 && j < rows; ++j) {
         float x;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(s + (j - h) * 128 + lane * 4));
-        if (p.add != nullptr) x += load_f32(p.add, add + j * p.ldadd + lane, p.odtype);
+        if (ADD && p.add != nullptr) x += load_f32(p.add, add + j * p.ldadd + lane, p.odtype);
         store_any(p.out, out + j * p.ldo + lane, p.odtype, x);
       }
     }
@@ -974,6 +976,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // weight: tokens past an accumulator's part are added in fp32, in scratch
       // that each thread reads back what it wrote to
       const int parts = T::kTokens ? 1 : max(1, (t.steps + STEPS_SUM - 1) / STEPS_SUM);
+      if constexpr (!T::kTokens) {
+        // what is added, to L2 while the products run: a row a lane, 32 m
+        if (p.add != nullptr && ms > 0) {
+          const int es = p.odtype == DT_F32 ? 4 : 2;
+          for (int c = half * 32 + lane; c < t.n; c += 64) {
+            const char* row = static_cast<const char*>(p.add) + (t.e * p.add_group + (t.n0 + c) * p.ldadd + m0) * es;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+          }
+        }
+      }
       for (int jh = 0; jh < parts * t.halves(); ++jh) {
         const int j = t.halves() == 2 ? jh >> 1 : jh, h = t.halves() == 2 ? jh & 1 : 0;
         const int acc = cur ^ h, n = t.count(h), n0 = t.n0 + (h == 0 ? 0 : t.first);
@@ -1038,7 +1050,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
               }
             }
           }
-          if (ms > 0) store_block(p, slot, v, out + c * p.ldo, add + c * p.ldadd, n - c, ms, lane);
+          if (ms > 0) store_block<!T::kTokens>(p, slot, v, out + c * p.ldo, add + c * p.ldadd, n - c, ms, lane);
         }
         if (some && half * 32 >= n) read();
       }

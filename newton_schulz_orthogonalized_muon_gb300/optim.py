@@ -12,10 +12,10 @@ their own shape (the printed Muon class of "迎接DeepSeek开源周…Muon优化
 §代码: ``g.view(g.size(0), -1)`` and ``p.shape[:2]``), passed to the library
 as ``scale_dim``.
 
-``Muon`` keeps the fp32 momentum of every Muon parameter and the two fp32
-AdamW moments of the rest on the device and calls ``muon_step`` and
-``adamw_step`` once each per ``step()``; all arithmetic runs in the
-library's kernels.
+``Muon`` keeps the fp32 momentum of every Muon parameter and the two AdamW
+moments of the rest, in fp32 or in 8 bits, on the device and calls ``muon_step``
+and ``adamw_step`` (or ``adamw8_step``) once each per ``step()``; all
+arithmetic runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -23,7 +23,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _binding
+from . import _binding, ops
 
 
 _ADAMW_NAME_KEYS = ("embed", "lm_head")
@@ -76,12 +76,16 @@ class Muon:
     module docstring).  The AdamW fallback takes ``adamw_lr`` (default
     ``lr``), ``adamw_betas``, ``adamw_eps`` and ``adamw_wd`` (default
     ``wd``); each AdamW parameter counts its own steps for the bias
-    correction, as the printed class does."""
+    correction, as the printed class does.  ``adamw_states``: 32, or 8 for
+    moments in 8 bits (ops.adamw8_step; 2 bytes a parameter instead of 8, each
+    step rounded with its count as the seed).  ``scale_dims`` maps a parameter
+    name to the max(A, B) of its update scale where that is not the
+    parameter's own (a weight of several experts' matrices)."""
 
     def __init__(self, named_params, *, lr: float, wd: float = 0.1, momentum: float = 0.95, nesterov: bool = True,
                  ns_steps: int = 5, ns_method: str = "standard", update_rms: float = 0.2, split_heads=None,
                  adamw_lr=None, adamw_betas=(0.9, 0.95), adamw_eps: float = 1e-8, adamw_wd=None, higher_rank=False,
-                 ns_dtype=None, handle=None):
+                 ns_dtype=None, handle=None, adamw_states: int = 32, scale_dims=None):
         self.muon, adamw = split_params(named_params, higher_rank)
         self.adamw_names = [n for n, _ in adamw]
         self.adamw_params = [p for _, p in adamw]
@@ -92,6 +96,12 @@ class Muon:
         self.ns_steps, self.ns_method, self.update_rms = int(ns_steps), ns_method, float(update_rms)
         heads = dict(split_heads or {})
         self.split = [int(heads.get(e.name, 1)) for e in self.muon]
+        dims = dict(scale_dims or {})
+        for e in self.muon:
+            e.scale_dim = int(dims.get(e.name, e.scale_dim))
+        if adamw_states not in (8, 32):
+            raise ValueError("adamw_states must be 8 or 32")
+        self.adamw_states = adamw_states
         self.adamw_lr = float(lr if adamw_lr is None else adamw_lr)
         self.betas = (float(adamw_betas[0]), float(adamw_betas[1]))
         self.eps = float(adamw_eps)
@@ -99,8 +109,11 @@ class Muon:
         self.ns_dtype = ns_dtype      # None: bf16 tensor cores when every Muon parameter is bf16, else the fp32 path
         self.handle = handle
         self.momenta = [torch.zeros(e.rows, e.cols, dtype=torch.float32, device=e.param.device) for e in self.muon]
-        self.exp_avg = [torch.zeros_like(p, dtype=torch.float32) for p in self.adamw_params]
-        self.exp_avg_sq = [torch.zeros_like(p, dtype=torch.float32) for p in self.adamw_params]
+        if adamw_states == 8:
+            self.adamw8 = [ops.adamw8_state(p) for p in self.adamw_params]
+        else:
+            self.exp_avg = [torch.zeros_like(p, dtype=torch.float32) for p in self.adamw_params]
+            self.exp_avg_sq = [torch.zeros_like(p, dtype=torch.float32) for p in self.adamw_params]
         self.adamw_steps = [0] * len(self.adamw_params)
 
     def step(self, closure=None):
@@ -133,18 +146,27 @@ class Muon:
                 self.adamw_steps[j] += 1
                 by_count.setdefault(self.adamw_steps[j], []).append(j)
         for count, jdx in sorted(by_count.items()):
-            _binding.adamw_step([self.adamw_params[j] for j in jdx],
-                                [self.adamw_params[j].grad.contiguous() for j in jdx],
-                                [self.exp_avg[j] for j in jdx], [self.exp_avg_sq[j] for j in jdx],
-                                step=count, lr=self.adamw_lr, beta1=self.betas[0], beta2=self.betas[1],
-                                eps=self.eps, wd=self.adamw_wd, handle=self.handle)
+            params = [self.adamw_params[j] for j in jdx]
+            grads = [self.adamw_params[j].grad.contiguous() for j in jdx]
+            kw = dict(step=count, lr=self.adamw_lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps,
+                      wd=self.adamw_wd, handle=self.handle)
+            if self.adamw_states == 8:
+                ops.adamw8_step(params, grads, [self.adamw8[j] for j in jdx], **kw)
+            else:
+                _binding.adamw_step(params, grads, [self.exp_avg[j] for j in jdx], [self.exp_avg_sq[j] for j in jdx], **kw)
+
+    def _moments(self, j: int) -> dict:
+        """The AdamW states of parameter j by name: fp32 moments, or codes and
+        scales as bytes."""
+        if self.adamw_states == 8:
+            return {k: t.view(torch.uint8) for k, t in self.adamw8[j]._asdict().items()}
+        return {"exp_avg": self.exp_avg[j], "exp_avg_sq": self.exp_avg_sq[j]}
 
     def state_dict(self):
         """The optimizer state (momenta, AdamW moments and step counts, by
         parameter name, as copies on the host) and its hyper-parameters."""
         return {"muon": {e.name: self.momenta[i].detach().cpu().clone() for i, e in enumerate(self.muon)},
-                "adamw": {n: {"exp_avg": self.exp_avg[j].detach().cpu().clone(),
-                              "exp_avg_sq": self.exp_avg_sq[j].detach().cpu().clone(),
+                "adamw": {n: {**{k: t.detach().cpu().clone() for k, t in self._moments(j).items()},
                               "step": self.adamw_steps[j]} for j, n in enumerate(self.adamw_names)},
                 "hparams": {"lr": self.lr, "wd": self.wd, "momentum": self.momentum, "nesterov": self.nesterov,
                             "ns_steps": self.ns_steps, "ns_method": self.ns_method, "update_rms": self.update_rms,
@@ -153,16 +175,20 @@ class Muon:
 
     def load_state_dict(self, state):
         """Restore a ``state_dict``: the same parameter names are required;
-        the hyper-parameters are taken from it."""
+        the hyper-parameters are taken from it.  AdamW states in 8 bits need a
+        state of 8 bits, those in 32 one of 32."""
         names = [e.name for e in self.muon]
         if sorted(state["muon"]) != sorted(names) or sorted(state["adamw"]) != sorted(self.adamw_names):
             raise ValueError("the state holds other parameters than this optimizer")
+        for j, n in enumerate(self.adamw_names):
+            if sorted(state["adamw"][n]) != sorted([*self._moments(j), "step"]):
+                raise ValueError(f"the AdamW states of {n} are not kept in {self.adamw_states} bits")
         for i, n in enumerate(names):
             self.momenta[i].copy_(state["muon"][n])
         for j, n in enumerate(self.adamw_names):
             st = state["adamw"][n]
-            self.exp_avg[j].copy_(st["exp_avg"])
-            self.exp_avg_sq[j].copy_(st["exp_avg_sq"])
+            for k, t in self._moments(j).items():
+                t.copy_(st[k])
             self.adamw_steps[j] = int(st["step"])
         hp = state["hparams"]
         self.lr, self.wd, self.momentum, self.nesterov = hp["lr"], hp["wd"], hp["momentum"], hp["nesterov"]

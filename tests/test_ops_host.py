@@ -165,3 +165,103 @@ def test_library_is_built_where_the_module_is_not(fake_build):
     broken.clear()
     build.build()
     assert (tmp / "module.so").exists()
+
+
+# ------------------------------- experts, products and states in 8 bits
+def test_expert_oracle_against_autograd():
+    rng = np.random.default_rng(5)
+    x, w, g = (rng.standard_normal(s) for s in ((20, 6), (4, 5, 6), (20, 5)))
+    at = [0, 7, 7, 18, 19]
+    tx, tw = torch.tensor(x, requires_grad=True), torch.tensor(w, requires_grad=True)
+    y = torch.cat([tx[a:b] @ tw[e].t() for e, (a, b) in enumerate(zip(at, at[1:]))] + [torch.zeros(1, 5, dtype=torch.float64)])
+    y.backward(torch.tensor(g))
+    assert np.allclose(oo.expert_matmul(x, w, at)[0], y.detach().numpy(), atol=1e-12)
+    assert np.allclose(oo.expert_matmul(g, w, at, True)[0], tx.grad.numpy(), atol=1e-12)
+    assert np.allclose(oo.expert_weight_grad(g, x, at)[0], tw.grad.numpy(), atol=1e-12)
+
+
+def test_expert_ranges_of_offsets_that_break_the_rule():
+    assert oo.expert_ranges([5, 100, 40, 90, 150], 120) == [(5, 100), (100, 100), (100, 100), (100, 120)]
+    assert oo.expert_ranges([-3, 2, 1], 10) == [(0, 2), (2, 2)]
+
+
+def test_weight_oracle_against_torch_casts():
+    rng = np.random.default_rng(6)
+    w = (rng.standard_normal((200, 300)) * np.exp(2 * rng.standard_normal((200, 1)))).astype(np.float32)
+    codes, scales = oo.act8_encode_weight(w.astype(np.float64))
+    unit = np.repeat(np.repeat(2.0 ** (scales.T.astype(np.float64) - 127), 128, 0)[:200], 128, 1)[:, :300]
+    cast = torch.tensor(w / unit).float().to(torch.float8_e4m3fn)
+    assert np.array_equal(cast.view(torch.uint8).numpy(), codes)
+    assert np.array_equal(oo.act8_decode_weight(codes, scales), cast.double().numpy() * unit)
+    top = np.abs(w[:128, :128]).max() / unit[0, 0]
+    assert 224 < top <= 448
+    # the transpose's codes are the codes transposed
+    other, other_s = oo.act8_encode_weight(w.T.astype(np.float64))
+    assert np.array_equal(other, codes.T) and np.array_equal(other_s, scales.T)
+
+
+def test_adamw8_oracle():
+    # the tables are those of the formats
+    assert oo.root_table()[1] == (1 + 1 / 16) / 256 and oo.root_table()[255] == 248.0 and oo.root_table()[0] == 0
+    assert (np.diff(oo.root_table()) > 0).all()
+    # the noise: the bytes of the hash, uniform enough
+    z = oo.adamw8_noise(1 << 16, 7)
+    assert abs(z.mean() - 0.5) < 0.005 and len(np.unique(z)) == 256
+    assert not np.array_equal(z, oo.adamw8_noise(1 << 16, 8))
+    # rounding is right on average: the mean of many roundings of one value
+    x = np.full(1 << 16, 0.3)
+    x[::128] = 1.0                                  # the block's largest
+    for table, largest, least in ((oo.e4m3_table()[:0x7F], 448.0, 0), (oo.root_table(), 248.0, 1)):
+        codes, scales, _ = oo.adamw8_codes(x, z, table, largest, least)
+        value = table[codes] * 2.0 ** (np.repeat(scales.astype(float), 128) - 127)
+        assert abs(value[x == 0.3].mean() - 0.3) < 0.3 * 2.0 ** -4 / 64
+    # the step itself is the 64-bit form's of AdamW
+    import oracle
+    rng = np.random.default_rng(8)
+    p, g, m, v = rng.standard_normal(50), rng.standard_normal(50), rng.standard_normal(50), rng.random(50)
+    kw = dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8, wd=0.1)
+    new, m1, r1 = oo.adamw8_step(p, g, m, np.sqrt(v), 3, **kw)
+    want, m2, v2 = oracle.adamw_step(p, g, m, v, 3, **kw)
+    assert np.allclose(new, want, atol=1e-13) and np.allclose(m1, m2, atol=1e-13) and np.allclose(r1 * r1, v2, atol=1e-13)
+
+
+def test_new_operators_reject_a_null_handle(lib):
+    out = ctypes.c_uint64()
+    assert lib.muon_expert_matmul(None, None, 8, None, 8, 64, None, None, 8, 1, 8, 8, 1, 0, 1, None) == 1
+    assert lib.muon_expert_weight_grad(None, None, 8, None, 8, None, None, 8, 64, None, 8, 64, 1, 8, 8, 1, 1, 0, None, 0, None) == 1
+    assert lib.muon_expert_weight_grad_workspace(None, 1, 8, 8, 1, ctypes.byref(out)) == 1
+    assert lib.muon_act8_store_weight(None, None, 1, None, 128, None, 128, None, 1, 1, 1, 0, None) == 1
+    assert lib.muon_act8_restore_weight(None, None, 128, None, 1, 1, None, 1, 1, 1, 0, None) == 1
+    assert lib.muon_act8_matmul(None, None, 128, None, 16, None, 128, None, 1, 1, None, 1, 1, 1, 1, 0, None) == 1
+    assert lib.muon_adamw8_step(None, None, 0, 1, 0, 1e-3, 0.9, 0.95, 1e-8, 0.1, None) == 1
+    assert lib.muon_adamw8_restore(None, None, None, None, 0, 0, None) == 1
+
+
+def test_new_operators_refuse_host_tensors():
+    import newton_schulz_orthogonalized_muon_gb300 as muon
+    x, w, at = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(1, 8, 8, dtype=torch.bfloat16), torch.tensor([0, 4]).int()
+    state = muon.adamw8_state(x)
+    assert state.avg.shape == x.shape and state.avg_scale.shape == (1,)
+    for call in (lambda: muon.expert_matmul(x, w, at), lambda: muon.expert_weight_grad(x, x, at), lambda: muon.act8_store_weight(x),
+                 lambda: muon.act8_matmul(x, x, x, x), lambda: muon.act8_restore_weight(x, x),
+                 lambda: muon.adamw8_step([x], [x], [state], step=1, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, wd=0.1),
+                 lambda: muon.adamw8_restore([state])):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(ValueError, match="length"):
+        muon.adamw8_step([], [x], [], step=1, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, wd=0.1)
+
+
+def test_adamw8_struct_layout_matches_the_c_compiler(tmp_path):
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    from newton_schulz_orthogonalized_muon_gb300._binding import MuonAdamw8C as A
+    names = [n for n, _ in A._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("#include <stdio.h>\n#include <stddef.h>\n#include \"muon.h\"\nint main(void) {\n"
+                   "printf(\"%zu\\n\", sizeof(muon_adamw8_t));\n"
+                   + "".join(f"printf(\"%zu\\n\", offsetof(muon_adamw8_t, {n}));\n" for n in names) + "return 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert got == [ctypes.sizeof(A)] + [getattr(A, n).offset for n in names]
