@@ -190,9 +190,15 @@ __device__ __forceinline__ void count_tiles(const ProductParams& p, int* at) {
   int* pre = at + kMaxExperts + 4;
   const int lane = threadIdx.x & 31, mt = (p.m + MT - 1) / MT;
   int last = 0, tiles = 0;               // offset and tiles of the groups so far
+  int ahead[4];                          // four at a time: one after the other they took 600 cycles each
   for (int d0 = 0; d0 <= p.groups; d0 += 32) {
-    const int d = d0 + lane;
-    int v = d <= p.groups ? min(max(p.offsets != nullptr ? p.offsets[d] : d == 0 ? 0 : p.tokens, 0), p.tokens) : p.tokens;
+    const int d = d0 + lane, turn = (d0 >> 5) & 3;
+    if (turn == 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        ahead[q] = p.offsets == nullptr ? (d + 32 * q == 0 ? 0 : p.tokens) : d + 32 * q <= p.groups ? p.offsets[d + 32 * q] : p.tokens;
+    }
+    int v = min(max(turn == 0 ? ahead[0] : turn == 1 ? ahead[1] : turn == 2 ? ahead[2] : ahead[3], 0), p.tokens);
     v = max(v, last);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -616,7 +622,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(&bar->tmem, 512);
-  if (warp == 2) count_tiles<KIND>(p, at);
+  if (warp == 3 && lane == 0) {
+    tma_prefetch_map(&ma);
+    tma_prefetch_map(&mb);
+    if (!T::kBmn) tma_prefetch_map(&mb32);
+  }
+  if (warp == 2) {
+    // (what follows the cluster's barrier comes after this wait too)
+    pdl_wait();
+    count_tiles<KIND>(p, at);
+  }
+  pdl_launch_dependents();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -1089,9 +1105,9 @@ cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pai
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(product_kernel<KIND>), SMEM, done);
   if (e != cudaSuccess) return e;
   const long long some = mt * nt < 1 ? 1 : mt * nt < pairs ? mt * nt : pairs;
-  product_kernel<KIND><<<dim3(2 * static_cast<unsigned>(some)), Traits<KIND>::THREADS, SMEM, s>>>(maps[0], maps[1],
-                                                                                                    maps[2], p);
-  return cudaGetLastError();
+  const cudaError_t l = launch_k(pdl_level() >= 1, product_kernel<KIND>, dim3(2 * static_cast<unsigned>(some)),
+                                 dim3(Traits<KIND>::THREADS), SMEM, s, maps[0], maps[1], maps[2], p);
+  return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 // dw = add + the splits' partial results, in their order.
