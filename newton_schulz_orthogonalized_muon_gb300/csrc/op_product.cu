@@ -622,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(&bar->tmem, 512);
-  if (warp == 3 && lane == 0) {
+  if (warp == 3 && lane == 0 && p.tokens > 0) {
     tma_prefetch_map(&ma);
     tma_prefetch_map(&mb);
     if (!T::kBmn) tma_prefetch_map(&mb32);

@@ -722,9 +722,23 @@ PyObject* act8_matmul(Args a) {
 }
 
 // ------------------------------------------------- AdamW with states in 8 bits
+// Where a refused item stands, put into words only then.
+struct Place {
+  const char* list;
+  Py_ssize_t i;
+  const char* part = "";
+  std::string text() const { return std::string(list) + "[" + std::to_string(i) + "]" + part; }
+};
+
 // A list or tuple, held while its items are read.
 struct Items {
   PyObject* seq;
+  Items(PyObject* o, const Place& what) : seq(PySequence_Fast(o, "")) {
+    if (seq == nullptr) {
+      PyErr_Clear();
+      refuse(what.text() + " must be an Adamw8State");
+    }
+  }
   Items(PyObject* o, const char* what) : seq(PySequence_Fast(o, "")) {
     if (seq == nullptr) {
       PyErr_Clear();
@@ -737,28 +751,29 @@ struct Items {
   Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
   PyObject* at(Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
   // item i, a contiguous tensor on the target's device of one of two types
-  const at::Tensor& tensor(Py_ssize_t i, const Target& t, const std::string& what, at::ScalarType one, at::ScalarType other) const {
-    if (!THPVariable_Check(at(i))) refuse(what + " must be a CUDA tensor");
+  const at::Tensor& tensor(Py_ssize_t i, const Target& t, const Place& what, at::ScalarType one, at::ScalarType other) const {
+    if (!THPVariable_Check(at(i))) refuse(what.text() + " must be a CUDA tensor");
     const at::Tensor& v = THPVariable_Unpack(at(i));
-    if (!v.is_cuda() || v.get_device() != t.dev) refuse(what + " must be a CUDA tensor on device " + std::to_string(t.dev));
-    if (!v.is_contiguous()) refuse(what + " must be contiguous");
-    if (v.scalar_type() != one && v.scalar_type() != other) refuse(what + " has a type that is not supported");
+    if (!v.is_cuda() || v.get_device() != t.dev) refuse(what.text() + " must be a CUDA tensor on device " + std::to_string(t.dev));
+    if (!v.is_contiguous()) refuse(what.text() + " must be contiguous");
+    if (v.scalar_type() != one && v.scalar_type() != other) refuse(what.text() + " has a type that is not supported");
     return v;
   }
 };
 
-// The states' part of a tensor's entry.
-muon_adamw8_t state_of(const Target& t, PyObject* state, const std::string& what, at::Tensor* shape_of) {
-  const Items s(state, what.c_str());
-  if (s.size() != 4) refuse(what + " must be an Adamw8State");
-  const at::Tensor &avg = s.tensor(0, t, what + ".avg", at::kFloat8_e4m3fn, at::kByte),
-                   &root = s.tensor(1, t, what + ".root", at::kByte, at::kByte),
-                   &as = s.tensor(2, t, what + ".avg_scale", at::kByte, at::kByte),
-                   &rs = s.tensor(3, t, what + ".root_scale", at::kByte, at::kByte);
+// The states' part of a tensor's entry.  Whatever a call reads is kept by it: the
+// lists may change while other Python threads run.
+muon_adamw8_t state_of(const Target& t, PyObject* state, Py_ssize_t i, std::vector<at::Tensor>& keep) {
+  const Items s(state, Place{"states", i});
+  if (s.size() != 4) refuse(Place{"states", i}.text() + " must be an Adamw8State");
+  const at::Tensor &avg = s.tensor(0, t, Place{"states", i, ".avg"}, at::kFloat8_e4m3fn, at::kByte),
+                   &root = s.tensor(1, t, Place{"states", i, ".root"}, at::kByte, at::kByte),
+                   &as = s.tensor(2, t, Place{"states", i, ".avg_scale"}, at::kByte, at::kByte),
+                   &rs = s.tensor(3, t, Place{"states", i, ".root_scale"}, at::kByte, at::kByte);
   const int64_t n = avg.numel(), blocks = round_up(n, kBlock) / kBlock;
   if (root.numel() != n || as.numel() != blocks || rs.numel() != blocks)
-    refuse(what + " needs as many roots as averages, and a scale of each for 128 of them");
-  if (shape_of != nullptr) *shape_of = avg;
+    refuse(Place{"states", i}.text() + " needs as many roots as averages, and a scale of each for 128 of them");
+  for (const at::Tensor* k : {&avg, &root, &as, &rs}) keep.push_back(*k);
   muon_adamw8_t e{};
   e.avg = static_cast<uint8_t*>(avg.data_ptr());
   e.root = static_cast<uint8_t*>(root.data_ptr());
@@ -777,21 +792,23 @@ PyObject* adamw8_step(Args a) {
   const Py_ssize_t n = params.size();
   if (grads.size() != n || states.size() != n) refuse("params, grads and states must have the same length");
   std::vector<muon_adamw8_t> all;
-  std::vector<at::Tensor> written;
+  std::vector<at::Tensor> written, keep;
   all.reserve(n);
   written.reserve(n);
+  keep.reserve(5 * n);
   for (Py_ssize_t i = 0; i < n; ++i) {
-    const std::string at = "[" + std::to_string(i) + "]";
-    const at::Tensor &p = params.tensor(i, t, "params" + at, at::kFloat, at::kBFloat16),
-                     &g = grads.tensor(i, t, "grads" + at, at::kFloat, at::kBFloat16);
-    muon_adamw8_t e = state_of(t, states.at(i), "states" + at, nullptr);
-    if (g.numel() != p.numel() || e.numel != p.numel()) refuse("grads" + at + " or states" + at + " has the wrong size");
+    const at::Tensor &p = params.tensor(i, t, Place{"params", i}, at::kFloat, at::kBFloat16),
+                     &g = grads.tensor(i, t, Place{"grads", i}, at::kFloat, at::kBFloat16);
+    muon_adamw8_t e = state_of(t, states.at(i), i, keep);
+    if (g.numel() != p.numel() || e.numel != p.numel())
+      refuse(Place{"grads", i}.text() + " or " + Place{"states", i}.text() + " has the wrong size");
     e.param = p.data_ptr();
     e.grad = g.data_ptr();
     e.param_dtype = code_of(p.scalar_type());
     e.grad_dtype = code_of(g.scalar_type());
     all.push_back(e);
     written.push_back(p);
+    keep.push_back(g);
   }
   muon_status_t st;
   {
@@ -811,27 +828,25 @@ PyObject* adamw8_restore(Args a) {
   if (!type || (*type != at::kFloat && *type != at::kBFloat16)) refuse("dtype must be float32 or bfloat16");
   const Py_ssize_t n = states.size();
   std::vector<muon_adamw8_t> all;
-  std::vector<at::Tensor> values, likes;
+  std::vector<at::Tensor> values, keep;                 // four of each state
   std::vector<void*> avg, root;
   std::vector<int64_t> bytes;
   int64_t total = 0;
   for (Py_ssize_t i = 0; i < n; ++i) {
-    at::Tensor like;
-    all.push_back(state_of(t, states.at(i), "states[" + std::to_string(i) + "]", &like));
-    likes.push_back(std::move(like));
+    all.push_back(state_of(t, states.at(i), i, keep));
     // each on a boundary of 256 bytes
     bytes.push_back(total);
     total += round_up(all.back().numel * static_cast<int64_t>(c10::elementSize(*type)), 256) * 2;
   }
   // one storage for all: an allocation for each took 1 us, most of a small call
-  const at::Tensor whole = n > 0 ? empty({total}, likes[0], at::kByte) : at::Tensor();
+  const at::Tensor whole = n > 0 ? empty({total}, keep[0], at::kByte) : at::Tensor();
   for (Py_ssize_t i = 0; i < n; ++i) {
     for (int k = 0; k < 2; ++k) {
       const int64_t from = bytes[i] + k * round_up(all[i].numel * static_cast<int64_t>(c10::elementSize(*type)), 256);
       at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
                                                               c10::scalarTypeToTypeMeta(*type));
       v.unsafeGetTensorImpl()->set_storage_offset(from / static_cast<int64_t>(c10::elementSize(*type)));
-      v.unsafeGetTensorImpl()->set_sizes_contiguous(likes[i].sizes());
+      v.unsafeGetTensorImpl()->set_sizes_contiguous(keep[4 * i].sizes());
       (k == 0 ? avg : root).push_back(v.data_ptr());
       values.push_back(std::move(v));
     }
