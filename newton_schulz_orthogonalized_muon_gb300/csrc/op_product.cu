@@ -125,41 +125,56 @@ struct Tiles {
   const ProductParams& p;
   const int* at;       // [groups + 1] offsets
   const int* pre;      // [groups + 1] tiles before a group (tokens)
-  int mt, total, e = 0;
+  // (a division takes 150 cycles; with seven of them a tile was 1000)
+  int mt, total, size = 0, nt = 0;     // size, nt: n of a tile and such tiles, of group `of` (weight: of all)
+  int e = 0, of = -1;
 
   __device__ __forceinline__ Tiles(const ProductParams& q, const int* a) : p(q), at(a), pre(a + kMaxExperts + 4) {
     mt = (p.m + MT - 1) / MT;
-    total = Traits<KIND>::kTokens ? pre[p.groups] : p.groups * mt * ((p.n + nsize() - 1) / nsize()) * p.splits;
+    if constexpr (Traits<KIND>::kTokens) {
+      total = pre[p.groups];
+    } else {
+      size = tile_n(p.n, p.most, false);
+      nt = (p.n + size - 1) / size;
+      total = p.groups * mt * nt * p.splits;
+    }
   }
-  __device__ __forceinline__ int nsize() const { return tile_n(p.n, p.most, false); }
   // A group's tiles go eight m at a time: the pairs that run together share
   // panels of A and of B in L2.
-  __device__ __forceinline__ void place(int in, int nt, int& m0, int& n0, int size) const {
-    const int band = in / (8 * nt), r = in - band * 8 * nt, rows = min(8, mt - band * 8), j = r / rows;
-    m0 = (band * 8 + r - j * rows) * MT;
-    n0 = j * size;
+  __device__ __forceinline__ void place(uint32_t in, Tile& t) const {
+    const uint32_t band = in < 8u * nt ? 0u : in / (8u * nt), r = in - band * 8u * nt;
+    const uint32_t rows = min(8u, static_cast<uint32_t>(mt) - band * 8u), j = rows == 8u ? r >> 3 : r / rows;
+    t.m0 = static_cast<int>(band * 8u + r - j * rows) * MT;
+    t.n0 = static_cast<int>(j) * size;
   }
   // (by way of shuffles: one tile for the warp)
   __device__ __forceinline__ Tile get(int i) {
     Tile t;
     if constexpr (Traits<KIND>::kTokens) {
       while (pre[e + 1] <= i) ++e;
-      const int len = at[e + 1] - at[e], size = tile_n(len, p.most, true);
+      if (e != of) {
+        of = e;
+        const int len = at[e + 1] - at[e];
+        size = tile_n(len, p.most, true);
+        nt = len <= size ? 1 : (len + size - 1) / size;
+      }
       t.e = e;
-      place(i - pre[e], (len + size - 1) / size, t.m0, t.n0, size);
+      place(i - pre[e], t);
       t.n0 += at[e];
       t.n = min(size, at[e + 1] - t.n0);
       t.steps = (p.k + Traits<KIND>::BK - 1) / Traits<KIND>::BK;
       t.t0 = t.len = t.split = 0;
     } else {
-      const int size = nsize(), per = mt * ((p.n + size - 1) / size);
+      uint32_t u = static_cast<uint32_t>(i);
       t.split = 0;
       if (p.splits > 1) {                // splits of a tile are neighbours
-        t.split = i % p.splits;
-        i /= p.splits;
+        const uint32_t n = static_cast<uint32_t>(p.splits), v = u / n;
+        t.split = static_cast<int>(u - v * n);
+        u = v;
       }
-      t.e = i / per;
-      place(i - t.e * per, per / mt, t.m0, t.n0, size);
+      const uint32_t per = static_cast<uint32_t>(mt) * nt, g = p.groups == 1 ? 0u : u / per;
+      t.e = static_cast<int>(g);
+      place(u - g * per, t);
       t.n = min(size, p.n - t.n0);
       t.t0 = at[t.e];
       t.len = at[t.e + 1] - t.t0;
