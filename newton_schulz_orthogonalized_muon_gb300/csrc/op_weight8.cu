@@ -8,7 +8,12 @@
 //
 // Bound by HBM.  A CTA takes a block: it is read once into registers (a half
 // warp a row, 8 columns a thread), its codes leave as they are and, turned
-// around in shared memory, as the transpose's.
+// around in shared memory, as the transpose's.  A block's loads and its stores
+// do not overlap, so the more blocks an SM holds the better, and 512 threads
+// with 3 CTAs an SM keep more bytes in flight than 256 with 4 (14336 x 4096
+// bf16: codes 34 us against 41, with the transpose's 44 against 50; 512 with 4
+// spill, 47 and 58).  That is 176 MB one way at 5.2 TB/s, 235 MB with the
+// transpose's at 5.4; the way back, which needs no maximum first, takes 30 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -20,12 +25,15 @@ namespace muon {
 namespace {
 
 constexpr int BLK = 128;
-constexpr int WTHREADS = 256;
-constexpr int PASSES = BLK / (WTHREADS / 16);      // rows a thread has
+constexpr int WTHREADS = 512;
+constexpr int ROWS = WTHREADS / 16;                // rows of a pass, 16 threads each
+constexpr int PASSES = BLK / ROWS;
+constexpr int LINES = WTHREADS / BLK;              // rows of a pass of single elements
 
 // The transpose's codes from the tile of codes, 16 rows (band) by 4 columns a
 // thread, turned around as 4 x 4 bytes.
 __device__ __forceinline__ void store_transposed(const Weight8Params& p, const uint32_t (*tile)[BLK / 4], long long o0, int c0) {
+  if (threadIdx.x >= 256) return;
   const int band = threadIdx.x & 7, word = threadIdx.x >> 3;
   uint32_t t[4][4];                                  // column, four rows a word
 #pragma unroll
@@ -79,7 +87,7 @@ __device__ __forceinline__ int block_scale(int top, int* tops) {
 // The transposing reads, 8 bands of 16 rows by 4 neighbouring words, then fall on
 // 32 different banks.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 4 : 2) weight8_store_kernel(const Weight8Params p, int blocks_c) {
+__global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 3 : 2) weight8_store_kernel(const Weight8Params p, int blocks_c) {
   __shared__ __align__(16) uint32_t tile[BLK][BLK / 4];
   __shared__ int tops[WTHREADS / 32];
   const int kb = blockIdx.x % blocks_c, ob = blockIdx.x / blocks_c;
@@ -92,7 +100,7 @@ __global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 4 : 2) weight8_stor
     uint4 raw[PASSES][NV];
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const long long o = o0 + r0 + 16 * i;
+      const long long o = o0 + r0 + ROWS * i;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         raw[i][v] = o < p.out && c < p.cols ? ld_stream16(w + o * p.ldw + c + v * kStep) : make_uint4(0u, 0u, 0u, 0u);
@@ -110,7 +118,7 @@ __global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 4 : 2) weight8_stor
     const float unit = __int_as_float((254 - e) << 23);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int r = r0 + 16 * i;
+      const int r = r0 + ROWS * i;
       float f[8];
 #pragma unroll
       for (int v = 0; v < NV; ++v) unpack16<T>(raw[i][v], f + v * kStep);
@@ -122,30 +130,30 @@ __global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 4 : 2) weight8_stor
     }
   } else {
     // rows without common alignment: a warp's lanes read elements next to each
-    // other, every second row a thread, and the codes leave by way of the tile
-    // (2612 x 6570 bf16, both ways round and back: 154 us with eight elements a
-    // lane)
+    // other, every fourth row a thread, and the codes leave by way of the tile
+    // (2612 x 6570 bf16, both ways round and back: 68 us; 154 with eight elements
+    // a lane)
     const int lc = threadIdx.x & 127, r0 = threadIdx.x >> 7, c = kb * BLK + lc;
-    T raw[BLK / 2];
+    T raw[BLK / LINES];
 #pragma unroll
-    for (int i = 0; i < BLK / 2; ++i) {
-      const long long o = o0 + r0 + 2 * i;
+    for (int i = 0; i < BLK / LINES; ++i) {
+      const long long o = o0 + r0 + LINES * i;
       raw[i] = o < p.out && c < p.cols ? w[o * p.ldw + c] : from_f32<T>(0.f);
     }
 #pragma unroll
-    for (int i = 0; i < BLK / 2; ++i) top = max(top, __float_as_int(to_f32(raw[i])) & 0x7FFFFFFF);
+    for (int i = 0; i < BLK / LINES; ++i) top = max(top, __float_as_int(to_f32(raw[i])) & 0x7FFFFFFF);
     e = block_scale(top, tops);
     const float unit = __int_as_float((254 - e) << 23);
     uint8_t* bytes = reinterpret_cast<uint8_t*>(tile);
 #pragma unroll
-    for (int i = 0; i < BLK / 2; i += 4) {
+    for (int i = 0; i < BLK / LINES; i += 4) {
       float f[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = to_f32(raw[i + k]) * unit;
       const uint32_t code = e != 255 ? e4m3x4(f) : 0u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int r = r0 + 2 * (i + k);
+        const int r = r0 + LINES * (i + k);
         bytes[r * BLK + (((lc >> 2) ^ (4 * ((r >> 4) & 7))) << 2) + (lc & 3)] = static_cast<uint8_t>(code >> (8 * k));
       }
     }
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(WTHREADS, sizeof(T) == 2 ? 4 : 2) weight8_stor
     const int l = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int r = (threadIdx.x >> 4) + 16 * i;
+      const int r = (threadIdx.x >> 4) + ROWS * i;
       store_eight(p, o0 + r, kb * BLK + l * 8, *reinterpret_cast<const uint2*>(&tile[r][(2 * l) ^ (4 * ((r >> 4) & 7))]));
     }
   }
@@ -171,12 +179,12 @@ __global__ void __launch_bounds__(WTHREADS) weight8_restore_kernel(const Weight8
   const long long o0 = static_cast<long long>(ob) * BLK;
   const float unit = __int_as_float(p.scales[kb * p.lds + ob * p.lds_row] << 23);      // 255: infinity, times 0: NaN
   T* w = static_cast<T*>(const_cast<void*>(p.w));
-  __shared__ T rows[VEC ? 1 : 16][VEC ? 1 : BLK + 2];
+  __shared__ T rows[VEC ? 1 : ROWS][VEC ? 1 : BLK + 2];
   if (VEC && c >= p.cols) return;
   uint2 code[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const long long o = o0 + r0 + 16 * i;
+    const long long o = o0 + r0 + ROWS * i;
     code[i] = make_uint2(0u, 0u);
     if (o < p.out && c < p.cols) {
       const uint8_t* from = p.codes + o * p.ldc + c;
@@ -189,7 +197,7 @@ __global__ void __launch_bounds__(WTHREADS) weight8_restore_kernel(const Weight8
   }
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const long long o = o0 + r0 + 16 * i;
+    const long long o = o0 + r0 + ROWS * i;
     if (VEC && o >= p.out) break;
     float f[8];
     e4m3x4_values(code[i].x, unit, f);
@@ -205,8 +213,8 @@ __global__ void __launch_bounds__(WTHREADS) weight8_restore_kernel(const Weight8
       __syncthreads();
       // a warp's lanes write elements next to each other
       const int cc = kb * BLK + (threadIdx.x & 127);
-      for (int r = threadIdx.x >> 7; r < 16; r += 2)
-        if (cc < p.cols && o0 + 16 * i + r < p.out) w[(o0 + 16 * i + r) * p.ldw + cc] = rows[r][threadIdx.x & 127];
+      for (int r = threadIdx.x >> 7; r < ROWS; r += LINES)
+        if (cc < p.cols && o0 + ROWS * i + r < p.out) w[(o0 + ROWS * i + r) * p.ldw + cc] = rows[r][threadIdx.x & 127];
       __syncthreads();
     }
   }
