@@ -12,18 +12,18 @@
 //   input      columns (W)          tokens (dy)        outputs
 //   weight     columns (x)          outputs (dy)       tokens
 //   8 bits     outputs (W's codes)  tokens (x's codes) columns
-// A CTA pair forms 256 m (128 a CTA) by up to 512 n (tcgen05.mma.cta_group::2).
+// A CTA pair forms 256 m (128 a CTA) by up to 256 n, 448 with 8 bits
+// (tcgen05.mma.cta_group::2), in one of two accumulators that tiles take in turn.
 // The ragged dimension, tokens, is n: the tensor core takes n in steps of 32,
 // so an expert's last tile costs what it has, where rows of m would be padded
 // to 256 (17% of the work at 768 tokens an expert).
 //
-// More than 256 n (224 with 8 bits) are two halves with an accumulator each,
-// that share A in shared memory: a step brings 48 KB for 1024 cycles of
-// products where two tiles bring 64.  Both accumulators (all of TMEM) are then
-// one tile's.  So that the products need not wait while one is read out, the
-// second half runs LAG steps behind the first: the first is read out while the
-// second's last steps run, the second while the next tile's first half starts.
-// Tiles of one half alternate between the accumulators.
+// With 8 bits more than 224 n are two halves with an accumulator each, that
+// share A in shared memory: a step brings 44 KB a CTA for 448 n where two tiles
+// bring 60.  So that the products need not wait while one accumulator is read
+// out, the second half runs LAG steps behind the first: the first is read out
+// while the second's last steps run, the second while the next tile's first half
+// starts.
 //
 // Operands come by TMA with 128-byte swizzle, K-major or MN-major as they lie in
 // memory, through two rings of 16 KB slots, A's and B's.  Eight epilogue warps
@@ -48,9 +48,10 @@ constexpr int STAGE = 2 * BOX;           // a step's part of an operand: 128 row
 constexpr int A_SLOTS = 6, B_SLOTS = 6;
 constexpr int LAG = 3;                   // steps that a tile's second half runs behind its first
 static_assert(A_SLOTS >= LAG + B_SLOTS / 2, "a slot of A is free when the slots of B that are loaded with it are");
+static_assert(A_SLOTS == B_SLOTS, "of a step's, where there is no second half, the same");
 constexpr int EPI_WARPS = 8, SLOT = 2048;
 constexpr int STEPS_SUM = 32;            // weight: steps of 64 tokens an accumulator takes
-constexpr int PART_WARP = 2 * 4 * 1024;  // floats of scratch of an epilogue warp
+constexpr int PART_WARP = 4 * 1024;      // floats of scratch of an epilogue warp
 constexpr int B_OFF = A_SLOTS * STAGE;
 constexpr int EPI_OFF = B_OFF + B_SLOTS * STAGE;
 constexpr int GROUP_OFF = EPI_OFF + EPI_WARPS * SLOT;
@@ -194,7 +195,7 @@ struct Tiles {
     t.len = __shfl_sync(0xffffffffu, t.len, 0);
     t.split = __shfl_sync(0xffffffffu, t.split, 0);
     t.steps = __shfl_sync(0xffffffffu, t.steps, 0);
-    t.first = t.n <= Traits<KIND>::NT ? t.n : ((t.n + 1) / 2 + 31) / 32 * 32;
+    t.first = !Traits<KIND>::k8 || t.n <= Traits<KIND>::NT ? t.n : ((t.n + 1) / 2 + 31) / 32 * 32;
     return t;
   }
 };
@@ -559,7 +560,7 @@ __device__ __forceinline__ void zero_rows(const ProductParams& p, int from, int 
 // A and B and the second half's part k = s - LAG of B (A's is there), a slot of B
 // each.  Steps go in runs of n that are alike: f(first, second, k0, k1, n), with
 // constants that say which halves have products and their first k, says whether to
-// go on.  LAST: a half's last step is a run of its own.  EVERY: a run ends where a
+// go on.  LAST: the first half's last step is a run of its own.  EVERY: a run ends where a
 // half's k is a multiple of it (0: nowhere).
 template <bool LAST, int EVERY, typename F>
 __device__ __forceinline__ void runs_of(const Tile& t, F&& f) {
@@ -570,7 +571,7 @@ __device__ __forceinline__ void runs_of(const Tile& t, F&& f) {
     const int k1 = s - LAG;
     int n = first ? t.steps - s : end - s;
     if (two && s < LAG) n = min(n, LAG - s);
-    if (LAST && n > 1 && ((first && s + n == t.steps) || (second && k1 + n == t.steps))) --n;
+    if (LAST && n > 1 && first && s + n == t.steps) --n;
     if constexpr (EVERY > 0) {
       if (first) n = min(n, EVERY - s % EVERY);
       if (second) n = min(n, EVERY - k1 % EVERY);
@@ -588,11 +589,6 @@ __device__ __forceinline__ void runs_of(const Tile& t, F&& f) {
     s += n;
   }
 }
-// Slots of B that a tile's steps before s take.
-__device__ __forceinline__ int slots_before(const Tile& t, int s) {
-  return min(s, t.steps) + (t.halves() == 2 ? max(0, s - LAG) : 0);
-}
-
 // An expert's last tokens, where the products take some that are not its own.
 template <int KIND>
 __device__ __forceinline__ bool mended(const Tile& t, int k) {
@@ -700,30 +696,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         constexpr bool D0 = decltype(first)::value, D1 = decltype(second)::value;
         // an expert's last tokens go to this CTA's own warp, which clears what
         // follows them (see below)
-        const bool own0 = D0 && mended<KIND>(t, k0), own1 = D1 && mended<KIND>(t, k1);
-        const uint32_t mine = (own0 ? b0 : 0u) + (own1 ? b1 : 0u);
-        const uint32_t both = 2 * ((D0 ? b0 : 0u) + (D1 ? b1 : 0u) - mine) + (mine > 0 ? static_cast<uint32_t>(sizeof(uint4)) : 0u);
+        const bool own = mended<KIND>(t, k0);
+        const uint32_t both = own ? static_cast<uint32_t>(sizeof(uint4)) : 2 * ((D0 ? b0 : 0u) + (D1 ? b1 : 0u));
 #pragma unroll 1
         for (; n > 0; --n) {
           ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
           if (!ok) return false;
           const uint32_t fb = lead + r.s * 8, ob = owns + r.s * 8, to0 = sb + B_OFF + r.s * STAGE;
           if (warp == 0) {
-            if (KIND == PRODUCT_WEIGHT && mine > 0) warp_expect(ob, mine);
+            if (own) warp_expect(ob, b0);
             if (rank == 0) {
               // (the weight's barriers count two arrivals, one of them the clearing warp's)
-              if (KIND == PRODUCT_WEIGHT && mine == 0) warp_arrive(here + r.s * 8);
+              if (KIND == PRODUCT_WEIGHT && !own) warp_arrive(here + r.s * 8);
               warp_expect(here + r.s * 8, both);
             }
             if constexpr (D0) {
-              if (KIND == PRODUCT_WEIGHT && own0)
+              if (own)
                 load_a(Own{}, k0, sb + ra.s * STAGE, ob);
               else
                 load_a(Pair{}, k0, sb + ra.s * STAGE, fb);
               ra.next();
             }
           } else if constexpr (D0) {
-            if (KIND == PRODUCT_WEIGHT && own0)
+            if (own)
               load_b(Own{}, part0, n0, k0, to0, ob);
             else
               load_b(Pair{}, part0, n0, k0, to0, fb);
@@ -735,17 +730,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
               ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
               if (!ok) return false;
               to1 = sb + B_OFF + r.s * STAGE;
-              if (warp == 0 && rank == 0) {
-                warp_arrive(here + r.s * 8);       // nothing waits for it: its phase goes on
-                if (KIND == PRODUCT_WEIGHT) warp_arrive(here + r.s * 8);
-              }
+              if (warp == 0 && rank == 0) warp_arrive(here + r.s * 8);       // nothing waits for it: its phase goes on
             }
-            if (warp == 3) {
-              if (KIND == PRODUCT_WEIGHT && own1)
-                load_b(Own{}, part1, n1, k1, to1, ob);
-              else
-                load_b(Pair{}, part1, n1, k1, to1, fb);
-            }
+            if (warp == 3) load_b(Pair{}, part1, n1, k1, to1, fb);
             r.next();
           }
           ++k0;
@@ -887,7 +874,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // cleared, in both operands: what they hold may be infinite or NaN.
       const uint32_t full = mapa_shared(smem_u32(&bar->full[0]), 0), to = mapa_shared(smem_u32(&bar->token[1]), 0);
       uint32_t phases = 0;               // of own[], a bit each
-      int sa = 0, sbb = 0;               // the tile's first slots
+      int first = 0;                     // the tile's first slot, of A and of B
       bool ok = true;
       auto clear = [&](uint32_t base, int boxes, int rest) {
         const int rows = 16 - (rest & 15);
@@ -900,13 +887,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
         if (t.steps == 0) continue;
-        for (int h = 0; ok && h < t.halves() && mended<KIND>(t, t.steps - 1); ++h) {
-          const int s = (sbb + slots_before(t, t.steps - 1 + h * LAG)) % B_SLOTS, rest = t.len & 63;
+        if (mended<KIND>(t, t.steps - 1)) {
+          const int s = (first + t.steps - 1) % B_SLOTS, rest = t.len & 63;
           ok = wait_warp(&bar->own[s], (phases >> s) & 1u, abort, p);
           if (!ok) break;
           phases ^= 1u << s;
-          if (h == 0) clear(sb + (sa + t.steps - 1) % A_SLOTS * STAGE, 2, rest);
-          clear(sb + B_OFF + s * STAGE, (t.padded(h) / 2 + 63) / 64, rest);
+          clear(sb + s * STAGE, 2, rest);
+          clear(sb + B_OFF + s * STAGE, (t.padded(0) / 2 + 63) / 64, rest);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -917,8 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           }
           __syncwarp();
         }
-        sa = (sa + t.steps) % A_SLOTS;
-        sbb = (sbb + t.halves() * t.steps) % B_SLOTS;
+        first = (first + t.steps) % B_SLOTS;
       }
     }
   } else if (T::k8 && warp >= 4 && warp < T::EPI_WARP0) {
@@ -1017,8 +1003,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           }
         }
       }
-      for (int jh = 0; jh < parts * t.halves(); ++jh) {
-        const int j = t.halves() == 2 ? jh >> 1 : jh, h = t.halves() == 2 ? jh & 1 : 0;
+      const int turns = T::k8 ? t.halves() : parts;
+      for (int j = 0; j < turns; ++j) {
+        const int h = T::k8 ? j : 0;
         const int acc = cur ^ h, n = t.count(h), n0 = t.n0 + (h == 0 ? 0 : t.first);
         const long long out = (T::kTokens ? 0 : t.e * p.out_group + t.split * p.out_split) + n0 * p.ldo + m0;
         const long long add = (T::kTokens ? 0 : t.e * p.add_group) + n0 * p.ldadd + m0;
@@ -1069,7 +1056,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           if constexpr (!T::kTokens) {
             if (parts > 1) {
               float* own = p.part + (static_cast<long long>(pair * 2 + static_cast<int>(rank)) * EPI_WARPS + ew) * PART_WARP +
-                           h * (PART_WARP / 2) + (c >> 6) * 1024 + lane;
+                           (c >> 6) * 1024 + lane;
               if (j > 0) {
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] += own[q * 32];
