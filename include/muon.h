@@ -491,11 +491,12 @@ muon_status_t muon_act8_restore_weight(muon_handle_t h, const uint8_t* codes, in
 /* y[t][o] = sum over c of x[t][c] w[o][c] of stored activations (muon_act8_store:
  * codes, ldc, scales, lds) and a stored weight (wcodes, ldw, wscales, s_col,
  * s_row as above).  On the tensor cores, from the codes and scales as they are:
- * the factors are exact, sums are fp32 (truncated with each 32 products that are
- * added), rounded once to odtype.  A value stored as NaN makes its token's row,
- * or its weight's columns, NaN.
+ * the factors are exact, sums are fp32 (truncated by up to 2^-23 of themselves
+ * with each 32 products that are added), rounded once to odtype.  A value stored
+ * as NaN makes its token's row, or its weight's columns, NaN.
  *   y        odtype [rows][out], row stride ldy
- * rows, out and cols are free; cols == 0 gives zeros. */
+ *   cols     at most 2^20, which lose up to 2^-8 of a sum of one sign
+ * rows and out are free; cols == 0 gives zeros. */
 muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
                                const uint8_t* wcodes, int64_t ldw, const uint8_t* wscales, int64_t s_col,
                                int64_t s_row, void* y, int64_t ldy, int64_t rows, int64_t cols, int64_t out,
@@ -514,8 +515,9 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
  * for element i: x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B,
  * x ^= x >> 16.  (e4m3 below its normal range: steps of 2^-9.)  Calls with other
  * seeds round apart, so an average that moves by less than half a step moves all
- * the same; use another one each step.  A NaN or an infinity in a block's new state makes the whole block's
- * state NaN (byte 255, codes 0).
+ * the same; use another one each step.  A NaN or an infinity in a block's new
+ * state makes the whole block's state NaN (byte 255, codes 0).  v below 2^-126,
+ * and eps + r below it, count as 0.
  * tensors: a host array, read during the call; a tensor may not be in it twice.
  * n == 0 is a valid no-op. */
 typedef struct {

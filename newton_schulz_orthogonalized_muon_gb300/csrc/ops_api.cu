@@ -15,7 +15,7 @@ using namespace muon;
 
 namespace {
 
-constexpr int64_t kMaxSide = int64_t(1) << 20;       // of an expert's weight
+constexpr int64_t kMaxSide = int64_t(1) << 20;       // of an expert's weight; products that an 8-bit sum has
 constexpr int64_t kMaxTokens = int64_t(1) << 30;     // token and row counts fit an int with room to spare
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -766,6 +766,7 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
     muon_status_t st = check_act8(h, codes, ldc, scales, lds, rows, cols);
     if (st == MUON_OK) st = check_weight8(h, wcodes, ldw, wscales, out, cols);
     if (st != MUON_OK) return st;
+    MUON_CHECK(cols <= kMaxSide, "cols must be at most 2^20");
     if (rows == 0 || out == 0) return MUON_OK;
     MUON_CHECK(s_col >= 0 && s_row >= 0, "negative scale stride");
     MUON_CHECK(y != nullptr && aligned(y, odtype == MUON_F32 ? 4 : 2) && (ldy >= out || rows == 1),

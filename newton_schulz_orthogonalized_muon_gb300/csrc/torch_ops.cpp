@@ -733,11 +733,10 @@ struct Place {
 // A list or tuple, held while its items are read.
 struct Items {
   PyObject* seq;
-  Items(PyObject* o, const Place& what) : seq(PySequence_Fast(o, "")) {
-    if (seq == nullptr) {
-      PyErr_Clear();
-      refuse(what.text() + " must be an Adamw8State");
-    }
+  // (no other sequence: reading one runs its code, which may change the lists)
+  Items(PyObject* o, const Place& what) : seq(o) {
+    if (!PyTuple_Check(o) && !PyList_Check(o)) refuse(what.text() + " must be an Adamw8State");
+    Py_INCREF(o);
   }
   Items(PyObject* o, const char* what) : seq(PySequence_Fast(o, "")) {
     if (seq == nullptr) {

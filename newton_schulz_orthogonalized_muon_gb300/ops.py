@@ -243,7 +243,8 @@ def act8_matmul(codes, scales, wcodes, wscales, *, dtype=torch.bfloat16, handle=
     w [out, cols] kept by act8_store_weight, on the tensor cores in 8 bits.
 
     The codes and their scales are multiplied as they are, exactly; sums are
-    fp32, rounded once.  What is stored as NaN makes its row (its column) NaN."""
+    fp32 (of at most 2^20 cols), rounded once.  What is stored as NaN makes its
+    row (its column) NaN."""
     if stream is not None:
         with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
             return act8_matmul(codes, scales, wcodes, wscales, dtype=dtype, handle=handle)
