@@ -494,24 +494,26 @@ __device__ __forceinline__ void store_packed(uint32_t slot, const uint32_t* w, u
     if (r + 8 * i < rows) *reinterpret_cast<uint4*>(to + (r + 8 * i) * ld + q * 8) = x[i];
 }
 
+// What is added to a block of 32 m by 32 n, from `add`: a lane has 4 m of every
+// fourth row.
+__device__ __forceinline__ void load_added(const ProductParams& p, long long add, int rows, int lane, float (*f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if ((lane >> 3) + 4 * i < rows) load4(p.add, add + ((lane >> 3) + 4 * i) * p.ldadd + (lane & 7) * 4, p.odtype, f[i]);
+}
+
 // The block in fp32, v[j] row j, to rows of 32 m from (out, add), of any type and
-// place.  Rows past `rows` and m past `ms` are not there.
+// place.  Rows past `rows` and m past `ms` are not there.  f: what is added, where
+// rows are wide.
 template <bool ADD>
-__device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slot, const float* v, long long out,
+__device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slot, const float* v, float (*f)[4], long long out,
                                             long long add, int rows, int ms, int lane) {
   const uint32_t s = smem_u32(slot);
   __syncwarp();
-  // 16 rows at a time; what is added is asked for first
   const bool wide = p.vec && ms >= 32;
   const int wr = lane >> 3, wq = lane & 7;
-  float f[8][4];
-  if (wide && ADD && p.add != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (wr + 4 * i < rows) load4(p.add, add + (wr + 4 * i) * p.ldadd + wq * 4, p.odtype, f[i]);
-  }
-#pragma unroll
-  for (int h = 0; h < 32; h += 16) {
+  for (int h = 0; h < 32; h += 16) {       // 16 rows at a time
     if (h > 0) __syncwarp();
 #pragma unroll
     for (int j = 0; j < 16; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s + j * 128 + lane * 4), "f"(v[h + j]) : "memory");
@@ -1009,6 +1011,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         const int acc = cur ^ h, n = t.count(h), n0 = t.n0 + (h == 0 ? 0 : t.first);
         const long long out = (T::kTokens ? 0 : t.e * p.out_group + t.split * p.out_split) + n0 * p.ldo + m0;
         const long long add = (T::kTokens ? 0 : t.e * p.add_group) + n0 * p.ldadd + m0;
+        // what is added to this warp's first block is asked for before the wait,
+        // each other block's when the one before is stored (8 experts of 125 rows,
+        // 768 x 2304 in fp32: 30.3 us; asked for when it is due 32.8, with a second
+        // set of registers 31.2)
+        float f[8][4];
+        const bool adds = !T::kTokens && p.add != nullptr && p.vec && ms >= 32 && j == turns - 1;
+        if constexpr (!T::kTokens) {
+          if (adds) load_added(p, add + half * 32 * p.ldadd, n - half * 32, lane, f);
+        }
         if (some) {
           ok = wait_warp<32>(&bar->tfull[acc], (ph >> acc) & 1u, abort, p);
           if (!ok) break;
@@ -1068,7 +1079,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
               }
             }
           }
-          if (ms > 0) store_block<!T::kTokens>(p, slot, v, out + c * p.ldo, add + c * p.ldadd, n - c, ms, lane);
+          if (ms > 0) store_block<!T::kTokens>(p, slot, v, f, out + c * p.ldo, add + c * p.ldadd, n - c, ms, lane);
+          if constexpr (!T::kTokens) {
+            if (adds && c + 64 < n) load_added(p, add + (c + 64) * p.ldadd, n - c - 64, lane, f);
+          }
         }
         if (some && half * 32 >= n) read();
       }
