@@ -378,7 +378,7 @@ cudaError_t launch_adamw8_restore(Adamw8Params& p, cudaStream_t s);
 enum ProductKind : int { PRODUCT_FORWARD = 0, PRODUCT_INPUT = 1, PRODUCT_WEIGHT = 2, PRODUCT_ACT8 = 3 };
 constexpr int kMaxExperts = 1024;
 struct ProductParams {
-  const int* offsets;      // [groups + 1] on the token axis, or nullptr (one group of all tokens)
+  const int* offsets;      // [groups + 1] on the token axis (8 bits: one group of all tokens, not read)
   const void* add;         // weight: [groups][n][m] of odtype, or nullptr
   void* out;               // tokens: [tokens][m]; weight: [groups][n][m]; of odtype
   long long ldo, out_group, out_split, ldadd, add_group;   // row and group strides in elements
@@ -392,9 +392,10 @@ struct ProductParams {
                            // over tokens)
   int odtype;
   int f16;                 // the operands are fp16 (else bf16)
-  int most;                // set by the launcher: n of a tile, at most
-  int splits;              // weight, set by the launcher: parts of an expert's tokens, results out_split apart
-  int vec;                 // set by the launcher: rows of out and add are 16-byte aligned
+  int most;                // set by the launcher, as what follows but err and timeout_ns: n of a tile, at most
+  int mt, size, nt, total; // tiles over m; where n is not ragged: n of a tile, tiles over n, tiles
+  int splits;              // weight: parts of an expert's tokens, results out_split apart
+  int vec;                 // rows of out and add are 16-byte aligned
   unsigned* err;           // the handle's error word
   unsigned long long timeout_ns;
 };

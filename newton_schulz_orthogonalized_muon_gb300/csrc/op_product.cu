@@ -66,6 +66,7 @@ static_assert(SMEM <= 232448, "shared memory");
 template <int KIND>
 struct Traits {
   static constexpr bool kTokens = KIND != PRODUCT_WEIGHT;                   // n are tokens
+  static constexpr bool kRagged = KIND == PRODUCT_FORWARD || KIND == PRODUCT_INPUT;   // of several experts
   static constexpr bool kAmn = KIND == PRODUCT_INPUT || KIND == PRODUCT_WEIGHT;   // A is read MN-major
   static constexpr bool kBmn = KIND == PRODUCT_WEIGHT;
   static constexpr bool k8 = KIND == PRODUCT_ACT8;
@@ -120,38 +121,36 @@ struct Tile {
   __device__ __forceinline__ int padded(int h) const { return (count(h) + 31) / 32 * 32; }
 };
 
-// The tiles in order of their groups; a thread asks for rising numbers.
+// The tiles in order of their groups; a thread asks for rising numbers.  What does
+// not hang on the offsets the host has worked out: a division takes 150 cycles, and
+// a short call waits for the first tile's.
 template <int KIND>
 struct Tiles {
   const ProductParams& p;
   const int* at;       // [groups + 1] offsets
-  const int* pre;      // [groups + 1] tiles before a group (tokens)
-  // (a division takes 150 cycles; with seven of them a tile was 1000)
-  int mt, total, size = 0, nt = 0;     // size, nt: n of a tile and such tiles, of group `of` (weight: of all)
+  const int* pre;      // [groups + 1] tiles before a group (ragged)
+  int total, size, nt; // size, nt: n of a tile and such tiles, of group `of` where they are ragged
   int e = 0, of = -1;
 
-  __device__ __forceinline__ Tiles(const ProductParams& q, const int* a) : p(q), at(a), pre(a + kMaxExperts + 4) {
-    mt = (p.m + MT - 1) / MT;
-    if constexpr (Traits<KIND>::kTokens) {
-      total = pre[p.groups];
-    } else {
-      size = tile_n(p.n, p.most, false);
-      nt = (p.n + size - 1) / size;
-      total = p.groups * mt * nt * p.splits;
-    }
-  }
+  __device__ __forceinline__ Tiles(const ProductParams& q, const int* a)
+      : p(q), at(a), pre(a + kMaxExperts + 4), total(Traits<KIND>::kRagged ? pre[q.groups] : q.total), size(q.size), nt(q.nt) {}
   // A group's tiles go eight m at a time: the pairs that run together share
   // panels of A and of B in L2.
   __device__ __forceinline__ void place(uint32_t in, Tile& t) const {
     const uint32_t band = in < 8u * nt ? 0u : in / (8u * nt), r = in - band * 8u * nt;
-    const uint32_t rows = min(8u, static_cast<uint32_t>(mt) - band * 8u), j = rows == 8u ? r >> 3 : r / rows;
+    const uint32_t rows = min(8u, static_cast<uint32_t>(p.mt) - band * 8u), j = rows == 8u ? r >> 3 : r / rows;
     t.m0 = static_cast<int>(band * 8u + r - j * rows) * MT;
     t.n0 = static_cast<int>(j) * size;
   }
   // (by way of shuffles: one tile for the warp)
   __device__ __forceinline__ Tile get(int i) {
     Tile t;
-    if constexpr (Traits<KIND>::kTokens) {
+    if constexpr (KIND == PRODUCT_ACT8) {
+      t.e = t.t0 = t.len = t.split = 0;
+      place(i, t);
+      t.n = min(size, p.tokens - t.n0);
+      t.steps = (p.k + Traits<KIND>::BK - 1) / Traits<KIND>::BK;
+    } else if constexpr (Traits<KIND>::kRagged) {
       while (pre[e + 1] <= i) ++e;
       if (e != of) {
         of = e;
@@ -173,7 +172,7 @@ struct Tiles {
         t.split = static_cast<int>(u - v * n);
         u = v;
       }
-      const uint32_t per = static_cast<uint32_t>(mt) * nt, g = p.groups == 1 ? 0u : u / per;
+      const uint32_t per = static_cast<uint32_t>(p.mt) * nt, g = p.groups == 1 ? 0u : u / per;
       t.e = static_cast<int>(g);
       place(u - g * per, t);
       t.n = min(size, p.n - t.n0);
@@ -204,7 +203,7 @@ struct Tiles {
 template <int KIND>
 __device__ __forceinline__ void count_tiles(const ProductParams& p, int* at) {
   int* pre = at + kMaxExperts + 4;
-  const int lane = threadIdx.x & 31, mt = (p.m + MT - 1) / MT;
+  const int lane = threadIdx.x & 31;
   int last = 0, tiles = 0;               // offset and tiles of the groups so far
   int ahead[4];                          // four at a time: one after the other they took 600 cycles each
   for (int d0 = 0; d0 <= p.groups; d0 += 32) {
@@ -212,7 +211,7 @@ __device__ __forceinline__ void count_tiles(const ProductParams& p, int* at) {
     if (turn == 0) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        ahead[q] = p.offsets == nullptr ? (d + 32 * q == 0 ? 0 : p.tokens) : d + 32 * q <= p.groups ? p.offsets[d + 32 * q] : p.tokens;
+        ahead[q] = d + 32 * q <= p.groups ? p.offsets[d + 32 * q] : p.tokens;
     }
     int v = min(max(turn == 0 ? ahead[0] : turn == 1 ? ahead[1] : turn == 2 ? ahead[2] : ahead[3], 0), p.tokens);
     v = max(v, last);
@@ -224,11 +223,11 @@ __device__ __forceinline__ void count_tiles(const ProductParams& p, int* at) {
     int before = __shfl_up_sync(0xffffffffu, v, 1);
     if (lane == 0) before = d0 == 0 ? v : last;
     int c = 0;                           // tiles of group d - 1
-    if constexpr (Traits<KIND>::kTokens) {
+    if constexpr (Traits<KIND>::kRagged) {
       const int len = v - before;
       if (len > 0) {
         const int size = tile_n(len, p.most, true);
-        c = (len + size - 1) / size * mt;
+        c = (len + size - 1) / size * p.mt;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -508,9 +507,37 @@ __device__ __forceinline__ void load_added(const ProductParams& p, long long add
 template <bool ADD>
 __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slot, const float* v, float (*f)[4], long long out,
                                             long long add, int rows, int ms, int lane) {
+  if (!p.vec || ms < 32) {
+    // a lane has one m: rows leave as they are, in 7200 cycles for 80 rows a warp
+    // (13000 by way of shared memory, an element at a time)
+    if (lane >= ms) return;
+    auto rows_of_type = [&](auto type) {
+      using O = decltype(type);
+      O* to = static_cast<O*>(p.out) + out + lane;
+      const O* more = static_cast<const O*>(p.add) + add + lane;
+#pragma unroll
+      for (int h = 0; h < 32; h += 8) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = v[h + j];
+          if (ADD && p.add != nullptr && h + j < rows) x[j] += to_f32(more[(h + j) * p.ldadd]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (h + j < rows) to[(h + j) * p.ldo] = from_f32<O>(x[j]);
+      }
+    };
+    if (p.odtype == DT_F32)
+      rows_of_type(0.f);
+    else if (p.odtype == DT_BF16)
+      rows_of_type(__nv_bfloat16{});
+    else
+      rows_of_type(__half{});
+    return;
+  }
   const uint32_t s = smem_u32(slot);
   __syncwarp();
-  const bool wide = p.vec && ms >= 32;
   const int wr = lane >> 3, wq = lane & 7;
 #pragma unroll
   for (int h = 0; h < 32; h += 16) {       // 16 rows at a time
@@ -518,30 +545,20 @@ __device__ __forceinline__ void store_block(const ProductParams& p, uint8_t* slo
 #pragma unroll
     for (int j = 0; j < 16; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s + j * 128 + lane * 4), "f"(v[h + j]) : "memory");
     __syncwarp();
-    if (wide) {
-      const int r = h + wr, q = wq;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (r + 4 * i >= rows) break;
-        const uint4 raw = lds16(s + (r - h + 4 * i) * 128 + q * 16);
-        float4 x = make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w));
-        if (ADD && p.add != nullptr) x.x += f[h / 4 + i][0], x.y += f[h / 4 + i][1], x.z += f[h / 4 + i][2], x.w += f[h / 4 + i][3];
-        const long long to = out + (r + 4 * i) * p.ldo + q * 4;
-        if (p.odtype == DT_F32)
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = x;
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
-              p.odtype == DT_BF16 ? make_uint2(pack2<__nv_bfloat16>(x.x, x.y), pack2<__nv_bfloat16>(x.z, x.w))
-                                  : make_uint2(pack2<__half>(x.x, x.y), pack2<__half>(x.z, x.w));
-      }
-    } else if (lane < ms) {
-#pragma unroll 1
-      for (int j = h; j < h + 16 && j < rows; ++j) {
-        float x;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(s + (j - h) * 128 + lane * 4));
-        if (ADD && p.add != nullptr) x += load_f32(p.add, add + j * p.ldadd + lane, p.odtype);
-        store_any(p.out, out + j * p.ldo + lane, p.odtype, x);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int r = h + wr + 4 * i;
+      if (r >= rows) break;
+      const uint4 raw = lds16(s + (wr + 4 * i) * 128 + wq * 16);
+      float4 x = make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w));
+      if (ADD && p.add != nullptr) x.x += f[h / 4 + i][0], x.y += f[h / 4 + i][1], x.z += f[h / 4 + i][2], x.w += f[h / 4 + i][3];
+      const long long to = out + r * p.ldo + wq * 4;
+      if (p.odtype == DT_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = x;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
+            p.odtype == DT_BF16 ? make_uint2(pack2<__nv_bfloat16>(x.x, x.y), pack2<__nv_bfloat16>(x.z, x.w))
+                                : make_uint2(pack2<__half>(x.x, x.y), pack2<__half>(x.z, x.w));
     }
   }
 }
@@ -643,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
   if (warp == 2) {
     // (what follows the cluster's barrier comes after this wait too)
     pdl_wait();
-    count_tiles<KIND>(p, at);
+    if constexpr (KIND != PRODUCT_ACT8) count_tiles<KIND>(p, at);
   }
   pdl_launch_dependents();
   tc_fence_before();
@@ -1088,7 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       }
       if (t.halves() == 1 && t.steps > 0) cur ^= 1;
     }
-    if constexpr (T::kTokens) {
+    if constexpr (T::kRagged) {
       const int w = (pair * 2 + static_cast<int>(rank)) * EPI_WARPS + ew, warps = npairs * 2 * EPI_WARPS;
       zero_rows(p, 0, at[0], w, warps, lane);
       zero_rows(p, at[p.groups], p.tokens, w, warps, lane);
@@ -1110,17 +1127,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
 }
 
 template <int KIND>
-cudaError_t launch_kind(const ProductParams& p, const CUtensorMap* maps, int pairs, cudaStream_t s) {
-  const long long mt = (p.m + MT - 1) / MT;
-  // tiles, at most: the tokens' experts are on the device
-  const long long nt = Traits<KIND>::kTokens
-                           ? p.tokens / p.most + (p.tokens < p.groups ? p.tokens : p.groups)
-                           : static_cast<long long>(p.groups) * ((p.n + 31) / 32) * p.splits;
-  if (mt * nt > 0x3FFFFFFFll) return cudaErrorInvalidValue;
+cudaError_t launch_kind(ProductParams p, const CUtensorMap* maps, int pairs, cudaStream_t s) {
+  p.mt = (p.m + MT - 1) / MT;
+  long long total;
+  if constexpr (Traits<KIND>::kRagged) {
+    // at most: the tokens' experts are on the device
+    total = static_cast<long long>(p.mt) * (p.tokens / p.most + (p.tokens < p.groups ? p.tokens : p.groups));
+  } else {
+    const int len = Traits<KIND>::kTokens ? p.tokens : p.n;
+    p.size = tile_n(len, p.most, Traits<KIND>::kTokens);
+    p.nt = len <= p.size ? 1 : (len + p.size - 1) / p.size;
+    total = static_cast<long long>(p.mt) * p.nt * p.groups * p.splits;
+  }
+  if (total > 0x3FFFFFFFll) return cudaErrorInvalidValue;
+  p.total = static_cast<int>(total);
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(product_kernel<KIND>), SMEM, done);
   if (e != cudaSuccess) return e;
-  const long long some = mt * nt < 1 ? 1 : mt * nt < pairs ? mt * nt : pairs;
+  const long long some = total < 1 ? 1 : total < pairs ? total : pairs;
   const cudaError_t l = launch_k(pdl_level() >= 1, product_kernel<KIND>, dim3(2 * static_cast<unsigned>(some)),
                                  dim3(Traits<KIND>::THREADS), SMEM, s, maps[0], maps[1], maps[2], p);
   return l != cudaSuccess ? l : cudaGetLastError();
