@@ -277,6 +277,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* w) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // What a whole warp issues, by one of its lanes: the lanes stay together, so that
 // addresses and coordinates are kept in uniform registers, which these
 // instructions take.  (Loops of a single lane took 550 cycles a step and more.)
@@ -657,14 +661,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     tma_prefetch_map(&mb);
     if (!T::kBmn) tma_prefetch_map(&mb32);
   }
+  // the cluster's barrier passes while the kernel before is waited for (after it, it
+  // held the first loads up by 1000 cycles)
+  tc_fence_before();
+  cluster_arrive();
   if (warp == 2) {
-    // (what follows the cluster's barrier comes after this wait too)
+    // (what follows the CTA's barrier comes after this wait too)
     pdl_wait();
     if constexpr (KIND != PRODUCT_ACT8) count_tiles<KIND>(p, at);
   }
   pdl_launch_dependents();
-  tc_fence_before();
-  cluster_sync_all();
+  cluster_wait();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar->tmem, 0);
   volatile int* abort = &bar->abort;
