@@ -259,9 +259,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// An arrival on a barrier of the pair that orders no memory: the accumulator has
-// been read into registers.  (With a release it waited 950 cycles for the stores
-// of the results before.)
+// An arrival on a barrier of the pair that orders no memory, for what is done in
+// TMEM and waited for there, a fence of the tensor core's before it.  (With a
+// release it waited 950 cycles for the stores of the results before.  That of the
+// scales waited for the weight's bytes that were asked for ahead: 16 x 4096 x
+// 14336 18.3 us, 13.9 without.)
 __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -998,7 +1000,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead + rs.s * 8);
+          if (lane == 0) arrive_relaxed(lead + rs.s * 8);
           rs.next();
         }
       }
