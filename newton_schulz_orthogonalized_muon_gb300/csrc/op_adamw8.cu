@@ -24,7 +24,8 @@
 // and only then are m and r rounded to codes.
 //
 // Bound by HBM: 10 bytes an element with bf16 parameters and gradients (fp32
-// states: 22).  A thread has 16 elements, 8 lanes a block.
+// states: 22).  A thread has 16 elements, 8 lanes a block.  1.05e9 bf16
+// parameters: 1.80 ms, 5.8 TB/s; their states' values in bf16 0.90 ms, 6.7 TB/s.
 #include "common.cuh"
 #include "internal.h"
 #include "op_code8.cuh"
@@ -168,7 +169,7 @@ __device__ __forceinline__ uint32_t gather4(const uint32_t* t) {
 
 // The step of 16 elements, and their states' new codes.  Measured by what it
 // executes: at the copy rate the SMs have 57 instructions for an element, 28 on
-// the ALU pipe; the plain way took 70 (45 of those), this one 40.  Arithmetic goes
+// the ALU pipe; the plain way took 70 (45 of those), this one 48.  Arithmetic goes
 // two elements at a time; codes are cut out of the fp32 pattern, scaled so that
 // they lie in it as they are kept; and what only small values need (codes below
 // the normal range, least codes, zeros) is done where a thread has one.
