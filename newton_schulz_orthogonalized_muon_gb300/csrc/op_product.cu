@@ -1186,12 +1186,9 @@ __global__ void __launch_bounds__(256) product_join_kernel(const ProductParams p
 // parts that an expert's tokens are split into (a second kernel adds their
 // results).  Wide tiles bring less to shared memory for each product; narrow ones
 // and splits give every pair of SMs something to do, down to a step's 330 cycles
-// of issue, which 160 n take: 1001 x 2042 x 1411 in 8 bits takes 31 us with tiles
-// of 448 and 21.5 with what this gives; the gradient of one weight 192 x 2088 over
-// 46894 rows 211 us without splits and 64 with them.  Two halves pay in 8 bits
-// alone: 16384 x 4096 x 14336 in 672 us against 762, but 64 experts of 768 rows,
-// 1408 -> 2048 in 217 against 205, since two halves of 16 bits are finished in
-// turn where two tiles overlap.
+// of issue, which 160 n take: 1001 x 2042 x 1411 in 8 bits takes 15.7 us with the
+// widest tiles and 10.5 with what this gives; the gradient of one weight 192 x 2088
+// over 46894 rows 212 us without splits and 62 with them.
 struct Plan {
   int most, splits;
 };
@@ -1201,7 +1198,7 @@ Plan plan_of(int kind, long long tokens, int groups, int m, int n, int k, int pa
   const long long len = weight ? n : each, steps = weight ? (each + 63) / 64 : (k + (k8 ? 127 : 63)) / (k8 ? 128 : 64);
   Plan best{};
   long long least = 0;
-  for (int most = 32; most <= (k8 ? 448 : 256); most = most == 224 && k8 ? 448 : most + 32) {
+  for (int most = 32; most <= (k8 ? 224 : 256); most += 32) {
     const long long size = tile_n(static_cast<int>(len < 1 ? 1 : len), most, !weight), rows = size < len ? size : len;
     const long long tiles = groups * mt * ((len + size - 1) / size), step = std::max<long long>(330, 2 * ((rows + 31) / 32 * 32));
     for (int splits = 1; splits == 1 || (weight && tiles * splits <= pairs && steps / splits >= 8); ++splits) {
