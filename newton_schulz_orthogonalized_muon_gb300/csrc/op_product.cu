@@ -12,21 +12,18 @@
 //   input      columns (W)          tokens (dy)        outputs
 //   weight     columns (x)          outputs (dy)       tokens
 //   8 bits     outputs (W's codes)  tokens (x's codes) columns
-// A CTA pair forms 256 m (128 a CTA) by up to 256 n, 448 with 8 bits
-// (tcgen05.mma.cta_group::2), in one of two accumulators that tiles take in turn.
-// The ragged dimension, tokens, is n: the tensor core takes n in steps of 32,
-// so an expert's last tile costs what it has, where rows of m would be padded
-// to 256 (17% of the work at 768 tokens an expert).
-//
-// With 8 bits more than 224 n are two halves with an accumulator each, that
-// share A in shared memory: a step brings 44 KB a CTA for 448 n where two tiles
-// bring 60.  So that the products need not wait while one accumulator is read
-// out, the second half runs LAG steps behind the first: the first is read out
-// while the second's last steps run, the second while the next tile's first half
-// starts.
+// A CTA pair forms 256 m (128 a CTA) by up to 256 n, 224 with 8 bits, whose scales
+// need TMEM too (tcgen05.mma.cta_group::2), in one of two accumulators that tiles
+// take in turn: one is read out while the other's products run.  The ragged
+// dimension, tokens, is n: the tensor core takes n in steps of 32, so an expert's
+// last tile costs what it has, where rows of m would be padded to 256 (17% of the
+// work at 768 tokens an expert).  (Tiles of twice the n in both accumulators, with a
+// quarter less to shared memory, are finished half by half in turn: 64 experts of
+// 768 rows, 1408 -> 2048 in 217 us against 205, 16384 x 4096 x 14336 in 8 bits in 644
+// against 635.)
 //
 // Operands come by TMA with 128-byte swizzle, K-major or MN-major as they lie in
-// memory, through two rings of 16 KB slots, A's and B's.  Eight epilogue warps
+// memory, through a ring of 16 KB slots for each.  Eight epilogue warps
 // turn 32 x 32 blocks around through shared memory (a lane holds one m), so that
 // rows leave in whole sectors.
 //
@@ -52,18 +49,15 @@ namespace {
 constexpr int MT = 256;                  // m of a pair's tile
 constexpr int BOX = 64 * 128;            // 64 rows of 128 bytes
 constexpr int STAGE = 2 * BOX;           // a step's part of an operand: 128 rows of 128 bytes, or 64 of 256
-constexpr int A_SLOTS = 6, B_SLOTS = 6;
-constexpr int LAG = 3;                   // steps that a tile's second half runs behind its first
-static_assert(A_SLOTS >= LAG + B_SLOTS / 2, "a slot of A is free when the slots of B that are loaded with it are");
-static_assert(A_SLOTS == B_SLOTS, "of a step's, where there is no second half, the same");
+constexpr int SLOTS = 6;                 // steps of both operands in flight
 constexpr int EPI_WARPS = 8, SLOT = 2048;
 constexpr int STEPS_SUM = 32;            // weight: steps of 64 tokens an accumulator takes
 constexpr int PART_WARP = 4 * 1024;      // floats of scratch of an epilogue warp
-constexpr int B_OFF = A_SLOTS * STAGE;
-constexpr int EPI_OFF = B_OFF + B_SLOTS * STAGE;
+constexpr int B_OFF = SLOTS * STAGE;
+constexpr int EPI_OFF = 2 * B_OFF;
 constexpr int GROUP_OFF = EPI_OFF + EPI_WARPS * SLOT;
 // 8 bits: the tokens' scales on their way, those of a tile for each of four blocks
-constexpr int SB_SLOTS = 3, SB_ROW = 448, SB_SLOT = 4 * SB_ROW;
+constexpr int SB_SLOTS = 3, SB_ROW = 224, SB_SLOT = 4 * SB_ROW;
 constexpr int SB_OFF = GROUP_OFF + 2 * 4 * (kMaxExperts + 4);
 constexpr int BAR_OFF = SB_OFF + SB_SLOTS * SB_SLOT;
 constexpr int SMEM = BAR_OFF + 512;
@@ -84,15 +78,14 @@ struct Traits {
   static constexpr int NT = k8 ? 224 : 256;
 };
 // The scales in TMEM, by groups of four 128-column blocks: a 32-bit word a row
-// of A (4 columns of 32 lanes) and of each half of B (8), a byte for each block.
-constexpr int SF_SLOTS = 3, SF_COLS = 20;
+// of A (4 columns of 32 lanes) and of B (8), a byte for each block.
+constexpr int SF_SLOTS = 3, SF_COLS = 12;
 static_assert(2 * Traits<PRODUCT_ACT8>::NT + SF_SLOTS * SF_COLS <= 512, "TMEM");
 
 struct alignas(16) Bars {
-  // of B's slots, that of a step's first for all that it loads
-  uint64_t full[B_SLOTS];                // the leader's, for both CTAs
-  uint64_t empty[B_SLOTS];               // each CTA's own
-  uint64_t own[B_SLOTS];                 // weight: this CTA's part of an expert's last step
+  uint64_t full[SLOTS];                  // the leader's, for both CTAs
+  uint64_t empty[SLOTS];                 // each CTA's own
+  uint64_t own[SLOTS];                   // weight: this CTA's part of an expert's last step
   uint64_t tfull[2], tempty[2];
   uint64_t sf_full[SF_SLOTS];            // 8 bits: the leader's, scales written by both CTAs
   uint64_t sf_empty[SF_SLOTS];
@@ -117,15 +110,11 @@ __host__ __device__ __forceinline__ int tile_n(int len, int most, bool even) {
 struct Tile {
   int e, m0, n0;       // group, first m, first n (of the token axis, or of the outputs)
   int n;               // that exist
-  int first;           // of them in the first half (n: there is no second)
   int t0, len;         // weight: first token and tokens of the group, or of its split
   int split;
   int steps;
 
-  __device__ __forceinline__ int halves() const { return first < n ? 2 : 1; }
-  // of half h: how many n, and the n that the product takes
-  __device__ __forceinline__ int count(int h) const { return h == 0 ? first : n - first; }
-  __device__ __forceinline__ int padded(int h) const { return (count(h) + 31) / 32 * 32; }
+  __device__ __forceinline__ int padded() const { return (n + 31) / 32 * 32; }       // the n that the product takes
 };
 
 // The tiles in order of their groups; a thread asks for rising numbers.  What does
@@ -201,7 +190,6 @@ struct Tiles {
     t.len = __shfl_sync(0xffffffffu, t.len, 0);
     t.split = __shfl_sync(0xffffffffu, t.split, 0);
     t.steps = __shfl_sync(0xffffffffu, t.steps, 0);
-    t.first = !Traits<KIND>::k8 || t.n <= Traits<KIND>::NT ? t.n : ((t.n + 1) / 2 + 31) / 32 * 32;
     return t;
   }
 };
@@ -335,9 +323,8 @@ __device__ __forceinline__ void warp_load(uint32_t dst, const CUtensorMap* map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// Commits of the products so far to one or two barriers, of both CTAs.
-template <bool TWO>
-__device__ __forceinline__ void warp_commit(uint32_t bar, uint32_t other) {
+// Commits the products so far to a barrier of both CTAs.
+__device__ __forceinline__ void warp_commit(uint32_t bar) {
   asm volatile(
       "{\n"
       " .reg .pred q;\n"
@@ -347,7 +334,6 @@ __device__ __forceinline__ void warp_commit(uint32_t bar, uint32_t other) {
       " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n"
       "}\n" ::"r"(bar)
       : "memory");
-  if constexpr (TWO) warp_commit<false>(other, 0u);
 }
 
 // A step's products of a pair, up to four of 32 bytes of k.  Descriptors by their
@@ -588,39 +574,6 @@ __device__ __forceinline__ void zero_rows(const ProductParams& p, int from, int 
   }
 }
 
-// The order of a tile's products.  Step s loads the first half's part k = s of
-// A and B and the second half's part k = s - LAG of B (A's is there), a slot of B
-// each.  Steps go in runs of n that are alike: f(first, second, k0, k1, n), with
-// constants that say which halves have products and their first k, says whether to
-// go on.  LAST: the first half's last step is a run of its own.  EVERY: a run ends where a
-// half's k is a multiple of it (0: nowhere).
-template <bool LAST, int EVERY, typename F>
-__device__ __forceinline__ void runs_of(const Tile& t, F&& f) {
-  const bool two = t.halves() == 2;
-  const int end = two && t.steps > 0 ? t.steps + LAG : t.steps;
-  for (int s = 0; s < end;) {
-    const bool first = s < t.steps, second = two && s >= LAG;
-    const int k1 = s - LAG;
-    int n = first ? t.steps - s : end - s;
-    if (two && s < LAG) n = min(n, LAG - s);
-    if (LAST && n > 1 && first && s + n == t.steps) --n;
-    if constexpr (EVERY > 0) {
-      if (first) n = min(n, EVERY - s % EVERY);
-      if (second) n = min(n, EVERY - k1 % EVERY);
-    }
-    using Yes = std::integral_constant<bool, true>;
-    using No = std::integral_constant<bool, false>;
-    bool ok = true;
-    if (first && second)
-      ok = f(Yes{}, Yes{}, s, k1, n);
-    else if (first)
-      ok = f(Yes{}, No{}, s, k1, n);
-    else if (second)
-      ok = f(No{}, Yes{}, s, k1, n);
-    if (!ok) return;
-    s += n;
-  }
-}
 // An expert's last tokens, where the products take some that are not its own.
 template <int KIND>
 __device__ __forceinline__ bool mended(const Tile& t, int k) {
@@ -641,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
   const int pair = static_cast<int>(cluster_id_x()), npairs = static_cast<int>(num_clusters_x());
   const uint32_t sb = smem_u32(smem);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < B_SLOTS; ++s) {
+    for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&bar->full[s], KIND == PRODUCT_WEIGHT ? 2 : 1);
       mbar_init(&bar->empty[s], 1);
       mbar_init(&bar->own[s], 1);
@@ -693,27 +646,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     // boxes.
     const uint32_t lead = mapa_shared(smem_u32(&bar->full[0]), 0), here = smem_u32(&bar->full[0]),
                    owns = smem_u32(&bar->own[0]);
-    Ring<A_SLOTS> ra;
-    Ring<B_SLOTS> r;
+    Ring<SLOTS> r;
     bool ok = true;
     for (int i = pair; ok && i < tiles.total; i += npairs) {
       const Tile t = tiles.get(i);
-      // of B, this CTA's part of a half, in boxes of 128 or 32 tokens, or of 64 outputs
-      const int part0 = t.padded(0) / 2, part1 = t.padded(1) / 2;
-      const int n0 = t.n0 + static_cast<int>(rank) * part0, n1 = t.n0 + t.first + static_cast<int>(rank) * part1;
-      auto bytes = [&](int part) {
-        return static_cast<uint32_t>(T::kBmn ? (part + 63) / 64 * BOX : part > 64 ? 2 * BOX : (part + 31) / 32 * (BOX / 2));
-      };
-      const uint32_t b0 = STAGE + bytes(part0), b1 = bytes(part1);       // a step's for each half, A with the first
-      const int m0 = t.m0 + static_cast<int>(rank) * 128;
-      auto load_b = [&](auto own, int part, int at, int k, uint32_t to, uint32_t fb) {
+      // of B, this CTA's half, in boxes of 128 or 32 tokens, or of 64 outputs
+      const int part = t.padded() / 2, n0 = t.n0 + static_cast<int>(rank) * part, m0 = t.m0 + static_cast<int>(rank) * 128;
+      const uint32_t bytes = STAGE + static_cast<uint32_t>(T::kBmn     ? (part + 63) / 64 * BOX
+                                                           : part > 64 ? 2 * BOX
+                                                                       : (part + 31) / 32 * (BOX / 2));       // of a step
+      auto load_b = [&](auto own, int k, uint32_t to, uint32_t fb) {
         constexpr bool PAIR = !decltype(own)::value;
         if constexpr (T::kBmn) {
-          for (int c = 0; c < part; c += 64) warp_load<PAIR>(to + c * 128, &mb, fb, at + c, t.t0 + k * 64, 0);
+          for (int c = 0; c < part; c += 64) warp_load<PAIR>(to + c * 128, &mb, fb, n0 + c, t.t0 + k * 64, 0);
         } else if (part > 64) {
-          warp_load<PAIR>(to, &mb, fb, k * T::BK, at, 0);
+          warp_load<PAIR>(to, &mb, fb, k * T::BK, n0, 0);
         } else {
-          for (int c = 0; c < part; c += 32) warp_load<PAIR>(to + c * 128, &mb32, fb, k * T::BK, at + c, 0);
+          for (int c = 0; c < part; c += 32) warp_load<PAIR>(to + c * 128, &mb32, fb, k * T::BK, n0 + c, 0);
         }
       };
       auto load_a = [&](auto own, int k, uint32_t to, uint32_t fb) {
@@ -728,54 +677,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       };
       using Own = std::integral_constant<bool, true>;
       using Pair = std::integral_constant<bool, false>;
-      runs_of<KIND == PRODUCT_WEIGHT, 0>(t, [&](auto first, auto second, int k0, int k1, int n) {
-        constexpr bool D0 = decltype(first)::value, D1 = decltype(second)::value;
+#pragma unroll 1
+      for (int k = 0; k < t.steps; ++k) {
         // an expert's last tokens go to this CTA's own warp, which clears what
         // follows them (see below)
-        const bool own = mended<KIND>(t, k0);
-        const uint32_t both = own ? static_cast<uint32_t>(sizeof(uint4)) : 2 * ((D0 ? b0 : 0u) + (D1 ? b1 : 0u));
-#pragma unroll 1
-        for (; n > 0; --n) {
-          ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
-          if (!ok) return false;
-          const uint32_t fb = lead + r.s * 8, ob = owns + r.s * 8, to0 = sb + B_OFF + r.s * STAGE;
-          if (warp == 0) {
-            if (own) warp_expect(ob, b0);
-            if (rank == 0) {
-              // (the weight's barriers count two arrivals, one of them the clearing warp's)
-              if (KIND == PRODUCT_WEIGHT && !own) warp_arrive(here + r.s * 8);
-              warp_expect(here + r.s * 8, both);
-            }
-            if constexpr (D0) {
-              if (own)
-                load_a(Own{}, k0, sb + ra.s * STAGE, ob);
-              else
-                load_a(Pair{}, k0, sb + ra.s * STAGE, fb);
-              ra.next();
-            }
-          } else if constexpr (D0) {
-            if (own)
-              load_b(Own{}, part0, n0, k0, to0, ob);
-            else
-              load_b(Pair{}, part0, n0, k0, to0, fb);
+        const bool own = mended<KIND>(t, k);
+        ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
+        if (!ok) break;
+        const uint32_t fb = lead + r.s * 8, ob = owns + r.s * 8, to = sb + r.s * STAGE;
+        if (warp == 0) {
+          if (own) warp_expect(ob, bytes);
+          if (rank == 0) {
+            // (the weight's barriers count two arrivals, one of them the clearing warp's)
+            if (KIND == PRODUCT_WEIGHT && !own) warp_arrive(here + r.s * 8);
+            warp_expect(here + r.s * 8, own ? static_cast<uint32_t>(sizeof(uint4)) : 2 * bytes);
           }
-          if constexpr (D0) r.next();
-          if constexpr (D1) {
-            uint32_t to1 = to0;
-            if constexpr (D0) {
-              ok = wait_warp(&bar->empty[r.s], r.ph ^ 1u, abort, p);
-              if (!ok) return false;
-              to1 = sb + B_OFF + r.s * STAGE;
-              if (warp == 0 && rank == 0) warp_arrive(here + r.s * 8);       // nothing waits for it: its phase goes on
-            }
-            if (warp == 3) load_b(Pair{}, part1, n1, k1, to1, fb);
-            r.next();
-          }
-          ++k0;
-          ++k1;
+          if (own)
+            load_a(Own{}, k, to, ob);
+          else
+            load_a(Pair{}, k, to, fb);
+        } else {
+          if (own)
+            load_b(Own{}, k, to + B_OFF, ob);
+          else
+            load_b(Pair{}, k, to + B_OFF, fb);
         }
-        return true;
-      });
+        r.next();
+      }
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -784,96 +712,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // and 29 (A)
       const uint32_t type = T::k8 ? 1u << 23 : (1u << 4) | (p.f16 ? 0u : (1u << 7) | (1u << 10));
       const uint32_t id0 = type | (T::kAmn ? 1u << 15 : 0u) | (T::kBmn ? 1u << 16 : 0u) | ((MT >> 4) << 24);
-      // a ring's place for each half: A's slots and the scales' are used by both
-      Ring<SF_SLOTS> rs[2];
-      Ring<A_SLOTS> ra[2];
-      Ring<B_SLOTS> rb;
+      Ring<SF_SLOTS> rs;
+      Ring<SLOTS> r;
       const uint64_t a0 = T::kAmn ? sdesc_sw128(sb, BOX, 1024) : sdesc_sw128(sb, 16, 1024);
       const uint64_t b0 = T::kBmn ? sdesc_sw128(sb + B_OFF, BOX, 1024) : sdesc_sw128(sb + B_OFF, 16, 1024);
       const uint32_t alo = static_cast<uint32_t>(a0), ahi = static_cast<uint32_t>(a0 >> 32), blo = static_cast<uint32_t>(b0),
                      bhi = static_cast<uint32_t>(b0 >> 32), empty0 = smem_u32(&bar->empty[0]);
-      int cur = 0;                       // the accumulator of the tile's first half
+      int acc = 0;
       uint32_t ph = 0u;                  // the accumulators' phases, a bit each
       bool ok = true;
       for (int i = pair; ok && i < tiles.total; i += npairs) {
         const Tile t = tiles.get(i);
-        const bool two = t.halves() == 2;
-        const uint32_t ids[2] = {id0 | (static_cast<uint32_t>(t.padded(0) >> 3) << 17),
-                                 id0 | (static_cast<uint32_t>(t.padded(1) >> 3) << 17)};
-        constexpr int PART = KIND == PRODUCT_WEIGHT ? STEPS_SUM : 1 << 30;   // steps that an accumulator takes
-        // part k of half h from the slot of B at rb
-        auto products = [&](auto half, int k) {
-          constexpr int h = decltype(half)::value;
-          const uint32_t d = tmem + (cur ^ h) * T::NT, a = alo + ra[h].s * (STAGE >> 4), b = blo + rb.s * (STAGE >> 4);
-          // of 16 k: two rows of 8 in an MN-major operand, 32 bytes of a K-major one
-          if constexpr (T::k8) {
-            const uint32_t sf = tmem + 2 * T::NT + rs[h].s * SF_COLS;
-            mma_step_scaled(d, a, ahi, b, bhi, ids[h] | ((k & 3u) << 4) | ((k & 3u) << 29), sf, sf + 4 + 8 * h, k);
-          } else {
-            mma_step<T::kAmn ? 2048 >> 4 : 2, T::kBmn ? 2048 >> 4 : 2, KIND == PRODUCT_WEIGHT>(
-                d, a, ahi, b, bhi, ids[h], k % PART, (min(t.len - k * 64, 64) + 15) / 16);
-          }
-          ra[h].next();
-        };
-        // a part's first products wait for the accumulator, its last hand it over
-        auto begins = [&](int h, int k) {
-          if (k % PART != 0) return true;
-          const bool ready = wait_warp<0, true>(&bar->tempty[cur ^ h], ((ph >> (cur ^ h)) & 1u) ^ 1u, abort, p);
-          tc_fence_after();
-          return ready;
-        };
-        auto ends = [&](auto half, int k) {
-          constexpr int h = decltype(half)::value;
-          if constexpr (T::k8) {
-            if ((k & 3) == 0 || k == t.steps) {    // the scales of a group of blocks are used
-              if (h == 1 || !two) warp_commit<false>(smem_u32(&bar->sf_empty[rs[h].s]), 0u);
-              rs[h].next();
-            }
-          }
-          if (k % PART != 0 && k != t.steps) return;
-          warp_commit<false>(smem_u32(&bar->tfull[cur ^ h]), 0u);
-          ph ^= 1u << (cur ^ h);
-        };
-        runs_of<false, KIND == PRODUCT_WEIGHT ? PART : T::k8 ? 4 : 0>(t, [&](auto first, auto second, int k0, int k1, int n) {
-          constexpr bool D0 = decltype(first)::value, D1 = decltype(second)::value;
-          if constexpr (D0) ok = begins(0, k0);
-          if constexpr (D1) ok = ok && begins(1, k1);
-          if constexpr (T::k8 && D0) {
-            if (ok && (k0 & 3) == 0) {
-              ok = wait_warp<0, true>(&bar->sf_full[rs[0].s], rs[0].ph, abort, p);
-              tc_fence_after();
-            }
-          }
-#pragma unroll 1
-          for (; ok && n > 0; --n) {
-            ok = wait_warp<0, KIND == PRODUCT_WEIGHT>(&bar->full[rb.s], rb.ph, abort, p);
+        const uint32_t id = id0 | (static_cast<uint32_t>(t.padded() >> 3) << 17), d = tmem + acc * T::NT;
+        // Steps in runs that are alike: the part of a sum that an accumulator takes
+        // (weight), a group of four blocks' scales (8 bits).
+        constexpr int RUN = KIND == PRODUCT_WEIGHT ? STEPS_SUM : T::k8 ? 4 : 1 << 30;
+        for (int k = 0; ok && k < t.steps;) {
+          if (k == 0 || KIND == PRODUCT_WEIGHT) {
+            ok = wait_warp<0, true>(&bar->tempty[acc], ((ph >> acc) & 1u) ^ 1u, abort, p);
             if (!ok) break;
-            const uint32_t free0 = empty0 + rb.s * 8;
-            if constexpr (D0) {
-              products(std::integral_constant<int, 0>{}, k0);
-              rb.next();
-            }
-            if constexpr (D1) {
-              const uint32_t free1 = empty0 + rb.s * 8;
-              products(std::integral_constant<int, 1>{}, k1);
-              rb.next();
-              warp_commit<D0>(free0, free1);
-            } else {
-              warp_commit<false>(free0, 0u);
-            }
-            ++k0;
-            ++k1;
+            tc_fence_after();
           }
-          if (!ok) return false;
-          if constexpr (D0) ends(std::integral_constant<int, 0>{}, k0);
-          if constexpr (D1) ends(std::integral_constant<int, 1>{}, k1);
-          return true;
-        });
-        if (!two) {
-          ra[1] = ra[0];
-          rs[1] = rs[0];
-          if (t.steps > 0) cur ^= 1;
+          if constexpr (T::k8) {
+            ok = wait_warp<0, true>(&bar->sf_full[rs.s], rs.ph, abort, p);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const int end = min(t.steps, k + RUN);
+#pragma unroll 1
+          for (const int k0 = k; k < end; ++k) {
+            ok = wait_warp<0, KIND == PRODUCT_WEIGHT>(&bar->full[r.s], r.ph, abort, p);
+            if (!ok) break;
+            const uint32_t a = alo + r.s * (STAGE >> 4), b = blo + r.s * (STAGE >> 4);
+            // of 16 k: two rows of 8 in an MN-major operand, 32 bytes of a K-major one
+            if constexpr (T::k8) {
+              const uint32_t sf = tmem + 2 * T::NT + rs.s * SF_COLS;
+              mma_step_scaled(d, a, ahi, b, bhi, id | ((k & 3u) << 4) | ((k & 3u) << 29), sf, sf + 4, k);
+            } else {
+              mma_step<T::kAmn ? 2048 >> 4 : 2, T::kBmn ? 2048 >> 4 : 2, KIND == PRODUCT_WEIGHT>(
+                  d, a, ahi, b, bhi, id, k - k0, (min(t.len - k * 64, 64) + 15) / 16);
+            }
+            warp_commit(empty0 + r.s * 8);
+            r.next();
+          }
+          if (!ok) break;
+          if constexpr (T::k8) {         // the scales of a group of blocks are used
+            warp_commit(smem_u32(&bar->sf_empty[rs.s]));
+            rs.next();
+          }
+          if (KIND == PRODUCT_WEIGHT || k == t.steps) {
+            warp_commit(smem_u32(&bar->tfull[acc]));
+            ph ^= 1u << acc;
+          }
         }
+        if (t.steps > 0) acc ^= 1;
       }
       commit_pair(&bar->drain, 0x1);
       if (lane == 0) mbar_wait_bounded(&bar->drain, 0, nullptr, DRAIN_NS);
@@ -910,7 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       // cleared, in both operands: what they hold may be infinite or NaN.
       const uint32_t full = mapa_shared(smem_u32(&bar->full[0]), 0), to = mapa_shared(smem_u32(&bar->token[1]), 0);
       uint32_t phases = 0;               // of own[], a bit each
-      int first = 0;                     // the tile's first slot, of A and of B
+      int first = 0;                     // the tile's first slot
       bool ok = true;
       auto clear = [&](uint32_t base, int boxes, int rest) {
         const int rows = 16 - (rest & 15);
@@ -924,12 +816,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         const Tile t = tiles.get(i);
         if (t.steps == 0) continue;
         if (mended<KIND>(t, t.steps - 1)) {
-          const int s = (first + t.steps - 1) % B_SLOTS, rest = t.len & 63;
+          const int s = (first + t.steps - 1) % SLOTS, rest = t.len & 63;
           ok = wait_warp(&bar->own[s], (phases >> s) & 1u, abort, p);
           if (!ok) break;
           phases ^= 1u << s;
           clear(sb + s * STAGE, 2, rest);
-          clear(sb + B_OFF + s * STAGE, (t.padded(0) / 2 + 63) / 64, rest);
+          clear(sb + B_OFF + s * STAGE, (t.padded() / 2 + 63) / 64, rest);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -940,7 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           }
           __syncwarp();
         }
-        first = (first + t.steps) % B_SLOTS;
+        first = (first + t.steps) % SLOTS;
       }
     }
   } else if (T::k8 && warp >= 4 && warp < T::EPI_WARP0) {
@@ -972,27 +864,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
       load();
       bool ok = true;
       for (int j = pair; ok && j < tiles.total; j += npairs) {
-        const Tile of = tiles.get(j);
-        const int behind = of.halves() == 2 ? of.first : 0;        // tokens of the first half
-        for (int k0 = 0; k0 < of.steps; k0 += 4) {
+        const int steps = tiles.get(j).steps;
+        for (int k0 = 0; k0 < steps; k0 += 4) {
           if ((k0 & 31) == 0) {
             now = next;
             load();
           }
           ok = wait_warp(&bar->sb_full[rb.s], rb.ph, abort, p);
           if (!ok) break;
-          uint32_t word[2][8];
-          const uint8_t* from = smem + SB_OFF + rb.s * SB_SLOT + lane;
+          uint32_t word[8];
+          const uint8_t* f = smem + SB_OFF + rb.s * SB_SLOT + lane;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // (the second half's columns hold nothing of use where there is none)
-            const uint8_t* f = from + (h == 0 ? 0 : behind);
-#pragma unroll
-            for (int c = 0; c < 7; ++c)
-              word[h][c] = f[c * 32] | f[SB_ROW + c * 32] << 8 | f[2 * SB_ROW + c * 32] << 16 |
-                           static_cast<uint32_t>(f[3 * SB_ROW + c * 32]) << 24;
-            word[h][7] = 0u;
-          }
+          for (int c = 0; c < 7; ++c)
+            word[c] = f[c * 32] | f[SB_ROW + c * 32] << 8 | f[2 * SB_ROW + c * 32] << 16 |
+                      static_cast<uint32_t>(f[3 * SB_ROW + c * 32]) << 24;
+          word[7] = 0u;
           uint32_t wword = 0u;
 #pragma unroll
           for (int q = 0; q < 4; ++q) wword |= __shfl_sync(0xffffffffu, now, (k0 & 31) + q) << (8 * q);
@@ -1002,8 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           if (!ok) break;
           tc_fence_after();
           tmem_st4(at0 + rs.s * SF_COLS, wword);
-          tmem_st8(at0 + rs.s * SF_COLS + 4, word[0]);
-          tmem_st8(at0 + rs.s * SF_COLS + 12, word[1]);
+          tmem_st8(at0 + rs.s * SF_COLS + 4, word);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -1019,7 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
     uint8_t* slot = smem + EPI_OFF + ew * SLOT;
     const uint32_t te[2] = {mapa_shared(smem_u32(&bar->tempty[0]), 0), mapa_shared(smem_u32(&bar->tempty[1]), 0)};
     const bool packed = p.vec && p.odtype != DT_F32 && p.add == nullptr;
-    int cur = 0;                         // the accumulator of the tile's first half
+    int acc = 0;
     uint32_t ph = 0u;                    // the accumulators' phases, a bit each
     bool ok = true;
     for (int i = pair; ok && i < tiles.total; i += npairs) {
@@ -1039,10 +924,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           }
         }
       }
-      const int turns = T::k8 ? t.halves() : parts;
-      for (int j = 0; j < turns; ++j) {
-        const int h = T::k8 ? j : 0;
-        const int acc = cur ^ h, n = t.count(h), n0 = t.n0 + (h == 0 ? 0 : t.first);
+      for (int j = 0; j < parts; ++j) {
+        const int n = t.n, n0 = t.n0;
         const long long out = (T::kTokens ? 0 : t.e * p.out_group + t.split * p.out_split) + n0 * p.ldo + m0;
         const long long add = (T::kTokens ? 0 : t.e * p.add_group) + n0 * p.ldadd + m0;
         // what is added to this warp's first block is asked for before the wait,
@@ -1050,7 +933,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         // 768 x 2304 in fp32: 30.3 us; asked for when it is due 32.8, with a second
         // set of registers 31.2)
         float f[8][4];
-        const bool adds = !T::kTokens && p.add != nullptr && p.vec && ms >= 32 && j == turns - 1;
+        const bool adds = !T::kTokens && p.add != nullptr && p.vec && ms >= 32 && j == parts - 1;
         if constexpr (!T::kTokens) {
           if (adds) load_added(p, add + half * 32 * p.ldadd, n - half * 32, lane, f);
         }
@@ -1120,7 +1003,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
         }
         if (some && half * 32 >= n) read();
       }
-      if (t.halves() == 1 && t.steps > 0) cur ^= 1;
+      if (some && t.steps > 0) acc ^= 1;
     }
     if constexpr (T::kRagged) {
       const int w = (pair * 2 + static_cast<int>(rank)) * EPI_WARPS + ew, warps = npairs * 2 * EPI_WARPS;
