@@ -33,8 +33,8 @@
 // Measured, calls that follow one another: 49152 rows through 64 experts 2048 ->
 // 1408 forward 213 - 221 us, input's gradient 200 - 206, weights' 217 - 225 (1.3 PFLOP/s,
 // the pipe 83, 81 and 64% busy), all under the power cap at 1.3 to 1.6 GHz; 48 rows
-// 37 - 38 us (214 MB at 5.7 TB/s); 16384 x 4096 -> 14336 in 8 bits 641 - 645 us (3.0
-// PFLOP/s), 16 rows 13.9 (58.7 MB at 4.2 TB/s).  Within a tile a step's operands come
+// 37 - 38 us (214 MB at 5.7 TB/s); 16384 x 4096 -> 14336 in 8 bits 635 - 638 us (3.0
+// PFLOP/s), 16 rows 13.2 (58.7 MB at 4.4 TB/s).  Within a tile a step's operands come
 // from L2 at 52 to 60 bytes a cycle and SM, which bounds the weights' gradients.
 #include <algorithm>
 
