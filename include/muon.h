@@ -510,12 +510,17 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
  *          root_scale: the smallest >= 16 with which the block's largest is at most
  *          248.  A root above 0 gets code 1 at least.
  * (all zero at start).  The step is computed from the states' values in fp32; the
- * new states are then rounded up where their part past a code plus (b + 1/2) / 256
+ * new states are then rounded up where their part past a code plus (b + u) / 256
  * is 1 or more, b being byte i % 4 of a 32-bit hash of (i / 4 + seed * 0x9E3779B1)
  * for element i: x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15, x *= 0x846CA68B,
- * x ^= x >> 16.  (e4m3 below its normal range: steps of 2^-9.)  Calls with other
- * seeds round apart, so an average that moves by less than half a step moves all
- * the same; use another one each step.  A NaN or an infinity in a block's new
+ * x ^= x >> 16.  (e4m3 below its normal range: steps of 2^-9.)  u is 1/2 where
+ * beta1 and beta2 are 31/32 at most, else (seed * 0x9E3779B1 mod 2^32) / 2^32 cut
+ * to 11 bits.  Calls with other seeds round apart, so an average that moves by less
+ * than half a step moves all the same; use another one each step, rising by one.
+ * With u = 1/2 the smallest move is 1/512 of a step: averages settle within 2^-12 /
+ * (1 - beta), at most 2^-7, of their value.  Above 31/32 any move is taken that fp32
+ * has; what its arithmetic loses of a root, up to 2^-22 a step, is 0.5% of the
+ * largest fall at beta2 = 0.9999 and 5% at 0.99999.  A NaN or an infinity in a block's new
  * state makes the whole block's state NaN (byte 255, codes 0).  v below 2^-126,
  * and eps + r below it, count as 0.
  * tensors: a host array, read during the call; a tensor may not be in it twice.

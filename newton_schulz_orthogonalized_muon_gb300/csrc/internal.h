@@ -367,6 +367,7 @@ constexpr int kAdamw8Tensors = 112;      // of a launch: its parameters are kept
 struct Adamw8Params {
   int n, pdtype, gdtype;   // (restore: pdtype is the values' type)
   uint32_t salt;
+  uint32_t part;           // what a byte of noise has past it, of 2048
   float omb1, omb2;        // 1 - beta
   float eps, decay, size;  // as AdamParams
   Adamw8Tensor t[kAdamw8Tensors];

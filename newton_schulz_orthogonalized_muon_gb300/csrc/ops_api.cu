@@ -840,6 +840,7 @@ muon_status_t muon_adamw8_step(muon_handle_t h, const muon_adamw8_t* tensors, in
     const double bc1 = 1.0 - std::pow(beta1, static_cast<double>(step)), bc2 = 1.0 - std::pow(beta2, static_cast<double>(step));
     Adamw8Params p{};
     p.salt = seed * 0x9E3779B1u;
+    p.part = std::max(beta1, beta2) > 31.0 / 32 ? p.salt >> 21 : 1024u;
     p.omb1 = static_cast<float>(1.0 - beta1);
     p.omb2 = static_cast<float>(1.0 - beta2);
     p.eps = static_cast<float>(eps);

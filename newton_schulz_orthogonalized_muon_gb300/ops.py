@@ -284,7 +284,9 @@ def adamw8_step(params, grads, states, *, step: int, lr: float, beta1: float, be
     params and grads: contiguous, fp32 or bf16; states: an Adamw8State each.
     The step is computed in fp32 from the states' values; what is kept of them
     is rounded up or down by a hash of the element's place and ``seed`` (default:
-    ``step``), so that averages move by less than a step of their codes too.
+    ``step``), so that averages move by less than a step of their codes too:
+    by as little as 1/512 of one, or, where a beta is above 31/32, by any part
+    that fp32 has, on average over seeds that rise by one.
     The same call gives the same result.  A NaN or an infinity in a gradient
     makes the state of its 128 elements NaN.  A captured call repeats its
     ``step`` and ``seed``."""

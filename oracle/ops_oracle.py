@@ -213,14 +213,17 @@ def root_table():
     return np.where(c == 0, 0.0, (1 + (c & 15) / 16.0) * 2.0 ** ((c >> 4) - 8.0))
 
 
-def adamw8_noise(n, seed):
-    """The number in (0, 1) that each element is rounded with."""
-    x = (np.arange(-(-n // 4), dtype=np.uint64) + np.uint64(seed * 0x9E3779B1 % 2 ** 32)) % np.uint64(2 ** 32)
+def adamw8_noise(n, seed, beta=0.0):
+    """The number in [0, 1) that each element is rounded with.  beta: the larger
+    of the two; above 31/32 the place in a byte's 1/256 is the call's, else its
+    middle."""
+    salt = seed * 0x9E3779B1 % 2 ** 32
+    x = (np.arange(-(-n // 4), dtype=np.uint64) + np.uint64(salt)) % np.uint64(2 ** 32)
     for shift, factor in ((16, 0x7FEB352D), (15, 0x846CA68B)):
         x = (x ^ (x >> np.uint64(shift))) * np.uint64(factor) % np.uint64(2 ** 32)
     x ^= x >> np.uint64(16)
     b = np.stack([(x >> np.uint64(8 * k)) & np.uint64(255) for k in range(4)], 1).reshape(-1)[:n]
-    return (b.astype(np.float64) + 0.5) / 256
+    return (b.astype(np.float64) + ((salt >> 21) / 2048 if beta > 31 / 32 else 0.5)) / 256
 
 
 def _blocks(x):
