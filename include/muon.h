@@ -520,9 +520,10 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
  * With u = 1/2 the smallest move is 1/512 of a step: averages settle within 2^-12 /
  * (1 - beta), at most 2^-7, of their value.  Above 31/32 any move is taken that fp32
  * has; what its arithmetic loses of a root, up to 2^-22 a step, is 0.5% of the
- * largest fall at beta2 = 0.9999 and 5% at 0.99999.  A NaN or an infinity in a block's new
- * state makes the whole block's state NaN (byte 255, codes 0).  v below 2^-126,
- * and eps + r below it, count as 0.
+ * largest fall at beta2 = 0.9999 and 5% at 0.99999.
+ * A finite gradient counts as 2^63 in magnitude at most.  A NaN or an infinity in
+ * one makes its block's states NaN (byte 255, codes 0), and the next step the
+ * block's parameters.  v below 2^-126, and eps + r below it, count as 0.
  * tensors: a host array, read during the call; a tensor may not be in it twice.
  * n == 0 is a valid no-op. */
 typedef struct {

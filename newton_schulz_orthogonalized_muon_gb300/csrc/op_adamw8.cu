@@ -32,7 +32,8 @@
 // The step is as adamw_kernel's, on the states' values in fp32:
 //   m <- m + (1 - beta1)(g - m);  v <- r^2 + (1 - beta2)(g^2 - r^2);  r = v^(1/2)
 //   p <- p decay - size m / (eps + r)
-// and only then are m and r rounded to codes.
+// and only then are m and r rounded to codes.  g is cut to 2^63 in magnitude, so
+// that squares are finite.
 //
 // Bound by HBM: 10 bytes an element with bf16 parameters and gradients (fp32
 // states: 22).  A thread has 16 elements, 8 lanes a block.  1.05e9 bf16
@@ -208,6 +209,16 @@ __device__ __forceinline__ void step16(const Adamw8Params& p, const Adamw8Tensor
 #pragma unroll
       for (int q = 0; q < 4; ++q) r[4 * k + q] = root_value((rc[k] >> (8 * q)) & 255u);
     }
+  }
+  // a finite gradient is 2^63 at most: an infinite square would make its block's
+  // states NaN, and the parameters of all 128 elements with the next step
+  float gtop = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) gtop = max3(gtop, g[k], g[k + 1]);
+  if (!(gtop < 0x1p63f)) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (fabsf(g[k]) < INFINITY) g[k] = fminf(fmaxf(g[k], -0x1p63f), 0x1p63f);
   }
   float mtop = 0.f, rtop = 0.f, mlow = INFINITY, rlow = INFINITY;
 #pragma unroll

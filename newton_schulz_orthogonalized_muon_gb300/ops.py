@@ -287,9 +287,10 @@ def adamw8_step(params, grads, states, *, step: int, lr: float, beta1: float, be
     ``step``), so that averages move by less than a step of their codes too:
     by as little as 1/512 of one, or, where a beta is above 31/32, by any part
     that fp32 has, on average over seeds that rise by one.
-    The same call gives the same result.  A NaN or an infinity in a gradient
-    makes the state of its 128 elements NaN.  A captured call repeats its
-    ``step`` and ``seed``."""
+    The same call gives the same result.  A finite gradient counts as at most
+    2^63 in magnitude.  A NaN or an infinity in one makes the states of its block
+    of 128 elements NaN, and the next step their parameters.  A captured call
+    repeats its ``step`` and ``seed``."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return adamw8_step(params, grads, states, step=step, lr=lr, beta1=beta1, beta2=beta2, eps=eps, wd=wd, seed=seed,

@@ -270,6 +270,7 @@ def adamw8_codes(x, noise, table, largest, least, given=None):
 
 def adamw8_step(p, g, m, r, step, lr, beta1, beta2, eps, wd):
     """(p, m, r) after the step, before the states are rounded."""
+    g = np.where(np.isfinite(g), np.clip(g, -2.0 ** 63, 2.0 ** 63), g)
     m = m + (1 - beta1) * (g - m)
     r = np.sqrt(r * r + (1 - beta2) * (g * g - r * r))
     size = lr * np.sqrt(1 - beta2 ** step) / (1 - beta1 ** step)

@@ -35,3 +35,14 @@ def test_a_root_that_moves_little_moves():
         frac = (u - table[lo]) / np.where(up > lo, table[up] - table[lo], 1.0)
         r = table[np.where(frac + z >= 1, up, lo)] * 2.0 ** e
     assert abs(r.mean() / beta2 ** 1500 - 1) < 0.01
+
+
+def test_large_gradients_count_as_two_to_the_63():
+    kw = dict(step=1, lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8, wd=0.1)
+    p, g = np.ones(4), np.array([1e20, -3e38, 2.0 ** 63, -1.0])
+    got = oo.adamw8_step(p, g, np.zeros(4), np.zeros(4), **kw)
+    want = oo.adamw8_step(p, np.clip(g, -2.0 ** 63, 2.0 ** 63), np.zeros(4), np.zeros(4), **kw)
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    with np.errstate(invalid="ignore"):
+        bad = oo.adamw8_step(p, np.array([np.inf, -np.inf, np.nan, 1.0]), np.zeros(4), np.zeros(4), **kw)
+    assert not np.isfinite(bad[2][:3]).any() and np.isfinite(bad[2][3])
