@@ -441,12 +441,13 @@ muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, const void* dy, i
  * zeros, whatever it holds.
  *   x, w, y   dtype (MUON_BF16 or MUON_F16); w [experts][out][cols], expert and
  *             row strides w_expert, ldw
- *   cols, out multiples of 8; strides of x and w multiples of 8, theirs and y's
- *             pointers 16-byte aligned
+ *   cols, out multiples of 8, up to 2^20, x's up to 2^16; strides of x and w
+ *             multiples of 8, theirs and y's pointers 16-byte aligned
  *   experts   1 .. 1024
- * Sums are fp32 on the tensor cores (truncated, as above: up to 6e-5 of
- * themselves over 16384 products of one sign), rounded once to dtype.
- * tokens == 0 is a valid no-op. */
+ * Sums are fp32 on the tensor cores, truncated by up to 2^-23 of themselves with
+ * each 16 products that are added (of one sign: 1.2e-4 over 16384, measured 1.1e-4;
+ * over 2^16 2^-11, what a rounding to fp16 may take, measured 4.3e-4), and rounded
+ * once to dtype.  tokens == 0 is a valid no-op. */
 muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, const void* w, int64_t ldw,
                                  int64_t w_expert, const int32_t* offsets, void* y, int64_t ldy, int64_t tokens,
                                  int64_t cols, int64_t out, int64_t experts, int32_t transpose, int32_t dtype,
@@ -457,6 +458,7 @@ muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, co
  *   dy, x    dtype, [tokens][out], [tokens][cols]
  *   add, dw  odtype (MUON_F32 or dtype) [experts][out][cols]; add may be NULL, or
  *            dw itself with its strides
+ *   cols, out up to 2^20
  * 2048 tokens at a time are added up on the tensor cores, with truncation, and
  * those sums in fp32 with rounding, in `workspace`. */
 muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,

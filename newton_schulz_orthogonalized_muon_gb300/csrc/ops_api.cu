@@ -16,6 +16,7 @@ using namespace muon;
 namespace {
 
 constexpr int64_t kMaxSide = int64_t(1) << 20;       // of an expert's weight; products that an 8-bit sum has
+constexpr int64_t kMaxSum = int64_t(1) << 16;        // products of a sum by expert: truncated by up to 2^-11, as fp16 rounds
 constexpr int64_t kMaxTokens = int64_t(1) << 30;     // token and row counts fit an int with room to spare
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -614,8 +615,9 @@ muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, co
     const muon_status_t st = check_experts(h, tokens, cols, out, experts, dtype);
     if (st != MUON_OK) return st;
     MUON_CHECK(offsets != nullptr && aligned(offsets, 4), "offsets is NULL or not aligned");
-    if (tokens == 0) return MUON_OK;
     const int64_t in = transpose ? out : cols, to = transpose ? cols : out;
+    MUON_CHECK(in <= kMaxSum, "the dimension that is summed over must be at most 2^16");
+    if (tokens == 0) return MUON_OK;
     MUON_CHECK(!bad_rows(x, ldx, tokens, in) && !bad_rows(w, ldw, out, cols) &&
                    (experts == 1 || (w_expert % 8 == 0 && w_expert >= (out - 1) * (out > 1 ? ldw : 0) + cols &&
                                      w_expert <= (int64_t(1) << 38))),

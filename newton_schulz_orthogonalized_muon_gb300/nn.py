@@ -180,7 +180,8 @@ class _ExpertLinear(torch.autograd.Function):
 def expert_linear(x, weight, offsets):
     """Differentiable ops.expert_matmul: x [tokens, cols], weight [experts,
     out, cols], offsets int32 [experts + 1], which are kept for the backward
-    pass like the other inputs: writing to them before it raises."""
+    pass like the other inputs: writing to them before it raises.  cols is 2^16
+    at most, and where x needs a gradient out is too."""
     return _ExpertLinear.apply(x, weight, offsets)
 
 

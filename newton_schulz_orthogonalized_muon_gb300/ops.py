@@ -178,7 +178,8 @@ def expert_matmul(x, weight, offsets, *, transpose: bool = False, handle=None, s
     offset below the largest before it is raised to that, one past the last
     token cut).  The result is [tokens, out]; tokens of no expert get zeros.
     ``transpose``: x is [tokens, out], the result [tokens, cols], each token
-    times its expert's transposed weight (the gradient of the input).  Strides
+    times its expert's transposed weight (the gradient of the input).  Sums are
+    fp32, of at most 2^16 products (x's columns), rounded once.  Strides
     that are not multiples of 8, or starts off 16-byte boundaries, cost a copy."""
     if stream is not None:
         with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
