@@ -438,7 +438,7 @@ muon_status_t muon_act8_weight_grad_workspace(muon_handle_t h, const void* dy, i
  *   transpose 0:  y[t] = W[e] x[t],    x [tokens][cols], y [tokens][out]
  *   transpose 1:  y[t] = W[e]^T x[t],  x [tokens][out], y [tokens][cols]
  * (the second gives the gradient of the input).  A token of no expert gets
- * zeros, whatever it holds.
+ * zeros, whatever it holds.  y overlaps no operand.
  *   x, w, y   dtype (MUON_BF16 or MUON_F16); w [experts][out][cols], expert and
  *             row strides w_expert, ldw
  *   cols, out multiples of 8, up to 2^20, x's up to 2^16; strides of x and w
@@ -457,7 +457,8 @@ muon_status_t muon_expert_matmul(muon_handle_t h, const void* x, int64_t ldx, co
  * (+ add[e]); an expert without tokens gets zeros (or add).
  *   dy, x    dtype, [tokens][out], [tokens][cols]
  *   add, dw  odtype (MUON_F32 or dtype) [experts][out][cols]; add may be NULL, or
- *            dw itself with its strides
+ *            dw itself with its strides; dw overlaps no other operand (add may lie
+ *            in gaps of dw's and the other way round, with the same strides)
  *   cols, out up to 2^20
  * 2048 tokens at a time are added up on the tensor cores, with truncation, and
  * those sums in fp32 with rounding, in `workspace`. */

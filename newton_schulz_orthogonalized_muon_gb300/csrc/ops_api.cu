@@ -279,6 +279,32 @@ muon_status_t check_adamw8(muon_handle_t h, const muon_adamw8_t* tensors, int32_
   return MUON_OK;
 }
 
+// [groups][rows][cols] elements of `size` bytes, rows and groups apart by strides
+// that count where there are several.
+struct Matrices {
+  const void* p;
+  int64_t groups, rows, cols, ld, group, size;
+  uintptr_t at() const { return reinterpret_cast<uintptr_t>(p); }
+  uintptr_t one() const { return static_cast<uintptr_t>(((rows - 1) * (rows > 1 ? ld : 0) + cols) * size); }     // bytes of a group
+  uintptr_t end() const { return at() + static_cast<uintptr_t>((groups - 1) * (groups > 1 ? group : 0) * size) + one(); }
+};
+bool apart(const Matrices& a, const Matrices& b) { return a.end() <= b.at() || b.end() <= a.at(); }
+// Two of one shape that are one, or have no element in common: spans apart, or
+// each in the other's gaps between columns or between groups.
+bool same_or_apart(const Matrices& a, const Matrices& b) {
+  const bool ld = a.rows == 1 || a.ld == b.ld, group = a.groups == 1 || a.group == b.group;
+  if (a.p == b.p) return ld && group;
+  if (apart(a, b)) return true;
+  const Matrices &lo = a.at() < b.at() ? a : b, &hi = a.at() < b.at() ? b : a;
+  auto gaps = [&](int64_t stride, uintptr_t first, uintptr_t second) {
+    const uintptr_t s = static_cast<uintptr_t>(stride * a.size), r = (hi.at() - lo.at()) % s;
+    return r >= first && r + second <= s;
+  };
+  const uintptr_t row = static_cast<uintptr_t>(a.cols * a.size);
+  if (a.rows > 1 && ld && group && (a.groups == 1 || a.group % a.ld == 0) && gaps(a.ld, row, row)) return true;
+  return a.groups > 1 && group && gaps(a.group, lo.one(), hi.one());
+}
+
 // Rows of 16-bit elements as TMA reads them.
 bool bad_rows(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return p == nullptr || !aligned(p, 16) || (rows > 1 && (ld < cols || ld % 8 != 0 || ld > (int64_t(1) << 38)));
@@ -683,6 +709,13 @@ muon_status_t muon_expert_weight_grad(muon_handle_t h, const void* dy, int64_t l
     };
     MUON_CHECK(whole(dw, lddw, dw_expert), "dw is NULL, not aligned or its strides are too small");
     MUON_CHECK(add == nullptr || whole(add, ldadd, add_expert), "add is not aligned or its strides are too small");
+    // tiles are written in any order
+    const int64_t es = odtype == MUON_F32 ? 4 : 2;
+    const Matrices to{dw, experts, out, cols, lddw, dw_expert, es};
+    MUON_CHECK(add == nullptr || same_or_apart(to, Matrices{add, experts, out, cols, ldadd, add_expert, es}),
+               "add and dw overlap and are not one");
+    MUON_CHECK(tokens == 0 || (apart(to, Matrices{x, 1, tokens, cols, ldx, 0, 2}) && apart(to, Matrices{dy, 1, tokens, out, lddy, 0, 2})),
+               "dw overlaps x or dy");
     DeviceGuard guard(h->device);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_arg);
     ProductParams p{};

@@ -196,8 +196,9 @@ def expert_weight_grad(dy, x, offsets, *, add=None, out=None, dtype=None, handle
     expert the sum over its tokens of dy[t] x[t]^T (+ add).
 
     dy: [tokens, out], x: [tokens, cols], bf16 or fp16; add: the gradient so
-    far; out: where the result is written (``out=add`` adds in place); dtype:
-    float32 (default) or dy's type, that of add and out if they are given."""
+    far; out: where the result is written (``out=add`` adds in place; it overlaps
+    no input otherwise); dtype: float32 (default) or dy's type, that of add and
+    out if they are given."""
     if stream is not None:
         with torch.cuda.stream(stream):  # torch ties outputs and scratch to it
             return expert_weight_grad(dy, x, offsets, add=add, out=out, dtype=dtype, handle=handle)
