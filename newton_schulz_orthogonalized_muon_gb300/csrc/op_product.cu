@@ -882,6 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Traits<KIND>::THREAD
           uint32_t wword = 0u;
 #pragma unroll
           for (int q = 0; q < 4; ++q) wword |= __shfl_sync(0xffffffffu, now, (k0 & 31) + q) << (8 * q);
+          __syncwarp();                  // every lane's reads are behind the arrival
           if (lane == 0) mbar_arrive(&bar->sb_empty[rb.s]);
           rb.next();
           ok = wait_warp(&bar->sf_empty[rs.s], rs.ph ^ 1u, abort, p);
