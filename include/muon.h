@@ -526,7 +526,9 @@ muon_status_t muon_act8_matmul(muon_handle_t h, const uint8_t* codes, int64_t ld
  * largest fall at beta2 = 0.9999 and 5% at 0.99999.
  * A finite gradient counts as 2^63 in magnitude at most.  A NaN or an infinity in
  * one makes its block's states NaN (byte 255, codes 0), and the next step the
- * block's parameters.  v below 2^-126, and eps + r below it, count as 0.
+ * block's parameters.  v below 2^-126, and eps + r below it, count as 0.  The root
+ * and the quotient are off by up to 2^-22 of themselves.  A gradient overlaps nothing
+ * that is written.
  * tensors: a host array, read during the call; a tensor may not be in it twice.
  * n == 0 is a valid no-op. */
 typedef struct {

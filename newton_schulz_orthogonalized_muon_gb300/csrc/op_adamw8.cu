@@ -33,11 +33,19 @@
 //   m <- m + (1 - beta1)(g - m);  v <- r^2 + (1 - beta2)(g^2 - r^2);  r = v^(1/2)
 //   p <- p decay - size m / (eps + r)
 // and only then are m and r rounded to codes.  g is cut to 2^63 in magnitude, so
-// that squares are finite.
+// that squares are finite.  The root and the quotient are the hardware's
+// approximations, off by up to 2^-22 of themselves.  Of 6.7e7 codes 25 (m) and 75 (r)
+// are other than the rule's on 64 bits with bf16 gradients, 116 and 46 with fp32
+// ones; in fp32 operation by operation, with a rounded root and quotient, 25 and 78,
+// 84 and 65.
 //
 // Bound by HBM: 10 bytes an element with bf16 parameters and gradients (fp32
 // states: 22).  A thread has 16 elements, 8 lanes a block.  1.05e9 bf16
-// parameters: 1.80 ms, 5.8 TB/s; their states' values in bf16 0.90 ms, 6.7 TB/s.
+// parameters: 1.62 ms, 6.5 TB/s; their states' values in bf16 0.90 ms, 6.7 TB/s.
+// 5.4e8 fp32 parameters with fp32 gradients 1.39 ms, 6.2 TB/s, with bf16 ones 1.20;
+// bf16 parameters with fp32 gradients 0.94.  Four CTAs an SM leave a thread 64
+// registers, 116 to 160 bytes of which are spilled.  Tensors that no vector access
+// fits go an element at a time, 4.4 to 4.9 ms.
 #include "common.cuh"
 #include "internal.h"
 #include "op_code8.cuh"

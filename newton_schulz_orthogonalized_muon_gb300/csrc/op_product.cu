@@ -14,7 +14,9 @@
 //   8 bits     outputs (W's codes)  tokens (x's codes) columns
 // A CTA pair forms 256 m (128 a CTA) by up to 256 n, 224 with 8 bits, whose scales
 // need TMEM too (tcgen05.mma.cta_group::2), in one of two accumulators that tiles
-// take in turn: one is read out while the other's products run.  The ragged
+// take in turn: one is read out while the other's products run.  (The parts of a
+// tile's sum over more than 2048 tokens all go to one, so the products wait for each
+// read-out: 8 experts of 6144 tokens 2048 x 1408 209 - 216 us.)  The ragged
 // dimension, tokens, is n: the tensor core takes n in steps of 32, so an expert's
 // last tile costs what it has, where rows of m would be padded to 256 (17% of the
 // work at 768 tokens an expert).  (Tiles of twice the n in both accumulators, with a
@@ -31,10 +33,10 @@
 // axis and the largest before them) and counts the tiles for itself.
 //
 // Measured, calls that follow one another: 49152 rows through 64 experts 2048 ->
-// 1408 forward 213 - 221 us, input's gradient 200 - 206, weights' 217 - 225 (1.3 PFLOP/s,
-// the pipe 83, 81 and 64% busy), all under the power cap at 1.3 to 1.6 GHz; 48 rows
-// 37 - 38 us (214 MB at 5.7 TB/s); 16384 x 4096 -> 14336 in 8 bits 635 - 638 us (3.0
-// PFLOP/s), 16 rows 13.2 (58.7 MB at 4.4 TB/s).  Within a tile a step's operands come
+// 1408 forward 213 - 222 us, input's gradient 200 - 207, weights' 217 - 225 (1.3 PFLOP/s,
+// the pipe 81, 81 and 66% busy), all under the power cap at 1.3 to 1.6 GHz; 48 rows
+// 37 - 38 us (214 MB at 5.7 TB/s); 16384 x 4096 -> 14336 in 8 bits 632 - 652 us by the
+// box (3.0 PFLOP/s, the pipe 84% busy), 16 rows 13.3 (58.7 MB at 4.4 TB/s).  Within a tile a step's operands come
 // from L2 at 52 to 60 bytes a cycle and SM, which bounds the weights' gradients.
 #include <algorithm>
 

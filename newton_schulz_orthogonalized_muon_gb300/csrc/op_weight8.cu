@@ -11,8 +11,9 @@
 // around in shared memory, as the transpose's.  A block's loads and its stores
 // do not overlap, so the more blocks an SM holds the better, and 512 threads
 // with 3 CTAs an SM keep more bytes in flight than 256 with 4 (14336 x 4096
-// bf16: codes 34 us against 41, with the transpose's 44 against 50; 512 with 4
-// spill, 47 and 58).  That is 176 MB one way at 5.2 TB/s, 235 MB with the
+// bf16: codes 34 us against 41, with the transpose's 44 against 50; with 4 CTAs of
+// 512, 47 and 58: with 3 the 16-bit kernels spill 16 to 32 bytes a thread, with 4
+// more).  That is 176 MB one way at 5.2 TB/s, 235 MB with the
 // transpose's at 5.4; the way back, which needs no maximum first, takes 30 us.
 #include <cuda_fp8.h>
 

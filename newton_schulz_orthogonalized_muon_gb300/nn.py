@@ -135,7 +135,9 @@ def linear8(x, weight, *, products8: bool = False):
 
     products8: the product and the input's gradient run in 8 bits too, of the
     stored input, weight and gradient of the output (ops.act8_matmul), each
-    value of which is rounded to e4m3, by up to 2^-4 of itself."""
+    value of which is rounded to e4m3, by up to 2^-4 of itself.  The weight is
+    stored anew by each call, which a step needs; for many calls on one weight
+    store it once (ops.act8_store_weight) and call ops.act8_matmul."""
     if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
         raise ValueError("linear8 takes bfloat16 inputs and weights")
     if products8:

@@ -292,7 +292,8 @@ def adamw8_step(params, grads, states, *, step: int, lr: float, beta1: float, be
     The same call gives the same result.  A finite gradient counts as at most
     2^63 in magnitude.  A NaN or an infinity in one makes the states of its block
     of 128 elements NaN, and the next step their parameters.  A captured call
-    repeats its ``step`` and ``seed``."""
+    repeats its ``step`` and ``seed`` with each replay: it rounds alike each time,
+    and what moves too little to pass once never does."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return adamw8_step(params, grads, states, step=step, lr=lr, beta1=beta1, beta2=beta2, eps=eps, wd=wd, seed=seed,
